@@ -8,6 +8,7 @@ not been built (``python compressed_output_head_amd/build.py``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -22,6 +23,8 @@ ARCHEAD_BF16, ARCHEAD_F32 = 1, 2
 ARCHEAD_PATH_AUTO, ARCHEAD_PATH_DECODE, ARCHEAD_PATH_TILE = 0, 1, 2
 # storage formats (archead_format): the method's head and the two comparison heads
 ARCHEAD_FMT_ARCHEAD, ARCHEAD_FMT_GROUP_INT4, ARCHEAD_FMT_ROW_INT8 = 0, 1, 2
+# preference losses (archead_preference_kind)
+ARCHEAD_PREF_SIGMOID, ARCHEAD_PREF_SQUARED = 0, 1
 # main kernels (archead_main_kernel), by the names the profiler shows
 KERNEL_NAMES = {0: "tile32_kernel", 1: "small_decode_kernel", 2: "decode_kernel", 3: "batch_kernel"}
 STATUS = {0: "OK", 1: "E_NULL", 2: "E_DIMS", 3: "E_UNSUPPORTED", 4: "E_DTYPE", 5: "E_SHAPE",
@@ -32,7 +35,7 @@ EXPORTS = ("archead_pack_layout", "archead_workspace_bytes", "archead_workspace_
            "archead_logits_path", "archead_logits_events", "archead_stats_workspace_bytes",
            "archead_logits_stats", "archead_quantize", "archead_topk_workspace_bytes", "archead_logits_topk",
            "archead_fit_workspace_bytes", "archead_fit", "archead_logit_error_workspace_bytes",
-           "archead_logit_error",
+           "archead_logit_error", "archead_loss_workspace_bytes", "archead_policy_loss", "archead_preference_loss",
            "archead_status_string", "archead_format_version")
 
 
@@ -100,6 +103,28 @@ class ArcheadFitOutputs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("A_c", "B_c", "A_w", "B_w", "E")]
 
 
+class ArcheadPolicyInputs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("labels", "advantage", "old_logp", "ref_logp", "weight")]
+                + [(n, ctypes.c_float) for n in ("clip_low", "clip_high", "kl_coef", "inv_temperature")])
+
+
+class ArcheadPolicyOutputs(ctypes.Structure):
+    _fields_ = [("loss", ctypes.c_void_p), ("logp", ctypes.c_void_p), ("row_loss", ctypes.c_void_p),
+                ("dY", ctypes.POINTER(ArcheadTensor))]
+
+
+class ArcheadPreferenceInputs(ctypes.Structure):
+    _fields_ = ([("labels", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("n_pairs", ctypes.c_int64)]
+                + [(n, ctypes.c_void_p) for n in ("ref_logp", "weight", "pair_weight")]
+                + [(n, ctypes.c_float) for n in ("beta", "label_smoothing", "inv_temperature")]
+                + [("kind", ctypes.c_int32)])
+
+
+class ArcheadPreferenceOutputs(ctypes.Structure):
+    _fields_ = [("loss", ctypes.c_void_p), ("logp", ctypes.c_void_p), ("chosen_reward", ctypes.c_void_p),
+                ("rejected_reward", ctypes.c_void_p), ("dY", ctypes.POINTER(ArcheadTensor))]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python compressed_output_head_amd/build.py`")
@@ -137,6 +162,11 @@ def _load():
     lib.archead_logit_error_workspace_bytes.argtypes = [P(ArcheadDims), ctypes.c_int64, P(ctypes.c_uint64)]
     lib.archead_logit_error.argtypes = [P(ArcheadTensor), P(ArcheadPackedHead), P(ArcheadTensor),
                                         P(ctypes.c_double), ctypes.c_void_p]
+    lib.archead_loss_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, P(ctypes.c_uint64)]
+    lib.archead_policy_loss.argtypes = [P(ArcheadTensor), P(ArcheadPolicyInputs), P(ArcheadPolicyOutputs),
+                                        ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]
+    lib.archead_preference_loss.argtypes = [P(ArcheadTensor), P(ArcheadPreferenceInputs), P(ArcheadPreferenceOutputs),
+                                            ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]
     lib.archead_status_string.argtypes = [ctypes.c_int]
     lib.archead_status_string.restype = ctypes.c_char_p
     lib.archead_format_version.argtypes = []
@@ -525,3 +555,119 @@ def archead_logit_error(H, head: PackedHead, W, stream=None):
     _check(lib.archead_logit_error(ctypes.byref(h), ctypes.byref(p), ctypes.byref(w), sums, ctypes.c_void_p(stream)),
            "archead_logit_error")
     return sums[0], sums[1]
+
+
+# ------------------------------------------------- losses and their gradient ---
+
+def _scope(device, stream):
+    """Context in which allocations and launches go to `stream` (a torch
+    stream, a raw handle, or None: the device's current stream) on `device`."""
+    torch = _torch()
+    if stream is None:
+        return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _vec(t, name: str, dtype, n: int, device):
+    """Address of a contiguous vector of n elements (None for None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}")
+    return t.data_ptr()
+
+
+def archead_loss_workspace_bytes(n_rows: int, V: int, n_pairs: int = 0) -> int:
+    out = ctypes.c_uint64(0)
+    _check(lib.archead_loss_workspace_bytes(int(n_rows), int(V), int(n_pairs), ctypes.byref(out)),
+           "archead_loss_workspace_bytes")
+    return out.value
+
+
+def _loss_setup(Y, dY, dY_dtype, with_gradient, workspace, n_pairs):
+    """(Y, dY, dY's tensor or None, workspace) of a loss call as the library
+    takes them; allocates what the caller did not bring."""
+    torch = _torch()
+    if not Y.is_cuda:
+        raise ValueError("Y must be a device tensor")
+    y = _tensor(Y)
+    if not with_gradient:
+        dY = None
+    elif dY is None:
+        dY = torch.empty(Y.shape, dtype=dY_dtype or Y.dtype, device=Y.device)
+    elif dY.device != Y.device or (dY_dtype is not None and dY_dtype != dY.dtype):
+        raise ValueError("dY must be on Y's device and of dY_dtype")
+    if workspace is None:
+        workspace = torch.empty(archead_loss_workspace_bytes(Y.shape[0], Y.shape[1], n_pairs), dtype=torch.uint8,
+                                device=Y.device)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != Y.device:
+        raise ValueError("workspace must be a contiguous uint8 tensor on Y's device")
+    return y, dY, None if dY is None else _tensor(dY), workspace
+
+
+def archead_policy_loss(Y, labels, advantage, old_logp=None, ref_logp=None, weight=None, clip_low: float = 0.2,
+                        clip_high: float = 0.2, kl_coef: float = 0.0, inv_temperature: float = 1.0, dY=None,
+                        dY_dtype=None, with_gradient: bool = True, workspace=None, stream=None):
+    """Clipped policy loss with a KL term on the rows of Y (fp32 or bf16
+    [N, V]) and its gradient.  labels: int32 [N]; advantage, old_logp (None:
+    this policy sampled), ref_logp (needed when kl_coef > 0), weight (None:
+    1): fp32 [N].  Returns a dict of device tensors "loss" (scalar), "logp",
+    "row_loss" (fp32 [N]) and, with_gradient, "dY" [N, V]: the given tensor
+    (Y itself is allowed) or a new one of dY_dtype (Y's dtype by default)."""
+    torch = _torch()
+    with _scope(Y.device, stream):
+        N, dev = Y.shape[0], Y.device
+        y, dY, dy, workspace = _loss_setup(Y, dY, dY_dtype, with_gradient, workspace, 0)
+        vec = torch.empty(2 * N + 1, dtype=torch.float32, device=dev)
+        out = {"loss": vec[2 * N], "logp": vec[:N], "row_loss": vec[N:2 * N]}
+        at = vec.data_ptr()
+        inp = ArcheadPolicyInputs(_vec(labels, "labels", torch.int32, N, dev),
+                                  _vec(advantage, "advantage", torch.float32, N, dev),
+                                  _vec(old_logp, "old_logp", torch.float32, N, dev),
+                                  _vec(ref_logp, "ref_logp", torch.float32, N, dev),
+                                  _vec(weight, "weight", torch.float32, N, dev),
+                                  clip_low, clip_high, kl_coef, inv_temperature)
+        outs = ArcheadPolicyOutputs(at + 8 * N, at, at + 4 * N, None if dy is None else ctypes.pointer(dy))
+        _check(lib.archead_policy_loss(ctypes.byref(y), ctypes.byref(inp), ctypes.byref(outs), workspace.data_ptr(),
+                                       workspace.numel(), torch.cuda.current_stream(dev).cuda_stream),
+               "archead_policy_loss")
+        if dY is not None:
+            out["dY"] = dY
+        return out
+
+
+def archead_preference_loss(Y, labels, offsets, ref_logp=None, weight=None, pair_weight=None, beta: float = 0.1,
+                            label_smoothing: float = 0.0, inv_temperature: float = 1.0,
+                            kind: int = ARCHEAD_PREF_SIGMOID, dY=None, dY_dtype=None, with_gradient: bool = True,
+                            workspace=None, stream=None):
+    """Preference loss over pairs of sequences of rows of Y (fp32 or bf16
+    [N, V]) and its gradient.  offsets: int32 [2 B + 1], sequence q is the rows
+    [offsets[q], offsets[q + 1]), pair i prefers sequence 2i over 2i + 1.
+    labels: int32 [N]; ref_logp (None: reference-free), weight (None: 1): fp32
+    [N]; pair_weight (None: 1): fp32 [B].  Returns a dict of device tensors
+    "loss" (scalar), "logp" [N], "chosen_reward", "rejected_reward" [B] and,
+    with_gradient, "dY" as archead_policy_loss does."""
+    torch = _torch()
+    with _scope(Y.device, stream):
+        N, dev, B = Y.shape[0], Y.device, (offsets.numel() - 1) // 2
+        y, dY, dy, workspace = _loss_setup(Y, dY, dY_dtype, with_gradient, workspace, B)
+        vec = torch.empty(N + 2 * B + 1, dtype=torch.float32, device=dev)
+        out = {"loss": vec[N + 2 * B], "logp": vec[:N], "chosen_reward": vec[N:N + B],
+               "rejected_reward": vec[N + B:N + 2 * B]}
+        at = vec.data_ptr()
+        inp = ArcheadPreferenceInputs(_vec(labels, "labels", torch.int32, N, dev),
+                                      _vec(offsets, "offsets", torch.int32, 2 * B + 1, dev), B,
+                                      _vec(ref_logp, "ref_logp", torch.float32, N, dev),
+                                      _vec(weight, "weight", torch.float32, N, dev),
+                                      _vec(pair_weight, "pair_weight", torch.float32, B, dev),
+                                      beta, label_smoothing, inv_temperature, kind)
+        outs = ArcheadPreferenceOutputs(at + 4 * (N + 2 * B), at, at + 4 * N, at + 4 * (N + B),
+                                        None if dy is None else ctypes.pointer(dy))
+        _check(lib.archead_preference_loss(ctypes.byref(y), ctypes.byref(inp), ctypes.byref(outs),
+                                           workspace.data_ptr(), workspace.numel(),
+                                           torch.cuda.current_stream(dev).cuda_stream), "archead_preference_loss")
+        if dY is not None:
+            out["dY"] = dY
+        return out

@@ -481,6 +481,118 @@ ARCHEAD_API int archead_topk_workspace_bytes(const archead_dims* d, int64_t n_to
 ARCHEAD_API int archead_logits_topk(const archead_tensor* H, const archead_packed_head* head, int32_t k,
                                     float* top_val, int32_t* top_idx, void* stream);
 
+/* ---- Training through a frozen packed head -------------------------------
+ * archead_logits (or any source of logits Y), a loss with its gradient dY on
+ * the rows of Y, and archead_logits_backward, which takes dY through the
+ * packed head to the hidden states.  archead_logits_stats gives the
+ * log-probabilities of an earlier policy or of a reference without Y
+ * (minus its cross-entropy).
+ *
+ * The losses take Y and dY in fp32 or bf16 each, any row stride, aligned to
+ * the element size.  With z = inv_temperature Y, log p_n is the
+ * log-probability of row n's label under softmax(z_n); the gradient is with
+ * respect to Y.  Rows of weight 0 do not count: they are not read (they may
+ * hold anything, their labels too), their log p and loss are 0 and their
+ * gradient is 0.  A row that counts with a label outside [0, V), with a NaN
+ * or +inf, or with nothing above -inf has log p NaN, and so have the loss and
+ * its gradient.  Logits of -inf have probability 0.
+ * dY may be Y itself (same data, dtype and stride: the gradient replaces the
+ * logits); otherwise the two must not overlap (E_SHAPE).  Sums of the losses
+ * and all per-row arithmetic are fp64, the sum of exponentials fp32; bf16
+ * gradients are rounded to nearest even from fp32.  Two calls with the same
+ * arguments give the same bits. */
+
+/* Device workspace of a loss call: n_rows rows of V logits, n_pairs pairs (0
+ * for the policy loss): 8 bytes per row and piece (at most 64 pieces a row),
+ * 20 per row, 8 per pair, each section rounded up to 256 bytes.  Pure host
+ * arithmetic.  E_NULL, E_SHAPE, E_UNSUPPORTED (n_rows or n_pairs above 2^22,
+ * V of 2^31 or more). */
+ARCHEAD_API int archead_loss_workspace_bytes(int64_t n_rows, int64_t V, int64_t n_pairs, uint64_t* bytes);
+
+/* Inputs of the clipped policy loss, device arrays of N = Y.rows elements,
+ * 4-byte aligned:
+ *   r_n = exp(log p_n - old_logp[n])
+ *   l_n = -min(r_n A_n, clip(r_n, 1 - clip_low, 1 + clip_high) A_n)
+ *         + kl_coef (exp(d_n) - d_n - 1),  d_n = ref_logp[n] - log p_n
+ *   loss = sum_n weight[n] l_n
+ * (the third term is the nonnegative estimate of KL(policy || reference) on
+ * the sampled tokens).  The weights hold the normalisation: 1/count for a
+ * mean over tokens, 1/(G length) for a mean of G sequence means.  The
+ * gradient passes where the unclipped term is the minimum, ties included. */
+typedef struct {
+  const int32_t* labels;    /* the sampled token of each row */
+  const float* advantage;   /* A */
+  const float* old_logp;    /* NULL: the policy that sampled is this one, r_n = 1 */
+  const float* ref_logp;    /* may be NULL when kl_coef is 0 */
+  const float* weight;      /* NULL: 1 for every row */
+  float clip_low, clip_high; /* >= 0; infinity does not clip */
+  float kl_coef;            /* >= 0 */
+  float inv_temperature;    /* > 0 */
+} archead_policy_inputs;
+
+/* Outputs; each pointer may be NULL (not computed). */
+typedef struct {
+  float* loss;              /* [1] */
+  float* logp;              /* [N] log p_n */
+  float* row_loss;          /* [N] l_n */
+  const archead_tensor* dY; /* [N][V] d loss / d Y */
+} archead_policy_outputs;
+
+/* Enqueue the clipped policy loss of the rows of Y on `stream`; N = 0 gives a
+ * loss of 0.  workspace: device, 256-byte aligned, at least
+ * archead_loss_workspace_bytes(N, V, 0) (unused when that is 0).  E_NULL,
+ * E_DTYPE, E_SHAPE, E_UNSUPPORTED, E_VALUE (a scalar out of range), E_ALIGN,
+ * E_WORKSPACE, E_HIP. */
+ARCHEAD_API int archead_policy_loss(const archead_tensor* Y, const archead_policy_inputs* in,
+                                    const archead_policy_outputs* out, void* workspace,
+                                    uint64_t workspace_bytes, void* stream);
+
+typedef enum {
+  ARCHEAD_PREF_SIGMOID = 0, /* -(1 - e) log sigmoid(beta h) - e log sigmoid(-beta h), e = label_smoothing */
+  ARCHEAD_PREF_SQUARED = 1  /* (h - 1 / (2 beta))^2; label_smoothing is not used */
+} archead_preference_kind;
+
+/* Inputs of the preference loss over n_pairs pairs of sequences, device
+ * arrays, 4-byte aligned.  Sequence q is the rows [offsets[q],
+ * offsets[q + 1]) of Y; pair i prefers sequence 2i (chosen) over 2i + 1
+ * (rejected):
+ *   S_q = sum over its rows of weight[n] (log p_n - ref_logp[n])
+ *   h_i = S_2i - S_2i+1,  loss = sum_i pair_weight[i] l(h_i)
+ * offsets must not descend; rows before the first and behind the last
+ * sequence do not count.  Offsets outside [0, N] end at its borders.  A
+ * sequence without rows (or without weights) has S = 0.  Weights of 1/length
+ * give the length-normalised form.  A pair of weight 0 adds nothing to the
+ * loss and its rows' gradient is 0. */
+typedef struct {
+  const int32_t* labels;     /* [N] the token of each row */
+  const int32_t* offsets;    /* [2 n_pairs + 1] */
+  int64_t n_pairs;
+  const float* ref_logp;     /* [N]; NULL: 0, the reference-free form */
+  const float* weight;       /* [N]; NULL: 1 */
+  const float* pair_weight;  /* [n_pairs]; NULL: 1 */
+  float beta;                /* > 0 */
+  float label_smoothing;     /* in [0, 0.5) */
+  float inv_temperature;     /* > 0 */
+  int32_t kind;              /* archead_preference_kind */
+} archead_preference_inputs;
+
+/* Outputs; each pointer may be NULL (not computed). */
+typedef struct {
+  float* loss;               /* [1] */
+  float* logp;               /* [N] log p_n, 0 in rows that do not count */
+  float* chosen_reward;      /* [n_pairs] beta S_2i */
+  float* rejected_reward;    /* [n_pairs] beta S_2i+1 */
+  const archead_tensor* dY;  /* [N][V] d loss / d Y */
+} archead_preference_outputs;
+
+/* Enqueue the preference loss on `stream`.  workspace: device, 256-byte
+ * aligned, at least archead_loss_workspace_bytes(N, V, n_pairs).  E_NULL,
+ * E_DTYPE, E_SHAPE, E_UNSUPPORTED (an unknown kind among them), E_VALUE,
+ * E_ALIGN, E_WORKSPACE, E_HIP. */
+ARCHEAD_API int archead_preference_loss(const archead_tensor* Y, const archead_preference_inputs* in,
+                                        const archead_preference_outputs* out, void* workspace,
+                                        uint64_t workspace_bytes, void* stream);
+
 /* Static string naming a status code. */
 ARCHEAD_API const char* archead_status_string(int status);
 

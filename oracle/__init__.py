@@ -11,3 +11,6 @@ from .archead_oracle import (  # noqa: F401
     ALT_FORMAT, ALT_PERM8, alt_persistent_bytes, pack_alt, unpack_alt, w_hat_alt, logits_alt,
     quant_group_int4,
 )
+from .training_oracle import (  # noqa: F401
+    PREF_SIGMOID, PREF_SQUARED, policy_loss, preference_loss, logits_backward,
+)
