@@ -19,11 +19,15 @@
 //
 // A row is cut into pieces so that few rows still fill the GPU:
 //   row_pieces_kernel   (M, S) of every piece, and the label's logit
-//   pair_kernel         preference loss only: sequence sums, the pairs'
-//                       losses and every row's coefficient
-//   row_gradient_kernel the gradient, piece by piece; for the policy loss
-//                       each workgroup first merges its row's pieces and works
-//                       the coefficient out; one more workgroup adds up the loss
+//   rows_kernel         a row's pieces merged, its loss and its coefficient
+//   pair_kernel         preference loss only: the sequences' sums, the pair's
+//                       loss and its slope for every row
+//   row_gradient_kernel the gradient, piece by piece; one more workgroup adds
+//                       up the loss
+// which reads the logits twice, as the coefficient of a row needs all of it (of
+// a pair, all of the pair).  Many rows of a policy loss take another way, that
+// reads most of them once:
+//   row_order_kernel, policy_fused_kernel, loss_total_kernel
 // Rows of weight zero are neither read nor counted; their gradient is zero.
 // Every sum has a fixed order, so results do not depend on scheduling.
 #include <math.h>
@@ -40,8 +44,13 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kRowUnroll = 4;        // 16-byte loads in flight per thread
-constexpr int kSumThreads = 1024;
+constexpr int kPairThreads = 1024;
+constexpr int kFusedThreads = 1024;
+constexpr int kOrderThreads = 1024;
+constexpr int kHeldChunks = 12;      // of 16 bytes, in registers
+constexpr int64_t kFusedLeastRows = 256;   // one per CU
 constexpr int64_t kMaxPieces = 64;
+constexpr int64_t kTargetGroups = 12288, kLeastWidth = 2048;
 
 // What the gradient of a row needs: dY_j = neg 2^(k (y_j - M)), label_g at the label.
 struct RowGrad {
@@ -60,6 +69,7 @@ struct RowArgs {
   int64_t N, V, y_stride, dy_stride;
   int64_t width;  // columns of a piece
   int pieces;
+  int lanes;      // that merge a row's pieces
   Scale k;
   float s;
   const int32_t* labels;
@@ -67,8 +77,11 @@ struct RowArgs {
   // workspace
   float2* part;    // [N][pieces] (M, S)
   float* ylab;     // [N]
-  RowGrad* grad;   // [N], preference loss
-  double* pair_loss;  // [B], preference loss
+  RowGrad* grad;   // [N]
+  double* term;    // [N] weighted, of the loss (policy) or of the sequence's sum (preference)
+  float* row_slope;   // [N], preference loss: of the pair's loss in the row's log-probability; else null
+  double* pair_loss;  // [B]
+  int32_t* order;     // [N + 1], policy loss
   // policy loss
   const float *old_logp, *ref_logp, *advantage;
   float clip_low, clip_high, kl_coef;
@@ -107,14 +120,17 @@ struct Elem<float> {
   static __device__ __forceinline__ float from(float f) { return f; }
 };
 
-// n = 4 or 8 values to consecutive elements, 16 or 8 bytes a store.
+// n = 4 or 8 values to consecutive elements, 16 or 8 bytes a store.  Gradients
+// are written once and too large to wait for their reader in the cache; stores
+// that say so leave it to the logits, which are read twice (480 rows of a
+// preference loss took 74 us with them and 83 without, 4096 rows 513 and 537).
 template <int n>
 __device__ __forceinline__ void store_run(uint16_t* p, const float* g) {
   if constexpr (n == 8) {
     const u2 a = pack_bf16x4(g[0], g[1], g[2], g[3]), b = pack_bf16x4(g[4], g[5], g[6], g[7]);
-    *reinterpret_cast<u4_any*>(p) = u4{a[0], a[1], b[0], b[1]};
+    __builtin_nontemporal_store(u4_any(u4{a[0], a[1], b[0], b[1]}), reinterpret_cast<u4_any*>(p));
   } else {
-    *reinterpret_cast<u2_any*>(p) = pack_bf16x4(g[0], g[1], g[2], g[3]);
+    __builtin_nontemporal_store(u2_any(pack_bf16x4(g[0], g[1], g[2], g[3])), reinterpret_cast<u2_any*>(p));
   }
 }
 template <int n>
@@ -122,7 +138,7 @@ __device__ __forceinline__ void store_run(float* p, const float* g) {
 #pragma unroll
   for (int i = 0; i < n; i += 4) {
     const f4 v = {g[i], g[i + 1], g[i + 2], g[i + 3]};
-    *reinterpret_cast<u4_any*>(p + i) = __builtin_bit_cast(u4, v);
+    __builtin_nontemporal_store(u4_any(__builtin_bit_cast(u4, v)), reinterpret_cast<u4_any*>(p + i));
   }
 }
 
@@ -163,13 +179,15 @@ __device__ __forceinline__ double block_sum(double v, double* buf) {
 
 __device__ __forceinline__ float weight_of(const RowArgs& a, int64_t n) { return a.weight ? a.weight[n] : 1.0f; }
 
-// Rows [first, last) that belong to a sequence of a pair.
-__device__ __forceinline__ bool in_pairs(const RowArgs& a, int64_t n) {
-  return n >= a.offsets[0] && n < a.offsets[2 * a.B];
+// Whether row n counts: its weight, and for pairs a place in a sequence.
+template <bool kPairs>
+__device__ __forceinline__ bool row_counts(const RowArgs& a, int64_t n) {
+  if (kPairs && !(n >= a.offsets[0] && n < a.offsets[2 * a.B])) return false;
+  return weight_of(a, n) != 0.0f;
 }
 
 // (M, S) of the elements [0, len) at p, one thread's share.
-template <typename T>
+template <typename T, int kThreads>
 __device__ __forceinline__ float2 thread_stats(const T* p, int64_t len, Scale k) {
   using E = Elem<T>;
   const int64_t full = len / E::kPer16;
@@ -180,11 +198,11 @@ __device__ __forceinline__ float2 thread_stats(const T* p, int64_t len, Scale k)
       M = M0 = top;
     }
   };
-  for (int64_t c0 = threadIdx.x; c0 < full; c0 += kRowThreads * kRowUnroll) {
+  for (int64_t c0 = threadIdx.x; c0 < full; c0 += kThreads * kRowUnroll) {
     u4 v[kRowUnroll];
 #pragma unroll
     for (int u = 0; u < kRowUnroll; ++u) {
-      const int64_t c = c0 + u * kRowThreads;
+      const int64_t c = c0 + u * kThreads;
       v[u] = c < full ? u4(*reinterpret_cast<const u4_any*>(p + c * E::kPer16))
                       : u4{E::kNegInf2, E::kNegInf2, E::kNegInf2, E::kNegInf2};
     }
@@ -215,90 +233,137 @@ __global__ __launch_bounds__(kRowThreads) void row_pieces_kernel(const RowArgs a
   __shared__ float2 buf[kRowThreads / 64];
   const int64_t n = blockIdx.x / a.pieces;
   const int p = (int)(blockIdx.x % a.pieces);
-  const bool on = weight_of(a, n) != 0.0f && (!kPairs || in_pairs(a, n));
-  if (p == 0 && threadIdx.x == 0) {
-    // what stays of a row that does not count (or that no sequence of descending offsets holds)
-    if (a.logp) a.logp[n] = 0.0f;
-    if (a.row_loss) a.row_loss[n] = 0.0f;
-    if (kPairs) a.grad[n] = RowGrad{0.0f, 0.0f, 0.0f, 0u};
-  }
-  if (!on) return;
+  if (!row_counts<kPairs>(a, n)) return;
   const T* row = static_cast<const T*>(a.Y) + n * a.y_stride;
   const int64_t c0 = p * a.width, c1 = c0 + a.width < a.V ? c0 + a.width : a.V;
   const int64_t label = a.labels[n];
   const bool valid = label >= 0 && label < a.V;
-  // in its own launch: the gradient may be written over Y
+  // read here, before any launch that may write the gradient over Y
   if (threadIdx.x == 0 && (valid ? label >= c0 && label < c1 : p == 0))
     a.ylab[n] = valid ? Elem<T>::one(row[label]) : __builtin_nanf("");
-  const float2 r = block_merge<kRowThreads>(thread_stats(row + c0, c1 - c0, a.k), a.k, buf);
+  const float2 r = block_merge<kRowThreads>(thread_stats<T, kRowThreads>(row + c0, c1 - c0, a.k), a.k, buf);
   if (threadIdx.x == 0) a.part[n * a.pieces + p] = r;
 }
 
-// The row's pieces in order.
-__device__ __forceinline__ float2 merged(const RowArgs& a, int64_t n) {
-  float2 r = a.part[n * a.pieces];
-  for (int p = 1; p < a.pieces; ++p) r = merge(r, a.part[n * a.pieces + p], a.k);
+// (M, S) of row n, merged by a.lanes neighbouring lanes (a power of two that
+// divides 64), of which this is number `lane`; all of them return it.
+__device__ __forceinline__ float2 merged(const RowArgs& a, int64_t n, int lane) {
+  float2 r = lane < a.pieces ? a.part[n * a.pieces + lane] : float2{-INFINITY, 0.0f};
+  for (int p = lane + a.lanes; p < a.pieces; p += a.lanes) r = merge(r, a.part[n * a.pieces + p], a.k);
+  for (int o = a.lanes >> 1; o > 0; o >>= 1) r = merge(r, float2{__shfl_xor(r.x, o), __shfl_xor(r.y, o)}, a.k);
   return r;
 }
 
-__device__ __forceinline__ double row_logp(const RowArgs& a, int64_t n, float2 r) {
-  return (double)a.s * ((double)a.ylab[n] - (double)r.x) - log((double)r.y);
-}
+// What the policy loss has of one row, and what comes of it.
+struct PolicyRow {
+  float y_label, M, S, advantage, old_logp, ref_logp, weight;
+};
+struct PolicyResult {
+  double loss, term;  // term = weight loss
+  float logp;
+  RowGrad grad;
+};
+struct PolicyScalars {
+  float s, clip_low, clip_high, kl_coef;
+  uint32_t own_ratio;  // 1: the policy that sampled is this one
+};
 
-__device__ __forceinline__ RowGrad row_grad(const RowArgs& a, double coef, double logp, float2 r) {
-  const double c = coef * (double)a.s;
-  return RowGrad{(float)(-c / (double)r.y), r.x, (float)(-c * expm1(logp)), coef != 0.0 ? 1u : 0u};
-}
-
-// The policy loss of one row and its derivative in the log-probability.
-__device__ __forceinline__ void policy_row(const RowArgs& a, int64_t n, double logp, double& loss, double& slope) {
-  const double A = a.advantage[n];
-  const double ratio = a.old_logp ? exp(logp - (double)a.old_logp[n]) : exp(logp - logp);
-  const double lo = 1.0 - (double)a.clip_low, hi = 1.0 + (double)a.clip_high;
+// Not inlined: in a loop, the compiler would hold every constant of the fp64
+// functions in registers that the row needs.
+__device__ __attribute__((noinline)) PolicyResult policy_row(PolicyRow x, PolicyScalars p) {
+  const double s = p.s, w = x.weight, A = x.advantage;
+  const double logp = s * ((double)x.y_label - (double)x.M) - log((double)x.S);
+  const double ratio = exp(logp - (p.own_ratio ? logp : (double)x.old_logp));
+  const double lo = 1.0 - (double)p.clip_low, hi = 1.0 + (double)p.clip_high;
   const double kept = ratio < lo ? lo : ratio > hi ? hi : ratio;  // NaN stays NaN
   const bool plain = !(kept * A < ratio * A);  // the unclipped term is the smaller one
-  loss = plain ? -(ratio * A) : -(kept * A);
-  slope = plain ? -(ratio * A) : 0.0;
-  if (a.kl_coef != 0.0f) {
-    const double d = (double)a.ref_logp[n] - logp, e = expm1(d);
-    loss += (double)a.kl_coef * (e - d);
-    slope -= (double)a.kl_coef * e;
+  double loss = plain ? -(ratio * A) : -(kept * A);
+  double slope = plain ? -(ratio * A) : 0.0;  // the loss's derivative in logp
+  if (p.kl_coef != 0.0f) {
+    const double d = (double)x.ref_logp - logp, e = expm1(d);
+    loss += (double)p.kl_coef * (e - d);
+    slope -= (double)p.kl_coef * e;
   }
+  const double c = w * slope * s;
+  return PolicyResult{loss, w * loss, (float)logp,
+                      RowGrad{(float)(-c / (double)x.S), x.M, (float)(-c * expm1(logp)), c != 0.0 ? 1u : 0u}};
 }
 
-// Workgroup i: pair i.  Threads take the rows of a sequence in turn.
-__global__ __launch_bounds__(kRowThreads) void pair_kernel(const RowArgs a) {
-  __shared__ double buf[kRowThreads / 64];
+__device__ __forceinline__ PolicyRow policy_inputs(const RowArgs& a, int64_t n) {
+  PolicyRow x{};
+  x.advantage = a.advantage[n];
+  x.old_logp = a.old_logp ? a.old_logp[n] : 0.0f;
+  x.ref_logp = a.ref_logp ? a.ref_logp[n] : 0.0f;
+  x.weight = weight_of(a, n);
+  return x;
+}
+
+__device__ __forceinline__ PolicyScalars policy_scalars(const RowArgs& a) {
+  return PolicyScalars{a.s, a.clip_low, a.clip_high, a.kl_coef, a.old_logp ? 0u : 1u};
+}
+
+// a.lanes lanes a row: its log-probability, its term of the loss (or of its
+// sequence's sum) and what its gradient needs, for pairs still to be
+// multiplied by the slope of the pair's loss.  (The fp64 functions here take
+// about as many instructions as a thread's share of a short row, so no
+// gradient workgroup repeats them.)
+template <bool kPairs>
+__global__ __launch_bounds__(kRowThreads) void rows_kernel(const RowArgs a) {
+  const int64_t t = (int64_t)blockIdx.x * kRowThreads + threadIdx.x, n = t / a.lanes;
+  const int lane = (int)(t % a.lanes);
+  if (n >= a.N) return;
+  PolicyResult r{0.0, 0.0, 0.0f, {0.0f, 0.0f, 0.0f, 0u}};
+  if (row_counts<kPairs>(a, n)) {
+    if constexpr (kPairs) {
+      const double w = weight_of(a, n);
+      const float2 st = merged(a, n, lane);
+      const double logp = (double)a.s * ((double)a.ylab[n] - (double)st.x) - log((double)st.y), c = w * (double)a.s;
+      r.logp = (float)logp;
+      r.term = w * (logp - (a.ref_logp ? (double)a.ref_logp[n] : 0.0));
+      r.grad = RowGrad{(float)(-c / (double)st.y), st.x, (float)(-c * expm1(logp)), 1u};
+    } else {
+      PolicyRow x = policy_inputs(a, n);
+      const float2 st = merged(a, n, lane);
+      x.y_label = a.ylab[n];
+      x.M = st.x;
+      x.S = st.y;
+      r = policy_row(x, policy_scalars(a));
+    }
+  }
+  if (lane != 0) return;
+  a.grad[n] = r.grad;
+  a.term[n] = r.term;
+  if (kPairs) a.row_slope[n] = 0.0f;
+  if (a.logp) a.logp[n] = r.logp;
+  if (a.row_loss) a.row_loss[n] = (float)r.loss;
+}
+
+// Workgroup i: pair i.  Its sequences are neighbours, so one walk over their
+// rows takes both.
+__global__ __launch_bounds__(kPairThreads) void pair_kernel(const RowArgs a) {
+  __shared__ double buf[2][kPairThreads / 64];
   const int64_t i = blockIdx.x;
   auto bound = [&](int64_t q) {  // offsets outside [0, N] end at its borders
     const int64_t o = a.offsets[q];
     return o < 0 ? (int64_t)0 : o > a.N ? a.N : o;
   };
-  const int64_t b[3] = {bound(2 * i), bound(2 * i + 1), bound(2 * i + 2)};
-  double sum[2];
-  for (int side = 0; side < 2; ++side) {
-    double part = 0.0;
-    for (int64_t n = b[side] + threadIdx.x; n < b[side + 1]; n += kRowThreads) {
-      const float w = weight_of(a, n);
-      if (w == 0.0f || !in_pairs(a, n)) continue;
-      const double logp = row_logp(a, n, merged(a, n));
-      if (a.logp) a.logp[n] = (float)logp;
-      part += (double)w * (logp - (a.ref_logp ? (double)a.ref_logp[n] : 0.0));
-    }
-    sum[side] = block_sum<kRowThreads>(part, buf);
-  }
+  const int64_t b0 = bound(2 * i), b1 = bound(2 * i + 1), b2 = bound(2 * i + 2);
+  const double pw = a.pair_weight ? (double)a.pair_weight[i] : 1.0;
+  double sum[2] = {0.0, 0.0};
+  for (int64_t n = b0 + threadIdx.x; n < b1; n += kPairThreads) sum[0] += a.term[n];
+  for (int64_t n = b1 + threadIdx.x; n < b2; n += kPairThreads) sum[1] += a.term[n];
+  for (int side = 0; side < 2; ++side) sum[side] = block_sum<kPairThreads>(sum[side], buf[side]);
   const double h = sum[0] - sum[1], beta = a.beta, eps = a.smoothing;
   double loss, slope;  // of the pair, and its derivative in h
   if (a.kind == ARCHEAD_PREF_SIGMOID) {
-    const double x = beta * h, t = log1p(exp(-fabs(x)));  // softplus(x) = max(x, 0) + t
+    const double x = beta * h, e = exp(-fabs(x)), t = log1p(e);  // softplus(x) = max(x, 0) + t
     loss = (1.0 - eps) * ((x < 0.0 ? -x : 0.0) + t) + eps * ((x > 0.0 ? x : 0.0) + t);
-    slope = beta * (eps - 1.0 / (1.0 + exp(x)));
+    slope = beta * (eps - (x < 0.0 ? 1.0 : e) / (1.0 + e));
   } else {
     const double u = h - 0.5 / beta;
     loss = u * u;
     slope = 2.0 * u;
   }
-  const double pw = a.pair_weight ? (double)a.pair_weight[i] : 1.0;
   // a pair of weight zero is left out, whatever its rows hold
   loss = pw != 0.0 ? pw * loss : 0.0;
   slope = pw != 0.0 ? pw * slope : 0.0;
@@ -307,13 +372,8 @@ __global__ __launch_bounds__(kRowThreads) void pair_kernel(const RowArgs a) {
     if (a.chosen) a.chosen[i] = (float)(beta * sum[0]);
     if (a.rejected) a.rejected[i] = (float)(beta * sum[1]);
   }
-  for (int side = 0; side < 2; ++side)
-    for (int64_t n = b[side] + threadIdx.x; n < b[side + 1]; n += kRowThreads) {
-      const float w = weight_of(a, n);
-      if (w == 0.0f || !in_pairs(a, n)) continue;
-      const float2 r = merged(a, n);
-      a.grad[n] = row_grad(a, (side ? -slope : slope) * (double)w, row_logp(a, n, r), r);
-    }
+  for (int64_t n = b0 + threadIdx.x; n < b1; n += kPairThreads) a.row_slope[n] = (float)slope;
+  for (int64_t n = b1 + threadIdx.x; n < b2; n += kPairThreads) a.row_slope[n] = (float)-slope;
 }
 
 // The elements [0, len) of a gradient row; `label` is the label's place in them, or no place.
@@ -351,63 +411,231 @@ __device__ __forceinline__ void thread_gradient(const T* y, G* dy, int64_t len, 
   }
 }
 
-// Workgroup n pieces + p: piece p of row n; the last workgroup: the loss.
-template <typename T, typename G, bool kPairs>
+// The loss from its rows' or pairs' parts, by one workgroup.
+__device__ __forceinline__ void loss_total(const RowArgs& a) {
+  __shared__ double buf[kRowThreads / 64];
+  double sum = 0.0;
+  const double* parts = a.row_slope ? a.pair_loss : a.term;
+  const int64_t count = a.row_slope ? a.B : a.N;
+  for (int64_t i = threadIdx.x; i < count; i += kRowThreads) sum += parts[i];
+  sum = block_sum<kRowThreads>(sum, buf);
+  if (threadIdx.x == 0 && a.loss) *a.loss = (float)sum;
+}
+
+__global__ __launch_bounds__(kRowThreads) void loss_total_kernel(const RowArgs a) { loss_total(a); }
+
+// Workgroup n pieces + p: piece p of row n; one more: the loss.
+template <typename T, typename G>
 __global__ __launch_bounds__(kRowThreads) void row_gradient_kernel(const RowArgs a) {
   const int64_t n = blockIdx.x / a.pieces;
   const int p = (int)(blockIdx.x % a.pieces);
-  RowGrad r{0.0f, 0.0f, 0.0f, 0u};
-  if constexpr (kPairs) {
-    r = a.grad[n];
-  } else {
-    const float w = weight_of(a, n);
-    if (w != 0.0f) {
-      const float2 st = merged(a, n);
-      const double logp = row_logp(a, n, st);
-      double loss, slope;
-      policy_row(a, n, logp, loss, slope);
-      r = row_grad(a, (double)w * slope, logp, st);
-    }
+  if (n >= a.N) return loss_total(a);
+  RowGrad r = a.grad[n];
+  if (a.row_slope) {
+    const float slope = a.row_slope[n];
+    r.neg *= slope;
+    r.label_g *= slope;
+    r.on = r.on && slope != 0.0f;
   }
   const int64_t c0 = p * a.width, c1 = c0 + a.width < a.V ? c0 + a.width : a.V;
   thread_gradient(static_cast<const T*>(a.Y) + n * a.y_stride + c0, static_cast<G*>(a.dY) + n * a.dy_stride + c0,
                   c1 - c0, (int64_t)a.labels[n] - c0, a.k, r);
 }
 
-// One workgroup: the policy loss's per-row outputs and the sum of either loss.
-template <bool kPairs>
-__global__ __launch_bounds__(kSumThreads) void loss_sum_kernel(const RowArgs a) {
-  __shared__ double buf[kSumThreads / 64];
-  double sum = 0.0;
-  if constexpr (kPairs) {
-    for (int64_t i = threadIdx.x; i < a.B; i += kSumThreads) sum += a.pair_loss[i];
-  } else {
-    for (int64_t n = threadIdx.x; n < a.N; n += kSumThreads) {
-      const float w = weight_of(a, n);
-      if (w == 0.0f) continue;
-      const double logp = row_logp(a, n, merged(a, n));
-      double loss, slope;
-      policy_row(a, n, logp, loss, slope);
-      if (a.logp) a.logp[n] = (float)logp;
-      if (a.row_loss) a.row_loss[n] = (float)loss;
-      sum += (double)w * loss;
+// The rows in the order policy_fused_kernel takes them: those that count from
+// the front, the others from the back, so that every workgroup gets the same
+// number of each to within one.
+__global__ __launch_bounds__(kOrderThreads) void row_order_kernel(const RowArgs a) {
+  constexpr int kWaves = kOrderThreads / 64;
+  __shared__ int count[2][kWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t front = 0, back = 0;  // rows placed so far
+  int turn = 0;
+  for (int64_t n0 = 0; n0 < a.N; n0 += kOrderThreads, turn ^= 1) {
+    const int64_t n = n0 + threadIdx.x;
+    const bool in = n < a.N, on = in && row_counts<false>(a, n);
+    const uint64_t ons = __ballot(on);
+    if (lane == 0) count[turn][wave] = __popcll(ons);
+    __syncthreads();  // the other turn's counts are read before the next one's are written
+    int before = 0, all = 0;
+    for (int w = 0; w < kWaves; ++w) {
+      before += w < wave ? count[turn][w] : 0;
+      all += count[turn][w];
+    }
+    const int rank = before + __popcll(ons & ((1ull << lane) - 1));  // rows that count before this one
+    const int64_t here = a.N - n0 < kOrderThreads ? a.N - n0 : kOrderThreads;
+    if (on) a.order[front + rank] = (int32_t)n;
+    if (in && !on) a.order[a.N - 1 - (back + (threadIdx.x - rank))] = (int32_t)n;
+    front += all;
+    back += here - all;
+  }
+  if (threadIdx.x == 0) a.order[a.N] = (int32_t)front;
+}
+
+// The policy loss of many rows in one launch: a workgroup of 16 waves takes
+// the first kHeldChunks 16-byte chunks a thread of a row into its registers
+// and reads them once, for the sum and for the gradient; the next row's are
+// loaded into the registers that the gradient's stores free.  The rest of a
+// row is read again from the cache.  On 4096 rows of 151936 bf16 logits (a
+// tenth of them left out), 0.52 ms: 4.5 TB/s of the bytes it cannot do
+// without, against 0.66 ms for the kernels above, which read all rows twice.
+// Holding the whole row (18 chunks) took 0.54 to 0.59 ms, and so did summing a
+// row's chunks between the stores of the row before it; two workgroups a CU
+// with half the registers each took 0.64 ms or more.
+//
+// What is subtracted in the exponents is the maximum of the row's first
+// kFusedThreads chunks: any number of the row's range will do, S >= 1 as those
+// chunks are in it, and a row whose S overflows (a logit about 100 octaves
+// above them, or first chunks of -inf) is summed again with running maxima.
+// A bf16 gradient leaves the low part of k out, 2^-25 of the exponent.
+template <typename T, typename G>
+__global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowArgs a) {
+  using E = Elem<T>;
+  constexpr int n16 = E::kPer16, kWaves = kFusedThreads / 64, kHeld = kHeldChunks;
+  __shared__ float top_buf[kWaves], sum_buf[kWaves];
+  __shared__ float2 pair_buf[kWaves];
+  __shared__ RowGrad grad;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int full = (int)(a.V / n16), rest = (int)(a.V % n16);
+  const int64_t count = a.order[a.N];  // rows that count
+  u4 v[kHeld];
+  float y_rest = -INFINITY, y_label = 0.0f;
+  auto row_of = [&](int64_t n) { return static_cast<const T*>(a.Y) + n * a.y_stride; };
+  // a uniform address and one small offset for all chunks: no address takes registers
+  const uint32_t y_off = (uint32_t)tid * 16, dy_off = (uint32_t)(tid * n16 * sizeof(G));
+  auto load = [&](const T* row, int c, int end) {
+    v[c] = u4{E::kNegInf2, E::kNegInf2, E::kNegInf2, E::kNegInf2};
+    if (tid < end - c * kFusedThreads)
+      v[c] = __builtin_nontemporal_load(
+          reinterpret_cast<const u4_any*>(reinterpret_cast<const char*>(row + c * kFusedThreads * n16) + y_off));
+  };
+  auto load_ends = [&](const T* row, int64_t n) {
+    const int64_t label = a.labels[n];
+    y_rest = tid < rest ? E::one(row[(int64_t)full * n16 + tid]) : -INFINITY;
+    y_label = label >= 0 && label < a.V ? E::one(row[label]) : __builtin_nanf("");
+  };
+  int64_t place = blockIdx.x;
+  if (place < count) {
+    const int64_t n = a.order[place];
+#pragma unroll
+    for (int c = 0; c < kHeld; ++c) load(row_of(n), c, full);
+    load_ends(row_of(n), n);
+  }
+  for (; place < count; place += gridDim.x) {
+    const int64_t n = a.order[place];
+    const T* row = row_of(n);
+    G* out = static_cast<G*>(a.dY) + n * a.dy_stride;
+    const bool more = place + gridDim.x < count;
+    const int64_t next = more ? a.order[place + gridDim.x] : n;
+    PolicyRow x = policy_inputs(a, n);
+    x.y_label = y_label;
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < n16; ++j) top = fmaxf(top, E::at(v[0], j));
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    if (lane == 0) top_buf[wave] = top;
+    __syncthreads();
+    top = top_buf[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, top_buf[w]);
+    const float shift = shift_of(top);
+    float S = tid < rest ? exp_at(y_rest - shift, a.k) : 0.0f;
+#pragma unroll
+    for (int c = 0; c < kHeld; ++c) {
+      float add = 0.0f;
+#pragma unroll
+      for (int j = 0; j < n16; ++j) add += exp_at(E::at(v[c], j) - shift, a.k);
+      S += add;
+      // the gradient converts the chunk anew: kept, the converted logits
+      // would take twice the registers that a row has
+      asm volatile("" : "+v"(v[c]));
+    }
+    for (int64_t c = kHeld * kFusedThreads + tid; c < full; c += kFusedThreads) {
+      const u4 y = *reinterpret_cast<const u4_any*>(row + c * n16);
+      float add = 0.0f;
+#pragma unroll
+      for (int j = 0; j < n16; ++j) add += exp_at(E::at(y, j) - shift, a.k);
+      S += add;
+    }
+    for (int o = 32; o > 0; o >>= 1) S += __shfl_xor(S, o);
+    if (lane == 0) sum_buf[wave] = S;
+    __syncthreads();
+    S = sum_buf[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) S += sum_buf[w];
+    x.M = shift;
+    x.S = S;
+    if (!(S >= 0.5f && S < INFINITY)) {  // the same decision in every thread
+      const float2 st = block_merge<kFusedThreads>(thread_stats<T, kFusedThreads>(row, a.V, a.k), a.k, pair_buf);
+      x.M = st.x;
+      x.S = st.y;
+    }
+    if (wave == 0) {
+      const PolicyResult r = policy_row(x, policy_scalars(a));
+      if (lane == 0) {
+        grad = r.grad;
+        a.term[n] = r.term;
+        if (a.logp) a.logp[n] = r.logp;
+        if (a.row_loss) a.row_loss[n] = (float)r.loss;
+      }
+    }
+    __syncthreads();
+    const RowGrad g = grad;
+    auto put = [&](const u4& y, G* at_chunk) {
+      float r[n16];
+#pragma unroll
+      for (int j = 0; j < n16; ++j) {
+        const float d = E::at(y, j) - g.M;
+        r[j] = g.neg * (sizeof(G) == 2 ? __builtin_amdgcn_exp2f(d * a.k.hi) : exp_at(d, a.k));
+      }
+      store_run<n16>(reinterpret_cast<G*>(reinterpret_cast<char*>(at_chunk) + dy_off), r);
+    };
+    const T* next_row = row_of(next);
+    const int next_full = more ? full : 0;
+#pragma unroll
+    for (int c = 0; c < kHeld; ++c) {
+      if (tid < full - c * kFusedThreads) put(v[c], out + c * kFusedThreads * n16);
+      load(next_row, c, next_full);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    for (int64_t c = kHeld * kFusedThreads; c + tid < full; c += kFusedThreads)
+      put(*reinterpret_cast<const u4_any*>(row + (c + tid) * n16), out + c * n16);
+    if (tid < rest) out[(int64_t)full * n16 + tid] = Elem<G>::from(g.neg * exp_at(y_rest - g.M, a.k));
+    // the label's element, by the thread that wrote it
+    const int64_t label = a.labels[n];
+    if (label >= 0 && label < a.V &&
+        tid == (int)(label < (int64_t)full * n16 ? label / n16 % kFusedThreads : label - (int64_t)full * n16))
+      out[label] = Elem<G>::from(g.label_g);
+    if (more) load_ends(next_row, next);
+  }
+  // the rows that do not count
+  for (; place < a.N; place += gridDim.x) {
+    const int64_t n = a.order[place];
+    G* out = static_cast<G*>(a.dY) + n * a.dy_stride;
+    const float zero[n16] = {};
+    for (int64_t c = tid; c < full; c += kFusedThreads) store_run<n16>(out + c * n16, zero);
+    if (tid < rest) out[(int64_t)full * n16 + tid] = Elem<G>::from(0.0f);
+    if (tid == 0) {
+      a.term[n] = 0.0;
+      if (a.logp) a.logp[n] = 0.0f;
+      if (a.row_loss) a.row_loss[n] = 0.0f;
     }
   }
-  sum = block_sum<kSumThreads>(sum, buf);
-  if (threadIdx.x == 0 && a.loss) *a.loss = (float)sum;
 }
 
 // ------------------------------------------------------------------- host ---
 
-// Pieces a row is cut into: about 16384 workgroups in all (8 rounds of the
-// GPU's 2048 resident ones), none under 2048 columns.
+// Pieces a row is cut into: about 12288 workgroups in all (six rounds of the
+// GPU's 2048 resident ones), none under 2048 columns.  With 4096 in all, 4096
+// rows of a preference loss took 4% longer, with 16384 the 257 rows of an odd
+// vocabulary 15%.
 int64_t row_pieces(int64_t N, int64_t V) {
-  const int64_t most = std::min<int64_t>(kMaxPieces, (V + 2047) / 2048);
-  return std::max<int64_t>(1, std::min<int64_t>(most, 16384 / std::max<int64_t>(N, 1)));
+  const int64_t most = std::min<int64_t>(kMaxPieces, (V + kLeastWidth - 1) / kLeastWidth);
+  return std::max<int64_t>(1, std::min<int64_t>(most, kTargetGroups / std::max<int64_t>(N, 1)));
 }
 
 struct LossWorkspace {
-  uint64_t part, ylab, grad, pair_loss, total;
+  uint64_t part, ylab, grad, term, row_words, pair_loss, total;
 };
 
 LossWorkspace loss_workspace(int64_t N, int64_t V, int64_t B) {
@@ -419,7 +647,9 @@ LossWorkspace loss_workspace(int64_t N, int64_t V, int64_t B) {
   };
   w.part = take((uint64_t)N * (uint64_t)row_pieces(N, V) * sizeof(float2));
   w.ylab = take((uint64_t)N * 4);
-  w.grad = take(B > 0 ? (uint64_t)N * sizeof(RowGrad) : 0);
+  w.grad = take((uint64_t)N * sizeof(RowGrad));
+  w.term = take((uint64_t)N * 8);
+  w.row_words = take(N > 0 ? (uint64_t)(N + 1) * 4 : 0);  // the order of rows (policy) or their slopes (preference)
   w.pair_loss = take((uint64_t)B * 8);
   return w;
 }
@@ -497,26 +727,61 @@ RowArgs row_args(const archead_tensor* Y, const archead_tensor* dY, float s, voi
   a.part = reinterpret_cast<float2*>(ws + W.part);
   a.ylab = reinterpret_cast<float*>(ws + W.ylab);
   a.grad = reinterpret_cast<RowGrad*>(ws + W.grad);
-  a.pair_loss = reinterpret_cast<double*>(ws + W.pair_loss);
+  a.term = reinterpret_cast<double*>(ws + W.term);
+  a.order = reinterpret_cast<int32_t*>(ws + W.row_words);
+  a.lanes = 1;
+  while (a.lanes < a.pieces && a.lanes < 16) a.lanes *= 2;
   return a;
+}
+
+template <typename T>
+hipError_t launch_gradient(const RowArgs& a, const archead_tensor* dY, hipStream_t s) {
+  const dim3 grid((unsigned)(a.N * a.pieces + 1)), block(kRowThreads);
+  if (!dY) {
+    if (a.loss) hipLaunchKernelGGL(loss_total_kernel, dim3(1), block, 0, s, a);
+  } else if (dY->dtype == ARCHEAD_BF16) {
+    hipLaunchKernelGGL((row_gradient_kernel<T, uint16_t>), grid, block, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((row_gradient_kernel<T, float>), grid, block, 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+// The fused kernel: a row for every CU, and rows that fill half of the chunks
+// held.  (At 257 rows of 100003 fp32 logits and at 512 of 151936 in bf16 it
+// and the split kernels take the same time to within 4%.)
+bool fused_takes(const RowArgs& a, int64_t size) {
+  return a.N >= kFusedLeastRows && a.V * size >= kHeldChunks / 2 * kFusedThreads * 16 && a.V < (int64_t(1) << 30);
 }
 
 template <typename T, bool kPairs>
 hipError_t launch_loss(const RowArgs& a, const archead_tensor* dY, hipStream_t s) {
-  const dim3 grid((unsigned)(a.N * a.pieces)), block(kRowThreads);
   (void)hipGetLastError();  // start from a clean error state
-  if (a.N > 0) hipLaunchKernelGGL((row_pieces_kernel<T, kPairs>), grid, block, 0, s, a);
-  if constexpr (kPairs) {
-    if (a.B > 0) hipLaunchKernelGGL(pair_kernel, dim3((unsigned)a.B), block, 0, s, a);
+  if constexpr (!kPairs) {
+    if (dY && fused_takes(a, sizeof(T))) {
+      int device = 0, cus = 0;
+      if (hipGetDevice(&device) != hipSuccess ||
+          hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess)
+        return hipErrorUnknown;
+      const dim3 grid((unsigned)std::min<int64_t>(a.N, cus)), block(kFusedThreads);
+      hipLaunchKernelGGL(row_order_kernel, dim3(1), dim3(kOrderThreads), 0, s, a);
+      if (dY->dtype == ARCHEAD_BF16)
+        hipLaunchKernelGGL((policy_fused_kernel<T, uint16_t>), grid, block, 0, s, a);
+      else
+        hipLaunchKernelGGL((policy_fused_kernel<T, float>), grid, block, 0, s, a);
+      if (a.loss) hipLaunchKernelGGL(loss_total_kernel, dim3(1), dim3(kRowThreads), 0, s, a);
+      return hipGetLastError();
+    }
   }
-  if (a.loss || a.logp || a.row_loss)
-    hipLaunchKernelGGL(loss_sum_kernel<kPairs>, dim3(1), dim3(kSumThreads), 0, s, a);
-  if (!dY || a.N == 0) return hipGetLastError();
-  if (dY->dtype == ARCHEAD_BF16)
-    hipLaunchKernelGGL((row_gradient_kernel<T, uint16_t, kPairs>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((row_gradient_kernel<T, float, kPairs>), grid, block, 0, s, a);
-  return hipGetLastError();
+  if (a.N > 0) {
+    const int64_t rows = kRowThreads / a.lanes;
+    hipLaunchKernelGGL((row_pieces_kernel<T, kPairs>), dim3((unsigned)(a.N * a.pieces)), dim3(kRowThreads), 0, s, a);
+    hipLaunchKernelGGL(rows_kernel<kPairs>, dim3((unsigned)((a.N + rows - 1) / rows)), dim3(kRowThreads), 0, s, a);
+  }
+  if constexpr (kPairs) {
+    if (a.B > 0) hipLaunchKernelGGL(pair_kernel, dim3((unsigned)a.B), dim3(kPairThreads), 0, s, a);
+  }
+  return launch_gradient<T>(a, dY, s);
 }
 
 template <bool kPairs>
@@ -603,6 +868,8 @@ int archead_preference_loss(const archead_tensor* Y, const archead_preference_in
   a.ref_logp = in->ref_logp;
   a.offsets = in->offsets;
   a.B = in->n_pairs;
+  a.row_slope = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + W.row_words);
+  a.pair_loss = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + W.pair_loss);
   a.pair_weight = in->pair_weight;
   a.beta = in->beta;
   a.smoothing = in->label_smoothing;

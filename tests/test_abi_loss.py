@@ -15,12 +15,12 @@ def _up(x):
 
 
 def _pieces(n, v):
-    return max(1, min(64, -(-v // 2048), 16384 // n))
+    return max(1, min(64, -(-v // 2048), 12288 // n))
 
 
 @pytest.mark.parametrize("n,v,b", [(4, 1024, 0), (1, 151936, 0), (4096, 151936, 0), (480, 151936, 4), (70000, 7, 3)])
 def test_loss_workspace_bytes(ah, n, v, b):  # noqa: F811
-    want = _up(n * _pieces(n, v) * 8) + _up(4 * n) + (_up(16 * n) if b else 0) + _up(8 * b)
+    want = _up(n * _pieces(n, v) * 8) + _up(4 * n) + _up(16 * n) + _up(8 * n) + _up(4 * n + 4) + _up(8 * b)
     assert ah.archead_loss_workspace_bytes(n, v, b) == want
 
 

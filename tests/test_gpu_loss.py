@@ -16,9 +16,10 @@ Tolerances, from the kernels' arithmetic (u = 2^-24, half an fp32 step):
           is bounded by r |A| + kl_coef (e^d + 1), times 1.01 for the move.
   sums    the sum over rows of |w| times the rows' errors, then u.
   dY      an element off the label is c 2^x / S: the exponential as above,
-          u (2 + 2 |x|), c / S rounded once, the product once, and S's own error
-          e_S <= lp_tol:  |dY| (u (5 + 2 spread) + lp_tol);  the label's is
-          rounded once, and its 1 - p moves by p lp_tol.  All move with the
+          u (2 + 2 |x|), c / S rounded once, a pair's slope and its product
+          with c / S once each, the product once, and S's own error
+          e_S <= lp_tol:  |dY| (u (8 + 2 spread) + lp_tol);  the label's has
+          fewer, and its 1 - p moves by p lp_tol.  All move with the
           coefficient's error, |w| s |d slope| p, where the slope moves by the
           same bound as l_n's.  bf16 adds 2^-8 |dY| and fp32 subnormals may
           flush: 2^-126.
@@ -87,7 +88,7 @@ def _check_gradient(dY, want, slope_tol, s, spread, lp_tol, labels, on, logp, bf
             coef[n] = want[n, labels[n]] / denom if denom != 0 else 0.0
             p[n] = np.abs(q / coef[n]) if coef[n] != 0 else 1.0
             p[n, labels[n]] = 1.0
-    rel = U * (5 + 2 * spread) + lp_tol
+    rel = U * (8 + 2 * spread) + lp_tol
     tol = np.abs(want) * rel[:, None] + p * (slope_tol * s)[:, None] + np.abs(coef * lp_tol)[:, None] * p + 2.0 ** -126
     if bf16:
         tol = tol * (1 + 2 ** -8) + np.abs(want) * 2.0 ** -8
@@ -140,7 +141,7 @@ def _check_policy(got, Y64, labels, A, s, kl, weight, old_logp, ref_logp, bf16, 
 
 
 SHAPES = [(1, 1), (1, 2), (3, 7), (2, 8), (5, 255), (4, 1024), (7, 2049), (3, 5003), (2, 33001), (1, 151936), (70, 777),
-          (300, 130)]
+          (300, 130), (600, 33001), (260, 60001)]
 
 
 @pytest.mark.parametrize("y,dy", [("bfloat16", "bfloat16"), ("float32", "float32"), ("float32", "bfloat16"),
@@ -243,6 +244,47 @@ def test_policy_masked_vocabulary(y):
     assert np.isnan(got["logp"][5:]).all() and np.isfinite(got["logp"][:5]).all() and np.isnan(got["loss"])
     assert abs(got["logp"][2] + np.log(V)) < 1e-5 and got["logp"][4] == 0.0 and not got["dY"][4].any()
     assert not got["dY"][0, :4400].any() and np.isfinite(want["dY"][:5]).all()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("y", ["bfloat16", "float32"])
+def test_policy_many_rows_with_special_ones(y, in_place):
+    """Enough rows and columns for the fused kernel: rows that do not count (in
+    runs and alone), -inf at the front, in the middle and everywhere, logits far
+    above the row's first ones, the type's lowest value, NaN, +inf, labels out
+    of range; a stride that is no multiple of 16 bytes."""
+    torch = torch_mod()
+    rng = np.random.default_rng(21)
+    N, V = 280, 50003
+    Y, _ = _make_Y(rng, N, V, getattr(torch, y), pad=2, first=3)
+    w = np.full(N, 0.5)
+    w[40:90] = 0
+    w[[0, 100, 279]] = 0
+    labels = rng.integers(0, V, N)
+    labels[:V // 4096] = np.arange(V // 4096) * 4096 + 4095
+    labels[20:24] = 0, V - 1, V - 2, V // 8 * 8
+    Y[[0, 45, 279]] = float("nan")
+    Y[100] = float("inf")
+    labels[[0, 45, 100, 279]] = -100
+    Y[1, :30000] = -float("inf")       # the first chunks of every thread
+    Y[2, :8] = -float("inf")           # ... of one
+    Y[3, 8:40000] = -float("inf")
+    Y[4] = torch.finfo(Y.dtype).min
+    Y[5, :V - 5] = torch.finfo(Y.dtype).min
+    Y[6, 40000] = 3000.0               # 2^k times the first chunks' maximum is infinite
+    Y[7, 5] = 3000.0
+    Y[8] = -2000.0
+    labels[1:9] = 40000, 40001, 40002, 3, V - 1, 40000, 17, 0
+    Y[9] = -float("inf")
+    Y[10, 49999] = float("nan")
+    Y[11, 3] = float("inf")
+    labels[12:14] = -1, V
+    Y64, A = Y.double().cpu().numpy(), rng.normal(0.2, 1, N).astype(np.float32)
+    got = _run_policy(Y, labels, A, weight=w, **(dict(dY=Y) if in_place else {}))
+    assert np.isnan(got["logp"][9:14]).all() and np.isfinite(got["logp"][:9]).all()
+    _check_policy(got, Y64, labels, A, 1.0, 0.0, w, None, None, y == "bfloat16", 0.2, 0.2)
+    none = _run_policy(Y, labels, A, weight=0 * w)
+    assert none["loss"] == 0 and not none["dY"].any()
 
 
 def test_policy_label_out_of_range_is_nan():
