@@ -36,6 +36,7 @@ EXPORTS = ("archead_pack_layout", "archead_workspace_bytes", "archead_workspace_
            "archead_logits_stats", "archead_quantize", "archead_topk_workspace_bytes", "archead_logits_topk",
            "archead_fit_workspace_bytes", "archead_fit", "archead_logit_error_workspace_bytes",
            "archead_logit_error", "archead_loss_workspace_bytes", "archead_policy_loss", "archead_preference_loss",
+           "archead_logits_backward_workspace_bytes", "archead_logits_backward",
            "archead_status_string", "archead_format_version")
 
 
@@ -167,6 +168,8 @@ def _load():
                                         ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]
     lib.archead_preference_loss.argtypes = [P(ArcheadTensor), P(ArcheadPreferenceInputs), P(ArcheadPreferenceOutputs),
                                             ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]
+    lib.archead_logits_backward_workspace_bytes.argtypes = [P(ArcheadDims), ctypes.c_int64, P(ctypes.c_uint64)]
+    lib.archead_logits_backward.argtypes = [P(ArcheadTensor), P(ArcheadPackedHead), P(ArcheadTensor), ctypes.c_void_p]
     lib.archead_status_string.argtypes = [ctypes.c_int]
     lib.archead_status_string.restype = ctypes.c_char_p
     lib.archead_format_version.argtypes = []
@@ -671,3 +674,36 @@ def archead_preference_loss(Y, labels, offsets, ref_logp=None, weight=None, pair
         if dY is not None:
             out["dY"] = dY
         return out
+
+
+def archead_logits_backward_workspace_bytes(V, D, r_c, r_r, g, n_tokens: int, fmt=ARCHEAD_FMT_ARCHEAD) -> int:
+    out = ctypes.c_uint64(0)
+    _check(lib.archead_logits_backward_workspace_bytes(ctypes.byref(_dims(V, D, r_c, r_r, g, fmt)), int(n_tokens),
+                                                       ctypes.byref(out)), "archead_logits_backward_workspace_bytes")
+    return out.value
+
+
+def archead_logits_backward(dY, head: PackedHead, dH=None, workspace=None, stream=None):
+    """dH = dY W_hat, the hidden states' gradient through the packed head.
+    dY: fp32 or bf16 [N, V]; dH: bf16 [N, D] (a new one by default).  The
+    workspace is the call's own unless one is given (uint8)."""
+    torch = _torch()
+    dev = head.buffer.device
+    if dY.device != dev or (dH is not None and dH.device != dev):
+        raise ValueError("dY and dH must be on the head's device")
+    with _scope(dev, stream):
+        g = _tensor(dY)
+        if dH is None:
+            dH = torch.empty((dY.shape[0], head.D), dtype=torch.bfloat16, device=dev)
+        h = _tensor(dH)
+        if workspace is None:
+            need = archead_logits_backward_workspace_bytes(head.V, head.D, head.r_c, head.r_r, head.g, dY.shape[0],
+                                                           fmt=head.fmt)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+            raise ValueError("workspace must be a contiguous uint8 tensor on the head's device")
+        p = ArcheadPackedHead(_dims(head.V, head.D, head.r_c, head.r_r, head.g, head.fmt), head.buffer.data_ptr(),
+                              head.buffer.numel(), workspace.data_ptr(), workspace.numel())
+        _check(lib.archead_logits_backward(ctypes.byref(g), ctypes.byref(p), ctypes.byref(h),
+                                           torch.cuda.current_stream(dev).cuda_stream), "archead_logits_backward")
+        return dH

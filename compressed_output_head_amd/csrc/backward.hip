@@ -1,0 +1,612 @@
+// The hidden states' gradient through the packed head,
+//   dH[n, d] = sum_v dY[n, v] W_hat[v, d],  W_hat = R + A_c B_c + A_w B_w,
+// for a head that stays as it is (archead_logits_backward).  With the stored
+// codes, R[v, d] = s_R[v] (q4 c8)[v, d] and A[v, j] = s_A[v] code[v, j], so
+//   dH = (dY s_R) (q4 c8) + Z_c B_c + Z_w B_w,  Z = (dY s_A) code:
+// the row scales go to the gradient's side, and the integers q4 c8 (below
+// 2048) and the INT8 codes are exact fp16 operands of the 32 x 32 x 16 MFMA.
+// dY s is rounded to fp16 after scaling its row by a power of two that brings
+// the row's largest product to [2^14, 2^15): 2^-12 of an element, a quarter
+// of the half step of the bf16 result, and independent from one vocabulary
+// entry to the next.  The scale is taken from the products themselves, so a
+// gradient that sits on vocabulary entries of tiny scales keeps its digits.
+//
+//   bwd_max_kernel     per row: the largest |dY s_R|, |dY s_Ac|, |dY s_Aw|
+//   bwd_prep_kernel    dY s_R as fp16 operand fragments; Z in fp32
+//   bwd_main_kernel    the product with the packed residual, the vocabulary
+//                      split over several workgroups where tiles are few
+//   bwd_finish_kernel  the splits' sums and Z B to dH
+// The packed residual is never expanded in memory: a stage of 32 vocabulary
+// rows is unpacked to fp16 in LDS, and the MFMA's operand, which runs along
+// the vocabulary, is read from there by transposing LDS reads.
+#include <algorithm>
+
+#include "device_common.h"
+#include "internal.h"
+
+namespace archead {
+
+namespace {
+
+constexpr int64_t kBwdChunkRows = 4096;  // rows of dY a pass takes
+constexpr int kMaxThreads = 256;
+constexpr int kPrepThreads = 256;
+constexpr int kMainThreads = 512;
+constexpr int kFinishThreads = 256;
+constexpr int kFinishRows = 8;
+constexpr int kRankTiles = 4;       // 32-rank tiles of Z a workgroup forms in one walk
+constexpr int kMaxMaxPieces = 32;
+constexpr int kMaxSplits = 64;
+
+struct BwdArgs {
+  int64_t V, D, N, n32, nb;
+  int r_c, r_r, g, ng, nkt, nA;
+  int nct, nwt;                    // 32-rank tiles of the two parts
+  const void* dY;
+  int64_t dy_stride;
+  uint16_t* dH;
+  int64_t dh_stride;
+  const uint8_t* r_codes;
+  const uint8_t* r_gcodes;
+  const uint16_t* r_rowscale;
+  const int8_t* a_codes;
+  const uint16_t* a_scales;
+  const int8_t* b_codes;
+  const uint16_t* b_scales;
+  // workspace
+  float* pmax;      // [N][pieces][3]
+  float* rscale;    // [n32][3] powers of two that undo the rows' scales
+  _Float16* hf;     // [n32/32][ksteps][64][8]
+  float* z;         // [zparts][n32][r_c + r_r]
+  float* part;      // [splits][N][D]
+  int pieces, zparts, splits, ksteps;
+  int64_t width;    // columns of a piece of bwd_max_kernel
+};
+
+typedef uint32_t u4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// Eight elements of a row that may start at any element.
+__device__ __forceinline__ void load8(const uint16_t* p, float* x) {
+  const u4 v = *reinterpret_cast<const u4_any*>(p);
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    x[2 * w] = __uint_as_float(v[w] << 16);
+    x[2 * w + 1] = __uint_as_float(v[w] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float* x) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const u4 v = *reinterpret_cast<const u4_any*>(p + 4 * h);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) x[4 * h + w] = __uint_as_float(v[w]);
+  }
+}
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+
+// The same with zeros from `end` on.
+template <typename T>
+__device__ __forceinline__ void load8_to(const T* row, int64_t v, int64_t end, float* x) {
+  if (v + 8 <= end) return load8(row + v, x);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = v + j < end ? load1(row + v + j) : 0.0f;
+}
+
+// The scales of eight vocabulary rows (v a multiple of 8 below V16): s_R, and
+// s_Ac, s_Aw of the parts that there are.
+struct Scales8 {
+  float R[8], c[8], w[8];
+};
+__device__ __forceinline__ Scales8 scales8(const BwdArgs& a, int64_t v) {
+  Scales8 s;
+  const u4 x = *reinterpret_cast<const u4*>(a.r_rowscale + v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    s.R[j] = f16_to_f32((uint16_t)(x[j >> 1] >> (16 * (j & 1))));
+    s.c[j] = s.w[j] = 0.0f;
+  }
+  if (a.nA == 1) {
+    const u4 y = *reinterpret_cast<const u4*>(a.a_scales + v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s.c[j] = s.w[j] = f16_to_f32((uint16_t)(y[j >> 1] >> (16 * (j & 1))));
+  } else if (a.nA == 2) {
+    const u4* y = reinterpret_cast<const u4*>(a.a_scales + 2 * v);
+    const u4 y0 = y[0], y1 = y[1];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t d = j < 4 ? y0[j] : y1[j - 4];
+      s.c[j] = f16_to_f32((uint16_t)d);
+      s.w[j] = f16_to_f32((uint16_t)(d >> 16));
+    }
+  }
+  return s;
+}
+
+// Workgroup n pieces + p: the largest products of piece p of row n.
+template <typename T>
+__global__ __launch_bounds__(kMaxThreads) void bwd_max_kernel(const BwdArgs a) {
+  __shared__ float buf[3][kMaxThreads / 64];
+  const int64_t n = blockIdx.x / a.pieces;
+  const int p = (int)(blockIdx.x % a.pieces);
+  const T* row = static_cast<const T*>(a.dY) + n * a.dy_stride;
+  const int64_t end = (p + 1) * a.width < a.V ? (p + 1) * a.width : a.V;
+  float m[3] = {0.0f, 0.0f, 0.0f};
+  for (int64_t v = p * a.width + 8 * threadIdx.x; v < end; v += 8 * kMaxThreads) {
+    float x[8];
+    load8_to(row, v, end, x);
+    const Scales8 s = scales8(a, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      m[0] = fmaxf(m[0], fabsf(x[j] * s.R[j]));
+      m[1] = fmaxf(m[1], fabsf(x[j] * s.c[j]));
+      m[2] = fmaxf(m[2], fabsf(x[j] * s.w[j]));
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    for (int o = 32; o > 0; o >>= 1) m[q] = fmaxf(m[q], __shfl_xor(m[q], o));
+    if ((threadIdx.x & 63) == 0) buf[q][threadIdx.x >> 6] = m[q];
+  }
+  __syncthreads();
+  if (threadIdx.x < 3) {
+    float t = buf[threadIdx.x][0];
+    for (int w = 1; w < kMaxThreads / 64; ++w) t = fmaxf(t, buf[threadIdx.x][w]);
+    a.pmax[(n * a.pieces + p) * 3 + threadIdx.x] = t;
+  }
+}
+
+// Grid (32-row tiles, parts of the vocabulary, groups of kRankTiles rank
+// tiles), four waves that take 128-column runs in turn.  In the operand's
+// layout lane l holds row l % 32 and columns 16 step + 8 (l / 32) .. + 8, for
+// which it loads 16 bytes of its row (32 of fp32) and the scales.  Rank tile
+// t of Z: the same lanes' dY s_A against the codes of ranks 32 t .. + 32,
+// gathered byte by byte (V r bytes in all, from the cache).
+template <typename T>
+__global__ __launch_bounds__(kPrepThreads) void bwd_prep_kernel(const BwdArgs a) {
+  constexpr int kWaves = kPrepThreads / 64;
+  __shared__ int sExp[3][32];
+  __shared__ float red[kWaves][32][33];
+  const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t tile = blockIdx.x, n = 32 * tile + c32;
+  const int part = blockIdx.y, t0 = kRankTiles * (int)blockIdx.z;
+  if (tid < 96) {
+    const int q = tid / 32;
+    const int64_t row = 32 * tile + tid % 32;
+    float m = 0.0f;
+    if (row < a.N)
+      for (int p = 0; p < a.pieces; ++p) m = fmaxf(m, a.pmax[(row * a.pieces + p) * 3 + q]);
+    const int S = row_exponent(m);
+    sExp[q][tid % 32] = S;
+    if (part == 0 && blockIdx.z == 0) a.rscale[row * 3 + q] = ldexpf(1.0f, -S);
+  }
+  __syncthreads();
+  const int eR = sExp[0][c32], ec = sExp[1][c32], ew = sExp[2][c32];
+  const bool real = n < a.N;
+  const T* row = static_cast<const T*>(a.dY) + (real ? n : 0) * a.dy_stride;
+  const int64_t V16 = 16 * a.nb;
+  const int r = a.r_c + a.r_r, tiles = a.nct + a.nwt;
+  const int runs = (a.ksteps + 7) / 8;  // of 8 steps
+  const int run0 = (int)((int64_t)part * runs / gridDim.y), run1 = (int)((int64_t)(part + 1) * runs / gridDim.y);
+  f16x acc[kRankTiles] = {};
+  for (int run = run0 + wave; run < run1; run += kWaves) {
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+      const int step = 8 * run + i;
+      if (step >= a.ksteps) break;
+      const int64_t v = 16 * (int64_t)step + 8 * half;
+      float x[8] = {};
+      if (real) load8_to(row, v, a.V, x);
+      const int64_t vs = v < V16 ? v : V16 - 8;  // past V16 dY is zero
+      const Scales8 s = scales8(a, vs);
+      if (blockIdx.z == 0) {
+        h8 f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = (_Float16)ldexpf(x[j] * s.R[j], eR);
+        *reinterpret_cast<h8*>(a.hf + ((tile * a.ksteps + step) * 64 + lane) * 8) = f;
+      }
+      if (t0 >= tiles) continue;
+      h8 fc, fw;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        fc[j] = (_Float16)ldexpf(x[j] * s.c[j], ec);
+        fw[j] = (_Float16)ldexpf(x[j] * s.w[j], ew);
+      }
+#pragma unroll
+      for (int q = 0; q < kRankTiles; ++q) {
+        const int t = t0 + q;
+        if (t >= tiles) break;
+        const bool in_c = t < a.nct;
+        const int j = 32 * (in_c ? t : t - a.nct) + c32;
+        const bool valid = j < (in_c ? a.r_c : a.r_r);
+        const int8_t* codes = a.a_codes + vs * r + (in_c ? 0 : a.r_c) + (valid ? j : 0);
+        h8 b;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) b[k] = (_Float16)(float)(valid ? codes[(int64_t)k * r] : 0);
+        acc[q] = mfma32(in_c ? fc : fw, b, acc[q]);
+      }
+    }
+  }
+  for (int q = 0; q < kRankTiles; ++q) {
+    const int t = t0 + q;
+    if (t >= tiles) break;
+    const bool in_c = t < a.nct;
+    const int j0 = 32 * (in_c ? t : t - a.nct), rank = in_c ? a.r_c : a.r_r;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < 16; ++v) red[wave][8 * (v >> 2) + 4 * half + (v & 3)][c32] = acc[q][v];
+    __syncthreads();
+    for (int e = tid; e < 32 * 32; e += kPrepThreads) {
+      const int i = e >> 5, j = e & 31;
+      float z = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) z += red[w][i][j];
+      if (j0 + j < rank) a.z[((int64_t)part * a.n32 + 32 * tile + i) * r + (in_c ? 0 : a.r_c) + j0 + j] = z;
+    }
+  }
+}
+
+// Place of 16-byte octet o (8 columns) of row k in a stage's fp16 tile of 32
+// rows x 256 columns: both the 16 rows that a wave writes at one octet and the
+// 4 rows x 4 octets that 32 lanes read at a time fall in different banks.
+__device__ __forceinline__ int tile_octet(int k, int o) {
+  return 32 * k + (o ^ (((k & 3) << 2) | ((k >> 2) & 3)));
+}
+
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+// Transposing read: of 16 lanes that point at 4 rows x 4 runs of 4 columns
+// (lane q at row q / 4, run q % 4), lane i receives column i of the 4 rows.
+__device__ __forceinline__ h4 read_tr(const _Float16* p) {
+  return __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)p));
+}
+
+// Tokens x 256 columns of dH per workgroup over a share of the vocabulary;
+// TT 32-token tiles, eight waves in WM rows.
+template <int TT>
+struct MainShape {
+  static constexpr int WM = TT >= 4 ? 2 : 1, WN = 8 / WM;
+  static constexpr int MT = TT / WM, NT = 8 / WN;  // 32 x 32 tiles of a wave
+  static constexpr int AF = 2 * TT;                // 1 KB operand fragments of a stage
+};
+
+// kCodes: group codes of 64 columns of a row, 2 for g = 32, else 1.
+template <int TT, int kCodes>
+__global__ __launch_bounds__(kMainThreads) void bwd_main_kernel(const BwdArgs a) {
+  using S = MainShape<TT>;
+  constexpr int kALoads = (S::AF + 7) / 8;
+  __shared__ h8 sA[2][S::AF][64];
+  __shared__ h8 sB[2][32 * 32];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int CB = (int)((a.D + 255) / 256), ntiles = (int)(a.n32 / 32), TB = (ntiles + TT - 1) / TT;
+  const int cb = blockIdx.x % CB, tb = blockIdx.x / CB % TB, split = blockIdx.x / CB / TB;
+  const int stages = a.ksteps / 2;
+  const int s0 = (int)((int64_t)split * stages / a.splits), s1 = (int)((int64_t)(split + 1) * stages / a.splits);
+
+  // this wave's share of unpacking: 16 rows x 64 columns
+  const int blk = (wave >> 1) & 1, kth = wave >> 2, whalf = wave & 1;
+  const int kt = std::min(2 * cb + kth, a.nkt - 1);
+  const int wrow = 16 * blk + (lane & 15);
+  const uint8_t* wsrc = a.r_codes + (int64_t)kt * a.nb * 1024 + lane * 16 + 8 * whalf;
+  const int group = (kKTile * kt + 64 * whalf) / a.g;
+  u2 w;
+  uint32_t code;
+  h8 av[kALoads];
+  auto load = [&](int s) {
+    const int64_t b = std::min<int64_t>(2 * (int64_t)s + blk, a.nb - 1);  // past the end: dY is zero
+    w = *reinterpret_cast<const u2*>(wsrc + b * 1024);
+    const uint8_t* c = a.r_gcodes + (16 * b + (lane & 15)) * a.ng + group;
+    code = kCodes == 2 ? *reinterpret_cast<const uint16_t*>(c) : *c;
+#pragma unroll
+    for (int i = 0; i < kALoads; ++i) {
+      const int f = std::min(8 * i + wave, S::AF - 1);
+      const int64_t tile = std::min(tb * TT + f / 2, ntiles - 1);
+      av[i] = *reinterpret_cast<const h8*>(a.hf + ((tile * a.ksteps + 2 * s + f % 2) * 64 + lane) * 8);
+    }
+  };
+  auto store = [&](int buf) {
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      const uint32_t c = kCodes == 2 ? (code >> (8 * d)) & 0xffu : code;
+      sB[buf][tile_octet(wrow, 16 * kth + 4 * (2 * whalf + d) + (lane >> 4))] =
+          unpack_q4_scaled(w[d], (_Float16)(float)c);
+    }
+#pragma unroll
+    for (int i = 0; i < kALoads; ++i)
+      if (8 * i + wave < S::AF) sA[buf][8 * i + wave][lane] = av[i];
+  };
+
+  f16x acc[S::MT][S::NT] = {};
+  const int q = lane & 15, colhalf = (lane >> 4) & 1, khalf = lane >> 5;
+  auto compute = [&](int buf) {
+    const _Float16* B = reinterpret_cast<const _Float16*>(sB[buf]);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      h8 b[S::NT];
+#pragma unroll
+      for (int c = 0; c < S::NT; ++c) {
+        const int ct = wn * S::NT + c;
+        h4 x[2];
+#pragma unroll
+        for (int rr = 0; rr < 2; ++rr) {
+          const int k = 16 * t + 8 * khalf + 4 * rr + q / 4;
+          x[rr] = read_tr(B + 8 * tile_octet(k, 4 * ct + 2 * colhalf + (q & 3) / 2) + 4 * (q & 1));
+        }
+        b[c] = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
+      }
+#pragma unroll
+      for (int m = 0; m < S::MT; ++m) {
+        const h8 av_ = sA[buf][2 * (wm * S::MT + m) + t][lane];
+#pragma unroll
+        for (int c = 0; c < S::NT; ++c) acc[m][c] = mfma32(av_, b[c], acc[m][c]);
+      }
+    }
+  };
+  if (s0 < s1) {
+    load(s0);
+    store(0);
+    __syncthreads();
+    for (int s = s0; s < s1; ++s) {
+      if (s + 1 < s1) load(s + 1);
+      compute((s - s0) & 1);
+      if (s + 1 < s1) store((s + 1 - s0) & 1);
+      __syncthreads();
+    }
+  }
+  // columns sit in the tile in the order the unpacking gives them
+  const int c32 = lane & 31;
+#pragma unroll
+  for (int m = 0; m < S::MT; ++m)
+#pragma unroll
+    for (int c = 0; c < S::NT; ++c) {
+      const int64_t d = 256 * (int64_t)cb + 32 * (wn * S::NT + c) + 8 * (c32 >> 3) + k_order_h(c32 & 7);
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int64_t n = 32 * (int64_t)(tb * TT + wm * S::MT + m) + 8 * (v >> 2) + 4 * khalf + (v & 3);
+        if (n < a.N && d < a.D) a.part[((int64_t)split * a.N + n) * a.D + d] = acc[m][c][v];
+      }
+    }
+}
+
+// Grid (blocks of kFinishRows rows, 256-column blocks), four waves: each takes
+// a quarter of the splits and of the ranks for all of the rows and columns
+// (four a lane), in fp32; the waves' sums are added in order.
+__global__ __launch_bounds__(kFinishThreads) void bwd_finish_kernel(const BwdArgs a) {
+  constexpr int kWaves = kFinishThreads / 64;
+  extern __shared__ float sZ[];  // [kFinishRows][r]
+  __shared__ f4 red[kWaves][kFinishRows][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * kFinishRows, d = 256 * (int64_t)blockIdx.y + 4 * lane;
+  const int rows = (int)std::min<int64_t>(kFinishRows, a.N - n0), r = a.r_c + a.r_r;
+  for (int e = tid; e < kFinishRows * r; e += kFinishThreads) {
+    const int i = e / r, j = e % r;
+    float z = 0.0f;
+    if (i < rows) {
+      for (int p = 0; p < a.zparts; ++p) z += a.z[((int64_t)p * a.n32 + n0 + i) * r + j];
+      z *= a.rscale[(n0 + i) * 3 + (j < a.r_c ? 1 : 2)];
+    }
+    sZ[e] = z;
+  }
+  __syncthreads();
+  const bool in = d < a.D;
+  f4 acc[kFinishRows] = {};
+  if (in) {
+    for (int i = 0; i < rows; ++i) {
+      f4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int p = wave; p < a.splits; p += kWaves)
+        y += *reinterpret_cast<const f4*>(a.part + ((int64_t)p * a.N + n0 + i) * a.D + d);
+      const float s = a.rscale[(n0 + i) * 3];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] *= s;
+#pragma unroll
+      for (int k = 0; k < kFinishRows; ++k)
+        if (k == i) acc[k] = y;
+    }
+    const int64_t group = d / a.g;
+#pragma unroll 4
+    for (int j = wave; j < r; j += kWaves) {
+      const uint32_t c = *reinterpret_cast<const uint32_t*>(a.b_codes + (int64_t)j * a.D + d);
+      const float s = f16_to_f32(a.b_scales[(int64_t)j * a.ng + group]);
+      float b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = s * (float)(int8_t)(c >> (8 * e));
+#pragma unroll
+      for (int i = 0; i < kFinishRows; ++i) {
+        const float z = sZ[i * r + j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(z, b[e], acc[i][e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kFinishRows; ++i) red[wave][i][lane] = acc[i];
+  __syncthreads();
+  for (int i = wave; i < rows; i += kWaves) {
+    f4 y = red[0][i][lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) y += red[w][i][lane];
+    if (in) {
+      uint16_t* out = a.dH + (n0 + i) * a.dh_stride + d;
+      typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(2)));
+      *reinterpret_cast<u2_any*>(out) = pack_bf16x4(y[0], y[1], y[2], y[3]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- host ---
+
+int main_tiles(int64_t N) { return N <= 32 ? 1 : N <= 64 ? 2 : N <= 128 ? 4 : 8; }
+
+// Parts of the vocabulary for the main kernel: the fewest whose workgroups
+// fill whole rounds of the resident ones (one a CU for 256-token tiles, two
+// for smaller ones) to within 4%, at least 8 stages each.
+int main_splits(int64_t N, int64_t D, int64_t stages) {
+  const int tt = main_tiles(N);
+  const int64_t tiles = (N + 32 * tt - 1) / (32 * tt) * ((D + 255) / 256);
+  const int64_t slots = tt == 8 ? 256 : 512;
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, stages / 8));
+  double best = 1e30;
+  int pick = 1;
+  for (int64_t p = 1; p <= most; ++p) {
+    const double rounds = (double)((tiles * p + slots - 1) / slots) / (double)p;
+    if (rounds < 0.96 * best) {
+      best = rounds;
+      pick = (int)p;
+    }
+  }
+  return pick;
+}
+
+struct BwdLayout {
+  int64_t rows, n32, ksteps, width;
+  int pieces, zparts, splits;
+  uint64_t pmax, rscale, hf, z, part, total;
+};
+
+BwdLayout bwd_layout(const archead_dims* d, int64_t n_tokens) {
+  BwdLayout L{};
+  L.rows = std::min(n_tokens, kBwdChunkRows);
+  if (L.rows <= 0) return L;
+  const int64_t V32 = (int64_t)round_up((uint64_t)d->V, 32), r = d->r_c + d->r_r;
+  L.n32 = (int64_t)round_up((uint64_t)L.rows, 32);
+  L.ksteps = V32 / 16;
+  L.pieces = (int)std::max<int64_t>(
+      1, std::min<int64_t>({(int64_t)kMaxMaxPieces, (d->V + 2047) / 2048, 8192 / L.rows}));
+  L.width = (int64_t)round_up((uint64_t)((d->V + L.pieces - 1) / L.pieces), 8);
+  L.zparts = (int)std::max<int64_t>(1, std::min<int64_t>({64, (L.ksteps + 31) / 32, 1024 * 32 / L.n32}));
+  L.splits = main_splits(L.rows, d->D, L.ksteps / 2);
+  auto take = [&](uint64_t bytes) {
+    const uint64_t at = L.total;
+    L.total += round_up(bytes, ARCHEAD_ALIGNMENT);
+    return at;
+  };
+  L.pmax = take((uint64_t)L.rows * L.pieces * 12);
+  L.rscale = take((uint64_t)L.n32 * 12);
+  L.hf = take((uint64_t)L.n32 * V32 * 2);
+  L.z = take((uint64_t)L.zparts * L.n32 * r * 4);
+  L.part = take((uint64_t)L.splits * L.rows * d->D * 4);
+  return L;
+}
+
+// Workspace of a call: of its chunks of kBwdChunkRows rows, or of the last, smaller one.
+uint64_t bwd_bytes(const archead_dims* d, int64_t n_tokens) {
+  return std::max(bwd_layout(d, n_tokens).total, bwd_layout(d, n_tokens % kBwdChunkRows).total);
+}
+
+template <int TT>
+void launch_main_tt(const BwdArgs& a, hipStream_t s) {
+  const int64_t tb = (a.n32 / 32 + TT - 1) / TT, cb = (a.D + 255) / 256;
+  const dim3 grid((unsigned)(tb * cb * a.splits)), block(kMainThreads);
+  if (a.g == 32)
+    hipLaunchKernelGGL((bwd_main_kernel<TT, 2>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((bwd_main_kernel<TT, 1>), grid, block, 0, s, a);
+}
+
+template <typename T>
+hipError_t launch_backward(const BwdArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(bwd_max_kernel<T>, dim3((unsigned)(a.N * a.pieces)), dim3(kMaxThreads), 0, s, a);
+  const int groups = std::max(1, (a.nct + a.nwt + kRankTiles - 1) / kRankTiles);
+  hipLaunchKernelGGL(bwd_prep_kernel<T>, dim3((unsigned)(a.n32 / 32), (unsigned)a.zparts, (unsigned)groups),
+                     dim3(kPrepThreads), 0, s, a);
+  switch (main_tiles(a.N)) {
+    case 1: launch_main_tt<1>(a, s); break;
+    case 2: launch_main_tt<2>(a, s); break;
+    case 4: launch_main_tt<4>(a, s); break;
+    default: launch_main_tt<8>(a, s);
+  }
+  hipLaunchKernelGGL(bwd_finish_kernel, dim3((unsigned)((a.N + kFinishRows - 1) / kFinishRows), (unsigned)((a.D + 255) / 256)),
+                     dim3(kFinishThreads), (size_t)kFinishRows * (a.r_c + a.r_r) * 4, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace archead
+
+using namespace archead;
+
+extern "C" {
+
+int archead_logits_backward_workspace_bytes(const archead_dims* d, int64_t n_tokens, uint64_t* bytes) {
+  if (!d || !bytes) return ARCHEAD_E_NULL;
+  if (int rc = check_dims(d)) return rc;
+  if (int rc = check_archead_format(d)) return rc;
+  if (n_tokens < 0) return ARCHEAD_E_SHAPE;
+  *bytes = bwd_bytes(d, n_tokens);
+  return ARCHEAD_OK;
+}
+
+int archead_logits_backward(const archead_tensor* dY, const archead_packed_head* head, archead_tensor* dH,
+                            void* stream) {
+  if (!dY || !head || !dH) return ARCHEAD_E_NULL;
+  const archead_dims* d = &head->dims;
+  if (int rc = check_kernel_dims(d)) return rc;
+  if (int rc = check_archead_format(d)) return rc;
+  if ((dY->dtype != ARCHEAD_BF16 && dY->dtype != ARCHEAD_F32) || dH->dtype != ARCHEAD_BF16) return ARCHEAD_E_DTYPE;
+  const int64_t N = dY->rows;
+  if (N < 0 || dY->cols != d->V || dY->row_stride < d->V) return ARCHEAD_E_SHAPE;
+  if (dH->rows != N || dH->cols != d->D || dH->row_stride < d->D) return ARCHEAD_E_SHAPE;
+  // 32-bit row and tile counts; Z of kFinishRows rows in LDS
+  if (N > (int64_t(1) << 22) || d->V > (int64_t(1) << 30) || d->r_c + d->r_r > kMaxRank) return ARCHEAD_E_UNSUPPORTED;
+  if (N == 0) return ARCHEAD_OK;
+  if (!dY->data || !dH->data || !head->buffer || !head->workspace) return ARCHEAD_E_NULL;
+  const int size = dY->dtype == ARCHEAD_F32 ? 4 : 2;
+  if ((uintptr_t)dY->data % size || (uintptr_t)dH->data % 2) return ARCHEAD_E_ALIGN;
+  if ((uintptr_t)head->buffer % ARCHEAD_ALIGNMENT || (uintptr_t)head->workspace % ARCHEAD_ALIGNMENT)
+    return ARCHEAD_E_ALIGN;
+  archead_layout P;
+  compute_layout(d, &P);
+  if (head->buffer_bytes < P.total_bytes) return ARCHEAD_E_SIZE;
+  if (head->workspace_bytes < bwd_bytes(d, N)) return ARCHEAD_E_WORKSPACE;
+  const uint8_t* buf = static_cast<const uint8_t*>(head->buffer);
+  uint8_t* ws = static_cast<uint8_t*>(head->workspace);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();  // start from a clean error state
+  for (int64_t n0 = 0; n0 < N; n0 += kBwdChunkRows) {
+    const BwdLayout L = bwd_layout(d, std::min(kBwdChunkRows, N - n0));
+    BwdArgs a{};
+    a.V = d->V;
+    a.D = d->D;
+    a.N = L.rows;
+    a.n32 = L.n32;
+    a.nb = P.padded_rows / 16;
+    a.r_c = d->r_c;
+    a.r_r = d->r_r;
+    a.g = d->g;
+    a.ng = (int)(d->D / d->g);
+    a.nkt = (int)(d->D / kKTile);
+    a.nA = (d->r_c > 0) + (d->r_r > 0);
+    a.nct = (d->r_c + 31) / 32;
+    a.nwt = (d->r_r + 31) / 32;
+    a.dY = static_cast<const uint8_t*>(dY->data) + (uint64_t)n0 * (uint64_t)dY->row_stride * size;
+    a.dy_stride = dY->row_stride;
+    a.dH = static_cast<uint16_t*>(dH->data) + n0 * dH->row_stride;
+    a.dh_stride = dH->row_stride;
+    a.r_codes = buf + P.r_codes.offset;
+    a.r_gcodes = buf + P.r_gcodes.offset;
+    a.r_rowscale = reinterpret_cast<const uint16_t*>(buf + P.r_rowscale.offset);
+    a.a_codes = reinterpret_cast<const int8_t*>(buf + P.a_codes.offset);
+    a.a_scales = reinterpret_cast<const uint16_t*>(buf + P.a_scales.offset);
+    a.b_codes = reinterpret_cast<const int8_t*>(buf + P.b_codes.offset);
+    a.b_scales = reinterpret_cast<const uint16_t*>(buf + P.b_scales.offset);
+    a.pmax = reinterpret_cast<float*>(ws + L.pmax);
+    a.rscale = reinterpret_cast<float*>(ws + L.rscale);
+    a.hf = reinterpret_cast<_Float16*>(ws + L.hf);
+    a.z = reinterpret_cast<float*>(ws + L.z);
+    a.part = reinterpret_cast<float*>(ws + L.part);
+    a.pieces = L.pieces;
+    a.zparts = L.zparts;
+    a.splits = L.splits;
+    a.ksteps = (int)L.ksteps;
+    a.width = L.width;
+    const hipError_t e = size == 4 ? launch_backward<float>(a, s) : launch_backward<uint16_t>(a, s);
+    if (e != hipSuccess) return ARCHEAD_E_HIP;
+  }
+  return ARCHEAD_OK;
+}
+
+}  // extern "C"

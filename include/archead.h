@@ -593,6 +593,29 @@ ARCHEAD_API int archead_preference_loss(const archead_tensor* Y, const archead_p
                                         const archead_preference_outputs* out, void* workspace,
                                         uint64_t workspace_bytes, void* stream);
 
+/* Device workspace archead_logits_backward needs for n_tokens rows: for
+ * min(n_tokens, 4096) rows, dY as fp16 operands (2 V32 bytes a row, rows and
+ * vocabulary rounded up to 32), fp32 partial sums of dH and of its low-rank
+ * part, and row scales.  Pure host arithmetic.  E_NULL, E_DIMS, E_SHAPE,
+ * E_UNSUPPORTED. */
+ARCHEAD_API int archead_logits_backward_workspace_bytes(const archead_dims* d, int64_t n_tokens, uint64_t* bytes);
+
+/* dH = dY W_hat, the gradient of the hidden states through the packed head
+ * (the transpose of archead_logits; the head itself is not trained).
+ *   dY: fp32 or bf16 [N][V] device tensor, any row stride, aligned to its
+ *       element size.  Rows of zeros give rows of zeros.
+ *   dH: bf16 [N][D] device tensor, any row stride, written completely.
+ * dY times the head's row scales is rounded to fp16 (after a power of two per
+ * row that keeps the row's largest product near the top of the range), the
+ * head's integers are exact, all sums are fp32, and dH is rounded to nearest
+ * even.  A row of dY that is not finite gives a row of dH that is not.
+ * head->workspace: at least archead_logits_backward_workspace_bytes.  Rows
+ * are taken 4096 at a time.  ARCHead-format heads only, r_c + r_r at most
+ * 1024.  E_NULL, E_DIMS, E_DTYPE, E_SHAPE, E_UNSUPPORTED, E_ALIGN, E_SIZE,
+ * E_WORKSPACE, E_HIP. */
+ARCHEAD_API int archead_logits_backward(const archead_tensor* dY, const archead_packed_head* head,
+                                        archead_tensor* dH, void* stream);
+
 /* Static string naming a status code. */
 ARCHEAD_API const char* archead_status_string(int status);
 
