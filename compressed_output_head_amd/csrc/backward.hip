@@ -11,8 +11,10 @@
 // entry to the next.  The scale is taken from the products themselves, so a
 // gradient that sits on vocabulary entries of tiny scales keeps its digits.
 //
-//   bwd_max_kernel     per row: the largest |dY s_R|, |dY s_Ac|, |dY s_Aw|
-//   bwd_prep_kernel    dY s_R as fp16 operand fragments; Z in fp32
+//   bwd_max_kernel     per row: the largest |dY s_R|, |dY s_Ac|, |dY s_Aw|;
+//                      beside that, the A codes in operand order
+//   bwd_prep_kernel    dY s_R as fp16 operand fragments; parts of Z
+//   bwd_zsum_kernel    Z in fp32
 //   bwd_main_kernel    the product with the packed residual, the vocabulary
 //                      split over several workgroups where tiles are few
 //   bwd_finish_kernel  the splits' sums and Z B to dH
@@ -30,11 +32,11 @@ namespace {
 
 constexpr int64_t kBwdChunkRows = 4096;  // rows of dY a pass takes
 constexpr int kMaxThreads = 256;
-constexpr int kPrepThreads = 256;
+constexpr int kMaxRows = 4;
+constexpr int kPrepWaves = 4;       // and 32-rank tiles of Z that a workgroup forms
 constexpr int kMainThreads = 512;
 constexpr int kFinishThreads = 256;
 constexpr int kFinishRows = 8;
-constexpr int kRankTiles = 4;       // 32-rank tiles of Z a workgroup forms in one walk
 constexpr int kMaxMaxPieces = 32;
 constexpr int kMaxSplits = 64;
 
@@ -57,7 +59,9 @@ struct BwdArgs {
   float* pmax;      // [N][pieces][3]
   float* rscale;    // [n32][3] powers of two that undo the rows' scales
   _Float16* hf;     // [n32/32][ksteps][64][8]
-  float* z;         // [zparts][n32][r_c + r_r]
+  uint8_t* af;      // A codes, [32-rank tiles][ksteps][64][8]
+  float* zpart;     // [zparts][n32][r_c + r_r]
+  float* z;         // [n32][r_c + r_r]
   float* part;      // [splits][N][D]
   int pieces, zparts, splits, ksteps;
   int64_t width;    // columns of a piece of bwd_max_kernel
@@ -123,54 +127,88 @@ __device__ __forceinline__ Scales8 scales8(const BwdArgs& a, int64_t v) {
   return s;
 }
 
-// Workgroup n pieces + p: the largest products of piece p of row n.
+// Thread i of the layout of the A codes: lane i % 64 of vocabulary step
+// (i / 64) % ksteps of rank tile i / 64 / ksteps gets the codes of rank
+// lane % 32 at 8 vocabulary rows, in the byte order that unpack_i8x8 turns into theirs.
+__device__ __forceinline__ void arrange_codes(const BwdArgs& a, int64_t i) {
+  const int lane = (int)(i & 63), c32 = lane & 31;
+  const int64_t step = (i >> 6) % a.ksteps, t = (i >> 6) / a.ksteps;
+  if (t >= a.nct + a.nwt) return;
+  const bool in_c = t < a.nct;
+  const int j = 32 * (int)(in_c ? t : t - a.nct) + c32, r = a.r_c + a.r_r;
+  const bool valid = j < (in_c ? a.r_c : a.r_r);
+  const int64_t v = 16 * step + 8 * (lane >> 5), V16 = 16 * a.nb;
+  const uint8_t* codes = reinterpret_cast<const uint8_t*>(a.a_codes) + (in_c ? 0 : a.r_c) + (valid ? j : 0);
+  uint32_t b[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) b[k] = valid && v + k < V16 ? codes[(v + k) * r] : 0u;
+  reinterpret_cast<u2*>(a.af)[i] = u2{b[0] | b[2] << 8 | b[1] << 16 | b[3] << 24, b[4] | b[6] << 8 | b[5] << 16 | b[7] << 24};
+}
+
+// Workgroup q pieces + p: the largest products of piece p of rows kMaxRows q
+// .. + kMaxRows, which share the scales they are multiplied with.  The
+// workgroups behind those lay the A codes out for bwd_prep_kernel, which the
+// rows do not wait for.
 template <typename T>
 __global__ __launch_bounds__(kMaxThreads) void bwd_max_kernel(const BwdArgs a) {
-  __shared__ float buf[3][kMaxThreads / 64];
-  const int64_t n = blockIdx.x / a.pieces;
+  constexpr int kWaves = kMaxThreads / 64;
+  __shared__ float buf[kWaves][kMaxRows][3];
+  const int64_t groups = (a.N + kMaxRows - 1) / kMaxRows;
+  if ((int64_t)blockIdx.x >= groups * a.pieces) {
+    arrange_codes(a, ((int64_t)blockIdx.x - groups * a.pieces) * kMaxThreads + threadIdx.x);
+    return;
+  }
+  const int64_t n0 = blockIdx.x / a.pieces * kMaxRows;
   const int p = (int)(blockIdx.x % a.pieces);
-  const T* row = static_cast<const T*>(a.dY) + n * a.dy_stride;
   const int64_t end = (p + 1) * a.width < a.V ? (p + 1) * a.width : a.V;
-  float m[3] = {0.0f, 0.0f, 0.0f};
+  float m[kMaxRows][3] = {};
   for (int64_t v = p * a.width + 8 * threadIdx.x; v < end; v += 8 * kMaxThreads) {
-    float x[8];
-    load8_to(row, v, end, x);
+    float x[kMaxRows][8];
+#pragma unroll
+    for (int i = 0; i < kMaxRows; ++i)  // rows past the end: the last one again
+      load8_to(static_cast<const T*>(a.dY) + (n0 + i < a.N ? n0 + i : a.N - 1) * a.dy_stride, v, end, x[i]);
     const Scales8 s = scales8(a, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m[0] = fmaxf(m[0], fabsf(x[j] * s.R[j]));
-      m[1] = fmaxf(m[1], fabsf(x[j] * s.c[j]));
-      m[2] = fmaxf(m[2], fabsf(x[j] * s.w[j]));
-    }
+    for (int i = 0; i < kMaxRows; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m[i][0] = fmaxf(m[i][0], fabsf(x[i][j] * s.R[j]));
+        m[i][1] = fmaxf(m[i][1], fabsf(x[i][j] * s.c[j]));
+        m[i][2] = fmaxf(m[i][2], fabsf(x[i][j] * s.w[j]));
+      }
   }
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    for (int o = 32; o > 0; o >>= 1) m[q] = fmaxf(m[q], __shfl_xor(m[q], o));
-    if ((threadIdx.x & 63) == 0) buf[q][threadIdx.x >> 6] = m[q];
-  }
+  for (int i = 0; i < kMaxRows; ++i)
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      for (int o = 32; o > 0; o >>= 1) m[i][q] = fmaxf(m[i][q], __shfl_xor(m[i][q], o));
+      if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6][i][q] = m[i][q];
+    }
   __syncthreads();
-  if (threadIdx.x < 3) {
-    float t = buf[threadIdx.x][0];
-    for (int w = 1; w < kMaxThreads / 64; ++w) t = fmaxf(t, buf[threadIdx.x][w]);
-    a.pmax[(n * a.pieces + p) * 3 + threadIdx.x] = t;
+  const int i = threadIdx.x / 3, q = threadIdx.x % 3;
+  if (i < kMaxRows && n0 + i < a.N) {
+    float t = buf[0][i][q];
+    for (int w = 1; w < kWaves; ++w) t = fmaxf(t, buf[w][i][q]);
+    a.pmax[((n0 + i) * a.pieces + p) * 3 + q] = t;
   }
 }
 
-// Grid (32-row tiles, parts of the vocabulary, groups of kRankTiles rank
-// tiles), four waves that take 128-column runs in turn.  In the operand's
-// layout lane l holds row l % 32 and columns 16 step + 8 (l / 32) .. + 8, for
-// which it loads 16 bytes of its row (32 of fp32) and the scales.  Rank tile
-// t of Z: the same lanes' dY s_A against the codes of ranks 32 t .. + 32,
-// gathered byte by byte (V r bytes in all, from the cache).
+// Grid (32-row tiles, parts of the vocabulary, groups of kPrepWaves rank
+// tiles).  A run of 128 columns of the 32 rows is read as whole 256-byte
+// pieces of rows (512 of fp32), multiplied with each of the three scales,
+// rounded to fp16 and put in LDS in the MFMA operand's order (lane l: row
+// l % 32, columns 16 step + 8 (l / 32) .. + 8).  From there dY s_R goes to
+// memory, 1 KB a store, and wave w multiplies dY s_A of its rank tile with
+// the codes that arrange_codes laid out.
 template <typename T>
-__global__ __launch_bounds__(kPrepThreads) void bwd_prep_kernel(const BwdArgs a) {
-  constexpr int kWaves = kPrepThreads / 64;
+__global__ __launch_bounds__(64 * kPrepWaves) void bwd_prep_kernel(const BwdArgs a) {
   __shared__ int sExp[3][32];
-  __shared__ float red[kWaves][32][33];
+  __shared__ h8 frag[3][8][66];  // steps two octets apart, so that a wave's writes meet no bank twice
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t tile = blockIdx.x, n = 32 * tile + c32;
-  const int part = blockIdx.y, t0 = kRankTiles * (int)blockIdx.z;
+  const int64_t tile = blockIdx.x;
+  const int part = blockIdx.y;
+  const bool first = blockIdx.z == 0;
   if (tid < 96) {
     const int q = tid / 32;
     const int64_t row = 32 * tile + tid % 32;
@@ -179,72 +217,88 @@ __global__ __launch_bounds__(kPrepThreads) void bwd_prep_kernel(const BwdArgs a)
       for (int p = 0; p < a.pieces; ++p) m = fmaxf(m, a.pmax[(row * a.pieces + p) * 3 + q]);
     const int S = row_exponent(m);
     sExp[q][tid % 32] = S;
-    if (part == 0 && blockIdx.z == 0) a.rscale[row * 3 + q] = ldexpf(1.0f, -S);
+    if (part == 0 && first) a.rscale[row * 3 + q] = ldexpf(1.0f, -S);
   }
   __syncthreads();
-  const int eR = sExp[0][c32], ec = sExp[1][c32], ew = sExp[2][c32];
-  const bool real = n < a.N;
-  const T* row = static_cast<const T*>(a.dY) + (real ? n : 0) * a.dy_stride;
+  // this thread's rows and columns of a run: octet tid % 16 of rows tid / 16 and + 16
+  const int oct = tid & 15;
+  int e[2][3];
+  const T* row[2];
+  bool real[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int rr = (tid >> 4) + 16 * i;
+    real[i] = 32 * tile + rr < a.N;
+    row[i] = static_cast<const T*>(a.dY) + (real[i] ? 32 * tile + rr : 0) * a.dy_stride;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) e[i][q] = sExp[q][rr];
+  }
   const int64_t V16 = 16 * a.nb;
   const int r = a.r_c + a.r_r, tiles = a.nct + a.nwt;
-  const int runs = (a.ksteps + 7) / 8;  // of 8 steps
+  const int t = kPrepWaves * (int)blockIdx.z + wave;  // this wave's rank tile
+  const bool in_c = t < a.nct;
+  const int runs = (a.ksteps + 7) / 8;
   const int run0 = (int)((int64_t)part * runs / gridDim.y), run1 = (int)((int64_t)(part + 1) * runs / gridDim.y);
-  f16x acc[kRankTiles] = {};
-  for (int run = run0 + wave; run < run1; run += kWaves) {
-#pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
-      const int step = 8 * run + i;
-      if (step >= a.ksteps) break;
-      const int64_t v = 16 * (int64_t)step + 8 * half;
-      float x[8] = {};
-      if (real) load8_to(row, v, a.V, x);
-      const int64_t vs = v < V16 ? v : V16 - 8;  // past V16 dY is zero
-      const Scales8 s = scales8(a, vs);
-      if (blockIdx.z == 0) {
-        h8 f;
+  const u2* codes = reinterpret_cast<const u2*>(a.af) + (int64_t)(t < tiles ? t : 0) * a.ksteps * 64 + lane;
+  f16x acc = {};
+  for (int run = run0; run < run1; ++run) {
+    const int64_t v = 128 * (int64_t)run + 8 * oct;
+    float x[2][8] = {};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = (_Float16)ldexpf(x[j] * s.R[j], eR);
-        *reinterpret_cast<h8*>(a.hf + ((tile * a.ksteps + step) * 64 + lane) * 8) = f;
-      }
-      if (t0 >= tiles) continue;
-      h8 fc, fw;
+    for (int i = 0; i < 2; ++i)
+      if (real[i]) load8_to(row[i], v, a.V, x[i]);
+    const Scales8 s = scales8(a, v < V16 ? v : V16 - 8);  // past V16 dY is zero
+    u2 b[8];
+    if (t < tiles) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) b[k] = codes[std::min(8 * run + k, a.ksteps - 1) * 64];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      h8 f[3];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        fc[j] = (_Float16)ldexpf(x[j] * s.c[j], ec);
-        fw[j] = (_Float16)ldexpf(x[j] * s.w[j], ew);
+        f[0][j] = (_Float16)ldexpf(x[i][j] * s.R[j], e[i][0]);
+        f[1][j] = (_Float16)ldexpf(x[i][j] * s.c[j], e[i][1]);
+        f[2][j] = (_Float16)ldexpf(x[i][j] * s.w[j], e[i][2]);
       }
+      const int at = 32 * (oct & 1) + (tid >> 4) + 16 * i;
 #pragma unroll
-      for (int q = 0; q < kRankTiles; ++q) {
-        const int t = t0 + q;
-        if (t >= tiles) break;
-        const bool in_c = t < a.nct;
-        const int j = 32 * (in_c ? t : t - a.nct) + c32;
-        const bool valid = j < (in_c ? a.r_c : a.r_r);
-        const int8_t* codes = a.a_codes + vs * r + (in_c ? 0 : a.r_c) + (valid ? j : 0);
-        h8 b;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) b[k] = (_Float16)(float)(valid ? codes[(int64_t)k * r] : 0);
-        acc[q] = mfma32(in_c ? fc : fw, b, acc[q]);
-      }
+      for (int q = 0; q < 3; ++q) frag[q][oct >> 1][at] = f[q];
     }
-  }
-  for (int q = 0; q < kRankTiles; ++q) {
-    const int t = t0 + q;
-    if (t >= tiles) break;
-    const bool in_c = t < a.nct;
-    const int j0 = 32 * (in_c ? t : t - a.nct), rank = in_c ? a.r_c : a.r_r;
     __syncthreads();
+    if (first) {
 #pragma unroll
-    for (int v = 0; v < 16; ++v) red[wave][8 * (v >> 2) + 4 * half + (v & 3)][c32] = acc[q][v];
-    __syncthreads();
-    for (int e = tid; e < 32 * 32; e += kPrepThreads) {
-      const int i = e >> 5, j = e & 31;
-      float z = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) z += red[w][i][j];
-      if (j0 + j < rank) a.z[((int64_t)part * a.n32 + 32 * tile + i) * r + (in_c ? 0 : a.r_c) + j0 + j] = z;
+      for (int k = wave; k < 8; k += kPrepWaves)
+        if (8 * run + k < a.ksteps)
+          *reinterpret_cast<h8*>(a.hf + ((tile * a.ksteps + 8 * run + k) * 64 + lane) * 8) = frag[0][k][lane];
     }
+    if (t < tiles) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)  // past the last step dY is zero
+        acc = mfma32(frag[in_c ? 1 : 2][k][lane], unpack_i8x8(b[k][0], b[k][1]), acc);
+    }
+    __syncthreads();
   }
+  if (t >= tiles) return;
+  const int j = 32 * (in_c ? t : t - a.nct) + c32;
+  if (j >= (in_c ? a.r_c : a.r_r)) return;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) {
+    const int i = 8 * (v >> 2) + 4 * half + (v & 3);
+    a.zpart[((int64_t)part * a.n32 + 32 * tile + i) * r + (in_c ? 0 : a.r_c) + j] = acc[v];
+  }
+}
+
+// Z from its parts of the vocabulary, in order, with the rows' scales undone.
+__global__ __launch_bounds__(kMaxThreads) void bwd_zsum_kernel(const BwdArgs a) {
+  const int r = a.r_c + a.r_r;
+  const int64_t i = (int64_t)blockIdx.x * kMaxThreads + threadIdx.x, count = a.n32 * r;
+  if (i >= count) return;
+  float z = 0.0f;
+#pragma unroll 8
+  for (int p = 0; p < a.zparts; ++p) z += a.zpart[p * count + i];
+  a.z[i] = z * a.rscale[i / r * 3 + (i % r < a.r_c ? 1 : 2)];
 }
 
 // Place of 16-byte octet o (8 columns) of row k in a stage's fp16 tile of 32
@@ -371,69 +425,83 @@ __global__ __launch_bounds__(kMainThreads) void bwd_main_kernel(const BwdArgs a)
     }
 }
 
-// Grid (blocks of kFinishRows rows, 256-column blocks), four waves: each takes
-// a quarter of the splits and of the ranks for all of the rows and columns
-// (four a lane), in fp32; the waves' sums are added in order.
+// kFinishRows rows x 256 columns of dH, four columns a lane: the splits' sums
+// and Z B, in fp32.  Few rows: the four waves of a workgroup take a quarter
+// each of the splits and of the ranks, and their sums are added in order.
+// Many rows: every wave has rows of its own.
+template <bool kShared>
 __global__ __launch_bounds__(kFinishThreads) void bwd_finish_kernel(const BwdArgs a) {
-  constexpr int kWaves = kFinishThreads / 64;
-  extern __shared__ float sZ[];  // [kFinishRows][r]
-  __shared__ f4 red[kWaves][kFinishRows][64];
+  constexpr int kWaves = kFinishThreads / 64, kRows = kFinishRows;
+  extern __shared__ __align__(16) float sZ[];  // [r][kRows] (of every wave)
+  __shared__ f4 red[kShared ? kWaves : 1][kShared ? kRows : 1][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * kFinishRows, d = 256 * (int64_t)blockIdx.y + 4 * lane;
-  const int rows = (int)std::min<int64_t>(kFinishRows, a.N - n0), r = a.r_c + a.r_r;
-  for (int e = tid; e < kFinishRows * r; e += kFinishThreads) {
+  const int r = a.r_c + a.r_r;
+  const int64_t n0 = ((int64_t)blockIdx.x * (kShared ? 1 : kWaves) + (kShared ? 0 : wave)) * kRows;
+  const int64_t d = 256 * (int64_t)blockIdx.y + 4 * lane;
+  const int rows = (int)std::max<int64_t>(0, std::min<int64_t>(kRows, a.N - n0));
+  float* Z = sZ + (kShared ? 0 : wave * r * kRows);
+  for (int e = kShared ? tid : lane; e < kRows * r; e += kShared ? kFinishThreads : 64) {
     const int i = e / r, j = e % r;
-    float z = 0.0f;
-    if (i < rows) {
-      for (int p = 0; p < a.zparts; ++p) z += a.z[((int64_t)p * a.n32 + n0 + i) * r + j];
-      z *= a.rscale[(n0 + i) * 3 + (j < a.r_c ? 1 : 2)];
-    }
-    sZ[e] = z;
+    Z[j * kRows + i] = i < rows ? a.z[(n0 + i) * r + j] : 0.0f;
   }
   __syncthreads();
+  const int first = kShared ? wave : 0, step = kShared ? kWaves : 1;
   const bool in = d < a.D;
-  f4 acc[kFinishRows] = {};
+  f4 acc[kRows] = {};
   if (in) {
-    for (int i = 0; i < rows; ++i) {
-      f4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int p = wave; p < a.splits; p += kWaves)
-        y += *reinterpret_cast<const f4*>(a.part + ((int64_t)p * a.N + n0 + i) * a.D + d);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      if (i >= rows) break;
+      for (int p = first; p < a.splits; p += step) {
+        const f4 y = *reinterpret_cast<const f4*>(a.part + ((int64_t)p * a.N + n0 + i) * a.D + d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] += y[e];
+      }
       const float s = a.rscale[(n0 + i) * 3];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] *= s;
-#pragma unroll
-      for (int k = 0; k < kFinishRows; ++k)
-        if (k == i) acc[k] = y;
+      for (int e = 0; e < 4; ++e) acc[i][e] *= s;
     }
     const int64_t group = d / a.g;
 #pragma unroll 4
-    for (int j = wave; j < r; j += kWaves) {
+    for (int j = first; j < r; j += step) {
       const uint32_t c = *reinterpret_cast<const uint32_t*>(a.b_codes + (int64_t)j * a.D + d);
       const float s = f16_to_f32(a.b_scales[(int64_t)j * a.ng + group]);
       float b[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) b[e] = s * (float)(int8_t)(c >> (8 * e));
 #pragma unroll
-      for (int i = 0; i < kFinishRows; ++i) {
-        const float z = sZ[i * r + j];
+      for (int i = 0; i < kRows; i += 4) {
+        const f4 z = *reinterpret_cast<const f4*>(Z + j * kRows + i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(z, b[e], acc[i][e]);
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i + k][e] = fmaf(z[k], b[e], acc[i + k][e]);
       }
     }
   }
+  auto write = [&](int i, f4 y) {
+    typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(2)));
+    if (in) *reinterpret_cast<u2_any*>(a.dH + (n0 + i) * a.dh_stride + d) = pack_bf16x4(y[0], y[1], y[2], y[3]);
+  };
+  if constexpr (kShared) {
 #pragma unroll
-  for (int i = 0; i < kFinishRows; ++i) red[wave][i][lane] = acc[i];
-  __syncthreads();
-  for (int i = wave; i < rows; i += kWaves) {
-    f4 y = red[0][i][lane];
+    for (int i = 0; i < kRows; ++i) red[wave][i][lane] = acc[i];
+    __syncthreads();
+    for (int i = wave; i < rows; i += kWaves) {
+      f4 y = red[0][i][lane];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) y += red[w][i][lane];
-    if (in) {
-      uint16_t* out = a.dH + (n0 + i) * a.dh_stride + d;
-      typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(2)));
-      *reinterpret_cast<u2_any*>(out) = pack_bf16x4(y[0], y[1], y[2], y[3]);
+      for (int w = 1; w < kWaves; ++w) {
+        const f4 x = red[w][i][lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += x[e];
+      }
+      write(i, y);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (i < rows) write(i, acc[i]);
   }
 }
 
@@ -464,7 +532,7 @@ int main_splits(int64_t N, int64_t D, int64_t stages) {
 struct BwdLayout {
   int64_t rows, n32, ksteps, width;
   int pieces, zparts, splits;
-  uint64_t pmax, rscale, hf, z, part, total;
+  uint64_t pmax, rscale, hf, af, zpart, z, part, total;
 };
 
 BwdLayout bwd_layout(const archead_dims* d, int64_t n_tokens) {
@@ -475,9 +543,9 @@ BwdLayout bwd_layout(const archead_dims* d, int64_t n_tokens) {
   L.n32 = (int64_t)round_up((uint64_t)L.rows, 32);
   L.ksteps = V32 / 16;
   L.pieces = (int)std::max<int64_t>(
-      1, std::min<int64_t>({(int64_t)kMaxMaxPieces, (d->V + 2047) / 2048, 8192 / L.rows}));
+      1, std::min<int64_t>({(int64_t)kMaxMaxPieces, (d->V + 2047) / 2048, 2048 * kMaxRows / L.rows}));
   L.width = (int64_t)round_up((uint64_t)((d->V + L.pieces - 1) / L.pieces), 8);
-  L.zparts = (int)std::max<int64_t>(1, std::min<int64_t>({64, (L.ksteps + 31) / 32, 1024 * 32 / L.n32}));
+  L.zparts = (int)std::max<int64_t>(1, std::min<int64_t>({256, (L.ksteps + 31) / 32, 1024 * 32 / L.n32}));
   L.splits = main_splits(L.rows, d->D, L.ksteps / 2);
   auto take = [&](uint64_t bytes) {
     const uint64_t at = L.total;
@@ -487,7 +555,9 @@ BwdLayout bwd_layout(const archead_dims* d, int64_t n_tokens) {
   L.pmax = take((uint64_t)L.rows * L.pieces * 12);
   L.rscale = take((uint64_t)L.n32 * 12);
   L.hf = take((uint64_t)L.n32 * V32 * 2);
-  L.z = take((uint64_t)L.zparts * L.n32 * r * 4);
+  L.af = take((uint64_t)((d->r_c + 31) / 32 + (d->r_r + 31) / 32) * L.ksteps * 512);
+  L.zpart = take((uint64_t)L.zparts * L.n32 * r * 4);
+  L.z = take((uint64_t)L.n32 * r * 4);
   L.part = take((uint64_t)L.splits * L.rows * d->D * 4);
   return L;
 }
@@ -509,18 +579,29 @@ void launch_main_tt(const BwdArgs& a, hipStream_t s) {
 
 template <typename T>
 hipError_t launch_backward(const BwdArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(bwd_max_kernel<T>, dim3((unsigned)(a.N * a.pieces)), dim3(kMaxThreads), 0, s, a);
-  const int groups = std::max(1, (a.nct + a.nwt + kRankTiles - 1) / kRankTiles);
-  hipLaunchKernelGGL(bwd_prep_kernel<T>, dim3((unsigned)(a.n32 / 32), (unsigned)a.zparts, (unsigned)groups),
-                     dim3(kPrepThreads), 0, s, a);
+  const int64_t ranks = a.nct + a.nwt, max_groups = (a.N + kMaxRows - 1) / kMaxRows * a.pieces;
+  hipLaunchKernelGGL(bwd_max_kernel<T>, dim3((unsigned)(max_groups + (ranks * a.ksteps * 64 + kMaxThreads - 1) / kMaxThreads)),
+                     dim3(kMaxThreads), 0, s, a);
+  hipLaunchKernelGGL(bwd_prep_kernel<T>,
+                     dim3((unsigned)(a.n32 / 32), (unsigned)a.zparts, (unsigned)std::max<int64_t>(1, (ranks + kPrepWaves - 1) / kPrepWaves)),
+                     dim3(64 * kPrepWaves), 0, s, a);
+  if (ranks > 0)
+    hipLaunchKernelGGL(bwd_zsum_kernel, dim3((unsigned)((a.n32 * (a.r_c + a.r_r) + kMaxThreads - 1) / kMaxThreads)),
+                       dim3(kMaxThreads), 0, s, a);
   switch (main_tiles(a.N)) {
     case 1: launch_main_tt<1>(a, s); break;
     case 2: launch_main_tt<2>(a, s); break;
     case 4: launch_main_tt<4>(a, s); break;
     default: launch_main_tt<8>(a, s);
   }
-  hipLaunchKernelGGL(bwd_finish_kernel, dim3((unsigned)((a.N + kFinishRows - 1) / kFinishRows), (unsigned)((a.D + 255) / 256)),
-                     dim3(kFinishThreads), (size_t)kFinishRows * (a.r_c + a.r_r) * 4, s, a);
+  const int64_t row_blocks = (a.N + kFinishRows - 1) / kFinishRows, waves = kFinishThreads / 64;
+  const size_t lds = (size_t)kFinishRows * (a.r_c + a.r_r) * 4;
+  const unsigned columns = (unsigned)((a.D + 255) / 256);
+  if (a.N <= 512)
+    hipLaunchKernelGGL(bwd_finish_kernel<true>, dim3((unsigned)row_blocks, columns), dim3(kFinishThreads), lds, s, a);
+  else
+    hipLaunchKernelGGL(bwd_finish_kernel<false>, dim3((unsigned)((row_blocks + waves - 1) / waves), columns),
+                       dim3(kFinishThreads), lds * waves, s, a);
   return hipGetLastError();
 }
 
@@ -596,6 +677,8 @@ int archead_logits_backward(const archead_tensor* dY, const archead_packed_head*
     a.pmax = reinterpret_cast<float*>(ws + L.pmax);
     a.rscale = reinterpret_cast<float*>(ws + L.rscale);
     a.hf = reinterpret_cast<_Float16*>(ws + L.hf);
+    a.af = ws + L.af;
+    a.zpart = reinterpret_cast<float*>(ws + L.zpart);
     a.z = reinterpret_cast<float*>(ws + L.z);
     a.part = reinterpret_cast<float*>(ws + L.part);
     a.pieces = L.pieces;
