@@ -22,10 +22,16 @@
 // rows is unpacked to fp16 in LDS, and the MFMA's operand, which runs along
 // the vocabulary, is read from there by transposing LDS reads.
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "internal.h"
 
+#ifndef D1
+#define D1 4
+#define D4 2
+#define D8 1
+#endif
 namespace archead {
 
 namespace {
@@ -34,10 +40,12 @@ constexpr int64_t kBwdChunkRows = 4096;  // rows of dY a pass takes
 constexpr int kMaxThreads = 256;
 constexpr int kMaxRows = 4;
 constexpr int kPrepWaves = 4;       // and 32-rank tiles of Z that a workgroup forms
+constexpr int kZsumThreads = 512, kZsumRanks = 64;
 constexpr int kMainThreads = 512;
 constexpr int kFinishThreads = 256;
 constexpr int kFinishRows = 8;
 constexpr int kMaxMaxPieces = 32;
+constexpr int kXcds = 8;
 constexpr int kMaxSplits = 64;
 
 struct BwdArgs {
@@ -69,80 +77,92 @@ struct BwdArgs {
 
 typedef uint32_t u4_any __attribute__((ext_vector_type(4), aligned(2)));
 
-// Eight elements of a row that may start at any element.
-__device__ __forceinline__ void load8(const uint16_t* p, float* x) {
-  const u4 v = *reinterpret_cast<const u4_any*>(p);
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    x[2 * w] = __uint_as_float(v[w] << 16);
-    x[2 * w + 1] = __uint_as_float(v[w] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void load8(const float* p, float* x) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const u4 v = *reinterpret_cast<const u4_any*>(p + 4 * h);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) x[4 * h + w] = __uint_as_float(v[w]);
-  }
-}
-__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-
-// The same with zeros from `end` on.
+// Eight elements of a row as they are stored; a row may start at any element.
 template <typename T>
-__device__ __forceinline__ void load8_to(const T* row, int64_t v, int64_t end, float* x) {
-  if (v + 8 <= end) return load8(row + v, x);
+struct Raw8 {
+  u4 w[sizeof(T) / 2];
+};
+__device__ __forceinline__ uint32_t raw_bits(const uint16_t* p) { return *p; }
+__device__ __forceinline__ uint32_t raw_bits(const float* p) { return __float_as_uint(*p); }
+// Elements v .. v + 8 of a row, zeros from `end` on.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* row, int64_t v, int64_t end) {
+  Raw8<T> x = {};
+  if (v + 8 <= end) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = v + j < end ? load1(row + v + j) : 0.0f;
+    for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+      x.w[h] = *reinterpret_cast<const u4_any*>(reinterpret_cast<const char*>(row + v) + 16 * h);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (v + j < end) {
+        if constexpr (sizeof(T) == 2)
+          x.w[0][j >> 1] |= raw_bits(row + v + j) << (16 * (j & 1));
+        else
+          x.w[j >> 2][j & 3] = raw_bits(row + v + j);
+      }
+  }
+  return x;
 }
+__device__ __forceinline__ float at(const Raw8<uint16_t>& x, int j) {
+  return __uint_as_float(j & 1 ? x.w[0][j >> 1] & 0xffff0000u : x.w[0][j >> 1] << 16);
+}
+__device__ __forceinline__ float at(const Raw8<float>& x, int j) { return __uint_as_float(x.w[j >> 2][j & 3]); }
 
-// The scales of eight vocabulary rows (v a multiple of 8 below V16): s_R, and
-// s_Ac, s_Aw of the parts that there are.
+// The fp16 scales of eight vocabulary rows (v a multiple of 8 below V16) as
+// they are stored: s_R, and s_Ac, s_Aw of the parts that there are.
 struct Scales8 {
-  float R[8], c[8], w[8];
+  u4 R, A[2];
 };
 __device__ __forceinline__ Scales8 scales8(const BwdArgs& a, int64_t v) {
-  Scales8 s;
-  const u4 x = *reinterpret_cast<const u4*>(a.r_rowscale + v);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    s.R[j] = f16_to_f32((uint16_t)(x[j >> 1] >> (16 * (j & 1))));
-    s.c[j] = s.w[j] = 0.0f;
-  }
-  if (a.nA == 1) {
-    const u4 y = *reinterpret_cast<const u4*>(a.a_scales + v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s.c[j] = s.w[j] = f16_to_f32((uint16_t)(y[j >> 1] >> (16 * (j & 1))));
-  } else if (a.nA == 2) {
-    const u4* y = reinterpret_cast<const u4*>(a.a_scales + 2 * v);
-    const u4 y0 = y[0], y1 = y[1];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t d = j < 4 ? y0[j] : y1[j - 4];
-      s.c[j] = f16_to_f32((uint16_t)d);
-      s.w[j] = f16_to_f32((uint16_t)(d >> 16));
-    }
+  Scales8 s = {};
+  s.R = *reinterpret_cast<const u4*>(a.r_rowscale + v);
+  if (a.nA == 1) s.A[0] = *reinterpret_cast<const u4*>(a.a_scales + v);
+  if (a.nA == 2) {
+    s.A[0] = *reinterpret_cast<const u4*>(a.a_scales + 2 * v);
+    s.A[1] = *reinterpret_cast<const u4*>(a.a_scales + 2 * v + 8);
   }
   return s;
 }
+__device__ __forceinline__ float scale_R(const Scales8& s, int j) {
+  return f16_to_f32((uint16_t)(s.R[j >> 1] >> (16 * (j & 1))));
+}
+// s_Ac (part 0) or s_Aw (part 1); of a head with one part, that one's for both
+__device__ __forceinline__ float scale_A(const Scales8& s, int nA, int part, int j) {
+  return nA == 2 ? f16_to_f32((uint16_t)(s.A[j >> 2][j & 3] >> (16 * part)))
+                 : f16_to_f32((uint16_t)(s.A[0][j >> 1] >> (16 * (j & 1))));
+}
 
-// Thread i of the layout of the A codes: lane i % 64 of vocabulary step
-// (i / 64) % ksteps of rank tile i / 64 / ksteps gets the codes of rank
-// lane % 32 at 8 vocabulary rows, in the byte order that unpack_i8x8 turns into theirs.
+// The layout of the A codes: rank tile t, vocabulary step, lane (rank lane % 32,
+// rows 16 step + 8 (lane / 32) .. + 8) hold 8 bytes in the order that
+// unpack_i8x8 turns into the rows'.  Thread i takes four ranks: eight words of
+// the stored rows, transposed byte by byte.
 __device__ __forceinline__ void arrange_codes(const BwdArgs& a, int64_t i) {
-  const int lane = (int)(i & 63), c32 = lane & 31;
-  const int64_t step = (i >> 6) % a.ksteps, t = (i >> 6) / a.ksteps;
+  const int quad = (int)(i & 7), half = (int)(i >> 3) & 1;
+  const int64_t step = (i >> 4) % a.ksteps, t = (i >> 4) / a.ksteps;
   if (t >= a.nct + a.nwt) return;
   const bool in_c = t < a.nct;
-  const int j = 32 * (int)(in_c ? t : t - a.nct) + c32, r = a.r_c + a.r_r;
-  const bool valid = j < (in_c ? a.r_c : a.r_r);
-  const int64_t v = 16 * step + 8 * (lane >> 5), V16 = 16 * a.nb;
-  const uint8_t* codes = reinterpret_cast<const uint8_t*>(a.a_codes) + (in_c ? 0 : a.r_c) + (valid ? j : 0);
-  uint32_t b[8];
+  const int j = 32 * (int)(in_c ? t : t - a.nct) + 4 * quad, r = a.r_c + a.r_r;
+  const bool valid = j < (in_c ? a.r_c : a.r_r);  // ranks come in eights
+  const int64_t v = 16 * step + 8 * half;
+  const int8_t* codes = a.a_codes + v * r + (in_c ? 0 : a.r_c) + j;
+  uint32_t w[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) b[k] = valid && v + k < V16 ? codes[(v + k) * r] : 0u;
-  reinterpret_cast<u2*>(a.af)[i] = u2{b[0] | b[2] << 8 | b[1] << 16 | b[3] << 24, b[4] | b[6] << 8 | b[5] << 16 | b[7] << 24};
+  for (int k = 0; k < 8; ++k)
+    w[k] = valid && v < 16 * a.nb ? *reinterpret_cast<const uint32_t*>(codes + (int64_t)k * r) : 0u;
+  u2* out = reinterpret_cast<u2*>(a.af) + ((t * a.ksteps + step) * 64 + 32 * half + 4 * quad);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {  // byte b of rows 0 2 1 3, and of rows 4 6 5 7
+    u2 x;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t sel = 0x0c0c0000u | (uint32_t)(4 + b) << 8 | (uint32_t)b;
+      const uint32_t lo = __builtin_amdgcn_perm(w[4 * h + 2], w[4 * h], sel);
+      const uint32_t hi = __builtin_amdgcn_perm(w[4 * h + 3], w[4 * h + 1], sel);
+      x[h] = lo | hi << 16;
+    }
+    out[b] = x;
+  }
 }
 
 // Workgroup q pieces + p: the largest products of piece p of rows kMaxRows q
@@ -163,19 +183,22 @@ __global__ __launch_bounds__(kMaxThreads) void bwd_max_kernel(const BwdArgs a) {
   const int64_t end = (p + 1) * a.width < a.V ? (p + 1) * a.width : a.V;
   float m[kMaxRows][3] = {};
   for (int64_t v = p * a.width + 8 * threadIdx.x; v < end; v += 8 * kMaxThreads) {
-    float x[kMaxRows][8];
+    Raw8<T> x[kMaxRows];
 #pragma unroll
     for (int i = 0; i < kMaxRows; ++i)  // rows past the end: the last one again
-      load8_to(static_cast<const T*>(a.dY) + (n0 + i < a.N ? n0 + i : a.N - 1) * a.dy_stride, v, end, x[i]);
+      x[i] = load8(static_cast<const T*>(a.dY) + (n0 + i < a.N ? n0 + i : a.N - 1) * a.dy_stride, v, end);
     const Scales8 s = scales8(a, v);
 #pragma unroll
-    for (int i = 0; i < kMaxRows; ++i)
+    for (int j = 0; j < 8; ++j) {
+      const float R = scale_R(s, j), c = scale_A(s, a.nA, 0, j), w = scale_A(s, a.nA, 1, j);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[i][0] = fmaxf(m[i][0], fabsf(x[i][j] * s.R[j]));
-        m[i][1] = fmaxf(m[i][1], fabsf(x[i][j] * s.c[j]));
-        m[i][2] = fmaxf(m[i][2], fabsf(x[i][j] * s.w[j]));
+      for (int i = 0; i < kMaxRows; ++i) {
+        const float y = at(x[i], j);
+        m[i][0] = fmaxf(m[i][0], fabsf(y * R));
+        m[i][1] = fmaxf(m[i][1], fabsf(y * c));
+        m[i][2] = fmaxf(m[i][2], fabsf(y * w));
       }
+    }
   }
 #pragma unroll
   for (int i = 0; i < kMaxRows; ++i)
@@ -241,31 +264,41 @@ __global__ __launch_bounds__(64 * kPrepWaves) void bwd_prep_kernel(const BwdArgs
   const int run0 = (int)((int64_t)part * runs / gridDim.y), run1 = (int)((int64_t)(part + 1) * runs / gridDim.y);
   const u2* codes = reinterpret_cast<const u2*>(a.af) + (int64_t)(t < tiles ? t : 0) * a.ksteps * 64 + lane;
   f16x acc = {};
-  for (int run = run0; run < run1; ++run) {
+  // the next run's loads are in flight while this one is converted and used
+  Raw8<T> x[2] = {};
+  Scales8 s;
+  u2 b[8];
+  auto load = [&](int run) {
     const int64_t v = 128 * (int64_t)run + 8 * oct;
-    float x[2][8] = {};
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (real[i]) load8_to(row[i], v, a.V, x[i]);
-    const Scales8 s = scales8(a, v < V16 ? v : V16 - 8);  // past V16 dY is zero
-    u2 b[8];
+      if (real[i]) x[i] = load8(row[i], v, a.V);
+    s = scales8(a, v < V16 ? v : V16 - 8);  // past V16 dY is zero
+  };
+  auto load_codes = [&](int run) {
     if (t < tiles) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) b[k] = codes[std::min(8 * run + k, a.ksteps - 1) * 64];
     }
+  };
+  if (run0 < run1) load(run0);
+  for (int run = run0; run < run1; ++run) {
+    load_codes(run);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       h8 f[3];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        f[0][j] = (_Float16)ldexpf(x[i][j] * s.R[j], e[i][0]);
-        f[1][j] = (_Float16)ldexpf(x[i][j] * s.c[j], e[i][1]);
-        f[2][j] = (_Float16)ldexpf(x[i][j] * s.w[j], e[i][2]);
+        const float y = at(x[i], j);
+        f[0][j] = (_Float16)ldexpf(y * scale_R(s, j), e[i][0]);
+        f[1][j] = (_Float16)ldexpf(y * scale_A(s, a.nA, 0, j), e[i][1]);
+        f[2][j] = (_Float16)ldexpf(y * scale_A(s, a.nA, 1, j), e[i][2]);
       }
-      const int at = 32 * (oct & 1) + (tid >> 4) + 16 * i;
+      const int at_ = 32 * (oct & 1) + (tid >> 4) + 16 * i;
 #pragma unroll
-      for (int q = 0; q < 3; ++q) frag[q][oct >> 1][at] = f[q];
+      for (int q = 0; q < 3; ++q) frag[q][oct >> 1][at_] = f[q];
     }
+    if (run + 1 < run1) load(run + 1);
     __syncthreads();
     if (first) {
 #pragma unroll
@@ -290,18 +323,42 @@ __global__ __launch_bounds__(64 * kPrepWaves) void bwd_prep_kernel(const BwdArgs
   }
 }
 
-// Z from its parts of the vocabulary, in order, with the rows' scales undone.
-__global__ __launch_bounds__(kMaxThreads) void bwd_zsum_kernel(const BwdArgs a) {
-  const int r = a.r_c + a.r_r;
-  const int64_t i = (int64_t)blockIdx.x * kMaxThreads + threadIdx.x, count = a.n32 * r;
-  if (i >= count) return;
-  float z = 0.0f;
+// Row blockIdx.x of Z from its parts of the vocabulary, with the row's scales
+// undone: kZsumRanks ranks at a time, the parts dealt to the threads of a rank
+// and their sums added in order.
+__global__ __launch_bounds__(kZsumThreads) void bwd_zsum_kernel(const BwdArgs a) {
+  constexpr int kDeal = kZsumThreads / kZsumRanks;
+  __shared__ float buf[kDeal][kZsumRanks];
+  const int r = a.r_c + a.r_r, jj = threadIdx.x % kZsumRanks, deal = threadIdx.x / kZsumRanks;
+  const int64_t n = blockIdx.x;
+  for (int j0 = 0; j0 < r; j0 += kZsumRanks) {
+    const int j = j0 + jj;
+    float z = 0.0f;
+    if (j < r) {
 #pragma unroll 8
-  for (int p = 0; p < a.zparts; ++p) z += a.zpart[p * count + i];
-  a.z[i] = z * a.rscale[i / r * 3 + (i % r < a.r_c ? 1 : 2)];
+      for (int p = deal; p < a.zparts; p += kDeal) z += a.zpart[((int64_t)p * a.n32 + n) * r + j];
+    }
+    buf[deal][jj] = z;
+    __syncthreads();
+    if (deal == 0 && j < r) {
+#pragma unroll
+      for (int d = 1; d < kDeal; ++d) z += buf[d][jj];
+      a.z[n * r + j] = z * a.rscale[n * 3 + (j < a.r_c ? 1 : 2)];
+    }
+    __syncthreads();
+  }
 }
 
-// Place of 16-byte octet o (8 columns) of row k in a stage's fp16 tile of 32
+// f(integral_constant<I>) for I = B .. E-1, unrolled at compile time
+template <int B, int E, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (B < E) {
+    f(std::integral_constant<int, B>{});
+    static_for<B + 1, E>(f);
+  }
+}
+
+// Place of 16-byte octet o (8 columns) of row k in a stage's fp16 tile of 64
 // rows x 256 columns: both the 16 rows that a wave writes at one octet and the
 // 4 rows x 4 octets that 32 lanes read at a time fall in different banks.
 __device__ __forceinline__ int tile_octet(int k, int o) {
@@ -316,61 +373,74 @@ __device__ __forceinline__ h4 read_tr(const _Float16* p) {
   return __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)p));
 }
 
-// Tokens x 256 columns of dH per workgroup over a share of the vocabulary;
-// TT 32-token tiles, eight waves in WM rows.
+// 32 TT tokens x 256 columns of dH per workgroup over a share of the
+// vocabulary, in stages of 64 vocabulary rows (4 MFMA steps).
 template <int TT>
 struct MainShape {
-  static constexpr int WM = TT >= 4 ? 2 : 1, WN = 8 / WM;
-  static constexpr int MT = TT / WM, NT = 8 / WN;  // 32 x 32 tiles of a wave
-  static constexpr int AF = 2 * TT;                // 1 KB operand fragments of a stage
+  static constexpr int WM = TT >= 4 ? 2 : 1, WN = 8 / WM;  // eight waves in WM rows
+  static constexpr int MT = TT / WM, NT = 8 / WN;          // 32 x 32 tiles of a wave
+  static constexpr int kFrags = 4 * TT;                    // 1 KB dY fragments of a stage
+  static constexpr int kLoads = (kFrags + 7) / 8;          // of those, per wave
+  static constexpr int kDepth = TT <= 2 ? D1 : TT == 4 ? D4 : D8;  // stages whose loads are in flight
 };
 
-// kCodes: group codes of 64 columns of a row, 2 for g = 32, else 1.
+// kCodes: group codes of 128 columns of a row: 4 for g = 32, 2 for 64, else 1.
 template <int TT, int kCodes>
-__global__ __launch_bounds__(kMainThreads) void bwd_main_kernel(const BwdArgs a) {
+__global__ __launch_bounds__(kMainThreads, TT >= 8 ? 2 : 4) void bwd_main_kernel(const BwdArgs a) {
   using S = MainShape<TT>;
-  constexpr int kALoads = (S::AF + 7) / 8;
-  __shared__ h8 sA[2][S::AF][64];
-  __shared__ h8 sB[2][32 * 32];
+  constexpr int kDepth = S::kDepth;
+  __shared__ h8 sA[2][S::kFrags][64];
+  __shared__ h8 sB[2][64 * 32];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
   const int CB = (int)((a.D + 255) / 256), ntiles = (int)(a.n32 / 32), TB = (ntiles + TT - 1) / TT;
-  const int cb = blockIdx.x % CB, tb = blockIdx.x / CB % TB, split = blockIdx.x / CB / TB;
-  const int stages = a.ksteps / 2;
+  // Workgroups are dealt to the XCDs round robin: each XCD gets a contiguous
+  // range of (split, token block, column block), so that those in one L2 share
+  // few streams of dY fragments, the larger of the two operands.
+  const int per = gridDim.x / kXcds, rem = gridDim.x % kXcds, x = blockIdx.x % kXcds;
+  const int item = x * per + std::min(x, rem) + blockIdx.x / kXcds;
+  const int cb = item % CB, tb = item / CB % TB, split = item / CB / TB;
+  const int stages = a.ksteps / 4;
   const int s0 = (int)((int64_t)split * stages / a.splits), s1 = (int)((int64_t)(split + 1) * stages / a.splits);
 
-  // this wave's share of unpacking: 16 rows x 64 columns
-  const int blk = (wave >> 1) & 1, kth = wave >> 2, whalf = wave & 1;
+  // this wave's share of unpacking: one packed tile, 16 rows x 128 columns
+  const int blk = wave & 3, kth = wave >> 2;
   const int kt = std::min(2 * cb + kth, a.nkt - 1);
-  const int wrow = 16 * blk + (lane & 15);
-  const uint8_t* wsrc = a.r_codes + (int64_t)kt * a.nb * 1024 + lane * 16 + 8 * whalf;
-  const int group = (kKTile * kt + 64 * whalf) / a.g;
-  u2 w;
-  uint32_t code;
-  h8 av[kALoads];
-  auto load = [&](int s) {
-    const int64_t b = std::min<int64_t>(2 * (int64_t)s + blk, a.nb - 1);  // past the end: dY is zero
-    w = *reinterpret_cast<const u2*>(wsrc + b * 1024);
-    const uint8_t* c = a.r_gcodes + (16 * b + (lane & 15)) * a.ng + group;
-    code = kCodes == 2 ? *reinterpret_cast<const uint16_t*>(c) : *c;
+  const uint8_t* wsrc = a.r_codes + (int64_t)kt * a.nb * 1024 + lane * 16;
+  const uint8_t* csrc = a.r_gcodes + (lane & 15) * a.ng + kKTile * kt / a.g;
+  u4 w[kDepth];
+  uint32_t code[kDepth];
+  h8 av[kDepth][S::kLoads];
+  auto load = [&](int s, auto slot_) {
+    constexpr int slot = decltype(slot_)::value;
+    s = std::min(s, s1 - 1);  // past the end: a stage that is cached, never used
+    const int64_t b = std::min<int64_t>(4 * (int64_t)s + blk, a.nb - 1);  // past the last rows dY is zero
+    w[slot] = *reinterpret_cast<const u4*>(wsrc + b * 1024);
+    const uint8_t* c = csrc + 16 * b * a.ng;
+    code[slot] = kCodes == 4   ? *reinterpret_cast<const uint32_t*>(c)
+                 : kCodes == 2 ? *reinterpret_cast<const uint16_t*>(c)
+                               : *c;
 #pragma unroll
-    for (int i = 0; i < kALoads; ++i) {
-      const int f = std::min(8 * i + wave, S::AF - 1);
-      const int64_t tile = std::min(tb * TT + f / 2, ntiles - 1);
-      av[i] = *reinterpret_cast<const h8*>(a.hf + ((tile * a.ksteps + 2 * s + f % 2) * 64 + lane) * 8);
+    for (int i = 0; i < S::kLoads; ++i) {
+      const int f = std::min(8 * i + wave, S::kFrags - 1);
+      const int64_t tile = std::min(tb * TT + f / 4, ntiles - 1);
+      av[slot][i] = *reinterpret_cast<const h8*>(a.hf + ((tile * a.ksteps + 4 * s + f % 4) * 64 + lane) * 8);
     }
   };
-  auto store = [&](int buf) {
+  auto store = [&](int buf, auto slot_) {
+    constexpr int slot = decltype(slot_)::value;
 #pragma unroll
-    for (int d = 0; d < 2; ++d) {
-      const uint32_t c = kCodes == 2 ? (code >> (8 * d)) & 0xffu : code;
-      sB[buf][tile_octet(wrow, 16 * kth + 4 * (2 * whalf + d) + (lane >> 4))] =
-          unpack_q4_scaled(w[d], (_Float16)(float)c);
+    for (int d = 0; d < 4; ++d) {
+      const uint32_t c = kCodes == 4 ? (code[slot] >> (8 * d)) & 0xffu
+                         : kCodes == 2 ? (code[slot] >> (8 * (d >> 1))) & 0xffu
+                                       : code[slot];
+      sB[buf][tile_octet(16 * blk + (lane & 15), 16 * kth + 4 * d + (lane >> 4))] =
+          unpack_q4_scaled(w[slot][d], (_Float16)(float)c);
     }
 #pragma unroll
-    for (int i = 0; i < kALoads; ++i)
-      if (8 * i + wave < S::AF) sA[buf][8 * i + wave][lane] = av[i];
+    for (int i = 0; i < S::kLoads; ++i)
+      if (8 * i + wave < S::kFrags) sA[buf][8 * i + wave][lane] = av[slot][i];
   };
 
   f16x acc[S::MT][S::NT] = {};
@@ -378,7 +448,7 @@ __global__ __launch_bounds__(kMainThreads) void bwd_main_kernel(const BwdArgs a)
   auto compute = [&](int buf) {
     const _Float16* B = reinterpret_cast<const _Float16*>(sB[buf]);
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < 4; ++t) {
       h8 b[S::NT];
 #pragma unroll
       for (int c = 0; c < S::NT; ++c) {
@@ -393,22 +463,28 @@ __global__ __launch_bounds__(kMainThreads) void bwd_main_kernel(const BwdArgs a)
       }
 #pragma unroll
       for (int m = 0; m < S::MT; ++m) {
-        const h8 av_ = sA[buf][2 * (wm * S::MT + m) + t][lane];
+        const h8 f = sA[buf][4 * (wm * S::MT + m) + t][lane];
 #pragma unroll
-        for (int c = 0; c < S::NT; ++c) acc[m][c] = mfma32(av_, b[c], acc[m][c]);
+        for (int c = 0; c < S::NT; ++c) acc[m][c] = mfma32(f, b[c], acc[m][c]);
       }
     }
   };
   if (s0 < s1) {
-    load(s0);
-    store(0);
+    static_for<0, kDepth>([&](auto i) { load(s0 + decltype(i)::value, i); });
+    store(0, std::integral_constant<int, 0>{});
+    load(s0 + kDepth, std::integral_constant<int, 0>{});
     __syncthreads();
-    for (int s = s0; s < s1; ++s) {
-      if (s + 1 < s1) load(s + 1);
-      compute((s - s0) & 1);
-      if (s + 1 < s1) store((s + 1 - s0) & 1);
-      __syncthreads();
-    }
+    for (int g0 = s0; g0 < s1; g0 += kDepth)
+      static_for<1, kDepth + 1>([&](auto i) {
+        // stage s; the next one waits in slot i mod kDepth
+        const int s = g0 + decltype(i)::value - 1;
+        constexpr std::integral_constant<int, decltype(i)::value % kDepth> slot{};
+        if (s >= s1) return;
+        compute((s - s0) & 1);
+        store((s - s0 + 1) & 1, slot);
+        load(s + 1 + kDepth, slot);
+        __syncthreads();
+      });
   }
   // columns sit in the tile in the order the unpacking gives them
   const int c32 = lane & 31;
@@ -511,12 +587,12 @@ int main_tiles(int64_t N) { return N <= 32 ? 1 : N <= 64 ? 2 : N <= 128 ? 4 : 8;
 
 // Parts of the vocabulary for the main kernel: the fewest whose workgroups
 // fill whole rounds of the resident ones (one a CU for 256-token tiles, two
-// for smaller ones) to within 4%, at least 8 stages each.
+// for smaller ones) to within 4%, at least 4 stages each.
 int main_splits(int64_t N, int64_t D, int64_t stages) {
   const int tt = main_tiles(N);
   const int64_t tiles = (N + 32 * tt - 1) / (32 * tt) * ((D + 255) / 256);
   const int64_t slots = tt == 8 ? 256 : 512;
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, stages / 8));
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, stages / 4));
   double best = 1e30;
   int pick = 1;
   for (int64_t p = 1; p <= most; ++p) {
@@ -539,14 +615,14 @@ BwdLayout bwd_layout(const archead_dims* d, int64_t n_tokens) {
   BwdLayout L{};
   L.rows = std::min(n_tokens, kBwdChunkRows);
   if (L.rows <= 0) return L;
-  const int64_t V32 = (int64_t)round_up((uint64_t)d->V, 32), r = d->r_c + d->r_r;
+  const int64_t V64 = (int64_t)round_up((uint64_t)d->V, 64), r = d->r_c + d->r_r;
   L.n32 = (int64_t)round_up((uint64_t)L.rows, 32);
-  L.ksteps = V32 / 16;
+  L.ksteps = V64 / 16;  // whole stages
   L.pieces = (int)std::max<int64_t>(
       1, std::min<int64_t>({(int64_t)kMaxMaxPieces, (d->V + 2047) / 2048, 2048 * kMaxRows / L.rows}));
   L.width = (int64_t)round_up((uint64_t)((d->V + L.pieces - 1) / L.pieces), 8);
   L.zparts = (int)std::max<int64_t>(1, std::min<int64_t>({256, (L.ksteps + 31) / 32, 1024 * 32 / L.n32}));
-  L.splits = main_splits(L.rows, d->D, L.ksteps / 2);
+  L.splits = main_splits(L.rows, d->D, L.ksteps / 4);
   auto take = [&](uint64_t bytes) {
     const uint64_t at = L.total;
     L.total += round_up(bytes, ARCHEAD_ALIGNMENT);
@@ -554,7 +630,7 @@ BwdLayout bwd_layout(const archead_dims* d, int64_t n_tokens) {
   };
   L.pmax = take((uint64_t)L.rows * L.pieces * 12);
   L.rscale = take((uint64_t)L.n32 * 12);
-  L.hf = take((uint64_t)L.n32 * V32 * 2);
+  L.hf = take((uint64_t)L.n32 * V64 * 2);
   L.af = take((uint64_t)((d->r_c + 31) / 32 + (d->r_r + 31) / 32) * L.ksteps * 512);
   L.zpart = take((uint64_t)L.zparts * L.n32 * r * 4);
   L.z = take((uint64_t)L.n32 * r * 4);
@@ -572,6 +648,8 @@ void launch_main_tt(const BwdArgs& a, hipStream_t s) {
   const int64_t tb = (a.n32 / 32 + TT - 1) / TT, cb = (a.D + 255) / 256;
   const dim3 grid((unsigned)(tb * cb * a.splits)), block(kMainThreads);
   if (a.g == 32)
+    hipLaunchKernelGGL((bwd_main_kernel<TT, 4>), grid, block, 0, s, a);
+  else if (a.g == 64)
     hipLaunchKernelGGL((bwd_main_kernel<TT, 2>), grid, block, 0, s, a);
   else
     hipLaunchKernelGGL((bwd_main_kernel<TT, 1>), grid, block, 0, s, a);
@@ -580,14 +658,13 @@ void launch_main_tt(const BwdArgs& a, hipStream_t s) {
 template <typename T>
 hipError_t launch_backward(const BwdArgs& a, hipStream_t s) {
   const int64_t ranks = a.nct + a.nwt, max_groups = (a.N + kMaxRows - 1) / kMaxRows * a.pieces;
-  hipLaunchKernelGGL(bwd_max_kernel<T>, dim3((unsigned)(max_groups + (ranks * a.ksteps * 64 + kMaxThreads - 1) / kMaxThreads)),
+  hipLaunchKernelGGL(bwd_max_kernel<T>, dim3((unsigned)(max_groups + (ranks * a.ksteps * 16 + kMaxThreads - 1) / kMaxThreads)),
                      dim3(kMaxThreads), 0, s, a);
   hipLaunchKernelGGL(bwd_prep_kernel<T>,
                      dim3((unsigned)(a.n32 / 32), (unsigned)a.zparts, (unsigned)std::max<int64_t>(1, (ranks + kPrepWaves - 1) / kPrepWaves)),
                      dim3(64 * kPrepWaves), 0, s, a);
   if (ranks > 0)
-    hipLaunchKernelGGL(bwd_zsum_kernel, dim3((unsigned)((a.n32 * (a.r_c + a.r_r) + kMaxThreads - 1) / kMaxThreads)),
-                       dim3(kMaxThreads), 0, s, a);
+    hipLaunchKernelGGL(bwd_zsum_kernel, dim3((unsigned)a.N), dim3(kZsumThreads), 0, s, a);
   switch (main_tiles(a.N)) {
     case 1: launch_main_tt<1>(a, s); break;
     case 2: launch_main_tt<2>(a, s); break;

@@ -594,9 +594,9 @@ ARCHEAD_API int archead_preference_loss(const archead_tensor* Y, const archead_p
                                         uint64_t workspace_bytes, void* stream);
 
 /* Device workspace archead_logits_backward needs for n_tokens rows: for
- * min(n_tokens, 4096) rows, dY as fp16 operands (2 V32 bytes a row, rows and
- * vocabulary rounded up to 32), fp32 partial sums of dH and of its low-rank
- * part, and row scales.  Pure host arithmetic.  E_NULL, E_DIMS, E_SHAPE,
+ * min(n_tokens, 4096) rows, dY as fp16 operands (2 bytes an element, rows
+ * rounded up to 32 and the vocabulary to 64), fp32 partial sums of dH and of
+ * its low-rank part, the A codes in operand order, and row scales.  Pure host arithmetic.  E_NULL, E_DIMS, E_SHAPE,
  * E_UNSUPPORTED. */
 ARCHEAD_API int archead_logits_backward_workspace_bytes(const archead_dims* d, int64_t n_tokens, uint64_t* bytes);
 
