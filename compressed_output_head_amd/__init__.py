@@ -8,8 +8,8 @@ not been built (``python compressed_output_head_amd/build.py``).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -351,8 +351,9 @@ def _tensor(t) -> ArcheadTensor:
     torch = _torch()
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError("expected a 2-D tensor with unit column stride")
-    code = {torch.bfloat16: ARCHEAD_BF16, torch.float32: ARCHEAD_F32}.get(t.dtype, 0)
-    return ArcheadTensor(t.data_ptr(), t.shape[0], t.shape[1], t.stride(0), code)
+    dtype, (rows, cols) = t.dtype, t.shape
+    code = ARCHEAD_BF16 if dtype is torch.bfloat16 else ARCHEAD_F32 if dtype is torch.float32 else 0
+    return ArcheadTensor(t.data_ptr(), rows, cols, t.stride(0), code)
 
 
 def archead_logits_path(H, head: PackedHead, Y, path: int = ARCHEAD_PATH_AUTO, stream=None):
@@ -567,19 +568,48 @@ def _scope(device, stream):
     stream, a raw handle, or None: the device's current stream) on `device`."""
     torch = _torch()
     if stream is None:
-        return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return torch.cuda.device(device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
+
+
+def _scoped(call):
+    """A call with a ``stream`` argument whose body runs on the current stream
+    of its first tensor's device: enters _scope where that is another one."""
+    torch = _torch()
+
+    @functools.wraps(call)
+    def run(first, *args, stream=None, **kw):
+        device = first.device
+        if stream is None and (device.type != "cuda" or device.index == torch.cuda.current_device()):
+            return call(first, *args, **kw)
+        with _scope(device, stream):
+            return call(first, *args, **kw)
+    return run
+
+
+def _raw_stream(device) -> int:
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 def _vec(t, name: str, dtype, n: int, device):
     """Address of a contiguous vector of n elements (None for None)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.device != device:
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}")
     return t.data_ptr()
+
+
+def _workspace(workspace, need: int, device):
+    """The caller's workspace, checked, or one of the call's own."""
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    return workspace
 
 
 def archead_loss_workspace_bytes(n_rows: int, V: int, n_pairs: int = 0) -> int:
@@ -589,62 +619,61 @@ def archead_loss_workspace_bytes(n_rows: int, V: int, n_pairs: int = 0) -> int:
     return out.value
 
 
-def _loss_setup(Y, dY, dY_dtype, with_gradient, workspace, n_pairs):
-    """(Y, dY, dY's tensor or None, workspace) of a loss call as the library
-    takes them; allocates what the caller did not bring."""
-    torch = _torch()
-    if not Y.is_cuda:
-        raise ValueError("Y must be a device tensor")
-    y = _tensor(Y)
+_loss_workspace_bytes = functools.lru_cache(maxsize=256)(archead_loss_workspace_bytes)
+
+
+def _gradient_of(Y, dY, dY_dtype, with_gradient):
+    """The tensor a loss writes its gradient to, or None."""
     if not with_gradient:
-        dY = None
-    elif dY is None:
-        dY = torch.empty(Y.shape, dtype=dY_dtype or Y.dtype, device=Y.device)
-    elif dY.device != Y.device or (dY_dtype is not None and dY_dtype != dY.dtype):
+        return None
+    if dY is None:
+        return _torch().empty(Y.shape, dtype=dY_dtype or Y.dtype, device=Y.device)
+    if dY.device != Y.device or (dY_dtype is not None and dY_dtype != dY.dtype):
         raise ValueError("dY must be on Y's device and of dY_dtype")
-    if workspace is None:
-        workspace = torch.empty(archead_loss_workspace_bytes(Y.shape[0], Y.shape[1], n_pairs), dtype=torch.uint8,
-                                device=Y.device)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != Y.device:
-        raise ValueError("workspace must be a contiguous uint8 tensor on Y's device")
-    return y, dY, None if dY is None else _tensor(dY), workspace
+    return dY
 
 
+@_scoped
 def archead_policy_loss(Y, labels, advantage, old_logp=None, ref_logp=None, weight=None, clip_low: float = 0.2,
                         clip_high: float = 0.2, kl_coef: float = 0.0, inv_temperature: float = 1.0, dY=None,
-                        dY_dtype=None, with_gradient: bool = True, workspace=None, stream=None):
+                        dY_dtype=None, with_gradient: bool = True, workspace=None):
     """Clipped policy loss with a KL term on the rows of Y (fp32 or bf16
     [N, V]) and its gradient.  labels: int32 [N]; advantage, old_logp (None:
     this policy sampled), ref_logp (needed when kl_coef > 0), weight (None:
     1): fp32 [N].  Returns a dict of device tensors "loss" (scalar), "logp",
     "row_loss" (fp32 [N]) and, with_gradient, "dY" [N, V]: the given tensor
-    (Y itself is allowed) or a new one of dY_dtype (Y's dtype by default)."""
+    (Y itself is allowed) or a new one of dY_dtype (Y's dtype by default).
+    stream: a torch stream or a raw handle (None: the current one)."""
     torch = _torch()
-    with _scope(Y.device, stream):
-        N, dev = Y.shape[0], Y.device
-        y, dY, dy, workspace = _loss_setup(Y, dY, dY_dtype, with_gradient, workspace, 0)
-        vec = torch.empty(2 * N + 1, dtype=torch.float32, device=dev)
-        out = {"loss": vec[2 * N], "logp": vec[:N], "row_loss": vec[N:2 * N]}
-        at = vec.data_ptr()
-        inp = ArcheadPolicyInputs(_vec(labels, "labels", torch.int32, N, dev),
-                                  _vec(advantage, "advantage", torch.float32, N, dev),
-                                  _vec(old_logp, "old_logp", torch.float32, N, dev),
-                                  _vec(ref_logp, "ref_logp", torch.float32, N, dev),
-                                  _vec(weight, "weight", torch.float32, N, dev),
-                                  clip_low, clip_high, kl_coef, inv_temperature)
-        outs = ArcheadPolicyOutputs(at + 8 * N, at, at + 4 * N, None if dy is None else ctypes.pointer(dy))
-        _check(lib.archead_policy_loss(ctypes.byref(y), ctypes.byref(inp), ctypes.byref(outs), workspace.data_ptr(),
-                                       workspace.numel(), torch.cuda.current_stream(dev).cuda_stream),
-               "archead_policy_loss")
-        if dY is not None:
-            out["dY"] = dY
-        return out
+    dev = Y.device
+    if dev.type != "cuda":
+        raise ValueError("Y must be a device tensor")
+    y = _tensor(Y)
+    N, V = Y.shape
+    f32 = torch.float32
+    inp = ArcheadPolicyInputs(_vec(labels, "labels", torch.int32, N, dev), _vec(advantage, "advantage", f32, N, dev),
+                              _vec(old_logp, "old_logp", f32, N, dev), _vec(ref_logp, "ref_logp", f32, N, dev),
+                              _vec(weight, "weight", f32, N, dev), clip_low, clip_high, kl_coef, inv_temperature)
+    dY = _gradient_of(Y, dY, dY_dtype, with_gradient)
+    dy = None if dY is None else ctypes.pointer(_tensor(dY))
+    ws = _workspace(workspace, _loss_workspace_bytes(N, V, 0), dev)
+    vec = torch.empty(2 * N + 1, dtype=f32, device=dev)
+    at = vec.data_ptr()
+    outs = ArcheadPolicyOutputs(at + 8 * N, at, at + 4 * N, dy)
+    status = lib.archead_policy_loss(y, inp, outs, ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if status:
+        _check(status, "archead_policy_loss")
+    out = {"loss": vec[2 * N], "logp": vec[:N], "row_loss": vec[N:2 * N]}
+    if dY is not None:
+        out["dY"] = dY
+    return out
 
 
+@_scoped
 def archead_preference_loss(Y, labels, offsets, ref_logp=None, weight=None, pair_weight=None, beta: float = 0.1,
                             label_smoothing: float = 0.0, inv_temperature: float = 1.0,
                             kind: int = ARCHEAD_PREF_SIGMOID, dY=None, dY_dtype=None, with_gradient: bool = True,
-                            workspace=None, stream=None):
+                            workspace=None):
     """Preference loss over pairs of sequences of rows of Y (fp32 or bf16
     [N, V]) and its gradient.  offsets: int32 [2 B + 1], sequence q is the rows
     [offsets[q], offsets[q + 1]), pair i prefers sequence 2i over 2i + 1.
@@ -653,27 +682,31 @@ def archead_preference_loss(Y, labels, offsets, ref_logp=None, weight=None, pair
     "loss" (scalar), "logp" [N], "chosen_reward", "rejected_reward" [B] and,
     with_gradient, "dY" as archead_policy_loss does."""
     torch = _torch()
-    with _scope(Y.device, stream):
-        N, dev, B = Y.shape[0], Y.device, (offsets.numel() - 1) // 2
-        y, dY, dy, workspace = _loss_setup(Y, dY, dY_dtype, with_gradient, workspace, B)
-        vec = torch.empty(N + 2 * B + 1, dtype=torch.float32, device=dev)
-        out = {"loss": vec[N + 2 * B], "logp": vec[:N], "chosen_reward": vec[N:N + B],
-               "rejected_reward": vec[N + B:N + 2 * B]}
-        at = vec.data_ptr()
-        inp = ArcheadPreferenceInputs(_vec(labels, "labels", torch.int32, N, dev),
-                                      _vec(offsets, "offsets", torch.int32, 2 * B + 1, dev), B,
-                                      _vec(ref_logp, "ref_logp", torch.float32, N, dev),
-                                      _vec(weight, "weight", torch.float32, N, dev),
-                                      _vec(pair_weight, "pair_weight", torch.float32, B, dev),
-                                      beta, label_smoothing, inv_temperature, kind)
-        outs = ArcheadPreferenceOutputs(at + 4 * (N + 2 * B), at, at + 4 * N, at + 4 * (N + B),
-                                        None if dy is None else ctypes.pointer(dy))
-        _check(lib.archead_preference_loss(ctypes.byref(y), ctypes.byref(inp), ctypes.byref(outs),
-                                           workspace.data_ptr(), workspace.numel(),
-                                           torch.cuda.current_stream(dev).cuda_stream), "archead_preference_loss")
-        if dY is not None:
-            out["dY"] = dY
-        return out
+    dev = Y.device
+    if dev.type != "cuda":
+        raise ValueError("Y must be a device tensor")
+    y = _tensor(Y)
+    N, V = Y.shape
+    B, f32 = (offsets.numel() - 1) // 2, torch.float32
+    inp = ArcheadPreferenceInputs(_vec(labels, "labels", torch.int32, N, dev),
+                                  _vec(offsets, "offsets", torch.int32, 2 * B + 1, dev), B,
+                                  _vec(ref_logp, "ref_logp", f32, N, dev), _vec(weight, "weight", f32, N, dev),
+                                  _vec(pair_weight, "pair_weight", f32, B, dev), beta, label_smoothing,
+                                  inv_temperature, kind)
+    dY = _gradient_of(Y, dY, dY_dtype, with_gradient)
+    dy = None if dY is None else ctypes.pointer(_tensor(dY))
+    ws = _workspace(workspace, _loss_workspace_bytes(N, V, B), dev)
+    M = N + 2 * B
+    vec = torch.empty(M + 1, dtype=f32, device=dev)
+    at = vec.data_ptr()
+    outs = ArcheadPreferenceOutputs(at + 4 * M, at, at + 4 * N, at + 4 * (N + B), dy)
+    status = lib.archead_preference_loss(y, inp, outs, ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if status:
+        _check(status, "archead_preference_loss")
+    out = {"loss": vec[M], "logp": vec[:N], "chosen_reward": vec[N:N + B], "rejected_reward": vec[N + B:M]}
+    if dY is not None:
+        out["dY"] = dY
+    return out
 
 
 def archead_logits_backward_workspace_bytes(V, D, r_c, r_r, g, n_tokens: int, fmt=ARCHEAD_FMT_ARCHEAD) -> int:
@@ -683,27 +716,27 @@ def archead_logits_backward_workspace_bytes(V, D, r_c, r_r, g, n_tokens: int, fm
     return out.value
 
 
-def archead_logits_backward(dY, head: PackedHead, dH=None, workspace=None, stream=None):
+_backward_workspace_bytes = functools.lru_cache(maxsize=256)(archead_logits_backward_workspace_bytes)
+
+
+@_scoped
+def archead_logits_backward(dY, head: PackedHead, dH=None, workspace=None):
     """dH = dY W_hat, the hidden states' gradient through the packed head.
     dY: fp32 or bf16 [N, V]; dH: bf16 [N, D] (a new one by default).  The
-    workspace is the call's own unless one is given (uint8)."""
+    workspace is the call's own unless one is given (uint8).  stream: a torch
+    stream or a raw handle (None: the current one)."""
     torch = _torch()
     dev = head.buffer.device
     if dY.device != dev or (dH is not None and dH.device != dev):
         raise ValueError("dY and dH must be on the head's device")
-    with _scope(dev, stream):
-        g = _tensor(dY)
-        if dH is None:
-            dH = torch.empty((dY.shape[0], head.D), dtype=torch.bfloat16, device=dev)
-        h = _tensor(dH)
-        if workspace is None:
-            need = archead_logits_backward_workspace_bytes(head.V, head.D, head.r_c, head.r_r, head.g, dY.shape[0],
-                                                           fmt=head.fmt)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
-            raise ValueError("workspace must be a contiguous uint8 tensor on the head's device")
-        p = ArcheadPackedHead(_dims(head.V, head.D, head.r_c, head.r_r, head.g, head.fmt), head.buffer.data_ptr(),
-                              head.buffer.numel(), workspace.data_ptr(), workspace.numel())
-        _check(lib.archead_logits_backward(ctypes.byref(g), ctypes.byref(p), ctypes.byref(h),
-                                           torch.cuda.current_stream(dev).cuda_stream), "archead_logits_backward")
-        return dH
+    g = _tensor(dY)
+    if dH is None:
+        dH = torch.empty((dY.shape[0], head.D), dtype=torch.bfloat16, device=dev)
+    ws = _workspace(workspace, _backward_workspace_bytes(head.V, head.D, head.r_c, head.r_r, head.g, dY.shape[0],
+                                                         head.fmt), dev)
+    p = ArcheadPackedHead(_dims(head.V, head.D, head.r_c, head.r_r, head.g, head.fmt), head.buffer.data_ptr(),
+                          head.buffer.numel(), ws.data_ptr(), ws.numel())
+    status = lib.archead_logits_backward(g, p, _tensor(dH), _raw_stream(dev))
+    if status:
+        _check(status, "archead_logits_backward")
+    return dH

@@ -28,6 +28,9 @@
 // a pair, all of the pair).  Many rows of a policy loss take another way, that
 // reads most of them once:
 //   row_order_kernel, policy_fused_kernel, loss_total_kernel
+// and so do calls whose launches take longer than their work:
+//   small_loss_kernel                          a few short rows
+//   row_pieces_kernel, few_gradient_kernel     a few long ones
 // Rows of weight zero are neither read nor counted; their gradient is zero.
 // Every sum has a fixed order, so results do not depend on scheduling.
 #include <math.h>
@@ -47,6 +50,9 @@ constexpr int kRowUnroll = 4;        // 16-byte loads in flight per thread
 constexpr int kPairThreads = 1024;
 constexpr int kFusedThreads = 1024;
 constexpr int kOrderThreads = 1024;
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallRows = 64;       // and pairs, of small_loss_kernel
+constexpr int kFewRows = 16;         // of few_gradient_kernel
 constexpr int kHeldChunks = 12;      // of 16 bytes, in registers
 constexpr int64_t kFusedLeastRows = 256;   // one per CU
 constexpr int64_t kMaxPieces = 64;
@@ -156,9 +162,14 @@ __device__ __forceinline__ float2 merge(float2 a, float2 b, Scale k) {
   return float2{M, a.y * exp_at(a.x - M0, k) + b.y * exp_at(b.x - M0, k)};
 }
 
+__device__ __forceinline__ float2 wave_merge(float2 v, Scale k) {
+  for (int o = 32; o > 0; o >>= 1) v = merge(v, float2{__shfl_xor(v.x, o), __shfl_xor(v.y, o)}, k);
+  return v;
+}
+
 template <int kThreads>
 __device__ __forceinline__ float2 block_merge(float2 v, Scale k, float2* buf) {
-  for (int o = 32; o > 0; o >>= 1) v = merge(v, float2{__shfl_xor(v.x, o), __shfl_xor(v.y, o)}, k);
+  v = wave_merge(v, k);
   if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
   __syncthreads();
   v = buf[0];
@@ -166,9 +177,14 @@ __device__ __forceinline__ float2 block_merge(float2 v, Scale k, float2* buf) {
   return v;
 }
 
+__device__ __forceinline__ double wave_sum(double v) {
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
 template <int kThreads>
 __device__ __forceinline__ double block_sum(double v, double* buf) {
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  v = wave_sum(v);
   if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
   __syncthreads();
   v = buf[0];
@@ -186,9 +202,9 @@ __device__ __forceinline__ bool row_counts(const RowArgs& a, int64_t n) {
   return weight_of(a, n) != 0.0f;
 }
 
-// (M, S) of the elements [0, len) at p, one thread's share.
+// (M, S) of the elements [0, len) at p, the share of thread tid of kThreads.
 template <typename T, int kThreads>
-__device__ __forceinline__ float2 thread_stats(const T* p, int64_t len, Scale k) {
+__device__ __forceinline__ float2 thread_stats(const T* p, int64_t len, Scale k, int tid) {
   using E = Elem<T>;
   const int64_t full = len / E::kPer16;
   float M = -INFINITY, M0 = 0.0f, S = 0.0f;
@@ -198,7 +214,7 @@ __device__ __forceinline__ float2 thread_stats(const T* p, int64_t len, Scale k)
       M = M0 = top;
     }
   };
-  for (int64_t c0 = threadIdx.x; c0 < full; c0 += kThreads * kRowUnroll) {
+  for (int64_t c0 = tid; c0 < full; c0 += kThreads * kRowUnroll) {
     u4 v[kRowUnroll];
 #pragma unroll
     for (int u = 0; u < kRowUnroll; ++u) {
@@ -219,7 +235,7 @@ __device__ __forceinline__ float2 thread_stats(const T* p, int64_t len, Scale k)
       for (int j = 0; j < E::kPer16; ++j) add += exp_at(E::at(v[u], j) - M0, k);
     S += add;
   }
-  const int64_t i = full * E::kPer16 + threadIdx.x;  // fewer than 8 elements are left
+  const int64_t i = full * E::kPer16 + tid;  // fewer than 8 elements are left
   if (i < len) {
     const float y = E::one(p[i]);
     rise(y);
@@ -241,7 +257,7 @@ __global__ __launch_bounds__(kRowThreads) void row_pieces_kernel(const RowArgs a
   // read here, before any launch that may write the gradient over Y
   if (threadIdx.x == 0 && (valid ? label >= c0 && label < c1 : p == 0))
     a.ylab[n] = valid ? Elem<T>::one(row[label]) : __builtin_nanf("");
-  const float2 r = block_merge<kRowThreads>(thread_stats<T, kRowThreads>(row + c0, c1 - c0, a.k), a.k, buf);
+  const float2 r = block_merge<kRowThreads>(thread_stats<T, kRowThreads>(row + c0, c1 - c0, a.k, threadIdx.x), a.k, buf);
   if (threadIdx.x == 0) a.part[n * a.pieces + p] = r;
 }
 
@@ -289,17 +305,41 @@ __device__ __attribute__((noinline)) PolicyResult policy_row(PolicyRow x, Policy
                       RowGrad{(float)(-c / (double)x.S), x.M, (float)(-c * expm1(logp)), c != 0.0 ? 1u : 0u}};
 }
 
-__device__ __forceinline__ PolicyRow policy_inputs(const RowArgs& a, int64_t n) {
+__device__ __forceinline__ PolicyScalars policy_scalars(const RowArgs& a) {
+  return PolicyScalars{a.s, a.clip_low, a.clip_high, a.kl_coef, a.old_logp ? 0u : 1u};
+}
+
+// A row of a pair: its term of the sequence's sum, and its gradient but for
+// the slope of the pair's loss.
+__device__ __forceinline__ PolicyResult pair_row(const PolicyRow& x, float s) {
+  const double w = x.weight, logp = (double)s * ((double)x.y_label - (double)x.M) - log((double)x.S), c = w * (double)s;
+  return PolicyResult{0.0, w * (logp - (double)x.ref_logp), (float)logp,
+                      RowGrad{(float)(-c / (double)x.S), x.M, (float)(-c * expm1(logp)), 1u}};
+}
+
+template <bool kPairs>
+__device__ __forceinline__ PolicyRow row_inputs(const RowArgs& a, int64_t n) {
   PolicyRow x{};
-  x.advantage = a.advantage[n];
-  x.old_logp = a.old_logp ? a.old_logp[n] : 0.0f;
   x.ref_logp = a.ref_logp ? a.ref_logp[n] : 0.0f;
   x.weight = weight_of(a, n);
+  if constexpr (!kPairs) {
+    x.advantage = a.advantage[n];
+    x.old_logp = a.old_logp ? a.old_logp[n] : 0.0f;
+  }
   return x;
 }
 
-__device__ __forceinline__ PolicyScalars policy_scalars(const RowArgs& a) {
-  return PolicyScalars{a.s, a.clip_low, a.clip_high, a.kl_coef, a.old_logp ? 0u : 1u};
+template <bool kPairs>
+__device__ __forceinline__ PolicyResult row_result(const RowArgs& a, const PolicyRow& x) {
+  if constexpr (kPairs)
+    return pair_row(x, a.s);
+  else
+    return policy_row(x, policy_scalars(a));
+}
+
+__device__ __forceinline__ void write_row(const RowArgs& a, int64_t n, const PolicyResult& r) {
+  if (a.logp) a.logp[n] = r.logp;
+  if (a.row_loss) a.row_loss[n] = (float)r.loss;
 }
 
 // a.lanes lanes a row: its log-probability, its term of the loss (or of its
@@ -312,49 +352,37 @@ __global__ __launch_bounds__(kRowThreads) void rows_kernel(const RowArgs a) {
   const int64_t t = (int64_t)blockIdx.x * kRowThreads + threadIdx.x, n = t / a.lanes;
   const int lane = (int)(t % a.lanes);
   if (n >= a.N) return;
-  PolicyResult r{0.0, 0.0, 0.0f, {0.0f, 0.0f, 0.0f, 0u}};
+  PolicyResult r{};
   if (row_counts<kPairs>(a, n)) {
-    if constexpr (kPairs) {
-      const double w = weight_of(a, n);
-      const float2 st = merged(a, n, lane);
-      const double logp = (double)a.s * ((double)a.ylab[n] - (double)st.x) - log((double)st.y), c = w * (double)a.s;
-      r.logp = (float)logp;
-      r.term = w * (logp - (a.ref_logp ? (double)a.ref_logp[n] : 0.0));
-      r.grad = RowGrad{(float)(-c / (double)st.y), st.x, (float)(-c * expm1(logp)), 1u};
-    } else {
-      PolicyRow x = policy_inputs(a, n);
-      const float2 st = merged(a, n, lane);
-      x.y_label = a.ylab[n];
-      x.M = st.x;
-      x.S = st.y;
-      r = policy_row(x, policy_scalars(a));
-    }
+    PolicyRow x = row_inputs<kPairs>(a, n);
+    const float2 st = merged(a, n, lane);
+    x.y_label = a.ylab[n];
+    x.M = st.x;
+    x.S = st.y;
+    r = row_result<kPairs>(a, x);
   }
   if (lane != 0) return;
   a.grad[n] = r.grad;
   a.term[n] = r.term;
   if (kPairs) a.row_slope[n] = 0.0f;
-  if (a.logp) a.logp[n] = r.logp;
-  if (a.row_loss) a.row_loss[n] = (float)r.loss;
+  write_row(a, n, r);
 }
 
-// Workgroup i: pair i.  Its sequences are neighbours, so one walk over their
-// rows takes both.
-__global__ __launch_bounds__(kPairThreads) void pair_kernel(const RowArgs a) {
-  __shared__ double buf[2][kPairThreads / 64];
-  const int64_t i = blockIdx.x;
-  auto bound = [&](int64_t q) {  // offsets outside [0, N] end at its borders
-    const int64_t o = a.offsets[q];
-    return o < 0 ? (int64_t)0 : o > a.N ? a.N : o;
-  };
-  const int64_t b0 = bound(2 * i), b1 = bound(2 * i + 1), b2 = bound(2 * i + 2);
+// Rows [first, last) of sequence q; offsets outside [0, N] end at its borders.
+__device__ __forceinline__ int64_t sequence_start(const RowArgs& a, int64_t q) {
+  const int64_t o = a.offsets[q];
+  return o < 0 ? (int64_t)0 : o > a.N ? a.N : o;
+}
+
+// Pair i from its sequences' sums: its outputs, its loss and the loss's
+// derivative in h = sum[0] - sum[1], both weighted.
+struct PairResult {
+  double loss, slope;
+};
+__device__ __forceinline__ PairResult pair_result(const RowArgs& a, int64_t i, double sum0, double sum1, bool writes) {
   const double pw = a.pair_weight ? (double)a.pair_weight[i] : 1.0;
-  double sum[2] = {0.0, 0.0};
-  for (int64_t n = b0 + threadIdx.x; n < b1; n += kPairThreads) sum[0] += a.term[n];
-  for (int64_t n = b1 + threadIdx.x; n < b2; n += kPairThreads) sum[1] += a.term[n];
-  for (int side = 0; side < 2; ++side) sum[side] = block_sum<kPairThreads>(sum[side], buf[side]);
-  const double h = sum[0] - sum[1], beta = a.beta, eps = a.smoothing;
-  double loss, slope;  // of the pair, and its derivative in h
+  const double h = sum0 - sum1, beta = a.beta, eps = a.smoothing;
+  double loss, slope;
   if (a.kind == ARCHEAD_PREF_SIGMOID) {
     const double x = beta * h, e = exp(-fabs(x)), t = log1p(e);  // softplus(x) = max(x, 0) + t
     loss = (1.0 - eps) * ((x < 0.0 ? -x : 0.0) + t) + eps * ((x > 0.0 ? x : 0.0) + t);
@@ -364,34 +392,48 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(const RowArgs a) {
     loss = u * u;
     slope = 2.0 * u;
   }
-  // a pair of weight zero is left out, whatever its rows hold
-  loss = pw != 0.0 ? pw * loss : 0.0;
-  slope = pw != 0.0 ? pw * slope : 0.0;
-  if (threadIdx.x == 0) {
-    a.pair_loss[i] = loss;
-    if (a.chosen) a.chosen[i] = (float)(beta * sum[0]);
-    if (a.rejected) a.rejected[i] = (float)(beta * sum[1]);
+  if (writes) {
+    if (a.chosen) a.chosen[i] = (float)(beta * sum0);
+    if (a.rejected) a.rejected[i] = (float)(beta * sum1);
   }
-  for (int64_t n = b0 + threadIdx.x; n < b1; n += kPairThreads) a.row_slope[n] = (float)slope;
-  for (int64_t n = b1 + threadIdx.x; n < b2; n += kPairThreads) a.row_slope[n] = (float)-slope;
+  // a pair of weight zero is left out, whatever its rows hold
+  return pw != 0.0 ? PairResult{pw * loss, pw * slope} : PairResult{0.0, 0.0};
 }
 
-// The elements [0, len) of a gradient row; `label` is the label's place in them, or no place.
-template <typename T, typename G>
-__device__ __forceinline__ void thread_gradient(const T* y, G* dy, int64_t len, int64_t label, Scale k, RowGrad r) {
+// Workgroup i: pair i.  Its sequences are neighbours, so one walk over their
+// rows takes both.
+__global__ __launch_bounds__(kPairThreads) void pair_kernel(const RowArgs a) {
+  __shared__ double buf[2][kPairThreads / 64];
+  const int64_t i = blockIdx.x;
+  const int64_t b0 = sequence_start(a, 2 * i), b1 = sequence_start(a, 2 * i + 1), b2 = sequence_start(a, 2 * i + 2);
+  double sum[2] = {0.0, 0.0};
+  for (int64_t n = b0 + threadIdx.x; n < b1; n += kPairThreads) sum[0] += a.term[n];
+  for (int64_t n = b1 + threadIdx.x; n < b2; n += kPairThreads) sum[1] += a.term[n];
+  for (int side = 0; side < 2; ++side) sum[side] = block_sum<kPairThreads>(sum[side], buf[side]);
+  const PairResult r = pair_result(a, i, sum[0], sum[1], threadIdx.x == 0);
+  if (threadIdx.x == 0) a.pair_loss[i] = r.loss;
+  for (int64_t n = b0 + threadIdx.x; n < b1; n += kPairThreads) a.row_slope[n] = (float)r.slope;
+  for (int64_t n = b1 + threadIdx.x; n < b2; n += kPairThreads) a.row_slope[n] = (float)-r.slope;
+}
+
+// The elements [0, len) of a gradient row, the share of thread tid of kThreads;
+// `label` is the label's place in them, or no place.
+template <typename T, typename G, int kThreads>
+__device__ __forceinline__ void thread_gradient(const T* y, G* dy, int64_t len, int64_t label, Scale k, RowGrad r,
+                                                int tid) {
   using E = Elem<T>;
   constexpr int n = E::kPer16;
   const int64_t full = len / n;
-  for (int64_t c0 = threadIdx.x; c0 < full; c0 += kRowThreads * kRowUnroll) {
+  for (int64_t c0 = tid; c0 < full; c0 += kThreads * kRowUnroll) {
     u4 v[kRowUnroll];
 #pragma unroll
     for (int u = 0; u < kRowUnroll; ++u) {
-      const int64_t c = c0 + u * kRowThreads;
+      const int64_t c = c0 + u * kThreads;
       if (r.on && c < full) v[u] = *reinterpret_cast<const u4_any*>(y + c * n);
     }
 #pragma unroll
     for (int u = 0; u < kRowUnroll; ++u) {
-      const int64_t c = c0 + u * kRowThreads;
+      const int64_t c = c0 + u * kThreads;
       if (c >= full) break;
       float g[n];
 #pragma unroll
@@ -404,7 +446,7 @@ __device__ __forceinline__ void thread_gradient(const T* y, G* dy, int64_t len, 
       store_run<n>(dy + c * n, g);
     }
   }
-  const int64_t i = full * n + threadIdx.x;
+  const int64_t i = full * n + tid;
   if (i < len) {
     const float g = !r.on ? 0.0f : i == label ? r.label_g : r.neg * exp_at(E::one(y[i]) - r.M, k);
     dy[i] = Elem<G>::from(g);
@@ -424,6 +466,21 @@ __device__ __forceinline__ void loss_total(const RowArgs& a) {
 
 __global__ __launch_bounds__(kRowThreads) void loss_total_kernel(const RowArgs a) { loss_total(a); }
 
+template <typename T, typename G>
+__device__ __forceinline__ void piece_gradient(const RowArgs& a, int64_t n, int p, const RowGrad& r) {
+  const int64_t c0 = p * a.width, c1 = c0 + a.width < a.V ? c0 + a.width : a.V;
+  thread_gradient<T, G, kRowThreads>(static_cast<const T*>(a.Y) + n * a.y_stride + c0,
+                                     static_cast<G*>(a.dY) + n * a.dy_stride + c0, c1 - c0,
+                                     (int64_t)a.labels[n] - c0, a.k, r, threadIdx.x);
+}
+
+__device__ __forceinline__ RowGrad with_slope(RowGrad r, float slope) {
+  r.neg *= slope;
+  r.label_g *= slope;
+  r.on = r.on && slope != 0.0f;
+  return r;
+}
+
 // Workgroup n pieces + p: piece p of row n; one more: the loss.
 template <typename T, typename G>
 __global__ __launch_bounds__(kRowThreads) void row_gradient_kernel(const RowArgs a) {
@@ -431,15 +488,98 @@ __global__ __launch_bounds__(kRowThreads) void row_gradient_kernel(const RowArgs
   const int p = (int)(blockIdx.x % a.pieces);
   if (n >= a.N) return loss_total(a);
   RowGrad r = a.grad[n];
-  if (a.row_slope) {
-    const float slope = a.row_slope[n];
-    r.neg *= slope;
-    r.label_g *= slope;
-    r.on = r.on && slope != 0.0f;
+  if (a.row_slope) r = with_slope(r, a.row_slope[n]);
+  piece_gradient<T, G>(a, n, p, r);
+}
+
+// The same for a policy loss of so few rows that one launch less is worth
+// working a row's numbers out in each of its workgroups (a.lanes is 64).
+template <typename T, typename G>
+__global__ __launch_bounds__(kRowThreads) void few_gradient_kernel(const RowArgs a) {
+  __shared__ RowGrad grad;
+  __shared__ double terms[kFewRows];
+  const int64_t n = blockIdx.x / a.pieces;
+  const int p = (int)(blockIdx.x % a.pieces);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  auto result = [&](int64_t row) {
+    if (!row_counts<false>(a, row)) return PolicyResult{};
+    PolicyRow x = row_inputs<false>(a, row);
+    const float2 st = merged(a, row, lane);
+    x.y_label = a.ylab[row];
+    x.M = st.x;
+    x.S = st.y;
+    return row_result<false>(a, x);
+  };
+  if (n >= a.N) {
+    for (int64_t row = wave; row < a.N; row += kRowThreads / 64) {
+      const PolicyResult r = result(row);
+      if (lane != 0) continue;
+      terms[row] = r.term;
+      write_row(a, row, r);
+    }
+    __syncthreads();
+    double sum = 0.0;
+    for (int64_t row = 0; row < a.N; ++row) sum += terms[row];
+    if (threadIdx.x == 0 && a.loss) *a.loss = (float)sum;
+    return;
   }
-  const int64_t c0 = p * a.width, c1 = c0 + a.width < a.V ? c0 + a.width : a.V;
-  thread_gradient(static_cast<const T*>(a.Y) + n * a.y_stride + c0, static_cast<G*>(a.dY) + n * a.dy_stride + c0,
-                  c1 - c0, (int64_t)a.labels[n] - c0, a.k, r);
+  if (wave == 0) {
+    const PolicyResult r = result(n);
+    if (lane == 0) grad = r.grad;
+  }
+  __syncthreads();
+  piece_gradient<T, G>(a, n, p, grad);
+}
+
+// Either loss of a few short rows in one launch of one workgroup: a wave a
+// row, what rows and pairs tell each other in LDS.
+template <typename T, typename G, bool kPairs>
+__global__ __launch_bounds__(kSmallThreads) void small_loss_kernel(const RowArgs a) {
+  constexpr int kWaves = kSmallThreads / 64;
+  __shared__ RowGrad grad[kSmallRows];
+  __shared__ double term[kSmallRows], pair_loss[kSmallRows];
+  __shared__ float slope[kSmallRows];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  auto row_of = [&](int64_t n) { return static_cast<const T*>(a.Y) + n * a.y_stride; };
+  for (int n = wave; n < a.N; n += kWaves) {
+    PolicyResult r{};
+    if (row_counts<kPairs>(a, n)) {
+      PolicyRow x = row_inputs<kPairs>(a, n);
+      const int64_t label = a.labels[n];
+      x.y_label = label >= 0 && label < a.V ? Elem<T>::one(row_of(n)[label]) : __builtin_nanf("");
+      const float2 st = wave_merge(thread_stats<T, 64>(row_of(n), a.V, a.k, lane), a.k);
+      x.M = st.x;
+      x.S = st.y;
+      r = row_result<kPairs>(a, x);
+    }
+    if (lane != 0) continue;
+    grad[n] = r.grad;
+    term[n] = r.term;
+    slope[n] = kPairs ? 0.0f : 1.0f;
+    write_row(a, n, r);
+  }
+  __syncthreads();
+  if constexpr (kPairs) {
+    for (int i = wave; i < a.B; i += kWaves) {
+      const int64_t b0 = sequence_start(a, 2 * i), b1 = sequence_start(a, 2 * i + 1), b2 = sequence_start(a, 2 * i + 2);
+      const double sum0 = wave_sum(b0 + lane < b1 ? term[b0 + lane] : 0.0);  // at most 64 rows
+      const double sum1 = wave_sum(b1 + lane < b2 ? term[b1 + lane] : 0.0);
+      const PairResult r = pair_result(a, i, sum0, sum1, lane == 0);
+      if (lane == 0) pair_loss[i] = r.loss;
+      if (b0 + lane < b1) slope[b0 + lane] = (float)r.slope;
+      if (b1 + lane < b2) slope[b1 + lane] = (float)-r.slope;
+    }
+    __syncthreads();
+  }
+  if (wave == 0) {
+    const double* parts = kPairs ? pair_loss : term;
+    const double sum = wave_sum(lane < (kPairs ? a.B : a.N) ? parts[lane] : 0.0);
+    if (lane == 0 && a.loss) *a.loss = (float)sum;
+  }
+  if (!a.dY) return;
+  for (int n = wave; n < a.N; n += kWaves)
+    thread_gradient<T, G, 64>(row_of(n), static_cast<G*>(a.dY) + n * a.dy_stride, a.V, a.labels[n], a.k,
+                              with_slope(grad[n], slope[n]), lane);
 }
 
 // The rows in the order policy_fused_kernel takes them: those that count from
@@ -527,7 +667,7 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
     G* out = static_cast<G*>(a.dY) + n * a.dy_stride;
     const bool more = place + gridDim.x < count;
     const int64_t next = more ? a.order[place + gridDim.x] : n;
-    PolicyRow x = policy_inputs(a, n);
+    PolicyRow x = row_inputs<false>(a, n);
     x.y_label = y_label;
     float top = -INFINITY;
 #pragma unroll
@@ -566,7 +706,7 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
     x.M = shift;
     x.S = S;
     if (!(S >= 0.5f && S < INFINITY)) {  // the same decision in every thread
-      const float2 st = block_merge<kFusedThreads>(thread_stats<T, kFusedThreads>(row, a.V, a.k), a.k, pair_buf);
+      const float2 st = block_merge<kFusedThreads>(thread_stats<T, kFusedThreads>(row, a.V, a.k, tid), a.k, pair_buf);
       x.M = st.x;
       x.S = st.y;
     }
@@ -575,8 +715,7 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
       if (lane == 0) {
         grad = r.grad;
         a.term[n] = r.term;
-        if (a.logp) a.logp[n] = r.logp;
-        if (a.row_loss) a.row_loss[n] = (float)r.loss;
+        write_row(a, n, r);
       }
     }
     __syncthreads();
@@ -754,9 +893,37 @@ bool fused_takes(const RowArgs& a, int64_t size) {
   return a.N >= kFusedLeastRows && a.V * size >= kHeldChunks / 2 * kFusedThreads * 16 && a.V < (int64_t(1) << 30);
 }
 
+// One workgroup: at 4 rows of 1024 logits it takes SMALLUS us and the three
+// launches 11; at 64 rows of 1024 as long as those.
+template <bool kPairs>
+bool small_takes(const RowArgs& a) {
+  return a.N <= kSmallRows && a.N * a.V <= 65536 && (!kPairs || a.B <= kSmallRows);
+}
+
 template <typename T, bool kPairs>
 hipError_t launch_loss(const RowArgs& a, const archead_tensor* dY, hipStream_t s) {
   (void)hipGetLastError();  // start from a clean error state
+  const bool bf16 = dY && dY->dtype == ARCHEAD_BF16;
+  if (small_takes<kPairs>(a)) {
+    if (bf16)
+      hipLaunchKernelGGL((small_loss_kernel<T, uint16_t, kPairs>), dim3(1), dim3(kSmallThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL((small_loss_kernel<T, float, kPairs>), dim3(1), dim3(kSmallThreads), 0, s, a);
+    return hipGetLastError();
+  }
+  if constexpr (!kPairs) {
+    if (dY && a.N > 0 && a.N <= kFewRows) {
+      RowArgs f = a;
+      f.lanes = 64;
+      const dim3 grid((unsigned)(a.N * a.pieces)), block(kRowThreads);
+      hipLaunchKernelGGL((row_pieces_kernel<T, kPairs>), grid, block, 0, s, f);
+      if (bf16)
+        hipLaunchKernelGGL((few_gradient_kernel<T, uint16_t>), dim3(grid.x + 1), block, 0, s, f);
+      else
+        hipLaunchKernelGGL((few_gradient_kernel<T, float>), dim3(grid.x + 1), block, 0, s, f);
+      return hipGetLastError();
+    }
+  }
   if constexpr (!kPairs) {
     if (dY && fused_takes(a, sizeof(T))) {
       int device = 0, cus = 0;

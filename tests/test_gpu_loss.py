@@ -192,11 +192,16 @@ def test_policy_wide_ratio_and_kl():
         _check_policy(got, Y64, labels, A, 1.0, kl, None, old, ref, False)
 
 
+# columns and copies of the rows below: one workgroup, a few long rows, rows cut into pieces
+WAYS = [(1500, 1), (9000, 1), (9000, 3)]
+
+
+@pytest.mark.parametrize("V,copies", WAYS)
 @pytest.mark.parametrize("y", ["bfloat16", "float32"])
-def test_policy_uncounted_rows_hold_anything(y):
+def test_policy_uncounted_rows_hold_anything(y, V, copies):
     torch = torch_mod()
     rng = np.random.default_rng(7)
-    N, V = 9, 4100
+    N = 9 * copies
     Y, Y64 = _make_Y(rng, N, V, getattr(torch, y))
     c = _policy_case(rng, N, V, Y64, 1.0)
     w = c["weight"].copy()
@@ -219,31 +224,33 @@ def test_policy_uncounted_rows_hold_anything(y):
     assert none["loss"] == 0 and not none["dY"].any() and not none["row_loss"].any()
 
 
+@pytest.mark.parametrize("V,copies", WAYS)
 @pytest.mark.parametrize("y", ["bfloat16", "float32"])
-def test_policy_masked_vocabulary(y):
+def test_policy_masked_vocabulary(y, V, copies):
     """Logits of -inf and of the type's lowest value in most of a row, whole
     pieces of it among them; rows with nothing left, NaN or +inf are NaN."""
     torch = torch_mod()
     rng = np.random.default_rng(8)
-    N, V = 8, 9000
+    N, at = 8, V // 2
     Y, _ = _make_Y(rng, N, V, getattr(torch, y))
-    labels = np.full(N, 4500)
-    Y[0, :4400] = -float("inf")
-    Y[1, 4501:] = -float("inf")
+    labels = np.full(N, at)
+    Y[0, :at - 100] = -float("inf")
+    Y[1, at + 1:] = -float("inf")
     Y[2, :] = torch.finfo(Y.dtype).min
-    Y[3, :4500] = torch.finfo(Y.dtype).min
+    Y[3, :at] = torch.finfo(Y.dtype).min
     Y[4] = -float("inf")
-    Y[4, 4500] = 1.0
+    Y[4, at] = 1.0
     Y[5] = -float("inf")
     Y[6, 17] = float("nan")
-    Y[7, 8999] = float("inf")
+    Y[7, V - 1] = float("inf")
+    Y, labels = Y.repeat(copies, 1), np.tile(labels, copies)
     Y64 = Y.double().cpu().numpy()
-    A = np.ones(N, np.float32)
+    A = np.ones(N * copies, np.float32)
     got = _run_policy(Y, labels, A)
     want = _check_policy(got, Y64, labels, A, 1.0, 0.0, None, None, None, y == "bfloat16", 0.2, 0.2)
-    assert np.isnan(got["logp"][5:]).all() and np.isfinite(got["logp"][:5]).all() and np.isnan(got["loss"])
+    assert np.isnan(got["logp"][5:8]).all() and np.isfinite(got["logp"][:5]).all() and np.isnan(got["loss"])
     assert abs(got["logp"][2] + np.log(V)) < 1e-5 and got["logp"][4] == 0.0 and not got["dY"][4].any()
-    assert not got["dY"][0, :4400].any() and np.isfinite(want["dY"][:5]).all()
+    assert not got["dY"][0, :at - 100].any() and np.isfinite(want["dY"][:5]).all()
 
 
 @pytest.mark.parametrize("in_place", [False, True])
@@ -297,7 +304,7 @@ def test_policy_label_out_of_range_is_nan():
     assert np.array_equal(np.isnan(got["dY"]).all(1), [False, True, True, False])
 
 
-@pytest.mark.parametrize("V", [1000, 20001])
+@pytest.mark.parametrize("V", [1000, 20001])  # one workgroup, a few long rows
 @pytest.mark.parametrize("y", ["bfloat16", "float32"])
 def test_policy_strides_alignments_and_in_place(y, V):
     """A gradient over its logits, rows of an odd stride and a start off every
@@ -404,6 +411,7 @@ PAIRS = [  # N, V, offsets
     (40, 2049, [0, 7, 20, 21, 40]),
     (40, 513, [3, 7, 7, 21, 30]),            # an empty sequence, rows before and behind
     (9, 20001, [0, 2, 4, 6, 7, 8, 9]),
+    (64, 1000, list(range(0, 65, 2))[:33]),  # sixteen pairs of four rows, one workgroup
     (600, 97, [0, 300, 600]),                # more rows than a workgroup has threads
 ]
 
@@ -440,13 +448,14 @@ def test_preference_large_margins_stay_finite():
         _check_preference(got, Y64, labels, [0, 4, 8], False, ref_logp=ref, beta=1.0, label_smoothing=0.1)
 
 
-def test_preference_pairs_and_rows_left_out():
+@pytest.mark.parametrize("V", [3000, 9000])  # one workgroup, rows cut into pieces
+def test_preference_pairs_and_rows_left_out(V):
     """A pair of weight 0 whose rows are NaN, rows outside every sequence that
     are NaN: the rest as if they were not there, their gradient 0."""
     torch = torch_mod()
     rng = np.random.default_rng(4)
-    Y, _ = _make_Y(rng, 14, 3000, torch.bfloat16)
-    labels = rng.integers(0, 3000, 14)
+    Y, _ = _make_Y(rng, 14, V, torch.bfloat16)
+    labels = rng.integers(0, V, 14)
     off = [2, 4, 6, 9, 12]
     clean = _run_preference(Y, labels, off, pair_weight=[1.0, 0.0])
     Y[6:] = float("nan")
@@ -459,15 +468,16 @@ def test_preference_pairs_and_rows_left_out():
     assert not got["logp"][[0, 1, 12, 13]].any() and np.isnan(got["chosen_reward"][1])
 
 
-def test_preference_offsets_outside_the_rows_end_at_their_borders():
+@pytest.mark.parametrize("V", [400, 12000])  # one workgroup, rows cut into pieces
+def test_preference_offsets_outside_the_rows_end_at_their_borders(V):
     torch = torch_mod()
     rng = np.random.default_rng(12)
-    Y, Y64 = _make_Y(rng, 6, 400, torch.float32)
-    labels = rng.integers(0, 400, 6)
+    Y, Y64 = _make_Y(rng, 6, V, torch.float32)
+    labels = rng.integers(0, V, 6)
     for off in ([-5, 3, 9], [0, 2, 100], [-7, -3, 4, 2 ** 31 - 1, 2 ** 31 - 1], [-(2 ** 31), 6, 6]):
         got = _run_preference(Y, labels, off)
         _check_preference(got, Y64, labels, np.array(off, np.int64), False)
-    # descending: the sequence is empty
+    # descending: the sequence is empty, the others have the rows that are theirs
     got = _run_preference(Y, labels, [4, 2, 6])
     assert got["chosen_reward"][0] == 0 and np.isfinite(got["dY"]).all()
 
