@@ -606,10 +606,14 @@ def _workspace(workspace, need: int, device):
     """The caller's workspace, checked, or one of the call's own."""
     torch = _torch()
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
     if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
     return workspace
+
+
+def _span(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
 
 
 def archead_loss_workspace_bytes(n_rows: int, V: int, n_pairs: int = 0) -> int:
@@ -660,7 +664,7 @@ def archead_policy_loss(Y, labels, advantage, old_logp=None, ref_logp=None, weig
     vec = torch.empty(2 * N + 1, dtype=f32, device=dev)
     at = vec.data_ptr()
     outs = ArcheadPolicyOutputs(at + 8 * N, at, at + 4 * N, dy)
-    status = lib.archead_policy_loss(y, inp, outs, ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    status = lib.archead_policy_loss(y, inp, outs, *_span(ws), _raw_stream(dev))
     if status:
         _check(status, "archead_policy_loss")
     out = {"loss": vec[2 * N], "logp": vec[:N], "row_loss": vec[N:2 * N]}
@@ -700,7 +704,7 @@ def archead_preference_loss(Y, labels, offsets, ref_logp=None, weight=None, pair
     vec = torch.empty(M + 1, dtype=f32, device=dev)
     at = vec.data_ptr()
     outs = ArcheadPreferenceOutputs(at + 4 * M, at, at + 4 * N, at + 4 * (N + B), dy)
-    status = lib.archead_preference_loss(y, inp, outs, ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    status = lib.archead_preference_loss(y, inp, outs, *_span(ws), _raw_stream(dev))
     if status:
         _check(status, "archead_preference_loss")
     out = {"loss": vec[M], "logp": vec[:N], "chosen_reward": vec[N:N + B], "rejected_reward": vec[N + B:M]}
@@ -735,7 +739,7 @@ def archead_logits_backward(dY, head: PackedHead, dH=None, workspace=None):
     ws = _workspace(workspace, _backward_workspace_bytes(head.V, head.D, head.r_c, head.r_r, head.g, dY.shape[0],
                                                          head.fmt), dev)
     p = ArcheadPackedHead(_dims(head.V, head.D, head.r_c, head.r_r, head.g, head.fmt), head.buffer.data_ptr(),
-                          head.buffer.numel(), ws.data_ptr(), ws.numel())
+                          head.buffer.numel(), *_span(ws))
     status = lib.archead_logits_backward(g, p, _tensor(dH), _raw_stream(dev))
     if status:
         _check(status, "archead_logits_backward")

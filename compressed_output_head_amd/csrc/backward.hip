@@ -18,6 +18,7 @@
 //   bwd_main_kernel    the product with the packed residual, the vocabulary
 //                      split over several workgroups where tiles are few
 //   bwd_finish_kernel  the splits' sums and Z B to dH
+// Up to 32 tokens: bwd_few_kernel in place of the three in the middle.
 // The packed residual is never expanded in memory: a stage of 32 vocabulary
 // rows is unpacked to fp16 in LDS, and the MFMA's operand, which runs along
 // the vocabulary, is read from there by transposing LDS reads.
@@ -27,11 +28,6 @@
 #include "device_common.h"
 #include "internal.h"
 
-#ifndef D1
-#define D1 4
-#define D4 2
-#define D8 1
-#endif
 namespace archead {
 
 namespace {
@@ -44,9 +40,10 @@ constexpr int kZsumThreads = 512, kZsumRanks = 64;
 constexpr int kMainThreads = 512;
 constexpr int kFinishThreads = 256;
 constexpr int kFinishRows = 8;
-constexpr int kMaxMaxPieces = 32;
+constexpr int kMaxMaxPieces = 128;
 constexpr int kXcds = 8;
 constexpr int kMaxSplits = 64;
+constexpr int64_t kFewTokens = 32;  // of bwd_few_kernel
 
 struct BwdArgs {
   int64_t V, D, N, n32, nb;
@@ -66,10 +63,10 @@ struct BwdArgs {
   // workspace
   float* pmax;      // [N][pieces][3]
   float* rscale;    // [n32][3] powers of two that undo the rows' scales
-  _Float16* hf;     // [n32/32][ksteps][64][8]
+  _Float16* hf;     // [n32/32][ksteps][64][8]; few tokens: for s_R, s_Ac, s_Aw in turn
   uint8_t* af;      // A codes, [32-rank tiles][ksteps][64][8]
   float* zpart;     // [zparts][n32][r_c + r_r]
-  float* z;         // [n32][r_c + r_r]
+  float* z;         // [n32][r_c + r_r]; null: the parts are summed where Z is used
   float* part;      // [splits][N][D]
   int pieces, zparts, splits, ksteps;
   int64_t width;    // columns of a piece of bwd_max_kernel
@@ -91,7 +88,7 @@ __device__ __forceinline__ Raw8<T> load8(const T* row, int64_t v, int64_t end) {
   if (v + 8 <= end) {
 #pragma unroll
     for (int h = 0; h < (int)sizeof(T) / 2; ++h)
-      x.w[h] = *reinterpret_cast<const u4_any*>(reinterpret_cast<const char*>(row + v) + 16 * h);
+      x.w[h] = __builtin_nontemporal_load(reinterpret_cast<const u4_any*>(reinterpret_cast<const char*>(row + v) + 16 * h));
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -222,30 +219,36 @@ __global__ __launch_bounds__(kMaxThreads) void bwd_max_kernel(const BwdArgs a) {
 // rounded to fp16 and put in LDS in the MFMA operand's order (lane l: row
 // l % 32, columns 16 step + 8 (l / 32) .. + 8).  From there dY s_R goes to
 // memory, 1 KB a store, and wave w multiplies dY s_A of its rank tile with
-// the codes that arrange_codes laid out.
-template <typename T>
-__global__ __launch_bounds__(64 * kPrepWaves) void bwd_prep_kernel(const BwdArgs a) {
-  __shared__ int sExp[3][32];
+// the codes that arrange_codes laid out; without kZ all three go to memory,
+// for bwd_few_kernel.
+// (Four waves a SIMD: with the three that its registers would else leave it takes 0.89 ms
+// on 4096 rows of 151936, with them 0.63, with five and their spills 1.46.)
+template <typename T, bool kZ>
+__global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdArgs a) {
+  __shared__ uint32_t sMax[3][32];
   __shared__ h8 frag[3][8][66];  // steps two octets apart, so that a wave's writes meet no bank twice
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t tile = blockIdx.x;
   const int part = blockIdx.y;
   const bool first = blockIdx.z == 0;
-  if (tid < 96) {
-    const int q = tid / 32;
-    const int64_t row = 32 * tile + tid % 32;
-    float m = 0.0f;
-    if (row < a.N)
-      for (int p = 0; p < a.pieces; ++p) m = fmaxf(m, a.pmax[(row * a.pieces + p) * 3 + q]);
-    const int S = row_exponent(m);
-    sExp[q][tid % 32] = S;
-    if (part == 0 && first) a.rscale[row * 3 + q] = ldexpf(1.0f, -S);
+  if (tid < 96) sMax[tid / 32][tid % 32] = 0u;
+  __syncthreads();
+  {
+    // the pieces' maxima of the tile's rows lie together; magnitudes order as their bits do
+    const int per_row = 3 * a.pieces, count = per_row * (int)std::min<int64_t>(32, a.N - 32 * tile);
+    const float* src = a.pmax + 32 * tile * per_row;
+    for (int i = tid; i < count; i += 64 * kPrepWaves)
+      atomicMax(&sMax[i % 3][i / per_row], __float_as_uint(src[i]));
   }
   __syncthreads();
+  // at most 112: a finite y of a vocabulary entry of scale 0 stays finite
+  auto exponent = [&](int q, int rr) { return std::min(row_exponent(__uint_as_float(sMax[q][rr])), 112); };
+  if (tid < 96 && part == 0 && first)
+    a.rscale[(32 * tile + tid % 32) * 3 + tid / 32] = ldexpf(1.0f, -exponent(tid / 32, tid % 32));
   // this thread's rows and columns of a run: octet tid % 16 of rows tid / 16 and + 16
   const int oct = tid & 15;
-  int e[2][3];
+  float P[2][3];
   const T* row[2];
   bool real[2];
 #pragma unroll
@@ -254,11 +257,11 @@ __global__ __launch_bounds__(64 * kPrepWaves) void bwd_prep_kernel(const BwdArgs
     real[i] = 32 * tile + rr < a.N;
     row[i] = static_cast<const T*>(a.dY) + (real[i] ? 32 * tile + rr : 0) * a.dy_stride;
 #pragma unroll
-    for (int q = 0; q < 3; ++q) e[i][q] = sExp[q][rr];
+    for (int q = 0; q < 3; ++q) P[i][q] = ldexpf(1.0f, exponent(q, rr));
   }
   const int64_t V16 = 16 * a.nb;
   const int r = a.r_c + a.r_r, tiles = a.nct + a.nwt;
-  const int t = kPrepWaves * (int)blockIdx.z + wave;  // this wave's rank tile
+  const int t = kZ ? kPrepWaves * (int)blockIdx.z + wave : tiles;  // this wave's rank tile
   const bool in_c = t < a.nct;
   const int runs = (a.ksteps + 7) / 8;
   const int run0 = (int)((int64_t)part * runs / gridDim.y), run1 = (int)((int64_t)(part + 1) * runs / gridDim.y);
@@ -289,10 +292,11 @@ __global__ __launch_bounds__(64 * kPrepWaves) void bwd_prep_kernel(const BwdArgs
       h8 f[3];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
+        // one rounding: the product with the power of two is exact
         const float y = at(x[i], j);
-        f[0][j] = (_Float16)ldexpf(y * scale_R(s, j), e[i][0]);
-        f[1][j] = (_Float16)ldexpf(y * scale_A(s, a.nA, 0, j), e[i][1]);
-        f[2][j] = (_Float16)ldexpf(y * scale_A(s, a.nA, 1, j), e[i][2]);
+        f[0][j] = (_Float16)fmaf(y * P[i][0], scale_R(s, j), 0.0f);
+        f[1][j] = (_Float16)fmaf(y * P[i][1], scale_A(s, a.nA, 0, j), 0.0f);
+        f[2][j] = (_Float16)fmaf(y * P[i][2], scale_A(s, a.nA, 1, j), 0.0f);
       }
       const int at_ = 32 * (oct & 1) + (tid >> 4) + 16 * i;
 #pragma unroll
@@ -302,9 +306,12 @@ __global__ __launch_bounds__(64 * kPrepWaves) void bwd_prep_kernel(const BwdArgs
     __syncthreads();
     if (first) {
 #pragma unroll
-      for (int k = wave; k < 8; k += kPrepWaves)
-        if (8 * run + k < a.ksteps)
-          *reinterpret_cast<h8*>(a.hf + ((tile * a.ksteps + 8 * run + k) * 64 + lane) * 8) = frag[0][k][lane];
+      for (int q = 0; q < (kZ ? 1 : 3); ++q)
+#pragma unroll
+        for (int k = wave; k < 8; k += kPrepWaves)
+          if (8 * run + k < a.ksteps)
+            *reinterpret_cast<h8*>(a.hf + (((q * (a.n32 / 32) + tile) * a.ksteps + 8 * run + k) * 64 + lane) * 8) =
+                frag[q][k][lane];
     }
     if (t < tiles) {
 #pragma unroll
@@ -380,8 +387,9 @@ struct MainShape {
   static constexpr int WM = TT >= 4 ? 2 : 1, WN = 8 / WM;  // eight waves in WM rows
   static constexpr int MT = TT / WM, NT = 8 / WN;          // 32 x 32 tiles of a wave
   static constexpr int kFrags = 4 * TT;                    // 1 KB dY fragments of a stage
-  static constexpr int kLoads = (kFrags + 7) / 8;          // of those, per wave
-  static constexpr int kDepth = TT <= 2 ? D1 : TT == 4 ? D4 : D8;  // stages whose loads are in flight
+  static constexpr int kLoads = kFrags / 8;                // of those, per wave
+  static_assert(kFrags % 8 == 0, "TT must be even");
+  static constexpr int kDepth = TT == 2 ? 4 : TT == 4 ? 2 : 1;  // stages whose loads are in flight
 };
 
 // kCodes: group codes of 128 columns of a row: 4 for g = 32, 2 for 64, else 1.
@@ -423,67 +431,96 @@ __global__ __launch_bounds__(kMainThreads, TT >= 8 ? 2 : 4) void bwd_main_kernel
                                : *c;
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
-      const int f = std::min(8 * i + wave, S::kFrags - 1);
+      const int f = 8 * i + wave;
       const int64_t tile = std::min(tb * TT + f / 4, ntiles - 1);
       av[slot][i] = *reinterpret_cast<const h8*>(a.hf + ((tile * a.ksteps + 4 * s + f % 4) * 64 + lane) * 8);
     }
   };
-  auto store = [&](int buf, auto slot_) {
-    constexpr int slot = decltype(slot_)::value;
+  // columns 32 d .. + 32 of the packed tile in a register slot to the LDS tile
+  auto unpack = [&](auto buf_, auto slot_, int d) {
+    constexpr int buf = decltype(buf_)::value, slot = decltype(slot_)::value;
+    const uint32_t c = kCodes == 4 ? (code[slot] >> (8 * d)) & 0xffu
+                       : kCodes == 2 ? (code[slot] >> (8 * (d >> 1))) & 0xffu
+                                     : code[slot];
+    sB[buf][tile_octet(16 * blk + (lane & 15), 16 * kth + 4 * d + (lane >> 4))] =
+        unpack_q4_scaled(w[slot][d], (_Float16)(float)c);
+  };
+  auto put_fragments = [&](auto buf_, auto slot_) {
+    constexpr int buf = decltype(buf_)::value, slot = decltype(slot_)::value;
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      const uint32_t c = kCodes == 4 ? (code[slot] >> (8 * d)) & 0xffu
-                         : kCodes == 2 ? (code[slot] >> (8 * (d >> 1))) & 0xffu
-                                       : code[slot];
-      sB[buf][tile_octet(16 * blk + (lane & 15), 16 * kth + 4 * d + (lane >> 4))] =
-          unpack_q4_scaled(w[slot][d], (_Float16)(float)c);
-    }
-#pragma unroll
-    for (int i = 0; i < S::kLoads; ++i)
-      if (8 * i + wave < S::kFrags) sA[buf][8 * i + wave][lane] = av[slot][i];
+    for (int i = 0; i < S::kLoads; ++i) sA[buf][8 * i + wave][lane] = av[slot][i];
   };
 
   f16x acc[S::MT][S::NT] = {};
   const int q = lane & 15, colhalf = (lane >> 4) & 1, khalf = lane >> 5;
-  auto compute = [&](int buf) {
+  // operands of an MFMA step, fetched while the step before it runs
+  h8 fa[2][S::MT], fb[2][S::NT];
+  auto fetch = [&](auto buf_, auto t_) {
+    constexpr int buf = decltype(buf_)::value, t = decltype(t_)::value, P = t & 1;
     const _Float16* B = reinterpret_cast<const _Float16*>(sB[buf]);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      h8 b[S::NT];
+    for (int c = 0; c < S::NT; ++c) {
+      const int ct = wn * S::NT + c;
+      h4 x[2];
 #pragma unroll
-      for (int c = 0; c < S::NT; ++c) {
-        const int ct = wn * S::NT + c;
-        h4 x[2];
-#pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-          const int k = 16 * t + 8 * khalf + 4 * rr + q / 4;
-          x[rr] = read_tr(B + 8 * tile_octet(k, 4 * ct + 2 * colhalf + (q & 3) / 2) + 4 * (q & 1));
-        }
-        b[c] = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
+      for (int rr = 0; rr < 2; ++rr) {
+        const int k = 16 * t + 8 * khalf + 4 * rr + q / 4;
+        x[rr] = read_tr(B + 8 * tile_octet(k, 4 * ct + 2 * colhalf + (q & 3) / 2) + 4 * (q & 1));
       }
-#pragma unroll
-      for (int m = 0; m < S::MT; ++m) {
-        const h8 f = sA[buf][4 * (wm * S::MT + m) + t][lane];
-#pragma unroll
-        for (int c = 0; c < S::NT; ++c) acc[m][c] = mfma32(f, b[c], acc[m][c]);
-      }
+      fb[P][c] = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
     }
+#pragma unroll
+    for (int m = 0; m < S::MT; ++m) fa[P][m] = sA[buf][4 * (wm * S::MT + m) + t][lane];
   };
+  auto multiply = [&](auto t_) {
+    constexpr int P = decltype(t_)::value & 1;
+#pragma unroll
+    for (int m = 0; m < S::MT; ++m)
+#pragma unroll
+      for (int c = 0; c < S::NT; ++c) acc[m][c] = mfma32(fa[P][m], fb[P][c], acc[m][c]);
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
   if (s0 < s1) {
+    constexpr int kUnroll = kDepth < 2 ? 2 : kDepth;
     static_for<0, kDepth>([&](auto i) { load(s0 + decltype(i)::value, i); });
-    store(0, std::integral_constant<int, 0>{});
-    load(s0 + kDepth, std::integral_constant<int, 0>{});
+    for (int d = 0; d < 4; ++d) unpack(I0{}, I0{}, d);
+    put_fragments(I0{}, I0{});
+    load(s0 + kDepth, I0{});
     __syncthreads();
-    for (int g0 = s0; g0 < s1; g0 += kDepth)
-      static_for<1, kDepth + 1>([&](auto i) {
-        // stage s; the next one waits in slot i mod kDepth
-        const int s = g0 + decltype(i)::value - 1;
-        constexpr std::integral_constant<int, decltype(i)::value % kDepth> slot{};
+    fetch(I0{}, I0{});
+    // One stage from LDS tile i & 1: each step's operands are fetched, and the
+    // next stage unpacked to the other tile, while the step before multiplies;
+    // its last step multiplies behind the barrier that opens the other tile.
+    for (int g0 = s0; g0 < s1; g0 += kUnroll)
+      static_for<0, kUnroll>([&](auto i_) {
+        constexpr int i = decltype(i_)::value;
+        constexpr std::integral_constant<int, i & 1> buf{};
+        constexpr std::integral_constant<int, (i + 1) & 1> other{};
+        constexpr std::integral_constant<int, (i + 1) % kDepth> slot{};
+        const int s = g0 + i;
         if (s >= s1) return;
-        compute((s - s0) & 1);
-        store((s - s0 + 1) & 1, slot);
+        fetch(buf, I1{});
+        unpack(other, slot, 0);
+        unpack(other, slot, 1);
+        multiply(I0{});
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(buf, I2{});
+        unpack(other, slot, 2);
+        unpack(other, slot, 3);
+        multiply(I1{});
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(buf, I3{});
+        put_fragments(other, slot);
         load(s + 1 + kDepth, slot);
+        multiply(I2{});
+        __builtin_amdgcn_sched_barrier(0);
         __syncthreads();
+        fetch(other, I0{});
+        multiply(I3{});
+        __builtin_amdgcn_sched_barrier(0);
       });
   }
   // columns sit in the tile in the order the unpacking gives them
@@ -499,6 +536,153 @@ __global__ __launch_bounds__(kMainThreads, TT >= 8 ? 2 : 4) void bwd_main_kernel
         if (n < a.N && d < a.D) a.part[((int64_t)split * a.N + n) * a.D + d] = acc[m][c][v];
       }
     }
+}
+
+constexpr int kFewWaves = kMainThreads / 64;
+
+// What the waves of bwd_few_kernel keep in LDS: a tile each, and at the end
+// half of the waves' sums.
+union FewShared {
+  h8 tile[kFewWaves][16 * 16];
+  float sum[kFewWaves / 2][4][16][64];
+};
+
+// The waves' sums of kCols result tiles added up in wave 0: the upper half of
+// the waves to LDS, added by the lower half, three times.  Elements 4 i .. + 4
+// of a result are rows 8 i .. + 8.
+template <int kCols>
+__device__ __forceinline__ void few_reduce(FewShared& sm, f16x (&acc)[kCols], int64_t N, int wave, int lane) {
+#pragma unroll
+  for (int half = kFewWaves / 2; half > 0; half >>= 1) {
+    __syncthreads();
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (8 * i >= N) break;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+          for (int v = 4 * i; v < 4 * i + 4; ++v) sm.sum[wave - half][c][v][lane] = acc[c][v];
+      }
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (8 * i >= N) break;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+          for (int v = 4 * i; v < 4 * i + 4; ++v) acc[c][v] += sm.sum[wave][c][v][lane];
+      }
+    }
+  }
+}
+
+// Rank tile t of Z over blocks [b0, b1) of 16 vocabulary rows.
+__device__ __forceinline__ void few_ranks(const BwdArgs& a, FewShared& sm, int t, int split, int b0, int b1, int wave,
+                                          int lane) {
+  const bool in_c = t < a.nct;
+  const _Float16* fsrc = a.hf + ((int64_t)(in_c ? 1 : 2) * a.ksteps * 64 + lane) * 8;
+  const u2* codes = reinterpret_cast<const u2*>(a.af) + (int64_t)t * a.ksteps * 64 + lane;
+  f16x acc[1] = {};
+#pragma unroll 4
+  for (int b = b0 + wave; b < b1; b += kFewWaves) {
+    const u2 c = codes[(int64_t)b * 64];
+    acc[0] = mfma32(*reinterpret_cast<const h8*>(fsrc + (int64_t)b * 512), unpack_i8x8(c[0], c[1]), acc[0]);
+  }
+  few_reduce(sm, acc, a.N, wave, lane);
+  const int j = 32 * (in_c ? t : t - a.nct) + (lane & 31), r = a.r_c + a.r_r;
+  if (wave != 0 || j >= (in_c ? a.r_c : a.r_r)) return;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) {
+    const int64_t n = 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+    if (n < a.N) a.zpart[((int64_t)split * a.n32 + n) * r + (in_c ? 0 : a.r_c) + j] = acc[0][v];
+  }
+}
+
+// Up to 32 tokens: one 128-column k-tile per workgroup over a share of the
+// vocabulary, or one 32-rank tile of Z.  Each of the eight waves streams
+// packed tiles of its own (16 vocabulary rows, one MFMA step) and the step's
+// dY fragment, turns them in 4 KB of LDS that no other wave reads, and keeps
+// the sums of all the tokens and columns; the waves' sums are added at the
+// end.  A rank tile's codes come in operand order already.
+// On one token of a 151936 x 4096 head the k-tiles take 88 us, 77 of them with
+// the packed tiles' loads alone (without the group codes and the fragments);
+// neither the unpacking nor the LDS traffic shows, and deeper rings with fewer
+// waves take longer.
+template <int kCodes>
+__global__ __launch_bounds__(kMainThreads, 4) void bwd_few_kernel(const BwdArgs a) {
+  constexpr int kDepth = kCodes == 4 ? 3 : 4;  // without spills
+  __shared__ __align__(16) FewShared sm;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tiles = a.nkt + a.nct + a.nwt, kt = blockIdx.x % tiles, split = blockIdx.x / tiles, nb = (int)a.nb;
+  const int b0 = (int)((int64_t)split * nb / a.splits), b1 = (int)((int64_t)(split + 1) * nb / a.splits);
+  if (kt >= a.nkt) return few_ranks(a, sm, kt - a.nkt, split, b0, b1, wave, lane);
+  const uint8_t* wsrc = a.r_codes + (int64_t)kt * a.nb * 1024 + lane * 16;
+  const uint8_t* csrc = a.r_gcodes + (lane & 15) * a.ng + kKTile * kt / a.g;
+  const _Float16* fsrc = a.hf + lane * 8;
+  u4 w[kDepth];
+  uint32_t code[kDepth];
+  h8 f[kDepth];
+  auto load = [&](int b, auto slot_) {
+    constexpr int slot = decltype(slot_)::value;
+    b = std::min(b, b1 - 1);  // past the end: a tile that is cached, never used
+    w[slot] = *reinterpret_cast<const u4*>(wsrc + (int64_t)b * 1024);
+    const uint8_t* c = csrc + (int64_t)b * 16 * a.ng;
+    code[slot] = kCodes == 4   ? *reinterpret_cast<const uint32_t*>(c)
+                 : kCodes == 2 ? *reinterpret_cast<const uint16_t*>(c)
+                               : *c;
+    f[slot] = *reinterpret_cast<const h8*>(fsrc + (int64_t)b * 512);
+  };
+  f16x acc[4] = {};
+  h8* tile = sm.tile[wave];
+  const int q = lane & 15, colhalf = (lane >> 4) & 1, khalf = lane >> 5;
+  auto place = [](int k, int o) { return 16 * k + (o ^ (((k & 3) << 2) | ((k >> 2) & 3))); };  // as tile_octet
+  auto use = [&](auto slot_) {
+    constexpr int slot = decltype(slot_)::value;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const uint32_t c = kCodes == 4   ? (code[slot] >> (8 * d)) & 0xffu
+                         : kCodes == 2 ? (code[slot] >> (8 * (d >> 1))) & 0xffu
+                                       : code[slot];
+      tile[place(lane & 15, 4 * d + (lane >> 4))] = unpack_q4_scaled(w[slot][d], (_Float16)(float)c);
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      h4 x[2];
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr)
+        x[rr] = read_tr(reinterpret_cast<const _Float16*>(tile) +
+                        8 * place(8 * khalf + 4 * rr + q / 4, 4 * c + 2 * colhalf + (q & 3) / 2) + 4 * (q & 1));
+      acc[c] = mfma32(f[slot], __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7), acc[c]);
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+  if (b0 + wave < b1) {
+    static_for<0, kDepth>([&](auto i) { load(b0 + wave + kFewWaves * decltype(i)::value, i); });
+    for (int g0 = b0 + wave; g0 < b1; g0 += kFewWaves * kDepth)
+      static_for<0, kDepth>([&](auto i) {
+        const int b = g0 + kFewWaves * decltype(i)::value;
+        if (b >= b1) return;
+        use(i);
+        load(b + kFewWaves * kDepth, i);
+      });
+  }
+  few_reduce(sm, acc, a.N, wave, lane);
+  if (wave != 0) return;
+  const int c32 = lane & 31;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int64_t d = 128 * (int64_t)kt + 32 * c + 8 * (c32 >> 3) + k_order_h(c32 & 7);
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int64_t n = 8 * (v >> 2) + 4 * khalf + (v & 3);
+      if (n < a.N) a.part[((int64_t)split * a.N + n) * a.D + d] = acc[c][v];
+    }
+  }
 }
 
 // kFinishRows rows x 256 columns of dH, four columns a lane: the splits' sums
@@ -519,7 +703,14 @@ __global__ __launch_bounds__(kFinishThreads) void bwd_finish_kernel(const BwdArg
   float* Z = sZ + (kShared ? 0 : wave * r * kRows);
   for (int e = kShared ? tid : lane; e < kRows * r; e += kShared ? kFinishThreads : 64) {
     const int i = e / r, j = e % r;
-    Z[j * kRows + i] = i < rows ? a.z[(n0 + i) * r + j] : 0.0f;
+    float z = 0.0f;
+    if (i < rows && a.z) z = a.z[(n0 + i) * r + j];
+    if (i < rows && !a.z) {  // few tokens: bwd_zsum_kernel is not worth its launch
+#pragma unroll 8
+      for (int p = 0; p < a.zparts; ++p) z += a.zpart[((int64_t)p * a.n32 + n0 + i) * r + j];
+      z *= a.rscale[(n0 + i) * 3 + (j < a.r_c ? 1 : 2)];
+    }
+    Z[j * kRows + i] = z;
   }
   __syncthreads();
   const int first = kShared ? wave : 0, step = kShared ? kWaves : 1;
@@ -583,22 +774,26 @@ __global__ __launch_bounds__(kFinishThreads) void bwd_finish_kernel(const BwdArg
 
 // ------------------------------------------------------------------- host ---
 
-int main_tiles(int64_t N) { return N <= 32 ? 1 : N <= 64 ? 2 : N <= 128 ? 4 : 8; }
+int main_tiles(int64_t N) { return N <= 64 ? 2 : N <= 128 ? 4 : 8; }
 
-// Parts of the vocabulary for the main kernel: the fewest whose workgroups
-// fill whole rounds of the resident ones (one a CU for 256-token tiles, two
-// for smaller ones) to within 4%, at least 4 stages each.
-int main_splits(int64_t N, int64_t D, int64_t stages) {
+// Parts of the vocabulary for the main kernel: the count that a model of its
+// time likes best, workgroups in rounds of the resident ones (one a CU for
+// 256-token tiles, two for smaller ones) of kRoundUs plus a stage's measured
+// time for every stage, and the partial sums written and read at 4 TB/s.
+int main_splits(int64_t N, int64_t D, int64_t ranks, int64_t stages) {
+  constexpr double kRoundUs = 4.0;
+  if (N <= kFewTokens)  // two workgroups a CU; a packed tile for each wave at least
+    return (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, 512 / (D / kKTile + ranks), (stages + 1) / 2}));
   const int tt = main_tiles(N);
-  const int64_t tiles = (N + 32 * tt - 1) / (32 * tt) * ((D + 255) / 256);
-  const int64_t slots = tt == 8 ? 256 : 512;
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, stages / 4));
+  const int64_t tiles = (N + 32 * tt - 1) / (32 * tt) * ((D + 255) / 256), slots = tt == 8 ? 256 : 512;
+  const double stage_us = tt == 8 ? 1.9 : tt == 4 ? 1.7 : 1.4;
   double best = 1e30;
   int pick = 1;
-  for (int64_t p = 1; p <= most; ++p) {
-    const double rounds = (double)((tiles * p + slots - 1) / slots) / (double)p;
-    if (rounds < 0.96 * best) {
-      best = rounds;
+  for (int64_t p = 1; p <= std::min<int64_t>(kMaxSplits, stages); ++p) {
+    const double us = (double)((tiles * p + slots - 1) / slots) * (kRoundUs + stage_us * (double)((stages + p - 1) / p)) +
+                      (double)(p * N * D) * 8.0 / 4e6;
+    if (us < best) {
+      best = us;
       pick = (int)p;
     }
   }
@@ -621,8 +816,10 @@ BwdLayout bwd_layout(const archead_dims* d, int64_t n_tokens) {
   L.pieces = (int)std::max<int64_t>(
       1, std::min<int64_t>({(int64_t)kMaxMaxPieces, (d->V + 2047) / 2048, 2048 * kMaxRows / L.rows}));
   L.width = (int64_t)round_up((uint64_t)((d->V + L.pieces - 1) / L.pieces), 8);
-  L.zparts = (int)std::max<int64_t>(1, std::min<int64_t>({256, (L.ksteps + 31) / 32, 1024 * 32 / L.n32}));
-  L.splits = main_splits(L.rows, d->D, L.ksteps / 4);
+  L.splits = main_splits(L.rows, d->D, (d->r_c + 31) / 32 + (d->r_r + 31) / 32, L.ksteps / 4);
+  L.zparts = L.rows <= kFewTokens
+                 ? L.splits
+                 : (int)std::max<int64_t>(1, std::min<int64_t>({256, (L.ksteps + 7) / 8, 1024 * 32 / L.n32}));
   auto take = [&](uint64_t bytes) {
     const uint64_t at = L.total;
     L.total += round_up(bytes, ARCHEAD_ALIGNMENT);
@@ -630,7 +827,7 @@ BwdLayout bwd_layout(const archead_dims* d, int64_t n_tokens) {
   };
   L.pmax = take((uint64_t)L.rows * L.pieces * 12);
   L.rscale = take((uint64_t)L.n32 * 12);
-  L.hf = take((uint64_t)L.n32 * V64 * 2);
+  L.hf = take((uint64_t)L.n32 * V64 * 2 * (L.rows <= kFewTokens ? 3 : 1));
   L.af = take((uint64_t)((d->r_c + 31) / 32 + (d->r_r + 31) / 32) * L.ksteps * 512);
   L.zpart = take((uint64_t)L.zparts * L.n32 * r * 4);
   L.z = take((uint64_t)L.n32 * r * 4);
@@ -655,21 +852,37 @@ void launch_main_tt(const BwdArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((bwd_main_kernel<TT, 1>), grid, block, 0, s, a);
 }
 
+void launch_few(const BwdArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.nkt + a.nct + a.nwt) * a.splits)), block(kMainThreads);
+  if (a.g == 32)
+    hipLaunchKernelGGL(bwd_few_kernel<4>, grid, block, 0, s, a);
+  else if (a.g == 64)
+    hipLaunchKernelGGL(bwd_few_kernel<2>, grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL(bwd_few_kernel<1>, grid, block, 0, s, a);
+}
+
 template <typename T>
 hipError_t launch_backward(const BwdArgs& a, hipStream_t s) {
   const int64_t ranks = a.nct + a.nwt, max_groups = (a.N + kMaxRows - 1) / kMaxRows * a.pieces;
   hipLaunchKernelGGL(bwd_max_kernel<T>, dim3((unsigned)(max_groups + (ranks * a.ksteps * 16 + kMaxThreads - 1) / kMaxThreads)),
                      dim3(kMaxThreads), 0, s, a);
-  hipLaunchKernelGGL(bwd_prep_kernel<T>,
-                     dim3((unsigned)(a.n32 / 32), (unsigned)a.zparts, (unsigned)std::max<int64_t>(1, (ranks + kPrepWaves - 1) / kPrepWaves)),
-                     dim3(64 * kPrepWaves), 0, s, a);
-  if (ranks > 0)
-    hipLaunchKernelGGL(bwd_zsum_kernel, dim3((unsigned)a.N), dim3(kZsumThreads), 0, s, a);
-  switch (main_tiles(a.N)) {
-    case 1: launch_main_tt<1>(a, s); break;
-    case 2: launch_main_tt<2>(a, s); break;
-    case 4: launch_main_tt<4>(a, s); break;
-    default: launch_main_tt<8>(a, s);
+  const int tt = main_tiles(a.N);
+  if (a.N <= kFewTokens) {
+    const unsigned runs = (unsigned)((a.ksteps + 7) / 8);
+    hipLaunchKernelGGL((bwd_prep_kernel<T, false>), dim3(1, std::min(runs, 1024u)), dim3(64 * kPrepWaves), 0, s, a);
+    launch_few(a, s);
+  } else {
+    hipLaunchKernelGGL((bwd_prep_kernel<T, true>),
+                       dim3((unsigned)(a.n32 / 32), (unsigned)a.zparts, (unsigned)std::max<int64_t>(1, (ranks + kPrepWaves - 1) / kPrepWaves)),
+                       dim3(64 * kPrepWaves), 0, s, a);
+    if (ranks > 0) hipLaunchKernelGGL(bwd_zsum_kernel, dim3((unsigned)a.N), dim3(kZsumThreads), 0, s, a);
+    if (tt == 2)
+      launch_main_tt<2>(a, s);
+    else if (tt == 4)
+      launch_main_tt<4>(a, s);
+    else
+      launch_main_tt<8>(a, s);
   }
   const int64_t row_blocks = (a.N + kFinishRows - 1) / kFinishRows, waves = kFinishThreads / 64;
   const size_t lds = (size_t)kFinishRows * (a.r_c + a.r_r) * 4;
@@ -756,7 +969,7 @@ int archead_logits_backward(const archead_tensor* dY, const archead_packed_head*
     a.hf = reinterpret_cast<_Float16*>(ws + L.hf);
     a.af = ws + L.af;
     a.zpart = reinterpret_cast<float*>(ws + L.zpart);
-    a.z = reinterpret_cast<float*>(ws + L.z);
+    a.z = L.rows <= kFewTokens ? nullptr : reinterpret_cast<float*>(ws + L.z);
     a.part = reinterpret_cast<float*>(ws + L.part);
     a.pieces = L.pieces;
     a.zparts = L.zparts;

@@ -503,10 +503,11 @@ ARCHEAD_API int archead_logits_topk(const archead_tensor* H, const archead_packe
  * arguments give the same bits. */
 
 /* Device workspace of a loss call: n_rows rows of V logits, n_pairs pairs (0
- * for the policy loss): 8 bytes per row and piece (at most 64 pieces a row),
- * 20 per row, 8 per pair, each section rounded up to 256 bytes.  Pure host
- * arithmetic.  E_NULL, E_SHAPE, E_UNSUPPORTED (n_rows or n_pairs above 2^22,
- * V of 2^31 or more). */
+ * for the policy loss).  0 for calls of at most 64 rows, 64 pairs and 65536
+ * logits in all; else 8 bytes per row and piece (at most 64 pieces a row), 32
+ * per row and 4 more, 8 per pair, each section rounded up to 256 bytes.  Pure
+ * host arithmetic.  E_NULL, E_SHAPE, E_UNSUPPORTED (n_rows or n_pairs above
+ * 2^22, V of 2^31 or more). */
 ARCHEAD_API int archead_loss_workspace_bytes(int64_t n_rows, int64_t V, int64_t n_pairs, uint64_t* bytes);
 
 /* Inputs of the clipped policy loss, device arrays of N = Y.rows elements,

@@ -546,8 +546,8 @@ def test_binding_refusals():
                       (lambda: ah.archead_policy_loss(Y, labels, A, dY=Y[:, :9]), 5),
                       (lambda: ah.archead_policy_loss(Y, labels, A, inv_temperature=0.0), 9),
                       (lambda: ah.archead_preference_loss(Y, labels, off, label_smoothing=0.6), 9),
-                      (lambda: ah.archead_policy_loss(Y, labels, A, workspace=torch.zeros(0, dtype=torch.uint8,
-                                                                                          device="cuda")), 1)]:
+                      (lambda: ah.archead_policy_loss(torch.zeros((4, 20000), device="cuda"), labels, A,
+                                                      workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")), 7)]:
         with pytest.raises(ah.ArcheadError) as e:
             f()
         assert e.value.status == status
