@@ -13,7 +13,7 @@
 // is a sum of terms of both signs, and one row is one thread's work).  The
 // difference is taken first: a fused k y - k M would save an instruction, but
 // overflows where every logit of a piece is the type's lowest value.  S is
-// summed in fp32 by thousands of partial sums of at most a few hundred terms.
+// summed in fp32 trees of 8 to 32 terms, and in fp64 from there.
 // The label's element of the gradient is -coef s expm1(log p), which keeps
 // its digits where p is close to 1.
 //
@@ -69,6 +69,12 @@ struct Scale {
   float hi, lo;
 };
 
+// The maximum M of some logits and the sum S of 2^(k (y - M)).
+struct Stat {
+  double S;
+  float M;
+};
+
 struct RowArgs {
   const void* Y;
   void* dY;
@@ -81,7 +87,7 @@ struct RowArgs {
   const int32_t* labels;
   const float* weight;
   // workspace
-  float2* part;    // [N][pieces] (M, S)
+  Stat* part;      // [N][pieces]
   float* ylab;     // [N]
   RowGrad* grad;   // [N]
   double* term;    // [N] weighted, of the loss (policy) or of the sequence's sum (preference)
@@ -157,18 +163,20 @@ __device__ __forceinline__ float exp_at(float d, Scale k) {
 __device__ __forceinline__ float shift_of(float M) { return M == -INFINITY ? 0.0f : M; }
 
 // Two (M, S) pieces as one.
-__device__ __forceinline__ float2 merge(float2 a, float2 b, Scale k) {
-  const float M = fmaxf(a.x, b.x), M0 = shift_of(M);
-  return float2{M, a.y * exp_at(a.x - M0, k) + b.y * exp_at(b.x - M0, k)};
+__device__ __forceinline__ Stat merge(Stat a, Stat b, Scale k) {
+  const float M = fmaxf(a.M, b.M), M0 = shift_of(M);
+  return Stat{a.S * (double)exp_at(a.M - M0, k) + b.S * (double)exp_at(b.M - M0, k), M};
 }
 
-__device__ __forceinline__ float2 wave_merge(float2 v, Scale k) {
-  for (int o = 32; o > 0; o >>= 1) v = merge(v, float2{__shfl_xor(v.x, o), __shfl_xor(v.y, o)}, k);
+__device__ __forceinline__ Stat lane_xor(Stat v, int o) { return Stat{__shfl_xor(v.S, o), __shfl_xor(v.M, o)}; }
+
+__device__ __forceinline__ Stat wave_merge(Stat v, Scale k) {
+  for (int o = 32; o > 0; o >>= 1) v = merge(v, lane_xor(v, o), k);
   return v;
 }
 
 template <int kThreads>
-__device__ __forceinline__ float2 block_merge(float2 v, Scale k, float2* buf) {
+__device__ __forceinline__ Stat block_merge(Stat v, Scale k, Stat* buf) {
   v = wave_merge(v, k);
   if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -202,15 +210,31 @@ __device__ __forceinline__ bool row_counts(const RowArgs& a, int64_t n) {
   return weight_of(a, n) != 0.0f;
 }
 
+// The sum of 2^(k (y - M0)) over a chunk, as a tree: one large term does not
+// round with every small one.
+template <typename T>
+__device__ __forceinline__ float chunk_sum(const u4& v, float M0, Scale k) {
+  using E = Elem<T>;
+  float e[E::kPer16];
+#pragma unroll
+  for (int j = 0; j < E::kPer16; ++j) e[j] = exp_at(E::at(v, j) - M0, k);
+#pragma unroll
+  for (int w = E::kPer16 / 2; w > 0; w >>= 1)
+#pragma unroll
+    for (int j = 0; j < w; ++j) e[j] += e[j + w];
+  return e[0];
+}
+
 // (M, S) of the elements [0, len) at p, the share of thread tid of kThreads.
 template <typename T, int kThreads>
-__device__ __forceinline__ float2 thread_stats(const T* p, int64_t len, Scale k, int tid) {
+__device__ __forceinline__ Stat thread_stats(const T* p, int64_t len, Scale k, int tid) {
   using E = Elem<T>;
   const int64_t full = len / E::kPer16;
-  float M = -INFINITY, M0 = 0.0f, S = 0.0f;
+  float M = -INFINITY, M0 = 0.0f;
+  double S = 0.0;
   auto rise = [&](float top) {  // of the running maximum
     if (top > M) {
-      S *= exp_at(M - top, k);
+      S *= (double)exp_at(M - top, k);
       M = M0 = top;
     }
   };
@@ -228,25 +252,23 @@ __device__ __forceinline__ float2 thread_stats(const T* p, int64_t len, Scale k,
 #pragma unroll
       for (int j = 0; j < E::kPer16; ++j) top = fmaxf(top, E::at(v[u], j));
     rise(top);
-    float add = 0.0f;
+    float add[kRowUnroll];
 #pragma unroll
-    for (int u = 0; u < kRowUnroll; ++u)
-#pragma unroll
-      for (int j = 0; j < E::kPer16; ++j) add += exp_at(E::at(v[u], j) - M0, k);
-    S += add;
+    for (int u = 0; u < kRowUnroll; ++u) add[u] = chunk_sum<T>(v[u], M0, k);
+    S += (double)((add[0] + add[1]) + (add[2] + add[3]));
   }
   const int64_t i = full * E::kPer16 + tid;  // fewer than 8 elements are left
   if (i < len) {
     const float y = E::one(p[i]);
     rise(y);
-    S += exp_at(y - M0, k);
+    S += (double)exp_at(y - M0, k);
   }
-  return float2{M, S};
+  return Stat{S, M};
 }
 
 template <typename T, bool kPairs>
 __global__ __launch_bounds__(kRowThreads) void row_pieces_kernel(const RowArgs a) {
-  __shared__ float2 buf[kRowThreads / 64];
+  __shared__ Stat buf[kRowThreads / 64];
   const int64_t n = blockIdx.x / a.pieces;
   const int p = (int)(blockIdx.x % a.pieces);
   if (!row_counts<kPairs>(a, n)) return;
@@ -257,22 +279,23 @@ __global__ __launch_bounds__(kRowThreads) void row_pieces_kernel(const RowArgs a
   // read here, before any launch that may write the gradient over Y
   if (threadIdx.x == 0 && (valid ? label >= c0 && label < c1 : p == 0))
     a.ylab[n] = valid ? Elem<T>::one(row[label]) : __builtin_nanf("");
-  const float2 r = block_merge<kRowThreads>(thread_stats<T, kRowThreads>(row + c0, c1 - c0, a.k, threadIdx.x), a.k, buf);
+  const Stat r = block_merge<kRowThreads>(thread_stats<T, kRowThreads>(row + c0, c1 - c0, a.k, threadIdx.x), a.k, buf);
   if (threadIdx.x == 0) a.part[n * a.pieces + p] = r;
 }
 
 // (M, S) of row n, merged by a.lanes neighbouring lanes (a power of two that
 // divides 64), of which this is number `lane`; all of them return it.
-__device__ __forceinline__ float2 merged(const RowArgs& a, int64_t n, int lane) {
-  float2 r = lane < a.pieces ? a.part[n * a.pieces + lane] : float2{-INFINITY, 0.0f};
+__device__ __forceinline__ Stat merged(const RowArgs& a, int64_t n, int lane) {
+  Stat r = lane < a.pieces ? a.part[n * a.pieces + lane] : Stat{0.0, -INFINITY};
   for (int p = lane + a.lanes; p < a.pieces; p += a.lanes) r = merge(r, a.part[n * a.pieces + p], a.k);
-  for (int o = a.lanes >> 1; o > 0; o >>= 1) r = merge(r, float2{__shfl_xor(r.x, o), __shfl_xor(r.y, o)}, a.k);
+  for (int o = a.lanes >> 1; o > 0; o >>= 1) r = merge(r, lane_xor(r, o), a.k);
   return r;
 }
 
 // What the policy loss has of one row, and what comes of it.
 struct PolicyRow {
-  float y_label, M, S, advantage, old_logp, ref_logp, weight;
+  double S;
+  float y_label, M, advantage, old_logp, ref_logp, weight;
 };
 struct PolicyResult {
   double loss, term;  // term = weight loss
@@ -288,7 +311,7 @@ struct PolicyScalars {
 // functions in registers that the row needs.
 __device__ __attribute__((noinline)) PolicyResult policy_row(PolicyRow x, PolicyScalars p) {
   const double s = p.s, w = x.weight, A = x.advantage;
-  const double logp = s * ((double)x.y_label - (double)x.M) - log((double)x.S);
+  const double logp = s * ((double)x.y_label - (double)x.M) - log(x.S);
   const double ratio = exp(logp - (p.own_ratio ? logp : (double)x.old_logp));
   const double lo = 1.0 - (double)p.clip_low, hi = 1.0 + (double)p.clip_high;
   const double kept = ratio < lo ? lo : ratio > hi ? hi : ratio;  // NaN stays NaN
@@ -302,7 +325,7 @@ __device__ __attribute__((noinline)) PolicyResult policy_row(PolicyRow x, Policy
   }
   const double c = w * slope * s;
   return PolicyResult{loss, w * loss, (float)logp,
-                      RowGrad{(float)(-c / (double)x.S), x.M, (float)(-c * expm1(logp)), c != 0.0 ? 1u : 0u}};
+                      RowGrad{(float)(-c / x.S), x.M, (float)(-c * expm1(logp)), c != 0.0 ? 1u : 0u}};
 }
 
 __device__ __forceinline__ PolicyScalars policy_scalars(const RowArgs& a) {
@@ -312,9 +335,9 @@ __device__ __forceinline__ PolicyScalars policy_scalars(const RowArgs& a) {
 // A row of a pair: its term of the sequence's sum, and its gradient but for
 // the slope of the pair's loss.
 __device__ __forceinline__ PolicyResult pair_row(const PolicyRow& x, float s) {
-  const double w = x.weight, logp = (double)s * ((double)x.y_label - (double)x.M) - log((double)x.S), c = w * (double)s;
+  const double w = x.weight, logp = (double)s * ((double)x.y_label - (double)x.M) - log(x.S), c = w * (double)s;
   return PolicyResult{0.0, w * (logp - (double)x.ref_logp), (float)logp,
-                      RowGrad{(float)(-c / (double)x.S), x.M, (float)(-c * expm1(logp)), 1u}};
+                      RowGrad{(float)(-c / x.S), x.M, (float)(-c * expm1(logp)), 1u}};
 }
 
 template <bool kPairs>
@@ -355,10 +378,10 @@ __global__ __launch_bounds__(kRowThreads) void rows_kernel(const RowArgs a) {
   PolicyResult r{};
   if (row_counts<kPairs>(a, n)) {
     PolicyRow x = row_inputs<kPairs>(a, n);
-    const float2 st = merged(a, n, lane);
+    const Stat st = merged(a, n, lane);
     x.y_label = a.ylab[n];
-    x.M = st.x;
-    x.S = st.y;
+    x.M = st.M;
+    x.S = st.S;
     r = row_result<kPairs>(a, x);
   }
   if (lane != 0) return;
@@ -506,10 +529,10 @@ __global__ __launch_bounds__(kRowThreads) void few_gradient_kernel(const RowArgs
   auto result = [&](int64_t row) {
     if (!row_counts<false>(a, row)) return PolicyResult{};
     PolicyRow x = row_inputs<false>(a, row);
-    const float2 st = merged(a, row, lane);
+    const Stat st = merged(a, row, lane);
     x.y_label = a.ylab[row];
-    x.M = st.x;
-    x.S = st.y;
+    x.M = st.M;
+    x.S = st.S;
     return row_result<false>(a, x);
   };
   if (n >= a.N) {
@@ -549,9 +572,9 @@ __global__ __launch_bounds__(kSmallThreads) void small_loss_kernel(const RowArgs
       PolicyRow x = row_inputs<kPairs>(a, n);
       const int64_t label = a.labels[n];
       x.y_label = label >= 0 && label < a.V ? Elem<T>::one(row_of(n)[label]) : __builtin_nanf("");
-      const float2 st = wave_merge(thread_stats<T, 64>(row_of(n), a.V, a.k, lane), a.k);
-      x.M = st.x;
-      x.S = st.y;
+      const Stat st = wave_merge(thread_stats<T, 64>(row_of(n), a.V, a.k, lane), a.k);
+      x.M = st.M;
+      x.S = st.S;
       r = row_result<kPairs>(a, x);
     }
     if (lane != 0) continue;
@@ -634,8 +657,9 @@ template <typename T, typename G>
 __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowArgs a) {
   using E = Elem<T>;
   constexpr int n16 = E::kPer16, kWaves = kFusedThreads / 64, kHeld = kHeldChunks;
-  __shared__ float top_buf[kWaves], sum_buf[kWaves];
-  __shared__ float2 pair_buf[kWaves];
+  __shared__ float top_buf[kWaves];
+  __shared__ double sum_buf[kWaves];
+  __shared__ Stat pair_buf[kWaves];
   __shared__ RowGrad grad;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int full = (int)(a.V / n16), rest = (int)(a.V % n16);
@@ -681,23 +705,16 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) top = fmaxf(top, top_buf[w]);
     const float shift = shift_of(top);
-    float S = tid < rest ? exp_at(y_rest - shift, a.k) : 0.0f;
+    double S = tid < rest ? exp_at(y_rest - shift, a.k) : 0.0f;
 #pragma unroll
     for (int c = 0; c < kHeld; ++c) {
-      float add = 0.0f;
-#pragma unroll
-      for (int j = 0; j < n16; ++j) add += exp_at(E::at(v[c], j) - shift, a.k);
-      S += add;
+      S += (double)chunk_sum<T>(v[c], shift, a.k);
       // the gradient converts the chunk anew: kept, the converted logits
       // would take twice the registers that a row has
       asm volatile("" : "+v"(v[c]));
     }
     for (int64_t c = kHeld * kFusedThreads + tid; c < full; c += kFusedThreads) {
-      const u4 y = *reinterpret_cast<const u4_any*>(row + c * n16);
-      float add = 0.0f;
-#pragma unroll
-      for (int j = 0; j < n16; ++j) add += exp_at(E::at(y, j) - shift, a.k);
-      S += add;
+      S += (double)chunk_sum<T>(u4(*reinterpret_cast<const u4_any*>(row + c * n16)), shift, a.k);
     }
     for (int o = 32; o > 0; o >>= 1) S += __shfl_xor(S, o);
     if (lane == 0) sum_buf[wave] = S;
@@ -707,10 +724,10 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
     for (int w = 1; w < kWaves; ++w) S += sum_buf[w];
     x.M = shift;
     x.S = S;
-    if (!(S >= 0.5f && S < INFINITY)) {  // the same decision in every thread
-      const float2 st = block_merge<kFusedThreads>(thread_stats<T, kFusedThreads>(row, a.V, a.k, tid), a.k, pair_buf);
-      x.M = st.x;
-      x.S = st.y;
+    if (!(S >= 0.5 && S < 3e38)) {  // the same decision in every thread
+      const Stat st = block_merge<kFusedThreads>(thread_stats<T, kFusedThreads>(row, a.V, a.k, tid), a.k, pair_buf);
+      x.M = st.M;
+      x.S = st.S;
     }
     if (wave == 0) {
       const PolicyResult r = policy_row(x, policy_scalars(a));
@@ -794,7 +811,7 @@ LossWorkspace loss_workspace(int64_t N, int64_t V, int64_t B) {
     w.total += round_up(bytes, ARCHEAD_ALIGNMENT);
     return at;
   };
-  w.part = take((uint64_t)N * (uint64_t)row_pieces(N, V) * sizeof(float2));
+  w.part = take((uint64_t)N * (uint64_t)row_pieces(N, V) * sizeof(Stat));
   w.ylab = take((uint64_t)N * 4);
   w.grad = take((uint64_t)N * sizeof(RowGrad));
   w.term = take((uint64_t)N * 8);
@@ -873,7 +890,7 @@ RowArgs row_args(const archead_tensor* Y, const archead_tensor* dY, float s, voi
   a.k.hi = (float)k;
   a.k.lo = (float)(k - (double)a.k.hi);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.part = reinterpret_cast<float2*>(ws + W.part);
+  a.part = reinterpret_cast<Stat*>(ws + W.part);
   a.ylab = reinterpret_cast<float*>(ws + W.ylab);
   a.grad = reinterpret_cast<RowGrad*>(ws + W.grad);
   a.term = reinterpret_cast<double*>(ws + W.term);

@@ -498,13 +498,13 @@ ARCHEAD_API int archead_logits_topk(const archead_tensor* H, const archead_packe
  * its gradient.  Logits of -inf have probability 0.
  * dY may be Y itself (same data, dtype and stride: the gradient replaces the
  * logits); otherwise the two must not overlap (E_SHAPE).  Sums of the losses
- * and all per-row arithmetic are fp64, the sum of exponentials fp32; bf16
+ * and all per-row arithmetic are fp64, exponentials fp32; bf16
  * gradients are rounded to nearest even from fp32.  Two calls with the same
  * arguments give the same bits. */
 
 /* Device workspace of a loss call: n_rows rows of V logits, n_pairs pairs (0
  * for the policy loss).  0 for calls of at most 64 rows, 64 pairs and 65536
- * logits in all; else 8 bytes per row and piece (at most 64 pieces a row), 32
+ * logits in all; else 16 bytes per row and piece (at most 64 pieces a row), 32
  * per row and 4 more, 8 per pair, each section rounded up to 256 bytes.  Pure
  * host arithmetic.  E_NULL, E_SHAPE, E_UNSUPPORTED (n_rows or n_pairs above
  * 2^22, V of 2^31 or more). */

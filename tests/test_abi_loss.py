@@ -20,7 +20,7 @@ def _pieces(n, v):
 
 @pytest.mark.parametrize("n,v,b", [(4, 1024, 0), (1, 151936, 0), (4096, 151936, 0), (480, 151936, 4), (70000, 7, 3)])
 def test_loss_workspace_bytes(ah, n, v, b):  # noqa: F811
-    want = 0 if n <= 64 and n * v <= 65536 and b <= 64 else _up(n * _pieces(n, v) * 8) + _up(4 * n) + _up(16 * n) + _up(8 * n) + _up(4 * n + 4) + _up(8 * b)
+    want = 0 if n <= 64 and n * v <= 65536 and b <= 64 else _up(n * _pieces(n, v) * 16) + _up(4 * n) + _up(16 * n) + _up(8 * n) + _up(4 * n + 4) + _up(8 * b)
     assert ah.archead_loss_workspace_bytes(n, v, b) == want
 
 
