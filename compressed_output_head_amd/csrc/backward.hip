@@ -714,23 +714,27 @@ __global__ __launch_bounds__(kFinishThreads) void bwd_finish_kernel(const BwdArg
   }
   __syncthreads();
   const int first = kShared ? wave : 0, step = kShared ? kWaves : 1;
-  const bool in = d < a.D;
+  const bool in = d < a.D && rows > 0;
   f4 acc[kRows] = {};
   if (in) {
+    for (int p = first; p < a.splits; p += step) {
+      f4 y[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)  // past the last row: that one again
+        y[i] = *reinterpret_cast<const f4*>(a.part + ((int64_t)p * a.N + n0 + std::min(i, rows - 1)) * a.D + d);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] += y[i][e];
+    }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      if (i >= rows) break;
-      for (int p = first; p < a.splits; p += step) {
-        const f4 y = *reinterpret_cast<const f4*>(a.part + ((int64_t)p * a.N + n0 + i) * a.D + d);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] += y[e];
-      }
-      const float s = a.rscale[(n0 + i) * 3];
+      const float s = a.rscale[(n0 + std::min(i, rows - 1)) * 3];
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] *= s;
     }
     const int64_t group = d / a.g;
-#pragma unroll 4
+#pragma unroll kShared ? 8 : 4
     for (int j = first; j < r; j += step) {
       const uint32_t c = *reinterpret_cast<const uint32_t*>(a.b_codes + (int64_t)j * a.D + d);
       const float s = f16_to_f32(a.b_scales[(int64_t)j * a.ng + group]);
@@ -887,7 +891,8 @@ hipError_t launch_backward(const BwdArgs& a, hipStream_t s) {
   const int64_t row_blocks = (a.N + kFinishRows - 1) / kFinishRows, waves = kFinishThreads / 64;
   const size_t lds = (size_t)kFinishRows * (a.r_c + a.r_r) * 4;
   const unsigned columns = (unsigned)((a.D + 255) / 256);
-  if (a.N <= 512)
+  // rows of their own for 2048 waves, or a block of rows for every four
+  if (row_blocks * columns < 2048)
     hipLaunchKernelGGL(bwd_finish_kernel<true>, dim3((unsigned)row_blocks, columns), dim3(kFinishThreads), lds, s, a);
   else
     hipLaunchKernelGGL(bwd_finish_kernel<false>, dim3((unsigned)((row_blocks + waves - 1) / waves), columns),
