@@ -242,8 +242,8 @@ __global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdA
       atomicMax(&sMax[i % 3][i / per_row], __float_as_uint(src[i]));
   }
   __syncthreads();
-  // at most 112: a finite y of a vocabulary entry of scale 0 stays finite
-  auto exponent = [&](int q, int rr) { return std::min(row_exponent(__uint_as_float(sMax[q][rr])), 112); };
+  // at most 126: the power and its inverse are normal fp32
+  auto exponent = [&](int q, int rr) { return std::min(row_exponent(__uint_as_float(sMax[q][rr])), 126); };
   if (tid < 96 && part == 0 && first)
     a.rscale[(32 * tile + tid % 32) * 3 + tid / 32] = ldexpf(1.0f, -exponent(tid / 32, tid % 32));
   // this thread's rows and columns of a run: octet tid % 16 of rows tid / 16 and + 16
@@ -292,11 +292,12 @@ __global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdA
       h8 f[3];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        // one rounding: the product with the power of two is exact
+        // the product first, as the maximum was taken: times the power it is below 2^15,
+        // also for a large y of an entry of scale 0; what the power adds is exact
         const float y = at(x[i], j);
-        f[0][j] = (_Float16)fmaf(y * P[i][0], scale_R(s, j), 0.0f);
-        f[1][j] = (_Float16)fmaf(y * P[i][1], scale_A(s, a.nA, 0, j), 0.0f);
-        f[2][j] = (_Float16)fmaf(y * P[i][2], scale_A(s, a.nA, 1, j), 0.0f);
+        f[0][j] = (_Float16)(fmaf(y, scale_R(s, j), 0.0f) * P[i][0]);
+        f[1][j] = (_Float16)(fmaf(y, scale_A(s, a.nA, 0, j), 0.0f) * P[i][1]);
+        f[2][j] = (_Float16)(fmaf(y, scale_A(s, a.nA, 1, j), 0.0f) * P[i][2]);
       }
       const int at_ = 32 * (oct & 1) + (tid >> 4) + 16 * i;
 #pragma unroll
@@ -891,8 +892,8 @@ hipError_t launch_backward(const BwdArgs& a, hipStream_t s) {
   const int64_t row_blocks = (a.N + kFinishRows - 1) / kFinishRows, waves = kFinishThreads / 64;
   const size_t lds = (size_t)kFinishRows * (a.r_c + a.r_r) * 4;
   const unsigned columns = (unsigned)((a.D + 255) / 256);
-  // rows of their own for 2048 waves, or a block of rows for every four
-  if (row_blocks * columns < 2048)
+  // rows of their own for 2048 waves (and their Z in 64 KB of LDS), or a block of rows for every four
+  if (row_blocks * columns < 2048 || lds * waves > 63 * 1024)
     hipLaunchKernelGGL(bwd_finish_kernel<true>, dim3((unsigned)row_blocks, columns), dim3(kFinishThreads), lds, s, a);
   else
     hipLaunchKernelGGL(bwd_finish_kernel<false>, dim3((unsigned)((row_blocks + waves - 1) / waves), columns),
@@ -926,12 +927,13 @@ int archead_logits_backward(const archead_tensor* dY, const archead_packed_head*
   const int64_t N = dY->rows;
   if (N < 0 || dY->cols != d->V || dY->row_stride < d->V) return ARCHEAD_E_SHAPE;
   if (dH->rows != N || dH->cols != d->D || dH->row_stride < d->D) return ARCHEAD_E_SHAPE;
-  // 32-bit row and tile counts; Z of kFinishRows rows in LDS
-  if (N > (int64_t(1) << 22) || d->V > (int64_t(1) << 30) || d->r_c + d->r_r > kMaxRank) return ARCHEAD_E_UNSUPPORTED;
+  // 32-bit row, fragment and work-item counts; Z of kFinishRows rows in LDS
+  if (N > (int64_t(1) << 22) || d->V > (int64_t(1) << 26) || d->r_c + d->r_r > kMaxRank) return ARCHEAD_E_UNSUPPORTED;
   if (N == 0) return ARCHEAD_OK;
   if (!dY->data || !dH->data || !head->buffer || !head->workspace) return ARCHEAD_E_NULL;
   const int size = dY->dtype == ARCHEAD_F32 ? 4 : 2;
   if ((uintptr_t)dY->data % size || (uintptr_t)dH->data % 2) return ARCHEAD_E_ALIGN;
+  if (overlap(dY, size, dH, 2)) return ARCHEAD_E_SHAPE;  // later rows are read after earlier ones are written
   if ((uintptr_t)head->buffer % ARCHEAD_ALIGNMENT || (uintptr_t)head->workspace % ARCHEAD_ALIGNMENT)
     return ARCHEAD_E_ALIGN;
   archead_layout P;

@@ -57,6 +57,17 @@ int check_kernel_dims(const archead_dims* d);
 int check_archead_format(const archead_dims* d);
 // Tokens per launch of the batched kernel for a comparison head.
 constexpr int64_t kAltChunk = 32;
+// Whether two tensors of the same rows share bytes: their spans
+// meet, and they are not two column windows of rows of the same stride.
+inline bool overlap(const archead_tensor* x, int xs, const archead_tensor* y, int ys) {
+  const uint64_t a = (uint64_t)x->data, b = (uint64_t)y->data;
+  const uint64_t sa = (uint64_t)x->row_stride * xs, sb = (uint64_t)y->row_stride * ys;
+  const uint64_t ra = (uint64_t)x->cols * xs, rb = (uint64_t)y->cols * ys, rows = (uint64_t)x->rows;
+  if (a + (rows - 1) * sa + ra <= b || b + (rows - 1) * sb + rb <= a) return false;
+  if (sa != sb) return true;
+  const uint64_t off = (b >= a ? b - a : sa - (a - b) % sa) % sa;
+  return !(off >= ra && off + rb <= sa);
+}
 void compute_layout(const archead_dims* d, archead_layout* L);
 
 // Whether a call with n_tokens rows of H runs the decode kernel (pure host

@@ -828,18 +828,6 @@ int check_shape(int64_t N, int64_t V) {
 
 int elem_size(int32_t dtype) { return dtype == ARCHEAD_F32 ? 4 : dtype == ARCHEAD_BF16 ? 2 : 0; }
 
-// Whether two tensors of the same rows and columns share bytes: their spans
-// meet, and they are not two column windows of rows of the same stride.
-bool overlap(const archead_tensor* x, int xs, const archead_tensor* y, int ys) {
-  const uint64_t a = (uint64_t)x->data, b = (uint64_t)y->data;
-  const uint64_t sa = (uint64_t)x->row_stride * xs, sb = (uint64_t)y->row_stride * ys;
-  const uint64_t ra = (uint64_t)x->cols * xs, rb = (uint64_t)y->cols * ys, rows = (uint64_t)x->rows;
-  if (a + (rows - 1) * sa + ra <= b || b + (rows - 1) * sb + rb <= a) return false;
-  if (sa != sb) return true;
-  const uint64_t off = (b >= a ? b - a : sa - (a - b) % sa) % sa;
-  return !(off >= ra && off + rb <= sa);
-}
-
 int check_rows(const archead_tensor* Y, const archead_tensor* dY, float s) {
   const int ys = elem_size(Y->dtype);
   if (!ys || (dY && !elem_size(dY->dtype))) return ARCHEAD_E_DTYPE;
@@ -943,8 +931,6 @@ hipError_t launch_loss(const RowArgs& a, const archead_tensor* dY, hipStream_t s
         hipLaunchKernelGGL((few_gradient_kernel<T, float>), dim3(grid.x + 1), block, 0, s, f);
       return hipGetLastError();
     }
-  }
-  if constexpr (!kPairs) {
     if (dY && fused_takes(a, sizeof(T))) {
       int device = 0, cus = 0;
       if (hipGetDevice(&device) != hipSuccess ||

@@ -500,7 +500,8 @@ ARCHEAD_API int archead_logits_topk(const archead_tensor* H, const archead_packe
  * logits); otherwise the two must not overlap (E_SHAPE).  Sums of the losses
  * and all per-row arithmetic are fp64, exponentials fp32; bf16
  * gradients are rounded to nearest even from fp32.  Two calls with the same
- * arguments give the same bits. */
+ * arguments give the same bits.  Calls that may run at the same time (other
+ * streams, other threads, captured graphs) need a workspace each. */
 
 /* Device workspace of a loss call: n_rows rows of V logits, n_pairs pairs (0
  * for the policy loss).  0 for calls of at most 64 rows, 64 pairs and 65536
@@ -597,22 +598,24 @@ ARCHEAD_API int archead_preference_loss(const archead_tensor* Y, const archead_p
 /* Device workspace archead_logits_backward needs for n_tokens rows: for
  * min(n_tokens, 4096) rows, dY as fp16 operands (2 bytes an element, rows
  * rounded up to 32 and the vocabulary to 64), fp32 partial sums of dH and of
- * its low-rank part, the A codes in operand order, and row scales.  Pure host arithmetic.  E_NULL, E_DIMS, E_SHAPE,
- * E_UNSUPPORTED. */
+ * its low-rank part, the A codes in operand order, and row scales.  Pure
+ * host arithmetic.  E_NULL, E_DIMS, E_SHAPE, E_UNSUPPORTED. */
 ARCHEAD_API int archead_logits_backward_workspace_bytes(const archead_dims* d, int64_t n_tokens, uint64_t* bytes);
 
 /* dH = dY W_hat, the gradient of the hidden states through the packed head
  * (the transpose of archead_logits; the head itself is not trained).
  *   dY: fp32 or bf16 [N][V] device tensor, any row stride, aligned to its
  *       element size.  Rows of zeros give rows of zeros.
- *   dH: bf16 [N][D] device tensor, any row stride, written completely.
+ *   dH: bf16 [N][D] device tensor, any row stride, written completely; it
+ *       must not overlap dY (E_SHAPE).
  * dY times the head's row scales is rounded to fp16 (after a power of two per
  * row that keeps the row's largest product near the top of the range), the
  * head's integers are exact, all sums are fp32, and dH is rounded to nearest
- * even.  A row of dY that is not finite gives a row of dH that is not.
+ * even.  A row of dY that is not finite (or whose products with the scales
+ * are not) gives a row of dH that is not, and changes no other.
  * head->workspace: at least archead_logits_backward_workspace_bytes.  Rows
  * are taken 4096 at a time.  ARCHead-format heads only, r_c + r_r at most
- * 1024.  E_NULL, E_DIMS, E_DTYPE, E_SHAPE, E_UNSUPPORTED, E_ALIGN, E_SIZE,
+ * 1024, N at most 2^22, V at most 2^26.  E_NULL, E_DIMS, E_DTYPE, E_SHAPE, E_UNSUPPORTED, E_ALIGN, E_SIZE,
  * E_WORKSPACE, E_HIP. */
 ARCHEAD_API int archead_logits_backward(const archead_tensor* dY, const archead_packed_head* head,
                                         archead_tensor* dH, void* stream);

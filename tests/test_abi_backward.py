@@ -30,6 +30,12 @@ def _call(ah, dims=DIMS, fmt=0, N=4, **kw):
     (dict(P_workspace_bytes=1000), 7), (dict(fmt=1, dims=(1024, 256, 0, 0, 64)), 3), (dict(fmt=3), 2),
     (dict(dims=(1024, 256, 16, 8, 16)), 3), (dict(dims=(1024, 256, 12, 8, 64)), 3), (dict(dims=(1024, 200, 0, 0, 8)), 2),
     (dict(dims=(1024, 256, 1024, 8, 64)), 3), (dict(N=1 << 23), 3),
+    (dict(dims=((1 << 26) + 1, 256, 16, 8, 64)), 3),
+    # dH in dY's rows, from before them into them, and behind dY but for its last row's last elements
+    (dict(dH_data=FAKE + 4096), 5), (dict(dH_data=FAKE - 1024), 5), (dict(dH_data=FAKE + 8190), 5),
+    # column windows of rows of one buffer do not meet: the next check answers
+    (dict(dH_data=FAKE + 2048, dH_row_stride=2048, dY_row_stride=2048, P_workspace_bytes=1000), 7),
+    (dict(dH_data=FAKE + 2046, dH_row_stride=2048, dY_row_stride=2048, P_workspace_bytes=1000), 5),
 ])
 def test_backward_error_paths(ah, kw, status):  # noqa: F811
     assert _call(ah, **kw) == status

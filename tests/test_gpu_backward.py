@@ -132,6 +132,67 @@ def test_one_hot_rows_give_the_residual_rows_exactly(V, D, g, N, scale):
         assert np.array_equal(got, want), (first, np.argwhere(got != want)[:4])
 
 
+@pytest.mark.parametrize("N", [3, 40])
+def test_large_values_of_entries_of_scale_zero(N):
+    """A row whose products with the scales are tiny, next to a value that only
+    meets a scale of 0: nothing overflows, and the tiny row is still exact."""
+    torch = torch_mod()
+    V, D, g = 96, 256, 64
+    h = synth.draw_head(np.random.default_rng(11), V, D, 0, 0, g)
+    h.s_R[5] = 0
+    head = ah_mod().PackedHead.from_components(h)
+    W = _dequant(h)
+    dY = torch.zeros((N, V), dtype=torch.float32, device="cuda")
+    v = [i % V for i in range(6, 6 + N)]
+    dY[torch.arange(N), torch.as_tensor(v)] = 2.0 ** -95
+    dY[:, 5] = 1e30
+    got = _run(head, dY)
+    want = torch.as_tensor(W[v] * 2.0 ** -95).to(torch.bfloat16).double().numpy()
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("N", [5, 4096])
+def test_backward_of_the_largest_ranks(N):
+    """r_c + r_r = 1024, with few and with many rows."""
+    torch = torch_mod()
+    V, D, g = 70, 1024, 128
+    h, head = _head(12, V, D, 512, 512, g)
+    dY = torch.as_tensor(_gradient(np.random.default_rng(12), N, V), device="cuda").bfloat16()
+    _check(head, h, dY, f"r=512+512 N={N}")
+
+
+def test_calls_on_two_streams_at_once():
+    """Losses and gradients of two streams that run at the same time, each call
+    with a workspace of its own: the results of calls alone."""
+    torch = torch_mod()
+    ah = ah_mod()
+    V, D = 5000, 512
+    h, head = _head(13, V, D, 16, 8, 64)
+    jobs = []
+    for N in (24, 700):
+        gen = torch.Generator(device="cuda").manual_seed(N)
+        Y = torch.randn((N, V), generator=gen, device="cuda").bfloat16()
+        labels = torch.randint(0, V, (N,), generator=gen, device="cuda", dtype=torch.int32)
+        adv = torch.randn((N,), generator=gen, device="cuda")
+        offsets = torch.tensor([0, N // 3, N // 2, N - 1, N], dtype=torch.int32, device="cuda")
+        jobs.append((Y, labels, adv, offsets, torch.cuda.Stream()))
+
+    def step(Y, labels, adv, offsets, stream=None):
+        p = ah.archead_policy_loss(Y, labels, adv, stream=stream)
+        q = ah.archead_preference_loss(Y, labels, offsets, stream=stream)
+        return [p["loss"], p["logp"], p["dY"], q["loss"], q["dY"],
+                ah.archead_logits_backward(p["dY"], head, stream=stream),
+                ah.archead_logits_backward(q["dY"], head, stream=stream)]
+
+    want = [[t.clone() for t in step(*j[:4])] for j in jobs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [step(*j[:4], stream=j[4]) for j in jobs]
+        torch.cuda.synchronize()
+        for w, x in zip(want, got):
+            assert all(torch.equal(a, b) for a, b in zip(w, x))
+
+
 def test_backward_strided_and_unaligned():
     torch = torch_mod()
     ah = ah_mod()
