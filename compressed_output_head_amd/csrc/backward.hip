@@ -63,8 +63,9 @@ struct BwdArgs {
   // workspace
   float* pmax;      // [N][pieces][3]
   float* rscale;    // [n32][3] powers of two that undo the rows' scales
-  _Float16* hf;     // [n32/32][ksteps][64][8]; few tokens: for s_R, s_Ac, s_Aw in turn
+  _Float16* hf;     // [n32/32][ksteps][64][8]; few tokens: [s_R, s_Ac, s_Aw][ksteps][2][N][8]
   uint8_t* af;      // A codes, [32-rank tiles][ksteps][64][8]
+  uint8_t* gt;      // few tokens: group codes, [D / 128 or D / g][16 nb][128 / g or 1]
   float* zpart;     // [zparts][n32][r_c + r_r]
   float* z;         // [n32][r_c + r_r]; null: the parts are summed where Z is used
   float* part;      // [splits][N][D]
@@ -162,17 +163,47 @@ __device__ __forceinline__ void arrange_codes(const BwdArgs& a, int64_t i) {
   }
 }
 
+// The group codes of 16 vocabulary rows by k-tile, for bwd_few_kernel: thread i
+// takes those of one k-tile (or of the two that share a code of 256 columns).
+// As they are stored, a k-tile's wave finds the 16 bytes that it needs in 16
+// sectors, which took 11 us of 89 on one token of a 151936 x 4096 head.
+template <typename C>
+__device__ __forceinline__ void arrange_groups(const BwdArgs& a, int64_t i) {
+  const int columns = a.ng / (int)sizeof(C);
+  const int64_t kk = i % columns, b = i / columns;
+  if (b >= a.nb) return;
+  const C* src = reinterpret_cast<const C*>(a.r_gcodes) + 16 * b * columns + kk;
+  C c[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) c[k] = src[k * columns];
+  u4* out = reinterpret_cast<u4*>(a.gt) + (kk * a.nb + b) * (int64_t)sizeof(C);
+#pragma unroll
+  for (int k = 0; k < (int)sizeof(C); ++k) {
+    u4 x;
+    __builtin_memcpy(&x, c + k * 16 / sizeof(C), 16);
+    out[k] = x;
+  }
+}
+
 // Workgroup q pieces + p: the largest products of piece p of rows kMaxRows q
 // .. + kMaxRows, which share the scales they are multiplied with.  The
-// workgroups behind those lay the A codes out for bwd_prep_kernel, which the
-// rows do not wait for.
+// workgroups behind those lay the A codes out for bwd_prep_kernel, or the
+// group codes for bwd_few_kernel, which the rows do not wait for.
 template <typename T>
 __global__ __launch_bounds__(kMaxThreads) void bwd_max_kernel(const BwdArgs a) {
   constexpr int kWaves = kMaxThreads / 64;
   __shared__ float buf[kWaves][kMaxRows][3];
   const int64_t groups = (a.N + kMaxRows - 1) / kMaxRows;
   if ((int64_t)blockIdx.x >= groups * a.pieces) {
-    arrange_codes(a, ((int64_t)blockIdx.x - groups * a.pieces) * kMaxThreads + threadIdx.x);
+    const int64_t i = ((int64_t)blockIdx.x - groups * a.pieces) * kMaxThreads + threadIdx.x;
+    if (!a.gt)
+      arrange_codes(a, i);
+    else if (a.g == 32)
+      arrange_groups<uint32_t>(a, i);
+    else if (a.g == 64)
+      arrange_groups<uint16_t>(a, i);
+    else
+      arrange_groups<uint8_t>(a, i);
     return;
   }
   const int64_t n0 = blockIdx.x / a.pieces * kMaxRows;
@@ -220,7 +251,7 @@ __global__ __launch_bounds__(kMaxThreads) void bwd_max_kernel(const BwdArgs a) {
 // l % 32, columns 16 step + 8 (l / 32) .. + 8).  From there dY s_R goes to
 // memory, 1 KB a store, and wave w multiplies dY s_A of its rank tile with
 // the codes that arrange_codes laid out; without kZ all three go to memory,
-// for bwd_few_kernel.
+// for bwd_few_kernel, without the rows that there are not.
 // (Four waves a SIMD: with the three that its registers would else leave it takes 0.89 ms
 // on 4096 rows of 151936, with them 0.63, with five and their spills 1.46.)
 template <typename T, bool kZ>
@@ -309,10 +340,12 @@ __global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdA
 #pragma unroll
       for (int q = 0; q < (kZ ? 1 : 3); ++q)
 #pragma unroll
-        for (int k = wave; k < 8; k += kPrepWaves)
-          if (8 * run + k < a.ksteps)
-            *reinterpret_cast<h8*>(a.hf + (((q * (a.n32 / 32) + tile) * a.ksteps + 8 * run + k) * 64 + lane) * 8) =
-                frag[q][k][lane];
+        for (int k = wave; k < 8; k += kPrepWaves) {
+          const int64_t step = (int64_t)q * a.ksteps + 8 * run + k;
+          if (8 * run + k >= a.ksteps || (!kZ && c32 >= a.N)) continue;
+          h8* out = reinterpret_cast<h8*>(a.hf) + (kZ ? (tile * a.ksteps + step) * 64 + lane : (2 * step + half) * a.N + c32);
+          *out = frag[q][k][lane];
+        }
     }
     if (t < tiles) {
 #pragma unroll
@@ -370,7 +403,7 @@ __device__ __forceinline__ void static_for(F&& f) {
 // rows x 256 columns: both the 16 rows that a wave writes at one octet and the
 // 4 rows x 4 octets that 32 lanes read at a time fall in different banks.
 __device__ __forceinline__ int tile_octet(int k, int o) {
-  return 32 * k + (o ^ (((k & 3) << 2) | ((k >> 2) & 3)));
+  return 32 * k + (o ^ (((k & 3) << 2) | ((k >> 1) & 3)));
 }
 
 typedef short s4 __attribute__((ext_vector_type(4)));
@@ -492,37 +525,54 @@ __global__ __launch_bounds__(kMainThreads, TT >= 8 ? 2 : 4) void bwd_main_kernel
     load(s0 + kDepth, I0{});
     __syncthreads();
     fetch(I0{}, I0{});
+    // A step's MFMAs, with what is around them dealt out between them: an LDS
+    // read, a little arithmetic and an LDS write behind each.  (4096 rows of
+    // 151936 x 4096: 5.05 ms a call against 5.18 in the compiler's own order;
+    // two to five instructions 5.04 to 5.11, the LDS read first 5.31.)
+    auto interleave = [] {
+      static_for<0, S::MT * S::NT>([](auto) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+        __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);  // VALU
+        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);  // LDS write
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    };
     // One stage from LDS tile i & 1: each step's operands are fetched, and the
     // next stage unpacked to the other tile, while the step before multiplies;
     // its last step multiplies behind the barrier that opens the other tile.
-    for (int g0 = s0; g0 < s1; g0 += kUnroll)
-      static_for<0, kUnroll>([&](auto i_) {
-        constexpr int i = decltype(i_)::value;
-        constexpr std::integral_constant<int, i & 1> buf{};
-        constexpr std::integral_constant<int, (i + 1) & 1> other{};
-        constexpr std::integral_constant<int, (i + 1) % kDepth> slot{};
-        const int s = g0 + i;
-        if (s >= s1) return;
-        fetch(buf, I1{});
-        unpack(other, slot, 0);
-        unpack(other, slot, 1);
-        multiply(I0{});
-        __builtin_amdgcn_sched_barrier(0);
-        fetch(buf, I2{});
-        unpack(other, slot, 2);
-        unpack(other, slot, 3);
-        multiply(I1{});
-        __builtin_amdgcn_sched_barrier(0);
-        fetch(buf, I3{});
-        put_fragments(other, slot);
-        load(s + 1 + kDepth, slot);
-        multiply(I2{});
-        __builtin_amdgcn_sched_barrier(0);
-        __syncthreads();
-        fetch(other, I0{});
-        multiply(I3{});
-        __builtin_amdgcn_sched_barrier(0);
-      });
+    auto stage = [&](auto i_, int s) __attribute__((always_inline)) {
+      constexpr int i = decltype(i_)::value;
+      constexpr std::integral_constant<int, i & 1> buf{};
+      constexpr std::integral_constant<int, (i + 1) & 1> other{};
+      constexpr std::integral_constant<int, (i + 1) % kDepth> slot{};
+      fetch(buf, I1{});
+      unpack(other, slot, 0);
+      unpack(other, slot, 1);
+      multiply(I0{});
+      interleave();
+      fetch(buf, I2{});
+      unpack(other, slot, 2);
+      unpack(other, slot, 3);
+      multiply(I1{});
+      interleave();
+      fetch(buf, I3{});
+      put_fragments(other, slot);
+      load(s + 1 + kDepth, slot);
+      multiply(I2{});
+      interleave();
+      __syncthreads();
+      fetch(other, I0{});
+      multiply(I3{});
+      interleave();
+    };
+    // whole rounds without an exit inside (an exit costs 2%), then the rest
+    int g0 = s0;
+    for (; g0 + kUnroll <= s1; g0 += kUnroll)
+      static_for<0, kUnroll>([&](auto i) { stage(i, g0 + decltype(i)::value); });
+    static_for<0, kUnroll - 1>([&](auto i) {
+      if (g0 + decltype(i)::value < s1) stage(i, g0 + decltype(i)::value);
+    });
   }
   // columns sit in the tile in the order the unpacking gives them
   const int c32 = lane & 31;
@@ -541,10 +591,15 @@ __global__ __launch_bounds__(kMainThreads, TT >= 8 ? 2 : 4) void bwd_main_kernel
 
 constexpr int kFewWaves = kMainThreads / 64;
 
+// 16-byte octets from a row of a wave's tile (128 columns) to the next: the four
+// rows that 16 lanes read fall in different banks, and every address is one
+// register and a constant, which tile_octet's are not.
+constexpr int kFewPitch = 21;
+
 // What the waves of bwd_few_kernel keep in LDS: a tile each, and at the end
 // half of the waves' sums.
 union FewShared {
-  h8 tile[kFewWaves][16 * 16];
+  h8 tile[kFewWaves][16 * kFewPitch];
   float sum[kFewWaves / 2][4][16][64];
 };
 
@@ -580,21 +635,62 @@ __device__ __forceinline__ void few_reduce(FewShared& sm, f16x (&acc)[kCols], in
   }
 }
 
+// A lane's place in a wave's tile, and the operand of an MFMA step of columns
+// 32 c .. + 32 from there (rows along the step).
+__device__ __forceinline__ const _Float16* few_operand(const h8* tile, int lane) {
+  const int q = lane & 15, colhalf = (lane >> 4) & 1, khalf = lane >> 5;
+  return reinterpret_cast<const _Float16*>(tile) + 8 * (kFewPitch * (8 * khalf + q / 4) + 2 * colhalf) + 4 * (q & 3);
+}
+__device__ __forceinline__ h8 few_read(const _Float16* at, int c) {
+  return __builtin_shufflevector(read_tr(at + 32 * c), read_tr(at + 32 * c + 32 * kFewPitch), 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
 // Rank tile t of Z over blocks [b0, b1) of 16 vocabulary rows.
 __device__ __forceinline__ void few_ranks(const BwdArgs& a, FewShared& sm, int t, int split, int b0, int b1, int wave,
                                           int lane) {
   const bool in_c = t < a.nct;
-  const _Float16* fsrc = a.hf + ((int64_t)(in_c ? 1 : 2) * a.ksteps * 64 + lane) * 8;
-  const u2* codes = reinterpret_cast<const u2*>(a.af) + (int64_t)t * a.ksteps * 64 + lane;
+  constexpr int kDepth = 8;
+  const int part = in_c ? a.r_c : a.r_r, r = a.r_c + a.r_r, j0 = 32 * (in_c ? t : t - a.nct);
+  const uint8_t* fsrc = reinterpret_cast<const uint8_t*>(a.hf) + (int64_t)(in_c ? 1 : 2) * a.ksteps * 32 * a.N;
+  // lane: eight ranks (they come in eights; past the last ones those again) of row lane / 4
+  const uint8_t* codes = reinterpret_cast<const uint8_t*>(a.a_codes) + (in_c ? 0 : a.r_c) + j0;
+  const uint32_t at_code = (uint32_t)((lane >> 2) * r + std::min(8 * (lane & 3), part - j0 - 8));
+  const uint32_t at_row = 16 * (uint32_t)((lane >> 5) * a.N + std::min<int64_t>(lane & 31, a.N - 1));
   f16x acc[1] = {};
-#pragma unroll 4
-  for (int b = b0 + wave; b < b1; b += kFewWaves) {
-    const u2 c = codes[(int64_t)b * 64];
-    acc[0] = mfma32(*reinterpret_cast<const h8*>(fsrc + (int64_t)b * 512), unpack_i8x8(c[0], c[1]), acc[0]);
+  u2 c[kDepth];
+  h8 f[kDepth];
+  auto load = [&](int b, auto slot_) __attribute__((always_inline)) {
+    constexpr int slot = decltype(slot_)::value;
+    b = std::min(b, b1 - 1);
+    c[slot] = *reinterpret_cast<const u2*>(codes + (int64_t)b * 16 * r + at_code);
+    f[slot] = *reinterpret_cast<const h8*>(fsrc + (int64_t)b * 32 * a.N + at_row);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  h8* put = sm.tile[wave] + kFewPitch * (lane >> 2) + (lane & 3);
+  const _Float16* get = few_operand(sm.tile[wave], lane);
+  auto use = [&](auto slot_) __attribute__((always_inline)) {
+    constexpr int slot = decltype(slot_)::value;
+    *put = unpack_i8x8(c[slot][0], c[slot][1]);
+    __builtin_amdgcn_sched_barrier(0);
+    acc[0] = mfma32(f[slot], few_read(get, 0), acc[0]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (b0 + wave < b1) {  // as the ring of bwd_few_kernel
+    static_for<0, kDepth>([&](auto i) { load(b0 + wave + kFewWaves * decltype(i)::value, i); });
+    int g0 = b0 + wave;
+    for (; g0 + kFewWaves * (kDepth - 1) < b1; g0 += kFewWaves * kDepth)
+      static_for<0, kDepth>([&](auto i) {
+        use(i);
+        load(g0 + kFewWaves * (decltype(i)::value + kDepth), i);
+      });
+    static_for<0, kDepth - 1>([&](auto i) {
+      if (g0 + kFewWaves * decltype(i)::value < b1) use(i);
+    });
   }
   few_reduce(sm, acc, a.N, wave, lane);
-  const int j = 32 * (in_c ? t : t - a.nct) + (lane & 31), r = a.r_c + a.r_r;
-  if (wave != 0 || j >= (in_c ? a.r_c : a.r_r)) return;
+  // ranks sit in the tile in the order the unpacking gives them
+  const int c32 = lane & 31, j = j0 + 8 * (c32 >> 3) + (c32 & 4) + 2 * (c32 & 1) + (c32 >> 1 & 1);
+  if (wave != 0 || j >= part) return;
 #pragma unroll
   for (int v = 0; v < 16; ++v) {
     const int64_t n = 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
@@ -621,60 +717,64 @@ __global__ __launch_bounds__(kMainThreads, 4) void bwd_few_kernel(const BwdArgs 
   const int tiles = a.nkt + a.nct + a.nwt, kt = blockIdx.x % tiles, split = blockIdx.x / tiles, nb = (int)a.nb;
   const int b0 = (int)((int64_t)split * nb / a.splits), b1 = (int)((int64_t)(split + 1) * nb / a.splits);
   if (kt >= a.nkt) return few_ranks(a, sm, kt - a.nkt, split, b0, b1, wave, lane);
-  const uint8_t* wsrc = a.r_codes + (int64_t)kt * a.nb * 1024 + lane * 16;
-  const uint8_t* csrc = a.r_gcodes + (lane & 15) * a.ng + kKTile * kt / a.g;
-  const _Float16* fsrc = a.hf + lane * 8;
+  // addresses: of the block (uniform), and the lane's place in it; lanes
+  // without a token read the last one's row, and their sums are not used
+  const uint8_t* wsrc = a.r_codes + (int64_t)kt * a.nb * 1024;
+  const uint8_t* csrc = a.gt + (int64_t)(kCodes > 1 ? kt : kKTile * kt / a.g) * a.nb * 16 * kCodes;
+  const uint32_t at_lane = (uint32_t)lane * 16, at_code = (uint32_t)(lane & 15) * kCodes;
+  const uint32_t at_row = 16 * (uint32_t)((lane >> 5) * a.N + std::min<int64_t>(lane & 31, a.N - 1));
+  const uint32_t f_step = 32 * (uint32_t)a.N;
   u4 w[kDepth];
   uint32_t code[kDepth];
   h8 f[kDepth];
-  auto load = [&](int b, auto slot_) {
+  auto load = [&](int b, auto slot_) __attribute__((always_inline)) {
     constexpr int slot = decltype(slot_)::value;
     b = std::min(b, b1 - 1);  // past the end: a tile that is cached, never used
-    w[slot] = *reinterpret_cast<const u4*>(wsrc + (int64_t)b * 1024);
-    const uint8_t* c = csrc + (int64_t)b * 16 * a.ng;
+    w[slot] = __builtin_nontemporal_load(reinterpret_cast<const u4*>(wsrc + (int64_t)b * 1024 + at_lane));
+    const uint8_t* c = csrc + (int64_t)b * 16 * kCodes + at_code;
     code[slot] = kCodes == 4   ? *reinterpret_cast<const uint32_t*>(c)
                  : kCodes == 2 ? *reinterpret_cast<const uint16_t*>(c)
                                : *c;
-    f[slot] = *reinterpret_cast<const h8*>(fsrc + (int64_t)b * 512);
+    f[slot] = *reinterpret_cast<const h8*>(reinterpret_cast<const uint8_t*>(a.hf) + (int64_t)b * f_step + at_row);
   };
   f16x acc[4] = {};
-  h8* tile = sm.tile[wave];
-  const int q = lane & 15, colhalf = (lane >> 4) & 1, khalf = lane >> 5;
-  auto place = [](int k, int o) { return 16 * k + (o ^ (((k & 3) << 2) | ((k >> 2) & 3))); };  // as tile_octet
-  auto use = [&](auto slot_) {
+  h8* put = sm.tile[wave] + kFewPitch * (lane & 15) + (lane >> 4);
+  const _Float16* get = few_operand(sm.tile[wave], lane);
+  auto use = [&](auto slot_) __attribute__((always_inline)) {
     constexpr int slot = decltype(slot_)::value;
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
       const uint32_t c = kCodes == 4   ? (code[slot] >> (8 * d)) & 0xffu
                          : kCodes == 2 ? (code[slot] >> (8 * (d >> 1))) & 0xffu
                                        : code[slot];
-      tile[place(lane & 15, 4 * d + (lane >> 4))] = unpack_q4_scaled(w[slot][d], (_Float16)(float)c);
+      put[4 * d] = unpack_q4_scaled(w[slot][d], (_Float16)(float)c);
     }
-    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      h4 x[2];
-#pragma unroll
-      for (int rr = 0; rr < 2; ++rr)
-        x[rr] = read_tr(reinterpret_cast<const _Float16*>(tile) +
-                        8 * place(8 * khalf + 4 * rr + q / 4, 4 * c + 2 * colhalf + (q & 3) / 2) + 4 * (q & 1));
-      acc[c] = mfma32(f[slot], __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7), acc[c]);
-    }
-    __builtin_amdgcn_wave_barrier();
+    for (int c = 0; c < 4; ++c) acc[c] = mfma32(f[slot], few_read(get, c), acc[c]);
+    __builtin_amdgcn_sched_barrier(0);
   };
   if (b0 + wave < b1) {
-    static_for<0, kDepth>([&](auto i) { load(b0 + wave + kFewWaves * decltype(i)::value, i); });
-    for (int g0 = b0 + wave; g0 < b1; g0 += kFewWaves * kDepth)
+    // Loads stay in the order of their use, and whole rounds have no exit
+    // inside: the waits then count loads exactly, and the others stay in flight.
+    static_for<0, kDepth>([&](auto i) {
+      load(b0 + wave + kFewWaves * decltype(i)::value, i);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    int g0 = b0 + wave;
+    for (; g0 + kFewWaves * (kDepth - 1) < b1; g0 += kFewWaves * kDepth)
       static_for<0, kDepth>([&](auto i) {
-        const int b = g0 + kFewWaves * decltype(i)::value;
-        if (b >= b1) return;
         use(i);
-        load(b + kFewWaves * kDepth, i);
+        load(g0 + kFewWaves * (decltype(i)::value + kDepth), i);
+        __builtin_amdgcn_sched_barrier(0);
       });
+    static_for<0, kDepth - 1>([&](auto i) {
+      if (g0 + kFewWaves * decltype(i)::value < b1) use(i);
+    });
   }
   few_reduce(sm, acc, a.N, wave, lane);
   if (wave != 0) return;
-  const int c32 = lane & 31;
+  const int c32 = lane & 31, khalf = lane >> 5;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const int64_t d = 128 * (int64_t)kt + 32 * c + 8 * (c32 >> 3) + k_order_h(c32 & 7);
@@ -808,7 +908,7 @@ int main_splits(int64_t N, int64_t D, int64_t ranks, int64_t stages) {
 struct BwdLayout {
   int64_t rows, n32, ksteps, width;
   int pieces, zparts, splits;
-  uint64_t pmax, rscale, hf, af, zpart, z, part, total;
+  uint64_t pmax, rscale, hf, af, gt, zpart, z, part, total;
 };
 
 BwdLayout bwd_layout(const archead_dims* d, int64_t n_tokens) {
@@ -832,8 +932,10 @@ BwdLayout bwd_layout(const archead_dims* d, int64_t n_tokens) {
   };
   L.pmax = take((uint64_t)L.rows * L.pieces * 12);
   L.rscale = take((uint64_t)L.n32 * 12);
-  L.hf = take((uint64_t)L.n32 * V64 * 2 * (L.rows <= kFewTokens ? 3 : 1));
-  L.af = take((uint64_t)((d->r_c + 31) / 32 + (d->r_r + 31) / 32) * L.ksteps * 512);
+  const bool few = L.rows <= kFewTokens;
+  L.hf = take((uint64_t)V64 * 2 * (few ? 3 * L.rows : L.n32));
+  L.af = take(few ? 0 : (uint64_t)((d->r_c + 31) / 32 + (d->r_r + 31) / 32) * L.ksteps * 512);
+  L.gt = take(few ? round_up((uint64_t)d->V, 16) * (uint64_t)(d->D / d->g) : 0);
   L.zpart = take((uint64_t)L.zparts * L.n32 * r * 4);
   L.z = take((uint64_t)L.n32 * r * 4);
   L.part = take((uint64_t)L.splits * L.rows * d->D * 4);
@@ -870,7 +972,8 @@ void launch_few(const BwdArgs& a, hipStream_t s) {
 template <typename T>
 hipError_t launch_backward(const BwdArgs& a, hipStream_t s) {
   const int64_t ranks = a.nct + a.nwt, max_groups = (a.N + kMaxRows - 1) / kMaxRows * a.pieces;
-  hipLaunchKernelGGL(bwd_max_kernel<T>, dim3((unsigned)(max_groups + (ranks * a.ksteps * 16 + kMaxThreads - 1) / kMaxThreads)),
+  const int64_t arrange = a.gt ? a.nb * a.ng / std::max(1, kKTile / a.g) : ranks * a.ksteps * 16;  // threads
+  hipLaunchKernelGGL(bwd_max_kernel<T>, dim3((unsigned)(max_groups + (arrange + kMaxThreads - 1) / kMaxThreads)),
                      dim3(kMaxThreads), 0, s, a);
   const int tt = main_tiles(a.N);
   if (a.N <= kFewTokens) {
@@ -975,6 +1078,7 @@ int archead_logits_backward(const archead_tensor* dY, const archead_packed_head*
     a.rscale = reinterpret_cast<float*>(ws + L.rscale);
     a.hf = reinterpret_cast<_Float16*>(ws + L.hf);
     a.af = ws + L.af;
+    a.gt = L.rows <= kFewTokens ? ws + L.gt : nullptr;
     a.zpart = reinterpret_cast<float*>(ws + L.zpart);
     a.z = L.rows <= kFewTokens ? nullptr : reinterpret_cast<float*>(ws + L.z);
     a.part = reinterpret_cast<float*>(ws + L.part);
