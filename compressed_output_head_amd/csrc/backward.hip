@@ -18,7 +18,7 @@
 //   bwd_main_kernel    the product with the packed residual, the vocabulary
 //                      split over several workgroups where tiles are few
 //   bwd_finish_kernel  the splits' sums and Z B to dH
-// Up to 32 tokens: bwd_few_kernel in place of the three in the middle.
+// Up to 32 tokens: bwd_few_kernel in place of zsum and main, and bwd_finish_few_kernel.
 // The packed residual is never expanded in memory: a stage of 32 vocabulary
 // rows is unpacked to fp16 in LDS, and the MFMA's operand, which runs along
 // the vocabulary, is read from there by transposing LDS reads.
@@ -67,7 +67,7 @@ struct BwdArgs {
   uint8_t* af;      // A codes, [32-rank tiles][ksteps][64][8]
   uint8_t* gt;      // few tokens: group codes, [D / 128 or D / g][16 nb][128 / g or 1]
   float* zpart;     // [zparts][n32][r_c + r_r]
-  float* z;         // [n32][r_c + r_r]; null: the parts are summed where Z is used
+  float* z;         // [n32][r_c + r_r]; few tokens: not used, bwd_finish_few_kernel sums the parts
   float* part;      // [splits][N][D]
   int pieces, zparts, splits, ksteps;
   int64_t width;    // columns of a piece of bwd_max_kernel
@@ -263,20 +263,6 @@ __global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdA
   const int64_t tile = blockIdx.x;
   const int part = blockIdx.y;
   const bool first = blockIdx.z == 0;
-  if (tid < 96) sMax[tid / 32][tid % 32] = 0u;
-  __syncthreads();
-  {
-    // the pieces' maxima of the tile's rows lie together; magnitudes order as their bits do
-    const int per_row = 3 * a.pieces, count = per_row * (int)std::min<int64_t>(32, a.N - 32 * tile);
-    const float* src = a.pmax + 32 * tile * per_row;
-    for (int i = tid; i < count; i += 64 * kPrepWaves)
-      atomicMax(&sMax[i % 3][i / per_row], __float_as_uint(src[i]));
-  }
-  __syncthreads();
-  // at most 126: the power and its inverse are normal fp32
-  auto exponent = [&](int q, int rr) { return std::min(row_exponent(__uint_as_float(sMax[q][rr])), 126); };
-  if (tid < 96 && part == 0 && first)
-    a.rscale[(32 * tile + tid % 32) * 3 + tid / 32] = ldexpf(1.0f, -exponent(tid / 32, tid % 32));
   // this thread's rows and columns of a run: octet tid % 16 of rows tid / 16 and + 16
   const int oct = tid & 15;
   float P[2][3];
@@ -287,8 +273,6 @@ __global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdA
     const int rr = (tid >> 4) + 16 * i;
     real[i] = 32 * tile + rr < a.N;
     row[i] = static_cast<const T*>(a.dY) + (real[i] ? 32 * tile + rr : 0) * a.dy_stride;
-#pragma unroll
-    for (int q = 0; q < 3; ++q) P[i][q] = ldexpf(1.0f, exponent(q, rr));
   }
   const int64_t V16 = 16 * a.nb;
   const int r = a.r_c + a.r_r, tiles = a.nct + a.nwt;
@@ -316,6 +300,25 @@ __global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdA
     }
   };
   if (run0 < run1) load(run0);
+  if (tid < 96) sMax[tid / 32][tid % 32] = 0u;
+  __syncthreads();
+  {
+    // the pieces' maxima of the tile's rows lie together; magnitudes order as their bits do
+    const int per_row = 3 * a.pieces, count = per_row * (int)std::min<int64_t>(32, a.N - 32 * tile);
+    const float* src = a.pmax + 32 * tile * per_row;
+#pragma unroll 8
+    for (int i = tid; i < count; i += 64 * kPrepWaves)
+      atomicMax(&sMax[i % 3][i / per_row], __float_as_uint(src[i]));
+  }
+  __syncthreads();
+  // at most 126: the power and its inverse are normal fp32
+  auto exponent = [&](int q, int rr) { return std::min(row_exponent(__uint_as_float(sMax[q][rr])), 126); };
+  if (tid < 96 && part == 0 && first)
+    a.rscale[(32 * tile + tid % 32) * 3 + tid / 32] = ldexpf(1.0f, -exponent(tid / 32, tid % 32));
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int q = 0; q < 3; ++q) P[i][q] = ldexpf(1.0f, exponent(q, (tid >> 4) + 16 * i));
   for (int run = run0; run < run1; ++run) {
     load_codes(run);
 #pragma unroll
@@ -786,6 +789,91 @@ __global__ __launch_bounds__(kMainThreads, 4) void bwd_few_kernel(const BwdArgs 
   }
 }
 
+// Four columns of row n of dH.
+__device__ __forceinline__ void write_dh(const BwdArgs& a, int64_t n, int64_t d, f4 y) {
+  typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(2)));
+  *reinterpret_cast<u2_any*>(a.dH + n * a.dh_stride + d) = pack_bf16x4(y[0], y[1], y[2], y[3]);
+}
+
+// Up to 32 tokens: one row x 256 columns of dH, four columns a lane; the waves
+// take a quarter each of the splits and of the ranks.  Latency is all it
+// takes: the sums of Z's parts (four lanes a rank), the splits' sums and the
+// first ranks' B are loaded before any of them is waited for.  (One row of
+// 4096, 15 parts, 64 ranks: 5.7 us; as bwd_finish_kernel does it 9.6.)
+__global__ __launch_bounds__(kFinishThreads) void bwd_finish_few_kernel(const BwdArgs a) {
+  constexpr int kWaves = kFinishThreads / 64, kParts = 8, kB = 16;
+  extern __shared__ __align__(16) float sZ[];  // [r]
+  __shared__ f4 red[kWaves][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = a.r_c + a.r_r;
+  const int64_t n = blockIdx.x, d = 256 * (int64_t)blockIdx.y + 4 * lane, dd = d < a.D ? d : 0, group = dd / a.g;
+  auto part = [&](int p) {  // past the last one: that one again
+    return *reinterpret_cast<const f4*>(a.part + ((int64_t)std::min(p, a.splits - 1) * a.N + n) * a.D + dd);
+  };
+  f4 y[kParts];
+#pragma unroll
+  for (int k = 0; k < kParts; ++k) y[k] = part(wave + kWaves * k);
+  uint32_t c[kB];
+  uint16_t s[kB];
+  auto load_b = [&](int j, int k) {
+    j = std::min(j, r - 1);
+    c[k] = *reinterpret_cast<const uint32_t*>(a.b_codes + (int64_t)j * a.D + dd);
+    s[k] = a.b_scales[(int64_t)j * a.ng + group];
+  };
+  if (r > 0) {
+#pragma unroll
+    for (int k = 0; k < kB; ++k) load_b(wave + kWaves * k, k);
+  }
+  for (int e = tid; e < 4 * r; e += kFinishThreads) {  // r is a multiple of 8: whole groups of four lanes
+    const int j = e >> 2;
+    const float* src = a.zpart + n * r + j;
+    float z = 0.0f;
+    for (int p = e & 3; p < a.zparts; p += 4 * kParts) {
+      float x[kParts];
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) x[k] = src[(int64_t)std::min(p + 4 * k, a.zparts - 1) * a.n32 * r];
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) z += p + 4 * k < a.zparts ? x[k] : 0.0f;
+    }
+    z += __shfl_xor(z, 1);
+    z += __shfl_xor(z, 2);
+    if ((e & 3) == 0) sZ[j] = z * a.rscale[n * 3 + (j < a.r_c ? 1 : 2)];
+  }
+  const float scale = a.rscale[n * 3];
+  f4 acc = {};
+  for (int p = wave; p < a.splits; p += kParts * kWaves) {
+    if (p != wave) {
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) y[k] = part(p + kWaves * k);
+    }
+#pragma unroll
+    for (int k = 0; k < kParts; ++k)
+      if (p + kWaves * k < a.splits) acc += y[k];
+  }
+  acc *= scale;
+  __syncthreads();
+  for (int j0 = wave; j0 < r; j0 += kB * kWaves) {
+    if (j0 != wave) {
+#pragma unroll
+      for (int k = 0; k < kB; ++k) load_b(j0 + kWaves * k, k);
+    }
+#pragma unroll
+    for (int k = 0; k < kB; ++k) {
+      const int j = j0 + kWaves * k;
+      const float z = j < r ? sZ[j] * f16_to_f32(s[k]) : 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = fmaf(z, (float)(int8_t)(c[k] >> (8 * e)), acc[e]);
+    }
+  }
+  red[wave][lane] = acc;
+  __syncthreads();
+  if (wave == 0 && d < a.D) {
+    for (int w = 1; w < kWaves; ++w) acc += red[w][lane];
+    write_dh(a, n, d, acc);
+  }
+}
+
 // kFinishRows rows x 256 columns of dH, four columns a lane: the splits' sums
 // and Z B, in fp32.  Few rows: the four waves of a workgroup take a quarter
 // each of the splits and of the ranks, and their sums are added in order.
@@ -804,14 +892,7 @@ __global__ __launch_bounds__(kFinishThreads) void bwd_finish_kernel(const BwdArg
   float* Z = sZ + (kShared ? 0 : wave * r * kRows);
   for (int e = kShared ? tid : lane; e < kRows * r; e += kShared ? kFinishThreads : 64) {
     const int i = e / r, j = e % r;
-    float z = 0.0f;
-    if (i < rows && a.z) z = a.z[(n0 + i) * r + j];
-    if (i < rows && !a.z) {  // few tokens: bwd_zsum_kernel is not worth its launch
-#pragma unroll 8
-      for (int p = 0; p < a.zparts; ++p) z += a.zpart[((int64_t)p * a.n32 + n0 + i) * r + j];
-      z *= a.rscale[(n0 + i) * 3 + (j < a.r_c ? 1 : 2)];
-    }
-    Z[j * kRows + i] = z;
+    Z[j * kRows + i] = i < rows ? a.z[(n0 + i) * r + j] : 0.0f;
   }
   __syncthreads();
   const int first = kShared ? wave : 0, step = kShared ? kWaves : 1;
@@ -852,10 +933,6 @@ __global__ __launch_bounds__(kFinishThreads) void bwd_finish_kernel(const BwdArg
       }
     }
   }
-  auto write = [&](int i, f4 y) {
-    typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(2)));
-    if (in) *reinterpret_cast<u2_any*>(a.dH + (n0 + i) * a.dh_stride + d) = pack_bf16x4(y[0], y[1], y[2], y[3]);
-  };
   if constexpr (kShared) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) red[wave][i][lane] = acc[i];
@@ -868,12 +945,12 @@ __global__ __launch_bounds__(kFinishThreads) void bwd_finish_kernel(const BwdArg
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] += x[e];
       }
-      write(i, y);
+      if (in) write_dh(a, n0 + i, d, y);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-      if (i < rows) write(i, acc[i]);
+      if (in && i < rows) write_dh(a, n0 + i, d, acc[i]);
   }
 }
 
@@ -996,7 +1073,9 @@ hipError_t launch_backward(const BwdArgs& a, hipStream_t s) {
   const size_t lds = (size_t)kFinishRows * (a.r_c + a.r_r) * 4;
   const unsigned columns = (unsigned)((a.D + 255) / 256);
   // rows of their own for 2048 waves (and their Z in 64 KB of LDS), or a block of rows for every four
-  if (row_blocks * columns < 2048 || lds * waves > 63 * 1024)
+  if (a.N <= kFewTokens)
+    hipLaunchKernelGGL(bwd_finish_few_kernel, dim3((unsigned)a.N, columns), dim3(kFinishThreads), lds / kFinishRows, s, a);
+  else if (row_blocks * columns < 2048 || lds * waves > 63 * 1024)
     hipLaunchKernelGGL(bwd_finish_kernel<true>, dim3((unsigned)row_blocks, columns), dim3(kFinishThreads), lds, s, a);
   else
     hipLaunchKernelGGL(bwd_finish_kernel<false>, dim3((unsigned)((row_blocks + waves - 1) / waves), columns),
