@@ -132,9 +132,8 @@ __device__ __forceinline__ float scale_A(const Scales8& s, int nA, int part, int
 }
 
 // The layout of the A codes: rank tile t, vocabulary step, lane (rank lane % 32,
-// rows 16 step + 8 (lane / 32) .. + 8) hold 8 bytes in the order that
-// unpack_i8x8 turns into the rows'.  Thread i takes four ranks: eight words of
-// the stored rows, transposed byte by byte.
+// rows 16 step + 8 (lane / 32) .. + 8) hold the rows' 8 codes + 128.  Thread i
+// takes four ranks: eight words of the stored rows, transposed byte by byte.
 __device__ __forceinline__ void arrange_codes(const BwdArgs& a, int64_t i) {
   const int quad = (int)(i & 7), half = (int)(i >> 3) & 1;
   const int64_t step = (i >> 4) % a.ksteps, t = (i >> 4) / a.ksteps;
@@ -150,14 +149,14 @@ __device__ __forceinline__ void arrange_codes(const BwdArgs& a, int64_t i) {
     w[k] = valid && v < 16 * a.nb ? *reinterpret_cast<const uint32_t*>(codes + (int64_t)k * r) : 0u;
   u2* out = reinterpret_cast<u2*>(a.af) + ((t * a.ksteps + step) * 64 + 32 * half + 4 * quad);
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {  // byte b of rows 0 2 1 3, and of rows 4 6 5 7
+  for (int b = 0; b < 4; ++b) {  // byte b of the eight rows
     u2 x;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t sel = 0x0c0c0000u | (uint32_t)(4 + b) << 8 | (uint32_t)b;
-      const uint32_t lo = __builtin_amdgcn_perm(w[4 * h + 2], w[4 * h], sel);
-      const uint32_t hi = __builtin_amdgcn_perm(w[4 * h + 3], w[4 * h + 1], sel);
-      x[h] = lo | hi << 16;
+      const uint32_t lo = __builtin_amdgcn_perm(w[4 * h + 1], w[4 * h], sel);
+      const uint32_t hi = __builtin_amdgcn_perm(w[4 * h + 3], w[4 * h + 2], sel);
+      x[h] = (lo | hi << 16) ^ 0x80808080u;
     }
     out[b] = x;
   }
@@ -183,6 +182,18 @@ __device__ __forceinline__ void arrange_groups(const BwdArgs& a, int64_t i) {
     __builtin_memcpy(&x, c + k * 16 / sizeof(C), 16);
     out[k] = x;
   }
+}
+
+// Eight of them as fp16: byte u under the byte 0x64 is 1024 + u, exactly.
+__device__ __forceinline__ h8 unpack_u8x8(u2 c) {
+  const h2 bias = {(_Float16)1152.0f, (_Float16)1152.0f};
+  u4 x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t pair = __builtin_amdgcn_perm(c[i >> 1], 0x64646464u, i & 1 ? 0x00070006u : 0x00050004u);
+    x[i] = h2_bits(bits_h2(pair) - bias);
+  }
+  return __builtin_bit_cast(h8, x);
 }
 
 // Workgroup q pieces + p: the largest products of piece p of rows kMaxRows q
@@ -353,7 +364,7 @@ __global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdA
     if (t < tiles) {
 #pragma unroll
       for (int k = 0; k < 8; ++k)  // past the last step dY is zero
-        acc = mfma32(frag[in_c ? 1 : 2][k][lane], unpack_i8x8(b[k][0], b[k][1]), acc);
+        acc = mfma32(frag[in_c ? 1 : 2][k][lane], unpack_u8x8(b[k]), acc);
     }
     __syncthreads();
   }
