@@ -12,15 +12,16 @@
 // gradient that sits on vocabulary entries of tiny scales keeps its digits.
 //
 //   bwd_max_kernel     per row: the largest |dY s_R|, |dY s_Ac|, |dY s_Aw|;
-//                      beside that, the A codes in operand order
+//                      beside that, the A codes in operand order (few
+//                      tokens: the group codes by k-tile)
 //   bwd_prep_kernel    dY s_R as fp16 operand fragments; parts of Z
 //   bwd_zsum_kernel    Z in fp32
 //   bwd_main_kernel    the product with the packed residual, the vocabulary
 //                      split over several workgroups where tiles are few
 //   bwd_finish_kernel  the splits' sums and Z B to dH
 // Up to 32 tokens: bwd_few_kernel in place of zsum and main, and bwd_finish_few_kernel.
-// The packed residual is never expanded in memory: a stage of 32 vocabulary
-// rows is unpacked to fp16 in LDS, and the MFMA's operand, which runs along
+// The packed residual is never expanded in memory: a stage of 64 vocabulary
+// rows (few tokens: 16) is unpacked to fp16 in LDS, and the MFMA's operand, which runs along
 // the vocabulary, is read from there by transposing LDS reads.
 #include <algorithm>
 #include <type_traits>
@@ -61,7 +62,7 @@ struct BwdArgs {
   const int8_t* b_codes;
   const uint16_t* b_scales;
   // workspace
-  float* pmax;      // [N][pieces][3]
+  float* pmax;      // [N][3][pieces]
   float* rscale;    // [n32][3] powers of two that undo the rows' scales
   _Float16* hf;     // [n32/32][ksteps][64][8]; few tokens: [s_R, s_Ac, s_Aw][ksteps][2][N][8]
   uint8_t* af;      // A codes, [32-rank tiles][ksteps][64][8]
@@ -165,7 +166,8 @@ __device__ __forceinline__ void arrange_codes(const BwdArgs& a, int64_t i) {
 // The group codes of 16 vocabulary rows by k-tile, for bwd_few_kernel: thread i
 // takes those of one k-tile (or of the two that share a code of 256 columns).
 // As they are stored, a k-tile's wave finds the 16 bytes that it needs in 16
-// sectors, which took 11 us of 89 on one token of a 151936 x 4096 head.
+// sectors, which took 11 us on one token of a 151936 x 4096 head; this, beside
+// the maxima, takes 2.
 template <typename C>
 __device__ __forceinline__ void arrange_groups(const BwdArgs& a, int64_t i) {
   const int columns = a.ng / (int)sizeof(C);
@@ -251,7 +253,7 @@ __global__ __launch_bounds__(kMaxThreads) void bwd_max_kernel(const BwdArgs a) {
   if (i < kMaxRows && n0 + i < a.N) {
     float t = buf[0][i][q];
     for (int w = 1; w < kWaves; ++w) t = fmaxf(t, buf[w][i][q]);
-    a.pmax[((n0 + i) * a.pieces + p) * 3 + q] = t;
+    a.pmax[((n0 + i) * 3 + q) * a.pieces + p] = t;
   }
 }
 
@@ -267,7 +269,7 @@ __global__ __launch_bounds__(kMaxThreads) void bwd_max_kernel(const BwdArgs a) {
 // on 4096 rows of 151936, with them 0.63, with five and their spills 1.46.)
 template <typename T, bool kZ>
 __global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdArgs a) {
-  __shared__ uint32_t sMax[3][32];
+  __shared__ float sMax[3][32];
   __shared__ h8 frag[3][8][66];  // steps two octets apart, so that a wave's writes meet no bank twice
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -311,19 +313,22 @@ __global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdA
     }
   };
   if (run0 < run1) load(run0);
-  if (tid < 96) sMax[tid / 32][tid % 32] = 0u;
-  __syncthreads();
-  {
-    // the pieces' maxima of the tile's rows lie together; magnitudes order as their bits do
-    const int per_row = 3 * a.pieces, count = per_row * (int)std::min<int64_t>(32, a.N - 32 * tile);
-    const float* src = a.pmax + 32 * tile * per_row;
-#pragma unroll 8
-    for (int i = tid; i < count; i += 64 * kPrepWaves)
-      atomicMax(&sMax[i % 3][i / per_row], __float_as_uint(src[i]));
+  // the tile's maxima from the pieces', eight lanes each
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const int i = tid / 8 + 32 * k, rr = i / 3;
+    float m = 0.0f;
+    if (32 * tile + rr < a.N) {
+      const float* src = a.pmax + (96 * tile + i) * a.pieces;
+#pragma unroll 4
+      for (int p = tid & 7; p < a.pieces; p += 8) m = fmaxf(m, src[p]);
+    }
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if ((tid & 7) == 0) sMax[i % 3][rr] = m;
   }
   __syncthreads();
   // at most 126: the power and its inverse are normal fp32
-  auto exponent = [&](int q, int rr) { return std::min(row_exponent(__uint_as_float(sMax[q][rr])), 126); };
+  auto exponent = [&](int q, int rr) { return std::min(row_exponent(sMax[q][rr]), 126); };
   if (tid < 96 && part == 0 && first)
     a.rscale[(32 * tile + tid % 32) * 3 + tid / 32] = ldexpf(1.0f, -exponent(tid / 32, tid % 32));
 #pragma unroll
@@ -429,7 +434,15 @@ __device__ __forceinline__ h4 read_tr(const _Float16* p) {
 }
 
 // 32 TT tokens x 256 columns of dH per workgroup over a share of the
-// vocabulary, in stages of 64 vocabulary rows (4 MFMA steps).
+// vocabulary, in stages of 64 vocabulary rows (4 MFMA steps).  The operands
+// come from LDS, 6 KB a wave and step for eight MFMAs, and the fragments of dY
+// and the unpacked tile are written there, 16 KB a step: 64% of the cycles
+// that the MFMAs take, so the two run side by side.
+// 4096 rows of 151936 x 4096: 4.1 ms, 1.25 PFLOP/s, MFMAs busy in 70% of the
+// cycles of a clock that the power limit holds at 1.64 GHz; a dense bf16
+// product of these sizes by the library, 3.6 to 4.1 ms.  (Four waves of 128 x
+// 128 read a third less from LDS, but one wave a SIMD waits for itself: 2%
+// slower.  Three workgroups' worth of registers do not exist at TT = 8.)
 template <int TT>
 struct MainShape {
   static constexpr int WM = TT >= 4 ? 2 : 1, WN = 8 / WM;  // eight waves in WM rows
@@ -541,8 +554,8 @@ __global__ __launch_bounds__(kMainThreads, TT >= 8 ? 2 : 4) void bwd_main_kernel
     fetch(I0{}, I0{});
     // A step's MFMAs, with what is around them dealt out between them: an LDS
     // read, a little arithmetic and an LDS write behind each.  (4096 rows of
-    // 151936 x 4096: 5.05 ms a call against 5.18 in the compiler's own order;
-    // two to five instructions 5.04 to 5.11, the LDS read first 5.31.)
+    // 151936 x 4096: 2.5% of a call less than in the compiler's own order; with
+    // two or five instructions 1.5%, with the LDS read first 2.5% more.)
     auto interleave = [] {
       static_for<0, S::MT * S::NT>([](auto) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
@@ -718,10 +731,12 @@ __device__ __forceinline__ void few_ranks(const BwdArgs& a, FewShared& sm, int t
 // dY fragment, turns them in 4 KB of LDS that no other wave reads, and keeps
 // the sums of all the tokens and columns; the waves' sums are added at the
 // end.  A rank tile's codes come in operand order already.
-// On one token of a 151936 x 4096 head the k-tiles take 88 us, 77 of them with
-// the packed tiles' loads alone (without the group codes and the fragments);
-// neither the unpacking nor the LDS traffic shows, and deeper rings with fewer
-// waves take longer.
+// One token of a 151936 x 4096 head: 77 us, 4.2 TB/s of the packed bytes; the
+// tiles' loads alone take 70.  With r_c = r_r = 0, where the k-tiles have all
+// 512 places to themselves, 72.  The group codes as stored cost 11 us more, all
+// 32 rows of a fragment where one is real 5, a ring whose waits the compiler
+// could not count 10 to 20.  Neither the order of the blocks over the
+// workgroups nor the XCDs, nor more k-tiles a workgroup show.
 template <int kCodes>
 __global__ __launch_bounds__(kMainThreads, 4) void bwd_few_kernel(const BwdArgs a) {
   constexpr int kDepth = kCodes == 4 ? 3 : 4;  // without spills
@@ -970,16 +985,16 @@ __global__ __launch_bounds__(kFinishThreads) void bwd_finish_kernel(const BwdArg
 int main_tiles(int64_t N) { return N <= 64 ? 2 : N <= 128 ? 4 : 8; }
 
 // Parts of the vocabulary for the main kernel: the count that a model of its
-// time likes best, workgroups in rounds of the resident ones (one a CU for
-// 256-token tiles, two for smaller ones) of kRoundUs plus a stage's measured
+// time likes best, workgroups in rounds of the resident ones (two a CU for
+// 64-token tiles, else one) of kRoundUs plus a stage's measured
 // time for every stage, and the partial sums written and read at 4 TB/s.
 int main_splits(int64_t N, int64_t D, int64_t ranks, int64_t stages) {
   constexpr double kRoundUs = 4.0;
   if (N <= kFewTokens)  // two workgroups a CU; a packed tile for each wave at least
     return (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, 512 / (D / kKTile + ranks), (stages + 1) / 2}));
   const int tt = main_tiles(N);
-  const int64_t tiles = (N + 32 * tt - 1) / (32 * tt) * ((D + 255) / 256), slots = tt == 8 ? 256 : 512;
-  const double stage_us = tt == 8 ? 1.9 : tt == 4 ? 1.7 : 1.4;
+  const int64_t tiles = (N + 32 * tt - 1) / (32 * tt) * ((D + 255) / 256), slots = tt == 2 ? 512 : 256;
+  const double stage_us = tt == 8 ? 1.75 : tt == 4 ? 1.15 : 1.4;
   double best = 1e30;
   int pick = 1;
   for (int64_t p = 1; p <= std::min<int64_t>(kMaxSplits, stages); ++p) {
