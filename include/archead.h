@@ -12,7 +12,9 @@
  * step), with W_d = Q(A_c) Q(B_c) + SC4(R).  This library computes exactly that
  * forward from the packed bytes; it never forms the V x D matrix.  Around the
  * forward: per-row statistics and top-k of the logits, the logit error of
- * Eq. 1, and the construction itself (packing, and the full fit of Algorithm 1).
+ * Eq. 1, the construction itself (packing, and the full fit of Algorithm 1),
+ * and training through a frozen head (losses on the logits with their gradient,
+ * and the hidden states' gradient).
  *
  * Conventions for every entry point:
  *   - All functions return an archead_status (0 = ARCHEAD_OK).  They never
@@ -598,8 +600,11 @@ ARCHEAD_API int archead_preference_loss(const archead_tensor* Y, const archead_p
 /* Device workspace archead_logits_backward needs for n_tokens rows: for
  * min(n_tokens, 4096) rows, dY as fp16 operands (2 bytes an element, rows
  * rounded up to 32 and the vocabulary to 64), fp32 partial sums of dH and of
- * its low-rank part, the A codes in operand order, and row scales.  Pure
- * host arithmetic.  E_NULL, E_DIMS, E_SHAPE, E_UNSUPPORTED. */
+ * its low-rank part, the A codes in operand order, and row scales; up to 32
+ * rows instead three sets of operands, without rounding the rows up, and the
+ * group codes.  A call of more rows may leave fewer than 4096 to its last
+ * pass, which this covers.  Pure host arithmetic.  E_NULL, E_DIMS, E_SHAPE,
+ * E_UNSUPPORTED. */
 ARCHEAD_API int archead_logits_backward_workspace_bytes(const archead_dims* d, int64_t n_tokens, uint64_t* bytes);
 
 /* dH = dY W_hat, the gradient of the hidden states through the packed head

@@ -109,6 +109,18 @@ def test_backward_matches_oracle(V, D, r_c, r_r, g, N, dtype):
     _check(head, h, dY, f"V={V} N={N}")
 
 
+@pytest.mark.parametrize("N", [1, 5, 31])
+@pytest.mark.parametrize("V,D,r_c,r_r,g", [(1031, 512, 40, 72, 256), (2500, 768, 0, 40, 256), (999, 640, 72, 0, 128),
+                                           (640, 384, 24, 8, 64), (1234, 256, 32, 136, 32)])
+def test_few_tokens_of_every_group_size(V, D, r_c, r_r, g, N):
+    """The few-token kernels: shared and several group codes a tile, rank tiles
+    that end early, rows of fewer tokens than an operand holds."""
+    torch = torch_mod()
+    h, head = _head(V + g, V, D, r_c, r_r, g)
+    dY = torch.as_tensor(_gradient(np.random.default_rng(N + V), N, V), device="cuda").bfloat16()
+    _check(head, h, dY, f"V={V} D={D} r={r_c}+{r_r} g={g} N={N}")
+
+
 def _dequant(h):
     return (h.q4.astype(np.float64) * np.repeat(h.c8.astype(np.float64), h.g, axis=1)
             * h.s_R.astype(np.float64)[:, None])
