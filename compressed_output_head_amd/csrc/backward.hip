@@ -19,7 +19,8 @@
 //   bwd_main_kernel    the product with the packed residual, the vocabulary
 //                      split over several workgroups where tiles are few
 //   bwd_finish_kernel  the splits' sums and Z B to dH
-// Up to 32 tokens: bwd_few_kernel in place of zsum and main, and bwd_finish_few_kernel.
+// Up to 32 tokens: bwd_few_kernel or (up to 16) bwd_few16_kernel in place of
+// zsum and main, and bwd_finish_few_kernel.
 // The packed residual is never expanded in memory: a stage of 64 vocabulary
 // rows (few tokens: 16) is unpacked to fp16 in LDS, and the MFMA's operand, which runs along
 // the vocabulary, is read from there by transposing LDS reads.
@@ -725,18 +726,16 @@ __device__ __forceinline__ void few_ranks(const BwdArgs& a, FewShared& sm, int t
   }
 }
 
-// Up to 32 tokens: one 128-column k-tile per workgroup over a share of the
+// 17 to 32 tokens: one 128-column k-tile per workgroup over a share of the
 // vocabulary, or one 32-rank tile of Z.  Each of the eight waves streams
 // packed tiles of its own (16 vocabulary rows, one MFMA step) and the step's
 // dY fragment, turns them in 4 KB of LDS that no other wave reads, and keeps
 // the sums of all the tokens and columns; the waves' sums are added at the
 // end.  A rank tile's codes come in operand order already.
-// One token of a 151936 x 4096 head: 77 us, 4.2 TB/s of the packed bytes; the
-// tiles' loads alone take 70.  With r_c = r_r = 0, where the k-tiles have all
-// 512 places to themselves, 72.  The group codes as stored cost 11 us more, all
-// 32 rows of a fragment where one is real 5, a ring whose waits the compiler
-// could not count 10 to 20.  Neither the order of the blocks over the
-// workgroups nor the XCDs, nor more k-tiles a workgroup show.
+// 32 tokens of a 151936 x 4096 head: 84 us; the accumulators leave registers
+// for four tiles in flight a wave, and none for operands that wait while the
+// next tile is unpacked.  The group codes as stored cost 11 us more, a ring
+// whose waits the compiler could not count 10 to 20.
 template <int kCodes>
 __global__ __launch_bounds__(kMainThreads, 4) void bwd_few_kernel(const BwdArgs a) {
   constexpr int kDepth = kCodes == 4 ? 3 : 4;  // without spills
@@ -810,6 +809,140 @@ __global__ __launch_bounds__(kMainThreads, 4) void bwd_few_kernel(const BwdArgs 
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
       const int64_t n = 8 * (v >> 2) + 4 * khalf + (v & 3);
+      if (n < a.N) a.part[((int64_t)split * a.N + n) * a.D + d] = acc[c][v];
+    }
+  }
+}
+
+constexpr int kFew16Pitch = 9;  // octets a row of half a tile
+
+// Up to 16 tokens: as bwd_few_kernel, on the 16 x 16 x 32 MFMA.  A step is two
+// packed tiles, 32 vocabulary rows, turned in LDS one half of the columns at a
+// time; the sums take half the registers, which go to a ring of six tiles a
+// wave and to operands that are read ahead: while they come, the next half is
+// unpacked over theirs (a wave's LDS accesses keep their order).  The
+// workgroups of a k-tile take steps in turn, so that they read one part of
+// memory together (1% over parts of their own).
+// One token of a 151936 x 4096 head: 67 us, 4.9 TB/s of the packed bytes;
+// bwd_few_kernel takes 77.  The packed tiles' loads alone take 51, all loads
+// 58; 480 of 512 places hold k-tiles, as the ranks' tiles need some.  A ring
+// of eight tiles takes the same.
+template <int kCodes>
+__global__ __launch_bounds__(kMainThreads, 4) void bwd_few16_kernel(const BwdArgs a) {
+  constexpr int kDepth = 3;
+  __shared__ __align__(16) FewShared sm;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tiles = a.nkt + a.nct + a.nwt, kt = blockIdx.x % tiles, split = blockIdx.x / tiles, nb = (int)a.nb;
+  if (kt >= a.nkt)
+    return few_ranks(a, sm, kt - a.nkt, split, (int)((int64_t)split * nb / a.splits),
+                     (int)((int64_t)(split + 1) * nb / a.splits), wave, lane);
+  const int first = split * kFewWaves + wave, stride = kFewWaves * a.splits, end = (nb + 1) / 2;
+  const uint8_t* wsrc = a.r_codes + (int64_t)kt * a.nb * 1024;
+  const uint8_t* csrc = a.gt + (int64_t)(kCodes > 1 ? kt : kKTile * kt / a.g) * a.nb * 16 * kCodes;
+  const uint32_t at_lane = (uint32_t)lane * 16, at_code = (uint32_t)(lane & 15) * kCodes;
+  const uint32_t at_row = 16 * (uint32_t)((lane >> 4) * a.N + std::min<int64_t>(lane & 15, a.N - 1));
+  const uint32_t f_step = 64 * (uint32_t)a.N;
+  u4 w[kDepth][2];
+  uint32_t code[kDepth][2];
+  h8 f[kDepth];
+  auto load = [&](int step, auto slot_) __attribute__((always_inline)) {
+    constexpr int slot = decltype(slot_)::value;
+    step = std::min(step, end - 1);  // past the end: tiles that are cached, never used
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int b = std::min(2 * step + j, nb - 1);  // past the last tile dY is zero
+      w[slot][j] = __builtin_nontemporal_load(reinterpret_cast<const u4*>(wsrc + (int64_t)b * 1024 + at_lane));
+      const uint8_t* c = csrc + (int64_t)b * 16 * kCodes + at_code;
+      code[slot][j] = kCodes == 4   ? *reinterpret_cast<const uint32_t*>(c)
+                      : kCodes == 2 ? *reinterpret_cast<const uint16_t*>(c)
+                                    : *c;
+    }
+    f[slot] = *reinterpret_cast<const h8*>(reinterpret_cast<const uint8_t*>(a.hf) + (int64_t)step * f_step + at_row);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  h8* put = sm.tile[wave] + kFew16Pitch * (lane & 15) + (lane >> 4);
+  auto unpack = [&](auto slot_, int half) __attribute__((always_inline)) {
+    constexpr int slot = decltype(slot_)::value;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int d = 2 * half + e;
+        const uint32_t c = kCodes == 4   ? (code[slot][j] >> (8 * d)) & 0xffu
+                           : kCodes == 2 ? (code[slot][j] >> (8 * half)) & 0xffu
+                                         : code[slot][j];
+        put[16 * kFew16Pitch * j + 4 * e] = unpack_q4_scaled(w[slot][j][d], (_Float16)(float)c);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const int q = lane & 15;
+  const _Float16* get = reinterpret_cast<const _Float16*>(sm.tile[wave]) +
+                        8 * kFew16Pitch * (8 * (lane >> 4) + q / 4) + 4 * (q & 3);
+  h8 x[4];
+  auto fetch = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      x[c] = __builtin_shufflevector(read_tr(get + 16 * c), read_tr(get + 16 * c + 32 * kFew16Pitch), 0, 1, 2, 3, 4, 5,
+                                     6, 7);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  f4 acc[8] = {};
+  auto multiply = [&](auto slot_, int half) __attribute__((always_inline)) {
+    constexpr int slot = decltype(slot_)::value;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      acc[4 * half + c] = mfma16(f[slot], x[c], acc[4 * half + c]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (first < end) {
+    // as in bwd_few_kernel: loads in the order of their use, rounds without an exit
+    static_for<0, kDepth>([&](auto i) { load(first + stride * decltype(i)::value, i); });
+    unpack(std::integral_constant<int, 0>{}, 0);
+    fetch();
+    auto step = [&](auto i) __attribute__((always_inline)) {
+      unpack(i, 1);
+      multiply(i, 0);
+      fetch();
+      unpack(std::integral_constant<int, (decltype(i)::value + 1) % kDepth>{}, 0);
+      multiply(i, 1);
+      fetch();
+    };
+    int g0 = first;
+    for (; g0 + stride * (kDepth - 1) < end; g0 += stride * kDepth)
+      static_for<0, kDepth>([&](auto i) __attribute__((always_inline)) {
+        step(i);
+        load(g0 + stride * (decltype(i)::value + kDepth), i);
+      });
+    static_for<0, kDepth - 1>([&](auto i) __attribute__((always_inline)) {
+      if (g0 + stride * decltype(i)::value < end) step(i);
+    });
+  }
+  // the waves' sums, halving the waves
+#pragma unroll
+  for (int half = kFewWaves / 2; half > 0; half >>= 1) {
+    __syncthreads();
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) sm.sum[wave - half][c >> 2][4 * (c & 3) + v][lane] = acc[c][v];
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[c][v] += sm.sum[wave][c >> 2][4 * (c & 3) + v][lane];
+    }
+  }
+  if (wave != 0) return;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const int64_t d = 128 * (int64_t)kt + 16 * c + (q & 8) + k_order_h(q & 7);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int64_t n = 4 * (lane >> 4) + v;
       if (n < a.N) a.part[((int64_t)split * a.N + n) * a.D + d] = acc[c][v];
     }
   }
@@ -1062,14 +1195,22 @@ void launch_main_tt(const BwdArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((bwd_main_kernel<TT, 1>), grid, block, 0, s, a);
 }
 
-void launch_few(const BwdArgs& a, hipStream_t s) {
+template <int kCodes>
+void launch_few_codes(const BwdArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((a.nkt + a.nct + a.nwt) * a.splits)), block(kMainThreads);
-  if (a.g == 32)
-    hipLaunchKernelGGL(bwd_few_kernel<4>, grid, block, 0, s, a);
-  else if (a.g == 64)
-    hipLaunchKernelGGL(bwd_few_kernel<2>, grid, block, 0, s, a);
+  if (a.N <= 16)  // tokens of its operands
+    hipLaunchKernelGGL(bwd_few16_kernel<kCodes>, grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL(bwd_few_kernel<1>, grid, block, 0, s, a);
+    hipLaunchKernelGGL(bwd_few_kernel<kCodes>, grid, block, 0, s, a);
+}
+
+void launch_few(const BwdArgs& a, hipStream_t s) {
+  if (a.g == 32)
+    launch_few_codes<4>(a, s);
+  else if (a.g == 64)
+    launch_few_codes<2>(a, s);
+  else
+    launch_few_codes<1>(a, s);
 }
 
 template <typename T>
