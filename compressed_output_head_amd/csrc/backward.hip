@@ -18,7 +18,8 @@
 //   bwd_zsum_kernel    Z in fp32
 //   bwd_main_kernel    the product with the packed residual, the vocabulary
 //                      split over several workgroups where tiles are few
-//   bwd_finish_kernel  the splits' sums and Z B to dH
+//   bwd_finish_kernel  the splits' sums and Z B to dH (many rows:
+//                      bwd_finish_many_kernel)
 // Up to 32 tokens: bwd_few_kernel or (up to 16) bwd_few16_kernel in place of
 // zsum and main, and bwd_finish_few_kernel.
 // The packed residual is never expanded in memory: a stage of 64 vocabulary
@@ -1034,49 +1035,38 @@ __global__ __launch_bounds__(kFinishThreads) void bwd_finish_few_kernel(const Bw
 }
 
 // kFinishRows rows x 256 columns of dH, four columns a lane: the splits' sums
-// and Z B, in fp32.  Few rows: the four waves of a workgroup take a quarter
-// each of the splits and of the ranks, and their sums are added in order.
-// Many rows: every wave has rows of its own.
-template <bool kShared>
+// and Z B, in fp32.  The four waves of a workgroup take a quarter each of the
+// splits and of the ranks, and their sums are added in order.
 __global__ __launch_bounds__(kFinishThreads) void bwd_finish_kernel(const BwdArgs a) {
   constexpr int kWaves = kFinishThreads / 64, kRows = kFinishRows;
-  extern __shared__ __align__(16) float sZ[];  // [r][kRows] (of every wave)
-  __shared__ f4 red[kShared ? kWaves : 1][kShared ? kRows : 1][64];
+  extern __shared__ __align__(16) float Z[];  // [r][kRows]
+  __shared__ f4 red[kWaves][kRows][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = a.r_c + a.r_r;
-  const int64_t n0 = ((int64_t)blockIdx.x * (kShared ? 1 : kWaves) + (kShared ? 0 : wave)) * kRows;
+  const int64_t n0 = (int64_t)blockIdx.x * kRows;
   const int64_t d = 256 * (int64_t)blockIdx.y + 4 * lane;
-  const int rows = (int)std::max<int64_t>(0, std::min<int64_t>(kRows, a.N - n0));
-  float* Z = sZ + (kShared ? 0 : wave * r * kRows);
-  for (int e = kShared ? tid : lane; e < kRows * r; e += kShared ? kFinishThreads : 64) {
+  const int rows = (int)std::min<int64_t>(kRows, a.N - n0);
+  for (int e = tid; e < kRows * r; e += kFinishThreads) {
     const int i = e / r, j = e % r;
     Z[j * kRows + i] = i < rows ? a.z[(n0 + i) * r + j] : 0.0f;
   }
   __syncthreads();
-  const int first = kShared ? wave : 0, step = kShared ? kWaves : 1;
-  const bool in = d < a.D && rows > 0;
   f4 acc[kRows] = {};
-  if (in) {
-    for (int p = first; p < a.splits; p += step) {
+  if (d < a.D) {
+    for (int p = wave; p < a.splits; p += kWaves) {
       f4 y[kRows];
 #pragma unroll
       for (int i = 0; i < kRows; ++i)  // past the last row: that one again
         y[i] = *reinterpret_cast<const f4*>(a.part + ((int64_t)p * a.N + n0 + std::min(i, rows - 1)) * a.D + d);
 #pragma unroll
-      for (int i = 0; i < kRows; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] += y[i][e];
+      for (int i = 0; i < kRows; ++i) acc[i] += y[i];
     }
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const float s = a.rscale[(n0 + std::min(i, rows - 1)) * 3];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] *= s;
-    }
+    for (int i = 0; i < kRows; ++i) acc[i] *= a.rscale[(n0 + std::min(i, rows - 1)) * 3];
     const int64_t group = d / a.g;
-#pragma unroll kShared ? 8 : 4
-    for (int j = first; j < r; j += step) {
+#pragma unroll 8
+    for (int j = wave; j < r; j += kWaves) {
       const uint32_t c = *reinterpret_cast<const uint32_t*>(a.b_codes + (int64_t)j * a.D + d);
       const float s = f16_to_f32(a.b_scales[(int64_t)j * a.ng + group]);
       float b[4];
@@ -1092,24 +1082,94 @@ __global__ __launch_bounds__(kFinishThreads) void bwd_finish_kernel(const BwdArg
       }
     }
   }
-  if constexpr (kShared) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) red[wave][i][lane] = acc[i];
-    __syncthreads();
-    for (int i = wave; i < rows; i += kWaves) {
-      f4 y = red[0][i][lane];
+  for (int i = 0; i < kRows; ++i) red[wave][i][lane] = acc[i];
+  __syncthreads();
+  for (int i = wave; i < rows; i += kWaves) {
+    f4 y = red[0][i][lane];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) {
-        const f4 x = red[w][i][lane];
+    for (int w = 1; w < kWaves; ++w) y += red[w][i][lane];
+    if (d < a.D) write_dh(a, n0 + i, d, y);
+  }
+}
+
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+// v as the sum of two bf16 numbers, to 2^-18 of it.
+struct Bf16Pair {
+  bf8 hi, lo;
+};
+__device__ __forceinline__ Bf16Pair split_bf16(const float (&v)[8]) {
+  Bf16Pair p;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] += x[e];
-      }
-      if (in) write_dh(a, n0 + i, d, y);
+  for (int i = 0; i < 8; ++i) {
+    p.hi[i] = (__bf16)v[i];
+    p.lo[i] = (__bf16)(v[i] - (float)p.hi[i]);
+  }
+  return p;
+}
+
+// Many rows: 32 rows x 128 columns of dH a wave, Z B on the bf16 MFMA with Z
+// and B as pairs of bf16 numbers (three products; bf16 has fp32's range, so
+// neither needs a scale).  Tile c of four holds the columns 4 i + c, so that
+// a lane has four neighbouring ones of a row: whole lines of the parts, of B
+// and of dH.  (4096 rows of 4096 columns, 128 ranks: 47 us, and 107 with fp32
+// products; 256 rows of 8192 columns, 8 parts: 22 and 25.)
+__global__ __launch_bounds__(kFinishThreads, 2) void bwd_finish_many_kernel(const BwdArgs a) {
+  constexpr int kWaves = kFinishThreads / 64;
+  const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = a.r_c + a.r_r;
+  const int64_t n0 = 32 * (int64_t)blockIdx.x, d0 = kKTile * ((int64_t)blockIdx.y * kWaves + wave);
+  if (d0 >= a.D) return;
+  const int64_t d = d0 + 4 * c32, group = d / a.g;
+  // row of element v of a result tile; past the last row that one
+  auto row = [&](int v) { return std::min<int64_t>(n0 + 8 * (v >> 2) + 4 * half + (v & 3), a.N - 1); };
+  f16x acc[4] = {};
+  for (int p = 0; p < a.splits; ++p) {
+    f4 y[16];
+#pragma unroll
+    for (int v = 0; v < 16; ++v) y[v] = *reinterpret_cast<const f4*>(a.part + ((int64_t)p * a.N + row(v)) * a.D + d);
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[c][v] += y[v][c];
+  }
+#pragma unroll
+  for (int v = 0; v < 16; ++v) {
+    const float s = a.rscale[row(v) * 3];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c][v] *= s;
+  }
+  const float* zrow = a.z + std::min<int64_t>(n0 + c32, a.N - 1) * r;
+  for (int j0 = 0; j0 < r; j0 += 16) {
+    const bool in = j0 + 8 * half < r;  // ranks come in eights
+    const int j = in ? j0 + 8 * half : j0;
+    uint32_t code[8];
+    float z[8], s[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      code[k] = *reinterpret_cast<const uint32_t*>(a.b_codes + (int64_t)(j + k) * a.D + d);
+      s[k] = f16_to_f32(a.b_scales[(int64_t)(j + k) * a.ng + group]);
+      z[k] = zrow[j + k];
     }
-  } else {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      if (in && i < rows) write_dh(a, n0 + i, d, acc[i]);
+    for (int k = 0; k < 8; ++k) z[k] = in ? z[k] : 0.0f;
+    const Bf16Pair zp = split_bf16(z);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float b[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) b[k] = s[k] * (float)(int8_t)(code[k] >> (8 * c));
+      const Bf16Pair bp = split_bf16(b);
+      acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(zp.hi, bp.lo, acc[c], 0, 0, 0);
+      acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(zp.lo, bp.hi, acc[c], 0, 0, 0);
+      acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(zp.hi, bp.hi, acc[c], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < 16; ++v) {
+    const int64_t n = n0 + 8 * (v >> 2) + 4 * half + (v & 3);
+    if (n < a.N) write_dh(a, n, d, f4{acc[0][v], acc[1][v], acc[2][v], acc[3][v]});
   }
 }
 
@@ -1236,17 +1296,18 @@ hipError_t launch_backward(const BwdArgs& a, hipStream_t s) {
     else
       launch_main_tt<8>(a, s);
   }
-  const int64_t row_blocks = (a.N + kFinishRows - 1) / kFinishRows, waves = kFinishThreads / 64;
-  const size_t lds = (size_t)kFinishRows * (a.r_c + a.r_r) * 4;
-  const unsigned columns = (unsigned)((a.D + 255) / 256);
-  // rows of their own for 2048 waves (and their Z in 64 KB of LDS), or a block of rows for every four
+  const size_t lds = (size_t)(a.r_c + a.r_r) * 4;
+  const unsigned columns = (unsigned)((a.D + 255) / 256), waves = kFinishThreads / 64;
+  // bwd_finish_many_kernel where its tiles give every CU two waves: with fewer, one wave
+  // for all parts of a tile is the longer way
   if (a.N <= kFewTokens)
-    hipLaunchKernelGGL(bwd_finish_few_kernel, dim3((unsigned)a.N, columns), dim3(kFinishThreads), lds / kFinishRows, s, a);
-  else if (row_blocks * columns < 2048 || lds * waves > 63 * 1024)
-    hipLaunchKernelGGL(bwd_finish_kernel<true>, dim3((unsigned)row_blocks, columns), dim3(kFinishThreads), lds, s, a);
+    hipLaunchKernelGGL(bwd_finish_few_kernel, dim3((unsigned)a.N, columns), dim3(kFinishThreads), lds, s, a);
+  else if (a.n32 / 32 * a.nkt < 512)
+    hipLaunchKernelGGL(bwd_finish_kernel, dim3((unsigned)((a.N + kFinishRows - 1) / kFinishRows), columns),
+                       dim3(kFinishThreads), lds * kFinishRows, s, a);
   else
-    hipLaunchKernelGGL(bwd_finish_kernel<false>, dim3((unsigned)((row_blocks + waves - 1) / waves), columns),
-                       dim3(kFinishThreads), lds * waves, s, a);
+    hipLaunchKernelGGL(bwd_finish_many_kernel, dim3((unsigned)(a.n32 / 32), (unsigned)((a.nkt + waves - 1) / waves)),
+                       dim3(kFinishThreads), 0, s, a);
   return hipGetLastError();
 }
 

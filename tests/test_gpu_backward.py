@@ -10,8 +10,9 @@ once, plus at most 64 + 64 partial sums).  With
     T[n, d] = sum_v |dY s_R| |q4 c8|,   Y[n, j] = sum_v |dY s_A| |code|
 the residual's part is off by (2^-11 + m 2^-24) T + 2^-39 max|dY s_R| sum_v
 |q4 c8|, Z by the same with its own terms, and dH by these, |Z's error| |B|,
-r 2^-23 |Z| |B| (products and sums of the last step), and the rounding to
-bf16, 2^-8 |dH|.
+r 2^-23 |Z| |B| (products and sums of the last step; of many rows 3 * 2^-18
+more, as Z and B are pairs of bf16 numbers there whose smallest product is
+left out), and the rounding to bf16, 2^-8 |dH|.
 """
 import ctypes
 
@@ -63,7 +64,7 @@ def _bound(dY, h, want):
     for x, w, B, r in parts:
         S = x @ w
         err = (2.0 ** -11 + m) * S + 2.0 ** -39 * x.max(1, keepdims=True) * w.sum(0)
-        tol += err if B is None else err @ B + r * 2.0 ** -23 * (S @ B)
+        tol += err if B is None else err @ B + (r * 2.0 ** -23 + 3 * 2.0 ** -18) * (S @ B)
     return tol + 2.0 ** -8 * (np.abs(want) + tol) + 2.0 ** -120
 
 
@@ -118,6 +119,17 @@ def test_few_tokens_of_every_group_size(V, D, r_c, r_r, g, N):
     torch = torch_mod()
     h, head = _head(V + g, V, D, r_c, r_r, g)
     dY = torch.as_tensor(_gradient(np.random.default_rng(N + V), N, V), device="cuda").bfloat16()
+    _check(head, h, dY, f"V={V} D={D} r={r_c}+{r_r} g={g} N={N}")
+
+
+@pytest.mark.parametrize("V,D,r_c,r_r,g,N", [(200, 1152, 24, 0, 128, 2100), (333, 1152, 8, 16, 32, 1999),
+                                             (3001, 4096, 40, 24, 64, 500), (150, 1024, 0, 0, 256, 2048)])
+def test_many_rows_of_wide_heads(V, D, r_c, r_r, g, N):
+    """The last kernel of many rows: ranks that end in a half step, columns and
+    rows that end inside a workgroup and a tile, several parts."""
+    torch = torch_mod()
+    h, head = _head(V + g, V, D, r_c, r_r, g)
+    dY = torch.as_tensor(_gradient(np.random.default_rng(N), N, V), device="cuda").bfloat16()
     _check(head, h, dY, f"V={V} D={D} r={r_c}+{r_r} g={g} N={N}")
 
 
