@@ -115,14 +115,13 @@ __device__ __forceinline__ float at(const Raw8<float>& x, int j) { return __uint
 struct Scales8 {
   u4 R, A[2];
 };
+// (without a branch: a load behind one is waited for with all others in flight)
 __device__ __forceinline__ Scales8 scales8(const BwdArgs& a, int64_t v) {
-  Scales8 s = {};
+  Scales8 s;
   s.R = *reinterpret_cast<const u4*>(a.r_rowscale + v);
-  if (a.nA == 1) s.A[0] = *reinterpret_cast<const u4*>(a.a_scales + v);
-  if (a.nA == 2) {
-    s.A[0] = *reinterpret_cast<const u4*>(a.a_scales + 2 * v);
-    s.A[1] = *reinterpret_cast<const u4*>(a.a_scales + 2 * v + 8);
-  }
+  const uint16_t* p = (a.nA ? a.a_scales : a.r_rowscale) + (a.nA == 2 ? 2 * v : v);
+  s.A[0] = *reinterpret_cast<const u4*>(p);
+  s.A[1] = *reinterpret_cast<const u4*>(p + (a.nA == 2 ? 8 : 0));
   return s;
 }
 __device__ __forceinline__ float scale_R(const Scales8& s, int j) {
@@ -267,8 +266,10 @@ __global__ __launch_bounds__(kMaxThreads) void bwd_max_kernel(const BwdArgs a) {
 // memory, 1 KB a store, and wave w multiplies dY s_A of its rank tile with
 // the codes that arrange_codes laid out; without kZ all three go to memory,
 // for bwd_few_kernel, without the rows that there are not.
-// (Four waves a SIMD: with the three that its registers would else leave it takes 0.89 ms
-// on 4096 rows of 151936, with them 0.63, with five and their spills 1.46.)
+// (4096 rows of 151936, 128 ranks: 0.57 ms, 4.4 TB/s of dY and the fragments,
+// the vector ALUs busy 60% of the time.  Loads behind branches, which the
+// compiler cannot count, took 0.62; three waves a SIMD instead of four the
+// same, five and their spills 1.46.)
 template <typename T, bool kZ>
 __global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdArgs a) {
   __shared__ float sMax[3][32];
@@ -282,36 +283,38 @@ __global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdA
   const int oct = tid & 15;
   float P[2][3];
   const T* row[2];
-  bool real[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int rr = (tid >> 4) + 16 * i;
-    real[i] = 32 * tile + rr < a.N;
-    row[i] = static_cast<const T*>(a.dY) + (real[i] ? 32 * tile + rr : 0) * a.dy_stride;
-  }
+  for (int i = 0; i < 2; ++i)  // past the last row: that one, whose results nobody reads
+    row[i] = static_cast<const T*>(a.dY) + std::min<int64_t>(32 * tile + (tid >> 4) + 16 * i, a.N - 1) * a.dy_stride;
   const int64_t V16 = 16 * a.nb;
   const int r = a.r_c + a.r_r, tiles = a.nct + a.nwt;
   const int t = kZ ? kPrepWaves * (int)blockIdx.z + wave : tiles;  // this wave's rank tile
   const bool in_c = t < a.nct;
-  const int runs = (a.ksteps + 7) / 8;
+  const int runs = a.ksteps / 8;
   const int run0 = (int)((int64_t)part * runs / gridDim.y), run1 = (int)((int64_t)(part + 1) * runs / gridDim.y);
-  const u2* codes = reinterpret_cast<const u2*>(a.af) + (int64_t)(t < tiles ? t : 0) * a.ksteps * 64 + lane;
+  // (waves without a rank tile load some other's: a load behind a branch would be waited for)
+  const u2* codes = reinterpret_cast<const u2*>(tiles ? a.af : reinterpret_cast<uint8_t*>(a.hf)) +
+                    (int64_t)(t < tiles ? t : 0) * a.ksteps * 64 + lane;
   f16x acc = {};
-  // the next run's loads are in flight while this one is converted and used
+  // the next run's loads are in flight while this one is stored and multiplied
   Raw8<T> x[2] = {};
   Scales8 s;
   u2 b[8];
   auto load = [&](int run) {
     const int64_t v = 128 * (int64_t)run + 8 * oct;
+    if (128 * (int64_t)(run + 1) <= a.V) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (real[i]) x[i] = load8(row[i], v, a.V);
+      for (int i = 0; i < 2; ++i) x[i] = load8(row[i], v, v + 8);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) x[i] = load8(row[i], v, a.V);
+    }
     s = scales8(a, v < V16 ? v : V16 - 8);  // past V16 dY is zero
   };
   auto load_codes = [&](int run) {
-    if (t < tiles) {
+    if constexpr (kZ) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) b[k] = codes[std::min(8 * run + k, a.ksteps - 1) * 64];
+      for (int k = 0; k < 8; ++k) b[k] = codes[(8 * run + k) * 64];
     }
   };
   if (run0 < run1) load(run0);
@@ -337,44 +340,51 @@ __global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdA
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int q = 0; q < 3; ++q) P[i][q] = ldexpf(1.0f, exponent(q, (tid >> 4) + 16 * i));
-  for (int run = run0; run < run1; ++run) {
-    load_codes(run);
+  auto all_runs = [&](auto store_) __attribute__((always_inline)) {
+    for (int run = run0; run < run1; ++run) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      h8 f[3];
+      for (int i = 0; i < 2; ++i) {
+        h8 f[3];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // the product first, as the maximum was taken: times the power it is below 2^15,
-        // also for a large y of an entry of scale 0; what the power adds is exact
-        const float y = at(x[i], j);
-        f[0][j] = (_Float16)(fmaf(y, scale_R(s, j), 0.0f) * P[i][0]);
-        f[1][j] = (_Float16)(fmaf(y, scale_A(s, a.nA, 0, j), 0.0f) * P[i][1]);
-        f[2][j] = (_Float16)(fmaf(y, scale_A(s, a.nA, 1, j), 0.0f) * P[i][2]);
-      }
-      const int at_ = 32 * (oct & 1) + (tid >> 4) + 16 * i;
-#pragma unroll
-      for (int q = 0; q < 3; ++q) frag[q][oct >> 1][at_] = f[q];
-    }
-    if (run + 1 < run1) load(run + 1);
-    __syncthreads();
-    if (first) {
-#pragma unroll
-      for (int q = 0; q < (kZ ? 1 : 3); ++q)
-#pragma unroll
-        for (int k = wave; k < 8; k += kPrepWaves) {
-          const int64_t step = (int64_t)q * a.ksteps + 8 * run + k;
-          if (8 * run + k >= a.ksteps || (!kZ && c32 >= a.N)) continue;
-          h8* out = reinterpret_cast<h8*>(a.hf) + (kZ ? (tile * a.ksteps + step) * 64 + lane : (2 * step + half) * a.N + c32);
-          *out = frag[q][k][lane];
+        for (int j = 0; j < 8; ++j) {
+          // the product first, as the maximum was taken: times the power it is below 2^15,
+          // also for a large y of an entry of scale 0; what the power adds is exact
+          const float y = at(x[i], j);
+          f[0][j] = (_Float16)(fmaf(y, scale_R(s, j), 0.0f) * P[i][0]);
+          f[1][j] = (_Float16)(fmaf(y, scale_A(s, a.nA, 0, j), 0.0f) * P[i][1]);
+          f[2][j] = (_Float16)(fmaf(y, scale_A(s, a.nA, 1, j), 0.0f) * P[i][2]);
         }
-    }
-    if (t < tiles) {
+        const int at_ = 32 * (oct & 1) + (tid >> 4) + 16 * i;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)  // past the last step dY is zero
-        acc = mfma32(frag[in_c ? 1 : 2][k][lane], unpack_u8x8(b[k]), acc);
+        for (int q = 0; q < 3; ++q) frag[q][oct >> 1][at_] = f[q];
+      }
+      load_codes(run);
+      load(std::min(run + 1, run1 - 1));
+      __syncthreads();
+      if constexpr (decltype(store_)::value) {
+#pragma unroll
+        for (int q = 0; q < (kZ ? 1 : 3); ++q)
+#pragma unroll
+          for (int i = 0; i < 8 / kPrepWaves; ++i) {
+            const int k = wave + kPrepWaves * i;
+            const int64_t step = (int64_t)q * a.ksteps + 8 * run + k;
+            if (!kZ && c32 >= a.N) continue;
+            h8* out = reinterpret_cast<h8*>(a.hf) + (kZ ? (tile * a.ksteps + step) * 64 + lane : (2 * step + half) * a.N + c32);
+            *out = frag[q][k][lane];
+          }
+      }
+      if (t < tiles) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          acc = mfma32(frag[in_c ? 1 : 2][k][lane], unpack_u8x8(b[k]), acc);
+      }
+      __syncthreads();
     }
-    __syncthreads();
-  }
+  };
+  if (first)
+    all_runs(std::true_type{});
+  else
+    all_runs(std::false_type{});
   if (t >= tiles) return;
   const int j = 32 * (in_c ? t : t - a.nct) + c32;
   if (j >= (in_c ? a.r_c : a.r_r)) return;
@@ -1211,16 +1221,16 @@ BwdLayout bwd_layout(const archead_dims* d, int64_t n_tokens) {
   BwdLayout L{};
   L.rows = std::min(n_tokens, kBwdChunkRows);
   if (L.rows <= 0) return L;
-  const int64_t V64 = (int64_t)round_up((uint64_t)d->V, 64), r = d->r_c + d->r_r;
+  const int64_t V128 = (int64_t)round_up((uint64_t)d->V, 128), r = d->r_c + d->r_r;
   L.n32 = (int64_t)round_up((uint64_t)L.rows, 32);
-  L.ksteps = V64 / 16;  // whole stages
+  L.ksteps = V128 / 16;  // whole runs of bwd_prep_kernel
   L.pieces = (int)std::max<int64_t>(
       1, std::min<int64_t>({(int64_t)kMaxMaxPieces, (d->V + 2047) / 2048, 2048 * kMaxRows / L.rows}));
   L.width = (int64_t)round_up((uint64_t)((d->V + L.pieces - 1) / L.pieces), 8);
   L.splits = main_splits(L.rows, d->D, (d->r_c + 31) / 32 + (d->r_r + 31) / 32, L.ksteps / 4);
   L.zparts = L.rows <= kFewTokens
                  ? L.splits
-                 : (int)std::max<int64_t>(1, std::min<int64_t>({256, (L.ksteps + 7) / 8, 1024 * 32 / L.n32}));
+                 : (int)std::max<int64_t>(1, std::min<int64_t>({256, L.ksteps / 8, 1024 * 32 / L.n32}));
   auto take = [&](uint64_t bytes) {
     const uint64_t at = L.total;
     L.total += round_up(bytes, ARCHEAD_ALIGNMENT);
@@ -1229,7 +1239,7 @@ BwdLayout bwd_layout(const archead_dims* d, int64_t n_tokens) {
   L.pmax = take((uint64_t)L.rows * L.pieces * 12);
   L.rscale = take((uint64_t)L.n32 * 12);
   const bool few = L.rows <= kFewTokens;
-  L.hf = take((uint64_t)V64 * 2 * (few ? 3 * L.rows : L.n32));
+  L.hf = take((uint64_t)V128 * 2 * (few ? 3 * L.rows : L.n32));
   L.af = take(few ? 0 : (uint64_t)((d->r_c + 31) / 32 + (d->r_r + 31) / 32) * L.ksteps * 512);
   L.gt = take(few ? round_up((uint64_t)d->V, 16) * (uint64_t)(d->D / d->g) : 0);
   L.zpart = take((uint64_t)L.zparts * L.n32 * r * 4);
@@ -1281,7 +1291,7 @@ hipError_t launch_backward(const BwdArgs& a, hipStream_t s) {
                      dim3(kMaxThreads), 0, s, a);
   const int tt = main_tiles(a.N);
   if (a.N <= kFewTokens) {
-    const unsigned runs = (unsigned)((a.ksteps + 7) / 8);
+    const unsigned runs = (unsigned)(a.ksteps / 8);
     hipLaunchKernelGGL((bwd_prep_kernel<T, false>), dim3(1, std::min(runs, 1024u)), dim3(64 * kPrepWaves), 0, s, a);
     launch_few(a, s);
   } else {

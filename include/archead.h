@@ -599,7 +599,7 @@ ARCHEAD_API int archead_preference_loss(const archead_tensor* Y, const archead_p
 
 /* Device workspace archead_logits_backward needs for n_tokens rows: for
  * min(n_tokens, 4096) rows, dY as fp16 operands (2 bytes an element, rows
- * rounded up to 32 and the vocabulary to 64), fp32 partial sums of dH and of
+ * rounded up to 32 and the vocabulary to 128), fp32 partial sums of dH and of
  * its low-rank part, the A codes in operand order, and row scales; up to 32
  * rows instead three sets of operands, without rounding the rows up, and the
  * group codes.  A call of more rows may leave fewer than 4096 to its last
