@@ -482,6 +482,7 @@ __device__ __forceinline__ void loss_total(const RowArgs& a) {
   double sum = 0.0;
   const double* parts = a.row_slope ? a.pair_loss : a.term;
   const int64_t count = a.row_slope ? a.B : a.N;
+#pragma unroll 8
   for (int64_t i = threadIdx.x; i < count; i += kRowThreads) sum += parts[i];
   sum = block_sum<kRowThreads>(sum, buf);
   if (threadIdx.x == 0 && a.loss) *a.loss = (float)sum;
@@ -616,9 +617,12 @@ __global__ __launch_bounds__(kOrderThreads) void row_order_kernel(const RowArgs 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t front = 0, back = 0;  // rows placed so far
   int turn = 0;
+  auto counts = [&](int64_t n) { return n < a.N && row_counts<false>(a, n); };
+  bool later = counts(threadIdx.x);
   for (int64_t n0 = 0; n0 < a.N; n0 += kOrderThreads, turn ^= 1) {
     const int64_t n = n0 + threadIdx.x;
-    const bool in = n < a.N, on = in && row_counts<false>(a, n);
+    const bool in = n < a.N, on = later;
+    later = counts(n + kOrderThreads);  // the next rows' weights are on their way meanwhile
     const uint64_t ons = __ballot(on);
     if (lane == 0) count[turn][wave] = __popcll(ons);
     __syncthreads();  // the other turn's counts are read before the next one's are written
