@@ -582,7 +582,7 @@ def _scoped(call):
     @functools.wraps(call)
     def run(first, *args, stream=None, **kw):
         device = first.device
-        if stream is None and (device.type != "cuda" or device.index == torch.cuda.current_device()):
+        if stream is None and (device.type != "cuda" or device.index == torch._C._cuda_getDevice()):
             return call(first, *args, **kw)
         with _scope(device, stream):
             return call(first, *args, **kw)
@@ -597,7 +597,7 @@ def _vec(t, name: str, dtype, n: int, device):
     """Address of a contiguous vector of n elements (None for None)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.device != device:
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != device.index:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}")
     return t.data_ptr()
 
@@ -631,7 +631,7 @@ def _gradient_of(Y, dY, dY_dtype, with_gradient):
     if not with_gradient:
         return None
     if dY is None:
-        return _torch().empty(Y.shape, dtype=dY_dtype or Y.dtype, device=Y.device)
+        return _torch().empty_like(Y, dtype=dY_dtype)
     if dY.device != Y.device or (dY_dtype is not None and dY_dtype != dY.dtype):
         raise ValueError("dY must be on Y's device and of dY_dtype")
     return dY
@@ -667,7 +667,8 @@ def archead_policy_loss(Y, labels, advantage, old_logp=None, ref_logp=None, weig
     status = lib.archead_policy_loss(y, inp, outs, *_span(ws), _raw_stream(dev))
     if status:
         _check(status, "archead_policy_loss")
-    out = {"loss": vec[2 * N], "logp": vec[:N], "row_loss": vec[N:2 * N]}
+    logp, row_loss, loss = vec.split_with_sizes((N, N, 1))
+    out = {"loss": loss.view(()), "logp": logp, "row_loss": row_loss}
     if dY is not None:
         out["dY"] = dY
     return out
@@ -707,7 +708,8 @@ def archead_preference_loss(Y, labels, offsets, ref_logp=None, weight=None, pair
     status = lib.archead_preference_loss(y, inp, outs, *_span(ws), _raw_stream(dev))
     if status:
         _check(status, "archead_preference_loss")
-    out = {"loss": vec[M], "logp": vec[:N], "chosen_reward": vec[N:N + B], "rejected_reward": vec[N + B:M]}
+    logp, chosen, rejected, loss = vec.split_with_sizes((N, B, B, 1))
+    out = {"loss": loss.view(()), "logp": logp, "chosen_reward": chosen, "rejected_reward": rejected}
     if dY is not None:
         out["dY"] = dY
     return out
