@@ -437,6 +437,20 @@ def test_preference_matches_oracle(N, V, offsets, kind, eps, y, dy):
     _check_preference(got, Y64, labels, offsets, y == "bfloat16", beta=0.25, kind=kind)
 
 
+@pytest.mark.parametrize("y,V", [("bfloat16", 40001), ("float32", 20003)])
+def test_preference_of_many_long_rows(y, V):
+    """Enough work that pieces are whole rounds of a workgroup's loads, which a
+    row's last piece is not."""
+    torch = torch_mod()
+    rng = np.random.default_rng(V)
+    N, offsets = 430, [3, 150, 200, 420, 425]
+    Y, Y64 = _make_Y(rng, N, V, getattr(torch, y))
+    labels = rng.integers(0, V, N)
+    labels[:4] = V - 1
+    got = _run_preference(Y, labels, offsets, beta=0.25)
+    _check_preference(got, Y64, labels, offsets, y == "bfloat16", beta=0.25)
+
+
 def test_preference_large_margins_stay_finite():
     torch = torch_mod()
     rng = np.random.default_rng(2)
