@@ -914,9 +914,15 @@ hipError_t launch_gradient(const RowArgs& a, const archead_tensor* dY, hipStream
 }
 
 // The fused kernel: a row for every CU, and rows that fill half of the chunks
-// held.  (At 257 rows of 100003 fp32 logits and at 512 of 151936 in bf16 it
-// and the split kernels take the same time to within 4%.)
+// held.  Of bf16 rows in between one round of the CUs and eight it would leave
+// part of them idle in the last round, and the split kernels' second read comes
+// from the cache.  (Microseconds of the fused and of the split kernels, 3/4 of
+// the rows counting, 151936 bf16 logits: 256 rows 40 and 44, 300 43 and 49, 400
+// 73 and 61, 512 81 and 77, 768 113 and 102, 1024 121 and 127, 1500 195 and 190,
+// 4096 518 and 627; 100003 fp32 logits: 256 rows 44 and 47, 400 73 and 67, 512
+// 82 and 86, 1024 156 and 168.)
 bool fused_takes(const RowArgs& a, int64_t size) {
+  if (size == 2 && a.N > kFusedLeastRows * 5 / 4 && a.N < kFusedLeastRows * 8) return false;
   return a.N >= kFusedLeastRows && a.V * size >= kHeldChunks / 2 * kFusedThreads * 16 && a.V < (int64_t(1) << 30);
 }
 
