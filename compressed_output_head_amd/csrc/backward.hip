@@ -47,6 +47,18 @@ constexpr int kMaxMaxPieces = 128;
 constexpr int kXcds = 8;
 constexpr int kMaxSplits = 64;
 constexpr int64_t kFewTokens = 32;  // of bwd_few_kernel
+// Where kOwnRounds rounds of loads reach all of dY, every workgroup of
+// bwd_prep_kernel finds the rows' maxima itself: a call of 4 rows of a 1024 x
+// 256 head takes 20 us, with a launch for them 24; sixteen rounds 25 and 24,
+// 32 rounds 36 and 25.
+constexpr int64_t kOwnRounds = 8;
+
+// Lanes a row then: as many as there are, a wave at most.
+__host__ __device__ constexpr int own_lanes(int64_t N) {
+  int lanes = 64;
+  while (lanes * N > 64 * kPrepWaves) lanes /= 2;
+  return lanes;
+}
 
 struct BwdArgs {
   int64_t V, D, N, n32, nb;
@@ -72,7 +84,7 @@ struct BwdArgs {
   float* zpart;     // [zparts][n32][r_c + r_r]
   float* z;         // [n32][r_c + r_r]; few tokens: not used, bwd_finish_few_kernel sums the parts
   float* part;      // [splits][N][D]
-  int pieces, zparts, splits, ksteps;
+  int pieces, zparts, splits, ksteps;  // pieces 0: bwd_prep_kernel finds the maxima itself
   int64_t width;    // columns of a piece of bwd_max_kernel
 };
 
@@ -187,6 +199,15 @@ __device__ __forceinline__ void arrange_groups(const BwdArgs& a, int64_t i) {
   }
 }
 
+__device__ __forceinline__ void arrange_groups(const BwdArgs& a, int64_t i) {
+  if (a.g == 32)
+    arrange_groups<uint32_t>(a, i);
+  else if (a.g == 64)
+    arrange_groups<uint16_t>(a, i);
+  else
+    arrange_groups<uint8_t>(a, i);
+}
+
 // Eight of them as fp16: byte u under the byte 0x64 is 1024 + u, exactly.
 __device__ __forceinline__ h8 unpack_u8x8(u2 c) {
   const h2 bias = {(_Float16)1152.0f, (_Float16)1152.0f};
@@ -210,14 +231,10 @@ __global__ __launch_bounds__(kMaxThreads) void bwd_max_kernel(const BwdArgs a) {
   const int64_t groups = (a.N + kMaxRows - 1) / kMaxRows;
   if ((int64_t)blockIdx.x >= groups * a.pieces) {
     const int64_t i = ((int64_t)blockIdx.x - groups * a.pieces) * kMaxThreads + threadIdx.x;
-    if (!a.gt)
-      arrange_codes(a, i);
-    else if (a.g == 32)
-      arrange_groups<uint32_t>(a, i);
-    else if (a.g == 64)
-      arrange_groups<uint16_t>(a, i);
+    if (a.gt)
+      arrange_groups(a, i);
     else
-      arrange_groups<uint8_t>(a, i);
+      arrange_codes(a, i);
     return;
   }
   const int64_t n0 = blockIdx.x / a.pieces * kMaxRows;
@@ -265,17 +282,26 @@ __global__ __launch_bounds__(kMaxThreads) void bwd_max_kernel(const BwdArgs a) {
 // l % 32, columns 16 step + 8 (l / 32) .. + 8).  From there dY s_R goes to
 // memory, 1 KB a store, and wave w multiplies dY s_A of its rank tile with
 // the codes that arrange_codes laid out; without kZ all three go to memory,
-// for bwd_few_kernel, without the rows that there are not.
+// for bwd_few_kernel, without the rows that there are not.  Of few columns
+// (kOwn) its workgroups find the rows' maxima themselves, and others beside
+// them lay the group codes out: a launch less.
 // (4096 rows of 151936, 128 ranks: 0.57 ms, 4.4 TB/s of dY and the fragments,
 // the vector ALUs busy 60% of the time.  Loads behind branches, which the
 // compiler cannot count, took 0.62; three waves a SIMD instead of four the
 // same, five and their spills 1.46.)
-template <typename T, bool kZ>
+template <typename T, bool kZ, bool kOwn>
 __global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdArgs a) {
   __shared__ float sMax[3][32];
   __shared__ h8 frag[3][8][66];  // steps two octets apart, so that a wave's writes meet no bank twice
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if constexpr (kOwn) {
+    if (blockIdx.x == 1) {
+      for (int64_t i = (int64_t)blockIdx.y * 64 * kPrepWaves + tid; i < a.nb * a.ng; i += (int64_t)gridDim.y * 64 * kPrepWaves)
+        arrange_groups(a, i);
+      return;
+    }
+  }
   const int64_t tile = blockIdx.x;
   const int part = blockIdx.y;
   const bool first = blockIdx.z == 0;
@@ -318,18 +344,45 @@ __global__ __launch_bounds__(64 * kPrepWaves, 4) void bwd_prep_kernel(const BwdA
     }
   };
   if (run0 < run1) load(run0);
-  // the tile's maxima from the pieces', eight lanes each
+  if constexpr (kOwn) {
+    const int lanes = own_lanes(a.N), rr = tid / lanes;
+    float m[3] = {};
+    if (rr < a.N) {
+      const T* src = static_cast<const T*>(a.dY) + rr * a.dy_stride;
+      for (int64_t v = 8 * (tid % lanes); v < a.V; v += 8 * lanes) {
+        const Raw8<T> y8 = load8(src, v, a.V);
+        const Scales8 s8 = scales8(a, v);
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const int i = tid / 8 + 32 * k, rr = i / 3;
-    float m = 0.0f;
-    if (32 * tile + rr < a.N) {
-      const float* src = a.pmax + (96 * tile + i) * a.pieces;
-#pragma unroll 4
-      for (int p = tid & 7; p < a.pieces; p += 8) m = fmaxf(m, src[p]);
+        for (int j = 0; j < 8; ++j) {
+          const float y = at(y8, j);
+          m[0] = fmaxf(m[0], fabsf(y * scale_R(s8, j)));
+          m[1] = fmaxf(m[1], fabsf(y * scale_A(s8, a.nA, 0, j)));
+          m[2] = fmaxf(m[2], fabsf(y * scale_A(s8, a.nA, 1, j)));
+        }
+      }
     }
-    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    if ((tid & 7) == 0) sMax[i % 3][rr] = m;
+    for (int o = lanes / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int q = 0; q < 3; ++q) m[q] = fmaxf(m[q], __shfl_xor(m[q], o));
+    if (tid < 96) sMax[tid / 32][tid % 32] = 0.0f;
+    __syncthreads();
+    if (rr < a.N && tid % lanes == 0)
+#pragma unroll
+      for (int q = 0; q < 3; ++q) sMax[q][rr] = m[q];
+  } else {
+    // the tile's maxima from the pieces', eight lanes each
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int i = tid / 8 + 32 * k, rr = i / 3;
+      float m = 0.0f;
+      if (32 * tile + rr < a.N) {
+        const float* src = a.pmax + (96 * tile + i) * a.pieces;
+#pragma unroll 4
+        for (int p = tid & 7; p < a.pieces; p += 8) m = fmaxf(m, src[p]);
+      }
+      for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+      if ((tid & 7) == 0) sMax[i % 3][rr] = m;
+    }
   }
   __syncthreads();
   // at most 126: the power and its inverse are normal fp32
@@ -1226,7 +1279,8 @@ BwdLayout bwd_layout(const archead_dims* d, int64_t n_tokens) {
   L.ksteps = V128 / 16;  // whole runs of bwd_prep_kernel
   L.pieces = (int)std::max<int64_t>(
       1, std::min<int64_t>({(int64_t)kMaxMaxPieces, (d->V + 2047) / 2048, 2048 * kMaxRows / L.rows}));
-  L.width = (int64_t)round_up((uint64_t)((d->V + L.pieces - 1) / L.pieces), 8);
+  if (L.rows <= kFewTokens && d->V <= 8 * kOwnRounds * own_lanes(L.rows)) L.pieces = 0;
+  L.width = L.pieces == 0 ? 0 : (int64_t)round_up((uint64_t)((d->V + L.pieces - 1) / L.pieces), 8);
   L.splits = main_splits(L.rows, d->D, (d->r_c + 31) / 32 + (d->r_r + 31) / 32, L.ksteps / 4);
   L.zparts = L.rows <= kFewTokens
                  ? L.splits
@@ -1287,15 +1341,19 @@ template <typename T>
 hipError_t launch_backward(const BwdArgs& a, hipStream_t s) {
   const int64_t ranks = a.nct + a.nwt, max_groups = (a.N + kMaxRows - 1) / kMaxRows * a.pieces;
   const int64_t arrange = a.gt ? a.nb * a.ng / std::max(1, kKTile / a.g) : ranks * a.ksteps * 16;  // threads
-  hipLaunchKernelGGL(bwd_max_kernel<T>, dim3((unsigned)(max_groups + (arrange + kMaxThreads - 1) / kMaxThreads)),
+  if (a.pieces > 0)
+    hipLaunchKernelGGL(bwd_max_kernel<T>, dim3((unsigned)(max_groups + (arrange + kMaxThreads - 1) / kMaxThreads)),
                      dim3(kMaxThreads), 0, s, a);
   const int tt = main_tiles(a.N);
   if (a.N <= kFewTokens) {
     const unsigned runs = (unsigned)(a.ksteps / 8);
-    hipLaunchKernelGGL((bwd_prep_kernel<T, false>), dim3(1, std::min(runs, 1024u)), dim3(64 * kPrepWaves), 0, s, a);
+    if (a.pieces > 0)
+      hipLaunchKernelGGL((bwd_prep_kernel<T, false, false>), dim3(1, std::min(runs, 1024u)), dim3(64 * kPrepWaves), 0, s, a);
+    else
+      hipLaunchKernelGGL((bwd_prep_kernel<T, false, true>), dim3(2, runs), dim3(64 * kPrepWaves), 0, s, a);
     launch_few(a, s);
   } else {
-    hipLaunchKernelGGL((bwd_prep_kernel<T, true>),
+    hipLaunchKernelGGL((bwd_prep_kernel<T, true, false>),
                        dim3((unsigned)(a.n32 / 32), (unsigned)a.zparts, (unsigned)std::max<int64_t>(1, (ranks + kPrepWaves - 1) / kPrepWaves)),
                        dim3(64 * kPrepWaves), 0, s, a);
     if (ranks > 0) hipLaunchKernelGGL(bwd_zsum_kernel, dim3((unsigned)a.N), dim3(kZsumThreads), 0, s, a);
