@@ -37,6 +37,7 @@
 
 #include <algorithm>
 #include <initializer_list>
+#include <limits>
 
 #include "device_common.h"
 #include "internal.h"
@@ -64,7 +65,7 @@ struct RowGrad {
   uint32_t on;  // 0: the gradient is zero
 };
 
-// s log2 e = hi + lo
+// s log2 e = hi + lo, both above zero
 struct Scale {
   float hi, lo;
 };
@@ -154,7 +155,8 @@ __device__ __forceinline__ void store_run(float* p, const float* g) {
   }
 }
 
-// 2^(k d)
+// 2^(k d).  d is -inf where a logit or a running maximum is: both products are
+// -inf then and the result 0, as neither part of k is negative or zero.
 __device__ __forceinline__ float exp_at(float d, Scale k) {
   return __builtin_amdgcn_exp2f(fmaf(d, k.hi, d * k.lo));
 }
@@ -656,7 +658,7 @@ __global__ __launch_bounds__(kOrderThreads) void row_order_kernel(const RowArgs 
 // kFusedThreads chunks: any number of the row's range will do, S >= 1 as those
 // chunks are in it, and a row whose S overflows (a logit about 100 octaves
 // above them, or first chunks of -inf) is summed again with running maxima.
-// A bf16 gradient leaves the low part of k out, 2^-25 of the exponent.
+// A bf16 gradient leaves the low part of k out, 2^-23 of the exponent at most.
 template <typename T, typename G>
 __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowArgs a) {
   using E = Elem<T>;
@@ -865,6 +867,17 @@ int check_workspace(const void* ws, uint64_t bytes, uint64_t need) {
   return bytes < need ? ARCHEAD_E_WORKSPACE : ARCHEAD_OK;
 }
 
+// The scale's two parts.  hi is s log2 e to nearest where that lies below it,
+// else the number before that, so that lo is above zero as well; where s is at
+// the end of fp32's range they stay in it.
+Scale scale_of(float s) {
+  constexpr float kLeast = std::numeric_limits<float>::denorm_min(), kMost = std::numeric_limits<float>::max();
+  const double k = (double)s * 1.44269504088896340736;
+  float hi = (float)std::min(k, (double)kMost);
+  if ((double)hi >= k) hi = nextafterf(hi, 0.0f);
+  return Scale{std::max(hi, kLeast), std::max((float)(k - (double)hi), kLeast)};
+}
+
 RowArgs row_args(const archead_tensor* Y, const archead_tensor* dY, float s, void* workspace, const LossWorkspace& W) {
   RowArgs a{};
   a.Y = Y->data;
@@ -886,9 +899,7 @@ RowArgs row_args(const archead_tensor* Y, const archead_tensor* dY, float s, voi
     a.pieces = (int)((a.V + a.width - 1) / a.width);
   }
   a.s = s;
-  const double k = (double)s * 1.44269504088896340736;
-  a.k.hi = (float)k;
-  a.k.lo = (float)(k - (double)a.k.hi);
+  a.k = scale_of(s);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.part = reinterpret_cast<Stat*>(ws + W.part);
   a.ylab = reinterpret_cast<float*>(ws + W.ylab);
