@@ -8,17 +8,20 @@
 // a coefficient per row.  With k = s log2 e as an fp32 pair (one fp32 number
 // alone would shift every log p of a call by a few 1e-7, the same way for all
 // rows) and M = max y
-//   e_j = 2^(k (y_j - M)),  S = sum_j e_j,  log p = s (y_label - M) - ln S,
-// where the last line and all per-row arithmetic after it are fp64 (a loss
-// is a sum of terms of both signs, and one row is one thread's work).  The
-// difference is taken first: a fused k y - k M would save an instruction, but
-// overflows where every logit of a piece is the type's lowest value.  S is
-// summed in fp32 trees of 8 to 32 terms, and in fp64 from there.
-// The label's element of the gradient is -coef s expm1(log p), which keeps
-// its digits where p is close to 1.
+//   e_j = 2^(k (y_j - M)),  S = sum of e_j but the label's,  E = exp(s (y_label - M)),
+//   log p = -ln(1 + S / E) where S < E, else s (y_label - M) - ln(S + E),
+// M being the maximum without the label too.  The last two and all per-row
+// arithmetic after them are fp64 (a loss is a sum of terms of both signs, and
+// one row is one thread's work).  With the label's own term in S, a row with p
+// close to 1 would lose log p in its rounding, as 1 + S rounds S's digits off;
+// so S / E keeps them, and so does the label's element of the gradient,
+// -coef s expm1(log p).  The difference y - M is taken before the product: a
+// fused k y - k M would save an instruction, but overflows where every logit
+// of a piece is the type's lowest value.  S is summed in fp32 trees of 8 to 32
+// terms, and in fp64 from there.
 //
 // A row is cut into pieces so that few rows still fill the GPU:
-//   row_pieces_kernel   (M, S) of every piece, and the label's logit
+//   row_pieces_kernel   (M, S) of every piece without the label, and the label's logit
 //   rows_kernel         a row's pieces merged, its loss and its coefficient
 //   pair_kernel         preference loss only: the sequences' sums, the pair's
 //                       loss and its slope for every row
@@ -227,11 +230,23 @@ __device__ __forceinline__ float chunk_sum(const u4& v, float M0, Scale k) {
   return e[0];
 }
 
-// (M, S) of the elements [0, len) at p, the share of thread tid of kThreads.
-template <typename T, int kThreads>
-__device__ __forceinline__ Stat thread_stats(const T* p, int64_t len, Scale k, int tid) {
+// A chunk whose element j is -inf.
+template <typename T>
+__device__ __forceinline__ u4 without(u4 v, int j) {
+  constexpr int n = Elem<T>::kPer16 / 4;  // elements of a word
+  const uint32_t keep = n == 1 ? 0u : 0xffff0000u >> (16 * (j & 1));
+#pragma unroll
+  for (int w = 0; w < 4; ++w) v[w] = w == j / n ? (v[w] & keep) | (Elem<T>::kNegInf2 & ~keep) : v[w];
+  return v;
+}
+
+// (M, S) of the elements [0, len) at p but that at `label` (none where it is
+// negative), the share of thread tid of kThreads.
+template <typename T, int kThreads, int kUnroll = kRowUnroll>
+__device__ __forceinline__ Stat thread_stats(const T* p, int64_t len, int64_t label, Scale k, int tid) {
   using E = Elem<T>;
   const int64_t full = len / E::kPer16;
+  const int64_t label_chunk = label >= 0 && label / E::kPer16 % kThreads == tid ? label / E::kPer16 : -1;
   float M = -INFINITY, M0 = 0.0f;
   double S = 0.0;
   auto rise = [&](float top) {  // of the running maximum
@@ -240,27 +255,36 @@ __device__ __forceinline__ Stat thread_stats(const T* p, int64_t len, Scale k, i
       M = M0 = top;
     }
   };
-  for (int64_t c0 = tid; c0 < full; c0 += kThreads * kRowUnroll) {
-    u4 v[kRowUnroll];
+  for (int64_t c0 = tid; c0 < full; c0 += kThreads * kUnroll) {
+    u4 v[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kRowUnroll; ++u) {
+    for (int u = 0; u < kUnroll; ++u) {
       const int64_t c = c0 + u * kThreads;
       v[u] = c < full ? u4(*reinterpret_cast<const u4_any*>(p + c * E::kPer16))
                       : u4{E::kNegInf2, E::kNegInf2, E::kNegInf2, E::kNegInf2};
     }
+    if (label_chunk >= c0 && label_chunk < c0 + kThreads * kUnroll) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (c0 + u * kThreads == label_chunk) v[u] = without<T>(v[u], (int)(label % E::kPer16));
+    }
     float top = M;
 #pragma unroll
-    for (int u = 0; u < kRowUnroll; ++u)
+    for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
       for (int j = 0; j < E::kPer16; ++j) top = fmaxf(top, E::at(v[u], j));
     rise(top);
-    float add[kRowUnroll];
+    float add[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kRowUnroll; ++u) add[u] = chunk_sum<T>(v[u], M0, k);
-    S += (double)((add[0] + add[1]) + (add[2] + add[3]));
+    for (int u = 0; u < kUnroll; ++u) add[u] = chunk_sum<T>(v[u], M0, k);
+#pragma unroll
+    for (int w = kUnroll / 2; w > 0; w >>= 1)
+#pragma unroll
+      for (int u = 0; u < w; ++u) add[u] += add[u + w];
+    S += (double)add[0];
   }
   const int64_t i = full * E::kPer16 + tid;  // fewer than 8 elements are left
-  if (i < len) {
+  if (i < len && i != label) {
     const float y = E::one(p[i]);
     rise(y);
     S += (double)exp_at(y - M0, k);
@@ -281,7 +305,9 @@ __global__ __launch_bounds__(kRowThreads) void row_pieces_kernel(const RowArgs a
   // read here, before any launch that may write the gradient over Y
   if (threadIdx.x == 0 && (valid ? label >= c0 && label < c1 : p == 0))
     a.ylab[n] = valid ? Elem<T>::one(row[label]) : __builtin_nanf("");
-  const Stat r = block_merge<kRowThreads>(thread_stats<T, kRowThreads>(row + c0, c1 - c0, a.k, threadIdx.x), a.k, buf);
+  const int64_t place = valid && label < c1 ? label - c0 : -1;  // negative in a later piece too
+  const Stat r =
+      block_merge<kRowThreads>(thread_stats<T, kRowThreads>(row + c0, c1 - c0, place, a.k, threadIdx.x), a.k, buf);
   if (threadIdx.x == 0) a.part[n * a.pieces + p] = r;
 }
 
@@ -309,11 +335,25 @@ struct PolicyScalars {
   uint32_t own_ratio;  // 1: the policy that sampled is this one
 };
 
+// A row's log-probability, its S with the label's term, and the M that S is by.
+struct RowLogp {
+  double logp, S;
+  float M;
+};
+__device__ __forceinline__ RowLogp row_logp(const PolicyRow& x, double s) {
+  // NaN and +inf have no log p; neither has a row with nothing above -inf, where the difference is NaN
+  const double y = x.y_label < INFINITY ? (double)x.y_label : __builtin_nan("");
+  const float M = x.M == -INFINITY ? x.y_label : x.M;  // the label is all there is
+  const double t = s * (y - (double)M), E = exp(t), S = x.S + E;
+  return RowLogp{x.S < E ? 0.0 - log1p(x.S / E) : t - log(S), S, M};
+}
+
 // Not inlined: in a loop, the compiler would hold every constant of the fp64
 // functions in registers that the row needs.
 __device__ __attribute__((noinline)) PolicyResult policy_row(PolicyRow x, PolicyScalars p) {
   const double s = p.s, w = x.weight, A = x.advantage;
-  const double logp = s * ((double)x.y_label - (double)x.M) - log(x.S);
+  const RowLogp row = row_logp(x, s);
+  const double logp = row.logp;
   const double ratio = exp(logp - (p.own_ratio ? logp : (double)x.old_logp));
   const double lo = 1.0 - (double)p.clip_low, hi = 1.0 + (double)p.clip_high;
   const double kept = ratio < lo ? lo : ratio > hi ? hi : ratio;  // NaN stays NaN
@@ -327,7 +367,7 @@ __device__ __attribute__((noinline)) PolicyResult policy_row(PolicyRow x, Policy
   }
   const double c = w * slope * s;
   return PolicyResult{loss, w * loss, (float)logp,
-                      RowGrad{(float)(-c / x.S), x.M, (float)(-c * expm1(logp)), c != 0.0 ? 1u : 0u}};
+                      RowGrad{(float)(-c / row.S), row.M, (float)(-c * expm1(logp)), c != 0.0 ? 1u : 0u}};
 }
 
 __device__ __forceinline__ PolicyScalars policy_scalars(const RowArgs& a) {
@@ -337,9 +377,10 @@ __device__ __forceinline__ PolicyScalars policy_scalars(const RowArgs& a) {
 // A row of a pair: its term of the sequence's sum, and its gradient but for
 // the slope of the pair's loss.
 __device__ __forceinline__ PolicyResult pair_row(const PolicyRow& x, float s) {
-  const double w = x.weight, logp = (double)s * ((double)x.y_label - (double)x.M) - log(x.S), c = w * (double)s;
-  return PolicyResult{0.0, w * (logp - (double)x.ref_logp), (float)logp,
-                      RowGrad{(float)(-c / x.S), x.M, (float)(-c * expm1(logp)), 1u}};
+  const RowLogp row = row_logp(x, s);
+  const double w = x.weight, c = w * (double)s;
+  return PolicyResult{0.0, w * (row.logp - (double)x.ref_logp), (float)row.logp,
+                      RowGrad{(float)(-c / row.S), row.M, (float)(-c * expm1(row.logp)), 1u}};
 }
 
 template <bool kPairs>
@@ -574,8 +615,9 @@ __global__ __launch_bounds__(kSmallThreads) void small_loss_kernel(const RowArgs
     if (row_counts<kPairs>(a, n)) {
       PolicyRow x = row_inputs<kPairs>(a, n);
       const int64_t label = a.labels[n];
-      x.y_label = label >= 0 && label < a.V ? Elem<T>::one(row_of(n)[label]) : __builtin_nanf("");
-      const Stat st = wave_merge(thread_stats<T, 64>(row_of(n), a.V, a.k, lane), a.k);
+      const bool valid = label >= 0 && label < a.V;
+      x.y_label = valid ? Elem<T>::one(row_of(n)[label]) : __builtin_nanf("");
+      const Stat st = wave_merge(thread_stats<T, 64>(row_of(n), a.V, valid ? label : -1, a.k, lane), a.k);
       x.M = st.M;
       x.S = st.S;
       r = row_result<kPairs>(a, x);
@@ -655,8 +697,7 @@ __global__ __launch_bounds__(kOrderThreads) void row_order_kernel(const RowArgs 
 // with half the registers each took 0.64 ms or more.
 //
 // What is subtracted in the exponents is the maximum of the row's first
-// kFusedThreads chunks: any number of the row's range will do, S >= 1 as those
-// chunks are in it, and a row whose S overflows (a logit about 100 octaves
+// kFusedThreads chunks without the label: S >= 1 as those chunks are in it, and a row whose S overflows (a logit about 100 octaves
 // above them, or first chunks of -inf) is summed again with running maxima.
 // A bf16 gradient leaves the low part of k out, 2^-23 of the exponent at most.
 template <typename T, typename G>
@@ -667,7 +708,7 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
   __shared__ double sum_buf[kWaves];
   __shared__ Stat pair_buf[kWaves];
   __shared__ RowGrad grad;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int full = (int)(a.V / n16), rest = (int)(a.V % n16);
   const int64_t count = a.order[a.N];  // rows that count
   u4 v[kHeld];
@@ -701,6 +742,16 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
     const int64_t next = more ? a.order[place + gridDim.x] : n;
     PolicyRow x = row_inputs<false>(a, n);
     x.y_label = y_label;
+    // the label out of its chunk, or out of the row's last elements (its gradient is written for itself)
+    const int label = __builtin_amdgcn_readfirstlane(a.labels[n]);
+    const bool valid = label >= 0 && label < a.V;
+    const int label_chunk = valid ? label / n16 : -1, label_at = label % n16;
+    if (valid && label_chunk % kFusedThreads / 64 == wave) {
+#pragma unroll
+      for (int c = 0; c < kHeld; ++c)
+        if (label_chunk / kFusedThreads == c && label_chunk % kFusedThreads == tid) v[c] = without<T>(v[c], label_at);
+    }
+    if (label_chunk == full && tid == label_at) y_rest = -INFINITY;
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < n16; ++j) top = fmaxf(top, E::at(v[0], j));
@@ -720,7 +771,9 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
       asm volatile("" : "+v"(v[c]));
     }
     for (int64_t c = kHeld * kFusedThreads + tid; c < full; c += kFusedThreads) {
-      S += (double)chunk_sum<T>(u4(*reinterpret_cast<const u4_any*>(row + c * n16)), shift, a.k);
+      u4 y = u4(*reinterpret_cast<const u4_any*>(row + c * n16));
+      if (c == label_chunk) y = without<T>(y, label_at);
+      S += (double)chunk_sum<T>(y, shift, a.k);
     }
     for (int o = 32; o > 0; o >>= 1) S += __shfl_xor(S, o);
     if (lane == 0) sum_buf[wave] = S;
@@ -731,7 +784,8 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
     x.M = shift;
     x.S = S;
     if (!(S >= 0.5 && S < 3e38)) {  // the same decision in every thread
-      const Stat st = block_merge<kFusedThreads>(thread_stats<T, kFusedThreads>(row, a.V, a.k, tid), a.k, pair_buf);
+      const Stat st = block_merge<kFusedThreads>(
+          thread_stats<T, kFusedThreads, 2>(row, a.V, valid ? label : -1, a.k, tid), a.k, pair_buf);
       x.M = st.M;
       x.S = st.S;
     }
@@ -766,10 +820,7 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
       put(*reinterpret_cast<const u4_any*>(row + (c + tid) * n16), out + c * n16);
     if (tid < rest) out[(int64_t)full * n16 + tid] = Elem<G>::from(g.neg * exp_at(y_rest - g.M, a.k));
     // the label's element, by the thread that wrote it
-    const int64_t label = a.labels[n];
-    if (label >= 0 && label < a.V &&
-        tid == (int)(label < (int64_t)full * n16 ? label / n16 % kFusedThreads : label - (int64_t)full * n16))
-      out[label] = Elem<G>::from(g.label_g);
+    if (valid && tid == (label_chunk < full ? label_chunk % kFusedThreads : label_at)) out[label] = Elem<G>::from(g.label_g);
     if (more) load_ends(next_row, next);
   }
   // the rows that do not count
