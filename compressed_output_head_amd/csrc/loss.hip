@@ -697,8 +697,11 @@ __global__ __launch_bounds__(kOrderThreads) void row_order_kernel(const RowArgs 
 // with half the registers each took 0.64 ms or more.
 //
 // What is subtracted in the exponents is the maximum of the row's first
-// kFusedThreads chunks without the label: S >= 1 as those chunks are in it, and a row whose S overflows (a logit about 100 octaves
-// above them, or first chunks of -inf) is summed again with running maxima.
+// kFusedThreads chunks without the label: S >= 1 as those chunks are in it.  A
+// row whose S passes 2^20 (logits about as many octaves above them), or whose
+// first chunks are -inf, is summed again with running maxima: the coefficient
+// over S has to stay a normal number for the gradient's other elements, and
+// the exponential of many octaves has fewer digits.
 // A bf16 gradient leaves the low part of k out, 2^-23 of the exponent at most.
 template <typename T, typename G>
 __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowArgs a) {
@@ -783,7 +786,7 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
     for (int w = 1; w < kWaves; ++w) S += sum_buf[w];
     x.M = shift;
     x.S = S;
-    if (!(S >= 0.5 && S < 3e38)) {  // the same decision in every thread
+    if (!(S >= 0.5 && S <= 0x1p20)) {  // the same decision in every thread
       const Stat st = block_merge<kFusedThreads>(
           thread_stats<T, kFusedThreads, 2>(row, a.V, valid ? label : -1, a.k, tid), a.k, pair_buf);
       x.M = st.M;

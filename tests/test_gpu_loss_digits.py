@@ -134,3 +134,26 @@ def test_labels_of_lowest_and_infinite_logits(N, V, y):
         want = Y64[n, labels[n]] - top - np.log(np.exp(others - top).sum())
         assert abs(got["logp"][n] - want) <= 1e-4 + U * abs(want)
     assert not got["dY"][1].any() and got["row_loss"][1] == 0  # r = 0
+
+
+@pytest.mark.parametrize("y,dy", [("bfloat16", "float32"), ("float32", "float32"), ("float32", "bfloat16")])
+@pytest.mark.parametrize("N,V", WAYS)
+def test_rows_whose_first_columns_are_far_below_the_rest(N, V, y, dy):
+    """A vocabulary whose first columns are pushed down by a finite number, 40 to 95 units, and
+    small weights: no element of the gradient that is a normal number loses its digits."""
+    torch = torch_mod()
+    rng = np.random.default_rng(V - N)
+    Y, _ = _make_Y(rng, N, V, getattr(torch, y))
+    first = min(V // 2, 9000)
+    Y[:, :first] -= torch.as_tensor(40.0 + 5.0 * (np.arange(N) % 12), dtype=Y.dtype, device="cuda")[:, None]
+    Y64 = Y.double().cpu().numpy()
+    labels = rng.integers(0, V, N)
+    w = np.full(N, 1e-5, np.float32)
+    got = _run_policy(Y, labels, np.ones(N), weight=w, dY_dtype=getattr(torch, dy))
+    e, q, rel = _want(Y64, labels, 1.0)
+    _relative(got["logp"], -np.log1p(q), rel, 0.0, "logp")
+    coef = w.astype(np.float64)
+    p = np.exp(np.where(e > 0, np.log(np.maximum(e, 1e-300)) - np.log1p(q)[:, None], -np.inf))
+    want = coef[:, None] * p
+    want[np.arange(N), labels] = -coef * q / (1 + q)
+    _relative(got["dY"], want, (2 * rel + (2.0 ** -8 if dy == "bfloat16" else 0.0))[:, None], 2.0 ** -126, "dY")
