@@ -354,7 +354,8 @@ __device__ __attribute__((noinline)) PolicyResult policy_row(PolicyRow x, Policy
   const double s = p.s, w = x.weight, A = x.advantage;
   const RowLogp row = row_logp(x, s);
   const double logp = row.logp;
-  const double ratio = exp(logp - (p.own_ratio ? logp : (double)x.old_logp));
+  // this policy's own ratio is 1 at a log p of -inf too
+  const double ratio = !p.own_ratio ? exp(logp - (double)x.old_logp) : logp == logp ? 1.0 : logp;
   const double lo = 1.0 - (double)p.clip_low, hi = 1.0 + (double)p.clip_high;
   const double kept = ratio < lo ? lo : ratio > hi ? hi : ratio;  // NaN stays NaN
   const bool plain = !(kept * A < ratio * A);  // the unclipped term is the smaller one

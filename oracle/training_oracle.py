@@ -54,7 +54,7 @@ def policy_loss(Y, labels, advantage, old_logp=None, ref_logp=None, weight=None,
     q, lp = _log_softmax(Yc, np.where(on, labels, 0), inv_temperature)
     A = np.asarray(advantage, np.float64)
     with np.errstate(invalid="ignore", over="ignore"):
-        r = np.exp(lp - (lp if old_logp is None else np.asarray(old_logp, np.float64)))
+        r = np.where(np.isnan(lp), lp, 1.0) if old_logp is None else np.exp(lp - np.asarray(old_logp, np.float64))
         kept = np.minimum(np.maximum(r, 1.0 - clip_low), 1.0 + clip_high)
         plain = ~(kept * A < r * A)
         row = -np.where(plain, r * A, kept * A)

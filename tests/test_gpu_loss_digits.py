@@ -157,3 +157,19 @@ def test_rows_whose_first_columns_are_far_below_the_rest(N, V, y, dy):
     want = coef[:, None] * p
     want[np.arange(N), labels] = -coef * q / (1 + q)
     _relative(got["dY"], want, (2 * rel + (2.0 ** -8 if dy == "bfloat16" else 0.0))[:, None], 2.0 ** -126, "dY")
+
+
+@pytest.mark.parametrize("N,V", WAYS[:4])
+def test_own_policy_of_a_label_at_minus_infinity(N, V):
+    """Without old_logp the ratio is 1 in every row that has a log p, -inf among them."""
+    torch = torch_mod()
+    rng = np.random.default_rng(N + V)
+    Y, _ = _make_Y(rng, N, V, torch.float32)
+    labels = rng.integers(0, V, N)
+    Y[1, int(labels[1])] = -float("inf")
+    got = _run_policy(Y, labels, np.full(N, 2.0))
+    assert got["logp"][1] == -np.inf and (got["row_loss"] == -2.0).all() and got["loss"] == -2.0 * N
+    p = np.exp(Y[1].double().cpu().numpy())
+    want = 2.0 * p / p.sum()
+    want[labels[1]] = -2.0
+    _relative(got["dY"][1], want, 2 * U * (3 * 50 + 160), 2.0 ** -125, "dY")  # the spread is below 50 octaves

@@ -86,3 +86,10 @@ def test_backward_is_the_adjoint_of_the_forward():
     Y, dH = oracle.logits(inp.H_bits, inp.head), oracle.logits_backward(dY, inp.head, v_chunk=30)
     H = oracle.bf16_bits_to_f64(inp.H_bits)
     assert np.isclose((dY * Y).sum(), (dH * H).sum(), rtol=1e-12)
+
+
+def test_own_ratio_is_one_where_log_p_is_minus_infinity():
+    Y = np.array([[-np.inf, 0.0, 0.0], [np.nan, 0.0, 0.0]])
+    got = oracle.policy_loss(Y, np.array([0, 0]), np.array([2.0, 2.0]))
+    assert got["logp"][0] == -np.inf and got["row_loss"][0] == -2.0 and np.array_equal(got["dY"][0], [-2.0, 1.0, 1.0])
+    assert np.isnan(got["row_loss"][1]) and np.isnan(got["dY"][1]).all()
