@@ -577,12 +577,10 @@ def _scope(device, stream):
 def _scoped(call):
     """A call with a ``stream`` argument whose body runs on the current stream
     of its first tensor's device: enters _scope where that is another one."""
-    torch = _torch()
-
     @functools.wraps(call)
     def run(first, *args, stream=None, **kw):
         device = first.device
-        if stream is None and (device.type != "cuda" or device.index == torch._C._cuda_getDevice()):
+        if stream is None and (device.type != "cuda" or device.index == _torch()._C._cuda_getDevice()):
             return call(first, *args, **kw)
         with _scope(device, stream):
             return call(first, *args, **kw)
