@@ -571,6 +571,8 @@ def _scope(device, stream):
         return torch.cuda.device(device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
+    elif stream.device != device:
+        raise ValueError(f"stream must be on {device}")
     return torch.cuda.stream(stream)
 
 
