@@ -916,6 +916,40 @@ int check_words(std::initializer_list<const void*> pointers) {
   return ARCHEAD_OK;
 }
 
+// A vector of n words; null or without words it meets nothing.
+struct Words {
+  const void* p;
+  int64_t n;
+};
+bool meet(uint64_t a, uint64_t a_bytes, uint64_t b, uint64_t b_bytes) { return a < b + b_bytes && b < a + a_bytes; }
+bool meet(Words x, const void* p, uint64_t bytes) {
+  return x.p && p && x.n > 0 && bytes > 0 && meet((uint64_t)x.p, 4 * (uint64_t)x.n, (uint64_t)p, bytes);
+}
+// ... some row of a tensor
+bool meet(Words x, const archead_tensor* t) {
+  if (!t || !x.p || x.n <= 0 || t->rows <= 0) return false;
+  const uint64_t size = elem_size(t->dtype), row = (uint64_t)t->cols * size, stride = (uint64_t)t->row_stride * size;
+  const uint64_t first = (uint64_t)t->data, at = (uint64_t)x.p;
+  const uint64_t i = at < first + row ? 0 : (at - first - row) / stride + 1;  // the first row that ends behind its start
+  return i < (uint64_t)t->rows && meet(at, 4 * (uint64_t)x.n, first + i * stride, row);
+}
+
+// Kernels read the vectors while others write: no output may share bytes with
+// another vector or the logits, and no vector with the gradient or the workspace.
+int check_apart(const archead_tensor* Y, const archead_tensor* dY, std::initializer_list<Words> in,
+                std::initializer_list<Words> out, const void* ws, uint64_t ws_bytes) {
+  for (const Words* x = out.begin(); x != out.end(); ++x) {
+    for (const Words& y : in)
+      if (meet(*x, y.p, 4 * (uint64_t)y.n)) return ARCHEAD_E_SHAPE;
+    for (const Words* y = out.begin(); y != x; ++y)
+      if (meet(*x, y->p, 4 * (uint64_t)y->n)) return ARCHEAD_E_SHAPE;
+    if (meet(*x, Y) || meet(*x, dY) || meet(*x, ws, ws_bytes)) return ARCHEAD_E_SHAPE;
+  }
+  for (const Words& x : in)
+    if (meet(x, dY) || meet(x, ws, ws_bytes)) return ARCHEAD_E_SHAPE;
+  return ARCHEAD_OK;
+}
+
 int check_workspace(const void* ws, uint64_t bytes, uint64_t need) {
   if (!ws) return ARCHEAD_E_NULL;
   if ((uintptr_t)ws % ARCHEAD_ALIGNMENT) return ARCHEAD_E_ALIGN;
@@ -1078,7 +1112,12 @@ int archead_policy_loss(const archead_tensor* Y, const archead_policy_inputs* in
   if (int rc = check_words({in->labels, in->weight, in->old_logp, in->ref_logp, in->advantage, out->loss, out->logp,
                             out->row_loss}))
     return rc;
-  const LossWorkspace W = loss_workspace(Y->rows, Y->cols, 0);
+  const int64_t N = Y->rows;
+  const LossWorkspace W = loss_workspace(N, Y->cols, 0);
+  if (int rc = check_apart(Y, out->dY,
+                           {{in->labels, N}, {in->advantage, N}, {in->old_logp, N}, {in->ref_logp, N}, {in->weight, N}},
+                           {{out->loss, 1}, {out->logp, N}, {out->row_loss, N}}, workspace, W.total))
+    return rc;
   if (W.total > 0)
     if (int rc = check_workspace(workspace, workspace_bytes, W.total)) return rc;
   if (Y->rows == 0 && !out->loss) return ARCHEAD_OK;
@@ -1115,7 +1154,13 @@ int archead_preference_loss(const archead_tensor* Y, const archead_preference_in
   if (int rc = check_words({in->labels, in->weight, in->ref_logp, in->offsets, in->pair_weight, out->loss, out->logp,
                             out->chosen_reward, out->rejected_reward}))
     return rc;
-  const LossWorkspace W = loss_workspace(Y->rows, Y->cols, in->n_pairs);
+  const int64_t N = Y->rows, B = in->n_pairs;
+  const LossWorkspace W = loss_workspace(N, Y->cols, B);
+  if (int rc = check_apart(
+          Y, out->dY,
+          {{in->labels, N}, {in->offsets, 2 * B + 1}, {in->ref_logp, N}, {in->weight, N}, {in->pair_weight, B}},
+          {{out->loss, 1}, {out->logp, N}, {out->chosen_reward, B}, {out->rejected_reward, B}}, workspace, W.total))
+    return rc;
   if (W.total > 0)
     if (int rc = check_workspace(workspace, workspace_bytes, W.total)) return rc;
   if (Y->rows == 0 && in->n_pairs == 0 && !out->loss) return ARCHEAD_OK;

@@ -499,8 +499,10 @@ ARCHEAD_API int archead_logits_topk(const archead_tensor* H, const archead_packe
  * or +inf, or with nothing above -inf has log p NaN, and so have the loss and
  * its gradient.  Logits of -inf have probability 0.
  * dY may be Y itself (same data, dtype and stride: the gradient replaces the
- * logits); otherwise the two must not overlap (E_SHAPE).  Sums of the losses
- * and all per-row arithmetic are fp64, exponentials fp32; bf16
+ * logits); otherwise the two must not overlap (E_SHAPE).  An output vector
+ * may not share bytes with another vector, the logits, the gradient or the
+ * workspace, nor an input vector with the last two (E_SHAPE).  Sums of the
+ * losses and all per-row arithmetic are fp64, exponentials fp32; bf16
  * gradients are rounded to nearest even from fp32.  Two calls with the same
  * arguments give the same bits.  Calls that may run at the same time (other
  * streams, other threads, captured graphs) need a workspace each. */
