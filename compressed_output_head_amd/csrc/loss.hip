@@ -240,9 +240,18 @@ __device__ __forceinline__ u4 without(u4 v, int j) {
   return v;
 }
 
+// The largest logit of a chunk; NaN is passed over (it is in the sum).
+template <typename T>
+__device__ __forceinline__ float chunk_max(const u4& v) {
+  float top = Elem<T>::at(v, 0);
+#pragma unroll
+  for (int j = 1; j < Elem<T>::kPer16; ++j) top = fmaxf(top, Elem<T>::at(v, j));
+  return top;
+}
+
 // (M, S) of the elements [0, len) at p but that at `label` (none where it is
 // negative), the share of thread tid of kThreads.
-template <typename T, int kThreads, int kUnroll = kRowUnroll>
+template <typename T, int kThreads>
 __device__ __forceinline__ Stat thread_stats(const T* p, int64_t len, int64_t label, Scale k, int tid) {
   using E = Elem<T>;
   const int64_t full = len / E::kPer16;
@@ -255,33 +264,27 @@ __device__ __forceinline__ Stat thread_stats(const T* p, int64_t len, int64_t la
       M = M0 = top;
     }
   };
-  for (int64_t c0 = tid; c0 < full; c0 += kThreads * kUnroll) {
-    u4 v[kUnroll];
+  for (int64_t c0 = tid; c0 < full; c0 += kThreads * kRowUnroll) {
+    u4 v[kRowUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kRowUnroll; ++u) {
       const int64_t c = c0 + u * kThreads;
       v[u] = c < full ? u4(*reinterpret_cast<const u4_any*>(p + c * E::kPer16))
                       : u4{E::kNegInf2, E::kNegInf2, E::kNegInf2, E::kNegInf2};
     }
-    if (label_chunk >= c0 && label_chunk < c0 + kThreads * kUnroll) {
+    if (label_chunk >= c0 && label_chunk < c0 + kThreads * kRowUnroll) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
+      for (int u = 0; u < kRowUnroll; ++u)
         if (c0 + u * kThreads == label_chunk) v[u] = without<T>(v[u], (int)(label % E::kPer16));
     }
     float top = M;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-      for (int j = 0; j < E::kPer16; ++j) top = fmaxf(top, E::at(v[u], j));
+    for (int u = 0; u < kRowUnroll; ++u) top = fmaxf(top, chunk_max<T>(v[u]));
     rise(top);
-    float add[kUnroll];
+    float add[kRowUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) add[u] = chunk_sum<T>(v[u], M0, k);
-#pragma unroll
-    for (int w = kUnroll / 2; w > 0; w >>= 1)
-#pragma unroll
-      for (int u = 0; u < w; ++u) add[u] += add[u + w];
-    S += (double)add[0];
+    for (int u = 0; u < kRowUnroll; ++u) add[u] = chunk_sum<T>(v[u], M0, k);
+    S += (double)((add[0] + add[1]) + (add[2] + add[3]));
   }
   const int64_t i = full * E::kPer16 + tid;  // fewer than 8 elements are left
   if (i < len && i != label) {
@@ -697,12 +700,14 @@ __global__ __launch_bounds__(kOrderThreads) void row_order_kernel(const RowArgs 
 // row's chunks between the stores of the row before it; two workgroups a CU
 // with half the registers each took 0.64 ms or more.
 //
-// What is subtracted in the exponents is the maximum of the row's first
-// kFusedThreads chunks without the label: S >= 1 as those chunks are in it.  A
-// row whose S passes 2^20 (logits about as many octaves above them), or whose
-// first chunks are -inf, is summed again with running maxima: the coefficient
-// over S has to stay a normal number for the gradient's other elements, and
-// the exponential of many octaves has fewer digits.
+// What is subtracted in the exponents is the maximum without the label of two
+// rounds of chunks, the first and one further on (a vocabulary may have its
+// first columns masked): S >= 1 as those chunks are in it.  A row whose S
+// passes 2^20 (logits about as many octaves above them), or which is -inf
+// there, is summed again by its own maximum: the coefficient over S has to stay
+// a normal number for the gradient's other elements, and the exponential of
+// many octaves has fewer digits.  (By its own maximum in the first place, a
+// pass more over the registers, the rows above take 0.57 ms.)
 // A bf16 gradient leaves the low part of k out, 2^-23 of the exponent at most.
 template <typename T, typename G>
 __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowArgs a) {
@@ -756,9 +761,7 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
         if (label_chunk / kFusedThreads == c && label_chunk % kFusedThreads == tid) v[c] = without<T>(v[c], label_at);
     }
     if (label_chunk == full && tid == label_at) y_rest = -INFINITY;
-    float top = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < n16; ++j) top = fmaxf(top, E::at(v[0], j));
+    float top = fmaxf(chunk_max<T>(v[0]), chunk_max<T>(v[kHeld / 2 - 1]));  // every row has these
     for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
     if (lane == 0) top_buf[wave] = top;
     __syncthreads();
@@ -774,11 +777,12 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
       // would take twice the registers that a row has
       asm volatile("" : "+v"(v[c]));
     }
-    for (int64_t c = kHeld * kFusedThreads + tid; c < full; c += kFusedThreads) {
-      u4 y = u4(*reinterpret_cast<const u4_any*>(row + c * n16));
-      if (c == label_chunk) y = without<T>(y, label_at);
-      S += (double)chunk_sum<T>(y, shift, a.k);
-    }
+    auto tail_chunk = [&](int64_t c) {
+      const u4 y = u4(*reinterpret_cast<const u4_any*>(row + c * n16));
+      return c == label_chunk ? without<T>(y, label_at) : y;
+    };
+    for (int64_t c = kHeld * kFusedThreads + tid; c < full; c += kFusedThreads)
+      S += (double)chunk_sum<T>(tail_chunk(c), shift, a.k);
     for (int o = 32; o > 0; o >>= 1) S += __shfl_xor(S, o);
     if (lane == 0) sum_buf[wave] = S;
     __syncthreads();
@@ -788,8 +792,29 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
     x.M = shift;
     x.S = S;
     if (!(S >= 0.5 && S <= 0x1p20)) {  // the same decision in every thread
-      const Stat st = block_merge<kFusedThreads>(
-          thread_stats<T, kFusedThreads, 2>(row, a.V, valid ? label : -1, a.k, tid), a.k, pair_buf);
+      Stat st{0.0, y_rest};
+#pragma unroll
+      for (int c = 0; c < kHeld; ++c) {
+        st.M = fmaxf(st.M, chunk_max<T>(v[c]));
+        asm volatile("" : "+v"(v[c]));
+      }
+      float shift = shift_of(st.M);
+      st.S = exp_at(y_rest - shift, a.k);
+#pragma unroll
+      for (int c = 0; c < kHeld; ++c) {
+        st.S += (double)chunk_sum<T>(v[c], shift, a.k);
+        asm volatile("" : "+v"(v[c]));
+      }
+      for (int64_t c = kHeld * kFusedThreads + tid; c < full; c += kFusedThreads) {
+        const u4 y = tail_chunk(c);
+        const float top = chunk_max<T>(y);
+        if (top > st.M) {
+          st.S *= (double)exp_at(st.M - top, a.k);
+          st.M = shift = top;
+        }
+        st.S += (double)chunk_sum<T>(y, shift, a.k);
+      }
+      st = block_merge<kFusedThreads>(st, a.k, pair_buf);
       x.M = st.M;
       x.S = st.S;
     }

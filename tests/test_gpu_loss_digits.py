@@ -173,3 +173,38 @@ def test_own_policy_of_a_label_at_minus_infinity(N, V):
     want = 2.0 * p / p.sum()
     want[labels[1]] = -2.0
     _relative(got["dY"][1], want, 2 * U * (3 * 50 + 160), 2.0 ** -125, "dY")  # the spread is below 50 octaves
+
+
+@pytest.mark.parametrize("what", ["finite mask", "mask", "one column"])
+@pytest.mark.parametrize("y,dy", [("bfloat16", "float32"), ("float32", "bfloat16")])
+@pytest.mark.parametrize("N,V", WAYS[3:])
+def test_rows_whose_largest_logits_are_in_their_last_columns(N, V, y, dy, what):
+    """Nine tenths of the columns 14 to 95 units below the rest, or at -inf; or one column, which is
+    not the label's, so far above all others."""
+    torch = torch_mod()
+    rng = np.random.default_rng(V + N)
+    Y, _ = _make_Y(rng, N, V, getattr(torch, y))
+    first = V - V // 10
+    by = torch.as_tensor(np.array([14.0, 20.0, 30.0, 50.0, 70.0, 80.0, 88.0, 95.0])[np.arange(N) % 8], dtype=Y.dtype,
+                         device="cuda")
+    if what == "one column":
+        Y[:, V - 3] = by
+    else:
+        Y[:, :first] -= by[:, None]
+        if what == "mask":
+            Y[:, :first] = -float("inf")
+    Y64 = Y.double().cpu().numpy()
+    labels = rng.integers(first, V - 3, N)
+    w = np.full(N, 1e-5, np.float32)
+    got = _run_policy(Y, labels, np.ones(N), weight=w, dY_dtype=getattr(torch, dy))
+    top = Y64.max(1, keepdims=True)
+    e = np.exp(Y64 - top)
+    p = e / e.sum(1, keepdims=True)
+    n = np.arange(N)
+    logp = (Y64 - top)[n, labels] - np.log(e.sum(1))
+    finite = np.where(np.isfinite(Y64), Y64, np.nan)
+    rel = U * (3 * np.minimum((np.nanmax(finite, 1) - np.nanmin(finite, 1)) / np.log(2), 150.0) + 160)
+    _relative(got["logp"], logp, U, rel, "logp")
+    want = w[:, None].astype(np.float64) * p
+    want[n, labels] -= w
+    _relative(got["dY"], want, (2 * rel + (2.0 ** -8 if dy == "bfloat16" else 0.0))[:, None], 2.0 ** -126, "dY")
