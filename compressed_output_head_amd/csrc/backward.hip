@@ -6,10 +6,11 @@
 // the row scales go to the gradient's side, and the integers q4 c8 (below
 // 2048) and the INT8 codes are exact fp16 operands of the 32 x 32 x 16 MFMA.
 // dY s is rounded to fp16 after scaling its row by a power of two that brings
-// the row's largest product to [2^14, 2^15): 2^-12 of an element, a quarter
-// of the half step of the bf16 result, and independent from one vocabulary
-// entry to the next.  The scale is taken from the products themselves, so a
-// gradient that sits on vocabulary entries of tiny scales keeps its digits.
+// the row's largest product to [2^14, 2^15): 2^-11 of an element at most, an
+// eighth of the half step of the bf16 result, and independent from one
+// vocabulary entry to the next.  (A pair of fp16 numbers would keep 22 bits,
+// for twice the MFMAs and fragments.)  The scale is taken from the products
+// themselves, so a gradient that sits on vocabulary entries of tiny scales keeps its digits.
 //
 //   bwd_max_kernel     per row: the largest |dY s_R|, |dY s_Ac|, |dY s_Aw|;
 //                      beside that, the A codes in operand order (few
@@ -795,7 +796,7 @@ __device__ __forceinline__ void few_ranks(const BwdArgs& a, FewShared& sm, int t
 // packed tiles of its own (16 vocabulary rows, one MFMA step) and the step's
 // dY fragment, turns them in 4 KB of LDS that no other wave reads, and keeps
 // the sums of all the tokens and columns; the waves' sums are added at the
-// end.  A rank tile's codes come in operand order already.
+// end.  A rank tile's codes are read as they are stored and turned the same way.
 // 32 tokens of a 151936 x 4096 head: 84 us; the accumulators leave registers
 // for four tiles in flight a wave, and none for operands that wait while the
 // next tile is unpacked.  The group codes as stored cost 11 us more, a ring
@@ -1157,7 +1158,8 @@ __global__ __launch_bounds__(kFinishThreads) void bwd_finish_kernel(const BwdArg
 }
 
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
-// v as the sum of two bf16 numbers, to 2^-18 of it.
+// v as the sum of two bf16 numbers, to 2^-17 of it: v in [2^e, 2^(e+1)) leaves
+// at most 2^(e-8) to lo, whose own half step is 2^(e-17) below that.
 struct Bf16Pair {
   bf8 hi, lo;
 };
@@ -1173,7 +1175,9 @@ __device__ __forceinline__ Bf16Pair split_bf16(const float (&v)[8]) {
 
 // Many rows: 32 rows x 128 columns of dH a wave, Z B on the bf16 MFMA with Z
 // and B as pairs of bf16 numbers (three products; bf16 has fp32's range, so
-// neither needs a scale).  Tile c of four holds the columns 4 i + c, so that
+// neither needs a scale).  What the pairs and the fourth product, of two lo's,
+// leave out is 2^-17 + 2^-17 + 2^-16 = 2^-15 of |Z| |B| at most, a sixteenth of
+// what Z has from dY's fp16.  Tile c of four holds the columns 4 i + c, so that
 // a lane has four neighbouring ones of a row: whole lines of the parts, of B
 // and of dH.  (4096 rows of 4096 columns, 128 ranks: 47 us, and 107 with fp32
 // products; 256 rows of 8192 columns, 8 parts: 22 and 25.)

@@ -695,7 +695,7 @@ __global__ __launch_bounds__(kOrderThreads) void row_order_kernel(const RowArgs 
 // loaded into the registers that the gradient's stores free.  The rest of a
 // row is read again from the cache.  On 4096 rows of 151936 bf16 logits (a
 // tenth of them left out), 0.52 ms: 4.5 TB/s of the bytes it cannot do
-// without, against 0.66 ms for the kernels above, which read all rows twice.
+// without, against 0.63 ms for the kernels above, which read all rows twice.
 // Holding the whole row (18 chunks) took 0.54 to 0.59 ms, and so did summing a
 // row's chunks between the stores of the row before it; two workgroups a CU
 // with half the registers each took 0.64 ms or more.
@@ -1041,11 +1041,17 @@ hipError_t launch_gradient(const RowArgs& a, const archead_tensor* dY, hipStream
 // The fused kernel: a row for every CU, and rows that fill half of the chunks
 // held.  Of bf16 rows in between one round of the CUs and eight it would leave
 // part of them idle in the last round, and the split kernels' second read comes
-// from the cache.  (Microseconds of the fused and of the split kernels, 3/4 of
-// the rows counting, 151936 bf16 logits: 256 rows 40 and 44, 300 43 and 49, 400
-// 73 and 61, 512 81 and 77, 768 113 and 102, 1024 121 and 127, 1500 195 and 190,
-// 4096 518 and 627; 100003 fp32 logits: 256 rows 44 and 47, 400 73 and 67, 512
-// 82 and 86, 1024 156 and 168.)
+// from the cache.  How full the last round is goes by the rows that count,
+// which the host does not know; the rule is the one for 3/4 of them.
+// (Microseconds of the fused and of the split kernels there, 151936 bf16
+// logits: 256 rows 40 and 46, 320 45 and 52, 400 74 and 63, 512 82 and 76, 640
+// 87 and 93, 768 115 and 103, 1024 123 and 129, 1280 160 and 165, 1536 198 and
+// 198, 2048 237 and 269, 4096 460 and 567; 100003 fp32 logits: 256 rows 42 and
+// 44, 320 50 and 50, 400 76 and 61, 512 82 and 77, 640 92 and 93, 768 120 and
+// 108, 1024 133 and 144, 1536 213 and 228, 2048 266 and 314, 4096 514 and 665.
+// So the rule is 5% off at 640, 1024 and 1280 bf16 rows, and 7 to 25% at 400 to
+// 768 fp32 rows but 640.  All rows counting: 300 rows 69 and 57, 512 85 and 90,
+// 1024 154 and 157; half of them: 512 55 and 62, 1024 105 and 112.)
 bool fused_takes(const RowArgs& a, int64_t size) {
   if (size == 2 && a.N > kFusedLeastRows * 5 / 4 && a.N < kFusedLeastRows * 8) return false;
   return a.N >= kFusedLeastRows && a.V * size >= kHeldChunks / 2 * kFusedThreads * 16 && a.V < (int64_t(1) << 30);

@@ -497,7 +497,8 @@ ARCHEAD_API int archead_logits_topk(const archead_tensor* H, const archead_packe
  * hold anything, their labels too), their log p and loss are 0 and their
  * gradient is 0.  A row that counts with a label outside [0, V), with a NaN
  * or +inf, or with nothing above -inf has log p NaN, and so have the loss and
- * its gradient.  Logits of -inf have probability 0.
+ * its gradient.  Logits of -inf have probability 0; a label there has log p
+ * -inf.
  * dY may be Y itself (same data, dtype and stride: the gradient replaces the
  * logits); otherwise the two must not overlap (E_SHAPE).  An output vector
  * may not share bytes with another vector, the logits, the gradient or the
@@ -510,8 +511,9 @@ ARCHEAD_API int archead_logits_topk(const archead_tensor* H, const archead_packe
 /* Device workspace of a loss call: n_rows rows of V logits, n_pairs pairs (0
  * for the policy loss).  0 for calls of at most 64 rows, 64 pairs and 65536
  * logits in all; else 16 bytes per row and piece (at most 64 pieces a row), 32
- * per row and 4 more, 8 per pair, each section rounded up to 256 bytes.  Pure
- * host arithmetic.  E_NULL, E_SHAPE, E_UNSUPPORTED (n_rows or n_pairs above
+ * per row and 4 more, 8 per pair, each section rounded up to 256 bytes.  A call
+ * of fewer rows may need more (they are cut into more pieces): ask for every
+ * number of rows that a workspace is kept for.  Pure host arithmetic.  E_NULL, E_SHAPE, E_UNSUPPORTED (n_rows or n_pairs above
  * 2^22, V of 2^31 or more). */
 ARCHEAD_API int archead_loss_workspace_bytes(int64_t n_rows, int64_t V, int64_t n_pairs, uint64_t* bytes);
 
@@ -605,7 +607,9 @@ ARCHEAD_API int archead_preference_loss(const archead_tensor* Y, const archead_p
  * its low-rank part, the A codes in operand order, and row scales; up to 32
  * rows instead three sets of operands, without rounding the rows up, and the
  * group codes.  A call of more rows may leave fewer than 4096 to its last
- * pass, which this covers.  Pure host arithmetic.  E_NULL, E_DIMS, E_SHAPE,
+ * pass, which this covers; a call of fewer rows may need more (its vocabulary
+ * is split further): ask for every number of rows that a workspace is kept
+ * for.  Pure host arithmetic.  E_NULL, E_DIMS, E_SHAPE,
  * E_UNSUPPORTED. */
 ARCHEAD_API int archead_logits_backward_workspace_bytes(const archead_dims* d, int64_t n_tokens, uint64_t* bytes);
 
