@@ -49,3 +49,19 @@ def test_largest_ranks_with_tens_of_rows(N, V, D, r_c, r_r, g):
     h, head = _head(V, V, D, r_c, r_r, g)
     dY = torch.as_tensor(_gradient(np.random.default_rng(N), N, V), device="cuda").bfloat16()
     _check(head, h, dY, f"N={N} r={r_c}+{r_r} g={g}")
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("V", [130, 1500])
+@pytest.mark.parametrize("more", [1, 4, 17, 32])
+def test_a_last_pass_of_few_rows(more, V, dtype):
+    """Rows past 4096 are a pass of their own: as a call of those rows alone."""
+    torch = torch_mod()
+    ah = ah_mod()
+    _, head = _head(V, V, 256, 8, 8, 64)
+    gen = torch.Generator(device="cuda").manual_seed(more)
+    dY = torch.randn((4096 + more, V), generator=gen, device="cuda").to(getattr(torch, dtype))
+    got = ah.archead_logits_backward(dY, head)
+    assert torch.equal(got[:4096], ah.archead_logits_backward(dY[:4096], head))
+    assert torch.equal(got[4096:], ah.archead_logits_backward(dY[4096:], head))
+    assert torch.isfinite(got.float()).all() and got[4096:].any(1).all()
