@@ -846,7 +846,7 @@ __global__ __launch_bounds__(kFusedThreads) void policy_fused_kernel(const RowAr
       __builtin_amdgcn_sched_barrier(0);
     }
     for (int64_t c = kHeld * kFusedThreads; c + tid < full; c += kFusedThreads)
-      put(*reinterpret_cast<const u4_any*>(row + (c + tid) * n16), out + c * n16);
+      put(u4(*reinterpret_cast<const u4_any*>(row + (c + tid) * n16)), out + c * n16);
     if (tid < rest) out[(int64_t)full * n16 + tid] = Elem<G>::from(g.neg * exp_at(y_rest - g.M, a.k));
     // the label's element, by the thread that wrote it
     if (valid && tid == (label_chunk < full ? label_chunk % kFusedThreads : label_at)) out[label] = Elem<G>::from(g.label_g);
