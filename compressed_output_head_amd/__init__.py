@@ -19,7 +19,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libarchead.so")
 
 ARCHEAD_OK = 0
-ARCHEAD_BF16, ARCHEAD_F32 = 1, 2
+ARCHEAD_BF16, ARCHEAD_F32, ARCHEAD_I8 = 1, 2, 3
 ARCHEAD_PATH_AUTO, ARCHEAD_PATH_DECODE, ARCHEAD_PATH_TILE = 0, 1, 2
 # storage formats (archead_format): the method's head and the two comparison heads
 ARCHEAD_FMT_ARCHEAD, ARCHEAD_FMT_GROUP_INT4, ARCHEAD_FMT_ROW_INT8 = 0, 1, 2
@@ -37,6 +37,8 @@ EXPORTS = ("archead_pack_layout", "archead_workspace_bytes", "archead_workspace_
            "archead_fit_workspace_bytes", "archead_fit", "archead_logit_error_workspace_bytes",
            "archead_logit_error", "archead_loss_workspace_bytes", "archead_policy_loss", "archead_preference_loss",
            "archead_logits_backward_workspace_bytes", "archead_logits_backward",
+           "archead_rmsnorm", "archead_rmsnorm_backward_workspace_bytes", "archead_rmsnorm_backward",
+           "archead_logits_int8_workspace_bytes", "archead_logits_int8",
            "archead_status_string", "archead_format_version")
 
 
@@ -126,6 +128,25 @@ class ArcheadPreferenceOutputs(ctypes.Structure):
                 ("rejected_reward", ctypes.c_void_p), ("dY", ctypes.POINTER(ArcheadTensor))]
 
 
+class ArcheadRmsnormInputs(ctypes.Structure):
+    _fields_ = [("x", ctypes.POINTER(ArcheadTensor)), ("residual", ctypes.POINTER(ArcheadTensor)),
+                ("weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class ArcheadRmsnormOutputs(ctypes.Structure):
+    _fields_ = [("sum", ctypes.POINTER(ArcheadTensor)), ("h", ctypes.POINTER(ArcheadTensor)),
+                ("codes", ctypes.POINTER(ArcheadTensor)), ("scale", ctypes.c_void_p), ("inv_rms", ctypes.c_void_p)]
+
+
+class ArcheadRmsnormGradInputs(ctypes.Structure):
+    _fields_ = [("dh", ctypes.POINTER(ArcheadTensor)), ("sum", ctypes.POINTER(ArcheadTensor)),
+                ("inv_rms", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("dsum", ctypes.POINTER(ArcheadTensor))]
+
+
+class ArcheadRmsnormGradOutputs(ctypes.Structure):
+    _fields_ = [("dx", ctypes.POINTER(ArcheadTensor)), ("dweight", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python compressed_output_head_amd/build.py`")
@@ -170,6 +191,13 @@ def _load():
                                             ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]
     lib.archead_logits_backward_workspace_bytes.argtypes = [P(ArcheadDims), ctypes.c_int64, P(ctypes.c_uint64)]
     lib.archead_logits_backward.argtypes = [P(ArcheadTensor), P(ArcheadPackedHead), P(ArcheadTensor), ctypes.c_void_p]
+    lib.archead_rmsnorm.argtypes = [P(ArcheadRmsnormInputs), P(ArcheadRmsnormOutputs), ctypes.c_void_p]
+    lib.archead_rmsnorm_backward_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64, P(ctypes.c_uint64)]
+    lib.archead_rmsnorm_backward.argtypes = [P(ArcheadRmsnormGradInputs), P(ArcheadRmsnormGradOutputs),
+                                             ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]
+    lib.archead_logits_int8_workspace_bytes.argtypes = [P(ArcheadDims), ctypes.c_int64, P(ctypes.c_uint64)]
+    lib.archead_logits_int8.argtypes = [P(ArcheadTensor), ctypes.c_void_p, P(ArcheadPackedHead), P(ArcheadTensor),
+                                        ctypes.c_void_p]
     lib.archead_status_string.argtypes = [ctypes.c_int]
     lib.archead_status_string.restype = ctypes.c_char_p
     lib.archead_format_version.argtypes = []
@@ -352,7 +380,8 @@ def _tensor(t) -> ArcheadTensor:
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError("expected a 2-D tensor with unit column stride")
     dtype, (rows, cols) = t.dtype, t.shape
-    code = ARCHEAD_BF16 if dtype is torch.bfloat16 else ARCHEAD_F32 if dtype is torch.float32 else 0
+    code = ARCHEAD_BF16 if dtype is torch.bfloat16 else ARCHEAD_F32 if dtype is torch.float32 else \
+        ARCHEAD_I8 if dtype is torch.int8 else 0
     return ArcheadTensor(t.data_ptr(), rows, cols, t.stride(0), code)
 
 
@@ -746,3 +775,132 @@ def archead_logits_backward(dY, head: PackedHead, dH=None, workspace=None):
     if status:
         _check(status, "archead_logits_backward")
     return dH
+
+
+# ------------------------------------------------------- in front of the head ---
+
+def _rows(t, name: str, device):
+    """Pointer to the struct of a 2-D device tensor (None for None)."""
+    if t is None:
+        return None
+    if t.get_device() != device.index or device.type != "cuda":
+        raise ValueError(f"{name} must be on {device}")
+    return ctypes.pointer(_tensor(t))
+
+
+@_scoped
+def archead_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, outputs=("h",), sum=None, h=None, codes=None):
+    """Root-mean-square norm of s = x + residual (bf16 [N, D]; weight: bf16
+    [D], None: 1).  Returns a dict of device tensors of the wanted `outputs`:
+    "h" (bf16 [N, D]), "codes" and "scale" (int8 [N, D] and fp32 [N], whose
+    product stands for h; each brings the other), "inv_rms" (fp32 [N], for the
+    gradient), and "sum" (bf16 [N, D]), which is always among them with a
+    residual.  sum, h, codes: tensors to write instead of new ones (sum or h
+    may be x or residual).  stream: a torch stream or a raw handle (None: the
+    current one)."""
+    torch = _torch()
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("x must be a device tensor")
+    xt = _tensor(x)
+    N, D = x.shape
+    wanted = set(outputs)
+    if not wanted <= {"sum", "h", "codes", "scale", "inv_rms"}:
+        raise ValueError("outputs are among sum, h, codes, scale, inv_rms")
+    out = {}
+    if residual is not None or sum is not None or "sum" in wanted:
+        out["sum"] = torch.empty_like(x, memory_format=torch.contiguous_format) if sum is None else sum
+    if h is not None or "h" in wanted:
+        out["h"] = torch.empty_like(x, memory_format=torch.contiguous_format) if h is None else h
+    if codes is not None or wanted & {"codes", "scale"}:
+        out["codes"] = torch.empty((N, D), dtype=torch.int8, device=dev) if codes is None else codes
+        out["scale"] = torch.empty(N, dtype=torch.float32, device=dev)
+    if "inv_rms" in wanted:
+        out["inv_rms"] = torch.empty(N, dtype=torch.float32, device=dev)
+    inp = ArcheadRmsnormInputs(ctypes.pointer(xt), _rows(residual, "residual", dev),
+                               _vec(weight, "weight", torch.bfloat16, D, dev), eps)
+    outs = ArcheadRmsnormOutputs(_rows(out.get("sum"), "sum", dev), _rows(out.get("h"), "h", dev),
+                                 _rows(out.get("codes"), "codes", dev),
+                                 *(out[k].data_ptr() if k in out else None for k in ("scale", "inv_rms")))
+    status = lib.archead_rmsnorm(inp, outs, _raw_stream(dev))
+    if status:
+        _check(status, "archead_rmsnorm")
+    return out
+
+
+def archead_rmsnorm_backward_workspace_bytes(n_rows: int, D: int) -> int:
+    out = ctypes.c_uint64(0)
+    _check(lib.archead_rmsnorm_backward_workspace_bytes(int(n_rows), int(D), ctypes.byref(out)),
+           "archead_rmsnorm_backward_workspace_bytes")
+    return out.value
+
+
+_rmsnorm_backward_workspace_bytes = functools.lru_cache(maxsize=256)(archead_rmsnorm_backward_workspace_bytes)
+
+
+@_scoped
+def archead_rmsnorm_backward(dh, sum, inv_rms, weight=None, dsum=None, dx=None, with_dweight: bool = True,
+                             workspace=None):
+    """Gradient of archead_rmsnorm: dh (bf16 [N, D]) arrives at h, dsum (None:
+    0) at the sum by the residual stream; sum and inv_rms as the forward pass
+    gave them (sum is x where there was no residual).  Returns a dict of "dx"
+    (bf16 [N, D], the gradient of x and of the residual alike; the given tensor,
+    which may be dh, sum or dsum, or a new one) and, with_dweight, "dweight"
+    (fp32 [D]).  stream: a torch stream or a raw handle (None: the current
+    one)."""
+    torch = _torch()
+    dev = dh.device
+    if dev.type != "cuda":
+        raise ValueError("dh must be a device tensor")
+    g = _tensor(dh)
+    N, D = dh.shape
+    if dx is None:
+        dx = torch.empty_like(dh, memory_format=torch.contiguous_format)
+    out = {"dx": dx}
+    ws = None
+    if with_dweight:
+        out["dweight"] = torch.empty(D, dtype=torch.float32, device=dev)
+        ws = _workspace(workspace, _rmsnorm_backward_workspace_bytes(N, D), dev)
+    inp = ArcheadRmsnormGradInputs(ctypes.pointer(g), _rows(sum, "sum", dev),
+                                   _vec(inv_rms, "inv_rms", torch.float32, N, dev),
+                                   _vec(weight, "weight", torch.bfloat16, D, dev), _rows(dsum, "dsum", dev))
+    outs = ArcheadRmsnormGradOutputs(_rows(dx, "dx", dev), out["dweight"].data_ptr() if with_dweight else None)
+    status = lib.archead_rmsnorm_backward(inp, outs, *_span(ws), _raw_stream(dev))
+    if status:
+        _check(status, "archead_rmsnorm_backward")
+    return out
+
+
+def archead_logits_int8_workspace_bytes(V, D, g, n_tokens: int, fmt=ARCHEAD_FMT_ROW_INT8) -> int:
+    out = ctypes.c_uint64(0)
+    _check(lib.archead_logits_int8_workspace_bytes(ctypes.byref(_dims(V, D, 0, 0, g, fmt)), int(n_tokens),
+                                                   ctypes.byref(out)), "archead_logits_int8_workspace_bytes")
+    return out.value
+
+
+_int8_workspace_bytes = functools.lru_cache(maxsize=256)(archead_logits_int8_workspace_bytes)
+
+
+@_scoped
+def archead_logits_int8(codes, scale, head: PackedHead, Y=None, out_dtype=None, workspace=None):
+    """Logits of INT8 hidden states (codes: int8 [N, D], scale: fp32 [N], as
+    archead_rmsnorm gives them) through a row-INT8 head, as a product of 8-bit
+    integers.  Returns Y: the given tensor, or a new one of out_dtype (fp32 by
+    default).  stream: a torch stream or a raw handle (None: the current one)."""
+    torch = _torch()
+    dev = head.buffer.device
+    if codes.device != dev or (Y is not None and Y.device != dev):
+        raise ValueError("codes and Y must be on the head's device")
+    x = _tensor(codes)
+    N = codes.shape[0]
+    if Y is None:
+        Y = torch.empty((N, head.V), dtype=out_dtype or torch.float32, device=dev)
+    elif out_dtype is not None and out_dtype != Y.dtype:
+        raise ValueError("Y must be of out_dtype")
+    ws = _workspace(workspace, _int8_workspace_bytes(head.V, head.D, head.g, N, head.fmt), dev)
+    p = ArcheadPackedHead(_dims(head.V, head.D, head.r_c, head.r_r, head.g, head.fmt), head.buffer.data_ptr(),
+                          head.buffer.numel(), *_span(ws))
+    status = lib.archead_logits_int8(x, _vec(scale, "scale", torch.float32, N, dev), p, _tensor(Y), _raw_stream(dev))
+    if status:
+        _check(status, "archead_logits_int8")
+    return Y

@@ -1,0 +1,492 @@
+// The norm in front of the head, and its gradient (archead_rmsnorm,
+// archead_rmsnorm_backward).  With s = bf16(x + residual), the sum that the
+// residual stream keeps, and inv = 1 / sqrt(sum_d s_d^2 / D + eps),
+//   h_d = s_d inv w_d,
+// in bf16, or in 8 bits with a scale for the row:
+//   code_d = rint(127 t_d / m), scale = m inv / 127,  t = s w, m = max_d |t_d|.
+// The factor inv cancels in the codes, and t is exact in fp32 (8 bits times 8
+// bits).  The quotient rounded to fp32 decides as the exact one does: with
+// t = T 2^a and m = M 2^b (T, M below 2^16) it misses a border (2k + 1) / 2,
+// where it does not meet it, by 1 / (2^(b-a+1) M) at least, and a quotient of
+// 1/2 or more has 2^(b-a) M <= 254 T: 1 / (508 T) > 2^-25, half a step of fp32
+// there (both grow alike from 1/2 up).
+//
+// One pass: a row is read once, held in registers from the sums to the
+// outputs.  Bound by HBM where rows are many, by the launch where they are few.
+#include <algorithm>
+
+#include "device_common.h"
+#include "internal.h"
+
+namespace archead {
+
+namespace {
+
+constexpr int64_t kNormMaxRows = int64_t(1) << 22;
+constexpr int64_t kNormMaxCols = 32768;
+
+typedef uint32_t u4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(1)));
+
+struct NormArgs {
+  int64_t N, D;
+  const uint16_t* x;
+  int64_t x_stride;
+  const uint16_t* residual;  // or null
+  int64_t r_stride;
+  const uint16_t* weight;    // or null
+  float eps;
+  uint16_t* sum;             // outputs, each or null
+  int64_t sum_stride;
+  uint16_t* h;
+  int64_t h_stride;
+  int8_t* codes;
+  int64_t c_stride;
+  float* scale;
+  float* inv_rms;
+};
+
+struct NormBwdArgs {
+  int64_t N, D;
+  const uint16_t* dh;
+  int64_t dh_stride;
+  const uint16_t* sum;
+  int64_t sum_stride;
+  const float* inv_rms;
+  const uint16_t* weight;  // or null
+  const uint16_t* dsum;    // or null
+  int64_t ds_stride;
+  uint16_t* dx;            // or null
+  int64_t dx_stride;
+  float* part;             // [parts][D], or null
+  float* dweight;
+  int parts;
+};
+
+// Elements v .. v + 8 of a row that starts at any element, zeros from `end` on.
+__device__ __forceinline__ u4 load8(const uint16_t* row, int64_t v, int64_t end) {
+  u4 x = {};
+  if (v + 8 <= end) {
+    x = *reinterpret_cast<const u4_any*>(row + v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (v + j < end) x[j >> 1] |= (uint32_t)row[v + j] << (16 * (j & 1));
+  }
+  return x;
+}
+__device__ __forceinline__ void store8(uint16_t* row, int64_t v, int64_t end, u4 x) {
+  if (v + 8 <= end) {
+    *reinterpret_cast<u4_any*>(row + v) = x;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (v + j < end) row[v + j] = (uint16_t)(x[j >> 1] >> (16 * (j & 1)));
+  }
+}
+__device__ __forceinline__ float at(const u4& x, int j) {
+  return __uint_as_float(j & 1 ? x[j >> 1] & 0xffff0000u : x[j >> 1] << 16);
+}
+__device__ __forceinline__ u4 pack8(const float (&y)[8]) {
+  const u2 lo = pack_bf16x4(y[0], y[1], y[2], y[3]), hi = pack_bf16x4(y[4], y[5], y[6], y[7]);
+  return u4{lo[0], lo[1], hi[0], hi[1]};
+}
+constexpr uint32_t kOnes = 0x3f803f80u;  // two bf16 ones
+
+// Sum (in a fixed order) and largest of a row's threads, given to all of them.
+template <int T>
+__device__ __forceinline__ void row_reduce(double& sum, uint32_t& top) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    sum += __shfl_xor(sum, o);
+    top = std::max(top, (uint32_t)__shfl_xor((int)top, o));
+  }
+  if constexpr (T > 64) {
+    constexpr int W = T / 64;
+    __shared__ double sSum[W];
+    __shared__ uint32_t sTop[W];
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      sSum[wave] = sum;
+      sTop[wave] = top;
+    }
+    __syncthreads();
+    sum = sSum[0];
+    top = sTop[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      sum += sSum[w];
+      top = std::max(top, sTop[w]);
+    }
+  }
+}
+
+constexpr int norm_threads(int T) { return T < 256 ? 256 : T; }
+
+// T threads a row, K octets of columns each.
+template <int T, int K>
+__global__ __launch_bounds__(norm_threads(T)) void rmsnorm_kernel(const NormArgs a) {
+  constexpr int kRows = norm_threads(T) / T;
+  const int t0 = threadIdx.x % T;
+  const int64_t n = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
+  if (n >= a.N) return;  // whole waves, and of T > 64 whole workgroups
+  u4 s[K], w[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int64_t v = 8 * (int64_t)(t0 + T * k);
+    s[k] = load8(a.x + n * a.x_stride, v, a.D);
+    w[k] = a.weight ? load8(a.weight, v, a.D) : u4{kOnes, kOnes, kOnes, kOnes};
+  }
+  if (a.residual) {
+    u4 r[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) r[k] = load8(a.residual + n * a.r_stride, 8 * (int64_t)(t0 + T * k), a.D);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = at(s[k], j) + at(r[k], j);
+      s[k] = pack8(y);
+    }
+  }
+  if (a.sum) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) store8(a.sum + n * a.sum_stride, 8 * (int64_t)(t0 + T * k), a.D, s[k]);
+  }
+  // squares and their sum in fp64: neither overflows for any bf16 row.  The
+  // largest by its bits, which puts a NaN above everything.
+  double sum = 0.0;
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double y = (double)at(s[k], j);
+      sum = fma(y, y, sum);
+      top = std::max(top, __float_as_uint(at(s[k], j) * at(w[k], j)) & 0x7fffffffu);
+    }
+  row_reduce<T>(sum, top);
+  const double inv = 1.0 / sqrt(sum / (double)a.D + (double)a.eps);
+  const float m = __uint_as_float(top), inv32 = (float)inv;
+  const bool finite = top < 0x7f800000u && sum < (double)__builtin_huge_valf();
+  if (t0 == 0) {
+    if (a.inv_rms) a.inv_rms[n] = inv32;
+    if (a.scale) a.scale[n] = finite ? (float)((double)m * inv / 127.0) : __builtin_nanf("");
+  }
+  if (a.h) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = at(s[k], j) * at(w[k], j) * inv32;
+      store8(a.h + n * a.h_stride, 8 * (int64_t)(t0 + T * k), a.D, pack8(y));
+    }
+  }
+  if (a.codes) {
+    const double step = finite && m > 0.0f ? 127.0 / (double)m : 0.0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t v = 8 * (int64_t)(t0 + T * k);
+      u2 c = {};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // 1.5 2^23 + q rounds q to a whole number, half to even, in the sum's low bits
+        const float q = (float)((double)(at(s[k], j) * at(w[k], j)) * step);
+        c[j >> 2] |= (__float_as_uint(q + 12582912.0f) & 0xffu) << (8 * (j & 3));
+      }
+      if (!finite) c = u2{};
+      int8_t* row = a.codes + n * a.c_stride;
+      if (v + 8 <= a.D) {
+        *reinterpret_cast<u2_any*>(row + v) = c;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (v + j < a.D) row[v + j] = (int8_t)(c[j >> 2] >> (8 * (j & 3)));
+      }
+    }
+  }
+}
+
+// dx = dsum + inv (g - s inv^2 sum_d(g s) / D), g = w dh, and part p of
+// dweight = sum_n dh s inv: row slot p takes the rows p, p + parts, ..., its
+// threads the same columns of all of them.
+template <int T, int K>
+__global__ __launch_bounds__(norm_threads(T)) void rmsnorm_backward_kernel(const NormBwdArgs a) {
+  constexpr int kSlots = norm_threads(T) / T;
+  const int t0 = threadIdx.x % T;
+  const int p = (int)blockIdx.x * kSlots + threadIdx.x / T;
+  if (p >= a.parts) return;
+  u4 w[K];
+  float dw[K][8] = {};
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    w[k] = a.weight ? load8(a.weight, 8 * (int64_t)(t0 + T * k), a.D) : u4{kOnes, kOnes, kOnes, kOnes};
+  for (int64_t n = p; n < a.N; n += a.parts) {
+    u4 s[K], d[K], e[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t v = 8 * (int64_t)(t0 + T * k);
+      s[k] = load8(a.sum + n * a.sum_stride, v, a.D);
+      d[k] = load8(a.dh + n * a.dh_stride, v, a.D);
+      e[k] = a.dsum ? load8(a.dsum + n * a.ds_stride, v, a.D) : u4{};
+    }
+    const float inv = a.inv_rms[n];
+    double dot = 0.0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float part = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) part = fmaf(at(d[k], j) * at(w[k], j), at(s[k], j), part);
+      dot += (double)part;
+    }
+    uint32_t none = 0;
+    if constexpr (T > 64) __syncthreads();  // the row before is done with the reduction's memory
+    row_reduce<T>(dot, none);
+    const float c = (float)(dot * (double)inv * (double)inv / (double)a.D);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        y[j] = fmaf(inv, at(d[k], j) * at(w[k], j) - at(s[k], j) * c, at(e[k], j));
+        dw[k][j] = fmaf(at(d[k], j), at(s[k], j) * inv, dw[k][j]);
+      }
+      if (a.dx) store8(a.dx + n * a.dx_stride, 8 * (int64_t)(t0 + T * k), a.D, pack8(y));
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t v = 8 * (int64_t)(t0 + T * k) + j;
+      if (v < a.D) a.part[p * a.D + v] = dw[k][j];
+    }
+}
+
+// 64 columns of dweight: 16 threads a column add its parts, in fp64.
+constexpr int kDeal = 16;
+__global__ __launch_bounds__(64 * kDeal) void rmsnorm_dweight_kernel(const NormBwdArgs a) {
+  __shared__ double buf[kDeal][64];
+  const int c = threadIdx.x & 63, deal = threadIdx.x >> 6;
+  const int64_t v = 64 * (int64_t)blockIdx.x + c;
+  double sum = 0.0;
+  if (v < a.D)
+#pragma unroll 4
+    for (int p = deal; p < a.parts; p += kDeal) sum += (double)a.part[p * a.D + v];
+  buf[deal][c] = sum;
+  __syncthreads();
+  if (deal == 0 && v < a.D) {
+#pragma unroll
+    for (int i = 1; i < kDeal; ++i) sum += buf[i][c];
+    a.dweight[v] = (float)sum;
+  }
+}
+
+// ------------------------------------------------------------------- host ---
+
+// Rows that are worked on at the same time: parts of dweight.
+int norm_parts(int64_t N, int64_t D) {
+  const int64_t most = D <= 2048 ? 2048 : D <= 16384 ? 512 : 256;
+  return (int)std::min(N, most);
+}
+
+template <template <int, int> class Launch, typename A>
+void by_width(int64_t D, const A& a, hipStream_t s) {
+  if (D <= 512)
+    Launch<64, 1>::run(a, s);
+  else if (D <= 1024)
+    Launch<64, 2>::run(a, s);
+  else if (D <= 2048)
+    Launch<64, 4>::run(a, s);
+  else if (D <= 4096)
+    Launch<256, 2>::run(a, s);
+  else if (D <= 8192)
+    Launch<256, 4>::run(a, s);
+  else if (D <= 16384)
+    Launch<256, 8>::run(a, s);
+  else
+    Launch<1024, 4>::run(a, s);
+}
+
+template <int T, int K>
+struct LaunchNorm {
+  static void run(const NormArgs& a, hipStream_t s) {
+    constexpr int kRows = norm_threads(T) / T;
+    hipLaunchKernelGGL((rmsnorm_kernel<T, K>), dim3((unsigned)((a.N + kRows - 1) / kRows)), dim3(norm_threads(T)), 0, s, a);
+  }
+};
+
+template <int T, int K>
+struct LaunchNormBwd {
+  static void run(const NormBwdArgs& a, hipStream_t s) {
+    constexpr int kSlots = norm_threads(T) / T;
+    hipLaunchKernelGGL((rmsnorm_backward_kernel<T, K>), dim3((unsigned)((a.parts + kSlots - 1) / kSlots)),
+                       dim3(norm_threads(T)), 0, s, a);
+  }
+};
+
+// A bf16 (or int8) tensor of N rows and D columns.
+int check_rows(const archead_tensor* t, int64_t N, int64_t D, int dtype) {
+  if (t->dtype != dtype) return ARCHEAD_E_DTYPE;
+  if (t->rows != N || t->cols != D || t->row_stride < D) return ARCHEAD_E_SHAPE;
+  return ARCHEAD_OK;
+}
+int size_of(const archead_tensor* t) { return t->dtype == ARCHEAD_I8 ? 1 : 2; }
+bool misaligned(const archead_tensor* t) { return t && (uintptr_t)t->data % size_of(t) != 0; }
+// The rows of `in` that `out` replaces as they are.
+bool same_rows(const archead_tensor* in, const archead_tensor* out) {
+  return in->data == out->data && in->row_stride == out->row_stride && in->dtype == out->dtype;
+}
+// A vector's bytes, as one row.
+archead_tensor bytes_of(const void* p, int64_t n) { return archead_tensor{const_cast<void*>(p), 1, n, n, ARCHEAD_I8}; }
+bool meets(const archead_tensor* x, const archead_tensor* y) {
+  if (x->rows == 0 || y->rows == 0) return false;
+  if (x->rows == y->rows) return overlap(x, size_of(x), y, size_of(y));
+  // a vector and a tensor: by their spans
+  const uint64_t a = (uint64_t)x->data, b = (uint64_t)y->data;
+  return a < b + ((uint64_t)(y->rows - 1) * y->row_stride + y->cols) * size_of(y) &&
+         b < a + ((uint64_t)(x->rows - 1) * x->row_stride + x->cols) * size_of(x);
+}
+
+}  // namespace
+}  // namespace archead
+
+using namespace archead;
+
+extern "C" {
+
+int archead_rmsnorm(const archead_rmsnorm_inputs* in, const archead_rmsnorm_outputs* out, void* stream) {
+  if (!in || !out || !in->x) return ARCHEAD_E_NULL;
+  const archead_tensor* x = in->x;
+  const int64_t N = x->rows, D = x->cols;
+  if (N < 0 || D < 1) return ARCHEAD_E_SHAPE;
+  if (int rc = check_rows(x, N, D, ARCHEAD_BF16)) return rc;
+  if (in->residual)
+    if (int rc = check_rows(in->residual, N, D, ARCHEAD_BF16)) return rc;
+  const archead_tensor* outs[] = {out->sum, out->h, out->codes};
+  for (const archead_tensor* t : outs)
+    if (t)
+      if (int rc = check_rows(t, N, D, t == out->codes ? ARCHEAD_I8 : ARCHEAD_BF16)) return rc;
+  if (!(in->eps > 0.0f) || !(in->eps < __builtin_huge_valf())) return ARCHEAD_E_VALUE;
+  if (N > kNormMaxRows || D > kNormMaxCols) return ARCHEAD_E_UNSUPPORTED;
+  if (N == 0) return ARCHEAD_OK;
+  if ((out->codes != nullptr) != (out->scale != nullptr)) return ARCHEAD_E_NULL;
+  if (!x->data || (in->residual && !in->residual->data)) return ARCHEAD_E_NULL;
+  for (const archead_tensor* t : outs)
+    if (t && !t->data) return ARCHEAD_E_NULL;
+  if (misaligned(x) || misaligned(in->residual) || misaligned(out->sum) || misaligned(out->h)) return ARCHEAD_E_ALIGN;
+  if ((uintptr_t)in->weight % 2 || (uintptr_t)out->scale % 4 || (uintptr_t)out->inv_rms % 4) return ARCHEAD_E_ALIGN;
+  // outputs meet no input, but that a row may be replaced by the sum or h of itself, and no other output
+  const archead_tensor weight = bytes_of(in->weight, 2 * D), scale = bytes_of(out->scale, 4 * N),
+                       inv = bytes_of(out->inv_rms, 4 * N);
+  const archead_tensor* all_out[] = {out->sum, out->h, out->codes, out->scale ? &scale : nullptr,
+                                     out->inv_rms ? &inv : nullptr};
+  const archead_tensor* all_in[] = {x, in->residual, in->weight ? &weight : nullptr};
+  for (int i = 0; i < 5; ++i) {
+    if (!all_out[i]) continue;
+    for (const archead_tensor* t : all_in)
+      if (t && !(i < 2 && same_rows(t, all_out[i])) && meets(t, all_out[i])) return ARCHEAD_E_SHAPE;
+    for (int j = 0; j < i; ++j)
+      if (all_out[j] && meets(all_out[i], all_out[j])) return ARCHEAD_E_SHAPE;
+  }
+  if (!out->sum && !out->h && !out->codes && !out->inv_rms) return ARCHEAD_OK;
+  NormArgs a{};
+  a.N = N;
+  a.D = D;
+  a.x = static_cast<const uint16_t*>(x->data);
+  a.x_stride = x->row_stride;
+  if (in->residual) {
+    a.residual = static_cast<const uint16_t*>(in->residual->data);
+    a.r_stride = in->residual->row_stride;
+  }
+  a.weight = static_cast<const uint16_t*>(in->weight);
+  a.eps = in->eps;
+  if (out->sum) {
+    a.sum = static_cast<uint16_t*>(out->sum->data);
+    a.sum_stride = out->sum->row_stride;
+  }
+  if (out->h) {
+    a.h = static_cast<uint16_t*>(out->h->data);
+    a.h_stride = out->h->row_stride;
+  }
+  if (out->codes) {
+    a.codes = static_cast<int8_t*>(out->codes->data);
+    a.c_stride = out->codes->row_stride;
+  }
+  a.scale = out->scale;
+  a.inv_rms = out->inv_rms;
+  (void)hipGetLastError();  // start from a clean error state
+  by_width<LaunchNorm>(D, a, static_cast<hipStream_t>(stream));
+  return hipGetLastError() == hipSuccess ? ARCHEAD_OK : ARCHEAD_E_HIP;
+}
+
+int archead_rmsnorm_backward_workspace_bytes(int64_t n_rows, int64_t D, uint64_t* bytes) {
+  if (!bytes) return ARCHEAD_E_NULL;
+  if (n_rows < 0 || D < 1) return ARCHEAD_E_SHAPE;
+  if (n_rows > kNormMaxRows || D > kNormMaxCols) return ARCHEAD_E_UNSUPPORTED;
+  *bytes = round_up((uint64_t)norm_parts(n_rows, D) * (uint64_t)D * 4, ARCHEAD_ALIGNMENT);
+  return ARCHEAD_OK;
+}
+
+int archead_rmsnorm_backward(const archead_rmsnorm_grad_inputs* in, const archead_rmsnorm_grad_outputs* out,
+                             void* workspace, uint64_t workspace_bytes, void* stream) {
+  if (!in || !out || !in->dh || !in->sum) return ARCHEAD_E_NULL;
+  const int64_t N = in->dh->rows, D = in->dh->cols;
+  if (N < 0 || D < 1) return ARCHEAD_E_SHAPE;
+  for (const archead_tensor* t : {in->dh, in->sum, in->dsum, out->dx})
+    if (t)
+      if (int rc = check_rows(t, N, D, ARCHEAD_BF16)) return rc;
+  if (N > kNormMaxRows || D > kNormMaxCols) return ARCHEAD_E_UNSUPPORTED;
+  if (!out->dx && !out->dweight) return ARCHEAD_OK;
+  for (const archead_tensor* t : {in->dh, in->sum, in->dsum, out->dx})
+    if (t && N > 0 && !t->data) return ARCHEAD_E_NULL;
+  if (N > 0 && !in->inv_rms) return ARCHEAD_E_NULL;
+  for (const archead_tensor* t : {in->dh, in->sum, in->dsum, out->dx})
+    if (misaligned(t)) return ARCHEAD_E_ALIGN;
+  if ((uintptr_t)in->weight % 2 || (uintptr_t)in->inv_rms % 4 || (uintptr_t)out->dweight % 4) return ARCHEAD_E_ALIGN;
+  const uint64_t need = out->dweight ? round_up((uint64_t)norm_parts(N, D) * (uint64_t)D * 4, ARCHEAD_ALIGNMENT) : 0;
+  if (need && !workspace) return ARCHEAD_E_NULL;
+  if (need && (uintptr_t)workspace % ARCHEAD_ALIGNMENT) return ARCHEAD_E_ALIGN;
+  if (workspace_bytes < need) return ARCHEAD_E_WORKSPACE;
+  const archead_tensor weight = bytes_of(in->weight, 2 * D), inv = bytes_of(in->inv_rms, 4 * N),
+                       dw = bytes_of(out->dweight, 4 * D), ws = bytes_of(workspace, (int64_t)need);
+  const archead_tensor* all_out[] = {out->dx, out->dweight ? &dw : nullptr, need ? &ws : nullptr};
+  const archead_tensor* all_in[] = {in->dh, in->dsum, in->sum, in->weight ? &weight : nullptr, N > 0 ? &inv : nullptr};
+  for (int i = 0; i < 3; ++i) {
+    if (!all_out[i]) continue;
+    for (int j = 0; j < 5; ++j)
+      if (all_in[j] && !(i == 0 && j < 3 && same_rows(all_in[j], all_out[i])) && meets(all_in[j], all_out[i]))
+        return ARCHEAD_E_SHAPE;
+    for (int j = 0; j < i; ++j)
+      if (all_out[j] && meets(all_out[i], all_out[j])) return ARCHEAD_E_SHAPE;
+  }
+  NormBwdArgs a{};
+  a.N = N;
+  a.D = D;
+  a.dh = static_cast<const uint16_t*>(in->dh->data);
+  a.dh_stride = in->dh->row_stride;
+  a.sum = static_cast<const uint16_t*>(in->sum->data);
+  a.sum_stride = in->sum->row_stride;
+  a.inv_rms = in->inv_rms;
+  a.weight = static_cast<const uint16_t*>(in->weight);
+  if (in->dsum) {
+    a.dsum = static_cast<const uint16_t*>(in->dsum->data);
+    a.ds_stride = in->dsum->row_stride;
+  }
+  if (out->dx) {
+    a.dx = static_cast<uint16_t*>(out->dx->data);
+    a.dx_stride = out->dx->row_stride;
+  }
+  a.part = out->dweight ? static_cast<float*>(workspace) : nullptr;
+  a.dweight = out->dweight;
+  a.parts = norm_parts(N, D);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();  // start from a clean error state
+  if (N > 0) by_width<LaunchNormBwd>(D, a, s);
+  // no rows: a gradient of zeros
+  if (out->dweight) hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((unsigned)((D + 63) / 64)), dim3(64 * kDeal), 0, s, a);
+  return hipGetLastError() == hipSuccess ? ARCHEAD_OK : ARCHEAD_E_HIP;
+}
+
+}  // extern "C"

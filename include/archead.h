@@ -30,8 +30,8 @@
  *     workspaces; the library holds no global state and is re-entrant.
  *   - The comparison heads (archead_format other than ARCHEAD_FMT_ARCHEAD) are
  *     served by archead_pack_layout, archead_pack, archead_workspace_bytes(_path),
- *     archead_main_kernel and archead_logits(_path, _events); every other
- *     entry point gives E_UNSUPPORTED for them.
+ *     archead_main_kernel, archead_logits(_path, _events) and, row INT8,
+ *     archead_logits_int8; every other entry point gives E_UNSUPPORTED for them.
  */
 #ifndef ARCHEAD_H
 #define ARCHEAD_H
@@ -61,7 +61,8 @@ typedef enum {
                                 rank above 1024, a forced decode path the decode kernel does not take,
                                 section offsets past 32 bits, a comparison head where only the
                                 ARCHead format is served) */
-  ARCHEAD_E_DTYPE = 4,       /* H is not bf16, or Y is neither fp32 nor bf16       */
+  ARCHEAD_E_DTYPE = 4,       /* H is not bf16, or Y is neither fp32 nor bf16; a tensor of
+                                another type than the entry point takes            */
   ARCHEAD_E_SHAPE = 5,       /* H.cols != D, Y.cols != V, Y.rows != H.rows, bad strides */
   ARCHEAD_E_ALIGN = 6,       /* buffer/workspace not 256-byte aligned, H rows not 16-byte aligned,
                                 Y not aligned to its element size                 */
@@ -71,7 +72,7 @@ typedef enum {
   ARCHEAD_E_SIZE = 10        /* packed buffer smaller than archead_layout.total_bytes */
 } archead_status;
 
-typedef enum { ARCHEAD_BF16 = 1, ARCHEAD_F32 = 2 } archead_dtype;
+typedef enum { ARCHEAD_BF16 = 1, ARCHEAD_F32 = 2, ARCHEAD_I8 = 3 } archead_dtype;
 
 typedef enum {
   ARCHEAD_PATH_AUTO = 0,   /* the decode path when it takes the call, else the tile path */
@@ -630,6 +631,98 @@ ARCHEAD_API int archead_logits_backward_workspace_bytes(const archead_dims* d, i
  * E_WORKSPACE, E_HIP. */
 ARCHEAD_API int archead_logits_backward(const archead_tensor* dY, const archead_packed_head* head,
                                         archead_tensor* dH, void* stream);
+
+/* ---- In front of the head ------------------------------------------------
+ * The norm that makes the head's input of the residual stream, its gradient,
+ * and the product of its 8-bit output with a row-INT8 head. */
+
+/* Inputs of the norm: N = x.rows rows of D = x.cols columns (1 to 32768, any;
+ * N at most 2^22), any row strides, tensors aligned to their element size.
+ *   s = x + residual, rounded to bf16 as the residual stream keeps it (s = x
+ *       without a residual)
+ *   h = s inv w,  inv = 1 / sqrt(sum_d s_d^2 / D + eps). */
+typedef struct {
+  const archead_tensor* x;        /* bf16 [N][D] */
+  const archead_tensor* residual; /* bf16 [N][D], or NULL */
+  const void* weight;             /* device bf16 [D], or NULL: 1 */
+  float eps;                      /* > 0 */
+} archead_rmsnorm_inputs;
+
+/* Outputs; each pointer may be NULL (not computed), codes and scale come
+ * together:
+ *   codes[n][d] = rint(127 t_d / m) (half to even), t = s w, m = max_d |t_d|;
+ *   scale[n]    = m inv / 127, so codes times scale is h; a row of zeros has
+ *                 codes and scale 0
+ * Products t are fp32 (exact but for under- and overflow); sums of squares
+ * fp64.  A row with a t or an s that is not finite has scale NaN and codes 0,
+ * and its h is what the formula gives; it changes no other row.  sum and h
+ * may replace x or residual row for row (same data and stride); outputs may
+ * share bytes with nothing else (E_SHAPE). */
+typedef struct {
+  const archead_tensor* sum;   /* bf16 [N][D] s */
+  const archead_tensor* h;     /* bf16 [N][D] */
+  const archead_tensor* codes; /* ARCHEAD_I8 [N][D] */
+  float* scale;                /* [N] */
+  float* inv_rms;              /* [N] inv, for the gradient */
+} archead_rmsnorm_outputs;
+
+/* Enqueue the norm on `stream`; N = 0 is a no-op.  E_NULL, E_DTYPE, E_SHAPE,
+ * E_VALUE (eps), E_UNSUPPORTED, E_ALIGN, E_HIP. */
+ARCHEAD_API int archead_rmsnorm(const archead_rmsnorm_inputs* in, const archead_rmsnorm_outputs* out, void* stream);
+
+/* The norm's gradient.  dh arrives at h, dsum at s by the residual stream:
+ *   dx = dsum + inv (g - s inv^2 sum_d(g s) / D),  g = w dh
+ *   dweight_d = sum_n dh s inv
+ * dx is the gradient of x and of the residual alike.  (Of the 8-bit output it
+ * is the gradient that takes the rounding as the identity.) */
+typedef struct {
+  const archead_tensor* dh;   /* bf16 [N][D] */
+  const archead_tensor* sum;  /* bf16 [N][D] s */
+  const float* inv_rms;       /* [N] */
+  const void* weight;         /* bf16 [D], or NULL: 1 */
+  const archead_tensor* dsum; /* bf16 [N][D], or NULL: 0 */
+} archead_rmsnorm_grad_inputs;
+
+/* Outputs; each may be NULL.  dx may replace dh, sum or dsum row for row. */
+typedef struct {
+  const archead_tensor* dx; /* bf16 [N][D] */
+  float* dweight;           /* fp32 [D]; zeros for N = 0 */
+} archead_rmsnorm_grad_outputs;
+
+/* Device workspace of the gradient where dweight is wanted (else 0 will do):
+ * fp32 partial sums of it.  Pure host arithmetic.  E_NULL, E_SHAPE,
+ * E_UNSUPPORTED. */
+ARCHEAD_API int archead_rmsnorm_backward_workspace_bytes(int64_t n_rows, int64_t D, uint64_t* bytes);
+
+/* Enqueue the gradient on `stream`.  Sums over a row are fp32 in eights and
+ * fp64 from there, sums over rows fp32 and fp64; two calls with the same
+ * arguments give the same bits.  workspace: device, 256-byte aligned.  E_NULL,
+ * E_DTYPE, E_SHAPE, E_UNSUPPORTED, E_ALIGN, E_WORKSPACE, E_HIP. */
+ARCHEAD_API int archead_rmsnorm_backward(const archead_rmsnorm_grad_inputs* in, const archead_rmsnorm_grad_outputs* out,
+                                         void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* Device workspace archead_logits_int8 needs for n_tokens rows: 0 for few
+ * (up to 16 that fit LDS), else min(n_tokens, 16384) rows of D bytes, rounded
+ * up to 32 rows.  Pure host arithmetic.  E_NULL, E_DIMS, E_SHAPE,
+ * E_UNSUPPORTED (not a row-INT8 head, D above 65536). */
+ARCHEAD_API int archead_logits_int8_workspace_bytes(const archead_dims* d, int64_t n_tokens, uint64_t* bytes);
+
+/* Y = diag(scale) X W_hat^T: the logits of INT8 hidden states (codes X and a
+ * scale for each token) through an ARCHEAD_FMT_ROW_INT8 head (codes and a scale
+ * for each row of the vocabulary), as a product of 8-bit integers:
+ *   Y[n, v] = (sum_k X[n, k] q8[v, k]) (scale[n] s[v])
+ * with exact int32 sums, the scales applied in fp32, rounded once more for
+ * bf16.
+ *   X: ARCHEAD_I8 [N][D] device tensor, any codes, rows 16-byte aligned.
+ *   scale: device fp32 [N].  Any values: one that is not finite gives a row of
+ *       Y that is not, and changes no other.
+ *   Y: fp32 or bf16 [N][V], any row stride, written completely; it may share
+ *       bytes with nothing else (E_SHAPE).
+ * head->workspace: at least archead_logits_int8_workspace_bytes (unused when
+ * that is 0).  N at most 2^22; N = 0 is a no-op.  E_NULL, E_DIMS, E_DTYPE,
+ * E_SHAPE, E_UNSUPPORTED, E_ALIGN, E_SIZE, E_WORKSPACE, E_HIP. */
+ARCHEAD_API int archead_logits_int8(const archead_tensor* X, const float* scale, const archead_packed_head* head,
+                                    const archead_tensor* Y, void* stream);
 
 /* Static string naming a status code. */
 ARCHEAD_API const char* archead_status_string(int status);

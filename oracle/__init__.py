@@ -14,3 +14,6 @@ from .archead_oracle import (  # noqa: F401
 from .training_oracle import (  # noqa: F401
     PREF_SIGMOID, PREF_SQUARED, policy_loss, preference_loss, logits_backward,
 )
+from .front_oracle import (  # noqa: F401
+    round_bf16, rmsnorm, rmsnorm_backward, logits_int8, cross_entropy,
+)
