@@ -37,6 +37,7 @@ EXPORTS = ("archead_pack_layout", "archead_workspace_bytes", "archead_workspace_
            "archead_fit_workspace_bytes", "archead_fit", "archead_logit_error_workspace_bytes",
            "archead_logit_error", "archead_loss_workspace_bytes", "archead_policy_loss", "archead_preference_loss",
            "archead_logits_backward_workspace_bytes", "archead_logits_backward",
+           "archead_cross_entropy_workspace_bytes", "archead_cross_entropy",
            "archead_rmsnorm", "archead_rmsnorm_backward_workspace_bytes", "archead_rmsnorm_backward",
            "archead_logits_int8_workspace_bytes", "archead_logits_int8",
            "archead_status_string", "archead_format_version")
@@ -128,6 +129,14 @@ class ArcheadPreferenceOutputs(ctypes.Structure):
                 ("rejected_reward", ctypes.c_void_p), ("dY", ctypes.POINTER(ArcheadTensor))]
 
 
+class ArcheadCrossEntropyInputs(ctypes.Structure):
+    _fields_ = [("labels", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("inv_temperature", ctypes.c_float)]
+
+
+class ArcheadCrossEntropyOutputs(ctypes.Structure):
+    _fields_ = [("loss", ctypes.c_void_p), ("logp", ctypes.c_void_p), ("dH", ctypes.POINTER(ArcheadTensor))]
+
+
 class ArcheadRmsnormInputs(ctypes.Structure):
     _fields_ = [("x", ctypes.POINTER(ArcheadTensor)), ("residual", ctypes.POINTER(ArcheadTensor)),
                 ("weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
@@ -191,6 +200,9 @@ def _load():
                                             ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p]
     lib.archead_logits_backward_workspace_bytes.argtypes = [P(ArcheadDims), ctypes.c_int64, P(ctypes.c_uint64)]
     lib.archead_logits_backward.argtypes = [P(ArcheadTensor), P(ArcheadPackedHead), P(ArcheadTensor), ctypes.c_void_p]
+    lib.archead_cross_entropy_workspace_bytes.argtypes = [P(ArcheadDims), ctypes.c_int64, P(ctypes.c_uint64)]
+    lib.archead_cross_entropy.argtypes = [P(ArcheadTensor), P(ArcheadPackedHead), P(ArcheadCrossEntropyInputs),
+                                          P(ArcheadCrossEntropyOutputs), ctypes.c_void_p]
     lib.archead_rmsnorm.argtypes = [P(ArcheadRmsnormInputs), P(ArcheadRmsnormOutputs), ctypes.c_void_p]
     lib.archead_rmsnorm_backward_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64, P(ctypes.c_uint64)]
     lib.archead_rmsnorm_backward.argtypes = [P(ArcheadRmsnormGradInputs), P(ArcheadRmsnormGradOutputs),
@@ -775,6 +787,52 @@ def archead_logits_backward(dY, head: PackedHead, dH=None, workspace=None):
     if status:
         _check(status, "archead_logits_backward")
     return dH
+
+
+def archead_cross_entropy_workspace_bytes(V, D, r_c, r_r, g, n_tokens: int, fmt=ARCHEAD_FMT_ARCHEAD) -> int:
+    out = ctypes.c_uint64(0)
+    _check(lib.archead_cross_entropy_workspace_bytes(ctypes.byref(_dims(V, D, r_c, r_r, g, fmt)), int(n_tokens),
+                                                     ctypes.byref(out)), "archead_cross_entropy_workspace_bytes")
+    return out.value
+
+
+_cross_entropy_workspace_bytes = functools.lru_cache(maxsize=256)(archead_cross_entropy_workspace_bytes)
+
+
+@_scoped
+def archead_cross_entropy(H, labels, head: PackedHead, weight=None, inv_temperature: float = 1.0, dH=None,
+                          with_gradient: bool = True, workspace=None):
+    """Cross entropy of labels through a packed ARCHead head, without the
+    logits: loss = -sum weight log p.  H: bf16 [N, D]; labels: int32 [N];
+    weight (None: 1): fp32 [N].  Returns a dict of device tensors "loss"
+    (scalar), "logp" (fp32 [N]) and, with_gradient, "dH" (bf16 [N, D], the given
+    tensor or a new one).  stream: a torch stream or a raw handle (None: the
+    current one)."""
+    torch = _torch()
+    dev = head.buffer.device
+    if H.device != dev or (dH is not None and dH.device != dev):
+        raise ValueError("H and dH must be on the head's device")
+    h = _tensor(H)
+    N, f32 = H.shape[0], torch.float32
+    inp = ArcheadCrossEntropyInputs(_vec(labels, "labels", torch.int32, N, dev), _vec(weight, "weight", f32, N, dev),
+                                    inv_temperature)
+    if with_gradient and dH is None:
+        dH = torch.empty((N, head.D), dtype=torch.bfloat16, device=dev)
+    dh = ctypes.pointer(_tensor(dH)) if with_gradient else None
+    ws = _workspace(workspace, _cross_entropy_workspace_bytes(head.V, head.D, head.r_c, head.r_r, head.g, N, head.fmt), dev)
+    vec = torch.empty(N + 1, dtype=f32, device=dev)
+    at = vec.data_ptr()
+    p = ArcheadPackedHead(_dims(head.V, head.D, head.r_c, head.r_r, head.g, head.fmt), head.buffer.data_ptr(),
+                          head.buffer.numel(), *_span(ws))
+    status = lib.archead_cross_entropy(h, p, inp, ArcheadCrossEntropyOutputs(at + 4 * N, at if N else None, dh),
+                                       _raw_stream(dev))
+    if status:
+        _check(status, "archead_cross_entropy")
+    logp, loss = vec.split_with_sizes((N, 1))
+    out = {"loss": loss.view(()), "logp": logp}
+    if with_gradient:
+        out["dH"] = dH
+    return out
 
 
 # ------------------------------------------------------- in front of the head ---

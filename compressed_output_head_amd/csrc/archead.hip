@@ -130,6 +130,20 @@ WorkspaceLayout workspace_layout(const archead_dims* d, int64_t n_tokens, bool s
   return w;
 }
 
+bool forward_takes(const archead_dims* d, int64_t n_tokens) {
+  const WorkspaceLayout W = workspace_layout(d, n_tokens);
+  FwdArgs a{};
+  a.V = d->V;
+  a.D = d->D;
+  a.N = n_tokens;
+  a.n32 = W.n32;
+  a.nb = (int64_t)round_up((uint64_t)d->V, 16) / 16;
+  a.r_c = d->r_c;
+  a.r_r = d->r_r;
+  a.ng = (int)(d->D / d->g);
+  return W.decode || tile32_eligible(a);
+}
+
 namespace {
 
 template <typename F>

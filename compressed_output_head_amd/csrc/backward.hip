@@ -29,6 +29,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "backward_main.h"
 #include "device_common.h"
 #include "internal.h"
 
@@ -41,13 +42,10 @@ constexpr int kMaxThreads = 256;
 constexpr int kMaxRows = 4;
 constexpr int kPrepWaves = 4;       // and 32-rank tiles of Z that a workgroup forms
 constexpr int kZsumThreads = 512, kZsumRanks = 64;
-constexpr int kMainThreads = 512;
 constexpr int kFinishThreads = 256;
 constexpr int kFinishRows = 8;
 constexpr int kMaxMaxPieces = 128;
-constexpr int kXcds = 8;
 constexpr int kMaxSplits = 64;
-constexpr int64_t kFewTokens = 32;  // of bwd_few_kernel
 // Where kOwnRounds rounds of loads reach all of dY, every workgroup of
 // bwd_prep_kernel finds the rows' maxima itself: a call of 4 rows of a 1024 x
 // 256 head takes 20 us, with a launch for them 24; sixteen rounds 25 and 24,
@@ -60,34 +58,6 @@ __host__ __device__ constexpr int own_lanes(int64_t N) {
   while (lanes * N > 64 * kPrepWaves) lanes /= 2;
   return lanes;
 }
-
-struct BwdArgs {
-  int64_t V, D, N, n32, nb;
-  int r_c, r_r, g, ng, nkt, nA;
-  int nct, nwt;                    // 32-rank tiles of the two parts
-  const void* dY;
-  int64_t dy_stride;
-  uint16_t* dH;
-  int64_t dh_stride;
-  const uint8_t* r_codes;
-  const uint8_t* r_gcodes;
-  const uint16_t* r_rowscale;
-  const int8_t* a_codes;
-  const uint16_t* a_scales;
-  const int8_t* b_codes;
-  const uint16_t* b_scales;
-  // workspace
-  float* pmax;      // [N][3][pieces]
-  float* rscale;    // [n32][3] powers of two that undo the rows' scales
-  _Float16* hf;     // [n32/32][ksteps][64][8]; few tokens: [s_R, s_Ac, s_Aw][ksteps][2][N][8]
-  uint8_t* af;      // A codes, [32-rank tiles][ksteps][64][8]
-  uint8_t* gt;      // few tokens: group codes, [D / 128 or D / g][16 nb][128 / g or 1]
-  float* zpart;     // [zparts][n32][r_c + r_r]
-  float* z;         // [n32][r_c + r_r]; few tokens: not used, bwd_finish_few_kernel sums the parts
-  float* part;      // [splits][N][D]
-  int pieces, zparts, splits, ksteps;  // pieces 0: bwd_prep_kernel finds the maxima itself
-  int64_t width;    // columns of a piece of bwd_max_kernel
-};
 
 typedef uint32_t u4_any __attribute__((ext_vector_type(4), aligned(2)));
 
@@ -175,38 +145,6 @@ __device__ __forceinline__ void arrange_codes(const BwdArgs& a, int64_t i) {
     }
     out[b] = x;
   }
-}
-
-// The group codes of 16 vocabulary rows by k-tile, for bwd_few_kernel: thread i
-// takes those of one k-tile (or of the two that share a code of 256 columns).
-// As they are stored, a k-tile's wave finds the 16 bytes that it needs in 16
-// sectors, which took 11 us on one token of a 151936 x 4096 head; this, beside
-// the maxima, takes 2.
-template <typename C>
-__device__ __forceinline__ void arrange_groups(const BwdArgs& a, int64_t i) {
-  const int columns = a.ng / (int)sizeof(C);
-  const int64_t kk = i % columns, b = i / columns;
-  if (b >= a.nb) return;
-  const C* src = reinterpret_cast<const C*>(a.r_gcodes) + 16 * b * columns + kk;
-  C c[16];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) c[k] = src[k * columns];
-  u4* out = reinterpret_cast<u4*>(a.gt) + (kk * a.nb + b) * (int64_t)sizeof(C);
-#pragma unroll
-  for (int k = 0; k < (int)sizeof(C); ++k) {
-    u4 x;
-    __builtin_memcpy(&x, c + k * 16 / sizeof(C), 16);
-    out[k] = x;
-  }
-}
-
-__device__ __forceinline__ void arrange_groups(const BwdArgs& a, int64_t i) {
-  if (a.g == 32)
-    arrange_groups<uint32_t>(a, i);
-  else if (a.g == 64)
-    arrange_groups<uint16_t>(a, i);
-  else
-    arrange_groups<uint8_t>(a, i);
 }
 
 // Eight of them as fp16: byte u under the byte 0x64 is 1024 + u, exactly.
@@ -473,213 +411,6 @@ __global__ __launch_bounds__(kZsumThreads) void bwd_zsum_kernel(const BwdArgs a)
     }
     __syncthreads();
   }
-}
-
-// f(integral_constant<I>) for I = B .. E-1, unrolled at compile time
-template <int B, int E, class F>
-__device__ __forceinline__ void static_for(F&& f) {
-  if constexpr (B < E) {
-    f(std::integral_constant<int, B>{});
-    static_for<B + 1, E>(f);
-  }
-}
-
-// Place of 16-byte octet o (8 columns) of row k in a stage's fp16 tile of 64
-// rows x 256 columns: both the 16 rows that a wave writes at one octet and the
-// 4 rows x 4 octets that 32 lanes read at a time fall in different banks.
-__device__ __forceinline__ int tile_octet(int k, int o) {
-  return 32 * k + (o ^ (((k & 3) << 2) | ((k >> 1) & 3)));
-}
-
-typedef short s4 __attribute__((ext_vector_type(4)));
-typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-// Transposing read: of 16 lanes that point at 4 rows x 4 runs of 4 columns
-// (lane q at row q / 4, run q % 4), lane i receives column i of the 4 rows.
-__device__ __forceinline__ h4 read_tr(const _Float16* p) {
-  return __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)p));
-}
-
-// 32 TT tokens x 256 columns of dH per workgroup over a share of the
-// vocabulary, in stages of 64 vocabulary rows (4 MFMA steps).  The operands
-// come from LDS, 6 KB a wave and step for eight MFMAs, and the fragments of dY
-// and the unpacked tile are written there, 16 KB a step: 64% of the cycles
-// that the MFMAs take, so the two run side by side.
-// 4096 rows of 151936 x 4096: 4.1 ms, 1.25 PFLOP/s, MFMAs busy in 70% of the
-// cycles of a clock that the power limit holds at 1.64 GHz; a dense bf16
-// product of these sizes by the library, 3.6 to 4.1 ms.  (Four waves of 128 x
-// 128 read a third less from LDS, but one wave a SIMD waits for itself: 2%
-// slower.  Three workgroups' worth of registers do not exist at TT = 8.)
-template <int TT>
-struct MainShape {
-  static constexpr int WM = TT >= 4 ? 2 : 1, WN = 8 / WM;  // eight waves in WM rows
-  static constexpr int MT = TT / WM, NT = 8 / WN;          // 32 x 32 tiles of a wave
-  static constexpr int kFrags = 4 * TT;                    // 1 KB dY fragments of a stage
-  static constexpr int kLoads = kFrags / 8;                // of those, per wave
-  static_assert(kFrags % 8 == 0, "TT must be even");
-  static constexpr int kDepth = TT == 2 ? 4 : TT == 4 ? 2 : 1;  // stages whose loads are in flight
-};
-
-// kCodes: group codes of 128 columns of a row: 4 for g = 32, 2 for 64, else 1.
-template <int TT, int kCodes>
-__global__ __launch_bounds__(kMainThreads, TT >= 8 ? 2 : 4) void bwd_main_kernel(const BwdArgs a) {
-  using S = MainShape<TT>;
-  constexpr int kDepth = S::kDepth;
-  __shared__ h8 sA[2][S::kFrags][64];
-  __shared__ h8 sB[2][64 * 32];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / S::WN, wn = wave % S::WN;
-  const int CB = (int)((a.D + 255) / 256), ntiles = (int)(a.n32 / 32), TB = (ntiles + TT - 1) / TT;
-  // Workgroups are dealt to the XCDs round robin: each XCD gets a contiguous
-  // range of (split, token block, column block), so that those in one L2 share
-  // few streams of dY fragments, the larger of the two operands.
-  const int per = gridDim.x / kXcds, rem = gridDim.x % kXcds, x = blockIdx.x % kXcds;
-  const int item = x * per + std::min(x, rem) + blockIdx.x / kXcds;
-  const int cb = item % CB, tb = item / CB % TB, split = item / CB / TB;
-  const int stages = a.ksteps / 4;
-  const int s0 = (int)((int64_t)split * stages / a.splits), s1 = (int)((int64_t)(split + 1) * stages / a.splits);
-
-  // this wave's share of unpacking: one packed tile, 16 rows x 128 columns
-  const int blk = wave & 3, kth = wave >> 2;
-  const int kt = std::min(2 * cb + kth, a.nkt - 1);
-  const uint8_t* wsrc = a.r_codes + (int64_t)kt * a.nb * 1024 + lane * 16;
-  const uint8_t* csrc = a.r_gcodes + (lane & 15) * a.ng + kKTile * kt / a.g;
-  u4 w[kDepth];
-  uint32_t code[kDepth];
-  h8 av[kDepth][S::kLoads];
-  auto load = [&](int s, auto slot_) {
-    constexpr int slot = decltype(slot_)::value;
-    s = std::min(s, s1 - 1);  // past the end: a stage that is cached, never used
-    const int64_t b = std::min<int64_t>(4 * (int64_t)s + blk, a.nb - 1);  // past the last rows dY is zero
-    w[slot] = *reinterpret_cast<const u4*>(wsrc + b * 1024);
-    const uint8_t* c = csrc + 16 * b * a.ng;
-    code[slot] = kCodes == 4   ? *reinterpret_cast<const uint32_t*>(c)
-                 : kCodes == 2 ? *reinterpret_cast<const uint16_t*>(c)
-                               : *c;
-#pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) {
-      const int f = 8 * i + wave;
-      const int64_t tile = std::min(tb * TT + f / 4, ntiles - 1);
-      av[slot][i] = *reinterpret_cast<const h8*>(a.hf + ((tile * a.ksteps + 4 * s + f % 4) * 64 + lane) * 8);
-    }
-  };
-  // columns 32 d .. + 32 of the packed tile in a register slot to the LDS tile
-  auto unpack = [&](auto buf_, auto slot_, int d) {
-    constexpr int buf = decltype(buf_)::value, slot = decltype(slot_)::value;
-    const uint32_t c = kCodes == 4 ? (code[slot] >> (8 * d)) & 0xffu
-                       : kCodes == 2 ? (code[slot] >> (8 * (d >> 1))) & 0xffu
-                                     : code[slot];
-    sB[buf][tile_octet(16 * blk + (lane & 15), 16 * kth + 4 * d + (lane >> 4))] =
-        unpack_q4_scaled(w[slot][d], (_Float16)(float)c);
-  };
-  auto put_fragments = [&](auto buf_, auto slot_) {
-    constexpr int buf = decltype(buf_)::value, slot = decltype(slot_)::value;
-#pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) sA[buf][8 * i + wave][lane] = av[slot][i];
-  };
-
-  f16x acc[S::MT][S::NT] = {};
-  const int q = lane & 15, colhalf = (lane >> 4) & 1, khalf = lane >> 5;
-  // operands of an MFMA step, fetched while the step before it runs
-  h8 fa[2][S::MT], fb[2][S::NT];
-  auto fetch = [&](auto buf_, auto t_) {
-    constexpr int buf = decltype(buf_)::value, t = decltype(t_)::value, P = t & 1;
-    const _Float16* B = reinterpret_cast<const _Float16*>(sB[buf]);
-#pragma unroll
-    for (int c = 0; c < S::NT; ++c) {
-      const int ct = wn * S::NT + c;
-      h4 x[2];
-#pragma unroll
-      for (int rr = 0; rr < 2; ++rr) {
-        const int k = 16 * t + 8 * khalf + 4 * rr + q / 4;
-        x[rr] = read_tr(B + 8 * tile_octet(k, 4 * ct + 2 * colhalf + (q & 3) / 2) + 4 * (q & 1));
-      }
-      fb[P][c] = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-#pragma unroll
-    for (int m = 0; m < S::MT; ++m) fa[P][m] = sA[buf][4 * (wm * S::MT + m) + t][lane];
-  };
-  auto multiply = [&](auto t_) {
-    constexpr int P = decltype(t_)::value & 1;
-#pragma unroll
-    for (int m = 0; m < S::MT; ++m)
-#pragma unroll
-      for (int c = 0; c < S::NT; ++c) acc[m][c] = mfma32(fa[P][m], fb[P][c], acc[m][c]);
-  };
-  using I0 = std::integral_constant<int, 0>;
-  using I1 = std::integral_constant<int, 1>;
-  using I2 = std::integral_constant<int, 2>;
-  using I3 = std::integral_constant<int, 3>;
-  if (s0 < s1) {
-    constexpr int kUnroll = kDepth < 2 ? 2 : kDepth;
-    static_for<0, kDepth>([&](auto i) { load(s0 + decltype(i)::value, i); });
-    for (int d = 0; d < 4; ++d) unpack(I0{}, I0{}, d);
-    put_fragments(I0{}, I0{});
-    load(s0 + kDepth, I0{});
-    __syncthreads();
-    fetch(I0{}, I0{});
-    // A step's MFMAs, with what is around them dealt out between them: an LDS
-    // read, a little arithmetic and an LDS write behind each.  (4096 rows of
-    // 151936 x 4096: 2.5% of a call less than in the compiler's own order; with
-    // two or five instructions 1.5%, with the LDS read first 2.5% more.)
-    auto interleave = [] {
-      static_for<0, S::MT * S::NT>([](auto) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
-        __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);  // VALU
-        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);  // LDS write
-      });
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    // One stage from LDS tile i & 1: each step's operands are fetched, and the
-    // next stage unpacked to the other tile, while the step before multiplies;
-    // its last step multiplies behind the barrier that opens the other tile.
-    auto stage = [&](auto i_, int s) __attribute__((always_inline)) {
-      constexpr int i = decltype(i_)::value;
-      constexpr std::integral_constant<int, i & 1> buf{};
-      constexpr std::integral_constant<int, (i + 1) & 1> other{};
-      constexpr std::integral_constant<int, (i + 1) % kDepth> slot{};
-      fetch(buf, I1{});
-      unpack(other, slot, 0);
-      unpack(other, slot, 1);
-      multiply(I0{});
-      interleave();
-      fetch(buf, I2{});
-      unpack(other, slot, 2);
-      unpack(other, slot, 3);
-      multiply(I1{});
-      interleave();
-      fetch(buf, I3{});
-      put_fragments(other, slot);
-      load(s + 1 + kDepth, slot);
-      multiply(I2{});
-      interleave();
-      __syncthreads();
-      fetch(other, I0{});
-      multiply(I3{});
-      interleave();
-    };
-    // whole rounds without an exit inside (an exit costs 2%), then the rest
-    int g0 = s0;
-    for (; g0 + kUnroll <= s1; g0 += kUnroll)
-      static_for<0, kUnroll>([&](auto i) { stage(i, g0 + decltype(i)::value); });
-    static_for<0, kUnroll - 1>([&](auto i) {
-      if (g0 + decltype(i)::value < s1) stage(i, g0 + decltype(i)::value);
-    });
-  }
-  // columns sit in the tile in the order the unpacking gives them
-  const int c32 = lane & 31;
-#pragma unroll
-  for (int m = 0; m < S::MT; ++m)
-#pragma unroll
-    for (int c = 0; c < S::NT; ++c) {
-      const int64_t d = 256 * (int64_t)cb + 32 * (wn * S::NT + c) + 8 * (c32 >> 3) + k_order_h(c32 & 7);
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int64_t n = 32 * (int64_t)(tb * TT + wm * S::MT + m) + 8 * (v >> 2) + 4 * khalf + (v & 3);
-        if (n < a.N && d < a.D) a.part[((int64_t)split * a.N + n) * a.D + d] = acc[m][c][v];
-      }
-    }
 }
 
 constexpr int kFewWaves = kMainThreads / 64;
@@ -1242,7 +973,7 @@ __global__ __launch_bounds__(kFinishThreads, 2) void bwd_finish_many_kernel(cons
 
 // ------------------------------------------------------------------- host ---
 
-int main_tiles(int64_t N) { return N <= 64 ? 2 : N <= 128 ? 4 : 8; }
+}  // namespace
 
 // Parts of the vocabulary for the main kernel: the count that a model of its
 // time likes best, workgroups in rounds of the resident ones (two a CU for
@@ -1267,6 +998,8 @@ int main_splits(int64_t N, int64_t D, int64_t ranks, int64_t stages) {
   }
   return pick;
 }
+
+namespace {
 
 struct BwdLayout {
   int64_t rows, n32, ksteps, width;
@@ -1332,14 +1065,19 @@ void launch_few_codes(const BwdArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(bwd_few_kernel<kCodes>, grid, block, 0, s, a);
 }
 
-void launch_few(const BwdArgs& a, hipStream_t s) {
+}  // namespace
+
+hipError_t launch_bwd_few(const BwdArgs& a, hipStream_t s) {
   if (a.g == 32)
     launch_few_codes<4>(a, s);
   else if (a.g == 64)
     launch_few_codes<2>(a, s);
   else
     launch_few_codes<1>(a, s);
+  return hipGetLastError();
 }
+
+namespace {
 
 template <typename T>
 hipError_t launch_backward(const BwdArgs& a, hipStream_t s) {
@@ -1355,7 +1093,7 @@ hipError_t launch_backward(const BwdArgs& a, hipStream_t s) {
       hipLaunchKernelGGL((bwd_prep_kernel<T, false, false>), dim3(1, std::min(runs, 1024u)), dim3(64 * kPrepWaves), 0, s, a);
     else
       hipLaunchKernelGGL((bwd_prep_kernel<T, false, true>), dim3(2, runs), dim3(64 * kPrepWaves), 0, s, a);
-    launch_few(a, s);
+    if (const hipError_t e = launch_bwd_few(a, s)) return e;
   } else {
     hipLaunchKernelGGL((bwd_prep_kernel<T, true, false>),
                        dim3((unsigned)(a.n32 / 32), (unsigned)a.zparts, (unsigned)std::max<int64_t>(1, (ranks + kPrepWaves - 1) / kPrepWaves)),

@@ -138,6 +138,9 @@ struct FwdArgs {
   const int32_t* targets;     // [N] or null
 };
 
+// Whether archead_logits takes a call of n_tokens rows (of fp32 logits that
+// span less than 4 GiB).
+bool forward_takes(const archead_dims* d, int64_t n_tokens);
 // tile path: H and Z into the workspace, then the tile kernel
 hipError_t launch_prep(const FwdArgs& a, hipStream_t s);
 // parts of the hidden dimension in the tile path's fp32 Z ([parts][n32][r])

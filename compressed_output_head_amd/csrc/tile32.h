@@ -121,6 +121,25 @@ struct T32Split {
   int full, s;
 };
 
+// The exponentials' epilogue (tile32_exp_kernel): the logits of a piece of the
+// vocabulary, whole 256-row tiles [vt0, vt0 + vtiles), leave as the operand of
+// the product that follows, and as what the softmax's sum needs of them.
+struct T32Exp {
+  const int32_t* n_rows;  // rows of H that count; N and n32 of FwdArgs are the most there can be
+  const int32_t* labels;  // [N] by row of H
+  float c_hi, c_lo;       // log2(e) times the inverse temperature, as a pair
+  int vt0, vtiles;
+  _Float16* e;            // [n32/32][16 vtiles][64][8] operand fragments, lane l: row l % 32, vocabulary rows
+                          // 16 step + 8 (l / 32) .. + 8
+  float* stat;            // [8 vtiles][n32][2] by 32-row block: the exponent M, the sum of 2^(z - M + kExpTop)
+  float* y_label;         // [n32] the label's logit, written where it is met
+};
+// Operands are 2^(z - M + kExpTop), z = log2(e) times the scaled logit and M the
+// least whole number that none of a row's z in its 32-row block exceeds:
+// below 2^14, exact powers of two apart from block to block, and normal fp16
+// down to 2^-28 of the largest.
+constexpr int kExpTop = 14;
+
 // One 16-byte buffer-to-LDS copy per lane.  Kept out of the kernel template:
 // called from inside it directly, the builtin makes the host pass reject the
 // template's instantiation without a diagnostic, and no launch stub is made.
@@ -138,8 +157,9 @@ __device__ __forceinline__ void lds_copy16(__amdgpu_buffer_rsrc_t rs, void* dst,
 
 // ST: instead of storing Y, each workgroup reduces its 256 logits of every
 // token to a row-statistics piece, written to a.st_part[token][vt].
-template <int GC, int TT, bool ST>
-__global__ __launch_bounds__(kT32Threads, 1) void tile32_kernel(const FwdArgs a, const T32Split sp) {
+// EX: instead of storing Y, the exponentials' epilogue.
+template <int GC, int TT, bool ST, bool EX>
+__device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp, const T32Exp& ex) {
   constexpr int kT32TT = TT, kT32MT = TT;     // token tiles per workgroup and per wave
   constexpr int KS = t32_ks(TT);              // MFMA steps per stage
   constexpr int kLK = KS == 8 ? 3 : 2;        // log2(KS)
@@ -150,13 +170,21 @@ __global__ __launch_bounds__(kT32Threads, 1) void tile32_kernel(const FwdArgs a,
   __shared__ h8 sH0[kT32TT][KS][64], sH1[kT32TT][KS][64], sH2[kT32TT][KS][64], sH3[kT32TT][KS][64];
   extern __shared__ __align__(16) uint8_t sCode[];  // [256 rows][t32_code_stride(ng)], sized at launch
   __shared__ float sTok[kT32TT * 32][2];  // hscale, zscale of the workgroup's tokens
-  __shared__ int sTgt[ST ? kT32TT * 32 : 1];  // targets of the workgroup's tokens (statistics)
+  __shared__ int sTgt[ST || EX ? kT32TT * 32 : 1];  // targets of the workgroup's tokens (statistics, exponentials)
   __shared__ __align__(16) float sVR[kT32CB * 32], sVC[kT32CB * 32], sVW[kT32CB * 32];  // s_R, s_Ac, s_Aw
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = 0, wn = wave;  // wave row 0: every wave takes all the tokens
   const int g = lane >> 5, c32 = lane & 31;
-  const T32Grid G = t32_grid(a, TT);
+  T32Grid G = t32_grid(a, TT);
+  int whole_tiles = sp.full;
+  if constexpr (EX) {  // the tiles of the rows that count
+    G.ntiles = (*ex.n_rows + 31) >> 5;
+    G.ttiles = (G.ntiles + TT - 1) / TT;
+    G.vtiles = ex.vtiles;
+    whole_tiles = G.ttiles * G.vtiles;
+    if ((int)blockIdx.x >= whole_tiles) return;
+  }
 
   // Workgroups are dealt to the XCDs round robin.  Those that take whole
   // tiles are renumbered so each XCD owns one contiguous range of the walk
@@ -164,10 +192,10 @@ __global__ __launch_bounds__(kT32Threads, 1) void tile32_kernel(const FwdArgs a,
   // packed vocabulary tiles in its L2.  The rest take one part of the hidden
   // dimension of a split tile.
   const int b = blockIdx.x;
-  const bool split = b >= sp.full;
+  const bool split = !EX && b >= sp.full;
   int L, part = 0;
   if (!split) {
-    const int per = sp.full / kXcds, rem = sp.full % kXcds, x = b % kXcds;
+    const int per = whole_tiles / kXcds, rem = whole_tiles % kXcds, x = b % kXcds;
     L = x * per + (x < rem ? x : rem) + b / kXcds;
   } else {
     const int q = b - sp.full, j = q / sp.s;
@@ -176,6 +204,7 @@ __global__ __launch_bounds__(kT32Threads, 1) void tile32_kernel(const FwdArgs a,
   }
   int vt, ttile;
   t32_tile(G, L, vt, ttile);
+  if constexpr (EX) vt += ex.vt0;
   const int tt0 = ttile * kT32TT;           // first 32-token tile
   const int cb0 = vt * kT32CB + wn * kT32WCB;  // first vocabulary block of this wave
   // stages of 16 KS columns: all of them (at least 2), or this part's share
@@ -346,6 +375,7 @@ __global__ __launch_bounds__(kT32Threads, 1) void tile32_kernel(const FwdArgs a,
     sTok[tid][0] = a.hscale[tok];
     sTok[tid][1] = part == 0 ? a.zscale[tok] : 0.0f;  // the low-rank term goes with part 0 only
     if constexpr (ST) sTgt[tid] = a.targets && 32 * (int64_t)tt0 + tid < a.N ? a.targets[32 * (int64_t)tt0 + tid] : -1;
+    if constexpr (EX) sTgt[tid] = ex.labels[tok < a.N ? tok : a.N - 1];
   }
   static_assert(kT32Threads >= kT32CB * 32, "one thread per vocabulary row of the workgroup");
   if (tid < kT32CB * 32) {
@@ -468,6 +498,113 @@ __global__ __launch_bounds__(kT32Threads, 1) void tile32_kernel(const FwdArgs a,
   // runs of 4 consecutive logits of one token.  The low-rank term (Z hi/lo
   // against exact INT8 A codes, 16 ranks per MFMA step, one accumulator per
   // part) is added with the scales, and each run is stored at once.
+  if constexpr (EX) {
+    __syncthreads();  // every wave's Z copies (complete after the wait above) are visible
+    auto zfrag_at = [&](int tt, int rem) {  // as zfrag below
+      int z = (tt << zsh) + rem;
+      if (z > 4 * KS * kT32TT - 1) z = 4 * KS * kT32TT - 1;
+      const int slot = z / (KS * kT32TT), pos = z - slot * KS * kT32TT;
+      const h8* base = slot == 0 ? &sH0[0][0][0] : slot == 1 ? &sH1[0][0][0] : slot == 2 ? &sH2[0][0][0] : &sH3[0][0][0];
+      return base[pos * 64 + lane];
+    };
+    const int blk = kT32CB * (vt - ex.vt0) + wn;  // of the piece
+    const int v0 = 32 * (kT32CB * vt + wn) + 4 * g;
+    const float infinity = __builtin_huge_valf();
+    static_for<0, kT32MT>([&](auto M_) {
+      constexpr int m = decltype(M_)::value;
+      __builtin_amdgcn_sched_barrier(0);
+      if (tt0 + m >= G.ntiles) return;
+      f16x pc = {}, pw = {};
+      if (zlds) {
+#pragma unroll
+        for (int s = 0; s < kEpiLdsSteps; ++s)
+          if (s < esteps) {
+            const h8 zh = zfrag_at(m, 2 * s), zl = zfrag_at(m, 2 * s + 1);
+            const h8 av = unpack_i8x8(ac[0][s][0], ac[0][s][1]);
+            if (s < csteps) {
+              pc = mfma32(av, zh, pc);
+              pc = mfma32(av, zl, pc);
+            } else {
+              pw = mfma32(av, zh, pw);
+              pw = mfma32(av, zl, pw);
+            }
+          }
+      } else {
+        const h8* zf = reinterpret_cast<const h8*>(a.zf) + (int64_t)(tt0 + m) * 2 * esteps * 64 + lane;
+        for (int s = 0; s < esteps; ++s) {
+          const u2 code = a_code(0, s);
+          const h8 av = unpack_i8x8(code[0], code[1]);
+          f16x& p = s < csteps ? pc : pw;
+          p = mfma32(av, zf[2 * s * 64], p);
+          p = mfma32(av, zf[(2 * s + 1) * 64], p);
+        }
+      }
+      const float hs = sTok[32 * m + c32][0], zs = sTok[32 * m + c32][1];
+      const int label = sTgt[32 * m + c32];
+      float y[16];
+#pragma unroll
+      for (int vg = 0; vg < 4; ++vg) {
+        const int lr = 32 * wn + 8 * vg + 4 * g;
+        const f4 vr = *reinterpret_cast<const f4*>(&sVR[lr]);
+        const f4 vc = *reinterpret_cast<const f4*>(&sVC[lr]);
+        const f4 vw = *reinterpret_cast<const f4*>(&sVW[lr]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int v = 4 * vg + e;
+          y[v] = fmaf(zs, fmaf(vw[e], pw[v], vc[e] * pc[v]), hs * (vr[e] * acc[m][0][v]));
+        }
+      }
+      // the label has no part in the sums, nor have rows past the vocabulary
+      const unsigned d = (unsigned)(label - v0);
+      if (d < 28u && (d & 4u) == 0u) {
+        const int at = (int)(d >> 3) * 4 + (int)(d & 3u);
+        float yl = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          yl = i == at ? y[i] : yl;
+          y[i] = i == at ? -infinity : y[i];
+        }
+        if (32 * (int64_t)(tt0 + m) + c32 < a.N) ex.y_label[32 * (int64_t)(tt0 + m) + c32] = yl;
+      }
+      if (v0 + 28 > a.V) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (v0 + 8 * (i >> 2) + (i & 3) >= a.V) y[i] = -infinity;
+      }
+      float top = y[0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) top = fmaxf(top, y[i]);
+      top = fmaxf(top, __shfl_xor(top, 32));
+      // no entry, or none above -inf: operands of 0 (a row that is not finite shows in its sum)
+      const float M = ceilf(fmaf(top, ex.c_hi, top * ex.c_lo));
+      const bool none = top == -infinity;
+      const float low = none ? 0.0f : (float)kExpTop - M;
+      float sum = 0.0f;
+      uint32_t pk[8];
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        float x[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          x[j] = __builtin_amdgcn_exp2f(fmaf(y[i + j], ex.c_lo, fmaf(y[i + j], ex.c_hi, low)));
+          sum += x[j];
+        }
+        pk[i >> 1] = h2_bits(h2{(_Float16)x[0], (_Float16)x[1]});
+      }
+      sum += __shfl_xor(sum, 32);
+      const int64_t tok = 32 * (int64_t)(tt0 + m) + c32;
+      if (g == 0) reinterpret_cast<u2*>(ex.stat)[(int64_t)blk * a.n32 + tok] = u2{__float_as_uint(none ? -infinity : M), __float_as_uint(sum)};
+      // lane halves hold the two fours of each eight rows; a fragment wants eights in one lane
+      u4* out = reinterpret_cast<u4*>(ex.e) + ((int64_t)(tt0 + m) * 16 * ex.vtiles + 2 * blk) * 64 + lane;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const auto a0 = __builtin_amdgcn_permlane32_swap(pk[4 * s], pk[4 * s + 2], false, false);
+        const auto a1 = __builtin_amdgcn_permlane32_swap(pk[4 * s + 1], pk[4 * s + 3], false, false);
+        out[64 * s] = u4{(uint32_t)a0[0], (uint32_t)a1[0], (uint32_t)a0[1], (uint32_t)a1[1]};
+      }
+    });
+    return;
+  }
   const bool vec = ((uintptr_t)a.Y & 15) == 0 && (a.Y_stride & 3) == 0;
   // statistics pieces of this lane's token in each token tile
   RowStat st[ST ? kT32MT : 1];
@@ -755,6 +892,16 @@ __global__ __launch_bounds__(kT32Threads, 1) void tile32_kernel(const FwdArgs a,
 }
 
 #undef T32_SLOT
+
+template <int GC, int TT, bool ST>
+__global__ __launch_bounds__(kT32Threads, 1) void tile32_kernel(const FwdArgs a, const T32Split sp) {
+  tile32_body<GC, TT, ST, false>(a, sp, T32Exp{});
+}
+
+template <int GC, int TT>
+__global__ __launch_bounds__(kT32Threads, 1) void tile32_exp_kernel(const FwdArgs a, const T32Exp ex) {
+  tile32_body<GC, TT, false, true>(a, T32Split{0, 1}, ex);
+}
 
 // Y of the split tiles: the sum of each tile's sp.s partial tiles in part
 // order, in the output format.  Workgroup w takes token rows 4 (w % (8 TT))

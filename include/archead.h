@@ -632,6 +632,52 @@ ARCHEAD_API int archead_logits_backward_workspace_bytes(const archead_dims* d, i
 ARCHEAD_API int archead_logits_backward(const archead_tensor* dY, const archead_packed_head* head,
                                         archead_tensor* dH, void* stream);
 
+/* Inputs of the cross entropy, device arrays of N = H.rows elements, 4-byte
+ * aligned:
+ *   log p_n = log softmax(inv_temperature Y_n)[labels[n]],  Y = H W_hat^T
+ *   loss    = -sum_n weight[n] log p_n
+ * Rows of weight 0 do not count: their H may hold anything, their labels too;
+ * their log p and gradient are 0.  A row that counts with a label outside
+ * [0, V), or with logits that are not finite, has log p and gradient NaN, and
+ * so has the loss; it changes no other row. */
+typedef struct {
+  const int32_t* labels;
+  const float* weight;   /* NULL: 1 for every row */
+  float inv_temperature; /* > 0 */
+} archead_cross_entropy_inputs;
+
+/* Outputs; each pointer may be NULL (not computed). */
+typedef struct {
+  float* loss;              /* [1]; 0 for N = 0 */
+  float* logp;              /* [N] */
+  const archead_tensor* dH; /* bf16 [N][D] d loss / d H, any row stride */
+} archead_cross_entropy_outputs;
+
+/* Device workspace archead_cross_entropy needs for n_tokens rows.  A call of
+ * fewer rows may need more: ask for every number of rows that a workspace is
+ * kept for.  Pure host arithmetic.  E_NULL, E_DIMS, E_SHAPE, E_UNSUPPORTED. */
+ARCHEAD_API int archead_cross_entropy_workspace_bytes(const archead_dims* d, int64_t n_tokens, uint64_t* bytes);
+
+/* Enqueue the cross entropy of H's rows through a packed ARCHead head, with the
+ * hidden states' gradient, on `stream`.  The N x V logits are never held: the
+ * vocabulary (or few rows of all of it) is taken in pieces, and the exponentials
+ * of a piece are multiplied with the head at once, under a running maximum of
+ * each row.  Logits are fp32 as archead_logits computes them; sums of
+ * exponentials fp32 in short runs and fp64 from there, row numbers fp64; the
+ * label's own term is in no sum, so that 1 - p of a row that is sure of it keeps
+ * its digits in log p and in the gradient.  Exponentials enter the product
+ * rounded to fp16, dH is rounded to nearest even.  Two calls with the same
+ * arguments give the same bits.
+ *   H: bf16 [N][D], rows 16-byte aligned, N at most 2^22.  dH must not overlap
+ *   H; outputs share bytes with nothing else (E_SHAPE).
+ * head->workspace: at least archead_cross_entropy_workspace_bytes.  V at most
+ * 2^24, r_c + r_r at most 1024; calls that archead_logits does not take give
+ * E_UNSUPPORTED.  E_NULL, E_DIMS, E_DTYPE, E_SHAPE, E_UNSUPPORTED, E_VALUE,
+ * E_ALIGN, E_SIZE, E_WORKSPACE, E_HIP. */
+ARCHEAD_API int archead_cross_entropy(const archead_tensor* H, const archead_packed_head* head,
+                                      const archead_cross_entropy_inputs* in, const archead_cross_entropy_outputs* out,
+                                      void* stream);
+
 /* ---- In front of the head ------------------------------------------------
  * The norm that makes the head's input of the residual stream, its gradient,
  * and the product of its 8-bit output with a row-INT8 head. */
