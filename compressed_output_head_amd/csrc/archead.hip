@@ -132,6 +132,7 @@ WorkspaceLayout workspace_layout(const archead_dims* d, int64_t n_tokens, bool s
 
 bool forward_takes(const archead_dims* d, int64_t n_tokens) {
   const WorkspaceLayout W = workspace_layout(d, n_tokens);
+  if (W.decode) return true;
   FwdArgs a{};
   a.V = d->V;
   a.D = d->D;
@@ -141,7 +142,7 @@ bool forward_takes(const archead_dims* d, int64_t n_tokens) {
   a.r_c = d->r_c;
   a.r_r = d->r_r;
   a.ng = (int)(d->D / d->g);
-  return W.decode || tile32_eligible(a);
+  return tile32_eligible(a);
 }
 
 namespace {
@@ -519,6 +520,16 @@ int logits_impl(const archead_tensor* H, const archead_packed_head* head, archea
   if (e != hipSuccess) return ARCHEAD_E_HIP;
   return ARCHEAD_OK;
 }
+
+}  // namespace
+
+int tile_args(const archead_tensor* H, const archead_packed_head* head, FwdArgs& a) {
+  WorkspaceLayout W;
+  if (int rc = setup_args(H, head, false, a, W, false, 0)) return rc;
+  return tile32_eligible(a) ? ARCHEAD_OK : ARCHEAD_E_UNSUPPORTED;
+}
+
+namespace {
 
 constexpr int kMaxDevices = 64;
 // ---- allocation-free variant: the scratch address of each device ---------------

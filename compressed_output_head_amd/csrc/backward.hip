@@ -888,22 +888,6 @@ __global__ __launch_bounds__(kFinishThreads) void bwd_finish_kernel(const BwdArg
   }
 }
 
-typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
-// v as the sum of two bf16 numbers, to 2^-17 of it: v in [2^e, 2^(e+1)) leaves
-// at most 2^(e-8) to lo, whose own half step is 2^(e-17) below that.
-struct Bf16Pair {
-  bf8 hi, lo;
-};
-__device__ __forceinline__ Bf16Pair split_bf16(const float (&v)[8]) {
-  Bf16Pair p;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    p.hi[i] = (__bf16)v[i];
-    p.lo[i] = (__bf16)(v[i] - (float)p.hi[i]);
-  }
-  return p;
-}
-
 // Many rows: 32 rows x 128 columns of dH a wave, Z B on the bf16 MFMA with Z
 // and B as pairs of bf16 numbers (three products; bf16 has fp32's range, so
 // neither needs a scale).  What the pairs and the fourth product, of two lo's,

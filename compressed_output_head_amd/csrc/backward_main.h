@@ -342,6 +342,22 @@ __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& e
     }
 }
 
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+// v as the sum of two bf16 numbers, to 2^-17 of it: v in [2^e, 2^(e+1)) leaves
+// at most 2^(e-8) to lo, whose own half step is 2^(e-17) below that.
+struct Bf16Pair {
+  bf8 hi, lo;
+};
+__device__ __forceinline__ Bf16Pair split_bf16(const float (&v)[8]) {
+  Bf16Pair p;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    p.hi[i] = (__bf16)v[i];
+    p.lo[i] = (__bf16)(v[i] - (float)p.hi[i]);
+  }
+  return p;
+}
+
 template <int TT, int kCodes>
 __global__ __launch_bounds__(kMainThreads, TT >= 8 ? 2 : 4) void bwd_main_kernel(const BwdArgs a) {
   bwd_main_body<TT, kCodes, false>(a, MainExp{});

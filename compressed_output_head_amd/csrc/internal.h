@@ -138,6 +138,30 @@ struct FwdArgs {
   const int32_t* targets;     // [N] or null
 };
 
+// The exponentials' epilogue (tile32_exp_kernel): the logits of a piece of the
+// vocabulary, whole 256-row tiles [vt0, vt0 + vtiles), leave as the operand of
+// the product that follows, and as what the softmax's sum needs of them.
+struct T32Exp {
+  const int32_t* n_rows;  // rows of H that count; N and n32 of FwdArgs are the most there can be
+  const int32_t* labels;  // [N] by row of H
+  float c_hi, c_lo;       // log2(e) times the inverse temperature, as a pair
+  int vt0, vtiles;
+  _Float16* e;            // null, or [n32/32][16 vtiles][64][8] operand fragments, lane l: row l % 32, vocabulary rows
+                          // 16 step + 8 (l / 32) .. + 8
+  float* stat;            // [8 vtiles][n32][2] by 32-row block: the exponent M, the sum of 2^(z - M + kExpTop)
+  float* y_label;         // [n32] the label's logit, written where it is met
+};
+// Operands are 2^(z - M + kExpTop), z = log2(e) times the scaled logit and M the
+// least whole number that none of a row's z in its 32-row block exceeds:
+// below 2^14, exact powers of two apart from block to block, and normal fp16
+// down to 2^-28 of the largest.
+constexpr int kExpTop = 14;
+
+// FwdArgs of the tile path without split tiles (workspace_layout(d, N, false,
+// 0, false)), with the checks of archead_logits.
+int tile_args(const archead_tensor* H, const archead_packed_head* head, FwdArgs& a);
+// The tile kernel with the exponentials' epilogue on H and Z in place.
+hipError_t launch_tile_exp(const FwdArgs& a, const T32Exp& ex, hipStream_t s);
 // Whether archead_logits takes a call of n_tokens rows (of fp32 logits that
 // span less than 4 GiB).
 bool forward_takes(const archead_dims* d, int64_t n_tokens);

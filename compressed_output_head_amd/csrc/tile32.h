@@ -121,25 +121,6 @@ struct T32Split {
   int full, s;
 };
 
-// The exponentials' epilogue (tile32_exp_kernel): the logits of a piece of the
-// vocabulary, whole 256-row tiles [vt0, vt0 + vtiles), leave as the operand of
-// the product that follows, and as what the softmax's sum needs of them.
-struct T32Exp {
-  const int32_t* n_rows;  // rows of H that count; N and n32 of FwdArgs are the most there can be
-  const int32_t* labels;  // [N] by row of H
-  float c_hi, c_lo;       // log2(e) times the inverse temperature, as a pair
-  int vt0, vtiles;
-  _Float16* e;            // [n32/32][16 vtiles][64][8] operand fragments, lane l: row l % 32, vocabulary rows
-                          // 16 step + 8 (l / 32) .. + 8
-  float* stat;            // [8 vtiles][n32][2] by 32-row block: the exponent M, the sum of 2^(z - M + kExpTop)
-  float* y_label;         // [n32] the label's logit, written where it is met
-};
-// Operands are 2^(z - M + kExpTop), z = log2(e) times the scaled logit and M the
-// least whole number that none of a row's z in its 32-row block exceeds:
-// below 2^14, exact powers of two apart from block to block, and normal fp16
-// down to 2^-28 of the largest.
-constexpr int kExpTop = 14;
-
 // One 16-byte buffer-to-LDS copy per lane.  Kept out of the kernel template:
 // called from inside it directly, the builtin makes the host pass reject the
 // template's instantiation without a diagnostic, and no launch stub is made.
@@ -375,7 +356,10 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
     sTok[tid][0] = a.hscale[tok];
     sTok[tid][1] = part == 0 ? a.zscale[tok] : 0.0f;  // the low-rank term goes with part 0 only
     if constexpr (ST) sTgt[tid] = a.targets && 32 * (int64_t)tt0 + tid < a.N ? a.targets[32 * (int64_t)tt0 + tid] : -1;
-    if constexpr (EX) sTgt[tid] = ex.labels[tok < a.N ? tok : a.N - 1];
+    if constexpr (EX) {
+      const int label = ex.labels[tok < a.N ? tok : a.N - 1];
+      sTgt[tid] = label < a.V ? label : -1;
+    }
   }
   static_assert(kT32Threads >= kT32CB * 32, "one thread per vocabulary row of the workgroup");
   if (tid < kT32CB * 32) {
@@ -596,6 +580,7 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
       if (g == 0) reinterpret_cast<u2*>(ex.stat)[(int64_t)blk * a.n32 + tok] = u2{__float_as_uint(none ? -infinity : M), __float_as_uint(sum)};
       // lane halves hold the two fours of each eight rows; a fragment wants eights in one lane
       u4* out = reinterpret_cast<u4*>(ex.e) + ((int64_t)(tt0 + m) * 16 * ex.vtiles + 2 * blk) * 64 + lane;
+      if (!ex.e) return;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const auto a0 = __builtin_amdgcn_permlane32_swap(pk[4 * s], pk[4 * s + 2], false, false);
@@ -978,7 +963,7 @@ inline int t32_tt(const FwdArgs& a) { return a.D < 256 ? 8 : a.N <= 64 ? 2 : a.N
 
 // Workgroups of one kernel instance resident at once on the current device
 // (0 if unknown).
-static int t32_slots(const void* kernel, size_t lds) {
+inline int t32_slots(const void* kernel, size_t lds) {
   int dev = 0, cus = 0, per_cu = 0;
   if (hipGetDevice(&dev) != hipSuccess ||
       hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
@@ -992,7 +977,7 @@ static int t32_slots(const void* kernel, size_t lds) {
 // as that round has room for (at most a quarter of the stages, so every part
 // has at least four, and as many as the workspace holds).
 template <int TT>
-static T32Split t32_split(const FwdArgs& a, int tiles, int slots) {
+inline T32Split t32_split(const FwdArgs& a, int tiles, int slots) {
   const int rem = slots > 0 ? tiles % slots : 0;
   if (rem == 0 || !a.part) return T32Split{tiles, 1};
   const uint64_t tile_bytes = (uint64_t)TT * 32 * kT32CB * 32 * 4;

@@ -15,6 +15,14 @@
 //   xent_operand_kernel     e s_R, e s_Ac, e s_Aw as fp16 operands; log p
 //   bwd_few_kernel, bwd_few16_kernel (backward.hip)
 //   xent_finish_few_kernel  the splits' sums, Z B and the label's row to dH
+// More rows, those that count gathered, up to 4096 at a time; for every piece
+//   tile32_exp_kernel       the exponentials as fp16 operands, with an exponent
+//                           and a sum for each row and 32 entries
+//   xent_merge_kernel       the rows' running exponent and sum, and what brings
+//                           the piece and the sums before it to that exponent
+//   xent_z_kernel           e (s_A code) added to Z
+//   xent_main_kernel        e (s_R q4 c8) added to the sums
+// and at the end xent_rows_kernel (log p, Z), xent_finish_kernel (dH).
 #include <algorithm>
 
 #include "backward_main.h"
@@ -312,6 +320,403 @@ __global__ __launch_bounds__(kFinishThreads) void xent_finish_few_kernel(const X
   }
 }
 
+// ------------------------------------------------------------ many rows ---
+
+constexpr int64_t kChunkRows = 4096;                // rows that count, a pass
+constexpr uint64_t kPieceBytes = 128ull << 20;      // of a piece's operands
+constexpr int kHeadParts = 64, kHeadThreads = 256;
+constexpr int kOrderThreads = 1024;
+constexpr int kMergeSlices = 32;
+constexpr int kZThreads = 512, kZTiles = 4;         // rank tiles of a workgroup
+
+struct ManyArgs {
+  BwdArgs b;               // of a pass: N its most rows; hf the piece's operands, ksteps its steps
+  int64_t rows;            // of the call
+  const uint16_t* H;
+  int64_t h_stride;
+  const int32_t* labels;   // of the call, by row
+  const float* weight;
+  float tau;
+  float* logp;
+  uint16_t* dH;
+  int64_t dh_stride;
+  float* head_max;         // [kHeadParts][3]
+  float* scale;            // [3][2] powers of two for s_R, s_Ac, s_Aw and their inverses
+  int32_t* map;            // [rows] rows that count, in order
+  int32_t* label;          // [rows] their labels
+  int32_t* counts;         // [passes] of each pass
+  double* terms;           // [rows] -w log p by row of the call
+  uint16_t* Hc;            // [n32][D] gathered H
+  float* stat;             // [blocks][n32][2]
+  uint32_t* factor;        // [blocks][n32]
+  float* alpha;            // [n32]
+  float* top;              // [n32] running exponent
+  double* sum;             // [n32] running sum
+  float* y_label;          // [n32]
+  RowOut* row;             // [n32]
+  _Float16* af;            // [rank tiles][16 vtiles of V][64][8] s_A code
+  int64_t asteps;          // steps of af
+  int pass, blocks, first, step0;
+};
+
+// Largest |s_R|, |s_Ac|, |s_Aw| of a part of the vocabulary.
+__global__ __launch_bounds__(kHeadThreads) void xent_head_kernel(const ManyArgs a) {
+  __shared__ float buf[kHeadThreads / 64][3];
+  float m[3] = {};
+  for (int64_t v = (int64_t)blockIdx.x * kHeadThreads + threadIdx.x; v < a.b.V; v += kHeadParts * kHeadThreads) {
+    float s[3];
+    scales_of(a.b, v, s);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) m[q] = fmaxf(m[q], fabsf(s[q]));
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    m[q] = wave_max(m[q]);
+    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6][q] = m[q];
+  }
+  __syncthreads();
+  if (threadIdx.x < 3) {
+    float t = buf[0][threadIdx.x];
+    for (int w = 1; w < kHeadThreads / 64; ++w) t = fmaxf(t, buf[w][threadIdx.x]);
+    a.head_max[3 * blockIdx.x + threadIdx.x] = t;
+  }
+}
+
+// One workgroup: the rows that count, in order; the powers of two that bring
+// the largest |q4 c8 s_R| (2040 at most before s_R) and |code s_A| to [2^14, 2^15).
+__global__ __launch_bounds__(kOrderThreads) void xent_order_kernel(const ManyArgs a, int passes) {
+  __shared__ int sCount[kOrderThreads];
+  const int tid = threadIdx.x;
+  if (tid < 3) {
+    float m = 0.0f;
+    for (int p = 0; p < kHeadParts; ++p) m = fmaxf(m, a.head_max[3 * p + tid]);
+    const int e = std::max(-126, std::min(row_exponent(m * (tid == 0 ? 2040.0f : 128.0f)), 126));
+    a.scale[2 * tid] = ldexpf(1.0f, e);
+    a.scale[2 * tid + 1] = ldexpf(1.0f, -e);
+  }
+  const int64_t per = (a.rows + kOrderThreads - 1) / kOrderThreads, n0 = std::min(tid * per, a.rows), n1 = std::min(n0 + per, a.rows);
+  int mine = 0;
+  for (int64_t n = n0; n < n1; ++n) mine += !a.weight || a.weight[n] != 0.0f;
+  sCount[tid] = mine;
+  __syncthreads();
+  for (int o = 1; o < kOrderThreads; o *= 2) {  // inclusive sums
+    const int x = tid >= o ? sCount[tid - o] : 0;
+    __syncthreads();
+    sCount[tid] += x;
+    __syncthreads();
+  }
+  int at = sCount[tid] - mine;
+  for (int64_t n = n0; n < n1; ++n) {
+    if (!a.weight || a.weight[n] != 0.0f) {
+      a.map[at] = (int32_t)n;
+      a.label[at++] = a.labels[n];
+    } else {
+      a.terms[n] = 0.0;
+      if (a.logp) a.logp[n] = 0.0f;
+    }
+  }
+  const int64_t total = sCount[kOrderThreads - 1];
+  for (int p = tid; p < passes; p += kOrderThreads)
+    a.counts[p] = (int32_t)std::max<int64_t>(0, std::min(total - p * kChunkRows, kChunkRows));
+}
+
+// The gradient of rows that do not count.
+__global__ __launch_bounds__(256) void xent_zero_kernel(const ManyArgs a) {
+  const int64_t n = blockIdx.x;
+  if (a.weight[n] != 0.0f) return;
+  for (int64_t d = threadIdx.x; d < a.b.D; d += 256) a.dH[n * a.dh_stride + d] = 0;
+}
+
+// Row blockIdx.x of the pass: its H (zeros behind the last one that counts),
+// and no sums.
+__global__ __launch_bounds__(256) void xent_gather_kernel(const ManyArgs a) {
+  const int64_t i = blockIdx.x, count = a.counts[a.pass];
+  if (threadIdx.x == 0) {
+    a.top[i] = -__builtin_huge_valf();
+    a.sum[i] = 0.0;
+    a.y_label[i] = __builtin_nanf("");  // stays where the label is outside the vocabulary
+  }
+  const u4* src = reinterpret_cast<const u4*>(a.H + (i < count ? (int64_t)a.map[a.pass * kChunkRows + i] : 0) * a.h_stride);
+  u4* dst = reinterpret_cast<u4*>(a.Hc + i * a.b.D);
+  for (int64_t c = threadIdx.x; c < a.b.D / 8; c += 256) dst[c] = i < count ? src[c] : u4{};
+}
+
+// The A codes times their row scales as operands of the product along the
+// vocabulary: rank tile t, step, lane (rank lane % 32, rows 16 step + 8 (lane
+// / 32) .. + 8).  Thread i takes four ranks of eight rows.
+__global__ __launch_bounds__(256) void xent_factors_kernel(const ManyArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const BwdArgs& b = a.b;
+  const int quad = (int)(i & 7), half = (int)(i >> 3) & 1;
+  const int64_t step = (i >> 4) % a.asteps, t = (i >> 4) / a.asteps;
+  if (t >= b.nct + b.nwt) return;
+  const bool in_c = t < b.nct;
+  const int j = 32 * (int)(in_c ? t : t - b.nct) + 4 * quad, r = b.r_c + b.r_r;
+  const bool valid = j < (in_c ? b.r_c : b.r_r);  // ranks come in eights
+  const float scale = a.scale[in_c ? 2 : 4];
+  const int64_t v = 16 * step + 8 * half;
+  h8 out[4] = {};
+  if (valid && v < 16 * b.nb) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(b.a_codes + (v + k) * r + (in_c ? 0 : b.r_c) + j);
+      const float s = f16_to_f32(b.a_scales[(v + k) * b.nA + (in_c ? 0 : b.nA - 1)]) * scale;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[e][k] = (_Float16)(s * (float)(int8_t)(w >> (8 * e)));
+    }
+  }
+  h8* dst = reinterpret_cast<h8*>(a.af) + (t * a.asteps + step) * 64 + 32 * half + 4 * quad;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) dst[e] = out[e];
+}
+
+// 2^-j as a product of two fp16 numbers (0 below 2^-44: such an operand is
+// below fp16's least).
+__device__ __forceinline__ uint32_t factor_of(float j) {
+  if (!(j >= 0.0f && j <= 44.0f)) return 0;
+  const int a = std::min((int)j, 20), b = (int)j - a;
+  auto half_power = [](int k) { return k <= 14 ? (uint32_t)(15 - k) << 10 : 1u << (24 - k); };
+  return half_power(a) | half_power(b) << 16;
+}
+
+// 32 rows a workgroup, kMergeSlices threads each: the running exponent of the
+// piece's blocks and of those before, the sum at that exponent, and the factors.
+__global__ __launch_bounds__(32 * kMergeSlices) void xent_merge_kernel(const ManyArgs a) {
+  __shared__ float sTop[kMergeSlices][32];
+  __shared__ double sSum[kMergeSlices][32];
+  const int c = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int64_t n = 32 * (int64_t)blockIdx.x + c;
+  if (32 * (int64_t)blockIdx.x >= a.counts[a.pass]) return;
+  const float infinity = __builtin_huge_valf();
+  const u2* stat = reinterpret_cast<const u2*>(a.stat) + n;
+  float m = -infinity;
+#pragma unroll 8
+  for (int k = slice; k < a.blocks; k += kMergeSlices) m = fmaxf(m, __uint_as_float(stat[(int64_t)k * a.b.n32][0]));
+  sTop[slice][c] = m;
+  __syncthreads();
+  const float old = a.top[n];
+  m = old;
+  for (int k = 0; k < kMergeSlices; ++k) m = fmaxf(m, sTop[k][c]);
+  double s = 0.0;
+  for (int k = slice; k < a.blocks; k += kMergeSlices) {
+    const u2 x = stat[(int64_t)k * a.b.n32];
+    const float j = m - __uint_as_float(x[0]);  // whole, or not finite where the block has no entry or the row is not
+    const float sum = __uint_as_float(x[1]);
+    s += j <= 1000.0f ? ldexp((double)sum, -(int)j) : (sum == sum ? 0.0 : (double)sum);
+    a.factor[(int64_t)k * a.b.n32 + n] = factor_of(j);
+  }
+  sSum[slice][c] = s;
+  __syncthreads();
+  if (slice == 0) {
+    const float j = m - old;
+    const bool kept = j <= 1000.0f;
+    s = kept ? ldexp(a.sum[n], -(int)j) : (a.sum[n] == a.sum[n] ? 0.0 : a.sum[n]);
+    for (int k = 0; k < kMergeSlices; ++k) s += sSum[k][c];
+    a.sum[n] = s;
+    a.top[n] = m;
+    a.alpha[n] = kept ? ldexpf(1.0f, -(int)j) : 0.0f;
+  }
+}
+
+// 64 rows x kZTiles rank tiles a workgroup over part blockIdx.y of the piece's
+// steps, dealt to the waves; their sums are added up in order and then to the
+// part's sums of the pieces before.
+__global__ __launch_bounds__(kZThreads, 2) void xent_z_kernel(const ManyArgs a) {
+  constexpr int kWaves = kZThreads / 64;
+  __shared__ float red[kWaves / 2][kZTiles][16][64];
+  const BwdArgs& b = a.b;
+  const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t count = a.counts[a.pass], ntiles = (count + 31) / 32, tile0 = 2 * (int64_t)blockIdx.x;
+  if (tile0 >= ntiles) return;
+  const int tiles = b.nct + b.nwt, t0 = kZTiles * (int)blockIdx.z, parts = gridDim.y, r = b.r_c + b.r_r;
+  const int k0 = (int)((int64_t)blockIdx.y * b.ksteps / parts), k1 = (int)((int64_t)(blockIdx.y + 1) * b.ksteps / parts);
+  const h8* e[2];
+  const uint32_t* fac[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t tile = std::min(tile0 + i, ntiles - 1);
+    e[i] = reinterpret_cast<const h8*>(b.hf) + tile * b.ksteps * 64 + lane;
+    fac[i] = a.factor + 32 * tile + c32;
+  }
+  const h8* af = reinterpret_cast<const h8*>(a.af) + (int64_t)a.step0 * 64 + lane;
+  f16x acc[2][kZTiles] = {};
+#pragma unroll 2
+  for (int k = k0 + wave; k < k1; k += kWaves) {
+    h8 x[2], y[kZTiles];
+    uint32_t f[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[i] = e[i][(int64_t)k * 64];
+      f[i] = fac[i][(int64_t)(k / 2) * b.n32];
+    }
+#pragma unroll
+    for (int t = 0; t < kZTiles; ++t)  // past the last tile: that one, not stored
+      y[t] = af[((int64_t)std::min(t0 + t, tiles - 1) * a.asteps + std::min<int64_t>(k, a.asteps - 1 - a.step0)) * 64];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const h2 g = bits_h2(f[i]);
+      x[i] = x[i] * h8{g[0], g[0], g[0], g[0], g[0], g[0], g[0], g[0]};
+      x[i] = x[i] * h8{g[1], g[1], g[1], g[1], g[1], g[1], g[1], g[1]};
+#pragma unroll
+      for (int t = 0; t < kZTiles; ++t) acc[i][t] = mfma32(x[i], y[t], acc[i][t]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int h = kWaves / 2; h > 0; h >>= 1) {
+      __syncthreads();
+      if (wave >= h && wave < 2 * h) {
+#pragma unroll
+        for (int t = 0; t < kZTiles; ++t)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) red[wave - h][t][v][lane] = acc[i][t][v];
+      }
+      __syncthreads();
+      if (wave < h) {
+#pragma unroll
+        for (int t = 0; t < kZTiles; ++t)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[i][t][v] += red[wave][t][v][lane];
+      }
+    }
+    if (wave != 0) continue;
+#pragma unroll
+    for (int t = 0; t < kZTiles; ++t) {
+      const bool in_c = t0 + t < b.nct;
+      const int j = 32 * (in_c ? t0 + t : t0 + t - b.nct) + c32;
+      if (t0 + t >= tiles || j >= (in_c ? b.r_c : b.r_r)) continue;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int64_t n = 32 * (tile0 + i) + 8 * (v >> 2) + 4 * half + (v & 3);
+        if (n >= count) continue;
+        float* z = b.zpart + ((int64_t)blockIdx.y * b.n32 + n) * r + (in_c ? 0 : b.r_c) + j;
+        *z = a.first ? acc[i][t][v] : fmaf(a.alpha[n], *z, acc[i][t][v]);
+      }
+    }
+  }
+}
+
+template <int TT, int kCodes>
+__global__ __launch_bounds__(kMainThreads, 2) void xent_main_kernel(const BwdArgs a, const MainExp ex) {
+  bwd_main_body<TT, kCodes, true>(a, ex);
+}
+
+// Row blockIdx.x of the pass: log p and its term of the loss, the factors of
+// its sums, and Z less the label's A, with those factors.
+__global__ __launch_bounds__(256) void xent_rows_kernel(const ManyArgs a) {
+  __shared__ RowOut sOut;
+  const BwdArgs& b = a.b;
+  const int64_t i = blockIdx.x;
+  if (i >= a.counts[a.pass]) return;
+  const int64_t at = a.pass * kChunkRows + i, label = a.label[at], l = label >= 0 && label < b.V ? label : 0;
+  if (threadIdx.x == 0) {
+    const int64_t n = a.map[at];
+    const double w = a.weight ? (double)a.weight[n] : 1.0, s = a.sum[i];
+    const float yl = a.y_label[i];
+    double logp = 0.0, q = 0.0;
+    RowOut out{0.0f, 0.0f};
+    if (!(fabsf(yl) < __builtin_huge_valf())) {
+      logp = q = __builtin_nan("");
+      out.mean = (float)q;
+    } else if (s != 0.0) {  // (a vocabulary of one entry: p = 1)
+      const double d = log(s) + ((double)a.top[i] - kExpTop) * 0.6931471805599453 - (double)a.tau * (double)yl;
+      logp = d == d ? -(fmax(d, 0.0) + log1p(exp(-fabs(d)))) : d;
+      q = 1.0 / (1.0 + exp(-d));
+      out.mean = (float)(w * (double)a.tau * q / s);
+    }
+    out.label = (float)(w * (double)a.tau * q);
+    a.terms[n] = -w * logp;
+    if (a.logp) a.logp[n] = (float)logp;
+    a.row[i] = sOut = out;
+  }
+  if (!a.dH) return;
+  __syncthreads();
+  const int r = b.r_c + b.r_r;
+  for (int j = threadIdx.x; j < r; j += 256) {
+    float z = 0.0f;
+#pragma unroll 8
+    for (int p = 0; p < b.zparts; ++p) z += b.zpart[((int64_t)p * b.n32 + i) * r + j];
+    const bool in_c = j < b.r_c;
+    const float al = (float)b.a_codes[l * r + j] * f16_to_f32(b.a_scales[l * b.nA + (in_c ? 0 : b.nA - 1)]);
+    b.z[i * r + j] = sOut.mean * (z * a.scale[in_c ? 3 : 5]) - sOut.label * al;
+  }
+}
+
+// 32 rows x 128 columns of dH a wave: the splits' sums, the label's row of the
+// residual, and Z B on the bf16 MFMA with Z and B as pairs of bf16 numbers (three
+// products, 2^-15 of |Z| |B| at most).  Tile c of four holds the columns 4 i +
+// c, so that a lane has four neighbouring ones of a row.
+__global__ __launch_bounds__(kFinishThreads, 2) void xent_finish_kernel(const ManyArgs a) {
+  constexpr int kWaves = kFinishThreads / 64;
+  const BwdArgs& b = a.b;
+  const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = b.r_c + b.r_r;
+  const int64_t n0 = 32 * (int64_t)blockIdx.x, kt = (int64_t)blockIdx.y * kWaves + wave, count = a.counts[a.pass];
+  if (n0 >= count || kt >= b.nkt) return;
+  const int64_t d = kKTile * kt + 4 * c32, group = d / b.g;
+  // row of element v of a result tile; past the last row that one
+  auto row = [&](int v) { return std::min<int64_t>(n0 + 8 * (v >> 2) + 4 * half + (v & 3), count - 1); };
+  f16x acc[4] = {};
+  for (int p = 0; p < b.splits; ++p) {
+    f4 y[16];
+#pragma unroll
+    for (int v = 0; v < 16; ++v) y[v] = *reinterpret_cast<const f4*>(b.part + ((int64_t)p * b.N + row(v)) * b.D + d);
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[c][v] += y[v][c];
+  }
+  const float undo = a.scale[1];
+#pragma unroll
+  for (int v = 0; v < 16; ++v) {
+    const RowOut out = a.row[row(v)];
+    const int64_t label = a.label[a.pass * kChunkRows + row(v)], l = label >= 0 && label < b.V ? label : 0;
+    const uint8_t* tile = b.r_codes + (kt * b.nb + l / 16) * kTileBytes;
+    const uint32_t w = *reinterpret_cast<const uint16_t*>(tile + 16 * (l % 16 + 16 * (c32 % 8 / 2)) + 4 * (c32 / 8) + 2 * (c32 % 2));
+    const float s = out.label * ((float)b.r_gcodes[l * b.ng + group] * f16_to_f32(b.r_rowscale[l]));
+    const float f = undo * out.mean;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c][v] = fmaf(-s, (float)((int32_t)(w << (28 - 4 * c)) >> 28), acc[c][v] * f);
+  }
+  const float* zrow = b.z + std::min<int64_t>(n0 + c32, count - 1) * r;
+  for (int j0 = 0; j0 < r; j0 += 16) {
+    const bool in = j0 + 8 * half < r;  // ranks come in eights
+    const int j = in ? j0 + 8 * half : j0;
+    uint32_t code[8];
+    float z[8], s[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      code[k] = *reinterpret_cast<const uint32_t*>(b.b_codes + (int64_t)(j + k) * b.D + d);
+      s[k] = f16_to_f32(b.b_scales[(int64_t)(j + k) * b.ng + group]);
+      z[k] = zrow[j + k];
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) z[k] = in ? z[k] : 0.0f;
+    const Bf16Pair zp = split_bf16(z);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = s[k] * (float)(int8_t)(code[k] >> (8 * c));
+      const Bf16Pair bp = split_bf16(x);
+      acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(zp.hi, bp.lo, acc[c], 0, 0, 0);
+      acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(zp.lo, bp.hi, acc[c], 0, 0, 0);
+      acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(zp.hi, bp.hi, acc[c], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < 16; ++v) {
+    const int64_t i = n0 + 8 * (v >> 2) + 4 * half + (v & 3);
+    if (i >= count) continue;
+    typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(2)));
+    *reinterpret_cast<u2_any*>(a.dH + (int64_t)a.map[a.pass * kChunkRows + i] * a.dh_stride + d) =
+        pack_bf16x4(acc[0][v], acc[1][v], acc[2][v], acc[3][v]);
+  }
+}
+
 // The loss: the rows' terms in fp64, in a fixed order.
 constexpr int kTotalThreads = 1024;
 __global__ __launch_bounds__(kTotalThreads) void xent_total_kernel(const double* terms, int64_t N, float* loss) {
@@ -338,10 +743,8 @@ struct XentLayout {
   uint64_t terms, y, fwd, fwd_bytes, piece, row, rscale, hf, gt, zpart, part, total;
 };
 
-// Of a pass of `rows` rows in a call of N.
-XentLayout xent_layout(const archead_dims* d, int64_t N, int64_t rows) {
+XentLayout xent_layout(const archead_dims* d, int64_t rows) {
   XentLayout L{};
-  if (N <= 0 || rows <= 0) return L;
   const uint64_t V128 = round_up((uint64_t)d->V, 128);
   const int64_t r = d->r_c + d->r_r;
   L.n32 = 32;
@@ -354,7 +757,7 @@ XentLayout xent_layout(const archead_dims* d, int64_t N, int64_t rows) {
     L.total += round_up(bytes, ARCHEAD_ALIGNMENT);
     return at;
   };
-  L.terms = take((uint64_t)N * 8);
+  L.terms = take((uint64_t)rows * 8);
   L.y = take((uint64_t)rows * (uint64_t)y_stride_of(d) * 4);
   L.fwd_bytes = workspace_layout(d, rows).total;
   L.fwd = take(L.fwd_bytes);
@@ -368,9 +771,6 @@ XentLayout xent_layout(const archead_dims* d, int64_t N, int64_t rows) {
   return L;
 }
 
-uint64_t xent_bytes(const archead_dims* d, int64_t N) {
-  return std::max(xent_layout(d, N, std::min(N, kFewTokens)).total, xent_layout(d, N, N % kFewTokens).total);
-}
 
 int check_xent_dims(const archead_dims* d) {
   if (int rc = check_kernel_dims(d)) return rc;
@@ -379,29 +779,13 @@ int check_xent_dims(const archead_dims* d) {
   return ARCHEAD_OK;
 }
 
-// A pass of few rows, from row n0 of the call on.
-int launch_few_rows(const archead_tensor* H, const archead_packed_head* head, const archead_cross_entropy_inputs* in,
-                    const archead_cross_entropy_outputs* out, int64_t n0, int64_t rows, hipStream_t s) {
+void set_head(const archead_packed_head* head, BwdArgs& b) {
   const archead_dims* d = &head->dims;
-  const XentLayout L = xent_layout(d, H->rows, rows);
   archead_layout P;
   compute_layout(d, &P);
   const uint8_t* buf = static_cast<const uint8_t*>(head->buffer);
-  uint8_t* ws = static_cast<uint8_t*>(head->workspace);
-  archead_tensor h = *H;
-  h.data = static_cast<uint16_t*>(H->data) + n0 * H->row_stride;
-  h.rows = rows;
-  archead_tensor y{ws + L.y, rows, d->V, y_stride_of(d), ARCHEAD_F32};
-  archead_packed_head p = *head;
-  p.workspace = ws + L.fwd;
-  p.workspace_bytes = L.fwd_bytes;
-  if (int rc = archead_logits(&h, &p, &y, s)) return rc;
-  XentArgs a{};
-  BwdArgs& b = a.b;
   b.V = d->V;
   b.D = d->D;
-  b.N = rows;
-  b.n32 = L.n32;
   b.nb = P.padded_rows / 16;
   b.r_c = d->r_c;
   b.r_r = d->r_r;
@@ -418,6 +802,31 @@ int launch_few_rows(const archead_tensor* H, const archead_packed_head* head, co
   b.a_scales = reinterpret_cast<const uint16_t*>(buf + P.a_scales.offset);
   b.b_codes = reinterpret_cast<const int8_t*>(buf + P.b_codes.offset);
   b.b_scales = reinterpret_cast<const uint16_t*>(buf + P.b_scales.offset);
+}
+
+// log2(e) tau as a pair of fp32 numbers
+void set_exponent(float tau, float& hi, float& lo) {
+  const double c = 1.4426950408889634 * (double)tau;
+  hi = (float)c;
+  lo = (float)(c - (double)hi);
+}
+
+int launch_few_rows(const archead_tensor* H, const archead_packed_head* head, const archead_cross_entropy_inputs* in,
+                    const archead_cross_entropy_outputs* out, hipStream_t s) {
+  const archead_dims* d = &head->dims;
+  const int64_t rows = H->rows;
+  const XentLayout L = xent_layout(d, rows);
+  uint8_t* ws = static_cast<uint8_t*>(head->workspace);
+  archead_tensor y{ws + L.y, rows, d->V, y_stride_of(d), ARCHEAD_F32};
+  archead_packed_head p = *head;
+  p.workspace = ws + L.fwd;
+  p.workspace_bytes = L.fwd_bytes;
+  if (int rc = archead_logits(H, &p, &y, s)) return rc;
+  XentArgs a{};
+  BwdArgs& b = a.b;
+  set_head(head, b);
+  b.N = rows;
+  b.n32 = L.n32;
   b.rscale = reinterpret_cast<float*>(ws + L.rscale);
   b.hf = reinterpret_cast<_Float16*>(ws + L.hf);
   b.gt = ws + L.gt;
@@ -427,20 +836,18 @@ int launch_few_rows(const archead_tensor* H, const archead_packed_head* head, co
   b.ksteps = (int)L.ksteps;
   a.Y = reinterpret_cast<const float*>(ws + L.y);
   a.y_stride = y.row_stride;
-  a.labels = in->labels + n0;
-  a.weight = in->weight ? in->weight + n0 : nullptr;
+  a.labels = in->labels;
+  a.weight = in->weight;
   a.tau = in->inv_temperature;
-  const double c = 1.4426950408889634 * (double)in->inv_temperature;
-  a.c_hi = (float)c;
-  a.c_lo = (float)(c - (double)a.c_hi);
-  a.logp = out->logp ? out->logp + n0 : nullptr;
+  set_exponent(a.tau, a.c_hi, a.c_lo);
+  a.logp = out->logp;
   if (out->dH) {
-    a.dH = static_cast<uint16_t*>(out->dH->data) + n0 * out->dH->row_stride;
+    a.dH = static_cast<uint16_t*>(out->dH->data);
     a.dh_stride = out->dH->row_stride;
   }
   a.piece = reinterpret_cast<Piece*>(ws + L.piece);
   a.row = reinterpret_cast<RowOut*>(ws + L.row);
-  a.terms = reinterpret_cast<double*>(ws + L.terms) + n0;
+  a.terms = reinterpret_cast<double*>(ws + L.terms);
   a.pieces = L.pieces;
   a.width = L.width;
   const int64_t arrange = a.dH ? b.nb * b.ng / std::max(1, kKTile / b.g) : 0;
@@ -453,6 +860,176 @@ int launch_few_rows(const archead_tensor* H, const archead_packed_head* head, co
   hipLaunchKernelGGL(xent_finish_few_kernel, dim3((unsigned)rows, (unsigned)((b.D + 255) / 256)), dim3(kFinishThreads),
                      (size_t)(b.r_c + b.r_r) * 4, s, a);
   return hipGetLastError() == hipSuccess ? ARCHEAD_OK : ARCHEAD_E_HIP;
+}
+
+// ---- many rows
+
+struct ManyLayout {
+  int64_t rows, n32, vtiles, piece;  // rows of a pass; 256-row tiles of the vocabulary, of a piece
+  int splits, zparts, passes;
+  uint64_t terms, head_max, scale, map, label, counts, fwd, fwd_bytes, Hc, e, stat, factor, alpha, top, sum, y_label, row, af,
+      zpart, z, part, total;
+};
+
+ManyLayout many_layout(const archead_dims* d, int64_t N) {
+  ManyLayout L{};
+  L.rows = std::min(N, kChunkRows);
+  L.passes = (int)((N + kChunkRows - 1) / kChunkRows);
+  L.n32 = (int64_t)round_up((uint64_t)L.rows, 32);
+  L.vtiles = (d->V + 255) / 256;
+  // whole rounds of 256 workgroups of 256 rows where there are several pieces
+  const int64_t most = std::max<int64_t>(1, (int64_t)(kPieceBytes / ((uint64_t)L.n32 * 512)));
+  const int64_t pieces = (L.vtiles + most - 1) / most;
+  L.piece = (L.vtiles + pieces - 1) / pieces;
+  if (pieces > 1) L.piece = std::min((int64_t)round_up((uint64_t)L.piece, 16), std::max<int64_t>(most / 16 * 16, 1));
+  L.splits = main_splits(L.rows, d->D, 0, 4 * L.piece);
+  const int64_t r = d->r_c + d->r_r, tiles = (d->r_c + 31) / 32 + (d->r_r + 31) / 32;
+  const int64_t groups = (L.n32 + 63) / 64 * std::max<int64_t>(1, (tiles + kZTiles - 1) / kZTiles);
+  L.zparts = (int)std::max<int64_t>(1, std::min<int64_t>({(256 + groups - 1) / groups, L.piece, 64}));
+  auto take = [&](uint64_t bytes) {
+    const uint64_t at = L.total;
+    L.total += round_up(bytes, ARCHEAD_ALIGNMENT);
+    return at;
+  };
+  const uint64_t n32 = (uint64_t)L.n32, blocks = 8 * (uint64_t)L.piece;
+  L.terms = take((uint64_t)N * 8);
+  L.head_max = take(kHeadParts * 12);
+  L.scale = take(24);
+  L.map = take((uint64_t)N * 4);
+  L.label = take((uint64_t)std::max(N, L.passes * L.rows) * 4);  // whole passes are read
+  L.counts = take((uint64_t)L.passes * 4);
+  L.fwd_bytes = workspace_layout(d, L.rows, false, 0, false).total;
+  L.fwd = take(L.fwd_bytes);
+  L.Hc = take(n32 * (uint64_t)d->D * 2);
+  L.e = take(n32 * (uint64_t)L.piece * 512);
+  L.stat = take(blocks * n32 * 8);
+  L.factor = take(blocks * n32 * 4);
+  L.alpha = take(n32 * 4);
+  L.top = take(n32 * 4);
+  L.sum = take(n32 * 8);
+  L.y_label = take(n32 * 4);
+  L.row = take(n32 * sizeof(RowOut));
+  L.af = take((uint64_t)tiles * (uint64_t)L.vtiles * 16 * 1024);
+  L.zpart = take((uint64_t)L.zparts * n32 * (uint64_t)r * 4);
+  L.z = take(n32 * (uint64_t)r * 4);
+  L.part = take((uint64_t)L.splits * (uint64_t)L.rows * (uint64_t)d->D * 4);
+  return L;
+}
+
+uint64_t xent_bytes(const archead_dims* d, int64_t N) {
+  return N == 0 ? 0 : N <= kFewTokens ? xent_layout(d, N).total : many_layout(d, N).total;
+}
+
+template <int TT>
+void launch_xent_main(const BwdArgs& b, const MainExp& ex, hipStream_t s) {
+  const int64_t tb = (b.n32 / 32 + TT - 1) / TT, cb = (b.D + 255) / 256;
+  const dim3 grid((unsigned)(tb * cb * b.splits)), block(kMainThreads);
+  if (b.g == 32)
+    hipLaunchKernelGGL((xent_main_kernel<TT, 4>), grid, block, 0, s, b, ex);
+  else if (b.g == 64)
+    hipLaunchKernelGGL((xent_main_kernel<TT, 2>), grid, block, 0, s, b, ex);
+  else
+    hipLaunchKernelGGL((xent_main_kernel<TT, 1>), grid, block, 0, s, b, ex);
+}
+
+int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, const archead_cross_entropy_inputs* in,
+                     const archead_cross_entropy_outputs* out, hipStream_t s) {
+  const archead_dims* d = &head->dims;
+  const int64_t N = H->rows;
+  const ManyLayout L = many_layout(d, N);
+  uint8_t* ws = static_cast<uint8_t*>(head->workspace);
+  ManyArgs a{};
+  set_head(head, a.b);
+  BwdArgs& b = a.b;
+  b.N = L.rows;
+  b.n32 = L.n32;
+  b.hf = reinterpret_cast<_Float16*>(ws + L.e);
+  b.zpart = reinterpret_cast<float*>(ws + L.zpart);
+  b.z = reinterpret_cast<float*>(ws + L.z);
+  b.part = reinterpret_cast<float*>(ws + L.part);
+  b.splits = L.splits;
+  b.zparts = L.zparts;
+  a.rows = N;
+  a.H = static_cast<const uint16_t*>(H->data);
+  a.h_stride = H->row_stride;
+  a.labels = in->labels;
+  a.weight = in->weight;
+  a.tau = in->inv_temperature;
+  a.logp = out->logp;
+  if (out->dH) {
+    a.dH = static_cast<uint16_t*>(out->dH->data);
+    a.dh_stride = out->dH->row_stride;
+  }
+  a.head_max = reinterpret_cast<float*>(ws + L.head_max);
+  a.scale = reinterpret_cast<float*>(ws + L.scale);
+  a.map = reinterpret_cast<int32_t*>(ws + L.map);
+  a.label = reinterpret_cast<int32_t*>(ws + L.label);
+  a.counts = reinterpret_cast<int32_t*>(ws + L.counts);
+  a.terms = reinterpret_cast<double*>(ws + L.terms);
+  a.Hc = reinterpret_cast<uint16_t*>(ws + L.Hc);
+  a.stat = reinterpret_cast<float*>(ws + L.stat);
+  a.factor = reinterpret_cast<uint32_t*>(ws + L.factor);
+  a.alpha = reinterpret_cast<float*>(ws + L.alpha);
+  a.top = reinterpret_cast<float*>(ws + L.top);
+  a.sum = reinterpret_cast<double*>(ws + L.sum);
+  a.y_label = reinterpret_cast<float*>(ws + L.y_label);
+  a.row = reinterpret_cast<RowOut*>(ws + L.row);
+  a.af = reinterpret_cast<_Float16*>(ws + L.af);
+  a.asteps = 16 * L.vtiles;
+  // the tile path's arguments, for the gathered rows
+  archead_tensor h{a.Hc, L.rows, d->D, d->D, ARCHEAD_BF16};
+  archead_packed_head p = *head;
+  p.workspace = ws + L.fwd;
+  p.workspace_bytes = L.fwd_bytes;
+  FwdArgs f;
+  if (int rc = tile_args(&h, &p, f)) return rc;
+  const int tiles = b.nct + b.nwt;
+  (void)hipGetLastError();  // start from a clean error state
+  hipLaunchKernelGGL(xent_head_kernel, dim3(kHeadParts), dim3(kHeadThreads), 0, s, a);
+  hipLaunchKernelGGL(xent_order_kernel, dim3(1), dim3(kOrderThreads), 0, s, a, L.passes);
+  if (a.dH && tiles)
+    hipLaunchKernelGGL(xent_factors_kernel, dim3((unsigned)((tiles * a.asteps * 16 + 255) / 256)), dim3(256), 0, s, a);
+  if (a.dH && a.weight) hipLaunchKernelGGL(xent_zero_kernel, dim3((unsigned)N), dim3(256), 0, s, a);
+  for (int pass = 0; pass < L.passes; ++pass) {
+    a.pass = pass;
+    hipLaunchKernelGGL(xent_gather_kernel, dim3((unsigned)L.n32), dim3(256), 0, s, a);
+    if (launch_prep(f, s) != hipSuccess) return ARCHEAD_E_HIP;
+    for (int64_t vt = 0; vt < L.vtiles; vt += L.piece) {
+      const int64_t vn = std::min(L.piece, L.vtiles - vt);
+      T32Exp ex{};
+      ex.n_rows = a.counts + pass;
+      ex.labels = a.label + pass * kChunkRows;
+      set_exponent(in->inv_temperature, ex.c_hi, ex.c_lo);
+      ex.vt0 = (int)vt;
+      ex.vtiles = (int)vn;
+      ex.e = a.dH ? b.hf : nullptr;
+      ex.stat = a.stat;
+      ex.y_label = a.y_label;
+      if (launch_tile_exp(f, ex, s) != hipSuccess) return ARCHEAD_E_HIP;
+      a.blocks = (int)(8 * vn);
+      a.first = vt == 0;
+      a.step0 = (int)(16 * vt);
+      b.ksteps = (int)(16 * vn);
+      hipLaunchKernelGGL(xent_merge_kernel, dim3((unsigned)(L.n32 / 32)), dim3(32 * kMergeSlices), 0, s, a);
+      if (!a.dH) continue;
+      if (tiles)
+        hipLaunchKernelGGL(xent_z_kernel, dim3((unsigned)((L.n32 + 63) / 64), (unsigned)L.zparts, (unsigned)((tiles + kZTiles - 1) / kZTiles)),
+                           dim3(kZThreads), 0, s, a);
+      const MainExp me{a.counts + pass, a.factor, a.alpha, a.scale, a.first, (int)(4 * vt)};
+      const int tt = main_tiles(L.rows);
+      if (tt == 2)
+        launch_xent_main<2>(b, me, s);
+      else if (tt == 4)
+        launch_xent_main<4>(b, me, s);
+      else
+        launch_xent_main<8>(b, me, s);
+    }
+    hipLaunchKernelGGL(xent_rows_kernel, dim3((unsigned)L.rows), dim3(256), 0, s, a);
+    if (a.dH)
+      hipLaunchKernelGGL(xent_finish_kernel, dim3((unsigned)(L.n32 / 32), (unsigned)((b.nkt + 3) / 4)), dim3(kFinishThreads), 0, s, a);
+    if (hipGetLastError() != hipSuccess) return ARCHEAD_E_HIP;
+  }
+  return ARCHEAD_OK;
 }
 
 }  // namespace
@@ -494,8 +1071,7 @@ int archead_cross_entropy(const archead_tensor* H, const archead_packed_head* he
     if (head->buffer_bytes < P.total_bytes) return ARCHEAD_E_SIZE;
     const uint64_t need = xent_bytes(d, N);
     if (head->workspace_bytes < need) return ARCHEAD_E_WORKSPACE;
-    if (!forward_takes(d, std::min(N, kFewTokens)) || (N % kFewTokens && !forward_takes(d, N % kFewTokens)))
-      return ARCHEAD_E_UNSUPPORTED;
+    if (N <= kFewTokens && !forward_takes(d, N)) return ARCHEAD_E_UNSUPPORTED;
     if (dH && overlap(H, 2, dH, 2)) return ARCHEAD_E_SHAPE;
     // what the call writes shares bytes with nothing else
     struct Span {
@@ -516,8 +1092,8 @@ int archead_cross_entropy(const archead_tensor* H, const archead_packed_head* he
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();  // start from a clean error state
-  for (int64_t n0 = 0; n0 < N; n0 += kFewTokens)
-    if (int rc = launch_few_rows(H, head, in, out, n0, std::min(kFewTokens, N - n0), s)) return rc;
+  if (N > 0)
+    if (int rc = N <= kFewTokens ? launch_few_rows(H, head, in, out, s) : launch_many_rows(H, head, in, out, s)) return rc;
   if (out->loss) {
     hipLaunchKernelGGL(xent_total_kernel, dim3(1), dim3(kTotalThreads), 0, s, static_cast<const double*>(head->workspace), N, out->loss);
     if (hipGetLastError() != hipSuccess) return ARCHEAD_E_HIP;
