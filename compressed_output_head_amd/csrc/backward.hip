@@ -116,49 +116,6 @@ __device__ __forceinline__ float scale_A(const Scales8& s, int nA, int part, int
                  : f16_to_f32((uint16_t)(s.A[0][j >> 1] >> (16 * (j & 1))));
 }
 
-// The layout of the A codes: rank tile t, vocabulary step, lane (rank lane % 32,
-// rows 16 step + 8 (lane / 32) .. + 8) hold the rows' 8 codes + 128.  Thread i
-// takes four ranks: eight words of the stored rows, transposed byte by byte.
-__device__ __forceinline__ void arrange_codes(const BwdArgs& a, int64_t i) {
-  const int quad = (int)(i & 7), half = (int)(i >> 3) & 1;
-  const int64_t step = (i >> 4) % a.ksteps, t = (i >> 4) / a.ksteps;
-  if (t >= a.nct + a.nwt) return;
-  const bool in_c = t < a.nct;
-  const int j = 32 * (int)(in_c ? t : t - a.nct) + 4 * quad, r = a.r_c + a.r_r;
-  const bool valid = j < (in_c ? a.r_c : a.r_r);  // ranks come in eights
-  const int64_t v = 16 * step + 8 * half;
-  const int8_t* codes = a.a_codes + v * r + (in_c ? 0 : a.r_c) + j;
-  uint32_t w[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    w[k] = valid && v < 16 * a.nb ? *reinterpret_cast<const uint32_t*>(codes + (int64_t)k * r) : 0u;
-  u2* out = reinterpret_cast<u2*>(a.af) + ((t * a.ksteps + step) * 64 + 32 * half + 4 * quad);
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {  // byte b of the eight rows
-    u2 x;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t sel = 0x0c0c0000u | (uint32_t)(4 + b) << 8 | (uint32_t)b;
-      const uint32_t lo = __builtin_amdgcn_perm(w[4 * h + 1], w[4 * h], sel);
-      const uint32_t hi = __builtin_amdgcn_perm(w[4 * h + 3], w[4 * h + 2], sel);
-      x[h] = (lo | hi << 16) ^ 0x80808080u;
-    }
-    out[b] = x;
-  }
-}
-
-// Eight of them as fp16: byte u under the byte 0x64 is 1024 + u, exactly.
-__device__ __forceinline__ h8 unpack_u8x8(u2 c) {
-  const h2 bias = {(_Float16)1152.0f, (_Float16)1152.0f};
-  u4 x;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t pair = __builtin_amdgcn_perm(c[i >> 1], 0x64646464u, i & 1 ? 0x00070006u : 0x00050004u);
-    x[i] = h2_bits(bits_h2(pair) - bias);
-  }
-  return __builtin_bit_cast(h8, x);
-}
-
 // Workgroup q pieces + p: the largest products of piece p of rows kMaxRows q
 // .. + kMaxRows, which share the scales they are multiplied with.  The
 // workgroups behind those lay the A codes out for bwd_prep_kernel, or the

@@ -54,6 +54,49 @@ namespace {
 constexpr int kMainThreads = 512;
 constexpr int kMainXcds = 8;
 
+// The layout of the A codes: rank tile t, vocabulary step, lane (rank lane % 32,
+// rows 16 step + 8 (lane / 32) .. + 8) hold the rows' 8 codes + 128.  Thread i
+// takes four ranks: eight words of the stored rows, transposed byte by byte.
+__device__ __forceinline__ void arrange_codes(const BwdArgs& a, int64_t i) {
+  const int quad = (int)(i & 7), half = (int)(i >> 3) & 1;
+  const int64_t step = (i >> 4) % a.ksteps, t = (i >> 4) / a.ksteps;
+  if (t >= a.nct + a.nwt) return;
+  const bool in_c = t < a.nct;
+  const int j = 32 * (int)(in_c ? t : t - a.nct) + 4 * quad, r = a.r_c + a.r_r;
+  const bool valid = j < (in_c ? a.r_c : a.r_r);  // ranks come in eights
+  const int64_t v = 16 * step + 8 * half;
+  const int8_t* codes = a.a_codes + v * r + (in_c ? 0 : a.r_c) + j;
+  uint32_t w[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    w[k] = valid && v < 16 * a.nb ? *reinterpret_cast<const uint32_t*>(codes + (int64_t)k * r) : 0u;
+  u2* out = reinterpret_cast<u2*>(a.af) + ((t * a.ksteps + step) * 64 + 32 * half + 4 * quad);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {  // byte b of the eight rows
+    u2 x;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t sel = 0x0c0c0000u | (uint32_t)(4 + b) << 8 | (uint32_t)b;
+      const uint32_t lo = __builtin_amdgcn_perm(w[4 * h + 1], w[4 * h], sel);
+      const uint32_t hi = __builtin_amdgcn_perm(w[4 * h + 3], w[4 * h + 2], sel);
+      x[h] = (lo | hi << 16) ^ 0x80808080u;
+    }
+    out[b] = x;
+  }
+}
+
+// Eight of them as fp16: byte u under the byte 0x64 is 1024 + u, exactly.
+__device__ __forceinline__ h8 unpack_u8x8(u2 c) {
+  const h2 bias = {(_Float16)1152.0f, (_Float16)1152.0f};
+  u4 x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t pair = __builtin_amdgcn_perm(c[i >> 1], 0x64646464u, i & 1 ? 0x00070006u : 0x00050004u);
+    x[i] = h2_bits(bits_h2(pair) - bias);
+  }
+  return __builtin_bit_cast(h8, x);
+}
+
 // The group codes of 16 vocabulary rows by k-tile, for bwd_few_kernel: thread i
 // takes those of one k-tile (or of the two that share a code of 256 columns).
 // As they are stored, a k-tile's wave finds the 16 bytes that it needs in 16
@@ -134,18 +177,27 @@ struct MainShape {
 // with the residual, added to the sums of the pieces before it.
 struct MainExp {
   const int32_t* n_rows;   // rows that count
-  const uint32_t* factor;  // [32-row block of the piece][n32] what brings the block's operands to the row's
-                           // exponent, a power of two as a product of two in fp16
+  const int32_t* splits;   // parts of the piece: sums are [splits][rows that count][D]
+  const float* stat;       // [32-row block of the piece][n32][2] the operands' exponents M
+  const float* top;        // [n32] the rows' exponents
   const float* alpha;      // [n32] what brings the sums so far there, a power of two
   const float* scale;      // [1] the power of two that the row scales s_R are taken with
+  int steps;               // of a row tile in a.hf
   int first;               // no sums yet
   int stage0;              // first stage of the piece in the vocabulary
 };
+// Operands are brought to the rows' exponents times 2^14: exactly, but for what
+// ends below 2^-14, 2^-28 of the row's largest.
+constexpr int kFactorTop = 14;
+
+// 2^t in fp16, t whole (0 where it is not a number or below fp16's range)
+__device__ __forceinline__ _Float16 fp16_power(float t) { return (_Float16)ldexpf(1.0f, (int)fmaxf(t, -100.0f)); }
 
 // kCodes: group codes of 128 columns of a row: 4 for g = 32, 2 for 64, else 1.
-// EX: a.hf and a.ksteps are of the piece of `ex`; the operand of the residual is
-// (q4 c8) s_R, rounded to fp16 (2^-11), as the exponentials' operands have no
-// row scales.
+// EX: a.hf and a.ksteps are of the piece of `ex`, the fragments are brought to
+// the rows' exponents on their way to LDS, and the residual's operand is (q4 c8)
+// s_R, rounded to fp16 (2^-11).  (With s_R in a second set of fragments from
+// the kernel that makes them, that kernel takes 12% longer and this one 1% less.)
 template <int TT, int kCodes, bool EX>
 __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& ex) {
   using S = MainShape<TT>;
@@ -157,7 +209,7 @@ __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& e
   const int wm = wave / S::WN, wn = wave % S::WN;
   const int64_t rows = EX ? *ex.n_rows : a.N;
   const int CB = (int)((a.D + 255) / 256), ntiles = (int)((EX ? rows + 31 : a.n32) / 32), TB = (ntiles + TT - 1) / TT;
-  const int items = EX ? CB * TB * a.splits : gridDim.x;
+  const int splits = EX ? *ex.splits : a.splits, items = EX ? CB * TB * splits : gridDim.x;
   if (EX && (int)blockIdx.x >= items) return;
   // Workgroups are dealt to the XCDs round robin: each XCD gets a contiguous
   // range of (split, token block, column block), so that those in one L2 share
@@ -166,7 +218,7 @@ __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& e
   const int item = x * per + std::min(x, rem) + blockIdx.x / kMainXcds;
   const int cb = item % CB, tb = item / CB % TB, split = item / CB / TB;
   const int stages = a.ksteps / 4;
-  const int s0 = (int)((int64_t)split * stages / a.splits), s1 = (int)((int64_t)(split + 1) * stages / a.splits);
+  const int s0 = (int)((int64_t)split * stages / splits), s1 = (int)((int64_t)(split + 1) * stages / splits);
 
   // this wave's share of unpacking: one packed tile, 16 rows x 128 columns
   const int blk = wave & 3, kth = wave >> 2;
@@ -176,26 +228,32 @@ __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& e
   u4 w[kDepth];
   uint32_t code[kDepth];
   h8 av[kDepth][S::kLoads];
-  uint16_t rs[EX ? kDepth : 1];                  // EX: the row's s_R, the fragments' factors
-  uint32_t fac[EX ? kDepth : 1][S::kLoads];
-  const float rscale = EX ? *ex.scale : 1.0f;
+  // EX: the row's s_R; the row's exponent in each fragment's block, and over all
+  uint16_t rs[EX ? kDepth : 1];
+  float fm[EX ? kDepth : 1][S::kLoads], ft[S::kLoads], scale = 1.0f;
+  if constexpr (EX) {
+    scale = *ex.scale;
+#pragma unroll
+    for (int i = 0; i < S::kLoads; ++i)
+      ft[i] = ex.top[32 * (int64_t)std::min(tb * TT + (8 * i + wave) / 4, ntiles - 1) + (lane & 31)] - (float)kFactorTop;
+  }
   auto load = [&](int s, auto slot_) {
     constexpr int slot = decltype(slot_)::value;
     s = std::min(s, s1 - 1);  // past the end: a stage that is cached, never used
     // past the last rows dY is zero
     const int64_t b = std::min<int64_t>(4 * (int64_t)(EX ? s + ex.stage0 : s) + blk, a.nb - 1);
     w[slot] = *reinterpret_cast<const u4*>(wsrc + b * 1024);
-    if constexpr (EX) rs[slot] = a.r_rowscale[16 * b + (lane & 15)];
     const uint8_t* c = csrc + 16 * b * a.ng;
     code[slot] = kCodes == 4   ? *reinterpret_cast<const uint32_t*>(c)
                  : kCodes == 2 ? *reinterpret_cast<const uint16_t*>(c)
                                : *c;
+    if constexpr (EX) rs[slot] = a.r_rowscale[16 * b + (lane & 15)];
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
       const int f = 8 * i + wave;
       const int64_t tile = std::min(tb * TT + f / 4, ntiles - 1);
-      if constexpr (EX) fac[slot][i] = ex.factor[(2 * (int64_t)s + (wave & 3) / 2) * a.n32 + 32 * tile + (lane & 31)];
-      av[slot][i] = *reinterpret_cast<const h8*>(a.hf + ((tile * a.ksteps + 4 * s + f % 4) * 64 + lane) * 8);
+      if constexpr (EX) fm[slot][i] = ex.stat[2 * ((2 * (int64_t)s + (wave & 3) / 2) * a.n32 + 32 * tile + (lane & 31))];
+      av[slot][i] = *reinterpret_cast<const h8*>(a.hf + ((tile * (EX ? ex.steps : a.ksteps) + 4 * s + f % 4) * 64 + lane) * 8);
     }
   };
   // columns 32 d .. + 32 of the packed tile in a register slot to the LDS tile
@@ -206,7 +264,7 @@ __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& e
                                      : code[slot];
     h8 x = unpack_q4_scaled(w[slot][d], (_Float16)(float)c);
     if constexpr (EX) {
-      const _Float16 r = (_Float16)(f16_to_f32(rs[slot]) * rscale);
+      const _Float16 r = (_Float16)(f16_to_f32(rs[slot]) * scale);
       x = x * h8{r, r, r, r, r, r, r, r};
     }
     sB[buf][tile_octet(16 * blk + (lane & 15), 16 * kth + 4 * d + (lane >> 4))] = x;
@@ -217,9 +275,8 @@ __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& e
     for (int i = 0; i < S::kLoads; ++i) {
       h8 x = av[slot][i];
       if constexpr (EX) {
-        const h2 f = bits_h2(fac[slot][i]);
-        x = x * h8{f[0], f[0], f[0], f[0], f[0], f[0], f[0], f[0]};
-        x = x * h8{f[1], f[1], f[1], f[1], f[1], f[1], f[1], f[1]};
+        const _Float16 f = fp16_power(fm[slot][i] - ft[i]);
+        x = x * h8{f, f, f, f, f, f, f, f};
       }
       sA[buf][8 * i + wave][lane] = x;
     }
@@ -327,7 +384,7 @@ __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& e
 #pragma unroll
           for (int v = 0; v < 16; ++v) {  // rows and columns past the last: those, not stored
             const int64_t n = std::min<int64_t>(32 * (int64_t)(tb * TT + wm * S::MT + m) + 8 * (v >> 2) + 4 * khalf + (v & 3), rows - 1);
-            old[v] = a.part[((int64_t)split * a.N + n) * a.D + std::min(d, a.D - 1)];
+            old[v] = a.part[((int64_t)split * rows + n) * a.D + std::min(d, a.D - 1)];
             al[v] = ex.alpha[n];
           }
 #pragma unroll
@@ -337,7 +394,7 @@ __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& e
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
         const int64_t n = 32 * (int64_t)(tb * TT + wm * S::MT + m) + 8 * (v >> 2) + 4 * khalf + (v & 3);
-        if (n < rows && d < a.D) a.part[((int64_t)split * a.N + n) * a.D + d] = acc[m][c][v];
+        if (n < rows && d < a.D) a.part[((int64_t)split * rows + n) * a.D + d] = acc[m][c][v];
       }
     }
 }

@@ -139,23 +139,24 @@ struct FwdArgs {
 };
 
 // The exponentials' epilogue (tile32_exp_kernel): the logits of a piece of the
-// vocabulary, whole 256-row tiles [vt0, vt0 + vtiles), leave as the operand of
-// the product that follows, and as what the softmax's sum needs of them.
+// vocabulary, whole 256-row tiles [vt0, vt0 + vtiles), leave as operands of the
+// products that follow, and as what the softmax's sum needs of them.  An
+// operand is e = 2^(z - M) in fp16, z = log2(e) times the scaled logit and M the
+// least whole number that none of a row's z in its 32-row block exceeds, so that
+// blocks differ by exact powers of two.  e is off by half a step, 2^-11 of
+// itself, or below 2^-14 by 2^-25, which is at most 2^-20 of the block's largest
+// in all of its 32 entries.
 struct T32Exp {
   const int32_t* n_rows;  // rows of H that count; N and n32 of FwdArgs are the most there can be
   const int32_t* labels;  // [N] by row of H
-  float c_hi, c_lo;       // log2(e) times the inverse temperature, as a pair
+  double c;               // log2(e) times the inverse temperature
   int vt0, vtiles;
-  _Float16* e;            // null, or [n32/32][16 vtiles][64][8] operand fragments, lane l: row l % 32, vocabulary rows
-                          // 16 step + 8 (l / 32) .. + 8
-  float* stat;            // [8 vtiles][n32][2] by 32-row block: the exponent M, the sum of 2^(z - M + kExpTop)
-  float* y_label;         // [n32] the label's logit, written where it is met
+  _Float16* e;            // null, or operands [n32/32][steps][64][8], lane l: row l % 32, vocabulary rows
+                          // 16 step + 8 (l / 32) .. + 8 of the piece
+  int steps;              // at least 16 vtiles
+  float* stat;            // [8 vtiles][n32][2] by 32-row block: M, the sum of e
+  float* z_label;         // [n32] the label's z, written where it is met
 };
-// Operands are 2^(z - M + kExpTop), z = log2(e) times the scaled logit and M the
-// least whole number that none of a row's z in its 32-row block exceeds:
-// below 2^14, exact powers of two apart from block to block, and normal fp16
-// down to 2^-28 of the largest.
-constexpr int kExpTop = 14;
 
 // FwdArgs of the tile path without split tiles (workspace_layout(d, N, false,
 // 0, false)), with the checks of archead_logits.

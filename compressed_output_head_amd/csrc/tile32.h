@@ -355,6 +355,10 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
     const int64_t tok = std::min<int64_t>(32 * (int64_t)tt0 + tid, a.n32 - 1);
     sTok[tid][0] = a.hscale[tok];
     sTok[tid][1] = part == 0 ? a.zscale[tok] : 0.0f;  // the low-rank term goes with part 0 only
+    if constexpr (EX) {
+      sTok[tid][0] = (float)(ex.c * (double)a.hscale[tok]);
+      sTok[tid][1] = (float)(ex.c * (double)a.zscale[tok]);
+    }
     if constexpr (ST) sTgt[tid] = a.targets && 32 * (int64_t)tt0 + tid < a.N ? a.targets[32 * (int64_t)tt0 + tid] : -1;
     if constexpr (EX) {
       const int label = ex.labels[tok < a.N ? tok : a.N - 1];
@@ -483,7 +487,6 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
   // against exact INT8 A codes, 16 ranks per MFMA step, one accumulator per
   // part) is added with the scales, and each run is stored at once.
   if constexpr (EX) {
-    __syncthreads();  // every wave's Z copies (complete after the wait above) are visible
     auto zfrag_at = [&](int tt, int rem) {  // as zfrag below
       int z = (tt << zsh) + rem;
       if (z > 4 * KS * kT32TT - 1) z = 4 * KS * kT32TT - 1;
@@ -492,6 +495,7 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
       return base[pos * 64 + lane];
     };
     const int blk = kT32CB * (vt - ex.vt0) + wn;  // of the piece
+    __syncthreads();  // every wave's Z copies (complete after the wait above) are visible
     const int v0 = 32 * (kT32CB * vt + wn) + 4 * g;
     const float infinity = __builtin_huge_valf();
     static_for<0, kT32MT>([&](auto M_) {
@@ -523,9 +527,9 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
           p = mfma32(av, zf[(2 * s + 1) * 64], p);
         }
       }
-      const float hs = sTok[32 * m + c32][0], zs = sTok[32 * m + c32][1];
+      const float hs = sTok[32 * m + c32][0], zs = sTok[32 * m + c32][1];  // times ex.c
       const int label = sTgt[32 * m + c32];
-      float y[16];
+      float z[16];
 #pragma unroll
       for (int vg = 0; vg < 4; ++vg) {
         const int lr = 32 * wn + 8 * vg + 4 * g;
@@ -535,52 +539,46 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int v = 4 * vg + e;
-          y[v] = fmaf(zs, fmaf(vw[e], pw[v], vc[e] * pc[v]), hs * (vr[e] * acc[m][0][v]));
+          z[v] = fmaf(zs, fmaf(vw[e], pw[v], vc[e] * pc[v]), hs * (vr[e] * acc[m][0][v]));
         }
       }
       // the label has no part in the sums, nor have rows past the vocabulary
       const unsigned d = (unsigned)(label - v0);
       if (d < 28u && (d & 4u) == 0u) {
         const int at = (int)(d >> 3) * 4 + (int)(d & 3u);
-        float yl = 0.0f;
+        float zl = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          yl = i == at ? y[i] : yl;
-          y[i] = i == at ? -infinity : y[i];
+          zl = i == at ? z[i] : zl;
+          z[i] = i == at ? -infinity : z[i];
         }
-        if (32 * (int64_t)(tt0 + m) + c32 < a.N) ex.y_label[32 * (int64_t)(tt0 + m) + c32] = yl;
+        ex.z_label[32 * (int64_t)(tt0 + m) + c32] = zl;
       }
       if (v0 + 28 > a.V) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (v0 + 8 * (i >> 2) + (i & 3) >= a.V) y[i] = -infinity;
+          if (v0 + 8 * (i >> 2) + (i & 3) >= a.V) z[i] = -infinity;
       }
-      float top = y[0];
+      float top = z[0];
 #pragma unroll
-      for (int i = 1; i < 16; ++i) top = fmaxf(top, y[i]);
+      for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
       top = fmaxf(top, __shfl_xor(top, 32));
       // no entry, or none above -inf: operands of 0 (a row that is not finite shows in its sum)
-      const float M = ceilf(fmaf(top, ex.c_hi, top * ex.c_lo));
-      const bool none = top == -infinity;
-      const float low = none ? 0.0f : (float)kExpTop - M;
+      const float M = ceilf(top), low = top == -infinity ? 0.0f : M;
       float sum = 0.0f;
       uint32_t pk[8];
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
-        float x[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          x[j] = __builtin_amdgcn_exp2f(fmaf(y[i + j], ex.c_lo, fmaf(y[i + j], ex.c_hi, low)));
-          sum += x[j];
-        }
-        pk[i >> 1] = h2_bits(h2{(_Float16)x[0], (_Float16)x[1]});
+        const float x0 = __builtin_amdgcn_exp2f(z[i] - low), x1 = __builtin_amdgcn_exp2f(z[i + 1] - low);
+        sum += x0 + x1;
+        pk[i >> 1] = h2_bits(h2{(_Float16)x0, (_Float16)x1});
       }
       sum += __shfl_xor(sum, 32);
       const int64_t tok = 32 * (int64_t)(tt0 + m) + c32;
-      if (g == 0) reinterpret_cast<u2*>(ex.stat)[(int64_t)blk * a.n32 + tok] = u2{__float_as_uint(none ? -infinity : M), __float_as_uint(sum)};
-      // lane halves hold the two fours of each eight rows; a fragment wants eights in one lane
-      u4* out = reinterpret_cast<u4*>(ex.e) + ((int64_t)(tt0 + m) * 16 * ex.vtiles + 2 * blk) * 64 + lane;
+      if (g == 0) reinterpret_cast<u2*>(ex.stat)[(int64_t)blk * a.n32 + tok] = u2{__float_as_uint(M), __float_as_uint(sum)};
       if (!ex.e) return;
+      // lane halves hold the two fours of each eight rows; a fragment wants eights in one lane
+      u4* out = reinterpret_cast<u4*>(ex.e) + ((int64_t)(tt0 + m) * ex.steps + 2 * blk) * 64 + lane;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const auto a0 = __builtin_amdgcn_permlane32_swap(pk[4 * s], pk[4 * s + 2], false, false);

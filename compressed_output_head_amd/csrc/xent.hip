@@ -19,8 +19,8 @@
 //   tile32_exp_kernel       the exponentials as fp16 operands, with an exponent
 //                           and a sum for each row and 32 entries
 //   xent_merge_kernel       the rows' running exponent and sum, and what brings
-//                           the piece and the sums before it to that exponent
-//   xent_z_kernel           e (s_A code) added to Z
+//                           the sums before the piece to that exponent
+//   xent_z_kernel           (e s_A) code added to Z
 //   xent_main_kernel        e (s_R q4 c8) added to the sums
 // and at the end xent_rows_kernel (log p, Z), xent_finish_kernel (dH).
 #include <algorithm>
@@ -330,7 +330,7 @@ constexpr int kMergeSlices = 32;
 constexpr int kZThreads = 512, kZTiles = 4;         // rank tiles of a workgroup
 
 struct ManyArgs {
-  BwdArgs b;               // of a pass: N its most rows; hf the piece's operands, ksteps its steps
+  BwdArgs b;               // of a pass: N its most rows; hf the piece's operands e, ksteps its steps
   int64_t rows;            // of the call
   const uint16_t* H;
   int64_t h_stride;
@@ -341,22 +341,23 @@ struct ManyArgs {
   uint16_t* dH;
   int64_t dh_stride;
   float* head_max;         // [kHeadParts][3]
-  float* scale;            // [3][2] powers of two for s_R, s_Ac, s_Aw and their inverses
+  float* scale;            // [4] the power of two that s_R are taken with; what undoes those of the sums, Z_c, Z_w
+  _Float16* scale_a;       // [2][16 vtiles of V][16] s_Ac, s_Aw times powers of two
   int32_t* map;            // [rows] rows that count, in order
   int32_t* label;          // [rows] their labels
   int32_t* counts;         // [passes] of each pass
+  int32_t* splits;         // [passes] parts of a piece in the product of each pass
   double* terms;           // [rows] -w log p by row of the call
   uint16_t* Hc;            // [n32][D] gathered H
   float* stat;             // [blocks][n32][2]
-  uint32_t* factor;        // [blocks][n32]
   float* alpha;            // [n32]
   float* top;              // [n32] running exponent
   double* sum;             // [n32] running sum
-  float* y_label;          // [n32]
+  float* z_label;          // [n32] log2(e) tau times the label's logit
   RowOut* row;             // [n32]
-  _Float16* af;            // [rank tiles][16 vtiles of V][64][8] s_A code
-  int64_t asteps;          // steps of af
-  int pass, blocks, first, step0;
+  int64_t asteps;          // steps of the whole vocabulary
+  int pass, passes, blocks, first, step0, steps;
+  int tile_rows;           // rows of a workgroup of the product
 };
 
 // Largest |s_R|, |s_Ac|, |s_Aw| of a part of the vocabulary.
@@ -382,18 +383,33 @@ __global__ __launch_bounds__(kHeadThreads) void xent_head_kernel(const ManyArgs 
   }
 }
 
-// One workgroup: the rows that count, in order; the powers of two that bring
-// the largest |q4 c8 s_R| (2040 at most before s_R) and |code s_A| to [2^14, 2^15).
-__global__ __launch_bounds__(kOrderThreads) void xent_order_kernel(const ManyArgs a, int passes) {
-  __shared__ int sCount[kOrderThreads];
+// Workgroup 0: the rows that count, in order, and how many parts the product
+// of each pass is cut into: as many as keep its workgroups what they are for a
+// pass of rows that all count.  The others: what the head's scales give.
+__global__ __launch_bounds__(kOrderThreads) void xent_order_kernel(const ManyArgs a) {
   const int tid = threadIdx.x;
-  if (tid < 3) {
-    float m = 0.0f;
-    for (int p = 0; p < kHeadParts; ++p) m = fmaxf(m, a.head_max[3 * p + tid]);
-    const int e = std::max(-126, std::min(row_exponent(m * (tid == 0 ? 2040.0f : 128.0f)), 126));
-    a.scale[2 * tid] = ldexpf(1.0f, e);
-    a.scale[2 * tid + 1] = ldexpf(1.0f, -e);
+  if (blockIdx.x > 0) {
+    // powers of two that bring the largest |q4 c8 s_R| (2040 at most before s_R)
+    // and the largest |s_A| to [2^14, 2^15) and [1/2, 1)
+    static_assert(kHeadParts == 64, "a part for each lane");
+    int k[3];
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const float m = wave_max(a.head_max[3 * (tid & 63) + q]);
+      k[q] = std::max(-100, std::min(q == 0 ? row_exponent(2040.0f * m) : row_exponent(m) - 15, 100));
+    }
+    const int64_t i = ((int64_t)blockIdx.x - 1) * kOrderThreads + tid;
+    if (i < 4) a.scale[i] = ldexpf(1.0f, i == 0 ? k[0] : -k[i - 1] - kFactorTop);
+    if (i < 16 * a.asteps)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float s[3] = {};
+        if (i < a.b.V) scales_of(a.b, i, s);
+        a.scale_a[q * 16 * a.asteps + i] = (_Float16)ldexpf(s[1 + q], k[1 + q]);
+      }
+    return;
   }
+  __shared__ int sCount[kOrderThreads];
   const int64_t per = (a.rows + kOrderThreads - 1) / kOrderThreads, n0 = std::min(tid * per, a.rows), n1 = std::min(n0 + per, a.rows);
   int mine = 0;
   for (int64_t n = n0; n < n1; ++n) mine += !a.weight || a.weight[n] != 0.0f;
@@ -416,8 +432,14 @@ __global__ __launch_bounds__(kOrderThreads) void xent_order_kernel(const ManyArg
     }
   }
   const int64_t total = sCount[kOrderThreads - 1];
-  for (int p = tid; p < passes; p += kOrderThreads)
-    a.counts[p] = (int32_t)std::max<int64_t>(0, std::min(total - p * kChunkRows, kChunkRows));
+  for (int p = tid; p < a.passes; p += kOrderThreads) {
+    const int64_t count = std::max<int64_t>(0, std::min(total - p * kChunkRows, kChunkRows));
+    const int64_t most = (a.b.N + a.tile_rows - 1) / a.tile_rows, tiles = std::max<int64_t>(1, (count + a.tile_rows - 1) / a.tile_rows);
+    a.counts[p] = (int32_t)count;
+    // (of which there is room for, too: tiles of rows in fewer of them)
+    const int64_t parts = std::min(a.b.splits * most / tiles, a.b.splits * a.b.N / std::max<int64_t>(count, 1));
+    a.splits[p] = (int32_t)std::max<int64_t>(1, std::min<int64_t>(parts, std::max<int64_t>(a.b.splits, a.b.ksteps / 32)));
+  }
 }
 
 // The gradient of rows that do not count.
@@ -434,133 +456,141 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(const ManyArgs a) {
   if (threadIdx.x == 0) {
     a.top[i] = -__builtin_huge_valf();
     a.sum[i] = 0.0;
-    a.y_label[i] = __builtin_nanf("");  // stays where the label is outside the vocabulary
+    a.z_label[i] = __builtin_nanf("");  // stays where the label is outside the vocabulary
   }
   const u4* src = reinterpret_cast<const u4*>(a.H + (i < count ? (int64_t)a.map[a.pass * kChunkRows + i] : 0) * a.h_stride);
   u4* dst = reinterpret_cast<u4*>(a.Hc + i * a.b.D);
   for (int64_t c = threadIdx.x; c < a.b.D / 8; c += 256) dst[c] = i < count ? src[c] : u4{};
 }
 
-// The A codes times their row scales as operands of the product along the
-// vocabulary: rank tile t, step, lane (rank lane % 32, rows 16 step + 8 (lane
-// / 32) .. + 8).  Thread i takes four ranks of eight rows.
-__global__ __launch_bounds__(256) void xent_factors_kernel(const ManyArgs a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const BwdArgs& b = a.b;
-  const int quad = (int)(i & 7), half = (int)(i >> 3) & 1;
-  const int64_t step = (i >> 4) % a.asteps, t = (i >> 4) / a.asteps;
-  if (t >= b.nct + b.nwt) return;
-  const bool in_c = t < b.nct;
-  const int j = 32 * (int)(in_c ? t : t - b.nct) + 4 * quad, r = b.r_c + b.r_r;
-  const bool valid = j < (in_c ? b.r_c : b.r_r);  // ranks come in eights
-  const float scale = a.scale[in_c ? 2 : 4];
-  const int64_t v = 16 * step + 8 * half;
-  h8 out[4] = {};
-  if (valid && v < 16 * b.nb) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(b.a_codes + (v + k) * r + (in_c ? 0 : b.r_c) + j);
-      const float s = f16_to_f32(b.a_scales[(v + k) * b.nA + (in_c ? 0 : b.nA - 1)]) * scale;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) out[e][k] = (_Float16)(s * (float)(int8_t)(w >> (8 * e)));
-    }
-  }
-  h8* dst = reinterpret_cast<h8*>(a.af) + (t * a.asteps + step) * 64 + 32 * half + 4 * quad;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) dst[e] = out[e];
-}
-
-// 2^-j as a product of two fp16 numbers (0 below 2^-44: such an operand is
-// below fp16's least).
-__device__ __forceinline__ uint32_t factor_of(float j) {
-  if (!(j >= 0.0f && j <= 44.0f)) return 0;
-  const int a = std::min((int)j, 20), b = (int)j - a;
-  auto half_power = [](int k) { return k <= 14 ? (uint32_t)(15 - k) << 10 : 1u << (24 - k); };
-  return half_power(a) | half_power(b) << 16;
+// The A codes in the order of the product along the vocabulary.
+__global__ __launch_bounds__(256) void xent_arrange_kernel(const BwdArgs b) {
+  arrange_codes(b, (int64_t)blockIdx.x * 256 + threadIdx.x);
 }
 
 // 32 rows a workgroup, kMergeSlices threads each: the running exponent of the
-// piece's blocks and of those before, the sum at that exponent, and the factors.
+// piece's blocks and of those before, and the sum at that exponent.
 __global__ __launch_bounds__(32 * kMergeSlices) void xent_merge_kernel(const ManyArgs a) {
   __shared__ float sTop[kMergeSlices][32];
   __shared__ double sSum[kMergeSlices][32];
+  constexpr int kBatch = 8;
   const int c = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int64_t n = 32 * (int64_t)blockIdx.x + c;
   if (32 * (int64_t)blockIdx.x >= a.counts[a.pass]) return;
   const float infinity = __builtin_huge_valf();
   const u2* stat = reinterpret_cast<const u2*>(a.stat) + n;
+  // sum s at exponent m moved to m + j (j whole and not below 0, or not finite
+  // where there is no entry or the row is not finite, which shows in s)
+  auto moved = [](double s, float j) { return j <= 1000.0f ? ldexp(s, -(int)j) : s == s ? 0.0 : s; };
   float m = -infinity;
-#pragma unroll 8
-  for (int k = slice; k < a.blocks; k += kMergeSlices) m = fmaxf(m, __uint_as_float(stat[(int64_t)k * a.b.n32][0]));
-  sTop[slice][c] = m;
-  __syncthreads();
-  const float old = a.top[n];
-  m = old;
-  for (int k = 0; k < kMergeSlices; ++k) m = fmaxf(m, sTop[k][c]);
   double s = 0.0;
-  for (int k = slice; k < a.blocks; k += kMergeSlices) {
-    const u2 x = stat[(int64_t)k * a.b.n32];
-    const float j = m - __uint_as_float(x[0]);  // whole, or not finite where the block has no entry or the row is not
-    const float sum = __uint_as_float(x[1]);
-    s += j <= 1000.0f ? ldexp((double)sum, -(int)j) : (sum == sum ? 0.0 : (double)sum);
-    a.factor[(int64_t)k * a.b.n32 + n] = factor_of(j);
+  for (int k0 = slice; k0 < a.blocks; k0 += kBatch * kMergeSlices) {
+    u2 x[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) x[i] = stat[(int64_t)std::min(k0 + i * kMergeSlices, a.blocks - 1) * a.b.n32];
+    float t = m;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) t = fmaxf(t, __uint_as_float(x[i][0]));
+    s = moved(s, t - m);
+    m = t;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (k0 + i * kMergeSlices < a.blocks) s += moved((double)__uint_as_float(x[i][1]), m - __uint_as_float(x[i][0]));
   }
+  sTop[slice][c] = m;
   sSum[slice][c] = s;
   __syncthreads();
   if (slice == 0) {
-    const float j = m - old;
-    const bool kept = j <= 1000.0f;
-    s = kept ? ldexp(a.sum[n], -(int)j) : (a.sum[n] == a.sum[n] ? 0.0 : a.sum[n]);
-    for (int k = 0; k < kMergeSlices; ++k) s += sSum[k][c];
-    a.sum[n] = s;
-    a.top[n] = m;
-    a.alpha[n] = kept ? ldexpf(1.0f, -(int)j) : 0.0f;
+    const float old = a.top[n];
+    float t = old;
+    for (int k = 0; k < kMergeSlices; ++k) t = fmaxf(t, sTop[k][c]);
+    double sum = moved(a.sum[n], t - old);
+    for (int k = 0; k < kMergeSlices; ++k) sum += moved(sSum[k][c], t - sTop[k][c]);
+    a.sum[n] = sum;
+    a.top[n] = t;
+    a.alpha[n] = t - old <= 1000.0f ? ldexpf(1.0f, -(int)(t - old)) : 0.0f;
   }
 }
 
-// 64 rows x kZTiles rank tiles a workgroup over part blockIdx.y of the piece's
-// steps, dealt to the waves; their sums are added up in order and then to the
-// part's sums of the pieces before.
+// 64 rows x kZTiles rank tiles (half of them of each part of the ranks) a
+// workgroup over part blockIdx.y of the piece's steps, dealt to the waves; e s_A is formed in registers (rounded
+// to fp16 once more), the codes are exact.  The waves' sums are added up in
+// order and then to the part's sums of the pieces before.
 __global__ __launch_bounds__(kZThreads, 2) void xent_z_kernel(const ManyArgs a) {
-  constexpr int kWaves = kZThreads / 64;
+  constexpr int kWaves = kZThreads / 64, kDepth = 3;
   __shared__ float red[kWaves / 2][kZTiles][16][64];
   const BwdArgs& b = a.b;
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t count = a.counts[a.pass], ntiles = (count + 31) / 32, tile0 = 2 * (int64_t)blockIdx.x;
   if (tile0 >= ntiles) return;
-  const int tiles = b.nct + b.nwt, t0 = kZTiles * (int)blockIdx.z, parts = gridDim.y, r = b.r_c + b.r_r;
+  const int parts = gridDim.y, r = b.r_c + b.r_r;
+  // rank tile of slot t: of part c (0) or w (1), its place in the part
+  auto part_of = [](int t) { return t / (kZTiles / 2); };
+  auto place_of = [&](int t) { return kZTiles / 2 * (int)blockIdx.z + t % (kZTiles / 2); };
   const int k0 = (int)((int64_t)blockIdx.y * b.ksteps / parts), k1 = (int)((int64_t)(blockIdx.y + 1) * b.ksteps / parts);
+  // row tiles start at different steps, so that they are not all at the same memory channels
+  const int turn = k1 > k0 ? (int)(blockIdx.x * 5 * kWaves % (unsigned)(k1 - k0)) : 0;
   const h8* e[2];
-  const uint32_t* fac[2];
+  const float* fm[2];
+  float ft[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int64_t tile = std::min(tile0 + i, ntiles - 1);
-    e[i] = reinterpret_cast<const h8*>(b.hf) + tile * b.ksteps * 64 + lane;
-    fac[i] = a.factor + 32 * tile + c32;
+    e[i] = reinterpret_cast<const h8*>(b.hf) + tile * a.steps * 64 + lane;
+    fm[i] = a.stat + 2 * (32 * tile + c32);
+    ft[i] = a.top[32 * tile + c32];
   }
-  const h8* af = reinterpret_cast<const h8*>(a.af) + (int64_t)a.step0 * 64 + lane;
+  const u2* codes[kZTiles];
+#pragma unroll
+  for (int t = 0; t < kZTiles; ++t)  // past a part's last tile: another, not stored
+    codes[t] = reinterpret_cast<const u2*>(b.af) +
+               ((int64_t)std::min(place_of(t) + (part_of(t) ? b.nct : 0), b.nct + b.nwt - 1) * a.asteps + a.step0) * 64 + lane;
+  const h8* scale[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) scale[q] = reinterpret_cast<const h8*>(a.scale_a) + 2 * (q * a.asteps + a.step0) + half;
   f16x acc[2][kZTiles] = {};
-#pragma unroll 2
-  for (int k = k0 + wave; k < k1; k += kWaves) {
-    h8 x[2], y[kZTiles];
-    uint32_t f[2];
+  h8 x[kDepth][2], s[kDepth][2];
+  float f[kDepth][2];
+  u2 y[kDepth][kZTiles];
+  auto load = [&](int k, auto slot_) __attribute__((always_inline)) {
+    constexpr int slot = decltype(slot_)::value;
+    k = std::min(k, k1 - 1) + turn;  // past the end: a step that is not used
+    k -= k >= k1 ? k1 - k0 : 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      x[i] = e[i][(int64_t)k * 64];
-      f[i] = fac[i][(int64_t)(k / 2) * b.n32];
+      f[slot][i] = fm[i][2 * (int64_t)(k / 2) * b.n32];
+      x[slot][i] = e[i][(int64_t)k * 64];
     }
 #pragma unroll
-    for (int t = 0; t < kZTiles; ++t)  // past the last tile: that one, not stored
-      y[t] = af[((int64_t)std::min(t0 + t, tiles - 1) * a.asteps + std::min<int64_t>(k, a.asteps - 1 - a.step0)) * 64];
+    for (int q = 0; q < 2; ++q) s[slot][q] = scale[q][2 * (int64_t)k];
+#pragma unroll
+    for (int t = 0; t < kZTiles; ++t) y[slot][t] = codes[t][(int64_t)k * 64];
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto use = [&](auto slot_) __attribute__((always_inline)) {
+    constexpr int slot = decltype(slot_)::value;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const h2 g = bits_h2(f[i]);
-      x[i] = x[i] * h8{g[0], g[0], g[0], g[0], g[0], g[0], g[0], g[0]};
-      x[i] = x[i] * h8{g[1], g[1], g[1], g[1], g[1], g[1], g[1], g[1]};
+      const _Float16 p = fp16_power(f[slot][i] - ft[i] + (float)kFactorTop);
+      const h8 v = x[slot][i] * h8{p, p, p, p, p, p, p, p};
+      const h8 part[2] = {v * s[slot][0], v * s[slot][1]};
 #pragma unroll
-      for (int t = 0; t < kZTiles; ++t) acc[i][t] = mfma32(x[i], y[t], acc[i][t]);
+      for (int t = 0; t < kZTiles; ++t) acc[i][t] = mfma32(part[part_of(t)], unpack_u8x8(y[slot][t]), acc[i][t]);
     }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (k0 + wave < k1) {
+    static_for<0, kDepth>([&](auto i) { load(k0 + wave + kWaves * decltype(i)::value, i); });
+    int g0 = k0 + wave;
+    for (; g0 + kWaves * (kDepth - 1) < k1; g0 += kWaves * kDepth)
+      static_for<0, kDepth>([&](auto i) {
+        use(i);
+        load(g0 + kWaves * (decltype(i)::value + kDepth), i);
+      });
+    static_for<0, kDepth - 1>([&](auto i) {
+      if (g0 + kWaves * decltype(i)::value < k1) use(i);
+    });
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -584,9 +614,9 @@ __global__ __launch_bounds__(kZThreads, 2) void xent_z_kernel(const ManyArgs a) 
     if (wave != 0) continue;
 #pragma unroll
     for (int t = 0; t < kZTiles; ++t) {
-      const bool in_c = t0 + t < b.nct;
-      const int j = 32 * (in_c ? t0 + t : t0 + t - b.nct) + c32;
-      if (t0 + t >= tiles || j >= (in_c ? b.r_c : b.r_r)) continue;
+      const bool in_c = part_of(t) == 0;
+      const int j = 32 * place_of(t) + c32;
+      if (j >= (in_c ? b.r_c : b.r_r)) continue;
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
         const int64_t n = 32 * (tile0 + i) + 8 * (v >> 2) + 4 * half + (v & 3);
@@ -614,14 +644,14 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(const ManyArgs a) {
   if (threadIdx.x == 0) {
     const int64_t n = a.map[at];
     const double w = a.weight ? (double)a.weight[n] : 1.0, s = a.sum[i];
-    const float yl = a.y_label[i];
+    const float zl = a.z_label[i];
     double logp = 0.0, q = 0.0;
     RowOut out{0.0f, 0.0f};
-    if (!(fabsf(yl) < __builtin_huge_valf())) {
+    if (!(fabsf(zl) < __builtin_huge_valf())) {
       logp = q = __builtin_nan("");
       out.mean = (float)q;
     } else if (s != 0.0) {  // (a vocabulary of one entry: p = 1)
-      const double d = log(s) + ((double)a.top[i] - kExpTop) * 0.6931471805599453 - (double)a.tau * (double)yl;
+      const double d = log(s) + ((double)a.top[i] - (double)zl) * 0.6931471805599453;
       logp = d == d ? -(fmax(d, 0.0) + log1p(exp(-fabs(d)))) : d;
       q = 1.0 / (1.0 + exp(-d));
       out.mean = (float)(w * (double)a.tau * q / s);
@@ -640,7 +670,7 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(const ManyArgs a) {
     for (int p = 0; p < b.zparts; ++p) z += b.zpart[((int64_t)p * b.n32 + i) * r + j];
     const bool in_c = j < b.r_c;
     const float al = (float)b.a_codes[l * r + j] * f16_to_f32(b.a_scales[l * b.nA + (in_c ? 0 : b.nA - 1)]);
-    b.z[i * r + j] = sOut.mean * (z * a.scale[in_c ? 3 : 5]) - sOut.label * al;
+    b.z[i * r + j] = sOut.mean * (z * a.scale[in_c ? 2 : 3]) - sOut.label * al;
   }
 }
 
@@ -659,11 +689,12 @@ __global__ __launch_bounds__(kFinishThreads, 2) void xent_finish_kernel(const Ma
   const int64_t d = kKTile * kt + 4 * c32, group = d / b.g;
   // row of element v of a result tile; past the last row that one
   auto row = [&](int v) { return std::min<int64_t>(n0 + 8 * (v >> 2) + 4 * half + (v & 3), count - 1); };
+  const int splits = a.splits[a.pass];
   f16x acc[4] = {};
-  for (int p = 0; p < b.splits; ++p) {
+  for (int p = 0; p < splits; ++p) {
     f4 y[16];
 #pragma unroll
-    for (int v = 0; v < 16; ++v) y[v] = *reinterpret_cast<const f4*>(b.part + ((int64_t)p * b.N + row(v)) * b.D + d);
+    for (int v = 0; v < 16; ++v) y[v] = *reinterpret_cast<const f4*>(b.part + ((int64_t)p * count + row(v)) * b.D + d);
 #pragma unroll
     for (int v = 0; v < 16; ++v)
 #pragma unroll
@@ -867,9 +898,16 @@ int launch_few_rows(const archead_tensor* H, const archead_packed_head* head, co
 struct ManyLayout {
   int64_t rows, n32, vtiles, piece;  // rows of a pass; 256-row tiles of the vocabulary, of a piece
   int splits, zparts, passes;
-  uint64_t terms, head_max, scale, map, label, counts, fwd, fwd_bytes, Hc, e, stat, factor, alpha, top, sum, y_label, row, af,
-      zpart, z, part, total;
+  uint64_t terms, head_max, scale, scale_a, map, label, counts, splits_at, fwd, fwd_bytes, Hc, e, stat,
+      alpha, top, sum, z_label, row, af, zpart, z, part, total;
 };
+
+// Workgroups of xent_z_kernel side by side for the ranks.
+int z_groups(const archead_dims* d) { return (std::max(d->r_c, d->r_r) + 16 * kZTiles - 1) / (16 * kZTiles); }
+
+// Steps of a row tile of a piece's operands: a few more than there are, as row
+// tiles that are a power of two apart meet in the same memory channels.
+int64_t piece_steps(int64_t vtiles) { return 16 * vtiles + 5; }
 
 ManyLayout many_layout(const archead_dims* d, int64_t N) {
   ManyLayout L{};
@@ -884,7 +922,7 @@ ManyLayout many_layout(const archead_dims* d, int64_t N) {
   if (pieces > 1) L.piece = std::min((int64_t)round_up((uint64_t)L.piece, 16), std::max<int64_t>(most / 16 * 16, 1));
   L.splits = main_splits(L.rows, d->D, 0, 4 * L.piece);
   const int64_t r = d->r_c + d->r_r, tiles = (d->r_c + 31) / 32 + (d->r_r + 31) / 32;
-  const int64_t groups = (L.n32 + 63) / 64 * std::max<int64_t>(1, (tiles + kZTiles - 1) / kZTiles);
+  const int64_t groups = (L.n32 + 63) / 64 * std::max(1, z_groups(d));
   L.zparts = (int)std::max<int64_t>(1, std::min<int64_t>({(256 + groups - 1) / groups, L.piece, 64}));
   auto take = [&](uint64_t bytes) {
     const uint64_t at = L.total;
@@ -894,22 +932,23 @@ ManyLayout many_layout(const archead_dims* d, int64_t N) {
   const uint64_t n32 = (uint64_t)L.n32, blocks = 8 * (uint64_t)L.piece;
   L.terms = take((uint64_t)N * 8);
   L.head_max = take(kHeadParts * 12);
-  L.scale = take(24);
+  L.scale = take(16);
+  L.scale_a = take(2 * 256 * (uint64_t)L.vtiles * 2);
   L.map = take((uint64_t)N * 4);
   L.label = take((uint64_t)std::max(N, L.passes * L.rows) * 4);  // whole passes are read
   L.counts = take((uint64_t)L.passes * 4);
+  L.splits_at = take((uint64_t)L.passes * 4);
   L.fwd_bytes = workspace_layout(d, L.rows, false, 0, false).total;
   L.fwd = take(L.fwd_bytes);
   L.Hc = take(n32 * (uint64_t)d->D * 2);
-  L.e = take(n32 * (uint64_t)L.piece * 512);
+  L.e = take(n32 / 32 * (uint64_t)piece_steps(L.piece) * 1024);
   L.stat = take(blocks * n32 * 8);
-  L.factor = take(blocks * n32 * 4);
   L.alpha = take(n32 * 4);
   L.top = take(n32 * 4);
   L.sum = take(n32 * 8);
-  L.y_label = take(n32 * 4);
+  L.z_label = take(n32 * 4);
   L.row = take(n32 * sizeof(RowOut));
-  L.af = take((uint64_t)tiles * (uint64_t)L.vtiles * 16 * 1024);
+  L.af = take((uint64_t)tiles * (uint64_t)L.vtiles * 16 * 512);
   L.zpart = take((uint64_t)L.zparts * n32 * (uint64_t)r * 4);
   L.z = take(n32 * (uint64_t)r * 4);
   L.part = take((uint64_t)L.splits * (uint64_t)L.rows * (uint64_t)d->D * 4);
@@ -944,6 +983,7 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
   b.N = L.rows;
   b.n32 = L.n32;
   b.hf = reinterpret_cast<_Float16*>(ws + L.e);
+  b.af = ws + L.af;
   b.zpart = reinterpret_cast<float*>(ws + L.zpart);
   b.z = reinterpret_cast<float*>(ws + L.z);
   b.part = reinterpret_cast<float*>(ws + L.part);
@@ -962,19 +1002,20 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
   }
   a.head_max = reinterpret_cast<float*>(ws + L.head_max);
   a.scale = reinterpret_cast<float*>(ws + L.scale);
+  a.scale_a = reinterpret_cast<_Float16*>(ws + L.scale_a);
+  a.splits = reinterpret_cast<int32_t*>(ws + L.splits_at);
   a.map = reinterpret_cast<int32_t*>(ws + L.map);
   a.label = reinterpret_cast<int32_t*>(ws + L.label);
   a.counts = reinterpret_cast<int32_t*>(ws + L.counts);
   a.terms = reinterpret_cast<double*>(ws + L.terms);
   a.Hc = reinterpret_cast<uint16_t*>(ws + L.Hc);
   a.stat = reinterpret_cast<float*>(ws + L.stat);
-  a.factor = reinterpret_cast<uint32_t*>(ws + L.factor);
   a.alpha = reinterpret_cast<float*>(ws + L.alpha);
   a.top = reinterpret_cast<float*>(ws + L.top);
   a.sum = reinterpret_cast<double*>(ws + L.sum);
-  a.y_label = reinterpret_cast<float*>(ws + L.y_label);
+  a.z_label = reinterpret_cast<float*>(ws + L.z_label);
+  a.steps = (int)piece_steps(L.piece);
   a.row = reinterpret_cast<RowOut*>(ws + L.row);
-  a.af = reinterpret_cast<_Float16*>(ws + L.af);
   a.asteps = 16 * L.vtiles;
   // the tile path's arguments, for the gathered rows
   archead_tensor h{a.Hc, L.rows, d->D, d->D, ARCHEAD_BF16};
@@ -986,9 +1027,16 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
   const int tiles = b.nct + b.nwt;
   (void)hipGetLastError();  // start from a clean error state
   hipLaunchKernelGGL(xent_head_kernel, dim3(kHeadParts), dim3(kHeadThreads), 0, s, a);
-  hipLaunchKernelGGL(xent_order_kernel, dim3(1), dim3(kOrderThreads), 0, s, a, L.passes);
-  if (a.dH && tiles)
-    hipLaunchKernelGGL(xent_factors_kernel, dim3((unsigned)((tiles * a.asteps * 16 + 255) / 256)), dim3(256), 0, s, a);
+  const int tt = main_tiles(L.rows);
+  a.passes = L.passes;
+  a.tile_rows = 32 * tt;
+  b.ksteps = (int)(16 * L.piece);
+  hipLaunchKernelGGL(xent_order_kernel, dim3((unsigned)(1 + (16 * a.asteps + kOrderThreads - 1) / kOrderThreads)), dim3(kOrderThreads), 0, s, a);
+  if (a.dH && tiles) {
+    BwdArgs all = b;
+    all.ksteps = (int)a.asteps;
+    hipLaunchKernelGGL(xent_arrange_kernel, dim3((unsigned)((tiles * a.asteps * 16 + 255) / 256)), dim3(256), 0, s, all);
+  }
   if (a.dH && a.weight) hipLaunchKernelGGL(xent_zero_kernel, dim3((unsigned)N), dim3(256), 0, s, a);
   for (int pass = 0; pass < L.passes; ++pass) {
     a.pass = pass;
@@ -999,12 +1047,13 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
       T32Exp ex{};
       ex.n_rows = a.counts + pass;
       ex.labels = a.label + pass * kChunkRows;
-      set_exponent(in->inv_temperature, ex.c_hi, ex.c_lo);
+      ex.c = 1.4426950408889634 * (double)in->inv_temperature;
       ex.vt0 = (int)vt;
       ex.vtiles = (int)vn;
       ex.e = a.dH ? b.hf : nullptr;
+      ex.steps = a.steps;
       ex.stat = a.stat;
-      ex.y_label = a.y_label;
+      ex.z_label = a.z_label;
       if (launch_tile_exp(f, ex, s) != hipSuccess) return ARCHEAD_E_HIP;
       a.blocks = (int)(8 * vn);
       a.first = vt == 0;
@@ -1013,10 +1062,9 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
       hipLaunchKernelGGL(xent_merge_kernel, dim3((unsigned)(L.n32 / 32)), dim3(32 * kMergeSlices), 0, s, a);
       if (!a.dH) continue;
       if (tiles)
-        hipLaunchKernelGGL(xent_z_kernel, dim3((unsigned)((L.n32 + 63) / 64), (unsigned)L.zparts, (unsigned)((tiles + kZTiles - 1) / kZTiles)),
+        hipLaunchKernelGGL(xent_z_kernel, dim3((unsigned)((L.n32 + 63) / 64), (unsigned)L.zparts, (unsigned)z_groups(d)),
                            dim3(kZThreads), 0, s, a);
-      const MainExp me{a.counts + pass, a.factor, a.alpha, a.scale, a.first, (int)(4 * vt)};
-      const int tt = main_tiles(L.rows);
+      const MainExp me{a.counts + pass, a.splits + pass, a.stat, a.top, a.alpha, a.scale, a.steps, a.first, (int)(4 * vt)};
       if (tt == 2)
         launch_xent_main<2>(b, me, s);
       else if (tt == 4)
