@@ -374,29 +374,31 @@ __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& e
   // columns sit in the tile in the order the unpacking gives them
   const int c32 = lane & 31;
 #pragma unroll
-  for (int m = 0; m < S::MT; ++m)
+  for (int m = 0; m < S::MT; ++m) {
+    auto column = [&](int c) { return 256 * (int64_t)cb + 32 * (wn * S::NT + c) + 8 * (c32 >> 3) + k_order_h(c32 & 7); };
+    auto row = [&](int v) { return 32 * (int64_t)(tb * TT + wm * S::MT + m) + 8 * (v >> 2) + 4 * khalf + (v & 3); };
+    if constexpr (EX) {
+      if (!ex.first) {  // all loads of a row tile in flight together
+        float old[S::NT][16], al[16];
 #pragma unroll
-    for (int c = 0; c < S::NT; ++c) {
-      const int64_t d = 256 * (int64_t)cb + 32 * (wn * S::NT + c) + 8 * (c32 >> 3) + k_order_h(c32 & 7);
-      if constexpr (EX) {
-        if (!ex.first) {
-          float old[16], al[16];
+        for (int v = 0; v < 16; ++v) {  // rows and columns past the last: those, not stored
+          const int64_t n = std::min(row(v), rows - 1);
+          al[v] = ex.alpha[n];
 #pragma unroll
-          for (int v = 0; v < 16; ++v) {  // rows and columns past the last: those, not stored
-            const int64_t n = std::min<int64_t>(32 * (int64_t)(tb * TT + wm * S::MT + m) + 8 * (v >> 2) + 4 * khalf + (v & 3), rows - 1);
-            old[v] = a.part[((int64_t)split * rows + n) * a.D + std::min(d, a.D - 1)];
-            al[v] = ex.alpha[n];
-          }
-#pragma unroll
-          for (int v = 0; v < 16; ++v) acc[m][c][v] = fmaf(al[v], old[v], acc[m][c][v]);
+          for (int c = 0; c < S::NT; ++c) old[c][v] = a.part[((int64_t)split * rows + n) * a.D + std::min(column(c), a.D - 1)];
         }
-      }
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int64_t n = 32 * (int64_t)(tb * TT + wm * S::MT + m) + 8 * (v >> 2) + 4 * khalf + (v & 3);
-        if (n < rows && d < a.D) a.part[((int64_t)split * rows + n) * a.D + d] = acc[m][c][v];
+        for (int c = 0; c < S::NT; ++c)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[m][c][v] = fmaf(al[v], old[c][v], acc[m][c][v]);
       }
     }
+#pragma unroll
+    for (int c = 0; c < S::NT; ++c)
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        if (row(v) < rows && column(c) < a.D) a.part[((int64_t)split * rows + row(v)) * a.D + column(c)] = acc[m][c][v];
+  }
 }
 
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));

@@ -611,19 +611,26 @@ __global__ __launch_bounds__(kZThreads, 2) void xent_z_kernel(const ManyArgs a) 
           for (int v = 0; v < 16; ++v) acc[i][t][v] += red[wave][t][v][lane];
       }
     }
-    if (wave != 0) continue;
+    if (wave != 0 || tile0 + i >= ntiles) continue;
+    float alpha[16];
+#pragma unroll
+    for (int v = 0; v < 16; ++v) alpha[v] = a.alpha[32 * (tile0 + i) + 8 * (v >> 2) + 4 * half + (v & 3)];
 #pragma unroll
     for (int t = 0; t < kZTiles; ++t) {
       const bool in_c = part_of(t) == 0;
       const int j = 32 * place_of(t) + c32;
       if (j >= (in_c ? b.r_c : b.r_r)) continue;
+      // (rows of a tile past the last one that counts have a place, too)
+      float* z = b.zpart + ((int64_t)blockIdx.y * b.n32 + 32 * (tile0 + i) + 4 * half) * r + (in_c ? 0 : b.r_c) + j;
+      if (!a.first) {
+        float old[16];
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int64_t n = 32 * (tile0 + i) + 8 * (v >> 2) + 4 * half + (v & 3);
-        if (n >= count) continue;
-        float* z = b.zpart + ((int64_t)blockIdx.y * b.n32 + n) * r + (in_c ? 0 : b.r_c) + j;
-        *z = a.first ? acc[i][t][v] : fmaf(a.alpha[n], *z, acc[i][t][v]);
+        for (int v = 0; v < 16; ++v) old[v] = z[(8 * (v >> 2) + (v & 3)) * r];
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][t][v] = fmaf(alpha[v], old[v], acc[i][t][v]);
       }
+#pragma unroll
+      for (int v = 0; v < 16; ++v) z[(8 * (v >> 2) + (v & 3)) * r] = acc[i][t][v];
     }
   }
 }
