@@ -45,7 +45,6 @@ constexpr int kZsumThreads = 512, kZsumRanks = 64;
 constexpr int kFinishThreads = 256;
 constexpr int kFinishRows = 8;
 constexpr int kMaxMaxPieces = 128;
-constexpr int kMaxSplits = 64;
 // Where kOwnRounds rounds of loads reach all of dY, every workgroup of
 // bwd_prep_kernel finds the rows' maxima itself: a call of 4 rows of a 1024 x
 // 256 head takes 20 us, with a launch for them 24; sixteen rounds 25 and 24,
@@ -916,28 +915,10 @@ __global__ __launch_bounds__(kFinishThreads, 2) void bwd_finish_many_kernel(cons
 
 }  // namespace
 
-// Parts of the vocabulary for the main kernel: the count that a model of its
-// time likes best, workgroups in rounds of the resident ones (two a CU for
-// 64-token tiles, else one) of kRoundUs plus a stage's measured
-// time for every stage, and the partial sums written and read at 4 TB/s.
 int main_splits(int64_t N, int64_t D, int64_t ranks, int64_t stages) {
-  constexpr double kRoundUs = 4.0;
   if (N <= kFewTokens)  // two workgroups a CU; a packed tile for each wave at least
     return (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, 512 / (D / kKTile + ranks), (stages + 1) / 2}));
-  const int tt = main_tiles(N);
-  const int64_t tiles = (N + 32 * tt - 1) / (32 * tt) * ((D + 255) / 256), slots = tt == 2 ? 512 : 256;
-  const double stage_us = tt == 8 ? 1.75 : tt == 4 ? 1.15 : 1.4;
-  double best = 1e30;
-  int pick = 1;
-  for (int64_t p = 1; p <= std::min<int64_t>(kMaxSplits, stages); ++p) {
-    const double us = (double)((tiles * p + slots - 1) / slots) * (kRoundUs + stage_us * (double)((stages + p - 1) / p)) +
-                      (double)(p * N * D) * 8.0 / 4e6;
-    if (us < best) {
-      best = us;
-      pick = (int)p;
-    }
-  }
-  return pick;
+  return best_parts(N, D, stages, main_tiles(N), std::min<int64_t>(kMaxSplits, stages));
 }
 
 namespace {

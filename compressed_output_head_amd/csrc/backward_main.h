@@ -45,7 +45,28 @@ struct BwdArgs {
 // The kernels of up to kFewTokens rows on operands that are in place: a.part
 // and a.zpart from a.hf and a.gt (backward.hip).
 hipError_t launch_bwd_few(const BwdArgs& a, hipStream_t s);
-// Parts of the vocabulary for `ranks` tiles of 32 ranks (0: none are in the product).
+constexpr int kMaxSplits = 64;
+// Parts of the vocabulary for the main kernel, at most `most`: the count that a
+// model of its time likes best, workgroups in rounds of the resident ones (two
+// a CU for 64-row tiles, else one) of kRoundUs plus a stage's measured time for
+// every stage, and the partial sums written and read at 4 TB/s.
+__host__ __device__ inline int best_parts(int64_t N, int64_t D, int64_t stages, int tt, int64_t most) {
+  constexpr double kRoundUs = 4.0;
+  const int64_t tiles = (N + 32 * tt - 1) / (32 * tt) * ((D + 255) / 256), slots = tt == 2 ? 512 : 256;
+  const double stage_us = tt == 8 ? 1.75 : tt == 6 ? 1.45 : tt == 4 ? 1.15 : 1.4;
+  double best = 1e30;
+  int pick = 1;
+  for (int64_t p = 1; p <= most; ++p) {
+    const double us = (double)((tiles * p + slots - 1) / slots) * (kRoundUs + stage_us * (double)((stages + p - 1) / p)) +
+                      (double)(p * N * D) * 8.0 / 4e6;
+    if (us < best) {
+      best = us;
+      pick = (int)p;
+    }
+  }
+  return pick;
+}
+// Parts of the vocabulary for `ranks` tiles of 32 ranks (of few rows).
 int main_splits(int64_t N, int64_t D, int64_t ranks, int64_t stages);
 inline int main_tiles(int64_t N) { return N <= 64 ? 2 : N <= 128 ? 4 : 8; }
 
@@ -176,28 +197,19 @@ struct MainShape {
 // The product of a piece's exponentials (tile32_exp_kernel's operands, a.hf)
 // with the residual, added to the sums of the pieces before it.
 struct MainExp {
-  const int32_t* n_rows;   // rows that count
-  const int32_t* splits;   // parts of the piece: sums are [splits][rows that count][D]
-  const float* stat;       // [32-row block of the piece][n32][2] the operands' exponents M
-  const float* top;        // [n32] the rows' exponents
-  const float* alpha;      // [n32] what brings the sums so far there, a power of two
+  const int32_t* plan;     // {rows that count, row tiles of a workgroup, parts of the piece}; sums are
+                           // [parts][rows that count][D]
+  const float* alpha;      // [n32] what brings the sums so far to the operands' exponents, a power of two
   const float* scale;      // [1] the power of two that the row scales s_R are taken with
   int steps;               // of a row tile in a.hf
   int first;               // no sums yet
   int stage0;              // first stage of the piece in the vocabulary
 };
-// Operands are brought to the rows' exponents times 2^14: exactly, but for what
-// ends below 2^-14, 2^-28 of the row's largest.
-constexpr int kFactorTop = 14;
-
-// 2^t in fp16, t whole (0 where it is not a number or below fp16's range)
-__device__ __forceinline__ _Float16 fp16_power(float t) { return (_Float16)ldexpf(1.0f, (int)fmaxf(t, -100.0f)); }
 
 // kCodes: group codes of 128 columns of a row: 4 for g = 32, 2 for 64, else 1.
-// EX: a.hf and a.ksteps are of the piece of `ex`, the fragments are brought to
-// the rows' exponents on their way to LDS, and the residual's operand is (q4 c8)
-// s_R, rounded to fp16 (2^-11).  (With s_R in a second set of fragments from
-// the kernel that makes them, that kernel takes 12% longer and this one 1% less.)
+// EX: a.hf and a.ksteps are of the piece of `ex`, and the residual's operand is
+// (q4 c8) s_R, rounded to fp16 (2^-11).  (With s_R in a second set of fragments
+// from the kernel that makes them, that kernel takes 12% longer; here it takes 4%.)
 template <int TT, int kCodes, bool EX>
 __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& ex) {
   using S = MainShape<TT>;
@@ -207,9 +219,10 @@ __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& e
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
-  const int64_t rows = EX ? *ex.n_rows : a.N;
+  if (EX && ex.plan[1] != TT) return;
+  const int64_t rows = EX ? ex.plan[0] : a.N;
   const int CB = (int)((a.D + 255) / 256), ntiles = (int)((EX ? rows + 31 : a.n32) / 32), TB = (ntiles + TT - 1) / TT;
-  const int splits = EX ? *ex.splits : a.splits, items = EX ? CB * TB * splits : gridDim.x;
+  const int splits = EX ? ex.plan[2] : a.splits, items = EX ? CB * TB * splits : gridDim.x;
   if (EX && (int)blockIdx.x >= items) return;
   // Workgroups are dealt to the XCDs round robin: each XCD gets a contiguous
   // range of (split, token block, column block), so that those in one L2 share
@@ -228,15 +241,8 @@ __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& e
   u4 w[kDepth];
   uint32_t code[kDepth];
   h8 av[kDepth][S::kLoads];
-  // EX: the row's s_R; the row's exponent in each fragment's block, and over all
-  uint16_t rs[EX ? kDepth : 1];
-  float fm[EX ? kDepth : 1][S::kLoads], ft[S::kLoads], scale = 1.0f;
-  if constexpr (EX) {
-    scale = *ex.scale;
-#pragma unroll
-    for (int i = 0; i < S::kLoads; ++i)
-      ft[i] = ex.top[32 * (int64_t)std::min(tb * TT + (8 * i + wave) / 4, ntiles - 1) + (lane & 31)] - (float)kFactorTop;
-  }
+  uint16_t rs[EX ? kDepth : 1];  // EX: the row's s_R
+  const float scale = EX ? *ex.scale : 1.0f;
   auto load = [&](int s, auto slot_) {
     constexpr int slot = decltype(slot_)::value;
     s = std::min(s, s1 - 1);  // past the end: a stage that is cached, never used
@@ -252,7 +258,6 @@ __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& e
     for (int i = 0; i < S::kLoads; ++i) {
       const int f = 8 * i + wave;
       const int64_t tile = std::min(tb * TT + f / 4, ntiles - 1);
-      if constexpr (EX) fm[slot][i] = ex.stat[2 * ((2 * (int64_t)s + (wave & 3) / 2) * a.n32 + 32 * tile + (lane & 31))];
       av[slot][i] = *reinterpret_cast<const h8*>(a.hf + ((tile * (EX ? ex.steps : a.ksteps) + 4 * s + f % 4) * 64 + lane) * 8);
     }
   };
@@ -272,14 +277,7 @@ __device__ __forceinline__ void bwd_main_body(const BwdArgs& a, const MainExp& e
   auto put_fragments = [&](auto buf_, auto slot_) {
     constexpr int buf = decltype(buf_)::value, slot = decltype(slot_)::value;
 #pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) {
-      h8 x = av[slot][i];
-      if constexpr (EX) {
-        const _Float16 f = fp16_power(fm[slot][i] - ft[i]);
-        x = x * h8{f, f, f, f, f, f, f, f};
-      }
-      sA[buf][8 * i + wave][lane] = x;
-    }
+    for (int i = 0; i < S::kLoads; ++i) sA[buf][8 * i + wave][lane] = av[slot][i];
   };
 
   f16x acc[S::MT][S::NT] = {};

@@ -141,28 +141,44 @@ struct FwdArgs {
 // The exponentials' epilogue (tile32_exp_kernel): the logits of a piece of the
 // vocabulary, whole 256-row tiles [vt0, vt0 + vtiles), leave as operands of the
 // products that follow, and as what the softmax's sum needs of them.  An
-// operand is e = 2^(z - M) in fp16, z = log2(e) times the scaled logit and M the
-// least whole number that none of a row's z in its 32-row block exceeds, so that
-// blocks differ by exact powers of two.  e is off by half a step, 2^-11 of
-// itself, or below 2^-14 by 2^-25, which is at most 2^-20 of the block's largest
-// in all of its 32 entries.
+// operand is 2^(z - B + kExpTop) in fp16, z = log2(e) times the scaled logit and
+// B a whole number: the row's exponent from the pieces before where none of its
+// z in the 32-row block exceeds that by more than 1, else the least that none
+// exceeds.  So blocks differ by exact powers of two, nearly always by none.  An
+// operand is at most 2^15 and off by half a step, 2^-11 of itself, or below
+// 2^-14 by 2^-25.
+constexpr int kExpTop = 14;
 struct T32Exp {
-  const int32_t* n_rows;  // rows of H that count; N and n32 of FwdArgs are the most there can be
+  const int32_t* plan;    // {rows of H that count, 32-row tiles of a workgroup}; N and n32 of FwdArgs are the most there can be
   const int32_t* labels;  // [N] by row of H
   double c;               // log2(e) times the inverse temperature
   int vt0, vtiles;
   _Float16* e;            // null, or operands [n32/32][steps][64][8], lane l: row l % 32, vocabulary rows
                           // 16 step + 8 (l / 32) .. + 8 of the piece
   int steps;              // at least 16 vtiles
-  float* stat;            // [8 vtiles][n32][2] by 32-row block: M, the sum of e
+  const float* ref;       // [n32] the rows' exponents (-inf: none yet)
+  float* stat;            // [8 vtiles][n32][2] by 32-row block: B, the sum of the operands before rounding
   float* z_label;         // [n32] the label's z, written where it is met
 };
+
+// Row tiles of 32 for a workgroup of the kernels that multiply with the head,
+// for `tiles` of them in all: a workgroup's time goes about as tiles + 4.
+// few: 2 and 4 may be taken (D of 256 at least).
+__host__ __device__ inline int exp_tiles(int64_t tiles, bool few) {
+  int best = 8;
+  for (int t = 6; t >= (few ? 2 : 6); t -= 2)
+    if ((tiles + t - 1) / t * (t + 4) < (tiles + best - 1) / best * (best + 4)) best = t;
+  return best;
+}
+// Passes of more rows than this take 8: another number saves little.
+constexpr int64_t kExpFewRows = 1024;
 
 // FwdArgs of the tile path without split tiles (workspace_layout(d, N, false,
 // 0, false)), with the checks of archead_logits.
 int tile_args(const archead_tensor* H, const archead_packed_head* head, FwdArgs& a);
 // The tile kernel with the exponentials' epilogue on H and Z in place.
-hipError_t launch_tile_exp(const FwdArgs& a, const T32Exp& ex, hipStream_t s);
+// `tt`: of the launches for 2, 4, 6 and 8 row tiles a workgroup, the one that ex.plan names runs.
+hipError_t launch_tile_exp(const FwdArgs& a, const T32Exp& ex, int tt, hipStream_t s);
 // Whether archead_logits takes a call of n_tokens rows (of fp32 logits that
 // span less than 4 GiB).
 bool forward_takes(const archead_dims* d, int64_t n_tokens);

@@ -147,10 +147,11 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
   constexpr int kSPT = 8 / KS;                // stages per 128-column k-tile
   constexpr int kT32HOps = TT * KS / kT32Waves;  // H copies per wave and stage
   constexpr int kWOps = kT32WCB * KS / 4;        // W loads per wave and stage
-  static_assert(kT32HOps >= 1 && TT * KS == kT32HOps * kT32Waves, "TT must be 2, 4 or 8");
+  static_assert(kT32HOps >= 1 && TT * KS == kT32HOps * kT32Waves, "TT must be 2, 4, 6 or 8");
   __shared__ h8 sH0[kT32TT][KS][64], sH1[kT32TT][KS][64], sH2[kT32TT][KS][64], sH3[kT32TT][KS][64];
   extern __shared__ __align__(16) uint8_t sCode[];  // [256 rows][t32_code_stride(ng)], sized at launch
   __shared__ float sTok[kT32TT * 32][2];  // hscale, zscale of the workgroup's tokens
+  __shared__ float sRef[EX ? kT32TT * 32 : 1];  // the tokens' exponents
   __shared__ int sTgt[ST || EX ? kT32TT * 32 : 1];  // targets of the workgroup's tokens (statistics, exponentials)
   __shared__ __align__(16) float sVR[kT32CB * 32], sVC[kT32CB * 32], sVW[kT32CB * 32];  // s_R, s_Ac, s_Aw
   const int tid = threadIdx.x, lane = tid & 63;
@@ -160,7 +161,8 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
   T32Grid G = t32_grid(a, TT);
   int whole_tiles = sp.full;
   if constexpr (EX) {  // the tiles of the rows that count
-    G.ntiles = (*ex.n_rows + 31) >> 5;
+    if (ex.plan[1] != TT) return;
+    G.ntiles = (ex.plan[0] + 31) >> 5;
     G.ttiles = (G.ntiles + TT - 1) / TT;
     G.vtiles = ex.vtiles;
     whole_tiles = G.ttiles * G.vtiles;
@@ -363,6 +365,7 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
     if constexpr (EX) {
       const int label = ex.labels[tok < a.N ? tok : a.N - 1];
       sTgt[tid] = label < a.V ? label : -1;
+      sRef[tid] = ex.ref[tok];
     }
   }
   static_assert(kT32Threads >= kT32CB * 32, "one thread per vocabulary row of the workgroup");
@@ -564,7 +567,8 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
       for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
       top = fmaxf(top, __shfl_xor(top, 32));
       // no entry, or none above -inf: operands of 0 (a row that is not finite shows in its sum)
-      const float M = ceilf(top), low = top == -infinity ? 0.0f : M;
+      const float M = ceilf(top), ref = sRef[32 * m + c32];
+      const float B = M <= ref + 1.0f ? ref : M, low = B == -infinity ? 0.0f : B - (float)kExpTop;
       float sum = 0.0f;
       uint32_t pk[8];
 #pragma unroll
@@ -575,7 +579,7 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
       }
       sum += __shfl_xor(sum, 32);
       const int64_t tok = 32 * (int64_t)(tt0 + m) + c32;
-      if (g == 0) reinterpret_cast<u2*>(ex.stat)[(int64_t)blk * a.n32 + tok] = u2{__float_as_uint(M), __float_as_uint(sum)};
+      if (g == 0) reinterpret_cast<u2*>(ex.stat)[(int64_t)blk * a.n32 + tok] = u2{__float_as_uint(B), __float_as_uint(sum)};
       if (!ex.e) return;
       // lane halves hold the two fours of each eight rows; a fragment wants eights in one lane
       u4* out = reinterpret_cast<u4*>(ex.e) + ((int64_t)(tt0 + m) * ex.steps + 2 * blk) * 64 + lane;

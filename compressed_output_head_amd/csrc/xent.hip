@@ -20,6 +20,7 @@
 //                           and a sum for each row and 32 entries
 //   xent_merge_kernel       the rows' running exponent and sum, and what brings
 //                           the sums before the piece to that exponent
+//   xent_move_kernel        operands at other exponents than their row's
 //   xent_z_kernel           (e s_A) code added to Z
 //   xent_main_kernel        e (s_R q4 c8) added to the sums
 // and at the end xent_rows_kernel (log p, Z), xent_finish_kernel (dH).
@@ -345,19 +346,19 @@ struct ManyArgs {
   _Float16* scale_a;       // [2][16 vtiles of V][16] s_Ac, s_Aw times powers of two
   int32_t* map;            // [rows] rows that count, in order
   int32_t* label;          // [rows] their labels
-  int32_t* counts;         // [passes] of each pass
-  int32_t* splits;         // [passes] parts of a piece in the product of each pass
+  int32_t* plan;           // [passes][4] rows that count, row tiles of a workgroup, parts of a piece's product
   double* terms;           // [rows] -w log p by row of the call
   uint16_t* Hc;            // [n32][D] gathered H
   float* stat;             // [blocks][n32][2]
   float* alpha;            // [n32]
-  float* top;              // [n32] running exponent
+  float* ref;              // [n32] running exponent
+  int32_t* moved;          // [n32/32] whether operands of a row tile are at others
   double* sum;             // [n32] running sum
   float* z_label;          // [n32] log2(e) tau times the label's logit
   RowOut* row;             // [n32]
   int64_t asteps;          // steps of the whole vocabulary
   int pass, passes, blocks, first, step0, steps;
-  int tile_rows;           // rows of a workgroup of the product
+  int64_t part_rows;       // room for partial sums
 };
 
 // Largest |s_R|, |s_Ac|, |s_Aw| of a part of the vocabulary.
@@ -383,9 +384,13 @@ __global__ __launch_bounds__(kHeadThreads) void xent_head_kernel(const ManyArgs 
   }
 }
 
-// Workgroup 0: the rows that count, in order, and how many parts the product
-// of each pass is cut into: as many as keep its workgroups what they are for a
-// pass of rows that all count.  The others: what the head's scales give.
+// Workgroups of the product's launches, for any number of rows that count.
+__host__ __device__ inline int64_t main_groups(int64_t rows, int64_t D, int tt) {
+  return std::max<int64_t>((rows + 32 * tt - 1) / (32 * tt) * ((D + 255) / 256), tt == 2 ? 1024 : 512);
+}
+
+// Workgroup 0: the rows that count, in order, and how the kernels that multiply
+// with the head cut each pass.  The others: what the head's scales give.
 __global__ __launch_bounds__(kOrderThreads) void xent_order_kernel(const ManyArgs a) {
   const int tid = threadIdx.x;
   if (blockIdx.x > 0) {
@@ -399,7 +404,7 @@ __global__ __launch_bounds__(kOrderThreads) void xent_order_kernel(const ManyArg
       k[q] = std::max(-100, std::min(q == 0 ? row_exponent(2040.0f * m) : row_exponent(m) - 15, 100));
     }
     const int64_t i = ((int64_t)blockIdx.x - 1) * kOrderThreads + tid;
-    if (i < 4) a.scale[i] = ldexpf(1.0f, i == 0 ? k[0] : -k[i - 1] - kFactorTop);
+    if (i < 4) a.scale[i] = ldexpf(1.0f, i == 0 ? k[0] : -k[i - 1]);
     if (i < 16 * a.asteps)
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -434,11 +439,13 @@ __global__ __launch_bounds__(kOrderThreads) void xent_order_kernel(const ManyArg
   const int64_t total = sCount[kOrderThreads - 1];
   for (int p = tid; p < a.passes; p += kOrderThreads) {
     const int64_t count = std::max<int64_t>(0, std::min(total - p * kChunkRows, kChunkRows));
-    const int64_t most = (a.b.N + a.tile_rows - 1) / a.tile_rows, tiles = std::max<int64_t>(1, (count + a.tile_rows - 1) / a.tile_rows);
-    a.counts[p] = (int32_t)count;
-    // (of which there is room for, too: tiles of rows in fewer of them)
-    const int64_t parts = std::min(a.b.splits * most / tiles, a.b.splits * a.b.N / std::max<int64_t>(count, 1));
-    a.splits[p] = (int32_t)std::max<int64_t>(1, std::min<int64_t>(parts, std::max<int64_t>(a.b.splits, a.b.ksteps / 32)));
+    const int tt = a.b.N > kExpFewRows ? 8 : exp_tiles((count + 31) / 32, a.b.D >= 256);
+    const int64_t tiles = std::max<int64_t>(1, (count + 32 * tt - 1) / (32 * tt) * ((a.b.D + 255) / 256));
+    const int64_t most = std::min(std::min<int64_t>(kMaxSplits, a.b.ksteps / 4),
+                                  std::min(main_groups(a.b.N, a.b.D, tt) / tiles, a.part_rows / std::max<int64_t>(count, 1)));
+    a.plan[4 * p] = (int32_t)count;
+    a.plan[4 * p + 1] = tt;
+    a.plan[4 * p + 2] = best_parts(count, a.b.D, a.b.ksteps / 4, tt, most);
   }
 }
 
@@ -452,9 +459,9 @@ __global__ __launch_bounds__(256) void xent_zero_kernel(const ManyArgs a) {
 // Row blockIdx.x of the pass: its H (zeros behind the last one that counts),
 // and no sums.
 __global__ __launch_bounds__(256) void xent_gather_kernel(const ManyArgs a) {
-  const int64_t i = blockIdx.x, count = a.counts[a.pass];
+  const int64_t i = blockIdx.x, count = a.plan[4 * a.pass];
   if (threadIdx.x == 0) {
-    a.top[i] = -__builtin_huge_valf();
+    a.ref[i] = -__builtin_huge_valf();
     a.sum[i] = 0.0;
     a.z_label[i] = __builtin_nanf("");  // stays where the label is outside the vocabulary
   }
@@ -468,15 +475,18 @@ __global__ __launch_bounds__(256) void xent_arrange_kernel(const BwdArgs b) {
   arrange_codes(b, (int64_t)blockIdx.x * 256 + threadIdx.x);
 }
 
-// 32 rows a workgroup, kMergeSlices threads each: the running exponent of the
-// piece's blocks and of those before, and the sum at that exponent.
+// 32 rows a workgroup, kMergeSlices threads each: the sum of the piece's blocks
+// and of those before, and the running exponent, which is moved only where a
+// block has one above it: to kHeadroom above the largest, so that few pieces
+// move it.
+constexpr float kHeadroom = 3.0f;
 __global__ __launch_bounds__(32 * kMergeSlices) void xent_merge_kernel(const ManyArgs a) {
   __shared__ float sTop[kMergeSlices][32];
   __shared__ double sSum[kMergeSlices][32];
   constexpr int kBatch = 8;
   const int c = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int64_t n = 32 * (int64_t)blockIdx.x + c;
-  if (32 * (int64_t)blockIdx.x >= a.counts[a.pass]) return;
+  if (32 * (int64_t)blockIdx.x >= a.plan[4 * a.pass]) return;
   const float infinity = __builtin_huge_valf();
   const u2* stat = reinterpret_cast<const u2*>(a.stat) + n;
   // sum s at exponent m moved to m + j (j whole and not below 0, or not finite
@@ -501,14 +511,61 @@ __global__ __launch_bounds__(32 * kMergeSlices) void xent_merge_kernel(const Man
   sSum[slice][c] = s;
   __syncthreads();
   if (slice == 0) {
-    const float old = a.top[n];
+    const float old = a.ref[n];
     float t = old;
     for (int k = 0; k < kMergeSlices; ++k) t = fmaxf(t, sTop[k][c]);
+    const bool raised = t > old;
+    if (raised) t += kHeadroom;
     double sum = moved(a.sum[n], t - old);
     for (int k = 0; k < kMergeSlices; ++k) sum += moved(sSum[k][c], t - sTop[k][c]);
     a.sum[n] = sum;
-    a.top[n] = t;
+    a.ref[n] = t;
     a.alpha[n] = t - old <= 1000.0f ? ldexpf(1.0f, -(int)(t - old)) : 0.0f;
+    const bool any = __any(raised);
+    if (c == 0) a.moved[blockIdx.x] = any;
+  }
+}
+
+// Operands times 2^t, t whole and below 0 (times 0 where it is not a number),
+// in two steps, as fp16's least power is 2^-24 and operands reach 2^15.
+__device__ __forceinline__ h8 times_power(h8 x, float t) {
+  t = fmaxf(t, -100.0f);
+  const float lo = fmaxf(t, -20.0f);
+  const _Float16 a = (_Float16)ldexpf(1.0f, (int)lo), b = (_Float16)ldexpf(1.0f, (int)(t - lo));
+  x = x * h8{a, a, a, a, a, a, a, a};
+  return x * h8{b, b, b, b, b, b, b, b};
+}
+
+// The operands of rows whose exponent this piece moved, brought there in place:
+// exactly, but for what ends below 2^-14.  Row tiles without such rows are left
+// alone, and of the others the rows.  (In the product, which reads every operand
+// once for 256 columns, the same takes 9% of all its time.)  Wave: every
+// gridDim.y kMoveWaves-th block of row tile blockIdx.x.
+constexpr int kMoveWaves = 4;
+__global__ __launch_bounds__(64 * kMoveWaves) void xent_move_kernel(const ManyArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t tile = blockIdx.x, n = 32 * tile + (lane & 31);
+  if (32 * tile >= a.plan[4 * a.pass] || !a.moved[tile]) return;
+  constexpr int kBatch = 4;
+  const float ref = a.ref[n];
+  h8* e = reinterpret_cast<h8*>(a.b.hf) + tile * a.steps * 64 + lane;
+  const int first = (int)blockIdx.y * kMoveWaves + (threadIdx.x >> 6), stride = kMoveWaves * gridDim.y;
+  for (int k0 = first; k0 < a.blocks; k0 += kBatch * stride) {
+    float t[kBatch];
+    h8 x[kBatch][2];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)  // past the last block: nothing
+      t[i] = k0 + i * stride < a.blocks ? a.stat[2 * ((int64_t)(k0 + i * stride) * a.b.n32 + n)] - ref : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (t[i] != 0.0f)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[i][h] = e[(2 * (int64_t)(k0 + i * stride) + h) * 64];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (t[i] != 0.0f)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) e[(2 * (int64_t)(k0 + i * stride) + h) * 64] = times_power(x[i][h], t[i]);
   }
 }
 
@@ -522,7 +579,7 @@ __global__ __launch_bounds__(kZThreads, 2) void xent_z_kernel(const ManyArgs a) 
   const BwdArgs& b = a.b;
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t count = a.counts[a.pass], ntiles = (count + 31) / 32, tile0 = 2 * (int64_t)blockIdx.x;
+  const int64_t count = a.plan[4 * a.pass], ntiles = (count + 31) / 32, tile0 = 2 * (int64_t)blockIdx.x;
   if (tile0 >= ntiles) return;
   const int parts = gridDim.y, r = b.r_c + b.r_r;
   // rank tile of slot t: of part c (0) or w (1), its place in the part
@@ -532,15 +589,9 @@ __global__ __launch_bounds__(kZThreads, 2) void xent_z_kernel(const ManyArgs a) 
   // row tiles start at different steps, so that they are not all at the same memory channels
   const int turn = k1 > k0 ? (int)(blockIdx.x * 5 * kWaves % (unsigned)(k1 - k0)) : 0;
   const h8* e[2];
-  const float* fm[2];
-  float ft[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t tile = std::min(tile0 + i, ntiles - 1);
-    e[i] = reinterpret_cast<const h8*>(b.hf) + tile * a.steps * 64 + lane;
-    fm[i] = a.stat + 2 * (32 * tile + c32);
-    ft[i] = a.top[32 * tile + c32];
-  }
+  for (int i = 0; i < 2; ++i)
+    e[i] = reinterpret_cast<const h8*>(b.hf) + std::min(tile0 + i, ntiles - 1) * a.steps * 64 + lane;
   const u2* codes[kZTiles];
 #pragma unroll
   for (int t = 0; t < kZTiles; ++t)  // past a part's last tile: another, not stored
@@ -551,17 +602,13 @@ __global__ __launch_bounds__(kZThreads, 2) void xent_z_kernel(const ManyArgs a) 
   for (int q = 0; q < 2; ++q) scale[q] = reinterpret_cast<const h8*>(a.scale_a) + 2 * (q * a.asteps + a.step0) + half;
   f16x acc[2][kZTiles] = {};
   h8 x[kDepth][2], s[kDepth][2];
-  float f[kDepth][2];
   u2 y[kDepth][kZTiles];
   auto load = [&](int k, auto slot_) __attribute__((always_inline)) {
     constexpr int slot = decltype(slot_)::value;
     k = std::min(k, k1 - 1) + turn;  // past the end: a step that is not used
     k -= k >= k1 ? k1 - k0 : 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      f[slot][i] = fm[i][2 * (int64_t)(k / 2) * b.n32];
-      x[slot][i] = e[i][(int64_t)k * 64];
-    }
+    for (int i = 0; i < 2; ++i) x[slot][i] = e[i][(int64_t)k * 64];
 #pragma unroll
     for (int q = 0; q < 2; ++q) s[slot][q] = scale[q][2 * (int64_t)k];
 #pragma unroll
@@ -572,9 +619,7 @@ __global__ __launch_bounds__(kZThreads, 2) void xent_z_kernel(const ManyArgs a) 
     constexpr int slot = decltype(slot_)::value;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const _Float16 p = fp16_power(f[slot][i] - ft[i] + (float)kFactorTop);
-      const h8 v = x[slot][i] * h8{p, p, p, p, p, p, p, p};
-      const h8 part[2] = {v * s[slot][0], v * s[slot][1]};
+      const h8 part[2] = {x[slot][i] * s[slot][0], x[slot][i] * s[slot][1]};
 #pragma unroll
       for (int t = 0; t < kZTiles; ++t) acc[i][t] = mfma32(part[part_of(t)], unpack_u8x8(y[slot][t]), acc[i][t]);
     }
@@ -646,7 +691,7 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(const ManyArgs a) {
   __shared__ RowOut sOut;
   const BwdArgs& b = a.b;
   const int64_t i = blockIdx.x;
-  if (i >= a.counts[a.pass]) return;
+  if (i >= a.plan[4 * a.pass]) return;
   const int64_t at = a.pass * kChunkRows + i, label = a.label[at], l = label >= 0 && label < b.V ? label : 0;
   if (threadIdx.x == 0) {
     const int64_t n = a.map[at];
@@ -658,7 +703,7 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(const ManyArgs a) {
       logp = q = __builtin_nan("");
       out.mean = (float)q;
     } else if (s != 0.0) {  // (a vocabulary of one entry: p = 1)
-      const double d = log(s) + ((double)a.top[i] - (double)zl) * 0.6931471805599453;
+      const double d = log(s) + ((double)a.ref[i] - kExpTop - (double)zl) * 0.6931471805599453;
       logp = d == d ? -(fmax(d, 0.0) + log1p(exp(-fabs(d)))) : d;
       q = 1.0 / (1.0 + exp(-d));
       out.mean = (float)(w * (double)a.tau * q / s);
@@ -691,12 +736,12 @@ __global__ __launch_bounds__(kFinishThreads, 2) void xent_finish_kernel(const Ma
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = b.r_c + b.r_r;
-  const int64_t n0 = 32 * (int64_t)blockIdx.x, kt = (int64_t)blockIdx.y * kWaves + wave, count = a.counts[a.pass];
+  const int64_t n0 = 32 * (int64_t)blockIdx.x, kt = (int64_t)blockIdx.y * kWaves + wave, count = a.plan[4 * a.pass];
   if (n0 >= count || kt >= b.nkt) return;
   const int64_t d = kKTile * kt + 4 * c32, group = d / b.g;
   // row of element v of a result tile; past the last row that one
   auto row = [&](int v) { return std::min<int64_t>(n0 + 8 * (v >> 2) + 4 * half + (v & 3), count - 1); };
-  const int splits = a.splits[a.pass];
+  const int splits = a.plan[4 * a.pass + 2];
   f16x acc[4] = {};
   for (int p = 0; p < splits; ++p) {
     f4 y[16];
@@ -904,9 +949,10 @@ int launch_few_rows(const archead_tensor* H, const archead_packed_head* head, co
 
 struct ManyLayout {
   int64_t rows, n32, vtiles, piece;  // rows of a pass; 256-row tiles of the vocabulary, of a piece
-  int splits, zparts, passes;
-  uint64_t terms, head_max, scale, scale_a, map, label, counts, splits_at, fwd, fwd_bytes, Hc, e, stat,
-      alpha, top, sum, z_label, row, af, zpart, z, part, total;
+  int zparts, passes;
+  int64_t part_rows;
+  uint64_t terms, head_max, scale, scale_a, map, label, plan, fwd, fwd_bytes, Hc, e, stat,
+      alpha, ref, moved, sum, z_label, row, af, zpart, z, part, total;
 };
 
 // Workgroups of xent_z_kernel side by side for the ranks.
@@ -927,7 +973,11 @@ ManyLayout many_layout(const archead_dims* d, int64_t N) {
   const int64_t pieces = (L.vtiles + most - 1) / most;
   L.piece = (L.vtiles + pieces - 1) / pieces;
   if (pieces > 1) L.piece = std::min((int64_t)round_up((uint64_t)L.piece, 16), std::max<int64_t>(most / 16 * 16, 1));
-  L.splits = main_splits(L.rows, d->D, 0, 4 * L.piece);
+  // partial sums: what all the rows take in as many parts as are best for them, or
+  // 64 MiB for fewer rows in more parts
+  const int64_t stages = 4 * L.piece;
+  L.part_rows = std::max(L.rows * best_parts(L.rows, d->D, stages, main_tiles(L.rows), std::min<int64_t>(kMaxSplits, stages)),
+                         std::min(L.rows * std::min<int64_t>(kMaxSplits, stages), (int64_t)(16 << 20) / d->D));
   const int64_t r = d->r_c + d->r_r, tiles = (d->r_c + 31) / 32 + (d->r_r + 31) / 32;
   const int64_t groups = (L.n32 + 63) / 64 * std::max(1, z_groups(d));
   L.zparts = (int)std::max<int64_t>(1, std::min<int64_t>({(256 + groups - 1) / groups, L.piece, 64}));
@@ -943,22 +993,22 @@ ManyLayout many_layout(const archead_dims* d, int64_t N) {
   L.scale_a = take(2 * 256 * (uint64_t)L.vtiles * 2);
   L.map = take((uint64_t)N * 4);
   L.label = take((uint64_t)std::max(N, L.passes * L.rows) * 4);  // whole passes are read
-  L.counts = take((uint64_t)L.passes * 4);
-  L.splits_at = take((uint64_t)L.passes * 4);
+  L.plan = take((uint64_t)L.passes * 16);
   L.fwd_bytes = workspace_layout(d, L.rows, false, 0, false).total;
   L.fwd = take(L.fwd_bytes);
   L.Hc = take(n32 * (uint64_t)d->D * 2);
   L.e = take(n32 / 32 * (uint64_t)piece_steps(L.piece) * 1024);
   L.stat = take(blocks * n32 * 8);
   L.alpha = take(n32 * 4);
-  L.top = take(n32 * 4);
+  L.ref = take(n32 * 4);
+  L.moved = take(n32 / 8);
   L.sum = take(n32 * 8);
   L.z_label = take(n32 * 4);
   L.row = take(n32 * sizeof(RowOut));
   L.af = take((uint64_t)tiles * (uint64_t)L.vtiles * 16 * 512);
   L.zpart = take((uint64_t)L.zparts * n32 * (uint64_t)r * 4);
   L.z = take(n32 * (uint64_t)r * 4);
-  L.part = take((uint64_t)L.splits * (uint64_t)L.rows * (uint64_t)d->D * 4);
+  L.part = take((uint64_t)L.part_rows * (uint64_t)d->D * 4);
   return L;
 }
 
@@ -968,8 +1018,7 @@ uint64_t xent_bytes(const archead_dims* d, int64_t N) {
 
 template <int TT>
 void launch_xent_main(const BwdArgs& b, const MainExp& ex, hipStream_t s) {
-  const int64_t tb = (b.n32 / 32 + TT - 1) / TT, cb = (b.D + 255) / 256;
-  const dim3 grid((unsigned)(tb * cb * b.splits)), block(kMainThreads);
+  const dim3 grid((unsigned)main_groups(b.N, b.D, TT)), block(kMainThreads);
   if (b.g == 32)
     hipLaunchKernelGGL((xent_main_kernel<TT, 4>), grid, block, 0, s, b, ex);
   else if (b.g == 64)
@@ -994,7 +1043,6 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
   b.zpart = reinterpret_cast<float*>(ws + L.zpart);
   b.z = reinterpret_cast<float*>(ws + L.z);
   b.part = reinterpret_cast<float*>(ws + L.part);
-  b.splits = L.splits;
   b.zparts = L.zparts;
   a.rows = N;
   a.H = static_cast<const uint16_t*>(H->data);
@@ -1010,15 +1058,16 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
   a.head_max = reinterpret_cast<float*>(ws + L.head_max);
   a.scale = reinterpret_cast<float*>(ws + L.scale);
   a.scale_a = reinterpret_cast<_Float16*>(ws + L.scale_a);
-  a.splits = reinterpret_cast<int32_t*>(ws + L.splits_at);
   a.map = reinterpret_cast<int32_t*>(ws + L.map);
   a.label = reinterpret_cast<int32_t*>(ws + L.label);
-  a.counts = reinterpret_cast<int32_t*>(ws + L.counts);
+  a.plan = reinterpret_cast<int32_t*>(ws + L.plan);
   a.terms = reinterpret_cast<double*>(ws + L.terms);
   a.Hc = reinterpret_cast<uint16_t*>(ws + L.Hc);
   a.stat = reinterpret_cast<float*>(ws + L.stat);
   a.alpha = reinterpret_cast<float*>(ws + L.alpha);
-  a.top = reinterpret_cast<float*>(ws + L.top);
+  a.ref = reinterpret_cast<float*>(ws + L.ref);
+  a.moved = reinterpret_cast<int32_t*>(ws + L.moved);
+  a.part_rows = L.part_rows;
   a.sum = reinterpret_cast<double*>(ws + L.sum);
   a.z_label = reinterpret_cast<float*>(ws + L.z_label);
   a.steps = (int)piece_steps(L.piece);
@@ -1034,9 +1083,13 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
   const int tiles = b.nct + b.nwt;
   (void)hipGetLastError();  // start from a clean error state
   hipLaunchKernelGGL(xent_head_kernel, dim3(kHeadParts), dim3(kHeadThreads), 0, s, a);
-  const int tt = main_tiles(L.rows);
+  // the launches that some number of rows may need: for each of 2, 4, 6 and 8 row tiles
+  bool may[5] = {};
+  if (L.rows > kExpFewRows)
+    may[4] = true;
+  else
+    for (int64_t t = 0; t <= L.n32 / 32; ++t) may[exp_tiles(t, d->D >= 256) / 2] = true;
   a.passes = L.passes;
-  a.tile_rows = 32 * tt;
   b.ksteps = (int)(16 * L.piece);
   hipLaunchKernelGGL(xent_order_kernel, dim3((unsigned)(1 + (16 * a.asteps + kOrderThreads - 1) / kOrderThreads)), dim3(kOrderThreads), 0, s, a);
   if (a.dH && tiles) {
@@ -1052,7 +1105,8 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
     for (int64_t vt = 0; vt < L.vtiles; vt += L.piece) {
       const int64_t vn = std::min(L.piece, L.vtiles - vt);
       T32Exp ex{};
-      ex.n_rows = a.counts + pass;
+      ex.plan = a.plan + 4 * pass;
+      ex.ref = a.ref;
       ex.labels = a.label + pass * kChunkRows;
       ex.c = 1.4426950408889634 * (double)in->inv_temperature;
       ex.vt0 = (int)vt;
@@ -1061,23 +1115,26 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
       ex.steps = a.steps;
       ex.stat = a.stat;
       ex.z_label = a.z_label;
-      if (launch_tile_exp(f, ex, s) != hipSuccess) return ARCHEAD_E_HIP;
+      for (int t = 1; t <= 4; ++t)
+        if (may[t] && launch_tile_exp(f, ex, 2 * t, s) != hipSuccess) return ARCHEAD_E_HIP;
       a.blocks = (int)(8 * vn);
       a.first = vt == 0;
       a.step0 = (int)(16 * vt);
       b.ksteps = (int)(16 * vn);
       hipLaunchKernelGGL(xent_merge_kernel, dim3((unsigned)(L.n32 / 32)), dim3(32 * kMergeSlices), 0, s, a);
       if (!a.dH) continue;
+      const int64_t row_tiles = L.n32 / 32;
+      // (2048 workgroups where there are row tiles enough, and a block for every wave)
+      hipLaunchKernelGGL(xent_move_kernel, dim3((unsigned)row_tiles, (unsigned)std::max<int64_t>(1, std::min((2048 + row_tiles - 1) / row_tiles, 2 * vn))),
+                         dim3(64 * kMoveWaves), 0, s, a);
       if (tiles)
         hipLaunchKernelGGL(xent_z_kernel, dim3((unsigned)((L.n32 + 63) / 64), (unsigned)L.zparts, (unsigned)z_groups(d)),
                            dim3(kZThreads), 0, s, a);
-      const MainExp me{a.counts + pass, a.splits + pass, a.stat, a.top, a.alpha, a.scale, a.steps, a.first, (int)(4 * vt)};
-      if (tt == 2)
-        launch_xent_main<2>(b, me, s);
-      else if (tt == 4)
-        launch_xent_main<4>(b, me, s);
-      else
-        launch_xent_main<8>(b, me, s);
+      const MainExp me{a.plan + 4 * pass, a.alpha, a.scale, a.steps, a.first, (int)(4 * vt)};
+      if (may[1]) launch_xent_main<2>(b, me, s);
+      if (may[2]) launch_xent_main<4>(b, me, s);
+      if (may[3]) launch_xent_main<6>(b, me, s);
+      if (may[4]) launch_xent_main<8>(b, me, s);
     }
     hipLaunchKernelGGL(xent_rows_kernel, dim3((unsigned)L.rows), dim3(256), 0, s, a);
     if (a.dH)

@@ -22,10 +22,11 @@ hipError_t launch_exp(const FwdArgs& a, const T32Exp& ex, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_tile_exp(const FwdArgs& a, const T32Exp& ex, hipStream_t s) {
-  switch (t32_tt(a)) {
+hipError_t launch_tile_exp(const FwdArgs& a, const T32Exp& ex, int tt, hipStream_t s) {
+  switch (tt) {
     case 2: return launch_exp<2>(a, ex, s);
     case 4: return launch_exp<4>(a, ex, s);
+    case 6: return launch_exp<6>(a, ex, s);
     default: return launch_exp<8>(a, ex, s);
   }
 }

@@ -8,8 +8,10 @@ at most, |W| the residual's and the factors' magnitudes.  Exponentials: their
 argument by 2^-24 of itself (up to 40 here), 2^x by the hardware 2^-22, sums in
 short fp32 runs: 2^-18 of a probability in all, and tau eps twice (its own and
 the sum's).  In the product they are rounded to fp16, 2^-11, and so is the
-residual's operand of many rows: 2^-10; below 2^-28 of the row's largest the
-half step is 2^-38 of that largest.  Sums over the vocabulary are fp32 sums of
+residual's operand of many rows: 2^-10.  The row's largest operand is at least
+2^10 (at most 2^14, less 3 powers of two of room for later pieces, and it is
+above half of that), and below 2^-14 the half step is 2^-25, twice where an
+operand is brought to another exponent: 2^-34 of the largest.  Sums over the vocabulary are fp32 sums of
 V / 16 + 128 terms, Z B as in the backward (r 2^-23 + 3 2^-18).  With
     T = sum_{v != l} p_v |W|_v + (1 - p_l) |W|_l
 dH is off by the sum of these times |w| tau T, and by its rounding, 2^-8; log p
@@ -80,7 +82,7 @@ def _check(got, H, labels, w, h, tau, what):
     S = np.maximum(e.sum(1, keepdims=True), 1e-300)
     T = q[:, None] * (e / S @ Wabs + Wabs[np.where(on, labels, 0)])
     rel = 2.0 ** -10 + 4 * tau * eps[:, None] + 2.0 ** -17 + (V / 16 + 128) * 2.0 ** -24 + r * 2.0 ** -23 + 3 * 2.0 ** -18
-    tol = np.abs(w64)[:, None] * tau * (rel * T + 2.0 ** -38 * q[:, None] / S * Wabs.sum(0))
+    tol = np.abs(w64)[:, None] * tau * (rel * T + 2.0 ** -34 * q[:, None] / S * Wabs.sum(0))
     tol = tol + 2.0 ** -8 * (np.abs(want["dH"]) + tol) + 2.0 ** -134
     err = np.abs(dH - want["dH"])
     assert (err <= tol)[on].all(), (what, (err / tol)[on].max())
