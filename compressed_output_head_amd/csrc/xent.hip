@@ -12,7 +12,7 @@
 //
 // Few rows (up to 32 at a time): the decode kernels' logits in fp32, then
 //   xent_pieces_kernel      maxima and sums of pieces of a row's logits
-//   xent_operand_kernel     e s_R, e s_Ac, e s_Aw as fp16 operands; log p
+//   xent_operand_kernel     e s_R, e s_Ac, e s_Aw as fp16 operands; log p, loss
 //   bwd_few_kernel, bwd_few16_kernel (backward.hip)
 //   xent_finish_few_kernel  the splits' sums, Z B and the label's row to dH
 // More rows, those that count gathered, up to 4096 at a time; for every piece
@@ -46,9 +46,11 @@ struct Piece {
   float m, s, top[3];  // maximum of y; sum of exponentials; largest e s_R, e s_Ac, e s_Aw
 };
 
-// What the last kernel needs of a row.
+// What the last kernel needs of a row: dH is `all` times the others' sum over S
+// less the label's row.  `all` comes last, since q and with it what it
+// multiplies may be below 2^-126.
 struct RowOut {
-  float mean, label;  // factors of the others' sum and of the label's row: w tau q / S, w tau q
+  float mean, all;  // 1 / S, w tau q
 };
 
 struct XentArgs {
@@ -63,7 +65,7 @@ struct XentArgs {
   int64_t dh_stride;
   Piece* piece;           // [N][pieces]
   RowOut* row;            // [N]
-  double* terms;          // [N] -w log p
+  float* loss;            // or null
   int pieces;
   int64_t width;          // columns of a piece
 };
@@ -164,12 +166,14 @@ __global__ __launch_bounds__(kPieceThreads) void xent_pieces_kernel(const XentAr
   }
 }
 
+constexpr int kOperandThreads = 256;
 // Run blockIdx.x of 128 columns of all rows as operands, thread t octet t % 16
 // of rows t / 16 and t / 16 + 16; the rows' pieces are merged by every
-// workgroup, and the first one writes what is known of the rows then.
-constexpr int kOperandThreads = 256;
+// workgroup, and the first one writes what is known of the rows then, and the
+// loss.
 __global__ __launch_bounds__(kOperandThreads) void xent_operand_kernel(const XentArgs a) {
   __shared__ float sM[32], sP[3][32];
+  __shared__ double sTerm[32];
   const int tid = threadIdx.x, N = (int)a.b.N;
   const float infinity = __builtin_huge_valf();
   {  // eight lanes a row
@@ -211,7 +215,7 @@ __global__ __launch_bounds__(kOperandThreads) void xent_operand_kernel(const Xen
           const double w = a.weight ? (double)a.weight[n] : 1.0;
           const float yl = label >= 0 && label < a.b.V ? a.Y[n * a.y_stride + label] : infinity;
           if (!(fabsf(yl) < infinity)) {
-            logp = out.mean = out.label = __builtin_nanf("");
+            logp = out.all = __builtin_nanf("");
           } else {
             const double z = (double)a.tau * ((double)m - (double)yl);
             double q = 0.0;
@@ -219,13 +223,13 @@ __global__ __launch_bounds__(kOperandThreads) void xent_operand_kernel(const Xen
               const double d = z + log(s);
               logp = d == d ? -(fmax(d, 0.0) + log1p(exp(-fabs(d)))) : d;
               q = 1.0 / (1.0 + exp(-d));
-              out.mean = (float)(w * (double)a.tau * q / s);
+              out.mean = (float)(1.0 / s);
             }
-            out.label = (float)(w * (double)a.tau * q);
+            out.all = (float)(w * (double)a.tau * q);
           }
-          a.terms[n] = -w * logp;
+          sTerm[n] = -w * logp;
         } else {
-          a.terms[n] = 0.0;
+          sTerm[n] = 0.0;
         }
         a.row[n] = out;
         if (a.logp) a.logp[n] = (float)logp;
@@ -235,8 +239,13 @@ __global__ __launch_bounds__(kOperandThreads) void xent_operand_kernel(const Xen
       }
     }
   }
-  if (!a.dH) return;
   __syncthreads();
+  if (blockIdx.x == 0 && tid == 0 && a.loss) {
+    double loss = 0.0;
+    for (int n = 0; n < N; ++n) loss += sTerm[n];
+    *a.loss = (float)loss;
+  }
+  if (!a.dH) return;
   const int oct = tid & 15, run = blockIdx.x;
   const int64_t v = 128 * (int64_t)run + 8 * oct, V16 = 16 * a.b.nb;
 #pragma unroll
@@ -288,7 +297,7 @@ __global__ __launch_bounds__(kFinishThreads) void xent_finish_few_kernel(const X
     for (int p = 0; p < b.splits; ++p) z += b.zpart[((int64_t)p * b.n32 + n) * r + j];
     const bool in_c = j < b.r_c;
     const float al = (float)b.a_codes[l * r + j] * f16_to_f32(b.a_scales[l * b.nA + (in_c ? 0 : b.nA - 1)]);
-    sZ[j] = out.mean * (z * b.rscale[n * 3 + (in_c ? 1 : 2)]) - out.label * al;
+    sZ[j] = out.mean * (z * b.rscale[n * 3 + (in_c ? 1 : 2)]) - al;
   }
   f4 acc = {};
 #pragma unroll 4
@@ -299,7 +308,7 @@ __global__ __launch_bounds__(kFinishThreads) void xent_finish_few_kernel(const X
     const int k = (int)(dd % kKTile);
     const uint8_t* tile = b.r_codes + (kt * b.nb + l / 16) * kTileBytes;
     const uint32_t w = *reinterpret_cast<const uint16_t*>(tile + 16 * (l % 16 + 16 * (k % 32 / 8)) + 4 * (k / 32) + k % 8 / 2);
-    const float s = out.label * ((float)b.r_gcodes[l * b.ng + group] * f16_to_f32(b.r_rowscale[l]));
+    const float s = (float)b.r_gcodes[l * b.ng + group] * f16_to_f32(b.r_rowscale[l]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] = fmaf(-s, (float)((int32_t)(w << (28 - 4 * e)) >> 28), acc[e]);
   }
@@ -315,7 +324,7 @@ __global__ __launch_bounds__(kFinishThreads) void xent_finish_few_kernel(const X
   __syncthreads();
   if (wave == 0 && d < b.D) {
     for (int w = 1; w < kWaves; ++w) acc += red[w][lane];
-    if (!on) acc = f4{};
+    acc = on ? acc * out.all : f4{};
     typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(2)));
     *reinterpret_cast<u2_any*>(a.dH + n * a.dh_stride + d) = pack_bf16x4(acc[0], acc[1], acc[2], acc[3]);
   }
@@ -701,14 +710,13 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(const ManyArgs a) {
     RowOut out{0.0f, 0.0f};
     if (!(fabsf(zl) < __builtin_huge_valf())) {
       logp = q = __builtin_nan("");
-      out.mean = (float)q;
     } else if (s != 0.0) {  // (a vocabulary of one entry: p = 1)
       const double d = log(s) + ((double)a.ref[i] - kExpTop - (double)zl) * 0.6931471805599453;
       logp = d == d ? -(fmax(d, 0.0) + log1p(exp(-fabs(d)))) : d;
       q = 1.0 / (1.0 + exp(-d));
-      out.mean = (float)(w * (double)a.tau * q / s);
+      out.mean = (float)(1.0 / s);
     }
-    out.label = (float)(w * (double)a.tau * q);
+    out.all = (float)(w * (double)a.tau * q);
     a.terms[n] = -w * logp;
     if (a.logp) a.logp[n] = (float)logp;
     a.row[i] = sOut = out;
@@ -722,7 +730,7 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(const ManyArgs a) {
     for (int p = 0; p < b.zparts; ++p) z += b.zpart[((int64_t)p * b.n32 + i) * r + j];
     const bool in_c = j < b.r_c;
     const float al = (float)b.a_codes[l * r + j] * f16_to_f32(b.a_scales[l * b.nA + (in_c ? 0 : b.nA - 1)]);
-    b.z[i * r + j] = sOut.mean * (z * a.scale[in_c ? 2 : 3]) - sOut.label * al;
+    b.z[i * r + j] = sOut.mean * (z * a.scale[in_c ? 2 : 3]) - al;
   }
 }
 
@@ -755,12 +763,11 @@ __global__ __launch_bounds__(kFinishThreads, 2) void xent_finish_kernel(const Ma
   const float undo = a.scale[1];
 #pragma unroll
   for (int v = 0; v < 16; ++v) {
-    const RowOut out = a.row[row(v)];
     const int64_t label = a.label[a.pass * kChunkRows + row(v)], l = label >= 0 && label < b.V ? label : 0;
     const uint8_t* tile = b.r_codes + (kt * b.nb + l / 16) * kTileBytes;
     const uint32_t w = *reinterpret_cast<const uint16_t*>(tile + 16 * (l % 16 + 16 * (c32 % 8 / 2)) + 4 * (c32 / 8) + 2 * (c32 % 2));
-    const float s = out.label * ((float)b.r_gcodes[l * b.ng + group] * f16_to_f32(b.r_rowscale[l]));
-    const float f = undo * out.mean;
+    const float s = (float)b.r_gcodes[l * b.ng + group] * f16_to_f32(b.r_rowscale[l]);
+    const float f = undo * a.row[row(v)].mean;
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[c][v] = fmaf(-s, (float)((int32_t)(w << (28 - 4 * c)) >> 28), acc[c][v] * f);
   }
@@ -794,9 +801,10 @@ __global__ __launch_bounds__(kFinishThreads, 2) void xent_finish_kernel(const Ma
   for (int v = 0; v < 16; ++v) {
     const int64_t i = n0 + 8 * (v >> 2) + 4 * half + (v & 3);
     if (i >= count) continue;
+    const float f = a.row[i].all;
     typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(2)));
     *reinterpret_cast<u2_any*>(a.dH + (int64_t)a.map[a.pass * kChunkRows + i] * a.dh_stride + d) =
-        pack_bf16x4(acc[0][v], acc[1][v], acc[2][v], acc[3][v]);
+        pack_bf16x4(acc[0][v] * f, acc[1][v] * f, acc[2][v] * f, acc[3][v] * f);
   }
 }
 
@@ -823,7 +831,7 @@ int64_t y_stride_of(const archead_dims* d) { return (int64_t)round_up((uint64_t)
 struct XentLayout {
   int64_t n32, ksteps, width;
   int pieces, splits;
-  uint64_t terms, y, fwd, fwd_bytes, piece, row, rscale, hf, gt, zpart, part, total;
+  uint64_t y, fwd, fwd_bytes, piece, row, rscale, hf, gt, zpart, part, total;
 };
 
 XentLayout xent_layout(const archead_dims* d, int64_t rows) {
@@ -840,7 +848,6 @@ XentLayout xent_layout(const archead_dims* d, int64_t rows) {
     L.total += round_up(bytes, ARCHEAD_ALIGNMENT);
     return at;
   };
-  L.terms = take((uint64_t)rows * 8);
   L.y = take((uint64_t)rows * (uint64_t)y_stride_of(d) * 4);
   L.fwd_bytes = workspace_layout(d, rows).total;
   L.fwd = take(L.fwd_bytes);
@@ -930,7 +937,7 @@ int launch_few_rows(const archead_tensor* H, const archead_packed_head* head, co
   }
   a.piece = reinterpret_cast<Piece*>(ws + L.piece);
   a.row = reinterpret_cast<RowOut*>(ws + L.row);
-  a.terms = reinterpret_cast<double*>(ws + L.terms);
+  a.loss = out->loss;
   a.pieces = L.pieces;
   a.width = L.width;
   const int64_t arrange = a.dH ? b.nb * b.ng / std::max(1, kKTile / b.g) : 0;
@@ -1206,7 +1213,7 @@ int archead_cross_entropy(const archead_tensor* H, const archead_packed_head* he
   (void)hipGetLastError();  // start from a clean error state
   if (N > 0)
     if (int rc = N <= kFewTokens ? launch_few_rows(H, head, in, out, s) : launch_many_rows(H, head, in, out, s)) return rc;
-  if (out->loss) {
+  if (out->loss && (N == 0 || N > kFewTokens)) {
     hipLaunchKernelGGL(xent_total_kernel, dim3(1), dim3(kTotalThreads), 0, s, static_cast<const double*>(head->workspace), N, out->loss);
     if (hipGetLastError() != hipSuccess) return ARCHEAD_E_HIP;
   }

@@ -277,3 +277,68 @@ def test_a_training_step_from_the_stream_to_its_gradient():
     assert abs(loss["loss"].item() - ol["loss"]) <= 1e-5 * abs(ol["loss"])
     for k in ("dx", "dweight"):  # two roundings to bf16 and the product's
         assert np.linalg.norm(n64(back[k]) - ob[k]) <= 2.0 ** -7 * np.linalg.norm(ob[k]), k
+
+
+# V, D, r_c, r_r, g, N, share of the rows that count: every number of row tiles
+# that a workgroup takes, chosen by the rows that count or by the call's; passes
+# of 4096 rows, the last of them without a row that counts; ranks behind the
+# first 64 of either kind, and factors of one kind alone
+SHARES = [
+    (700, 256, 8, 8, 64, 100, 0.1), (700, 256, 8, 8, 64, 300, 0.3), (700, 256, 8, 8, 64, 300, 0.9),
+    (650, 384, 16, 0, 128, 500, 0.7), (650, 128, 0, 16, 64, 900, 0.95), (650, 512, 8, 8, 256, 1024, 0.02),
+    (333, 128, 8, 8, 128, 1100, 0.5), (1500, 256, 160, 0, 64, 70, 0.8), (1500, 256, 0, 104, 64, 70, 1.0),
+    (1500, 512, 72, 136, 32, 90, 1.0), (200, 128, 8, 8, 64, 4097, 1.0), (200, 128, 8, 8, 64, 8300, 0.4),
+]
+
+
+@pytest.mark.parametrize("V,D,r_c,r_r,g,N,share", SHARES)
+def test_shares_of_the_rows(V, D, r_c, r_r, g, N, share):
+    log(f"xent V={V} D={D} r_c={r_c} r_r={r_r} g={g} N={N} share={share}")
+    torch, ah = torch_mod(), ah_mod()
+    h, head = _head(V + N, V, D, r_c, r_r, g)
+    rng = np.random.default_rng(N)
+    labels = rng.integers(0, V, N)
+    H = _hidden(N, N, D, oracle.w_hat(h), labels)
+    on = rng.random(N) < share
+    w = torch.from_numpy((rng.uniform(0.5, 1.5, N) * on).astype(np.float32)).cuda()
+    labels = np.where(on, labels, -100)
+    H[torch.from_numpy(~on).cuda()] = float("nan")
+    need = ah.archead_cross_entropy_workspace_bytes(V, D, r_c, r_r, g, N)
+    ws = torch.full((need + 512,), 255, dtype=torch.uint8, device="cuda")
+    got = ah.archead_cross_entropy(H, torch.from_numpy(labels).int().cuda(), head, weight=w, workspace=ws[:need])
+    assert (ws[need:] == 255).all()
+    H[torch.from_numpy(~on).cuda()] = 0.0
+    _check(got, H, labels, w, h, 1.0, f"V={V} N={N}")
+
+
+@pytest.mark.parametrize("r_c,r_r", [(16, 8), (0, 0)])
+def test_rows_whose_maximum_rises_along_the_vocabulary(r_c, r_r):
+    """A vocabulary in several pieces, and rows whose logits rise from one to
+    the next, also by more than an exponent of fp32 holds."""
+    torch, ah = torch_mod(), ah_mod()
+    V, D, N, g = 120000, 128, 600, 64
+    h, head = _head(21, V, D, r_c, r_r, g)
+    W = oracle.w_hat(h)
+    rng = np.random.default_rng(1)
+    labels = rng.integers(0, V, N)
+    H = rng.normal(0, 1, (N, D))
+    late = rng.integers(V // 2, V, N)
+    rise = rng.choice([0.0, 5.0, 20.0, 60.0, 200.0], N)
+    H += (rise / (W[late] ** 2).sum(1))[:, None] * W[late]
+    labels = np.where(rng.random(N) < 0.3, late, labels)
+    H = torch.from_numpy(H.astype(np.float32)).cuda().bfloat16()
+    got = ah.archead_cross_entropy(H, torch.from_numpy(labels).int().cuda(), head)
+    _check(got, H, labels, None, h, 1.0, "rising")
+
+
+@pytest.mark.parametrize("N", ROWS)
+def test_flat_and_huge_logits(N):
+    torch, ah = torch_mod(), ah_mod()
+    V, D = 1501, 256
+    for spread, H in ((2.0, torch.zeros((N, D), device="cuda").bfloat16()),
+                      (2000.0, torch.randn((N, D), device="cuda").bfloat16())):
+        h, head = _head(31, V, D, 8, 8, 64, spread=spread)
+        labels = np.random.default_rng(N).integers(0, V, N)
+        labels[-1] = V - 1
+        got = ah.archead_cross_entropy(H, torch.from_numpy(labels).int().cuda(), head)
+        _check(got, H, labels, None, h, 1.0, f"spread {spread} N={N}")
