@@ -137,23 +137,20 @@ class ArcheadCrossEntropyOutputs(ctypes.Structure):
     _fields_ = [("loss", ctypes.c_void_p), ("logp", ctypes.c_void_p), ("dH", ctypes.POINTER(ArcheadTensor))]
 
 
-class ArcheadRmsnormInputs(ctypes.Structure):
-    _fields_ = [("x", ctypes.POINTER(ArcheadTensor)), ("residual", ctypes.POINTER(ArcheadTensor)),
-                ("weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
+class ArcheadRmsnormInputs(ctypes.Structure):  # x, residual: addresses of ArcheadTensor, as in the next three
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "residual", "weight")] + [("eps", ctypes.c_float)]
 
 
 class ArcheadRmsnormOutputs(ctypes.Structure):
-    _fields_ = [("sum", ctypes.POINTER(ArcheadTensor)), ("h", ctypes.POINTER(ArcheadTensor)),
-                ("codes", ctypes.POINTER(ArcheadTensor)), ("scale", ctypes.c_void_p), ("inv_rms", ctypes.c_void_p)]
+    _fields_ = [(n, ctypes.c_void_p) for n in ("sum", "h", "codes", "scale", "inv_rms")]
 
 
 class ArcheadRmsnormGradInputs(ctypes.Structure):
-    _fields_ = [("dh", ctypes.POINTER(ArcheadTensor)), ("sum", ctypes.POINTER(ArcheadTensor)),
-                ("inv_rms", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("dsum", ctypes.POINTER(ArcheadTensor))]
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dh", "sum", "inv_rms", "weight", "dsum")]
 
 
 class ArcheadRmsnormGradOutputs(ctypes.Structure):
-    _fields_ = [("dx", ctypes.POINTER(ArcheadTensor)), ("dweight", ctypes.c_void_p)]
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "dweight")]
 
 
 def _load():
@@ -387,14 +384,18 @@ class PackedHead:
                                  ws.numel() if ws is not None else 0)
 
 
-def _tensor(t) -> ArcheadTensor:
+@functools.lru_cache(maxsize=None)
+def _code(dtype) -> int:
     torch = _torch()
-    if t.dim() != 2 or t.stride(1) != 1:
+    return {torch.bfloat16: ARCHEAD_BF16, torch.float32: ARCHEAD_F32, torch.int8: ARCHEAD_I8}.get(dtype, 0)
+
+
+def _tensor(t) -> ArcheadTensor:
+    stride = t.stride()
+    if len(stride) != 2 or stride[1] != 1:
         raise ValueError("expected a 2-D tensor with unit column stride")
-    dtype, (rows, cols) = t.dtype, t.shape
-    code = ARCHEAD_BF16 if dtype is torch.bfloat16 else ARCHEAD_F32 if dtype is torch.float32 else \
-        ARCHEAD_I8 if dtype is torch.int8 else 0
-    return ArcheadTensor(t.data_ptr(), rows, cols, t.stride(0), code)
+    rows, cols = t.shape
+    return ArcheadTensor(t.data_ptr(), rows, cols, stride[0], _code(t.dtype))
 
 
 def archead_logits_path(H, head: PackedHead, Y, path: int = ARCHEAD_PATH_AUTO, stream=None):
@@ -838,12 +839,20 @@ def archead_cross_entropy(H, labels, head: PackedHead, weight=None, inv_temperat
 # ------------------------------------------------------- in front of the head ---
 
 def _rows(t, name: str, device):
-    """Pointer to the struct of a 2-D device tensor (None for None)."""
+    """Struct of a 2-D tensor on the device (None for None)."""
     if t is None:
         return None
-    if t.get_device() != device.index or device.type != "cuda":
+    if t.get_device() != device.index:
         raise ValueError(f"{name} must be on {device}")
-    return ctypes.pointer(_tensor(t))
+    return _tensor(t)
+
+
+def _at(struct):
+    """Address of a struct (which the caller holds) or None."""
+    return None if struct is None else ctypes.addressof(struct)
+
+
+_NORM_OUTPUTS = frozenset(("sum", "h", "codes", "scale", "inv_rms"))
 
 
 @_scoped
@@ -862,28 +871,30 @@ def archead_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, outputs=("
         raise ValueError("x must be a device tensor")
     xt = _tensor(x)
     N, D = x.shape
-    wanted = set(outputs)
-    if not wanted <= {"sum", "h", "codes", "scale", "inv_rms"}:
+    if not _NORM_OUTPUTS.issuperset(outputs):
         raise ValueError("outputs are among sum, h, codes, scale, inv_rms")
-    out = {}
-    if residual is not None or sum is not None or "sum" in wanted:
-        out["sum"] = torch.empty_like(x, memory_format=torch.contiguous_format) if sum is None else sum
-    if h is not None or "h" in wanted:
-        out["h"] = torch.empty_like(x, memory_format=torch.contiguous_format) if h is None else h
-    if codes is not None or wanted & {"codes", "scale"}:
-        out["codes"] = torch.empty((N, D), dtype=torch.int8, device=dev) if codes is None else codes
-        out["scale"] = torch.empty(N, dtype=torch.float32, device=dev)
-    if "inv_rms" in wanted:
-        out["inv_rms"] = torch.empty(N, dtype=torch.float32, device=dev)
-    inp = ArcheadRmsnormInputs(ctypes.pointer(xt), _rows(residual, "residual", dev),
-                               _vec(weight, "weight", torch.bfloat16, D, dev), eps)
-    outs = ArcheadRmsnormOutputs(_rows(out.get("sum"), "sum", dev), _rows(out.get("h"), "h", dev),
-                                 _rows(out.get("codes"), "codes", dev),
-                                 *(out[k].data_ptr() if k in out else None for k in ("scale", "inv_rms")))
+    rt, st, ht, ct = (_rows(t, k, dev) for t, k in ((residual, "residual"), (sum, "sum"), (h, "h"), (codes, "codes")))
+    scale = inv_rms = None
+    if st is None and (rt is not None or "sum" in outputs):
+        sum = torch.empty((N, D), dtype=torch.bfloat16, device=dev)
+        st = ArcheadTensor(sum.data_ptr(), N, D, D, ARCHEAD_BF16)
+    if ht is None and "h" in outputs:
+        h = torch.empty((N, D), dtype=torch.bfloat16, device=dev)
+        ht = ArcheadTensor(h.data_ptr(), N, D, D, ARCHEAD_BF16)
+    if ct is None and ("codes" in outputs or "scale" in outputs):
+        codes = torch.empty((N, D), dtype=torch.int8, device=dev)
+        ct = ArcheadTensor(codes.data_ptr(), N, D, D, ARCHEAD_I8)
+    if ct is not None:
+        scale = torch.empty(N, dtype=torch.float32, device=dev)
+    if "inv_rms" in outputs:
+        inv_rms = torch.empty(N, dtype=torch.float32, device=dev)
+    inp = ArcheadRmsnormInputs(_at(xt), _at(rt), _vec(weight, "weight", torch.bfloat16, D, dev), eps)
+    outs = ArcheadRmsnormOutputs(_at(st), _at(ht), _at(ct), *(None if t is None else t.data_ptr() for t in (scale, inv_rms)))
     status = lib.archead_rmsnorm(inp, outs, _raw_stream(dev))
     if status:
         _check(status, "archead_rmsnorm")
-    return out
+    got = {"sum": sum, "h": h, "codes": codes, "scale": scale, "inv_rms": inv_rms}
+    return {k: t for k, t in got.items() if t is not None}
 
 
 def archead_rmsnorm_backward_workspace_bytes(n_rows: int, D: int) -> int:
@@ -910,19 +921,22 @@ def archead_rmsnorm_backward(dh, sum, inv_rms, weight=None, dsum=None, dx=None, 
     dev = dh.device
     if dev.type != "cuda":
         raise ValueError("dh must be a device tensor")
-    g = _tensor(dh)
+    gt = _tensor(dh)
     N, D = dh.shape
     if dx is None:
-        dx = torch.empty_like(dh, memory_format=torch.contiguous_format)
+        dx = torch.empty((N, D), dtype=torch.bfloat16, device=dev)
+        xt = ArcheadTensor(dx.data_ptr(), N, D, D, ARCHEAD_BF16)
+    else:
+        xt = _rows(dx, "dx", dev)
     out = {"dx": dx}
-    ws = None
+    ws = dweight = None
     if with_dweight:
-        out["dweight"] = torch.empty(D, dtype=torch.float32, device=dev)
+        dweight = out["dweight"] = torch.empty(D, dtype=torch.float32, device=dev)
         ws = _workspace(workspace, _rmsnorm_backward_workspace_bytes(N, D), dev)
-    inp = ArcheadRmsnormGradInputs(ctypes.pointer(g), _rows(sum, "sum", dev),
-                                   _vec(inv_rms, "inv_rms", torch.float32, N, dev),
-                                   _vec(weight, "weight", torch.bfloat16, D, dev), _rows(dsum, "dsum", dev))
-    outs = ArcheadRmsnormGradOutputs(_rows(dx, "dx", dev), out["dweight"].data_ptr() if with_dweight else None)
+    st, rt = _rows(sum, "sum", dev), _rows(dsum, "dsum", dev)
+    inp = ArcheadRmsnormGradInputs(_at(gt), _at(st), _vec(inv_rms, "inv_rms", torch.float32, N, dev),
+                                   _vec(weight, "weight", torch.bfloat16, D, dev), _at(rt))
+    outs = ArcheadRmsnormGradOutputs(_at(xt), dweight.data_ptr() if with_dweight else None)
     status = lib.archead_rmsnorm_backward(inp, outs, *_span(ws), _raw_stream(dev))
     if status:
         _check(status, "archead_rmsnorm_backward")

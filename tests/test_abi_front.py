@@ -26,7 +26,7 @@ class _Norm:
         self.eps = 1e-6
 
     def __call__(self):
-        p = lambda k: ctypes.pointer(self.t[k]) if self.t[k] is not None else None  # noqa: E731
+        p = lambda k: ctypes.addressof(self.t[k]) if self.t[k] is not None else None  # noqa: E731
         inp = self.ah.ArcheadRmsnormInputs(p("x"), p("residual"), self.v["weight"], self.eps)
         out = self.ah.ArcheadRmsnormOutputs(p("sum"), p("h"), p("codes"), self.v["scale"], self.v["inv_rms"])
         return self.ah.lib.archead_rmsnorm(inp, out, None)
@@ -41,7 +41,7 @@ class _Grad(_Norm):
         self.bytes = 1 << 20
 
     def __call__(self):
-        p = lambda k: ctypes.pointer(self.t[k]) if self.t[k] is not None else None  # noqa: E731
+        p = lambda k: ctypes.addressof(self.t[k]) if self.t[k] is not None else None  # noqa: E731
         inp = self.ah.ArcheadRmsnormGradInputs(p("dh"), p("sum"), self.v["inv_rms"], self.v["weight"], p("dsum"))
         out = self.ah.ArcheadRmsnormGradOutputs(p("dx"), self.v["dweight"])
         return self.ah.lib.archead_rmsnorm_backward(inp, out, self.v["ws"], self.bytes, None)
