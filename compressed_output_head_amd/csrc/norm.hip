@@ -97,7 +97,7 @@ constexpr uint32_t kOnes = 0x3f803f80u;  // two bf16 ones
 template <int T>
 __device__ __forceinline__ void row_reduce(double& sum, uint32_t& top) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
+  for (int o = std::min(T, 64) / 2; o > 0; o >>= 1) {
     sum += __shfl_xor(sum, o);
     top = std::max(top, (uint32_t)__shfl_xor((int)top, o));
   }
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(norm_threads(T)) void rmsnorm_kernel(const NormArgs
   constexpr int kRows = norm_threads(T) / T;
   const int t0 = threadIdx.x % T;
   const int64_t n = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
-  if (n >= a.N) return;  // whole waves, and of T > 64 whole workgroups
+  if (n >= a.N) return;  // all threads of a row, and of T > 64 whole workgroups
   u4 s[K], w[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -207,69 +207,132 @@ __global__ __launch_bounds__(norm_threads(T)) void rmsnorm_kernel(const NormArgs
   }
 }
 
+// An octet of a row's operands of the gradient.
+struct GradOctet {
+  u4 s, d, e;
+  __device__ __forceinline__ void load(const NormBwdArgs& a, int64_t n, int64_t v) {
+    s = load8(a.sum + n * a.sum_stride, v, a.D);
+    d = load8(a.dh + n * a.dh_stride, v, a.D);
+    e = a.dsum ? load8(a.dsum + n * a.ds_stride, v, a.D) : u4{};
+  }
+  __device__ __forceinline__ float dot(const u4& w) const {
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(at(d, j) * at(w, j), at(s, j), sum);
+    return sum;
+  }
+  // dx, and what the octet adds to dweight
+  __device__ __forceinline__ u4 apply(const u4& w, float inv, float c, float (&dw)[8]) const {
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      y[j] = fmaf(inv, at(d, j) * at(w, j) - at(s, j) * c, at(e, j));
+      dw[j] = fmaf(at(d, j), at(s, j) * inv, dw[j]);
+    }
+    return pack8(y);
+  }
+};
+
 // dx = dsum + inv (g - s inv^2 sum_d(g s) / D), g = w dh, and part p of
 // dweight = sum_n dh s inv: row slot p takes the rows p, p + parts, ..., its
-// threads the same columns of all of them.
+// threads the same columns of all of them.  The next row is on its way while
+// one is worked on; rows too long for that (K > 2) are read again for dx, from
+// the cache, and their threads hold the sums of dweight in LDS.
 template <int T, int K>
 __global__ __launch_bounds__(norm_threads(T)) void rmsnorm_backward_kernel(const NormBwdArgs a) {
   constexpr int kSlots = norm_threads(T) / T;
+  constexpr bool kHeld = K <= 2;
   const int t0 = threadIdx.x % T;
   const int p = (int)blockIdx.x * kSlots + threadIdx.x / T;
   if (p >= a.parts) return;
-  u4 w[K];
-  float dw[K][8] = {};
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-    w[k] = a.weight ? load8(a.weight, 8 * (int64_t)(t0 + T * k), a.D) : u4{kOnes, kOnes, kOnes, kOnes};
-  for (int64_t n = p; n < a.N; n += a.parts) {
-    u4 s[K], d[K], e[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int64_t v = 8 * (int64_t)(t0 + T * k);
-      s[k] = load8(a.sum + n * a.sum_stride, v, a.D);
-      d[k] = load8(a.dh + n * a.dh_stride, v, a.D);
-      e[k] = a.dsum ? load8(a.dsum + n * a.ds_stride, v, a.D) : u4{};
-    }
-    const float inv = a.inv_rms[n];
-    double dot = 0.0;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float part = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) part = fmaf(at(d[k], j) * at(w[k], j), at(s[k], j), part);
-      dot += (double)part;
-    }
+  auto column = [&](int k) { return 8 * (int64_t)(t0 + T * k); };
+  auto weight = [&](int k) { return a.weight ? load8(a.weight, column(k), a.D) : u4{kOnes, kOnes, kOnes, kOnes}; };
+  auto finish = [&](double dot, float inv) {
     uint32_t none = 0;
     if constexpr (T > 64) __syncthreads();  // the row before is done with the reduction's memory
     row_reduce<T>(dot, none);
-    const float c = (float)(dot * (double)inv * (double)inv / (double)a.D);
+    return (float)(dot * (double)inv * (double)inv / (double)a.D);
+  };
+  if constexpr (kHeld) {
+    u4 w[K];
+    float dw[K][8] = {};
+    GradOctet next[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float y[8];
+      w[k] = weight(k);
+      next[k].load(a, p, column(k));
+    }
+    float next_inv = a.inv_rms[p];
+    for (int64_t n = p; n < a.N; n += a.parts) {
+      GradOctet row[K];
+      const float inv = next_inv;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        y[j] = fmaf(inv, at(d[k], j) * at(w[k], j) - at(s[k], j) * c, at(e[k], j));
-        dw[k][j] = fmaf(at(d[k], j), at(s[k], j) * inv, dw[k][j]);
+      for (int k = 0; k < K; ++k) row[k] = next[k];
+      if (n + a.parts < a.N) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) next[k].load(a, n + a.parts, column(k));
+        next_inv = a.inv_rms[n + a.parts];
       }
-      if (a.dx) store8(a.dx + n * a.dx_stride, 8 * (int64_t)(t0 + T * k), a.D, pack8(y));
+      double dot = 0.0;
+#pragma unroll
+      for (int k = 0; k < K; ++k) dot += (double)row[k].dot(w[k]);
+      const float c = finish(dot, inv);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        // new values to the compiler: it would keep the products and the
+        // unpacked elements of the sum above, three times the registers
+        asm("" : "+v"(row[k].s), "+v"(row[k].d), "+v"(w[k]));
+        const u4 y = row[k].apply(w[k], inv, c, dw[k]);
+        if (a.dx) store8(a.dx + n * a.dx_stride, column(k), a.D, y);
+      }
     }
+    if (!a.part) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (column(k) + j < a.D) a.part[p * a.D + column(k) + j] = dw[k][j];
+  } else {
+    extern __shared__ f4 sDw[];  // [2 K][T], each thread's own
+    f4* mine = sDw + t0;
+    for (int i = 0; i < 2 * K; ++i) mine[i * T] = f4{};
+    for (int64_t n = p; n < a.N; n += a.parts) {
+      const float inv = a.inv_rms[n];
+      double dot = 0.0;
+#pragma unroll 2
+      for (int k = 0; k < K; ++k) {
+        GradOctet x;
+        x.load(a, n, column(k));
+        dot += (double)x.dot(weight(k));
+      }
+      const float c = finish(dot, inv);
+#pragma unroll 1
+      for (int k = 0; k < K; ++k) {
+        GradOctet x;
+        x.load(a, n, column(k));
+        float dw[8];
+        *reinterpret_cast<f4*>(dw) = mine[2 * k * T];
+        *reinterpret_cast<f4*>(dw + 4) = mine[(2 * k + 1) * T];
+        const u4 y = x.apply(weight(k), inv, c, dw);
+        mine[2 * k * T] = *reinterpret_cast<f4*>(dw);
+        mine[(2 * k + 1) * T] = *reinterpret_cast<f4*>(dw + 4);
+        if (a.dx) store8(a.dx + n * a.dx_stride, column(k), a.D, y);
+      }
+    }
+    if (!a.part) return;
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (column(k) + j < a.D) a.part[p * a.D + column(k) + j] = mine[(2 * k + j / 4) * T][j % 4];
   }
-  if (!a.part) return;
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t v = 8 * (int64_t)(t0 + T * k) + j;
-      if (v < a.D) a.part[p * a.D + v] = dw[k][j];
-    }
 }
 
-// 64 columns of dweight: 16 threads a column add its parts, in fp64.
-constexpr int kDeal = 16;
-__global__ __launch_bounds__(64 * kDeal) void rmsnorm_dweight_kernel(const NormBwdArgs a) {
-  __shared__ double buf[kDeal][64];
-  const int c = threadIdx.x & 63, deal = threadIdx.x >> 6;
-  const int64_t v = 64 * (int64_t)blockIdx.x + c;
+// kSumCols columns of dweight: kDeal threads a column add its parts, in fp64.
+constexpr int kSumCols = 16, kDeal = 64;
+__global__ __launch_bounds__(kSumCols * kDeal) void rmsnorm_dweight_kernel(const NormBwdArgs a) {
+  __shared__ double buf[kDeal][kSumCols];
+  const int c = threadIdx.x % kSumCols, deal = threadIdx.x / kSumCols;
+  const int64_t v = kSumCols * (int64_t)blockIdx.x + c;
   double sum = 0.0;
   if (v < a.D)
 #pragma unroll 4
@@ -285,46 +348,47 @@ __global__ __launch_bounds__(64 * kDeal) void rmsnorm_dweight_kernel(const NormB
 
 // ------------------------------------------------------------------- host ---
 
-// Rows that are worked on at the same time: parts of dweight.
+// Threads of a row, and octets of columns that each takes.
+template <int T_, int K_>
+struct Width {
+  static constexpr int T = T_, K = K_;
+};
+template <class F>
+auto norm_width(int64_t D, F&& f) {
+  return D <= 128    ? f(Width<16, 1>{})
+         : D <= 256  ? f(Width<32, 1>{})
+         : D <= 512  ? f(Width<64, 1>{})
+         : D <= 1024 ? f(Width<64, 2>{})
+         : D <= 2048 ? f(Width<64, 4>{})
+         : D <= 4096 ? f(Width<256, 2>{})
+         : D <= 8192 ? f(Width<256, 4>{})
+         : D <= 16384 ? f(Width<256, 8>{})
+                      : f(Width<1024, 4>{});
+}
+// The gradient holds the sums of dweight too, and a second row: two octets at
+// most, where the norm has up to eight.  (8192 rows of 8192: 105 us with 1024
+// threads of one octet, 114 with 512 of two.)
+template <class F>
+auto backward_width(int64_t D, F&& f) {
+  return D <= 128    ? f(Width<16, 1>{})
+         : D <= 256  ? f(Width<32, 1>{})
+         : D <= 512  ? f(Width<64, 1>{})
+         : D <= 1024 ? f(Width<64, 2>{})
+         : D <= 2048 ? f(Width<256, 1>{})
+         : D <= 4096 ? f(Width<512, 1>{})
+         : D <= 8192 ? f(Width<1024, 1>{})
+         : D <= 16384 ? f(Width<1024, 2>{})
+                      : f(Width<1024, 4>{});
+}
+
+// Rows that are worked on at the same time: parts of dweight.  More of them
+// hide more latency, and are more to write and to add up: with 2^17 and 2^18
+// threads in all, 131072 rows of 512 take 99 and 113 us, 32768 of 2048 101 and
+// 108, 8192 of 8192 165 and 105, 2048 of 32768 206 and 156.
 int norm_parts(int64_t N, int64_t D) {
-  const int64_t most = D <= 2048 ? 2048 : D <= 16384 ? 512 : 256;
-  return (int)std::min(N, most);
+  const int64_t threads = backward_width(D, [](auto w) { return (int64_t)decltype(w)::T; });
+  return (int)std::min(N, (int64_t(1) << (D <= 2048 ? 17 : 18)) / threads);
 }
-
-template <template <int, int> class Launch, typename A>
-void by_width(int64_t D, const A& a, hipStream_t s) {
-  if (D <= 512)
-    Launch<64, 1>::run(a, s);
-  else if (D <= 1024)
-    Launch<64, 2>::run(a, s);
-  else if (D <= 2048)
-    Launch<64, 4>::run(a, s);
-  else if (D <= 4096)
-    Launch<256, 2>::run(a, s);
-  else if (D <= 8192)
-    Launch<256, 4>::run(a, s);
-  else if (D <= 16384)
-    Launch<256, 8>::run(a, s);
-  else
-    Launch<1024, 4>::run(a, s);
-}
-
-template <int T, int K>
-struct LaunchNorm {
-  static void run(const NormArgs& a, hipStream_t s) {
-    constexpr int kRows = norm_threads(T) / T;
-    hipLaunchKernelGGL((rmsnorm_kernel<T, K>), dim3((unsigned)((a.N + kRows - 1) / kRows)), dim3(norm_threads(T)), 0, s, a);
-  }
-};
-
-template <int T, int K>
-struct LaunchNormBwd {
-  static void run(const NormBwdArgs& a, hipStream_t s) {
-    constexpr int kSlots = norm_threads(T) / T;
-    hipLaunchKernelGGL((rmsnorm_backward_kernel<T, K>), dim3((unsigned)((a.parts + kSlots - 1) / kSlots)),
-                       dim3(norm_threads(T)), 0, s, a);
-  }
-};
 
 // A bf16 (or int8) tensor of N rows and D columns.
 int check_rows(const archead_tensor* t, int64_t N, int64_t D, int dtype) {
@@ -417,7 +481,11 @@ int archead_rmsnorm(const archead_rmsnorm_inputs* in, const archead_rmsnorm_outp
   a.scale = out->scale;
   a.inv_rms = out->inv_rms;
   (void)hipGetLastError();  // start from a clean error state
-  by_width<LaunchNorm>(D, a, static_cast<hipStream_t>(stream));
+  norm_width(D, [&](auto w) {
+    constexpr int T = decltype(w)::T, K = decltype(w)::K, kRows = norm_threads(T) / T;
+    hipLaunchKernelGGL((rmsnorm_kernel<T, K>), dim3((unsigned)((N + kRows - 1) / kRows)), dim3(norm_threads(T)), 0,
+                       static_cast<hipStream_t>(stream), a);
+  });
   return hipGetLastError() == hipSuccess ? ARCHEAD_OK : ARCHEAD_E_HIP;
 }
 
@@ -483,9 +551,17 @@ int archead_rmsnorm_backward(const archead_rmsnorm_grad_inputs* in, const archea
   a.parts = norm_parts(N, D);
   hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();  // start from a clean error state
-  if (N > 0) by_width<LaunchNormBwd>(D, a, s);
+  if (N > 0)
+    backward_width(D, [&](auto w) {
+      constexpr int T = decltype(w)::T, K = decltype(w)::K, kSlots = norm_threads(T) / T;
+      constexpr size_t lds = K > 2 ? (size_t)32 * K * T : 0;
+      const auto kernel = rmsnorm_backward_kernel<T, K>;
+      if (lds > 64 * 1024)  // more is opted into per kernel
+        (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((a.parts + kSlots - 1) / kSlots)), dim3(norm_threads(T)), lds, s, a);
+    });
   // no rows: a gradient of zeros
-  if (out->dweight) hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((unsigned)((D + 63) / 64)), dim3(64 * kDeal), 0, s, a);
+  if (out->dweight) hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((unsigned)((D + kSumCols - 1) / kSumCols)), dim3(kSumCols * kDeal), 0, s, a);
   return hipGetLastError() == hipSuccess ? ARCHEAD_OK : ARCHEAD_E_HIP;
 }
 

@@ -257,3 +257,32 @@ def test_norm_in_graphs_and_on_streams():
         for got in o:
             for name in want:
                 assert torch.equal(got[name], want[name]), name
+
+
+# widths of every number of threads a row, and either side of where it changes
+WIDTHS = [(1, 40), (128, 33), (129, 70), (256, 17), (257, 9), (513, 300), (1025, 40), (2049, 700), (4097, 300), (8193, 300),
+          (16385, 300), (20480, 600), (32761, 260), (32768, 300)]
+
+
+@pytest.mark.parametrize("D,N", WIDTHS)
+def test_gradient_of_many_rows_in_place(D, N):
+    """More rows than are worked on at a time, dx over dsum or over dh."""
+    torch, ah = torch_mod(), ah_mod()
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    x, dh, dsum = (torch.randn((N, D), generator=gen, device="cuda").bfloat16() for _ in range(3))
+    w = (1 + 0.3 * torch.randn(D, generator=gen, device="cuda")).bfloat16()
+    inv = ah.archead_rmsnorm(x, weight=w, outputs=("inv_rms",))["inv_rms"]
+    want = ah.archead_rmsnorm_backward(dh, x, inv, weight=w, dsum=dsum)
+    n64 = lambda t: t.double().cpu().numpy()  # noqa: E731
+    exact = oracle.rmsnorm_backward(n64(dh), n64(x), n64(inv), n64(w), n64(dsum))
+    # dx: fp32 sums of eight and few roundings (2^-20 of the terms), then bf16; dweight: a part's
+    # fp32 sum of its rows and two roundings of each term
+    s, g, i64 = n64(x), np.abs(n64(w) * n64(dh)), n64(inv)[:, None]
+    terms = np.abs(n64(dsum)) + i64 * (g + np.abs(s) * i64 ** 2 * (g * np.abs(s)).mean(1, keepdims=True))
+    assert (np.abs(n64(want["dx"]) - exact["dx"]) <= 2.0 ** -8 * np.abs(exact["dx"]) + 2.0 ** -19 * terms).all()
+    size = (np.abs(n64(dh) * s) * i64).sum(0)
+    assert (np.abs(n64(want["dweight"]) - exact["dweight"]) <= (N + 4) * 2.0 ** -24 * size + 2.0 ** -140).all()
+    for k in ("dsum", "dh"):
+        args = {"dsum": dsum.clone(), "dh": dh.clone()}
+        got = ah.archead_rmsnorm_backward(args["dh"], x, inv, weight=w, dsum=args["dsum"], dx=args[k])
+        assert torch.equal(got["dx"], want["dx"]) and torch.equal(got["dweight"], want["dweight"]), k
