@@ -311,12 +311,12 @@ def test_shares_of_the_rows(V, D, r_c, r_r, g, N, share):
     _check(got, H, labels, w, h, 1.0, f"V={V} N={N}")
 
 
-@pytest.mark.parametrize("r_c,r_r", [(16, 8), (0, 0)])
-def test_rows_whose_maximum_rises_along_the_vocabulary(r_c, r_r):
+@pytest.mark.parametrize("V,r_c,r_r,N", [(150000, 16, 8, 1000), (120000, 0, 0, 1200), (1000000, 8, 0, 150)])
+def test_rows_whose_maximum_rises_along_the_vocabulary(V, r_c, r_r, N):
     """A vocabulary in several pieces, and rows whose logits rise from one to
     the next, also by more than an exponent of fp32 holds."""
     torch, ah = torch_mod(), ah_mod()
-    V, D, N, g = 120000, 128, 600, 64
+    D, g = 128, 64
     h, head = _head(21, V, D, r_c, r_r, g)
     W = oracle.w_hat(h)
     rng = np.random.default_rng(1)
