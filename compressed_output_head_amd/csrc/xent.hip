@@ -339,7 +339,7 @@ constexpr int64_t kChunkRows = 4096;                // rows that count, a pass
 constexpr uint64_t kPieceBytes = 256ull << 20;
 constexpr int kHeadParts = 64, kHeadThreads = 256;
 constexpr int kOrderThreads = 1024;
-constexpr int kMergeSlices = 32;
+constexpr int kMergeRows = 8, kMergeSlices = 128;
 constexpr int kZThreads = 512, kZTiles = 4;         // rank tiles of a workgroup
 
 struct ManyArgs {
@@ -364,7 +364,7 @@ struct ManyArgs {
   float* stat;             // [blocks][n32][2]
   float* alpha;            // [n32]
   float* ref;              // [n32] running exponent
-  int32_t* moved;          // [n32/32] whether operands of a row tile are at others
+  int32_t* moved;          // [n32/kMergeRows] whether operands of these rows are at others
   double* sum;             // [n32] running sum
   float* z_label;          // [n32] log2(e) tau times the label's logit
   RowOut* row;             // [n32]
@@ -487,18 +487,19 @@ __global__ __launch_bounds__(256) void xent_arrange_kernel(const BwdArgs b) {
   arrange_codes(b, (int64_t)blockIdx.x * 256 + threadIdx.x);
 }
 
-// 32 rows a workgroup, kMergeSlices threads each: the sum of the piece's blocks
+// kMergeRows rows a workgroup (a CU reads no faster), kMergeSlices threads each: the sum of the piece's blocks
 // and of those before, and the running exponent, which is moved only where a
 // block has one above it: to kHeadroom above the largest, so that few pieces
 // move it.
 constexpr float kHeadroom = 3.0f;
-__global__ __launch_bounds__(32 * kMergeSlices) void xent_merge_kernel(const ManyArgs a) {
-  __shared__ float sTop[kMergeSlices][32];
-  __shared__ double sSum[kMergeSlices][32];
-  constexpr int kBatch = 8;
-  const int c = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int64_t n = 32 * (int64_t)blockIdx.x + c;
-  if (32 * (int64_t)blockIdx.x >= a.plan[4 * a.pass]) return;
+__global__ __launch_bounds__(kMergeRows * kMergeSlices) void xent_merge_kernel(const ManyArgs a) {
+  constexpr int kWaves = kMergeRows * kMergeSlices / 64;
+  __shared__ float sTop[kWaves][kMergeRows];
+  __shared__ double sSum[kWaves][kMergeRows];
+  constexpr int kBatch = 16;  // loads in flight: their latency is what a round takes
+  const int c = threadIdx.x % kMergeRows, slice = threadIdx.x / kMergeRows;
+  const int64_t n = kMergeRows * (int64_t)blockIdx.x + c;
+  if (n / 32 * 32 >= a.plan[4 * a.pass]) return;
   const float infinity = __builtin_huge_valf();
   const u2* stat = reinterpret_cast<const u2*>(a.stat) + n;
   // sum s at exponent m moved to m + j (j whole and not below 0, or not finite
@@ -517,20 +518,31 @@ __global__ __launch_bounds__(32 * kMergeSlices) void xent_merge_kernel(const Man
     m = t;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (k0 + i * kMergeSlices < a.blocks) s += moved((double)__uint_as_float(x[i][1]), m - __uint_as_float(x[i][0]));
+      if (k0 + i * kMergeSlices < a.blocks) {  // (2^-149 is nothing here: the largest is 2^10 at least)
+        const float y = __uint_as_float(x[i][1]), j = m - __uint_as_float(x[i][0]);
+        s += (double)(j <= 1000.0f ? ldexpf(y, -(int)j) : y == y ? 0.0f : y);
+      }
   }
-  sTop[slice][c] = m;
-  sSum[slice][c] = s;
+  auto join = [&](float m1, double s1) {
+    const float t = fmaxf(m, m1);
+    s = moved(s, t - m) + moved(s1, t - m1);
+    m = t;
+  };
+#pragma unroll
+  for (int o = kMergeRows; o < 64; o *= 2) join(__shfl_xor(m, o), __shfl_xor(s, o));
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) < kMergeRows) {
+    sTop[wave][c] = m;
+    sSum[wave][c] = s;
+  }
   __syncthreads();
   if (slice == 0) {
+    for (int k = 1; k < kWaves; ++k) join(sTop[k][c], sSum[k][c]);
     const float old = a.ref[n];
-    float t = old;
-    for (int k = 0; k < kMergeSlices; ++k) t = fmaxf(t, sTop[k][c]);
+    float t = fmaxf(old, m);
     const bool raised = t > old;
     if (raised) t += kHeadroom;
-    double sum = moved(a.sum[n], t - old);
-    for (int k = 0; k < kMergeSlices; ++k) sum += moved(sSum[k][c], t - sTop[k][c]);
-    a.sum[n] = sum;
+    a.sum[n] = moved(a.sum[n], t - old) + moved(s, t - m);
     a.ref[n] = t;
     a.alpha[n] = t - old <= 1000.0f ? ldexpf(1.0f, -(int)(t - old)) : 0.0f;
     const bool any = __any(raised);
@@ -557,7 +569,11 @@ constexpr int kMoveWaves = 4;
 __global__ __launch_bounds__(64 * kMoveWaves) void xent_move_kernel(const ManyArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t tile = blockIdx.x, n = 32 * tile + (lane & 31);
-  if (32 * tile >= a.plan[4 * a.pass] || !a.moved[tile]) return;
+  if (32 * tile >= a.plan[4 * a.pass]) return;
+  int any = 0;
+#pragma unroll
+  for (int i = 0; i < 32 / kMergeRows; ++i) any |= a.moved[32 / kMergeRows * tile + i];
+  if (!any) return;
   constexpr int kBatch = 4;
   const float ref = a.ref[n];
   h8* e = reinterpret_cast<h8*>(a.b.hf) + tile * a.steps * 64 + lane;
@@ -1011,7 +1027,7 @@ ManyLayout many_layout(const archead_dims* d, int64_t N) {
   L.stat = take(blocks * n32 * 8);
   L.alpha = take(n32 * 4);
   L.ref = take(n32 * 4);
-  L.moved = take(n32 / 8);
+  L.moved = take(n32 / kMergeRows * 4);
   L.sum = take(n32 * 8);
   L.z_label = take(n32 * 4);
   L.row = take(n32 * sizeof(RowOut));
@@ -1131,7 +1147,7 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
       a.first = vt == 0;
       a.step0 = (int)(16 * vt);
       b.ksteps = (int)(16 * vn);
-      hipLaunchKernelGGL(xent_merge_kernel, dim3((unsigned)(L.n32 / 32)), dim3(32 * kMergeSlices), 0, s, a);
+      hipLaunchKernelGGL(xent_merge_kernel, dim3((unsigned)(L.n32 / kMergeRows)), dim3(kMergeRows * kMergeSlices), 0, s, a);
       if (!a.dH) continue;
       const int64_t row_tiles = L.n32 / 32;
       // (2048 workgroups where there are row tiles enough, and a block for every wave)
