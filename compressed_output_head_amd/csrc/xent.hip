@@ -373,9 +373,20 @@ struct ManyArgs {
   int64_t part_rows;       // room for partial sums
 };
 
-// Largest |s_R|, |s_Ac|, |s_Aw| of a part of the vocabulary.
-__global__ __launch_bounds__(kHeadThreads) void xent_head_kernel(const ManyArgs a) {
+// What waits for nothing.  Workgroup 0 .. kHeadParts - 1: largest |s_R|, |s_Ac|,
+// |s_Aw| of a part of the vocabulary.  The next `arrange`: the A codes in the
+// order of the product along the vocabulary.  Those behind, for rows that do
+// not count: their gradient.
+__global__ __launch_bounds__(kHeadThreads) void xent_head_kernel(const ManyArgs a, int64_t arrange) {
   __shared__ float buf[kHeadThreads / 64][3];
+  if (blockIdx.x >= kHeadParts) {
+    const int64_t i = (int64_t)blockIdx.x - kHeadParts, n = i - arrange;
+    if (n < 0)
+      arrange_codes(a.b, i * kHeadThreads + threadIdx.x);
+    else if (a.weight[n] == 0.0f)
+      for (int64_t d = threadIdx.x; d < a.b.D; d += kHeadThreads) a.dH[n * a.dh_stride + d] = 0;
+    return;
+  }
   float m[3] = {};
   for (int64_t v = (int64_t)blockIdx.x * kHeadThreads + threadIdx.x; v < a.b.V; v += kHeadParts * kHeadThreads) {
     float s[3];
@@ -461,13 +472,6 @@ __global__ __launch_bounds__(kOrderThreads) void xent_order_kernel(const ManyArg
   }
 }
 
-// The gradient of rows that do not count.
-__global__ __launch_bounds__(256) void xent_zero_kernel(const ManyArgs a) {
-  const int64_t n = blockIdx.x;
-  if (a.weight[n] != 0.0f) return;
-  for (int64_t d = threadIdx.x; d < a.b.D; d += 256) a.dH[n * a.dh_stride + d] = 0;
-}
-
 // Row blockIdx.x of the pass: its H (zeros behind the last one that counts),
 // and no sums.
 __global__ __launch_bounds__(256) void xent_gather_kernel(const ManyArgs a) {
@@ -480,11 +484,6 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(const ManyArgs a) {
   const u4* src = reinterpret_cast<const u4*>(a.H + (i < count ? (int64_t)a.map[a.pass * kChunkRows + i] : 0) * a.h_stride);
   u4* dst = reinterpret_cast<u4*>(a.Hc + i * a.b.D);
   for (int64_t c = threadIdx.x; c < a.b.D / 8; c += 256) dst[c] = i < count ? src[c] : u4{};
-}
-
-// The A codes in the order of the product along the vocabulary.
-__global__ __launch_bounds__(256) void xent_arrange_kernel(const BwdArgs b) {
-  arrange_codes(b, (int64_t)blockIdx.x * 256 + threadIdx.x);
 }
 
 // kMergeRows rows a workgroup (a CU reads no faster), kMergeSlices threads each: the sum of the piece's blocks
@@ -757,20 +756,23 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(const ManyArgs a) {
 // residual, and Z B on the bf16 MFMA with Z and B as pairs of bf16 numbers (three
 // products, 2^-15 of |Z| |B| at most).  Tile c of four holds the columns 4 i +
 // c, so that a lane has four neighbouring ones of a row.
+template <bool kShare>
 __global__ __launch_bounds__(kFinishThreads, 2) void xent_finish_kernel(const ManyArgs a) {
   constexpr int kWaves = kFinishThreads / 64;
   const BwdArgs& b = a.b;
   const int tid = threadIdx.x, lane = tid & 63, c32 = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = b.r_c + b.r_r;
-  const int64_t n0 = 32 * (int64_t)blockIdx.x, kt = (int64_t)blockIdx.y * kWaves + wave, count = a.plan[4 * a.pass];
+  const int first = kShare ? wave : 0, waves = kShare ? kWaves : 1;  // of the splits and of the ranks
+  const int64_t n0 = 32 * (int64_t)blockIdx.x, kt = kShare ? (int64_t)blockIdx.y : (int64_t)blockIdx.y * kWaves + wave;
+  const int64_t count = a.plan[4 * a.pass];
   if (n0 >= count || kt >= b.nkt) return;
   const int64_t d = kKTile * kt + 4 * c32, group = d / b.g;
   // row of element v of a result tile; past the last row that one
   auto row = [&](int v) { return std::min<int64_t>(n0 + 8 * (v >> 2) + 4 * half + (v & 3), count - 1); };
   const int splits = a.plan[4 * a.pass + 2];
   f16x acc[4] = {};
-  for (int p = 0; p < splits; ++p) {
+  for (int p = first; p < splits; p += waves) {
     f4 y[16];
 #pragma unroll
     for (int v = 0; v < 16; ++v) y[v] = *reinterpret_cast<const f4*>(b.part + ((int64_t)p * count + row(v)) * b.D + d);
@@ -788,10 +790,10 @@ __global__ __launch_bounds__(kFinishThreads, 2) void xent_finish_kernel(const Ma
     const float s = (float)b.r_gcodes[l * b.ng + group] * f16_to_f32(b.r_rowscale[l]);
     const float f = undo * a.row[row(v)].mean;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c][v] = fmaf(-s, (float)((int32_t)(w << (28 - 4 * c)) >> 28), acc[c][v] * f);
+    for (int c = 0; c < 4; ++c) acc[c][v] = fmaf(first == 0 ? -s : 0.0f, (float)((int32_t)(w << (28 - 4 * c)) >> 28), acc[c][v] * f);
   }
   const float* zrow = b.z + std::min<int64_t>(n0 + c32, count - 1) * r;
-  for (int j0 = 0; j0 < r; j0 += 16) {
+  for (int j0 = 16 * first; j0 < r; j0 += 16 * waves) {
     const bool in = j0 + 8 * half < r;  // ranks come in eights
     const int j = in ? j0 + 8 * half : j0;
     uint32_t code[8];
@@ -815,6 +817,18 @@ __global__ __launch_bounds__(kFinishThreads, 2) void xent_finish_kernel(const Ma
       acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(zp.lo, bp.hi, acc[c], 0, 0, 0);
       acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(zp.hi, bp.hi, acc[c], 0, 0, 0);
     }
+  }
+  if constexpr (kShare) {
+    __shared__ f16x red[kWaves - 1][4][64];
+    if (wave > 0)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) red[wave - 1][c][lane] = acc[c];
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int w = 0; w < kWaves - 1; ++w)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[c] += red[w][c][lane];
   }
 #pragma unroll
   for (int v = 0; v < 16; ++v) {
@@ -1108,22 +1122,19 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
   if (int rc = tile_args(&h, &p, f)) return rc;
   const int tiles = b.nct + b.nwt;
   (void)hipGetLastError();  // start from a clean error state
-  hipLaunchKernelGGL(xent_head_kernel, dim3(kHeadParts), dim3(kHeadThreads), 0, s, a);
-  // the launches that some number of rows may need: for each of 2, 4, 6 and 8 row tiles
+  b.ksteps = (int)a.asteps;
+  const int64_t arrange = a.dH ? (tiles * a.asteps * 16 + kHeadThreads - 1) / kHeadThreads : 0;
+  hipLaunchKernelGGL(xent_head_kernel, dim3((unsigned)(kHeadParts + arrange + (a.dH && a.weight ? N : 0))), dim3(kHeadThreads), 0, s, a, arrange);
+  // the launches that some number of rows that count may need (without weights it
+  // is known): for each of 2, 4, 6 and 8 row tiles
   bool may[5] = {};
   if (L.rows > kExpFewRows)
     may[4] = true;
   else
-    for (int64_t t = 0; t <= L.n32 / 32; ++t) may[exp_tiles(t, d->D >= 256) / 2] = true;
+    for (int64_t t = a.weight ? 1 : L.n32 / 32; t <= L.n32 / 32; ++t) may[exp_tiles(t, d->D >= 256) / 2] = true;
   a.passes = L.passes;
   b.ksteps = (int)(16 * L.piece);
   hipLaunchKernelGGL(xent_order_kernel, dim3((unsigned)(1 + (16 * a.asteps + kOrderThreads - 1) / kOrderThreads)), dim3(kOrderThreads), 0, s, a);
-  if (a.dH && tiles) {
-    BwdArgs all = b;
-    all.ksteps = (int)a.asteps;
-    hipLaunchKernelGGL(xent_arrange_kernel, dim3((unsigned)((tiles * a.asteps * 16 + 255) / 256)), dim3(256), 0, s, all);
-  }
-  if (a.dH && a.weight) hipLaunchKernelGGL(xent_zero_kernel, dim3((unsigned)N), dim3(256), 0, s, a);
   for (int pass = 0; pass < L.passes; ++pass) {
     a.pass = pass;
     hipLaunchKernelGGL(xent_gather_kernel, dim3((unsigned)L.n32), dim3(256), 0, s, a);
@@ -1164,7 +1175,12 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
     }
     hipLaunchKernelGGL(xent_rows_kernel, dim3((unsigned)L.rows), dim3(256), 0, s, a);
     if (a.dH)
-      hipLaunchKernelGGL(xent_finish_kernel, dim3((unsigned)(L.n32 / 32), (unsigned)((b.nkt + 3) / 4)), dim3(kFinishThreads), 0, s, a);
+      // where tiles are few, four waves share one: 64, 500, 1000 and 2000 rows of 4096
+      // columns take 14, 20, 34 and 49 us, with a wave each 26, 23, 27 and 39
+      if (L.n32 / 32 * b.nkt < 1024)
+        hipLaunchKernelGGL(xent_finish_kernel<true>, dim3((unsigned)(L.n32 / 32), (unsigned)b.nkt), dim3(kFinishThreads), 0, s, a);
+      else
+        hipLaunchKernelGGL(xent_finish_kernel<false>, dim3((unsigned)(L.n32 / 32), (unsigned)((b.nkt + 3) / 4)), dim3(kFinishThreads), 0, s, a);
     if (hipGetLastError() != hipSuccess) return ARCHEAD_E_HIP;
   }
   return ARCHEAD_OK;
