@@ -8,7 +8,7 @@
 // any order, so the codes are used as they lie, and X is brought to their
 // order: P swaps the middle pairs of every eight columns.
 //
-//   i8_few_kernel      up to 16 tokens: streams the head once
+//   i8_few_kernel      up to 8 tokens: streams the head once
 //   i8_arrange_kernel  X in operand order
 //   i8_tile_kernel     32 TT tokens x 32 WN WCB rows of the vocabulary a workgroup
 #include <algorithm>
@@ -28,7 +28,6 @@ constexpr int64_t kI8ChunkRows = 16384;  // rows of X whose operands the workspa
 constexpr int64_t kI8MaxCols = 65536;    // 2^14 D below 2^30
 constexpr int64_t kI8MaxRows = int64_t(1) << 22;
 constexpr int kI8Tile = 2048;            // bytes of a tile of 16 rows x 128 columns
-constexpr int kFewTokens = 16;
 constexpr uint32_t kFewLds = 128 * 1024;
 constexpr int kXcds = 8;
 
@@ -75,18 +74,24 @@ __device__ __forceinline__ void static_for(F&& f) {
   }
 }
 
-// Up to 16 tokens: every wave takes blocks of 16 rows of the vocabulary, a
+// Few tokens: bound by the head's bytes, 622 MB of a 151936 x 4096 head in 106
+// us, 5.9 TB/s (the 16 columns of an MFMA cost nothing beside that, and one
+// workgroup of 16 waves a CU reads as fast as two of eight).  The tokens'
+// operands come from LDS for every 16 rows: 1, 8 and 16 tokens take 108, 116
+// and 130 us, in a tile of 64 tokens, whose waves take 32 rows, 115, 119 and 122.
+// So up to 8, where they fit LDS.  Every wave takes blocks of 16 rows of the vocabulary, a
 // grid's waves apart, over all columns, with kRing packed tiles in flight
 // across the blocks' borders; X in operand order in LDS (tile, step pair h, run
 // q, token).  Tiles past the last column meet operands of zero.
+constexpr int kFewTokens = 8;
+constexpr int kFewThreads = 1024;
 constexpr int kRing = 4;
-template <int NW>
-__global__ __launch_bounds__(64 * NW, 4) void i8_few_kernel(const I8Args a) {
+__global__ __launch_bounds__(kFewThreads, 4) void i8_few_kernel(const I8Args a) {
   extern __shared__ __align__(16) u4 sX[];  // [nkt rounded up to kRing][2][4][N]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int N = (int)a.N, groups = (a.nkt + kRing - 1) / kRing;
-  const int64_t first = (int64_t)wave * gridDim.x + blockIdx.x, waves = (int64_t)gridDim.x * NW;
+  const int64_t first = (int64_t)wave * gridDim.x + blockIdx.x, waves = (int64_t)gridDim.x * (kFewThreads / 64);
   const uint8_t* const src = a.codes + 32 * lane;
   const int64_t tstride = a.nb * kI8Tile;
   u4 w[kRing][2];
@@ -98,7 +103,7 @@ __global__ __launch_bounds__(64 * NW, 4) void i8_few_kernel(const I8Args a) {
   };
   // (past the last block: tiles of that one, which are cached and not used)
   static_for<0, kRing>([&](auto i) { load(std::min(first, a.nb - 1), decltype(i)::value, i); });
-  for (int e = tid; e < groups * kRing * 8 * N; e += 64 * NW) {
+  for (int e = tid; e < groups * kRing * 8 * N; e += kFewThreads) {
     const int n = e % N, hq = e / N % 8, kt = e / N / 8;
     sX[e] = kt < a.nkt ? operand(a.X + n * a.x_stride, kt, hq & 3, hq >> 2) : u4{};
   }
@@ -168,7 +173,10 @@ __device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t rs, void* dst
 // MFMA steps: the tokens' fragments by copies straight to an LDS ring of four
 // stages, the head's codes to registers of the wave that uses them, AHEAD
 // stages before; a step's registers are loaded again as soon as it is
-// multiplied.
+// multiplied.  256 tokens x 256 rows have every code fetched for 128 tokens and
+// every token's for 64 rows: 4096 tokens of a 151936 x 4096 head 2.75 ms, 1.86
+// POP/s (a large library product of 8-bit integers: 1.94), bound by the MFMAs
+// under the power limit; 16 to 64 tokens are bound by the head's bytes.
 template <int TT, int WM, int WN, int WCB>
 struct I8Shape {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves, MT = TT / WM;
@@ -341,15 +349,14 @@ int check_int8_head(const archead_dims* d) {
   return ARCHEAD_OK;
 }
 
-template <int NW>
 hipError_t launch_i8_few(const I8Args& a, hipStream_t s) {
   const uint32_t lds = few_lds(a.N, a.D);
-  const int64_t blocks = std::min<int64_t>(a.nb, NW == 8 ? 512 : 256);
+  const int64_t blocks = std::min<int64_t>(a.nb, 256);  // one a CU
   if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute((const void*)&i8_few_kernel<NW>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    const hipError_t e = hipFuncSetAttribute((const void*)&i8_few_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(i8_few_kernel<NW>, dim3((unsigned)blocks), dim3(64 * NW), lds, s, a);
+  hipLaunchKernelGGL(i8_few_kernel, dim3((unsigned)blocks), dim3(kFewThreads), lds, s, a);
   return hipGetLastError();
 }
 
@@ -362,11 +369,13 @@ hipError_t launch_i8_tile(const I8Args& a, hipStream_t s) {
 }
 
 hipError_t launch_i8(const I8Args& a, hipStream_t s) {
-  if (few_fits(a.N, a.D)) return few_lds(a.N, a.D) <= 76 * 1024 ? launch_i8_few<8>(a, s) : launch_i8_few<16>(a, s);
+  if (few_fits(a.N, a.D)) return launch_i8_few(a, s);
   const int64_t pieces = (int64_t)a.ntiles * a.nkt * 256;
   hipLaunchKernelGGL(i8_arrange_kernel, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, s, a);
   if (const hipError_t e = hipGetLastError()) return e;
-  if (a.N <= 32) return launch_i8_tile<1, 1, 4, 1>(a, s);
+  // 64 tokens x 128 rows, 128 x 256 and 256 x 256: 64 tokens of a 151936 x 4096
+  // head take 136, 170 us (with the first and the second), 128 take 183 and 216
+  // (second, third), 256 take 232 and 264 (third, second)
   if (a.N <= 64) return launch_i8_tile<2, 1, 4, 1>(a, s);
   if (a.N <= 128) return launch_i8_tile<4, 2, 4, 2>(a, s);
   return launch_i8_tile<8, 2, 4, 2>(a, s);

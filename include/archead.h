@@ -748,7 +748,7 @@ ARCHEAD_API int archead_rmsnorm_backward(const archead_rmsnorm_grad_inputs* in, 
                                          void* workspace, uint64_t workspace_bytes, void* stream);
 
 /* Device workspace archead_logits_int8 needs for n_tokens rows: 0 for few
- * (up to 16 that fit LDS), else min(n_tokens, 16384) rows of D bytes, rounded
+ * (up to 8 that fit LDS), else min(n_tokens, 16384) rows of D bytes, rounded
  * up to 32 rows.  Pure host arithmetic.  E_NULL, E_DIMS, E_SHAPE,
  * E_UNSUPPORTED (not a row-INT8 head, D above 65536). */
 ARCHEAD_API int archead_logits_int8_workspace_bytes(const archead_dims* d, int64_t n_tokens, uint64_t* bytes);

@@ -208,8 +208,8 @@ def test_int8_error_paths(ah, kw, status):  # noqa: F811
 def test_int8_no_rows_and_workspace(ah):  # noqa: F811
     assert _int8(ah, n=0, X_data=None, Y_data=None, P_buffer=None, P_workspace=None, scale=None) == 0
     f = ah.archead_logits_int8_workspace_bytes
-    assert f(1000, 256, 64, 0) == 0 and f(1000, 256, 64, 16) == 0 and f(1000, 256, 64, 17) == 32 * 256
-    assert f(1000, 16384, 64, 16) == 32 * 16384  # 16 rows of this size do not fit LDS
+    assert f(1000, 256, 64, 0) == 0 and f(1000, 256, 64, 8) == 0 and f(1000, 256, 64, 9) == 32 * 256
+    assert f(1000, 32768, 64, 8) == 32 * 32768  # 8 rows of this size do not fit LDS
     assert f(1000, 256, 64, 1 << 20) == 16384 * 256
     out = ctypes.c_uint64()
     g = ah.lib.archead_logits_int8_workspace_bytes

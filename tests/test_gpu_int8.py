@@ -37,11 +37,12 @@ def _check(Y, X, s, h, dtype):
     assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4])
 
 
-CASES = [  # V, D, N: few tokens in LDS, the four token tiles, ragged ends
+CASES = [  # V, D, N: few tokens in LDS, the token tiles, ragged ends
     (1, 128, 1), (15, 128, 16), (1000, 256, 1), (777, 640, 3), (2003, 1024, 16), (4099, 512, 7),
     (300, 8192, 16), (200, 16384, 5), (64, 65536, 2),
     (1000, 128, 17), (333, 384, 32), (2003, 512, 33), (1031, 1152, 64), (999, 256, 65), (517, 640, 128),
     (4099, 256, 129), (530, 896, 257), (1000, 512, 700), (129, 128, 1100), (70, 16384, 40),
+    (1000, 512, 8), (1000, 512, 9), (500, 16384, 8), (40, 32768, 8),
 ]
 
 
