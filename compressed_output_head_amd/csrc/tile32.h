@@ -138,7 +138,12 @@ __device__ __forceinline__ void lds_copy16(__amdgpu_buffer_rsrc_t rs, void* dst,
 
 // ST: instead of storing Y, each workgroup reduces its 256 logits of every
 // token to a row-statistics piece, written to a.st_part[token][vt].
-// EX: instead of storing Y, the exponentials' epilogue.
+// EX: instead of storing Y, the exponentials' epilogue, on the tiles of the rows
+// that count: e = 2^(z - B + 14) in fp16 as operands of the product with the
+// head, B the row's exponent rounded up over 32 vocabulary entries or its running
+// one if that is above (or less than 1 below), with B and the sum for each row
+// and block.  3690 rows of a 151936 x 4096 head take 4.8 ms, 0.96 PFLOP/s with the
+// MFMAs busy 56% of the clock that the power limit leaves.
 template <int GC, int TT, bool ST, bool EX>
 __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp, const T32Exp& ex) {
   constexpr int kT32TT = TT, kT32MT = TT;     // token tiles per workgroup and per wave

@@ -24,6 +24,15 @@
 //   xent_z_kernel           (e s_A) code added to Z
 //   xent_main_kernel        e (s_R q4 c8) added to the sums
 // and at the end xent_rows_kernel (log p, Z), xent_finish_kernel (dH).
+//
+// Few rows are bound by the head's bytes, which are read twice, for the logits
+// and for dH: one row of a 151936 x 4096 head 150 us, of it 57 and 67 of the
+// two readings and 29 of the launches around them.  (One reading would have to
+// hold a workgroup's vocabulary rows over all columns, unpacked twice, between a
+// logit and its exponential.)  Many rows are bound by the MFMAs under the power
+// limit, two products of the head with the rows: 4096 rows, nine in ten of
+// which count, 9.3 ms, 4.8 in tile32_exp_kernel (0.96 PFLOP/s) and 4.1 in
+// xent_main_kernel (1.13), 0.7 in what joins the pieces.
 #include <algorithm>
 
 #include "backward_main.h"
@@ -486,10 +495,10 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(const ManyArgs a) {
   for (int64_t c = threadIdx.x; c < a.b.D / 8; c += 256) dst[c] = i < count ? src[c] : u4{};
 }
 
-// kMergeRows rows a workgroup (a CU reads no faster), kMergeSlices threads each: the sum of the piece's blocks
+// kMergeRows rows a workgroup, kMergeSlices threads each: the sum of the piece's blocks
 // and of those before, and the running exponent, which is moved only where a
 // block has one above it: to kHeadroom above the largest, so that few pieces
-// move it.
+// move it.  (With 32 rows a workgroup, 8 of them read 8 MB: 34 us, now 20.)
 constexpr float kHeadroom = 3.0f;
 __global__ __launch_bounds__(kMergeRows * kMergeSlices) void xent_merge_kernel(const ManyArgs a) {
   constexpr int kWaves = kMergeRows * kMergeSlices / 64;
@@ -597,9 +606,10 @@ __global__ __launch_bounds__(64 * kMoveWaves) void xent_move_kernel(const ManyAr
 }
 
 // 64 rows x kZTiles rank tiles (half of them of each part of the ranks) a
-// workgroup over part blockIdx.y of the piece's steps, dealt to the waves; e s_A is formed in registers (rounded
-// to fp16 once more), the codes are exact.  The waves' sums are added up in
-// order and then to the part's sums of the pieces before.
+// workgroup over part blockIdx.y of the piece's steps, dealt to the waves; e s_A
+// is formed in registers (rounded to fp16 once more), the codes are exact.  The
+// waves' sums are added up in order and then to the part's sums of the pieces
+// before.  Bound by the operands' bytes (250 MB a full piece, 84 us).
 __global__ __launch_bounds__(kZThreads, 2) void xent_z_kernel(const ManyArgs a) {
   constexpr int kWaves = kZThreads / 64, kDepth = 3;
   __shared__ float red[kWaves / 2][kZTiles][16][64];
