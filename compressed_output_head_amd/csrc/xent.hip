@@ -346,6 +346,12 @@ constexpr int64_t kChunkRows = 4096;                // rows that count, a pass
 // take 9.97 ms with 64 MiB, 9.64 with 128, 9.52 with 192, 9.34 with 256 and with
 // 384, 9.35 with 512.
 constexpr uint64_t kPieceBytes = 256ull << 20;
+// Where 512 workgroups of 2 row tiles (two a CU) do the tiles of the first
+// product, they get 2, and the launches for other numbers are left out: 200 rows
+// of 8192 x 1024 take 126 us in place of 156, 250 of 32000 x 2048 194 (206), 4096
+// of 1024 x 2048 166 (193); with up to 1536 workgroups, 250 of 65536 x 2048 take
+// 287 in place of 256, 130 of 65536 x 4096 350 (286).
+constexpr int64_t kSmall = 512;
 constexpr int kHeadParts = 64, kHeadThreads = 256;
 constexpr int kOrderThreads = 1024;
 constexpr int kMergeRows = 8, kMergeSlices = 128;
@@ -378,6 +384,7 @@ struct ManyArgs {
   float* z_label;          // [n32] log2(e) tau times the label's logit
   RowOut* row;             // [n32]
   int64_t asteps;          // steps of the whole vocabulary
+  int row_tiles;           // of a workgroup for any number of rows that count, or 0: by that number
   int pass, passes, blocks, first, step0, steps;
   int64_t part_rows;       // room for partial sums
 };
@@ -471,7 +478,7 @@ __global__ __launch_bounds__(kOrderThreads) void xent_order_kernel(const ManyArg
   const int64_t total = sCount[kOrderThreads - 1];
   for (int p = tid; p < a.passes; p += kOrderThreads) {
     const int64_t count = std::max<int64_t>(0, std::min(total - p * kChunkRows, kChunkRows));
-    const int tt = a.b.N > kExpFewRows ? 8 : exp_tiles((count + 31) / 32, a.b.D >= 256);
+    const int tt = a.row_tiles ? a.row_tiles : exp_tiles((count + 31) / 32, a.b.D >= 256);
     const int64_t tiles = std::max<int64_t>(1, (count + 32 * tt - 1) / (32 * tt) * ((a.b.D + 255) / 256));
     const int64_t most = std::min(std::min<int64_t>(kMaxSplits, a.b.ksteps / 4),
                                   std::min(main_groups(a.b.N, a.b.D, tt) / tiles, a.part_rows / std::max<int64_t>(count, 1)));
@@ -1138,8 +1145,9 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
   // the launches that some number of rows that count may need (without weights it
   // is known): for each of 2, 4, 6 and 8 row tiles
   bool may[5] = {};
-  if (L.rows > kExpFewRows)
-    may[4] = true;
+  a.row_tiles = d->D >= 256 && L.vtiles * ((L.n32 + 63) / 64) <= kSmall ? 2 : L.rows > kExpFewRows ? 8 : 0;
+  if (a.row_tiles)
+    may[a.row_tiles / 2] = true;
   else
     for (int64_t t = a.weight ? 1 : L.n32 / 32; t <= L.n32 / 32; ++t) may[exp_tiles(t, d->D >= 256) / 2] = true;
   a.passes = L.passes;
