@@ -52,13 +52,15 @@ constexpr int kMaxSplits = 64;
 // every stage, and the partial sums written and read at 4 TB/s.
 __host__ __device__ inline int best_parts(int64_t N, int64_t D, int64_t stages, int tt, int64_t most) {
   constexpr double kRoundUs = 4.0;
-  const int64_t tiles = (N + 32 * tt - 1) / (32 * tt) * ((D + 255) / 256), slots = tt == 2 ? 512 : 256;
+  // (32 bits: a kernel does this too, one thread, whose wide divisions would take 10 us)
+  const uint32_t tiles = (uint32_t)((N + 32 * tt - 1) / (32 * tt) * ((D + 255) / 256)), slots = tt == 2 ? 512 : 256;
+  const uint32_t steps = (uint32_t)stages, top = (uint32_t)std::max<int64_t>(most, 0);
   const double stage_us = tt == 8 ? 1.75 : tt == 6 ? 1.45 : tt == 4 ? 1.15 : 1.4;
   double best = 1e30;
   int pick = 1;
-  for (int64_t p = 1; p <= most; ++p) {
-    const double us = (double)((tiles * p + slots - 1) / slots) * (kRoundUs + stage_us * (double)((stages + p - 1) / p)) +
-                      (double)(p * N * D) * 8.0 / 4e6;
+  for (uint32_t p = 1; p <= top; ++p) {
+    const double us = (double)((tiles * p + slots - 1) / slots) * (kRoundUs + stage_us * (double)((steps + p - 1) / p)) +
+                      (double)((int64_t)p * N * D) * 8.0 / 4e6;
     if (us < best) {
       best = us;
       pick = (int)p;

@@ -353,7 +353,6 @@ constexpr uint64_t kPieceBytes = 256ull << 20;
 // 287 in place of 256, 130 of 65536 x 4096 350 (286).
 constexpr int64_t kSmall = 512;
 constexpr int kHeadParts = 64, kHeadThreads = 256;
-constexpr int kOrderThreads = 1024;
 constexpr int kMergeRows = 8, kMergeSlices = 128;
 constexpr int kZThreads = 512, kZTiles = 4;         // rank tiles of a workgroup
 
@@ -387,16 +386,71 @@ struct ManyArgs {
   int row_tiles;           // of a workgroup for any number of rows that count, or 0: by that number
   int pass, passes, blocks, first, step0, steps;
   int64_t part_rows;       // room for partial sums
+  int64_t main_steps;      // steps of a whole piece
 };
 
-// What waits for nothing.  Workgroup 0 .. kHeadParts - 1: largest |s_R|, |s_Ac|,
-// |s_Aw| of a part of the vocabulary.  The next `arrange`: the A codes in the
-// order of the product along the vocabulary.  Those behind, for rows that do
-// not count: their gradient.
+// Workgroups of the product's launches, for any number of rows that count.
+__host__ __device__ inline int64_t main_groups(int64_t rows, int64_t D, int tt) {
+  return std::max<int64_t>((rows + 32 * tt - 1) / (32 * tt) * ((D + 255) / 256), tt == 2 ? 1024 : 512);
+}
+
+// The rows that count, in order, by one workgroup, and how the kernels that
+// multiply with the head cut each pass.
+__device__ __forceinline__ void order_rows(const ManyArgs& a) {
+  constexpr int kRows = 4, kWaves = kHeadThreads / 64;  // rows of a thread at a time
+  __shared__ int sCount[kRows][kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int64_t total = 0;
+  for (int64_t n0 = 0; n0 < a.rows; n0 += kRows * kHeadThreads) {
+    uint64_t on[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t n = n0 + kHeadThreads * i + tid;
+      on[i] = __ballot(n < a.rows && (!a.weight || a.weight[n] != 0.0f));
+      if (lane == 0) sCount[i][wave] = __popcll(on[i]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t n = n0 + kHeadThreads * i + tid;
+      int64_t at = total + __popcll(on[i] & ((1ull << lane) - 1));
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        at += w < wave ? sCount[i][w] : 0;
+        total += sCount[i][w];
+      }
+      if (on[i] >> lane & 1) {
+        a.map[at] = (int32_t)n;
+        a.label[at] = a.labels[n];
+      } else if (n < a.rows) {
+        a.terms[n] = 0.0;
+        if (a.logp) a.logp[n] = 0.0f;
+      }
+    }
+    __syncthreads();
+  }
+  for (int p = tid; p < a.passes; p += kHeadThreads) {
+    const int64_t count = std::max<int64_t>(0, std::min(total - p * kChunkRows, kChunkRows));
+    const int tt = a.row_tiles ? a.row_tiles : exp_tiles((count + 31) / 32, a.b.D >= 256);
+    const int64_t tiles = std::max<int64_t>(1, (count + 32 * tt - 1) / (32 * tt) * ((a.b.D + 255) / 256));
+    const int64_t most = std::min(std::min<int64_t>(kMaxSplits, a.main_steps / 4),
+                                  std::min(main_groups(a.b.N, a.b.D, tt) / tiles, a.part_rows / std::max<int64_t>(count, 1)));
+    a.plan[4 * p] = (int32_t)count;
+    a.plan[4 * p + 1] = tt;
+    a.plan[4 * p + 2] = best_parts(count, a.b.D, a.main_steps / 4, tt, most);
+  }
+}
+
+// What waits for nothing.  Workgroup 0: order_rows.  The next kHeadParts: largest
+// |s_R|, |s_Ac|, |s_Aw| of a part of the vocabulary.  The next `arrange`: the A
+// codes in the order of the product along the vocabulary.  Those behind, for
+// rows that do not count: their gradient.
 __global__ __launch_bounds__(kHeadThreads) void xent_head_kernel(const ManyArgs a, int64_t arrange) {
   __shared__ float buf[kHeadThreads / 64][3];
-  if (blockIdx.x >= kHeadParts) {
-    const int64_t i = (int64_t)blockIdx.x - kHeadParts, n = i - arrange;
+  if (blockIdx.x == 0) return order_rows(a);
+  const int64_t part = (int64_t)blockIdx.x - 1;
+  if (part >= kHeadParts) {
+    const int64_t i = part - kHeadParts, n = i - arrange;
     if (n < 0)
       arrange_codes(a.b, i * kHeadThreads + threadIdx.x);
     else if (a.weight[n] == 0.0f)
@@ -404,7 +458,7 @@ __global__ __launch_bounds__(kHeadThreads) void xent_head_kernel(const ManyArgs 
     return;
   }
   float m[3] = {};
-  for (int64_t v = (int64_t)blockIdx.x * kHeadThreads + threadIdx.x; v < a.b.V; v += kHeadParts * kHeadThreads) {
+  for (int64_t v = part * kHeadThreads + threadIdx.x; v < a.b.V; v += kHeadParts * kHeadThreads) {
     float s[3];
     scales_of(a.b, v, s);
 #pragma unroll
@@ -419,79 +473,37 @@ __global__ __launch_bounds__(kHeadThreads) void xent_head_kernel(const ManyArgs 
   if (threadIdx.x < 3) {
     float t = buf[0][threadIdx.x];
     for (int w = 1; w < kHeadThreads / 64; ++w) t = fmaxf(t, buf[w][threadIdx.x]);
-    a.head_max[3 * blockIdx.x + threadIdx.x] = t;
+    a.head_max[3 * part + threadIdx.x] = t;
   }
 }
 
-// Workgroups of the product's launches, for any number of rows that count.
-__host__ __device__ inline int64_t main_groups(int64_t rows, int64_t D, int tt) {
-  return std::max<int64_t>((rows + 32 * tt - 1) / (32 * tt) * ((D + 255) / 256), tt == 2 ? 1024 : 512);
-}
-
-// Workgroup 0: the rows that count, in order, and how the kernels that multiply
-// with the head cut each pass.  The others: what the head's scales give.
-__global__ __launch_bounds__(kOrderThreads) void xent_order_kernel(const ManyArgs a) {
-  const int tid = threadIdx.x;
-  if (blockIdx.x > 0) {
-    // powers of two that bring the largest |q4 c8 s_R| (2040 at most before s_R)
-    // and the largest |s_A| to [2^14, 2^15) and [1/2, 1)
-    static_assert(kHeadParts == 64, "a part for each lane");
-    int k[3];
+// What the head's scales give: powers of two that bring the largest |q4 c8 s_R|
+// (2040 at most before s_R) and the largest |s_A| to [2^14, 2^15) and [1/2, 1),
+// and s_A times theirs, of entry i.  (An s_R below 2^-25 of the largest one loses
+// digits by that, 2^-40 of the largest weight.)
+__device__ __forceinline__ void head_scales(const ManyArgs& a, int64_t i) {
+  static_assert(kHeadParts == 64, "a part for each lane");
+  int k[3];
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      const float m = wave_max(a.head_max[3 * (tid & 63) + q]);
-      k[q] = std::max(-100, std::min(q == 0 ? row_exponent(2040.0f * m) : row_exponent(m) - 15, 100));
-    }
-    const int64_t i = ((int64_t)blockIdx.x - 1) * kOrderThreads + tid;
-    if (i < 4) a.scale[i] = ldexpf(1.0f, i == 0 ? k[0] : -k[i - 1]);
-    if (i < 16 * a.asteps)
+  for (int q = 0; q < 3; ++q) {
+    const float m = wave_max(a.head_max[3 * (threadIdx.x & 63) + q]);
+    k[q] = std::max(-100, std::min(q == 0 ? row_exponent(2040.0f * m) : row_exponent(m) - 15, 100));
+  }
+  if (i < 4) a.scale[i] = ldexpf(1.0f, i == 0 ? k[0] : -k[i - 1]);
+  if (i < 16 * a.asteps)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float s[3] = {};
-        if (i < a.b.V) scales_of(a.b, i, s);
-        a.scale_a[q * 16 * a.asteps + i] = (_Float16)ldexpf(s[1 + q], k[1 + q]);
-      }
-    return;
-  }
-  __shared__ int sCount[kOrderThreads];
-  const int64_t per = (a.rows + kOrderThreads - 1) / kOrderThreads, n0 = std::min(tid * per, a.rows), n1 = std::min(n0 + per, a.rows);
-  int mine = 0;
-  for (int64_t n = n0; n < n1; ++n) mine += !a.weight || a.weight[n] != 0.0f;
-  sCount[tid] = mine;
-  __syncthreads();
-  for (int o = 1; o < kOrderThreads; o *= 2) {  // inclusive sums
-    const int x = tid >= o ? sCount[tid - o] : 0;
-    __syncthreads();
-    sCount[tid] += x;
-    __syncthreads();
-  }
-  int at = sCount[tid] - mine;
-  for (int64_t n = n0; n < n1; ++n) {
-    if (!a.weight || a.weight[n] != 0.0f) {
-      a.map[at] = (int32_t)n;
-      a.label[at++] = a.labels[n];
-    } else {
-      a.terms[n] = 0.0;
-      if (a.logp) a.logp[n] = 0.0f;
+    for (int q = 0; q < 2; ++q) {
+      float s[3] = {};
+      if (i < a.b.V) scales_of(a.b, i, s);
+      a.scale_a[q * 16 * a.asteps + i] = (_Float16)ldexpf(s[1 + q], k[1 + q]);
     }
-  }
-  const int64_t total = sCount[kOrderThreads - 1];
-  for (int p = tid; p < a.passes; p += kOrderThreads) {
-    const int64_t count = std::max<int64_t>(0, std::min(total - p * kChunkRows, kChunkRows));
-    const int tt = a.row_tiles ? a.row_tiles : exp_tiles((count + 31) / 32, a.b.D >= 256);
-    const int64_t tiles = std::max<int64_t>(1, (count + 32 * tt - 1) / (32 * tt) * ((a.b.D + 255) / 256));
-    const int64_t most = std::min(std::min<int64_t>(kMaxSplits, a.b.ksteps / 4),
-                                  std::min(main_groups(a.b.N, a.b.D, tt) / tiles, a.part_rows / std::max<int64_t>(count, 1)));
-    a.plan[4 * p] = (int32_t)count;
-    a.plan[4 * p + 1] = tt;
-    a.plan[4 * p + 2] = best_parts(count, a.b.D, a.b.ksteps / 4, tt, most);
-  }
 }
 
 // Row blockIdx.x of the pass: its H (zeros behind the last one that counts),
-// and no sums.
+// and no sums.  Workgroups behind the rows: head_scales.
 __global__ __launch_bounds__(256) void xent_gather_kernel(const ManyArgs a) {
   const int64_t i = blockIdx.x, count = a.plan[4 * a.pass];
+  if (i >= a.b.n32) return head_scales(a, (i - a.b.n32) * 256 + threadIdx.x);
   if (threadIdx.x == 0) {
     a.ref[i] = -__builtin_huge_valf();
     a.sum[i] = 0.0;
@@ -1139,9 +1151,7 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
   if (int rc = tile_args(&h, &p, f)) return rc;
   const int tiles = b.nct + b.nwt;
   (void)hipGetLastError();  // start from a clean error state
-  b.ksteps = (int)a.asteps;
   const int64_t arrange = a.dH ? (tiles * a.asteps * 16 + kHeadThreads - 1) / kHeadThreads : 0;
-  hipLaunchKernelGGL(xent_head_kernel, dim3((unsigned)(kHeadParts + arrange + (a.dH && a.weight ? N : 0))), dim3(kHeadThreads), 0, s, a, arrange);
   // the launches that some number of rows that count may need (without weights it
   // is known): for each of 2, 4, 6 and 8 row tiles
   bool may[5] = {};
@@ -1151,11 +1161,12 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
   else
     for (int64_t t = a.weight ? 1 : L.n32 / 32; t <= L.n32 / 32; ++t) may[exp_tiles(t, d->D >= 256) / 2] = true;
   a.passes = L.passes;
-  b.ksteps = (int)(16 * L.piece);
-  hipLaunchKernelGGL(xent_order_kernel, dim3((unsigned)(1 + (16 * a.asteps + kOrderThreads - 1) / kOrderThreads)), dim3(kOrderThreads), 0, s, a);
+  a.main_steps = 16 * L.piece;
+  b.ksteps = (int)a.asteps;
+  hipLaunchKernelGGL(xent_head_kernel, dim3((unsigned)(1 + kHeadParts + arrange + (a.dH && a.weight ? N : 0))), dim3(kHeadThreads), 0, s, a, arrange);
   for (int pass = 0; pass < L.passes; ++pass) {
     a.pass = pass;
-    hipLaunchKernelGGL(xent_gather_kernel, dim3((unsigned)L.n32), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(xent_gather_kernel, dim3((unsigned)(L.n32 + (pass == 0 ? (16 * a.asteps + 255) / 256 : 0))), dim3(256), 0, s, a);
     if (launch_prep(f, s) != hipSuccess) return ARCHEAD_E_HIP;
     for (int64_t vt = 0; vt < L.vtiles; vt += L.piece) {
       const int64_t vn = std::min(L.piece, L.vtiles - vt);

@@ -288,6 +288,7 @@ SHARES = [
     (650, 384, 16, 0, 128, 500, 0.7), (650, 128, 0, 16, 64, 900, 0.95), (650, 512, 8, 8, 256, 1024, 0.02),
     (333, 128, 8, 8, 128, 1100, 0.5), (1500, 256, 160, 0, 64, 70, 0.8), (1500, 256, 0, 104, 64, 70, 1.0),
     (1500, 512, 72, 136, 32, 90, 1.0), (200, 128, 8, 8, 64, 4097, 1.0), (200, 128, 8, 8, 64, 8300, 0.4),
+    (300, 256, 8, 8, 64, 1500, 0.8), (260, 256, 8, 0, 256, 4500, 0.95), (20000, 256, 8, 8, 64, 500, 0.5),
 ]
 
 
