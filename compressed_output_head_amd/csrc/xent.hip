@@ -31,8 +31,8 @@
 // hold a workgroup's vocabulary rows over all columns, unpacked twice, between a
 // logit and its exponential.)  Many rows are bound by the MFMAs under the power
 // limit, two products of the head with the rows: 4096 rows, nine in ten of
-// which count, 9.3 ms, 4.8 in tile32_exp_kernel (0.96 PFLOP/s) and 4.1 in
-// xent_main_kernel (1.13), 0.7 in what joins the pieces.
+// which count, 9.1 to 9.3 ms, 4.8 in tile32_exp_kernel (0.96 PFLOP/s) and 3.9 to
+// 4.1 in xent_main_kernel (1.13), 0.7 in what joins the pieces.
 #include <algorithm>
 
 #include "backward_main.h"

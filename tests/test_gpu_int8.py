@@ -176,3 +176,16 @@ def test_from_the_residual_stream_to_logits(N, residual):
     W = np.abs(oracle.w_hat_alt(h)).sum(1)
     bound = f["scale"].double().cpu().numpy()[:, None] * (0.5 + 127 * 2.0 ** -8) * W * 1.0001
     assert (np.abs((Y - Y16).double().cpu().numpy()) <= bound).all()
+
+
+def test_offsets_past_32_bits():
+    """Logits of more than 2^31 elements in two passes: the last rows as in a
+    call of their own."""
+    torch, ah = torch_mod(), ah_mod()
+    V, D, N = 131071, 128, 16390
+    h, head = _head(8, V, D)
+    X, s = _codes(8, N, D)
+    Y = ah.archead_logits_int8(X, s, head, out_dtype=torch.bfloat16)
+    for rows in (slice(0, 3), slice(16380, 16384), slice(16384, N)):
+        alone = ah.archead_logits_int8(X[rows].contiguous(), s[rows].contiguous(), head, out_dtype=torch.bfloat16)
+        assert torch.equal(Y[rows], alone), rows

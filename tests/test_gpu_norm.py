@@ -286,3 +286,23 @@ def test_gradient_of_many_rows_in_place(D, N):
         args = {"dsum": dsum.clone(), "dh": dh.clone()}
         got = ah.archead_rmsnorm_backward(args["dh"], x, inv, weight=w, dsum=args["dsum"], dx=args[k])
         assert torch.equal(got["dx"], want["dx"]) and torch.equal(got["dweight"], want["dweight"]), k
+
+
+def test_offsets_past_32_bits():
+    """2^31 elements and more: the last rows as in a call of their own."""
+    torch, ah = torch_mod(), ah_mod()
+    N, D, last = (1 << 21) + 5, 1030, 7
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    block = torch.randn((4096, D), generator=gen, device="cuda").bfloat16()
+    x = block.repeat((N + 4095) // 4096, 1)[:N]
+    x[-last:] = torch.randn((last, D), generator=gen, device="cuda").bfloat16()
+    w = (1 + 0.3 * torch.randn(D, generator=gen, device="cuda")).bfloat16()
+    got = ah.archead_rmsnorm(x, weight=w, residual=x, outputs=("codes", "scale", "inv_rms"))
+    want = ah.archead_rmsnorm(x[-last:].clone(), weight=w, residual=x[-last:].clone(), outputs=("codes", "scale", "inv_rms"))
+    for k in want:
+        assert torch.equal(got[k][-last:], want[k]), k
+    del got["codes"]
+    dx = ah.archead_rmsnorm_backward(x, got["sum"], got["inv_rms"], weight=w, dx=x, with_dweight=False)["dx"]
+    assert torch.equal(dx[:4096], dx[4096:8192])  # the rows of the block, first and again
+    alone = ah.archead_rmsnorm_backward(want["sum"] * 0.5, want["sum"], want["inv_rms"], weight=w, with_dweight=False)["dx"]
+    assert torch.equal(dx[-last:], alone)  # x + x is twice x, exactly

@@ -343,3 +343,34 @@ def test_flat_and_huge_logits(N):
         labels[-1] = V - 1
         got = ah.archead_cross_entropy(H, torch.from_numpy(labels).int().cuda(), head)
         _check(got, H, labels, None, h, 1.0, f"spread {spread} N={N}")
+
+
+def test_graphs_that_share_a_workspace():
+    """Few and many rows captured on one workspace, replayed in turn between
+    eager calls."""
+    torch, ah = torch_mod(), ah_mod()
+    V, D = 3000, 512
+    h, head = _head(41, V, D, 8, 8, 64)
+    W = oracle.w_hat(h)
+    sets = []
+    for N in (20, 150, 700):
+        labels = np.random.default_rng(N).integers(0, V, N)
+        sets.append((_hidden(N, N, D, W, labels), torch.from_numpy(labels).int().cuda(), torch.rand(N, device="cuda")))
+    need = max(ah.archead_cross_entropy_workspace_bytes(V, D, 8, 8, 64, len(H)) for H, _, _ in sets)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    run = lambda i: ah.archead_cross_entropy(*sets[i][:2], head, weight=sets[i][2], workspace=ws)  # noqa: E731
+    want = [run(i) for i in range(3)]
+    torch.cuda.synchronize()
+    graphs, held = [], []
+    for i in range(3):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            held.append(run(i))
+    for i in (0, 1, 2, 1, 0, 2, 2, 0):
+        for t in held[i].values():
+            t.fill_(float("nan"))
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        for k in want[i]:
+            assert torch.equal(held[i][k], want[i][k]), (i, k)
+        run((i + 1) % 3)
