@@ -1203,13 +1203,14 @@ int launch_many_rows(const archead_tensor* H, const archead_packed_head* head, c
       if (may[4]) launch_xent_main<8>(b, me, s);
     }
     hipLaunchKernelGGL(xent_rows_kernel, dim3((unsigned)L.rows), dim3(256), 0, s, a);
-    if (a.dH)
+    if (a.dH) {
       // where tiles are few, four waves share one: 64, 500, 1000 and 2000 rows of 4096
       // columns take 14, 20, 34 and 49 us, with a wave each 26, 23, 27 and 39
       if (L.n32 / 32 * b.nkt < 1024)
         hipLaunchKernelGGL(xent_finish_kernel<true>, dim3((unsigned)(L.n32 / 32), (unsigned)b.nkt), dim3(kFinishThreads), 0, s, a);
       else
         hipLaunchKernelGGL(xent_finish_kernel<false>, dim3((unsigned)(L.n32 / 32), (unsigned)((b.nkt + 3) / 4)), dim3(kFinishThreads), 0, s, a);
+    }
     if (hipGetLastError() != hipSuccess) return ARCHEAD_E_HIP;
   }
   return ARCHEAD_OK;
