@@ -34,6 +34,7 @@
 // which count, 9.1 to 9.3 ms, 4.8 in tile32_exp_kernel (0.96 PFLOP/s) and 3.9 to
 // 4.1 in xent_main_kernel (1.13), 0.7 in what joins the pieces.
 #include <algorithm>
+#include <limits>
 
 #include "backward_main.h"
 #include "device_common.h"
@@ -68,7 +69,7 @@ struct XentArgs {
   int64_t y_stride;
   const int32_t* labels;
   const float* weight;
-  float tau, c_hi, c_lo;  // log2(e) tau = c_hi + c_lo
+  float tau, c_hi, c_lo;  // log2(e) tau = c_hi + c_lo, both above zero
   float* logp;            // or null
   uint16_t* dH;           // or null
   int64_t dh_stride;
@@ -92,11 +93,17 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-// exp(z - m) of a logit: differences before the scale, so that nothing overflows
+// exp(z - m) of a logit: differences before the scale, so that nothing
+// overflows.  The difference is -inf of a logit that is: both products are -inf
+// then and the result 0, as neither part of the scale is negative or zero.
 __device__ __forceinline__ float exp_of(const XentArgs& a, float y, float m) {
   const float d = y - m;
   return __builtin_amdgcn_exp2f(fmaf(d, a.c_hi, d * a.c_lo));
 }
+
+// What exponentials are taken relative to where the maximum is m: of no logit
+// above -inf any number, so that they are 0 (and NaN of a NaN).
+__device__ __forceinline__ float base_of(float m) { return m == -__builtin_huge_valf() ? 0.0f : m; }
 
 // The scales of vocabulary row v: s_R, and s_Ac, s_Aw of the parts that there are.
 __device__ __forceinline__ void scales_of(const BwdArgs& b, int64_t v, float (&s)[3]) {
@@ -140,6 +147,7 @@ __global__ __launch_bounds__(kPieceThreads) void xent_pieces_kernel(const XentAr
   __syncthreads();
   m = fmaxf(fmaxf(buf[0][0], buf[1][0]), fmaxf(buf[2][0], buf[3][0]));
   __syncthreads();
+  const float base = base_of(m);
   float sum = 0.0f, top[3] = {};
   for (int64_t v = v0 + 4 * threadIdx.x; v < v1; v += 4 * kPieceThreads) {
     const f4 x = load4(v);
@@ -147,7 +155,7 @@ __global__ __launch_bounds__(kPieceThreads) void xent_pieces_kernel(const XentAr
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (v + j >= v1 || v + j == label) continue;
-      const float e = exp_of(a, x[j], m);
+      const float e = exp_of(a, x[j], base);
       float s[3];
       scales_of(a.b, v + j, s);
       part += e;
@@ -197,11 +205,11 @@ __global__ __launch_bounds__(kOperandThreads) void xent_operand_kernel(const Xen
     for (int o = lanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
     if (on)
       for (int p = lane; p < a.pieces; p += lanes) {
-        if (piece[p].m == -infinity && m != -infinity) {  // no entry, or none above -inf
+        if (piece[p].m == -infinity) {  // no entry, or none above -inf
           s += (double)piece[p].s;
           continue;
         }
-        const float f = m == -infinity ? 1.0f : exp_of(a, piece[p].m, m);
+        const float f = exp_of(a, piece[p].m, m);
         s += (double)piece[p].s * (double)f;
 #pragma unroll
         for (int q = 0; q < 3; ++q) top[q] = fmaxf(top[q], piece[p].top[q] * f);
@@ -212,7 +220,7 @@ __global__ __launch_bounds__(kOperandThreads) void xent_operand_kernel(const Xen
       for (int q = 0; q < 3; ++q) top[q] = fmaxf(top[q], __shfl_xor(top[q], o));
     }
     if (lane == 0) {
-      sM[n] = m;
+      sM[n] = base_of(m);
 #pragma unroll
       for (int q = 0; q < 3; ++q) sP[q][n] = ldexpf(1.0f, std::min(row_exponent(top[q]), 126));
       if (blockIdx.x == 0 && n < N) {
@@ -956,11 +964,16 @@ void set_head(const archead_packed_head* head, BwdArgs& b) {
   b.b_scales = reinterpret_cast<const uint16_t*>(buf + P.b_scales.offset);
 }
 
-// log2(e) tau as a pair of fp32 numbers
+// log2(e) tau as a pair of fp32 numbers.  The first is the nearest one where
+// that lies below, else the one before it, so that the second is above zero as
+// well; at the ends of fp32's range both stay in it.
 void set_exponent(float tau, float& hi, float& lo) {
+  constexpr float kLeast = std::numeric_limits<float>::denorm_min(), kMost = std::numeric_limits<float>::max();
   const double c = 1.4426950408889634 * (double)tau;
-  hi = (float)c;
-  lo = (float)(c - (double)hi);
+  hi = (float)std::min(c, (double)kMost);
+  if ((double)hi >= c) hi = nextafterf(hi, 0.0f);
+  hi = std::max(hi, kLeast);
+  lo = std::max((float)(c - (double)hi), kLeast);
 }
 
 int launch_few_rows(const archead_tensor* H, const archead_packed_head* head, const archead_cross_entropy_inputs* in,

@@ -637,9 +637,10 @@ ARCHEAD_API int archead_logits_backward(const archead_tensor* dY, const archead_
  *   log p_n = log softmax(inv_temperature Y_n)[labels[n]],  Y = H W_hat^T
  *   loss    = -sum_n weight[n] log p_n
  * Rows of weight 0 do not count: their H may hold anything, their labels too;
- * their log p and gradient are 0.  A row that counts with a label outside
- * [0, V), or with logits that are not finite, has log p and gradient NaN, and
- * so has the loss; it changes no other row. */
+ * their log p and gradient are 0.  A row that counts has log p and gradient NaN,
+ * and so has the loss, if its label is outside [0, V) or the label's logit not
+ * finite, or another logit is NaN or +inf; it changes no other row.  (A logit is
+ * -inf where the product leaves fp32 downwards: probability 0.) */
 typedef struct {
   const int32_t* labels;
   const float* weight;   /* NULL: 1 for every row */
