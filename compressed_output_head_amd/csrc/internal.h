@@ -141,13 +141,11 @@ struct FwdArgs {
 // The exponentials' epilogue (tile32_exp_kernel): the logits of a piece of the
 // vocabulary, whole 256-row tiles [vt0, vt0 + vtiles), leave as operands of the
 // products that follow, and as what the softmax's sum needs of them.  An
-// operand is 2^(z - B + kExpTop) in fp16, z = log2(e) times the scaled logit and
-// B a whole number: the row's exponent from the pieces before where none of its
-// z in the 32-row block exceeds that by more than 1, else the least that none
-// exceeds.  So blocks differ by exact powers of two, nearly always by none.  An
-// operand is at most 2^15 and off by half a step, 2^-11 of itself, or below
-// 2^-14 by 2^-25.
-constexpr int kExpTop = 14;
+// operand is 2^(z - E) in fp16, z = log2(e) times the scaled logit and E, of each
+// row and 32-row block, what exp_exponent gives of the row's running one and
+// the block's largest z.  So blocks differ by exact powers of two, nearly always
+// by none.  An operand is at most 2^15 and off by half a step, 2^-11 of itself,
+// or below 2^-14 by 2^-25.
 struct T32Exp {
   const int32_t* plan;    // {rows of H that count, 32-row tiles of a workgroup}; N and n32 of FwdArgs are the most there can be
   const int32_t* labels;  // [N] by row of H
@@ -157,7 +155,7 @@ struct T32Exp {
                           // 16 step + 8 (l / 32) .. + 8 of the piece
   int steps;              // at least 16 vtiles
   const float* ref;       // [n32] the rows' exponents (-inf: none yet)
-  float* stat;            // [8 vtiles][n32][2] by 32-row block: B, the sum of the operands before rounding
+  float* stat;            // [8 vtiles][n32][2] by 32-row block: E, the sum of the operands before rounding
   float* z_label;         // [n32] the label's z, written where it is met
 };
 

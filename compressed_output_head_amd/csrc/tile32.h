@@ -7,6 +7,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "exp_range.h"
 #include "internal.h"
 #include "rowstat.h"
 
@@ -139,11 +140,11 @@ __device__ __forceinline__ void lds_copy16(__amdgpu_buffer_rsrc_t rs, void* dst,
 // ST: instead of storing Y, each workgroup reduces its 256 logits of every
 // token to a row-statistics piece, written to a.st_part[token][vt].
 // EX: instead of storing Y, the exponentials' epilogue, on the tiles of the rows
-// that count: e = 2^(z - B + 14) in fp16 as operands of the product with the
-// head, B the row's exponent rounded up over 32 vocabulary entries or its running
-// one if that is above (or less than 1 below), with B and the sum for each row
-// and block.  3690 rows of a 151936 x 4096 head take 4.8 ms, 0.96 PFLOP/s with the
-// MFMAs busy 56% of the clock that the power limit leaves.
+// that count: e = 2^(z - E) in fp16 as operands of the product with the head, E
+// the row's running exponent or one for these 32 vocabulary entries (exp_range.h),
+// with E and the sum for each row and block.  3690 rows of a 151936 x 4096 head
+// take 4.8 ms, 0.96 PFLOP/s with the MFMAs busy 56% of the clock that the power
+// limit leaves.
 template <int GC, int TT, bool ST, bool EX>
 __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp, const T32Exp& ex) {
   constexpr int kT32TT = TT, kT32MT = TT;     // token tiles per workgroup and per wave
@@ -572,8 +573,7 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
       for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
       top = fmaxf(top, __shfl_xor(top, 32));
       // no entry, or none above -inf: operands of 0 (a row that is not finite shows in its sum)
-      const float M = ceilf(top), ref = sRef[32 * m + c32];
-      const float B = M <= ref + 1.0f ? ref : M, low = B == -infinity ? 0.0f : B - (float)kExpTop;
+      const float E = exp_exponent(ceilf(top), sRef[32 * m + c32]), low = E == -infinity ? 0.0f : E;
       float sum = 0.0f;
       uint32_t pk[8];
 #pragma unroll
@@ -584,7 +584,7 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
       }
       sum += __shfl_xor(sum, 32);
       const int64_t tok = 32 * (int64_t)(tt0 + m) + c32;
-      if (g == 0) reinterpret_cast<u2*>(ex.stat)[(int64_t)blk * a.n32 + tok] = u2{__float_as_uint(B), __float_as_uint(sum)};
+      if (g == 0) reinterpret_cast<u2*>(ex.stat)[(int64_t)blk * a.n32 + tok] = u2{__float_as_uint(E), __float_as_uint(sum)};
       if (!ex.e) return;
       // lane halves hold the two fours of each eight rows; a fragment wants eights in one lane
       u4* out = reinterpret_cast<u4*>(ex.e) + ((int64_t)(tt0 + m) * ex.steps + 2 * blk) * 64 + lane;

@@ -553,7 +553,7 @@ __global__ __launch_bounds__(kMergeRows * kMergeSlices) void xent_merge_kernel(c
     m = t;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (k0 + i * kMergeSlices < a.blocks) {  // (2^-149 is nothing here: the largest is 2^10 at least)
+      if (k0 + i * kMergeSlices < a.blocks) {  // (2^-149 is nothing beside the largest, 2^-8 at least)
         const float y = __uint_as_float(x[i][1]), j = m - __uint_as_float(x[i][0]);
         s += (double)(j <= 1000.0f ? ldexpf(y, -(int)j) : y == y ? 0.0f : y);
       }
@@ -766,7 +766,7 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(const ManyArgs a) {
     if (!(fabsf(zl) < __builtin_huge_valf())) {
       logp = q = __builtin_nan("");
     } else if (s != 0.0) {  // (a vocabulary of one entry: p = 1)
-      const double d = log(s) + ((double)a.ref[i] - kExpTop - (double)zl) * 0.6931471805599453;
+      const double d = log(s) + ((double)a.ref[i] - (double)zl) * 0.6931471805599453;
       logp = d == d ? -(fmax(d, 0.0) + log1p(exp(-fabs(d)))) : d;
       q = 1.0 / (1.0 + exp(-d));
       out.mean = (float)(1.0 / s);

@@ -640,7 +640,9 @@ ARCHEAD_API int archead_logits_backward(const archead_tensor* dY, const archead_
  * their log p and gradient are 0.  A row that counts has log p and gradient NaN,
  * and so has the loss, if its label is outside [0, V) or the label's logit not
  * finite, or another logit is NaN or +inf; it changes no other row.  (A logit is
- * -inf where the product leaves fp32 downwards: probability 0.) */
+ * -inf where the product leaves fp32 downwards: probability 0.)  Up to 32 rows
+ * differences of logits are scaled; of more the logits are, in fp32, by log2(e)
+ * inv_temperature, and the same holds for what that gives. */
 typedef struct {
   const int32_t* labels;
   const float* weight;   /* NULL: 1 for every row */
