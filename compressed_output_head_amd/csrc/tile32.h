@@ -129,6 +129,10 @@ __device__ __forceinline__ void lds_copy16(__amdgpu_buffer_rsrc_t rs, void* dst,
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 16, voff, soff, 0, 0);
 }
 
+// EX: a power of two of the scale that goes with the head's scales in place of
+// the row's, which alone would leave fp32 at inverse temperatures near its end.
+constexpr float kExpShare = 4294967296.0f;
+
 // GC: group codes per k-tile and row that one stage needs: 0 -> one (g >= 128),
 // 1 -> two (g = 64), 2 -> four (g = 32)
 // The H ring is four separate LDS arrays, one per slot, chosen at compile
@@ -364,8 +368,8 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
     sTok[tid][0] = a.hscale[tok];
     sTok[tid][1] = part == 0 ? a.zscale[tok] : 0.0f;  // the low-rank term goes with part 0 only
     if constexpr (EX) {
-      sTok[tid][0] = (float)(ex.c * (double)a.hscale[tok]);
-      sTok[tid][1] = (float)(ex.c * (double)a.zscale[tok]);
+      sTok[tid][0] = (float)(ex.c / kExpShare * (double)a.hscale[tok]);
+      sTok[tid][1] = (float)(ex.c / kExpShare * (double)a.zscale[tok]);
     }
     if constexpr (ST) sTgt[tid] = a.targets && 32 * (int64_t)tt0 + tid < a.N ? a.targets[32 * (int64_t)tt0 + tid] : -1;
     if constexpr (EX) {
@@ -380,6 +384,11 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
     sVR[tid] = f16_to_f32(a.r_rowscale[v]);
     sVC[tid] = a.r_c > 0 ? f16_to_f32(a.a_scales[v * a.nA]) : 0.0f;
     sVW[tid] = a.r_r > 0 ? f16_to_f32(a.a_scales[v * a.nA + a.nA - 1]) : 0.0f;
+    if constexpr (EX) {
+      sVR[tid] *= kExpShare;
+      sVC[tid] *= kExpShare;
+      sVW[tid] *= kExpShare;
+    }
   }
 
   // group codes of this lane's rows for one stage: the code of MFMA step t
@@ -536,7 +545,7 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
           p = mfma32(av, zf[(2 * s + 1) * 64], p);
         }
       }
-      const float hs = sTok[32 * m + c32][0], zs = sTok[32 * m + c32][1];  // times ex.c
+      const float hs = sTok[32 * m + c32][0], zs = sTok[32 * m + c32][1];  // times ex.c / kExpShare
       const int label = sTgt[32 * m + c32];
       float z[16];
 #pragma unroll

@@ -91,7 +91,7 @@ def _run(N, V, D, tau, exponent, w):
 # log2(e) inv_temperature times the largest logit from 2^22 to 2^31, across the whole range, and by
 # the logits' own size
 SCALES = [(1e5, 0), (6e5, 0), (1e6, 0), (2.0 ** 20, 0), (3e6, 0), (1e7, 0), (1e8, 0), (1.0, 22), (0.7, 26), (1e30, 0),
-          (2e-20, 90)]
+          (3e38, -60), (2e-20, 90)]
 
 
 @pytest.mark.parametrize("tau,exponent", SCALES)
@@ -103,3 +103,21 @@ def test_huge_scaled_logits(N, tau, exponent):
 @pytest.mark.parametrize("tau", [1e6, 1e8])
 def test_huge_scaled_logits_in_pieces_of_the_vocabulary(tau):
     _run(2100, 70001, 128, tau, 0, 1.0)
+
+
+def test_scaled_logits_past_the_range_of_fp32():
+    """Up to 32 rows differences are scaled, else the logits: rows in which a
+    scaled logit is infinite are NaN then, and no other row is."""
+    torch, ah = torch_mod(), ah_mod()
+    h, W, kind, H, labels, _ = _case(1, 40, 1003, 256, 0)
+    head = ah.PackedHead.from_components(h)
+    H[::2] *= 2.0 ** -20
+    lab = torch.from_numpy(labels).int().cuda()
+    X = torch.from_numpy(H).cuda().bfloat16()
+    many = ah.archead_cross_entropy(X, lab, head, weight=torch.full((40,), 2.0 ** -60, device="cuda"), inv_temperature=3e38)
+    few = ah.archead_cross_entropy(X[:32], lab[:32], head, weight=torch.full((32,), 2.0 ** -60, device="cuda"),
+                                   inv_temperature=3e38)
+    bad = torch.arange(40, device="cuda") % 2 == 1
+    assert torch.isnan(many["logp"][bad]).all() and torch.isnan(many["dH"][bad]).all()
+    assert not torch.isnan(many["logp"][~bad]).any() and not torch.isnan(many["dH"][~bad]).any()
+    assert not torch.isnan(few["logp"]).any() and not torch.isnan(few["dH"]).any()
