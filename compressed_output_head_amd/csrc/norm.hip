@@ -218,26 +218,28 @@ struct GradOctet {
     d = load8(a.dh + n * a.dh_stride, v, a.D);
     e = a.dsum ? load8(a.dsum + n * a.ds_stride, v, a.D) : u4{};
   }
-  __device__ __forceinline__ float dot(const u4& w) const {
+  // sum of g s inv: s inv is at most sqrt(D), where s may be at the end of fp32
+  __device__ __forceinline__ float dot(const u4& w, float inv) const {
     float sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum = fmaf(at(d, j) * at(w, j), at(s, j), sum);
+    for (int j = 0; j < 8; ++j) sum = fmaf(at(d, j) * at(w, j), at(s, j) * inv, sum);
     return sum;
   }
-  // dx, and what the octet adds to dweight
+  // dx, with c the row's mean of g s inv, and what the octet adds to dweight
   __device__ __forceinline__ u4 apply(const u4& w, float inv, float c, float (&dw)[8]) const {
     float y[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      y[j] = fmaf(inv, at(d, j) * at(w, j) - at(s, j) * c, at(e, j));
-      dw[j] = fmaf(at(d, j), at(s, j) * inv, dw[j]);
+      const float unit = at(s, j) * inv;
+      y[j] = fmaf(inv, at(d, j) * at(w, j) - unit * c, at(e, j));
+      dw[j] = fmaf(at(d, j), unit, dw[j]);
     }
     return pack8(y);
   }
 };
 
-// dx = dsum + inv (g - s inv^2 sum_d(g s) / D), g = w dh, and part p of
-// dweight = sum_n dh s inv: row slot p takes the rows p, p + parts, ..., its
+// dx = dsum + inv (g - u sum_d(g u) / D), g = w dh, u = s inv, and part p of
+// dweight = sum_n dh u: row slot p takes the rows p, p + parts, ..., its
 // threads the same columns of all of them.  The next row is on its way while
 // one is worked on; rows too long for that (K > 2) are read again for dx, from
 // the cache, and their threads hold the sums of dweight in LDS.
@@ -250,11 +252,11 @@ __global__ __launch_bounds__(norm_threads(T)) void rmsnorm_backward_kernel(const
   if (p >= a.parts) return;
   auto column = [&](int k) { return 8 * (int64_t)(t0 + T * k); };
   auto weight = [&](int k) { return a.weight ? load8(a.weight, column(k), a.D) : u4{kOnes, kOnes, kOnes, kOnes}; };
-  auto finish = [&](double dot, float inv) {
+  auto finish = [&](double dot) {
     uint32_t none = 0;
     if constexpr (T > 64) __syncthreads();  // the row before is done with the reduction's memory
     row_reduce<T>(dot, none);
-    return (float)(dot * (double)inv * (double)inv / (double)a.D);
+    return (float)(dot / (double)a.D);
   };
   if constexpr (kHeld) {
     u4 w[K];
@@ -278,8 +280,8 @@ __global__ __launch_bounds__(norm_threads(T)) void rmsnorm_backward_kernel(const
       }
       double dot = 0.0;
 #pragma unroll
-      for (int k = 0; k < K; ++k) dot += (double)row[k].dot(w[k]);
-      const float c = finish(dot, inv);
+      for (int k = 0; k < K; ++k) dot += (double)row[k].dot(w[k], inv);
+      const float c = finish(dot);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         // new values to the compiler: it would keep the products and the
@@ -306,9 +308,9 @@ __global__ __launch_bounds__(norm_threads(T)) void rmsnorm_backward_kernel(const
       for (int k = 0; k < K; ++k) {
         GradOctet x;
         x.load(a, n, column(k));
-        dot += (double)x.dot(weight(k));
+        dot += (double)x.dot(weight(k), inv);
       }
-      const float c = finish(dot, inv);
+      const float c = finish(dot);
 #pragma unroll 1
       for (int k = 0; k < K; ++k) {
         GradOctet x;

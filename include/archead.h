@@ -723,7 +723,9 @@ ARCHEAD_API int archead_rmsnorm(const archead_rmsnorm_inputs* in, const archead_
  *   dx = dsum + inv (g - s inv^2 sum_d(g s) / D),  g = w dh
  *   dweight_d = sum_n dh s inv
  * dx is the gradient of x and of the residual alike.  (Of the 8-bit output it
- * is the gradient that takes the rounding as the identity.) */
+ * is the gradient that takes the rounding as the identity.)  Rows of s of any
+ * size; products w dh below 2^116, so that eight of them times s inv, which is
+ * at most sqrt(D), stay in fp32. */
 typedef struct {
   const archead_tensor* dh;   /* bf16 [N][D] */
   const archead_tensor* sum;  /* bf16 [N][D] s */
