@@ -94,6 +94,13 @@ __device__ __forceinline__ u4 pack8(const float (&y)[8]) {
   const u2 lo = pack_bf16x4(y[0], y[1], y[2], y[3]), hi = pack_bf16x4(y[4], y[5], y[6], y[7]);
   return u4{lo[0], lo[1], hi[0], hi[1]};
 }
+// x + r, rounded to bf16
+__device__ __forceinline__ u4 add8(u4 x, u4 r) {
+  float y[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = at(x, j) + at(r, j);
+  return pack8(y);
+}
 constexpr uint32_t kOnes = 0x3f803f80u;  // two bf16 ones
 
 // Sum (in a fixed order) and largest of a row's threads, given to all of them.
@@ -126,8 +133,9 @@ __device__ __forceinline__ void row_reduce(double& sum, uint32_t& top) {
 
 constexpr int norm_threads(int T) { return T < 256 ? 256 : T; }
 
-// T threads a row, K octets of columns each.
-template <int T, int K>
+// T threads a row, K octets of columns each; kH: h is wanted.  (Calls for codes
+// alone in a kernel of their own: beside h they take 4% longer, 4096 rows of 8192.)
+template <int T, int K, bool kH>
 __global__ __launch_bounds__(norm_threads(T)) void rmsnorm_kernel(const NormArgs a) {
   constexpr int kRows = norm_threads(T) / T;
   const int t0 = threadIdx.x % T;
@@ -145,12 +153,7 @@ __global__ __launch_bounds__(norm_threads(T)) void rmsnorm_kernel(const NormArgs
 #pragma unroll
     for (int k = 0; k < K; ++k) r[k] = load8(a.residual + n * a.r_stride, 8 * (int64_t)(t0 + T * k), a.D);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float y[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = at(s[k], j) + at(r[k], j);
-      s[k] = pack8(y);
-    }
+    for (int k = 0; k < K; ++k) s[k] = add8(s[k], r[k]);
   }
   if (a.sum) {
 #pragma unroll
@@ -176,15 +179,6 @@ __global__ __launch_bounds__(norm_threads(T)) void rmsnorm_kernel(const NormArgs
     if (a.inv_rms) a.inv_rms[n] = inv32;
     if (a.scale) a.scale[n] = finite ? (float)((double)m * inv / 127.0) : __builtin_nanf("");
   }
-  if (a.h) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float y[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = at(s[k], j) * at(w[k], j) * inv32;
-      store8(a.h + n * a.h_stride, 8 * (int64_t)(t0 + T * k), a.D, pack8(y));
-    }
-  }
   if (a.codes) {
     const double step = finite && m > 0.0f ? 127.0 / (double)m : 0.0;
 #pragma unroll
@@ -206,6 +200,41 @@ __global__ __launch_bounds__(norm_threads(T)) void rmsnorm_kernel(const NormArgs
         for (int j = 0; j < 8; ++j)
           if (v + j < a.D) row[v + j] = (int8_t)(c[j >> 2] >> (8 * (j & 3)));
       }
+    }
+  }
+  if constexpr (!kH) return;
+  if (top < 0x7f800000u && inv <= 32768.0) {
+    // (a product below 2^-126 is off by 2^-150, and h by 2^-135: nothing)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = at(s[k], j) * at(w[k], j) * inv32;
+      store8(a.h + n * a.h_stride, 8 * (int64_t)(t0 + T * k), a.D, pack8(y));
+    }
+  } else {
+    // s w leaves fp32 where h may not: (s 2^e w) (inv 2^-e), the factor in [1, 2),
+    // leaves it where h does.  (s 2^e is exact: where it is subnormal s is 2^-126
+    // of the row's mean.)  The row is read again, from the sum where that may
+    // stand in the place of x or the residual by now, so that rows as above need
+    // not hold s and w beside their products.  inv is 0 or NaN of a row that is
+    // not finite.
+    int e = 0;
+    float power = inv32, factor = 1.0f;
+    if (inv > 0.0) {
+      factor = (float)(2.0 * frexp(inv, &e));
+      power = ldexpf(1.0f, e - 1);
+    }
+#pragma unroll 1
+    for (int k = 0; k < K; ++k) {
+      const int64_t v = 8 * (int64_t)(t0 + T * k);
+      u4 x = a.sum ? load8(a.sum + n * a.sum_stride, v, a.D) : load8(a.x + n * a.x_stride, v, a.D);
+      if (a.residual && !a.sum) x = add8(x, load8(a.residual + n * a.r_stride, v, a.D));
+      const u4 g = a.weight ? load8(a.weight, v, a.D) : u4{kOnes, kOnes, kOnes, kOnes};
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = at(x, j) * power * at(g, j) * factor;
+      store8(a.h + n * a.h_stride, v, a.D, pack8(y));
     }
   }
 }
@@ -488,8 +517,12 @@ int archead_rmsnorm(const archead_rmsnorm_inputs* in, const archead_rmsnorm_outp
   (void)hipGetLastError();  // start from a clean error state
   norm_width(D, [&](auto w) {
     constexpr int T = decltype(w)::T, K = decltype(w)::K, kRows = norm_threads(T) / T;
-    hipLaunchKernelGGL((rmsnorm_kernel<T, K>), dim3((unsigned)((N + kRows - 1) / kRows)), dim3(norm_threads(T)), 0,
-                       static_cast<hipStream_t>(stream), a);
+    const dim3 grid((unsigned)((N + kRows - 1) / kRows)), block(norm_threads(T));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (a.h)
+      hipLaunchKernelGGL((rmsnorm_kernel<T, K, true>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((rmsnorm_kernel<T, K, false>), grid, block, 0, s, a);
   });
   return hipGetLastError() == hipSuccess ? ARCHEAD_OK : ARCHEAD_E_HIP;
 }

@@ -703,10 +703,10 @@ typedef struct {
  *   scale[n]    = m inv / 127, so codes times scale is h; a row of zeros has
  *                 codes and scale 0
  * Products t are fp32 (exact but for under- and overflow); sums of squares
- * fp64.  A row with a t or an s that is not finite has scale NaN and codes 0,
- * and its h is what the formula gives; it changes no other row.  sum and h
- * may replace x or residual row for row (same data and stride); outputs may
- * share bytes with nothing else (E_SHAPE). */
+ * fp64.  A row with a t or an s that is not finite has scale NaN and codes 0;
+ * its h is what the formula gives all the same, also where t leaves fp32 and
+ * s inv w does not.  Such a row changes no other one.  sum and h may replace x or residual row for row (same
+ * data and stride); outputs may share bytes with nothing else (E_SHAPE). */
 typedef struct {
   const archead_tensor* sum;   /* bf16 [N][D] s */
   const archead_tensor* h;     /* bf16 [N][D] */
