@@ -1,7 +1,8 @@
 // Logits of INT8 hidden states through a row-INT8 head (archead_logits_int8):
-//   Y[n, v] = (sum_k X[n, k] q8[v, k]) (scale[n] s[v]),
+//   Y[n, v] = (sum_k X[n, k] q8[v, k]) s[v] scale[n],
 // on the 8-bit integer MFMA: products and sums are exact (|sum| <= 2^14 D, D
-// up to 65536), and only the scales round.
+// up to 65536), and only the scales round: the row's first, as a sum times an fp16
+// number stays within 2^-24 and 2^46, where two scales alone may leave fp32.
 //
 // The head is stored for fp16 operands (tile (b, kt), lane l: row l % 16,
 // columns 32 s + 8 (l / 16) + P[p], byte 8 s + p).  A sum may take its terms in
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void i8_few_kernel(const I8Args a) 
     if (t < N) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (v0 + e < a.V) put(a, t, v0 + e, (float)acc[e] * (ts * f16_to_f32(a.rowscale[v0 + e])));
+        if (v0 + e < a.V) put(a, t, v0 + e, (float)acc[e] * f16_to_f32(a.rowscale[v0 + e]) * ts);
     }
   }
 }
@@ -325,7 +326,7 @@ __global__ __launch_bounds__(64 * WM * WN, WCB == 2 ? 2 : 4) void i8_tile_kernel
       for (int e = 0; e < 16; ++e) {
         const int tl = 32 * (MT * wm + m) + 8 * (e >> 2) + 4 * half + (e & 3);
         const int64_t n = 32 * (int64_t)tile0 + tl;
-        if (n < a.N && v < a.V) put(a, n, v, (float)acc[m][cb][e] * (sTok[tl] * s));
+        if (n < a.N && v < a.V) put(a, n, v, (float)acc[m][cb][e] * s * sTok[tl]);
       }
   }
 }

@@ -705,8 +705,9 @@ typedef struct {
  * Products t are fp32 (exact but for under- and overflow); sums of squares
  * fp64.  A row with a t or an s that is not finite has scale NaN and codes 0;
  * its h is what the formula gives all the same, also where t leaves fp32 and
- * s inv w does not.  Such a row changes no other one.  sum and h may replace x or residual row for row (same
- * data and stride); outputs may share bytes with nothing else (E_SHAPE). */
+ * s inv w does not.  Such a row changes no other one.  sum and h may replace x
+ * or residual row for row (same data and stride); outputs may share bytes with
+ * nothing else (E_SHAPE). */
 typedef struct {
   const archead_tensor* sum;   /* bf16 [N][D] s */
   const archead_tensor* h;     /* bf16 [N][D] */
@@ -761,9 +762,9 @@ ARCHEAD_API int archead_logits_int8_workspace_bytes(const archead_dims* d, int64
 /* Y = diag(scale) X W_hat^T: the logits of INT8 hidden states (codes X and a
  * scale for each token) through an ARCHEAD_FMT_ROW_INT8 head (codes and a scale
  * for each row of the vocabulary), as a product of 8-bit integers:
- *   Y[n, v] = (sum_k X[n, k] q8[v, k]) (scale[n] s[v])
- * with exact int32 sums, the scales applied in fp32, rounded once more for
- * bf16.
+ *   Y[n, v] = (sum_k X[n, k] q8[v, k]) s[v] scale[n]
+ * with exact int32 sums, the scales applied in fp32 in this order (the first
+ * product never leaves its range), rounded once more for bf16.
  *   X: ARCHEAD_I8 [N][D] device tensor, any codes, rows 16-byte aligned.
  *   scale: device fp32 [N].  Any values: one that is not finite gives a row of
  *       Y that is not, and changes no other.
