@@ -257,7 +257,9 @@ __global__ __launch_bounds__(64 * WM * WN, WCB == 2 ? 2 : 4) void i8_tile_kernel
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2>;
   using I3 = std::integral_constant<int, 3>;
+  // in this order, which the first barrier's count is of
   load_h(0, I0{});
+  __builtin_amdgcn_sched_barrier(0);
   load_w4(0, I0{});
   load_h(1, I1{});
   load_w4(1, I1{});
@@ -284,8 +286,11 @@ __global__ __launch_bounds__(64 * WM * WN, WCB == 2 ? 2 : 4) void i8_tile_kernel
   };
   ring_barrier<S_::kBehindFirst>();
   fetch(I0{}, I0{});
-  auto stage = [&](int ks, auto slot_) __attribute__((always_inline)) {
+  // (of the last stages the codes loaded ahead are used by none, and the compiler
+  // drops such loads: only the copies are sure to be behind)
+  auto stage = [&](int ks, auto slot_, auto last_) __attribute__((always_inline)) {
     constexpr int slot = decltype(slot_)::value;
+    constexpr int behind = decltype(last_)::value ? 2 * kHOps : S_::kBehind;
     constexpr std::integral_constant<int, slot> here{};
     constexpr std::integral_constant<int, (slot + 1) & 3> there{};
     constexpr std::integral_constant<int, slot % kAhead> ring{};
@@ -296,7 +301,7 @@ __global__ __launch_bounds__(64 * WM * WN, WCB == 2 ? 2 : 4) void i8_tile_kernel
       load_w(ks + kAhead, ring, t_);
       __builtin_amdgcn_sched_barrier(0);
     });
-    ring_barrier<S_::kBehind>();
+    ring_barrier<behind>();
     load_h(ks + 4, here);
     fetch(there, I0{});  // past the last stage: not used
     multiply(here, I3{});
@@ -305,14 +310,14 @@ __global__ __launch_bounds__(64 * WM * WN, WCB == 2 ? 2 : 4) void i8_tile_kernel
   };
   int ks = 0;
   for (; ks + 4 <= nS; ks += 4) {
-    stage(ks, I0{});
-    stage(ks + 1, I1{});
-    stage(ks + 2, I2{});
-    stage(ks + 3, I3{});
+    stage(ks, I0{}, std::false_type{});
+    stage(ks + 1, I1{}, std::false_type{});
+    stage(ks + 2, I2{}, std::false_type{});
+    stage(ks + 3, I3{}, std::false_type{});
   }
-  if (ks < nS) stage(ks, I0{});
-  if (ks + 1 < nS) stage(ks + 1, I1{});
-  if (ks + 2 < nS) stage(ks + 2, I2{});
+  if (ks < nS) stage(ks, I0{}, std::true_type{});
+  if (ks + 1 < nS) stage(ks + 1, I1{}, std::true_type{});
+  if (ks + 2 < nS) stage(ks + 2, I2{}, std::true_type{});
   __builtin_amdgcn_s_waitcnt(0);
 
   // lane: row c32 of each block, tokens 8 (e / 4) + 4 half + e % 4 of each tile
