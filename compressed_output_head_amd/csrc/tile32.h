@@ -455,8 +455,9 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
   // frees: W once the last step is unpacked, H after the barrier that ends
   // every wave's reads of it.  Past the last stage the H slot receives Z
   // instead (or the last stage again), and W repeats the last stage, which
-  // keeps the count of operations in flight the same.
-  auto stage = [&](int ks, auto S_) {
+  // keeps the count of operations in flight the same while the loop runs; of the
+  // stages behind it (last_) the compiler may drop W that no stage uses.
+  auto stage = [&](int ks, auto S_, auto last_) {
     constexpr int S = decltype(S_)::value;
     constexpr std::integral_constant<int, S> Sc{};
     constexpr std::integral_constant<int, (S + 1) & 3> Sn{};
@@ -474,7 +475,7 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
     });
     // stage ks + 1 is complete once this wave has at most the loads of the
     // three stages after it (W of ks + 4 included) in flight
-    stage_barrier<3 * kWOps + 2 * kT32HOps>();
+    stage_barrier<(decltype(last_)::value ? 0 : 3 * kWOps) + 2 * kT32HOps>();
     load_slot(ks + kT32Ahead, Sc);
     fetch(Sn, I0{}, I0{});  // past the last stage: harmless reads, never used
     mma(std::integral_constant<int, (KS - 1) & 1>{});
@@ -482,20 +483,20 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
   };
   int ks = 0;
   for (; ks + 4 <= nS; ks += 4) {
-    stage(ks, I0{});
-    stage(ks + 1, I1{});
-    stage(ks + 2, I2{});
-    stage(ks + 3, I3{});
+    stage(ks, I0{}, std::false_type{});
+    stage(ks + 1, I1{}, std::false_type{});
+    stage(ks + 2, I2{}, std::false_type{});
+    stage(ks + 3, I3{}, std::false_type{});
   }
   if constexpr (KS == 4) {
     if (ks < nS) {  // nS is even: two stages remain
-      stage(ks, I0{});
-      stage(ks + 1, I1{});
+      stage(ks, I0{}, std::true_type{});
+      stage(ks + 1, I1{}, std::true_type{});
     }
   } else {  // one to three stages remain
-    if (ks < nS) stage(ks, I0{});
-    if (ks + 1 < nS) stage(ks + 1, I1{});
-    if (ks + 2 < nS) stage(ks + 2, I2{});
+    if (ks < nS) stage(ks, I0{}, std::true_type{});
+    if (ks + 1 < nS) stage(ks + 1, I1{}, std::true_type{});
+    if (ks + 2 < nS) stage(ks + 2, I2{}, std::true_type{});
   }
   __builtin_amdgcn_s_waitcnt(0);
 
