@@ -487,8 +487,12 @@ __global__ __launch_bounds__(kHeadThreads) void xent_head_kernel(const ManyArgs 
 
 // What the head's scales give: powers of two that bring the largest |q4 c8 s_R|
 // (2040 at most before s_R) and the largest |s_A| to [2^14, 2^15) and [1/2, 1),
-// and s_A times theirs, of entry i.  (An s_R below 2^-25 of the largest one loses
-// digits by that, 2^-40 of the largest weight.)
+// and s_A times theirs, of entry i.  Nothing is lost by that where the largest s_R
+// is below 16 and the largest s_A below 1, as a power of 1 and more makes no fp16
+// number subnormal; else an s_R below 2^-17 (s_A: 2^-13) of the largest loses digits,
+// half a step being 2^-28 (2^-24) of the largest at most.  The product (q4 c8) s_R
+// is rounded to fp16 in any case, 2^-11 of itself or 2^-39 of the largest weight,
+// and so is e s_A, 2^-11 or, beside a row's largest e, 2^-34 of the largest s_A.
 __device__ __forceinline__ void head_scales(const ManyArgs& a, int64_t i) {
   static_assert(kHeadParts == 64, "a part for each lane");
   int k[3];

@@ -668,9 +668,13 @@ ARCHEAD_API int archead_cross_entropy_workspace_bytes(const archead_dims* d, int
  * each row.  Logits are fp32 as archead_logits computes them; sums of
  * exponentials fp32 in short runs and fp64 from there, row numbers fp64; the
  * label's own term is in no sum, so that 1 - p of a row that is sure of it keeps
- * its digits in log p and in the gradient.  Exponentials enter the product
- * rounded to fp16, dH is rounded to nearest even.  Two calls with the same
- * arguments give the same bits.
+ * its digits in log p and in the gradient.  The product that gives dH takes fp16
+ * operands, 2^-11 each: up to 32 rows the exponentials times the vocabulary
+ * rows' scales; of more rows the exponentials, the residual's values (q4 c8 s_R,
+ * under one power of two for the head) and the exponentials times s_Ac and s_Aw,
+ * and below 2^-14 of the row's largest an exponential may be rounded again.  In
+ * all about 2^-11 of the terms, beside dH's own rounding to nearest even, 2^-8.
+ * Two calls with the same arguments give the same bits.
  *   H: bf16 [N][D], rows 16-byte aligned, N at most 2^22.  dH must not overlap
  *   H; outputs share bytes with nothing else (E_SHAPE).
  * head->workspace: at least archead_cross_entropy_workspace_bytes.  V at most
