@@ -152,15 +152,6 @@ __device__ __forceinline__ void arrange_groups(const BwdArgs& a, int64_t i) {
     arrange_groups<uint8_t>(a, i);
 }
 
-// f(integral_constant<I>) for I = B .. E-1, unrolled at compile time
-template <int B, int E, class F>
-__device__ __forceinline__ void static_for(F&& f) {
-  if constexpr (B < E) {
-    f(std::integral_constant<int, B>{});
-    static_for<B + 1, E>(f);
-  }
-}
-
 // Place of 16-byte octet o (8 columns) of row k in a stage's fp16 tile of 64
 // rows x 256 columns: both the 16 rows that a wave writes at one octet and the
 // 4 rows x 4 octets that 32 lanes read at a time fall in different banks.

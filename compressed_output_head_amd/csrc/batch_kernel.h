@@ -59,32 +59,9 @@ constexpr int kBMaxBlocks2 = 3;  // ... with two workgroups per CU
 constexpr int kBMaxGroups = 64;  // group codes per row (D/g)
 constexpr int kNonTemporal = 2;  // cache policy of the packed tiles: streamed once
 
-template <int B, int E, class F>
-__device__ __forceinline__ void static_for(F&& f) {
-  if constexpr (B < E) {
-    f(std::integral_constant<int, B>{});
-    static_for<B + 1, E>(f);
-  }
-}
-
 __device__ __forceinline__ float wave_max(float v) {
   for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
   return v;
-}
-
-// This wave's vector-memory operations up to the last n and all its LDS
-// accesses are complete, then every wave meets.  Buffer-to-LDS copies land
-// when their vmcnt retires, so after the barrier every wave's copies are
-// visible.  No fence (it would wait for every load in flight).
-template <int n>
-__device__ __forceinline__ void ring_barrier() {
-  static_assert(n >= 0 && n < 64, "vmcnt has six bits");
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070 | (n & 0xF) | (((n >> 4) & 3) << 14));
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
 }
 
 // This wave's vector-memory operations up to the last n and all its LDS
@@ -97,13 +74,6 @@ __device__ __forceinline__ void vm_wait() {
   __builtin_amdgcn_s_waitcnt(0x0070 | (n & 0xF) | (((n >> 4) & 3) << 14));
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
-}
-
-// One 16-byte buffer-to-LDS copy per lane (lane l writes dst + 16 l).  Not
-// inlined into the kernel template by hand: called there directly, the
-// builtin keeps the host pass from emitting the template's launch stub.
-__device__ __forceinline__ void lds_copy16(__amdgpu_buffer_rsrc_t rs, void* dst, uint32_t voff, uint32_t soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 16, voff, soff, 0, 0);
 }
 
 // Wait states after the last MFMA of a chain whose results are copied or

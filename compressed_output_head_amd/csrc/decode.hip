@@ -119,15 +119,6 @@ __host__ inline int wave_blocks_max(int cnt) {
 __host__ __device__ inline int z_slices(int nkt) { return (nkt + kZSliceKts - 1) / kZSliceKts; }
 __host__ __device__ inline int z_stride(int nkt) { return (z_slices(nkt) + 3) & ~3; }
 
-// f(integral_constant<I>) for I = B .. E-1, unrolled at compile time
-template <int B, int E, class F>
-__device__ __forceinline__ void static_for(F&& f) {
-  if constexpr (B < E) {
-    f(std::integral_constant<int, B>{});
-    static_for<B + 1, E>(f);
-  }
-}
-
 // Workgroup barrier for LDS only: this wave's LDS accesses are complete, then
 // every wave meets.  No memory fence: __syncthreads() would also wait for
 // every global load in flight (the packed tiles).  The empty asm statements

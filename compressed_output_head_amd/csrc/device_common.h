@@ -1,9 +1,12 @@
 // Device helpers shared by the gfx950 kernels: operand types, exact integer
-// unpacking into fp16 MFMA operands, and number conversions.
+// unpacking into fp16 MFMA operands, number conversions, and what LDS rings are
+// made of.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 namespace archead {
 
@@ -121,6 +124,40 @@ __device__ __forceinline__ int row_exponent(float maxabs) {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0,
                                            (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+
+// f(integral_constant<I>) for I = B .. E-1, unrolled at compile time
+template <int B, int E, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (B < E) {
+    f(std::integral_constant<int, B>{});
+    static_for<B + 1, E>(f);
+  }
+}
+
+// Workgroup barrier of an LDS ring: this wave's vector-memory operations up to
+// the last n and all its LDS accesses are complete, then every wave meets.
+// Buffer-to-LDS copies land in LDS when their vmcnt retires, so after the
+// barrier every wave's copies are visible.  No fence is emitted (it would wait
+// for every copy in flight); the empty asm statements with a memory clobber keep
+// the compiler from moving memory accesses across.
+template <int n>
+__device__ __forceinline__ void ring_barrier() {
+  static_assert(n >= 0 && n < 64, "vmcnt has six bits");
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (n & 0xF) | (((n >> 4) & 3) << 14));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// One 16-byte buffer-to-LDS copy per lane (lane l writes dst + 16 l).  Kept out
+// of the kernel templates: called from inside one directly, the builtin makes
+// the host pass reject the template's instantiation without a diagnostic, and no
+// launch stub is made.
+__device__ __forceinline__ void lds_copy16(__amdgpu_buffer_rsrc_t rs, void* dst, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 16, voff, soff, 0, 0);
 }
 
 // 16 x 16 x 32: lane l holds A row l%16 / B column l%16, k 8*(l/16) .. +8;

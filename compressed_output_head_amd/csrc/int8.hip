@@ -66,15 +66,6 @@ __device__ __forceinline__ void put(const I8Args& a, int64_t n, int64_t v, float
     static_cast<float*>(a.Y)[n * a.y_stride + v] = y;
 }
 
-// f(integral_constant<I>) for I = B .. E-1, unrolled at compile time
-template <int B, int E, class F>
-__device__ __forceinline__ void static_for(F&& f) {
-  if constexpr (B < E) {
-    f(std::integral_constant<int, B>{});
-    static_for<B + 1, E>(f);
-  }
-}
-
 // Few tokens: bound by the head's bytes, 622 MB of a 151936 x 4096 head in 106
 // us, 5.9 TB/s (the 16 columns of an MFMA cost nothing beside that, and one
 // workgroup of 16 waves a CU reads as fast as two of eight).  The tokens'
@@ -149,26 +140,6 @@ __global__ __launch_bounds__(256) void i8_arrange_kernel(const I8Args a) {
   a.xf[i] = n < a.N ? operand(a.X + n * a.x_stride, kt, q, lane >> 5) : u4{};
 }
 
-// Workgroup barrier for the LDS ring: this wave's copies up to the last n
-// vector-memory operations and all its LDS reads are complete, then every
-// wave meets.  No fence is emitted (it would wait for every copy in flight);
-// the empty asm statements keep memory accesses on their side.
-template <int n>
-__device__ __forceinline__ void ring_barrier() {
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070 | (n & 0xF) | (((n >> 4) & 3) << 14));
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-
-// One 16-byte buffer-to-LDS copy per lane (out of the kernel template: from
-// inside it the builtin makes the host pass drop the launch stub).
-__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t rs, void* dst, uint32_t voff, uint32_t soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 16, voff, soff, 0, 0);
-}
-
 // TT token tiles of 32, WM x WN waves, each MT = TT / WM token tiles and WCB
 // blocks of 32 rows of the vocabulary.  A stage is one 128-column tile, four
 // MFMA steps: the tokens' fragments by copies straight to an LDS ring of four
@@ -233,7 +204,7 @@ __global__ __launch_bounds__(64 * WM * WN, WCB == 2 ? 2 : 4) void i8_tile_kernel
     constexpr int slot = decltype(slot_)::value;
 #pragma unroll
     for (int i = 0; i < kHOps; ++i)
-      copy_to_lds(hrs, &I8_SLOT(slot)[kWaves * i + wave][0], lane16, hoff[i] + (uint32_t)std::min(ks, nS - 1) * 4096u);
+      lds_copy16(hrs, &I8_SLOT(slot)[kWaves * i + wave][0], lane16, hoff[i] + (uint32_t)std::min(ks, nS - 1) * 4096u);
   };
   // codes: row c32 of block cb, the step's run in the tile's order; blocks past
   // the last one read that one, and are not stored

@@ -56,33 +56,6 @@ constexpr int kEpiChunk = 2;  // low-rank rank steps whose loads are issued toge
 constexpr int kEpiLdsSteps = 8;  // up to 128 padded ranks: Z of the workgroup fits the H ring
 constexpr int kXcds = 8;
 
-
-// Workgroup barrier for the LDS ring: this wave's copies up to the last n
-// vector-memory operations and all its LDS reads are complete, then every
-// wave meets.  Buffer-to-LDS copies land in LDS when their vmcnt retires, so
-// after the barrier every wave's copies are visible.  No fence is emitted (a
-// fence would wait for every copy in flight); the empty asm statements with a
-// memory clobber keep the compiler from moving memory accesses across.
-template <int n>
-__device__ __forceinline__ void stage_barrier() {
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070 | (n & 0xF) | (((n >> 4) & 3) << 14));
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-
-
-// f(integral_constant<I>) for I = B .. E-1, unrolled at compile time
-template <int B, int E, class F>
-__device__ __forceinline__ void static_for(F&& f) {
-  if constexpr (B < E) {
-    f(std::integral_constant<int, B>{});
-    static_for<B + 1, E>(f);
-  }
-}
-
 struct Acc4 {  // low-rank accumulators of one wave's vocabulary blocks
   f16x v[kT32WCB];
 };
@@ -121,13 +94,6 @@ __host__ __device__ inline void t32_tile(const T32Grid& G, int L, int& vt, int& 
 struct T32Split {
   int full, s;
 };
-
-// One 16-byte buffer-to-LDS copy per lane.  Kept out of the kernel template:
-// called from inside it directly, the builtin makes the host pass reject the
-// template's instantiation without a diagnostic, and no launch stub is made.
-__device__ __forceinline__ void lds_copy16(__amdgpu_buffer_rsrc_t rs, void* dst, uint32_t voff, uint32_t soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 16, voff, soff, 0, 0);
-}
 
 // EX: a power of two of the scale that goes with the head's scales in place of
 // the row's, which alone would leave fp32 at inverse temperatures near its end.
@@ -446,7 +412,7 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
 
   // stage 0 complete: wait past the loads of stages 1..3, then publish every
   // wave's copies and the codes
-  stage_barrier<3 * (kWOps + kT32HOps)>();
+  ring_barrier<3 * (kWOps + kT32HOps)>();
   read_codes(0, cd[0]);
   fetch(I0{}, I0{}, I0{});
 
@@ -475,7 +441,7 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
     });
     // stage ks + 1 is complete once this wave has at most the loads of the
     // three stages after it (W of ks + 4 included) in flight
-    stage_barrier<(decltype(last_)::value ? 0 : 3 * kWOps) + 2 * kT32HOps>();
+    ring_barrier<(decltype(last_)::value ? 0 : 3 * kWOps) + 2 * kT32HOps>();
     load_slot(ks + kT32Ahead, Sc);
     fetch(Sn, I0{}, I0{});  // past the last stage: harmless reads, never used
     mma(std::integral_constant<int, (KS - 1) & 1>{});
