@@ -528,7 +528,7 @@ __device__ __forceinline__ void tile32_body(const FwdArgs& a, const T32Split& sp
         }
       }
       // the label has no part in the sums, nor have rows past the vocabulary
-      const unsigned d = (unsigned)(label - v0);
+      const unsigned d = (unsigned)label - (unsigned)v0;  // any label: no difference leaves its type
       if (d < 28u && (d & 4u) == 0u) {
         const int at = (int)(d >> 3) * 4 + (int)(d & 3u);
         float zl = 0.0f;
