@@ -12,7 +12,7 @@
 
 namespace archead {
 
-constexpr int64_t kFewTokens = 32;  // of bwd_few_kernel
+constexpr int64_t kFewTokens = 32;  // of bwd_few_kernel: as many as its operands' tile holds
 
 struct BwdArgs {
   int64_t V, D, N, n32, nb;
