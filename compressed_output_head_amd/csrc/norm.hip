@@ -12,11 +12,12 @@
 // there (both grow alike from 1/2 up).
 //
 // One pass: a row is read once, held in registers from the sums to the
-// outputs (h of a row whose t leaves fp32: twice).  Bound by HBM where rows are many, by the launch where they are few:
-// 16384 rows of 4096 with a residual, sum and codes 81 us, 5.8 TB/s of what is
-// read and written (rows that start at odd elements or leave threads idle 4.6 to
-// 5.0), to bf16 with the factor 95 us, 5.6 TB/s, without a residual 50, 5.3; their
-// gradient 108 us, 5.0 TB/s; one row 3.1 us.
+// outputs (a row whose t leaves fp32 again for h).  Bound by HBM where rows are
+// many, by the launch where they are few: 16384 rows of 4096 with a residual, sum
+// and codes 81 us, 5.8 TB/s of what is read and written (rows that start at odd
+// elements or leave threads idle 4.6 to 5.0), to bf16 with the factor 95 us, 5.6
+// TB/s, without a residual 50, 5.3; their gradient 108 us, 5.0 TB/s; one row 3.1
+// us.
 #include <algorithm>
 
 #include "device_common.h"

@@ -31,11 +31,13 @@
 // at the border, calls of at most 32 rows each and the other one: 33 rows of a
 // 151936 x 4096 head 394 and 341 us, 64 rows 493 and 361; of 32000 x 2048 124 and
 // 133, 148 and 135; of 1024 x 256 82 and 72, 95 and 72.  32 rows in one call take
-// 245, 75 and 48, and as much as 33 the other way.  Many rows are bound by the MFMAs under the power
-// limit, two products of the head with the rows: 4096 rows, nine in ten of
-// which count, 9.1 to 9.3 ms, 4.8 in tile32_exp_kernel (0.96 PFLOP/s) and 3.9 to
-// 4.1 in xent_main_kernel (1.13), 0.7 in what joins the pieces; 4096 rows that all
-// count 10.1 ms, their loss alone 5.0 (bf16 logits of them 4.6).
+// 245, 75 and 48, and as much as 33 the other way.
+//
+// Many rows are bound by the MFMAs under the power limit, two products of the
+// head with the rows: 4096 rows, nine in ten of which count, 9.1 to 9.3 ms, 4.8 in
+// tile32_exp_kernel (0.96 PFLOP/s) and 3.9 to 4.1 in xent_main_kernel (1.13), 0.7
+// in what joins the pieces; 4096 rows that all count 10.1 ms, their loss alone 5.0
+// (bf16 logits of them 4.6).
 #include <algorithm>
 #include <limits>
 

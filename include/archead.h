@@ -658,7 +658,8 @@ typedef struct {
 
 /* Device workspace archead_cross_entropy needs for n_tokens rows, with dH or
  * without.  A call of fewer rows may need more: ask for every number of rows that
- * a workspace is kept for.  Pure host arithmetic.  E_NULL, E_DIMS, E_SHAPE, E_UNSUPPORTED. */
+ * a workspace is kept for.  Pure host arithmetic.  E_NULL, E_DIMS, E_SHAPE,
+ * E_UNSUPPORTED. */
 ARCHEAD_API int archead_cross_entropy_workspace_bytes(const archead_dims* d, int64_t n_tokens, uint64_t* bytes);
 
 /* Enqueue the cross entropy of H's rows through a packed ARCHead head, with the
